@@ -456,6 +456,133 @@ AFF_API aff_status affinity_gather_blocks(const void* in, void* out, int64_t row
                                           int64_t block_bytes, const int32_t* order, void* workspace,
                                           size_t workspace_bytes, aff_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The forward pass around the scores: a step's keys and values into a paged
+ * cache, attention over it, and the norms between blocks.  They produce a
+ * layer's `a` (attention output) and `x` (residual) from a model, before or
+ * after its layout is realised: the cache is per KV group, so a device's
+ * shard of a realised layout is a contiguous slice of groups.
+ *
+ * A step is a set of query tokens of B sequences, sequence b's at rows
+ * q_start[b] .. q_start[b+1]-1 of the step's T tokens (any number, none
+ * included).  A sequence sees a prefix that all of them share and then its own
+ * tokens.  kv_len[b] counts its own tokens in the cache, those of this step
+ * included: its i-th query of n has own index kv_len[b] - n + i and position
+ * prefix_len + that index.  Tokens past q_start[B], and queries whose own index
+ * is negative, are padding: they are not stored and their output rows are zero.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * A layer's paged cache: k and v are device pools of n_pages pages of
+ * page_size tokens; element (page, group, token, j) is at
+ * page * page_stride + group * group_stride + token * token_stride + j
+ * (strides in elements, the same for both pools).
+ * dtype AFF_BF16 or AFF_FP32.  d_head <= 256 (affinity_prefix_attention: <=
+ * 128), a multiple of 16 bytes, as are the strides; page_size a multiple of 8.
+ */
+typedef struct {
+  void *k, *v;
+  int64_t n_pages, page_stride, group_stride, token_stride;
+  int32_t G, page_size, d_head, dtype;
+} aff_kv_cache;
+
+/*
+ * A step.  q_start int32 [B+1], kv_len int32 [B], pages int32 [B][pages_stride]
+ * (page ids of each sequence's own tokens, in order), prefix_pages int32
+ * [ceil(prefix_len / page_size)] (NULL if prefix_len is 0): device, 4-byte
+ * aligned.  H query heads, H % cache->G == 0, H <= 4096; T * H <= 2^30;
+ * B <= 2^20; prefix_len and pages_stride * page_size <= 2^30.
+ */
+typedef struct {
+  int64_t T, prefix_len, pages_stride;
+  const int32_t *q_start, *kv_len, *pages, *prefix_pages;
+  int32_t B, H;
+} aff_step;
+
+/* Device bytes of a step's plan. */
+AFF_API aff_status affinity_step_plan_size(const aff_step* step, const aff_kv_cache* cache, size_t* bytes);
+
+/*
+ * Plans a step: where every token stands and how the attention's work is cut.
+ * Made once per step and read by affinity_kv_append and
+ * affinity_prefix_attention of every layer whose cache has the same shape (the
+ * pools themselves may differ); remade when q_start, kv_len or a page table
+ * changes.  `plan` (device, 256-byte aligned) also holds the attention's
+ * partial rows, so calls that share a plan must not overlap, and the status
+ * word that affinity_device_status(plan) reads: AFF_ERR_RANGE for starts out of
+ * order, a kv_len past its pages, a page id outside the pool or a position
+ * outside the rotary table; AFF_ERR_INVALID_ARG for a plan made for other shapes.
+ */
+AFF_API aff_status affinity_step_plan(const aff_step* step, const aff_kv_cache* cache, void* plan, size_t plan_bytes,
+                                      aff_stream_t stream);
+
+/*
+ * Rotation and norms of affinity_kv_append.  cos, sin: device fp32
+ * [n_pos][rot/2].  The leading `rot` elements of a head are rotated (even, 0 ..
+ * d_head): pairs (j, j + rot/2), or (2j, 2j+1) if interleaved.  q_gain, k_gain
+ * [d_head] in the cache's type, or NULL for no norm.
+ */
+typedef struct {
+  const float *cos, *sin;
+  const void *q_gain, *k_gain;
+  int64_t n_pos;
+  float eps;
+  int32_t rot, interleaved;
+} aff_rotary;
+
+/*
+ * Appends a step to a layer's cache.  q [T, H*d_head], k and v [T, G*d_head],
+ * rows q_stride, k_stride, v_stride elements apart (views of one projection
+ * are fine).  Every query and key row z is replaced by
+ *   z / sqrt(mean(z^2) + eps) * gain   (with a gain)
+ * and rotated by its token's position; queries go to q_out (rows q_out_stride
+ * apart; may be q itself with the same stride), keys and values to their slots.
+ * Everything is computed in fp32 and rounded once.  Pointers and strides:
+ * multiples of 16 bytes.
+ */
+AFF_API aff_status affinity_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const aff_kv_cache* cache, const aff_step* step,
+                                      const aff_rotary* rotary, void* q_out, int64_t q_out_stride, void* plan,
+                                      size_t plan_bytes, aff_stream_t stream);
+
+/*
+ * Causal attention of a step over the cache, the shared prefix read once for
+ * the whole batch:
+ *   out[t, h] = sum_j softmax_j(scale q[t, h].k_j) v_j,
+ * j over the prefix's keys and the own keys with index <= t's, k and v of group
+ * h / (H/G).  lse[t, h] (fp32, may be NULL) is the log of the softmax's
+ * denominator, sum_j exp(scale q.k_j).  A row without keys (padding) is 0, its
+ * lse -inf.  q [T, H*d_head] with rows q_stride apart, out [T, H*d_head] dense.
+ * Keys past a sequence's own are not read into any sum, whatever the pool holds
+ * there.  scale must be positive.  AFF_BF16: fp32 scores, sums and softmax,
+ * probabilities rounded to bf16 for the second product.  AFF_FP32: fp32
+ * throughout on the CUDA cores (meant for small shapes).
+ */
+AFF_API aff_status affinity_prefix_attention(const void* q, int64_t q_stride, const aff_kv_cache* cache,
+                                             const aff_step* step, float scale, void* out, float* lse, void* plan,
+                                             size_t plan_bytes, aff_stream_t stream);
+
+/*
+ * The norms around a block with its gate and residual scale:
+ *   u = f / rms(f) * post_gain   (u = f if post_gain is NULL)
+ *   y = x + scale * gate * u     (gate NULL: ones)
+ *   h = y / rms(y) * pre_gain    (only if h and pre_gain are given, both or neither)
+ * with rms(v) = sqrt(mean(v^2) + eps); all in fp32, h from the unrounded y.
+ * x, f, y, h [T, D], rows *_stride elements apart; gains [D]; gate row t /
+ * rows_per_gate serves token t (rows_per_gate = T: one row for all).  D <=
+ * 16384.  y may be x and h may be f (same strides).  16-byte aligned pointers;
+ * rows that all start on 16 bytes take the vector path.
+ */
+typedef struct {
+  const void *x, *f, *gate, *post_gain, *pre_gain;
+  void *y, *h;
+  int64_t T, D, x_stride, f_stride, gate_stride, y_stride, h_stride, rows_per_gate;
+  float scale, eps;
+  int32_t dtype;
+} aff_block_norm;
+
+AFF_API aff_status affinity_block_norm(const aff_block_norm* args, aff_stream_t stream);
+
 /*
  * Profiling hook (no effect on results): register two caller-created CUDA
  * events (cudaEvent_t handles) that later affinity_up / affinity_down calls

@@ -55,6 +55,34 @@ class aff_layout_opts(ctypes.Structure):
                 ("layer_mask", ctypes.c_void_p), ("assign", aff_assign_opts)]
 
 
+class aff_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("group_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("G", ctypes.c_int32), ("page_size", ctypes.c_int32), ("d_head", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class aff_step(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("prefix_len", ctypes.c_int64), ("pages_stride", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("prefix_pages", ctypes.c_void_p), ("B", ctypes.c_int32), ("H", ctypes.c_int32)]
+
+
+class aff_rotary(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("q_gain", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class aff_block_norm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("f", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("post_gain", ctypes.c_void_p), ("pre_gain", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("f_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 class AffinityError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -121,6 +149,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.affinity_gather_blocks.argtypes = [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
                                            ctypes.c_size_t, _P]
     lib.affinity_gather_blocks.restype = st
+    lib.affinity_step_plan_size.argtypes = [ctypes.POINTER(aff_step), ctypes.POINTER(aff_kv_cache),
+                                            ctypes.POINTER(ctypes.c_size_t)]
+    lib.affinity_step_plan_size.restype = st
+    lib.affinity_step_plan.argtypes = [ctypes.POINTER(aff_step), ctypes.POINTER(aff_kv_cache), _P, ctypes.c_size_t, _P]
+    lib.affinity_step_plan.restype = st
+    lib.affinity_kv_append.argtypes = [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64,
+                                       ctypes.POINTER(aff_kv_cache), ctypes.POINTER(aff_step),
+                                       ctypes.POINTER(aff_rotary), _P, ctypes.c_int64, _P, ctypes.c_size_t, _P]
+    lib.affinity_kv_append.restype = st
+    lib.affinity_prefix_attention.argtypes = [_P, ctypes.c_int64, ctypes.POINTER(aff_kv_cache),
+                                              ctypes.POINTER(aff_step), ctypes.c_float, _P, _P, _P, ctypes.c_size_t,
+                                              _P]
+    lib.affinity_prefix_attention.restype = st
+    lib.affinity_block_norm.argtypes = [ctypes.POINTER(aff_block_norm), _P]
+    lib.affinity_block_norm.restype = st
     lib.affinity_strerror.argtypes = [ctypes.c_int32]
     lib.affinity_strerror.restype = ctypes.c_char_p
     lib.affinity_last_cuda_error.argtypes = []
@@ -380,6 +423,154 @@ def gather_blocks(src, dst, rows: int, n_blocks: int, block_bytes: int, order, w
     _check(load().affinity_gather_blocks(_ptr(src), _ptr(dst), int(rows), int(n_blocks), int(block_bytes),
                                          o.ctypes.data, _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
                                          _stream(stream)), "affinity_gather_blocks")
+
+
+def _dtype(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return AFF_BF16
+    if t.dtype == torch.float32:
+        return AFF_FP32
+    raise TypeError("tensors must be bfloat16 or float32")
+
+
+def _row_stride(t, width: int, name: str) -> int:
+    """Elements between the rows of a [T, ...] tensor whose rows are dense and `width` elements wide."""
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != inner:
+            raise ValueError(f"{name}: rows must be dense")
+        inner *= n
+    if inner != width:
+        raise ValueError(f"{name}: rows of {width} elements expected, got {inner}")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _same_type(like, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != like.dtype or t.device != like.device):
+            raise TypeError(f"{name} must be {like.dtype} on {like.device}")
+
+
+def kv_cache(k, v) -> aff_kv_cache:
+    """A layer's paged cache from its pools, [n_pages, G, page_size, d_head] in any order of the first three."""
+    if k.shape != v.shape or k.dim() != 4:
+        raise ValueError("k and v must be [n_pages, G, page_size, d_head]")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v must have the same strides and dense rows")
+    _same_type(k, v=v)
+    c = aff_kv_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[1],
+                     k.shape[2], k.shape[3], _dtype(k))
+    c.keep = (k, v)
+    return c
+
+
+def step(T: int, H: int, q_start, kv_len, pages, prefix_pages=None, prefix_len: int = 0) -> aff_step:
+    """A step of T query tokens with H heads: q_start [B+1], kv_len [B], pages [B, n], prefix_pages (CUDA int32)."""
+    import torch
+    for name, t in (("q_start", q_start), ("kv_len", kv_len), ("pages", pages), ("prefix_pages", prefix_pages)):
+        if t is not None and (t.dtype != torch.int32 or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1)):
+            raise ValueError(f"{name} must be dense int32")
+    B = kv_len.shape[0]
+    if q_start.shape != (B + 1,) or pages.dim() != 2 or pages.shape[0] != B:
+        raise ValueError("q_start must be [B+1], kv_len [B] and pages [B, n]")
+    if B > 1 and pages.stride(0) < pages.shape[1]:
+        raise ValueError("the rows of pages must not overlap")
+    if B > 1 and pages.stride(0) != pages.shape[1]:
+        pages = pages.contiguous()
+    s = aff_step(int(T), int(prefix_len), pages.shape[1], q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(),
+                 _ptr(prefix_pages), B, int(H))
+    s.keep = (q_start, kv_len, pages, prefix_pages)
+    s.n_prefix_pages = 0 if prefix_pages is None else prefix_pages.shape[0]
+    return s
+
+
+def _prefix_covered(s: aff_step, c: aff_kv_cache) -> None:
+    n = getattr(s, "n_prefix_pages", None)
+    if n is not None and n * c.page_size < s.prefix_len:
+        raise ValueError("prefix_pages does not cover prefix_len")
+
+
+def step_plan_size(s: aff_step, c: aff_kv_cache) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().affinity_step_plan_size(ctypes.byref(s), ctypes.byref(c), ctypes.byref(n)),
+           "affinity_step_plan_size")
+    return n.value
+
+
+def step_plan(s: aff_step, c: aff_kv_cache, plan, stream=None, plan_bytes=None) -> None:
+    """Enqueue the plan of a step (affinity_step_plan) into `plan`, a CUDA uint8 tensor of step_plan_size bytes."""
+    _prefix_covered(s, c)
+    _check(load().affinity_step_plan(ctypes.byref(s), ctypes.byref(c), _ptr(plan), _ws_bytes(plan, plan_bytes),
+                                     _stream(stream)), "affinity_step_plan")
+
+
+def rotary(cos, sin, interleaved: bool = False, q_gain=None, k_gain=None, eps: float = 1e-6) -> aff_rotary:
+    """Rotation tables [n_pos, rot / 2] (CUDA fp32) and the optional per-head norm gains of kv_append."""
+    import torch
+    if cos.shape != sin.shape or cos.dim() != 2 or cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        raise ValueError("cos and sin must be fp32 [n_pos, rot / 2]")
+    if not (cos.is_contiguous() and sin.is_contiguous()):
+        raise ValueError("cos and sin must be dense")
+    r = aff_rotary(cos.data_ptr(), sin.data_ptr(), _ptr(q_gain), _ptr(k_gain), cos.shape[0], float(eps),
+                   2 * cos.shape[1], int(bool(interleaved)))
+    r.keep = (cos, sin, q_gain, k_gain)
+    return r
+
+
+def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan, stream=None,
+              plan_bytes=None) -> None:
+    """Enqueue affinity_kv_append: q [T, H, d_head], k and v [T, G, d_head] (rows may be strided), q_out like q."""
+    hd, gd = s.H * c.d_head, c.G * c.d_head
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
+        if t.shape[0] != s.T or _dtype(t) != c.dtype:
+            raise ValueError(f"{name} must have {s.T} rows of the cache's type")
+    for name, t in zip(("q_gain", "k_gain"), getattr(r, "keep", (None,) * 4)[2:]):
+        if t is not None and (t.shape != (c.d_head,) or _dtype(t) != c.dtype):
+            raise ValueError(f"{name} must be [d_head] of the cache's type")
+    _check(load().affinity_kv_append(_ptr(q), _row_stride(q, hd, "q"), _ptr(k), _row_stride(k, gd, "k"), _ptr(v),
+                                     _row_stride(v, gd, "v"), ctypes.byref(c), ctypes.byref(s), ctypes.byref(r),
+                                     _ptr(q_out), _row_stride(q_out, hd, "q_out"), _ptr(plan),
+                                     _ws_bytes(plan, plan_bytes), _stream(stream)), "affinity_kv_append")
+
+
+def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, plan, stream=None,
+                     plan_bytes=None) -> None:
+    """Enqueue affinity_prefix_attention: q and out [T, H, d_head], lse fp32 [T, H] or None."""
+    hd = s.H * c.d_head
+    for name, t in (("q", q), ("out", out)):
+        if t.shape[0] != s.T or _dtype(t) != c.dtype:
+            raise ValueError(f"{name} must have {s.T} rows of the cache's type")
+    if _row_stride(out, hd, "out") != hd:
+        raise ValueError("out must be dense")
+    if lse is not None and (_dtype(lse) != AFF_FP32 or not lse.is_contiguous() or lse.numel() != s.T * s.H):
+        raise ValueError("lse must be dense fp32 [T, H]")
+    _check(load().affinity_prefix_attention(_ptr(q), _row_stride(q, hd, "q"), ctypes.byref(c), ctypes.byref(s),
+                                            float(scale), _ptr(out), _ptr(lse), _ptr(plan),
+                                            _ws_bytes(plan, plan_bytes), _stream(stream)),
+           "affinity_prefix_attention")
+
+
+def block_norm(x, f, y, h=None, post_gain=None, pre_gain=None, gate=None, rows_per_gate: int = 1, scale: float = 1.0,
+               eps: float = 1e-6, stream=None) -> None:
+    """Enqueue affinity_block_norm: x, f, y, h [T, D] (rows may be strided), gains [D], gate [n, D]."""
+    T, D = x.shape
+    _same_type(x, f=f, y=y, h=h, post_gain=post_gain, pre_gain=pre_gain, gate=gate)
+    for name, t in (("f", f), ("y", y), ("h", h)):
+        if t is not None and t.shape != (T, D):
+            raise ValueError(f"{name} must be [{T}, {D}]")
+    for name, t in (("post_gain", post_gain), ("pre_gain", pre_gain)):
+        if t is not None and (t.shape != (D,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be dense [{D}]")
+    if gate is not None and (gate.dim() != 2 or gate.shape[1] != D or gate.shape[0] * rows_per_gate < T):
+        raise ValueError("gate must be [n, D] with n * rows_per_gate >= T")
+
+    def rs(t, name):
+        return 0 if t is None else _row_stride(t, D, name)
+    a = aff_block_norm(_ptr(x), _ptr(f), _ptr(gate), _ptr(post_gain), _ptr(pre_gain), _ptr(y), _ptr(h), T, D,
+                       rs(x, "x"), rs(f, "f"), rs(gate, "gate"), rs(y, "y"), rs(h, "h"), int(rows_per_gate),
+                       float(scale), float(eps), _dtype(x))
+    _check(load().affinity_block_norm(ctypes.byref(a), _stream(stream)), "affinity_block_norm")
 
 
 def set_timing_events(start_event, stop_event) -> None:

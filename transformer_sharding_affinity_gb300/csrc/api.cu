@@ -250,6 +250,15 @@ aff_status make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* d
   return AFF_OK;
 }
 
+}  // namespace
+
+aff_status aff::map_16bit_sw128(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                                const uint64_t* strides, uint32_t box1, int box1_dim) {
+  return make_map(m, ptr, rank, dims, strides, box1, box1_dim);
+}
+
+namespace {
+
 // 16-bit tensor [rows][inner] (row stride inner * 2 bytes), box (32 innermost
 // elements = 64 bytes, box1 rows), 64-byte swizzle; OOB reads zero.
 aff_status map_sw64_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box1) {

@@ -1,0 +1,947 @@
+// attention.cu -- affinity_prefix_attention: causal softmax attention over a
+// paged cache for a batch whose sequences share a prefix, the prefix's keys and
+// values read once for the whole batch.
+//
+//   out[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - m)
+//   lse[t, h] = m + log sum_j p_j
+//
+// over the prefix's keys and the sequence's own keys j <= own index of t.
+//
+// bf16: attention_kernel, persistent, one CTA per SM, on the tensor cores.
+//   A work item (step.cuh) is up to 256 packed rows against a run of 128-key
+//   tiles.  Two streams alternate on the tensor core: while the threads of one
+//   turn its scores S into probabilities P, the products of the other run.
+//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
+//     warp 8           TMA: key and value tiles through the page tables
+//     warp 9           issues the products  S = Q K^T (both from shared memory)
+//                      and O += P V (P from tensor memory)
+//     warps 10, 11     copy the item's query rows; 11 also clears the rows of a
+//                      value tile past its keys, since 0 * NaN would stay
+//   Tensor memory: S of both streams (128 columns each, P overlays its first
+//   half), O of both (128 columns each).
+//   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
+//   when m has grown by more than 8 (in log2): until then p <= 2^8, far inside
+//   fp32 and bf16.  P is rounded to bf16, the type of V (a product's operands
+//   share it): one more rounding of at most 2^-8 per probability, unbiased and averaged
+//   over the keys; l sums the unrounded p.
+// fp32: attention_f32_kernel, CUDA cores, for small shapes.
+// Rows in several parts are merged by join_kernel from fp32 partial rows.
+#include "affinity.h"
+#include "internal.h"
+#include "launch.cuh"
+#include "sm103_primitives.cuh"
+#include "step.cuh"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+namespace aff {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;                   // rows of a stream
+constexpr int kHalfBytes = kRows * 128;      // a tile's 64-column half: 128 rows of 128 bytes
+constexpr int kMaxStages = 12;
+constexpr int kSmemMax = 227 * 1024;
+constexpr float kRescale = 8.f;              // log2 growth of the maximum that O is rescaled for
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;              // O of stream s at kColO + 128 s; S at 128 s
+constexpr uint32_t kStatusInvalid = 1;
+
+struct AttnParams {
+  StepGeom g;
+  const uint16_t* q;
+  int64_t q_stride;
+  void* out;
+  float* lse;               // [T][H] or null
+  float scale, scale_log2;
+  int32_t halves;           // 64-column halves of a head row
+  int32_t kd;               // head width rounded up to 16
+  int32_t box;              // keys of a TMA box: gcd(page_size, 128)
+  int32_t stages;
+  const float *kc, *vc;     // the pools, read by the fp32 kernel (the bf16 kernel has tensor maps)
+  int64_t page_stride, group_stride, token_stride;
+};
+
+struct alignas(8) Bars {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_fixed[kMaxStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t merge, drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: the probabilities stay in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 32 consecutive 32-bit columns (same lane mapping as tmem_ld16).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor for an MN-major operand tile written by TMA
+// with 128-byte swizzling: rows of 64 16-bit elements (128 B) along N, one row per
+// K index; 8-row atoms (1024 B) follow each other along K, groups of 64 N elements
+// lie `group_bytes` apart.  The k-th 16-element K slice starts 2048 k bytes further.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t group_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((group_bytes >> 4) & 0x3FFFu) << 16;   // leading byte offset: next 64 N elements
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;                       // stride byte offset: next 8 K rows
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;                               // swizzle mode: 128 B
+  return d;
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The whole warp waits; false (in every lane) once the CTA has given up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* status) {
+  const bool ok = mbar_wait(bar, parity, reinterpret_cast<volatile int*>(&b->abort_flag), status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Keys that tile `ti` of an item holds (1 .. 128), and the first of them within its segment.
+__device__ __forceinline__ int tile_keys(const WorkItem& it, int prefix_len, int ti, int* key0) {
+  const bool pre = ti < it.np;
+  *key0 = (pre ? ti : ti - it.np) * kKeyTile;
+  return min(kKeyTile, (pre ? prefix_len : it.own_len) - *key0);
+}
+
+__device__ __forceinline__ WorkItem load_item(const WorkItem* p) {
+  WorkItem it;
+  const int4* s = reinterpret_cast<const int4*>(p);
+  int4* d = reinterpret_cast<int4*>(&it);
+  d[0] = s[0];
+  d[1] = s[1];
+  d[2] = s[2];
+  return it;
+}
+
+// The order in which an item's key and value tiles are first used; the producer,
+// the MMA thread and the clearing warp all walk it.  f(is_value, stream, j, fresh,
+// last) returns false to stop: fresh, the tile is not loaded yet; last, nobody
+// uses it afterwards.  Streams that share their tiles (alt == 0) have n0 <= n1.
+template <typename F>
+__device__ __forceinline__ bool walk_item(const WorkItem& it, F&& f) {
+  const int n = max(it.n0, it.n1);
+  auto use = [&](bool value, int s, int j) {
+    const int mine = s ? it.n1 : it.n0;
+    if (j >= mine) return true;
+    const bool fresh = it.alt || s == 0 || j >= it.n0;
+    const bool last = it.alt || s == 1 || j >= it.n1;
+    return f(value, s, j, fresh, last);
+  };
+  if (!use(false, 0, 0) || !use(false, 1, 0)) return false;
+  for (int j = 0; j < n; ++j)
+    for (int s = 0; s < 2; ++s)
+      if (!use(true, s, j) || !use(false, s, j + 1)) return false;
+  return true;
+}
+
+__device__ __forceinline__ int tile_of(const WorkItem& it, int s, int j) { return it.t0 + (it.alt ? 2 * j + s : j); }
+
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const StepGeom& g = p.g;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tile_bytes = p.halves * kHalfBytes;
+  uint8_t* q_smem = smem;                              // two row tiles
+  uint8_t* kv_smem = smem + 2 * tile_bytes;
+  float2* merge_ml = reinterpret_cast<float2*>(kv_smem + p.stages * tile_bytes);   // stream 1's (m, l) of every row
+  Bars* bars = reinterpret_cast<Bars*>(merge_ml + kRows);
+  uint32_t* status = &g.head->status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&bars->kv_full[i], 1);
+      mbar_init(&bars->kv_empty[i], 2);      // the products that read it, and the clearing warp
+      mbar_init(&bars->kv_fixed[i], 1);
+    }
+    mbar_init(&bars->q_full, 2);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 4);
+      mbar_init(&bars->o_full[s], 1);
+      mbar_init(&bars->o_empty[s], 4);
+    }
+    mbar_init(&bars->merge, 4);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_enter();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const bool fits = plan_matches(g);
+  if (!fits && threadIdx.x == 0) latch_status(status, kStatusInvalid);
+  const int n_items = fits ? g.head->n_items : 0;
+
+  // The softmax threads hold a row of scores each: registers move to them from the other warps.
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
+    // ------------------------------------------------------------ key and value tiles
+    Ring r;
+    bool ok = true;
+    const int nb_all = kKeyTile / p.box;
+    int in_flight = 0;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const WorkItem it = load_item(g.items + i);
+      ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool) {
+        if (!fresh) return true;
+        const int ti = tile_of(it, s, j);
+        int key0;
+        const int keys = tile_keys(it, g.prefix_len, ti, &key0);
+        const int32_t* table = ti < it.np ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+        const int boxes = (keys + p.box - 1) / p.box;
+        // one lane per box (a lane and its upper neighbours share one page id)
+        const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
+        int page = 0, off = 0;
+        if (bx < boxes && bx < nb_all) {
+          const int key = key0 + bx * p.box;
+          const int pi = key / g.page_size;
+          off = key - pi * g.page_size;
+          page = __ldg(table + pi);
+          if (page < 0 || page >= g.n_pages) {      // the copy would read zeros: report it
+            latch_status(status, kStatusRange);
+            page = 0;
+          }
+        }
+        if (!warp_wait(&bars->kv_empty[r.s], r.ph ^ 1u, bars, status)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.s], (uint32_t)(boxes * p.halves * p.box * 128));
+        __syncwarp();
+        uint8_t* dst = kv_smem + r.s * tile_bytes + hf * kHalfBytes + bx * p.box * 128;
+        if (bx < boxes)
+          tma_load_4d(dst, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64, off, it.group, page);
+        __syncwarp();
+        r.next(p.stages);
+        in_flight = min(in_flight + 1, p.stages);
+        return true;
+      });
+    }
+    if (!ok) {      // given up: wait for the copies that were issued before shared memory goes away
+      for (int i = 0; i < in_flight; ++i) {
+        const int st = (r.s + p.stages - 1 - i) % p.stages;
+        const uint32_t ph = st < r.s ? r.ph : r.ph ^ 1u;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test_wait(&bars->kv_full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      Ring r;
+      volatile int* ab = &bars->abort_flag;
+      const uint32_t q_addr = smem_u32(q_smem), kv_addr = smem_u32(kv_smem);
+      const uint32_t id_qk = idesc_f16(kRows, kKeyTile, 1);
+      const uint32_t id_pv = idesc_f16(kRows, (uint32_t)p.kd, 1) | (1u << 16);   // V is N-major
+      uint32_t q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {0, 0}, fix_ph = 0;
+      int k_st = 0, v_st = 0;          // stages of the shared key and value tile
+      bool ok = true;
+      for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+        const WorkItem it = load_item(g.items + i);
+        if (!mbar_wait(&bars->q_full, q_ph, ab, status)) { ok = false; break; }
+        q_ph ^= 1u;
+        ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool last) {
+          const int ti = tile_of(it, s, j);
+          int key0;
+          const int keys = tile_keys(it, g.prefix_len, ti, &key0);
+          if (value) {
+            if (!mbar_wait(&bars->p_full[s], p_ph[s], ab, status)) return false;
+            p_ph[s] ^= 1u;
+            if (j == 0) {
+              if (!mbar_wait(&bars->o_empty[s], oe_ph[s] ^ 1u, ab, status)) return false;
+              oe_ph[s] ^= 1u;
+            }
+          }
+          int st;
+          if (fresh) {
+            st = r.s;
+            if (!mbar_wait(&bars->kv_full[st], r.ph, ab, status)) return false;
+            if (value && (keys & 15)) {       // its last rows are cleared by another warp
+              if (!mbar_wait(&bars->kv_fixed[st], (fix_ph >> st) & 1u, ab, status)) return false;
+              fix_ph ^= 1u << st;
+            }
+            r.next(p.stages);
+            (value ? v_st : k_st) = st;
+          } else {
+            st = value ? v_st : k_st;
+          }
+          tc_fence_after();
+          const uint32_t tile = kv_addr + st * tile_bytes;
+          if (!value) {
+            const uint32_t qa = q_addr + (it.alt ? 0 : s) * tile_bytes;
+            for (int k = 0; k < p.kd / 16; ++k) {
+              const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
+              mma_f16_ss(tmem + s * kKeyTile, smem_desc_k_sw128(qa + o), smem_desc_k_sw128(tile + o), id_qk, k > 0);
+            }
+            mma_commit(&bars->s_full[s]);
+            if (last) mma_commit(&bars->kv_empty[st]);
+            // the item's last scores: the query rows may be replaced
+            if (it.n1 >= it.n0 ? s == 1 && j + 1 == it.n1 : s == 0 && j + 1 == it.n0) mma_commit(&bars->q_empty);
+          } else {
+            const int ks = (keys + 15) >> 4;
+            for (int k = 0; k < ks; ++k)
+              mma_f16_ts(tmem + kColO + s * kRows, tmem + s * kKeyTile + k * 8,
+                         smem_desc_mn_sw128(tile + k * 2048, kHalfBytes), id_pv, j > 0 || k > 0);
+            if (last) mma_commit(&bars->kv_empty[st]);
+            if (j + 1 == (s ? it.n1 : it.n0)) mma_commit(&bars->o_full[s]);
+          }
+          return true;
+        });
+        if (ok && it.n0 == 0 && it.n1 == 0) mma_commit(&bars->q_empty);
+      }
+      mma_commit(&bars->drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_test_wait(&bars->drain, 0) && global_timer_ns() - t0 < 2000000000ull) {}
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ query rows; ragged value tiles
+    Ring r;
+    uint32_t q_ph = 0;
+    bool ok = true;
+    const int mine = warp - 10;          // row tile
+    const int chunks = p.kd / 8;         // 16-byte pieces of a row, at most 16
+    const int c = lane & 15, rsub = lane >> 4;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const WorkItem it = load_item(g.items + i);
+      if (!warp_wait(&bars->q_empty, q_ph ^ 1u, bars, status)) break;
+      q_ph ^= 1u;
+      const int rows = min(kRows, it.nrows - mine * kRows);
+      if (max(it.n0, it.n1) > 0) {
+        uint8_t* dst = q_smem + mine * tile_bytes + (c >> 3) * kHalfBytes;
+        const int bytes = c * 8 < g.d ? 16 : 0;
+        int rr = it.row0 + mine * kRows + rsub;
+        int tok = rr / g.R, hh = rr - tok * g.R;
+        for (int row = rsub; row < rows; row += 2) {
+          const uint16_t* src = p.q + (int64_t)tok * p.q_stride + (it.group * g.R + hh) * g.d + (bytes ? c * 8 : 0);
+          if (c < chunks)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_u32(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4))),
+                         "l"(src), "r"(bytes)
+                         : "memory");
+          hh += 2;
+          while (hh >= g.R) {
+            hh -= g.R;
+            ++tok;
+          }
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
+      if (mine == 1)
+        ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool) {
+          if (!fresh) return true;
+          const int st = r.s;
+          const uint32_t ph = r.ph;
+          r.next(p.stages);
+          // every tile is waited for, so that this warp never trails a barrier by a whole round
+          if (!warp_wait(&bars->kv_full[st], ph, bars, status)) return false;
+          int key0;
+          const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
+          if (value && (keys & 15)) {
+            // rows keys .. the next multiple of 16: whole 128-byte rows, so the swizzle does not matter
+            const int rows_clear = 16 - (keys & 15);
+            uint8_t* tile = kv_smem + st * tile_bytes + keys * 128;
+            for (int q = lane; q < rows_clear * 8; q += 32)
+              for (int h = 0; h < p.halves; ++h)
+                *reinterpret_cast<uint4*>(tile + h * kHalfBytes + q * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->kv_fixed[st]);
+          }
+          if (lane == 0) mbar_arrive(&bars->kv_empty[st]);
+          return true;
+        });
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int s = warp >> 2;                         // stream
+    const int row = threadIdx.x & (kRows - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + s * kKeyTile;
+    const uint32_t tO = tmem + lane_base + kColO + s * kRows;
+    uint32_t s_ph = 0, o_ph = 0, m_ph = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const WorkItem it = load_item(g.items + i);
+      const int n = s ? it.n1 : it.n0;
+      const int r_item = row + (it.alt ? 0 : s * kRows);
+      const int rr = it.row0 + r_item;
+      const bool live = r_item < it.nrows;
+      const bool warp_live = (row & ~31) + (it.alt ? 0 : s * kRows) < it.nrows;
+      const int tok = rr / g.R;
+      // own keys in view of this row; padding rows see nothing at all
+      const int own_vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+      const bool blind = !live || (it.seq >= 0 && own_vis <= 0);
+      float m = -INFINITY, l = 0.f;                  // m: the maximum that O and l refer to
+      for (int j = 0; j < n; ++j) {
+        if (!warp_wait(&bars->s_full[s], s_ph, bars, status)) { ok = false; break; }
+        s_ph ^= 1u;
+        if (warp_live) {
+          tc_fence_after();
+          uint32_t v[128];
+          tmem_ld32(tS, v);
+          tmem_ld32(tS + 32, v + 32);
+          tmem_ld32(tS + 64, v + 64);
+          tmem_ld32(tS + 96, v + 96);
+          const int ti = tile_of(it, s, j);
+          int key0;
+          const int keys = tile_keys(it, g.prefix_len, ti, &key0);
+          int vis = ti < it.np ? keys : min(keys, own_vis - key0);
+          if (blind) vis = 0;
+          tmem_ld_wait();
+          if (__any_sync(0xffffffffu, vis < kKeyTile)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= vis) v[c] = 0xff800000u;      // -inf: chosen, not added, so a NaN behind the mask is gone
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 4]));
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 4])));
+          const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (j == 0) {
+            m = m_new;
+          } else {
+            const bool grow = (m_new - m) * p.scale_log2 > kRescale;
+            if (__any_sync(0xffffffffu, grow)) {
+              // the products of earlier tiles are done: S of this tile was issued after them
+              const float f = grow ? ex2((m - m_new) * p.scale_log2) : 1.f;
+              if (grow) m = m_new;
+              l *= f;
+              for (int c = 0; c < p.kd; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(tO + c, o);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+          const uint64_t sc2 = pk(p.scale_log2, p.scale_log2), ng2 = pk(neg, neg);
+          uint64_t sum0 = pk(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = unpk(fma2(pk_u(v[c + 2 * e], v[c + 2 * e + 1]), sc2, ng2));
+              const float a = ex2(x.x), b = ex2(x.y);
+              if (e & 1) sum1 = add2(sum1, pk(a, b));
+              else sum0 = add2(sum0, pk(a, b));
+              w[e] = bf16x2(a, b);
+            }
+            tmem_st16(tS + c / 2, w);
+          }
+          const float2 z = unpk(add2(sum0, sum1));
+          l += z.x + z.y;
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[s]);
+      }
+      if (!ok) break;
+      // ---- output.  Streams that share the rows are merged by stream 0's threads.
+      const bool merging = it.alt && it.n1 > 0;
+      if (n > 0) {
+        if (!warp_wait(&bars->o_full[s], o_ph, bars, status)) { ok = false; break; }
+        o_ph ^= 1u;
+      }
+      if (s == 1 && it.alt) {
+        if (n > 0) {
+          // stream 0 has read the previous item's (m, l): it freed this O, hence these products, afterwards
+          merge_ml[row] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->merge);
+        }
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (merging) {
+        // arrives after stream 1's last product, so its O is complete as well
+        if (!warp_wait(&bars->merge, m_ph, bars, status)) { ok = false; break; }
+        m_ph ^= 1u;
+        const float2 o = merge_ml[row];
+        const float mm = fmaxf(m, o.x);
+        if (mm != -INFINITY) {
+          f0 = ex2((m - mm) * p.scale_log2);
+          f1 = ex2((o.x - mm) * p.scale_log2);
+        }
+        l = l * f0 + o.y * f1;
+        m = mm;
+      }
+      if (warp_live) {
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;      // a row without keys: zero
+        f0 *= inv;
+        f1 *= inv;
+        tc_fence_after();
+        const int h = it.group * g.R + rr - tok * g.R;
+        const bool direct = it.part_row < 0;
+        uint16_t* ob = static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d;
+        float* of = g.part_out + (int64_t)(it.part_row + r_item) * g.d;
+        for (int c = 0; c < p.kd; c += 16) {
+          uint32_t o[16], o1[16];
+          float y[16];
+          if (n > 0) {
+            tmem_ld16(tO + c, o);
+            if (merging) tmem_ld16(tO + kRows + c, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              y[e] = __uint_as_float(o[e]) * f0;
+              if (merging) y[e] += __uint_as_float(o1[e]) * f1;
+              if (l == 0.f) y[e] = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 0.f;
+          }
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (c + q * 8 >= g.d) break;
+              if (direct) {
+                *reinterpret_cast<uint4*>(ob + c + q * 8) =
+                    make_uint4(bf16x2(y[q * 8], y[q * 8 + 1]), bf16x2(y[q * 8 + 2], y[q * 8 + 3]),
+                               bf16x2(y[q * 8 + 4], y[q * 8 + 5]), bf16x2(y[q * 8 + 6], y[q * 8 + 7]));
+              } else {
+                *reinterpret_cast<float4*>(of + c + q * 8) =
+                    make_float4(y[q * 8], y[q * 8 + 1], y[q * 8 + 2], y[q * 8 + 3]);
+                *reinterpret_cast<float4*>(of + c + q * 8 + 4) =
+                    make_float4(y[q * 8 + 4], y[q * 8 + 5], y[q * 8 + 6], y[q * 8 + 7]);
+              }
+            }
+          }
+        }
+        if (live) {
+          const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+          if (direct) {
+            if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+          } else {
+            g.part_lse[it.part_row + r_item] = lse;
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (n > 0) mbar_arrive(&bars->o_empty[s]);
+        if (merging) mbar_arrive(&bars->o_empty[1]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+
+// ---------------------------------------------------------------- fp32
+constexpr int kF32Threads = 256;
+constexpr int kF32Keys = 64;
+
+// One item of up to 16 * RT rows: thread (ty, tx) holds rows ty * RT .. + RT - 1,
+// scores of keys tx, tx + 16, .. and output columns 4 tx .. + 3 of each 64.  Scores go
+// through shared memory between the two products.  Bound by the fp32 FMA rate and
+// by shared-memory loads; meant for small shapes, like every fp32 path here.
+template <int RT>
+__device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
+  const StepGeom& g = p.g;
+  const int d = g.d, ld = d + 4;
+  constexpr int kR = 16 * RT;
+  float* qs = smem;                       // [kR][ld]
+  float* ks = qs + 64 * ld;               // [64][ld]
+  float* vs = ks + kF32Keys * ld;         // [64][ld]
+  float* ps = vs + kF32Keys * ld;         // [kR][68]
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float* q = reinterpret_cast<const float*>(p.q);
+  const int d4 = d / 4;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kR * d4; i += kF32Threads) {
+    const int r = i / d4, c = (i - r * d4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < it.nrows) {
+      const int rr = it.row0 + r, tok = rr / g.R;
+      v = *reinterpret_cast<const float4*>(q + (int64_t)tok * p.q_stride + (int64_t)(it.group * g.R + rr - tok * g.R) * d + c);
+    }
+    *reinterpret_cast<float4*>(qs + r * ld + c) = v;
+  }
+  float m[RT], l[RT], o[RT][8];
+  int own_vis[RT];
+#pragma unroll
+  for (int a = 0; a < RT; ++a) {
+    const int r = ty * RT + a, tok = (it.row0 + r) / g.R;
+    m[a] = -INFINITY;
+    l[a] = 0.f;
+    own_vis[a] = it.seq < 0 ? 1 : tok + it.own_off + 1;
+    if (r >= it.nrows) own_vis[a] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[a][e] = 0.f;
+  }
+  for (int j = 0; j < 2 * it.n0; ++j) {
+    const int ti = it.t0 + (j >> 1);
+    int key0;
+    int keys = tile_keys(it, g.prefix_len, ti, &key0);
+    key0 += (j & 1) * kF32Keys;
+    keys = min(keys - (j & 1) * kF32Keys, kF32Keys);
+    if (keys <= 0) continue;
+    const bool pre = ti < it.np;
+    const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kF32Keys * d4; i += kF32Threads) {
+      const int r = i / d4, c = (i - r * d4) * 4;
+      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      if (r < keys) {
+        const int key = key0 + r, pi = key / g.page_size;
+        const int page = __ldg(table + pi);
+        if (page >= 0 && page < g.n_pages) {
+          const int64_t at = page * p.page_stride + it.group * p.group_stride + (int64_t)(key - pi * g.page_size) * p.token_stride + c;
+          kv = *reinterpret_cast<const float4*>(p.kc + at);
+          vv = *reinterpret_cast<const float4*>(p.vc + at);
+        } else {
+          latch_status(&g.head->status, kStatusRange);
+        }
+      }
+      *reinterpret_cast<float4*>(ks + r * ld + c) = kv;
+      *reinterpret_cast<float4*>(vs + r * ld + c) = vv;
+    }
+    __syncthreads();
+    float sc[RT][4];
+#pragma unroll
+    for (int a = 0; a < RT; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) sc[a][b] = 0.f;
+    for (int c = 0; c < d; c += 4) {
+      float4 kf[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) kf[b] = *reinterpret_cast<const float4*>(ks + (tx + 16 * b) * ld + c);
+#pragma unroll
+      for (int a = 0; a < RT; ++a) {
+        const float4 qf = *reinterpret_cast<const float4*>(qs + (ty * RT + a) * ld + c);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          sc[a][b] += qf.x * kf[b].x + qf.y * kf[b].y + qf.z * kf[b].z + qf.w * kf[b].w;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < RT; ++a) {
+      int vis = pre ? keys : min(keys, own_vis[a] - key0);
+      if (own_vis[a] <= 0) vis = 0;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (tx + 16 * b >= vis) sc[a][b] = -INFINITY;
+        mx = fmaxf(mx, sc[a][b]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float m_new = fmaxf(m[a], mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float f = m[a] == -INFINITY ? 0.f : expf((m[a] - ref) * p.scale);
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float e = expf((sc[a][b] - ref) * p.scale);
+        sum += e;
+        ps[(ty * RT + a) * 68 + tx + 16 * b] = e;
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l[a] = l[a] * f + sum;
+      m[a] = m_new;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[a][e] *= f;
+    }
+    __syncwarp();      // a row's scores are written and read by the same half warp
+    for (int k = 0; k < keys; ++k) {
+      float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+      if (4 * tx < d) v0 = *reinterpret_cast<const float4*>(vs + k * ld + 4 * tx);
+      if (64 + 4 * tx < d) v1 = *reinterpret_cast<const float4*>(vs + k * ld + 64 + 4 * tx);
+#pragma unroll
+      for (int a = 0; a < RT; ++a) {
+        const float w = ps[(ty * RT + a) * 68 + k];
+        if (w == 0.f) continue;                 // masked: whatever lies there
+        o[a][0] += w * v0.x; o[a][1] += w * v0.y; o[a][2] += w * v0.z; o[a][3] += w * v0.w;
+        o[a][4] += w * v1.x; o[a][5] += w * v1.y; o[a][6] += w * v1.z; o[a][7] += w * v1.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < RT; ++a) {
+    const int r = ty * RT + a;
+    if (r >= it.nrows) continue;
+    const int rr = it.row0 + r, tok = rr / g.R, h = it.group * g.R + rr - tok * g.R;
+    const bool empty = l[a] == 0.f;
+    const float inv = empty ? 0.f : 1.f / l[a];
+    float* dst = it.part_row < 0 ? static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * d
+                                 : g.part_out + (int64_t)(it.part_row + r) * d;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int c = 64 * x + 4 * tx;
+      if (c >= d) continue;
+      *reinterpret_cast<float4*>(dst + c) =
+          empty ? make_float4(0.f, 0.f, 0.f, 0.f)
+                : make_float4(o[a][4 * x] * inv, o[a][4 * x + 1] * inv, o[a][4 * x + 2] * inv, o[a][4 * x + 3] * inv);
+    }
+    if (tx == 0) {
+      const float lse = empty ? -INFINITY : m[a] * p.scale + logf(l[a]);
+      if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
+      else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+    }
+  }
+}
+
+size_t f32_smem_bytes(int d) { return (size_t)(64 * (d + 4) * 3 + 64 * 68) * 4; }
+
+__global__ void __launch_bounds__(kF32Threads) attention_f32_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  pdl_enter();
+  const StepGeom& g = p.g;
+  if (!plan_matches(g)) {
+    if (threadIdx.x == 0) latch_status(&g.head->status, kStatusInvalid);
+    return;
+  }
+  const int n = g.head->n_items;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const WorkItem it = load_item(g.items + i);
+    if (it.nrows <= 16) f32_item<1>(p, it, reinterpret_cast<float*>(smem_raw));
+    else f32_item<4>(p, it, reinterpret_cast<float*>(smem_raw));
+  }
+}
+
+// ---------------------------------------------------------------- join
+__device__ __forceinline__ void put4(float* dst, float4 v) { *reinterpret_cast<float4*>(dst) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16* dst, float4 v) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+}
+
+// One warp per row (token, head): out = sum_p w_p out_p / sum_p w_p, w_p = exp(lse_p - max lse),
+// over the row's parts in a fixed order.  Rows that an item wrote whole are skipped; padding is zero.
+template <typename E>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
+  pdl_enter();
+  const StepGeom& g = p.g;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (at >= (int64_t)g.T * g.H || !plan_matches(g) || g.head->n_items < 0) return;
+  const int t = (int)(at / g.H), h = (int)(at - (int64_t)t * g.H);
+  const int group = h / g.R, rr = t * g.R + h - group * g.R;
+  const TokenInfo ti = g.tok[t];
+  const PlanHeader& hd = *g.head;
+  int n_pre = 0, pre0 = 0, pre_step = 0, n_own = 0, own0 = 0, own_step = 0;
+  if (ti.seq >= 0 && (ti.own >= 0 || !g.separate)) {
+    const SeqInfo si = g.seq[ti.seq];
+    const SeqShape s = seq_shape(g, si.q0, si.q1, si.kv);
+    const int local = rr - s.q0 * g.R, k = local / s.tr;
+    const int tiles = key_tiles(g, s, (k + 1) * s.tr);
+    int per;
+    n_own = job_parts(tiles, s.tr > 128 ? 2 : 1, hd.unit, &per);
+    if (n_own == 1 && !g.separate) return;
+    if (tiles == 0) n_own = 0;
+    own_step = s.nt == 1 ? s.rows : s.tr;
+    own0 = si.part_row + (group * s.nt + k) * si.parts * own_step + local - k * s.tr;
+    if (g.separate) {
+      const int kp = rr / g.prefix_rows;
+      n_pre = hd.prefix_parts;
+      pre_step = g.prefix_rows;
+      pre0 = (group * g.prefix_tiles + kp) * n_pre * pre_step + rr - kp * pre_step;
+    }
+  }
+  const int n = n_pre + n_own;
+  auto row_of = [&](int i) { return i < n_pre ? pre0 + i * pre_step : own0 + (i - n_pre) * own_step; };
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < n; i += 32) {
+    const float x = g.part_lse[row_of(i)];
+    nan |= x != x;
+    mx = fmaxf(mx, x);
+  }
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float w_mine = i0 + lane < n ? expf(g.part_lse[row_of(i0 + lane)] - ref) : 0.f;
+    const int upto = min(32, n - i0);
+    for (int i = 0; i < upto; ++i) {
+      const float w = __shfl_sync(0xffffffffu, w_mine, i);
+      if (w == 0.f) continue;                  // an empty part's row
+      sum += w;
+      if (4 * lane < g.d) {
+        const float4 v = *reinterpret_cast<const float4*>(g.part_out + (int64_t)row_of(i0 + i) * g.d + 4 * lane);
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (4 * lane < g.d)
+    put4(static_cast<E*>(p.out) + at * g.d + 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : ref + logf(sum);
+}
+
+}  // namespace
+}  // namespace aff
+
+using namespace aff;
+
+extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride, const aff_kv_cache* cache,
+                                                const aff_step* step, float scale, void* out, float* lse, void* plan,
+                                                size_t plan_bytes, aff_stream_t stream) {
+  AttnParams p{};
+  aff_status st = step_geom(step, cache, plan, &p.g);
+  if (st != AFF_OK) return st;
+  const StepGeom& g = p.g;
+  if (!q || !out || q_stride < (int64_t)g.H * g.d) return AFF_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return AFF_ERR_INVALID_ARG;
+  if (g.d > 128) return AFF_ERR_UNSUPPORTED_SHAPE;
+  const int es = g.dtype == AFF_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u || q_stride * es % 16 ||
+      reinterpret_cast<uintptr_t>(lse) & 3u)
+    return AFF_ERR_ALIGNMENT;
+  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AFF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.out = out;
+  p.lse = lse;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.kc = static_cast<const float*>(cache->k);
+  p.vc = static_cast<const float*>(cache->v);
+  p.page_stride = cache->page_stride;
+  p.group_stride = cache->group_stride;
+  p.token_stride = cache->token_stride;
+  const unsigned grid = (unsigned)(g.max_items < sms ? g.max_items : sms);
+  if (g.dtype == AFF_FP32) {
+    const size_t smem = f32_smem_bytes(g.d);
+    AFF_CUDA(cudaFuncSetAttribute(attention_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    AFF_CUDA(launch_pdl(attention_f32_kernel, grid * 2, kF32Threads, smem, s, p));
+  } else {
+    p.halves = g.d > 64 ? 2 : 1;
+    p.kd = (g.d + 15) / 16 * 16;
+    p.box = 128;
+    while (g.page_size % p.box) p.box /= 2;       // page_size % 8 == 0: at least 8
+    const int tile = p.halves * kHalfBytes;
+    const int fixed = 1024 + 2 * tile + kRows * (int)sizeof(float2) + (int)sizeof(Bars);
+    p.stages = (kSmemMax - fixed) / tile;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    const int smem = fixed + p.stages * tile;
+    CUtensorMap mk, mv;
+    const uint64_t dims[4] = {(uint64_t)g.d, (uint64_t)g.page_size, (uint64_t)g.G, (uint64_t)g.n_pages};
+    const uint64_t str[3] = {(uint64_t)cache->token_stride * 2, (uint64_t)cache->group_stride * 2,
+                             (uint64_t)cache->page_stride * 2};
+    if ((st = map_16bit_sw128(&mk, cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
+    if ((st = map_16bit_sw128(&mv, cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
+    // The register split needs the launch to own 168 registers a thread: 2 x 208 + 88 = 3 x 168.
+    static const cudaError_t ready = [] {
+      cudaFuncAttributes fa;
+      cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel);
+      if (e == cudaSuccess && fa.numRegs != 168) e = cudaErrorInvalidConfiguration;
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+      return e;
+    }();
+    AFF_CUDA(ready);
+    AFF_CUDA(launch_pdl(attention_kernel, grid, kThreads, (size_t)smem, s, mk, mv, p));
+  }
+  if (g.may_split) {
+    const unsigned blocks = (unsigned)(((int64_t)g.T * g.H + 7) / 8);
+    if (g.dtype == AFF_BF16) AFF_CUDA(launch_pdl(join_kernel<__nv_bfloat16>, blocks, 256, 0, s, p));
+    else AFF_CUDA(launch_pdl(join_kernel<float>, blocks, 256, 0, s, p));
+  }
+  return AFF_OK;
+}

@@ -4,6 +4,7 @@
 
 #include "affinity.h"
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace aff {
@@ -15,6 +16,11 @@ aff_status cuda_fail(cudaError_t e, const char* where);
 // AFF_OK with the SM count when the current device is an sm_103 part;
 // AFF_ERR_ARCH otherwise (also when there is no device).
 aff_status check_device(int* sm_count);
+
+// Tensor map of a 16-bit tensor of `rank` dims (dims[0] innermost, contiguous; strides in bytes),
+// 128 B swizzle, box = 64 innermost elements x box1 in dimension box1_dim; out of bounds reads zero.
+aff_status map_16bit_sw128(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                           uint32_t box1, int box1_dim);
 
 }  // namespace aff
 

@@ -1,0 +1,150 @@
+// step.cuh -- the plan of one forward step: where each of its tokens stands,
+// and the attention's work items.  Written by affinity_step_plan (step_plan.cu),
+// read by affinity_kv_append (kv_append.cu) and affinity_prefix_attention
+// (attention.cu) of every layer of the step.
+//
+// Rows.  Attention works on packed rows: row t * R + r of KV group g is query
+// head g * R + r of token t, R = H / G.  The heads of a group share its keys and
+// values, so a tile of rows meets each key tile once.
+//
+// Jobs and items.  A job is a tile of rows of one group against a run of key
+// tiles (128 keys each).  A sequence's rows are cut into tiles of `big` rows (of
+// `small` rows, one tile, when it has no more than that).  The shared prefix is
+// read in one of two ways, chosen on the host from the shapes alone:
+//   separate   its own jobs, whose row tiles run across sequences, so each key
+//              tile of the prefix is loaded once per `big` rows of the whole
+//              batch; a row then has parts from the prefix and from its own keys;
+//   joined     as the first key tiles of every sequence's own jobs.
+// Jobs longer than `unit` are cut into items along the keys; an item that is
+// its rows' only one writes the output, the others write partial rows (fp32
+// output and log-sum-exp), which the join kernel merges.
+#pragma once
+
+#include "affinity.h"
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace aff {
+
+constexpr int kKeyTile = 128;
+constexpr int kPlanSms = 152;            // SMs of a GB300: sizes the plan without a device
+constexpr uint32_t kPlanMagic = 0x41465331u;
+
+struct TokenInfo {       // one per token of the step; 16 bytes
+  int64_t slot;          // page * page_size + offset of its own key, -1: padding
+  int32_t own;           // index among its sequence's own tokens, -1: padding
+  int32_t seq;           // its sequence, -1: none
+};
+
+struct SeqInfo {         // one per sequence, for the join: what the plan was made from; 32 bytes
+  int32_t q0, q1, kv;    // its tokens of the step, its own keys
+  int32_t part_row;      // first partial row
+  int32_t parts;         // partial rows' stride in parts: the most parts a tile of its rows has
+  int32_t reserved[3];
+};
+
+struct WorkItem {        // 48 bytes
+  int32_t row0, nrows, group, seq;   // packed rows row0 .. +nrows of `group`; seq -1: prefix alone, or padding
+  int32_t t0, n0, n1, part_row;      // first key tile; tiles of stream 0 and 1; partial row of row0 (-1: the output)
+  int32_t own_off, own_len, alt, np; // own index = token + own_off; own keys in view; see below; prefix tiles before own tiles
+};
+// alt == 0: stream s holds rows s*128 .. of the item and walks tiles t0 .. t0 + n_s - 1.
+// alt == 1: at most 128 rows; both streams hold them, stream s walks tiles t0 + s, t0 + s + 2, ...
+
+struct PlanHeader {      // at the start of the plan buffer; its first word is the status word
+  uint32_t status;
+  uint32_t magic;
+  int32_t n_items;       // -1: the step was malformed
+  int32_t unit;          // most cost (key tiles x streams) of an item; 0: jobs are not cut
+  int32_t prefix_parts;  // separate: parts of each prefix job
+  int32_t prefix_per;    // separate: key tiles of each part
+  int32_t key[10];       // the geometry it was made for
+};
+
+// Everything the kernels need to know of the step, by value.
+struct StepGeom {
+  int32_t T, B, H, G, R, d;
+  int32_t page_size, dtype;
+  int32_t pages_stride, prefix_len;
+  int32_t np;            // key tiles of the prefix
+  int32_t separate;      // the prefix has jobs of its own
+  int32_t may_split;     // jobs may be cut (then the join kernel runs)
+  int32_t small, big;    // row tiles
+  int32_t prefix_rows;   // row tile of the prefix's jobs
+  int32_t prefix_tiles;  // row tiles of the prefix's jobs
+  int32_t max_items, max_part_rows;
+  int64_t n_pages;
+  const int32_t *q_start, *kv_len, *pages, *prefix_pages;
+  // plan buffer
+  PlanHeader* head;
+  TokenInfo* tok;
+  SeqInfo* seq;
+  WorkItem* items;
+  float* part_lse;
+  float* part_out;
+  size_t bytes;
+};
+
+// Validates (step, cache) and lays the plan out over `plan` (may be null).
+aff_status step_geom(const aff_step* step, const aff_kv_cache* cache, void* plan, StepGeom* g);
+
+// The plan buffer of a call: present, aligned, large enough.
+aff_status check_plan(const StepGeom& g, const void* plan, size_t plan_bytes);
+
+#ifdef __CUDACC__
+__host__ __device__ inline int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
+
+struct SeqShape {        // what a sequence's jobs are cut from
+  int32_t q0, q1, kv, rows, tr, nt;
+};
+
+__device__ __forceinline__ SeqShape seq_shape(const StepGeom& g, int q0, int q1, int kv) {
+  SeqShape s;
+  s.q0 = q0;
+  s.q1 = q1;
+  s.kv = kv;
+  s.rows = (q1 - q0) * g.R;
+  s.tr = s.rows <= g.small ? g.small : g.big;
+  s.nt = (s.rows + s.tr - 1) / s.tr;
+  return s;
+}
+
+// As the step's arrays give it (planning only: later kernels go by the plan).
+__device__ __forceinline__ SeqShape seq_shape(const StepGeom& g, int b) {
+  const int q0 = min(max(g.q_start[b], 0), g.T);
+  const int q1 = min(max(g.q_start[b + 1], q0), g.T);
+  const int64_t room = (int64_t)g.pages_stride * g.page_size;
+  return seq_shape(g, q0, q1, (int)min((int64_t)max(g.kv_len[b], 0), room));
+}
+
+// Own keys that the last of the first `upto` rows of a sequence sees.
+__device__ __forceinline__ int keys_in_view(const StepGeom& g, const SeqShape& s, int upto) {
+  const int last = (min(upto, s.rows) - 1) / g.R;
+  return min(max(s.kv - (s.q1 - s.q0) + last + 1, 0), s.kv);
+}
+
+// Key tiles that the first `upto` rows of a sequence meet in its own jobs.
+__device__ __forceinline__ int key_tiles(const StepGeom& g, const SeqShape& s, int upto) {
+  const int v = keys_in_view(g, s, upto);
+  return v == 0 ? 0 : (v + kKeyTile - 1) / kKeyTile + (g.separate ? 0 : g.np);
+}
+
+// Parts of a job of `tiles` key tiles, `streams` row tiles at a time, and the key tiles of each.
+__device__ __forceinline__ int job_parts(int tiles, int streams, int unit, int* per) {
+  int parts = unit > 0 && tiles > 0 ? (tiles * streams + unit - 1) / unit : 1;
+  if (parts > tiles) parts = tiles > 0 ? tiles : 1;
+  *per = tiles > 0 ? (tiles + parts - 1) / parts : 0;
+  return *per > 0 ? (tiles + *per - 1) / *per : 1;
+}
+
+__device__ __forceinline__ bool plan_matches(const StepGeom& g) {
+  const PlanHeader& h = *g.head;
+  return h.magic == kPlanMagic && h.key[0] == g.T && h.key[1] == g.B && h.key[2] == g.H && h.key[3] == g.G &&
+         h.key[4] == g.d && h.key[5] == g.page_size && h.key[6] == g.pages_stride && h.key[7] == g.prefix_len &&
+         h.key[8] == g.dtype && h.key[9] == (int)min(g.n_pages, (int64_t)INT32_MAX);
+}
+#endif
+
+}  // namespace aff

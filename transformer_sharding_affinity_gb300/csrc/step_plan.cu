@@ -1,0 +1,398 @@
+// step_plan.cu -- affinity_step_plan: one launch that writes a step's plan
+// (step.cuh).  Block 0 cuts the jobs; the other blocks fill the token table.
+#include "affinity.h"
+#include "internal.h"
+#include "launch.cuh"
+#include "sm103_primitives.cuh"
+#include "step.cuh"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+namespace aff {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kItemsPerSm = 4;    // items that a cut aims at for each SM
+constexpr int kMinUnit = 4;       // least cost of an item when jobs are cut
+
+__device__ int64_t warp_sum(int64_t v) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the block; the result is in every thread.
+__device__ int64_t block_sum(int64_t v, int64_t* sh) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(sh[threadIdx.x & 31]);
+}
+
+__device__ int warp_inclusive(int v) {
+  const int lane = threadIdx.x & 31;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// A sequence's (row tile, group) pairs, late row tiles first: they have the most keys.
+struct Job {
+  int k, group, tiles, parts, per, streams;
+};
+
+__device__ __forceinline__ Job job_of(const StepGeom& g, const SeqShape& s, int i, int unit) {
+  Job j;
+  j.k = s.nt - 1 - i / g.G;
+  j.group = i % g.G;
+  j.streams = s.tr > 128 ? 2 : 1;
+  j.tiles = key_tiles(g, s, (j.k + 1) * s.tr);
+  j.parts = job_parts(j.tiles, j.streams, unit, &j.per);
+  if (j.tiles == 0 && g.separate) j.parts = 0;     // the join writes such rows
+  return j;
+}
+
+__device__ void plan_items(const StepGeom& g) {
+  __shared__ int64_t wide_sh[32];
+  __shared__ int sh[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the batch as given: starts in order, from 0, within the step
+  int bad = 0;
+  for (int b = threadIdx.x; b < g.B; b += kThreads) {
+    const int q0 = g.q_start[b], q1 = g.q_start[b + 1], kv = g.kv_len[b];
+    if ((b == 0 && q0 != 0) || q1 < q0 || q1 > g.T || kv < 0 || kv > (int64_t)g.pages_stride * g.page_size) bad = 1;
+  }
+  if (block_sum(bad, wide_sh)) {
+    if (threadIdx.x == 0) {
+      g.head->n_items = -1;
+      latch_status(&g.head->status, kStatusRange);
+    }
+    return;
+  }
+
+  // ---- the cost of all jobs, in key tiles x streams, and from it the most cost of an item
+  const int prefix_streams = g.prefix_rows > 128 ? 2 : 1;
+  int unit = 0;
+  if (g.may_split) {
+    int64_t cost = 0;      // of one group; warp w takes sequences w, w + 32, ...
+    for (int b = warp; b < g.B; b += kThreads / 32) {
+      const SeqShape s = seq_shape(g, b);
+      for (int k = lane; k < s.nt; k += 32)
+        cost += (int64_t)key_tiles(g, s, (k + 1) * s.tr) * (s.tr > 128 ? 2 : 1);
+    }
+    cost = block_sum(cost, wide_sh) + (int64_t)g.prefix_tiles * g.np * prefix_streams;
+    const int64_t aim = kPlanSms * kItemsPerSm;
+    unit = (int)min(max((int64_t)kMinUnit, (cost * g.G + aim - 1) / aim), (int64_t)INT32_MAX / 4);
+  }
+
+  // ---- the smallest unit (by doubling) whose partial rows and items fit; uncut jobs always do
+  int prefix_parts = 0, prefix_per = 0;
+  for (;;) {
+    if (g.separate) prefix_parts = job_parts(g.np, prefix_streams, unit, &prefix_per);
+    if (unit == 0) break;
+    int64_t rows = 0, items = 0;
+    for (int b = threadIdx.x; b < g.B; b += kThreads) {
+      const SeqShape s = seq_shape(g, b);
+      if (s.rows == 0) continue;
+      int per;
+      const int most = job_parts(key_tiles(g, s, s.rows), s.tr > 128 ? 2 : 1, unit, &per);
+      if (g.separate || most > 1) rows += (int64_t)most * g.G * (s.nt == 1 ? s.rows : s.nt * s.tr);
+      items += (int64_t)most * s.nt * g.G;
+    }
+    const int64_t prefix_jobs = (int64_t)prefix_parts * g.prefix_tiles * g.G;
+    rows = block_sum(rows, wide_sh) + prefix_jobs * g.prefix_rows;
+    items = block_sum(items, wide_sh) + prefix_jobs;
+    if (rows <= g.max_part_rows && items <= g.max_items) break;
+    unit = unit > (1 << 28) ? 0 : unit * 2;
+  }
+
+  // ---- first item and first partial row of every sequence
+  const int prefix_items = prefix_parts * g.prefix_tiles * g.G;
+  int item_base = prefix_items;
+  int row_base = prefix_parts * g.prefix_tiles * g.prefix_rows * g.G;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {         // 32 sequences at a time, one per warp
+    const int b = b0 + warp;
+    int n_items = 0, n_rows = 0, most = 0;
+    if (b < g.B) {
+      const SeqShape s = seq_shape(g, b);
+      const int n_jobs = s.nt * g.G;
+      for (int i = lane; i < n_jobs; i += 32) n_items += job_of(g, s, i, unit).parts;
+      n_items = __reduce_add_sync(0xffffffffu, n_items);
+      if (s.rows > 0) {
+        int per;
+        most = job_parts(key_tiles(g, s, s.rows), s.tr > 128 ? 2 : 1, unit, &per);
+        if (g.separate || most > 1) n_rows = most * g.G * (s.nt == 1 ? s.rows : s.nt * s.tr);
+      }
+    }
+    __syncthreads();
+    if (lane == 0) sh[warp] = n_items;
+    __syncthreads();
+    const int it_incl = warp_inclusive(sh[lane]);
+    __syncthreads();
+    if (lane == 0) sh[warp] = n_rows;
+    __syncthreads();
+    const int ro_incl = warp_inclusive(sh[lane]);
+    const int it0 = item_base + __shfl_sync(0xffffffffu, it_incl, warp) - n_items;
+    const int ro0 = row_base + __shfl_sync(0xffffffffu, ro_incl, warp) - n_rows;
+    item_base += __shfl_sync(0xffffffffu, it_incl, 31);
+    row_base += __shfl_sync(0xffffffffu, ro_incl, 31);
+    if (b >= g.B) continue;                       // whole warps only
+    const SeqShape s = seq_shape(g, b);
+    if (lane == 0) g.seq[b] = SeqInfo{s.q0, s.q1, s.kv, ro0, most, {0, 0, 0}};
+    // ---- its items
+    const int n_jobs = s.nt * g.G;
+    int at = it0;
+    for (int i0 = 0; i0 < n_jobs; i0 += 32) {
+      const int i = i0 + lane;
+      Job j{};
+      if (i < n_jobs) j = job_of(g, s, i, unit);
+      const int incl = warp_inclusive(j.parts);
+      int w = at + incl - j.parts;
+      at += __shfl_sync(0xffffffffu, incl, 31);
+      if (i >= n_jobs) continue;
+      const int r0 = j.k * s.tr;
+      const int nrows = min(s.tr, s.rows - r0);
+      const int slot_rows = s.nt == 1 ? s.rows : s.tr;
+      const bool direct = j.parts == 1 && !g.separate;
+      const int alt = nrows <= 128 && g.dtype == AFF_BF16;
+      const int first = key_tiles(g, s, r0 + 128);    // key tiles that stream 0's rows meet
+      for (int p = 0; p < j.parts; ++p, ++w) {
+        if (w >= g.max_items) break;
+        WorkItem it;
+        it.row0 = s.q0 * g.R + r0;
+        it.nrows = nrows;
+        it.group = j.group;
+        it.seq = b;
+        it.t0 = p * j.per;
+        const int n = min(j.per, j.tiles - it.t0);
+        if (g.dtype != AFF_BF16) {
+          it.n0 = n;
+          it.n1 = 0;
+        } else if (alt) {
+          it.n0 = (n + 1) / 2;
+          it.n1 = n / 2;
+        } else {
+          it.n0 = min(max(first - it.t0, 0), n);
+          it.n1 = n;
+        }
+        it.part_row = direct ? -1 : ro0 + ((j.group * s.nt + j.k) * most + p) * slot_rows;
+        it.own_off = s.kv - s.q1;                  // token t has own index kv - (q1 - q0) + t - q0
+        it.own_len = keys_in_view(g, s, r0 + nrows);
+        it.alt = alt;
+        it.np = g.separate ? 0 : g.np;
+        g.items[w] = it;
+      }
+    }
+  }
+
+  // ---- the prefix's items: row tiles of one key run next to each other, then groups, then runs
+  for (int i = threadIdx.x; i < prefix_items; i += kThreads) {
+    if (i >= g.max_items) break;
+    const int k = i % g.prefix_tiles, rest = i / g.prefix_tiles;
+    const int group = rest % g.G, p = rest / g.G;
+    WorkItem it;
+    it.row0 = k * g.prefix_rows;
+    it.nrows = min(g.prefix_rows, g.T * g.R - it.row0);
+    it.group = group;
+    it.seq = -1;
+    it.t0 = p * prefix_per;
+    const int n = min(prefix_per, g.np - it.t0);
+    it.alt = it.nrows <= 128 && g.dtype == AFF_BF16;
+    it.n0 = it.alt ? (n + 1) / 2 : n;
+    it.n1 = it.alt ? n / 2 : (g.dtype == AFF_BF16 ? n : 0);
+    it.part_row = ((group * g.prefix_tiles + k) * prefix_parts + p) * g.prefix_rows;
+    it.own_off = 0;
+    it.own_len = 0;
+    it.np = g.np;
+    g.items[i] = it;
+  }
+
+  // ---- rows of tokens that belong to no sequence: the output is zero (the join writes it when it runs)
+  const int tail = g.T - min(max(g.q_start[g.B], 0), g.T);
+  if (tail > 0 && !g.may_split && !g.separate) {
+    const int row0 = (g.T - tail) * g.R, n = ceil_div_i(tail * g.R, g.big);
+    for (int i = threadIdx.x; i < n * g.G; i += kThreads) {
+      if (item_base + i >= g.max_items) break;
+      const int k = i / g.G;
+      WorkItem it{};
+      it.row0 = row0 + k * g.big;
+      it.nrows = min(g.big, g.T * g.R - it.row0);
+      it.group = i % g.G;
+      it.seq = -1;
+      it.part_row = -1;
+      g.items[item_base + i] = it;
+    }
+    item_base += n * g.G;
+  }
+  if (threadIdx.x == 0) {
+    PlanHeader& h = *g.head;
+    h.n_items = min(item_base, g.max_items);
+    h.unit = unit;
+    h.prefix_parts = prefix_parts;
+    h.prefix_per = prefix_per;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) step_plan_kernel(const __grid_constant__ StepGeom g) {
+  pdl_enter();
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      PlanHeader& h = *g.head;
+      const int key[10] = {g.T, g.B, g.H, g.G, g.d, g.page_size, g.pages_stride, g.prefix_len, g.dtype,
+                           (int)min(g.n_pages, (int64_t)INT32_MAX)};
+      for (int i = 0; i < 10; ++i) h.key[i] = key[i];
+      h.magic = kPlanMagic;
+    }
+    plan_items(g);
+    return;
+  }
+  // the token table: the last sequence that starts at or before the token, if it holds it
+  const int t = (blockIdx.x - 1) * kThreads + threadIdx.x;
+  if (t >= g.T) return;
+  TokenInfo ti{-1, -1, -1};
+  int lo = 0, hi = g.B;            // q_start[lo] <= t < q_start[hi] when the starts are in order
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.q_start[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int q0 = g.q_start[lo], q1 = g.q_start[lo + 1], kv = g.kv_len[lo];
+  if (t >= q0 && t < q1) {
+    const int64_t own = (int64_t)kv - (q1 - q0) + (t - q0);
+    ti.seq = lo;
+    if (own >= 0 && own < (int64_t)g.pages_stride * g.page_size) {
+      const int page = g.pages[(int64_t)lo * g.pages_stride + own / g.page_size];
+      if (page >= 0 && page < g.n_pages) {
+        ti.own = (int)own;
+        ti.slot = (int64_t)page * g.page_size + own % g.page_size;
+      } else {
+        latch_status(&g.head->status, kStatusRange);
+      }
+    }
+  }
+  g.tok[t] = ti;
+}
+
+}  // namespace
+
+aff_status check_plan(const StepGeom& g, const void* plan, size_t plan_bytes) {
+  if (!plan || plan_bytes < g.bytes || (reinterpret_cast<uintptr_t>(plan) & 255u)) return AFF_ERR_WORKSPACE;
+  return AFF_OK;
+}
+
+aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, StepGeom* out) {
+  if (!st || !c) return AFF_ERR_INVALID_ARG;
+  if (c->dtype != AFF_BF16 && c->dtype != AFF_FP32) return AFF_ERR_UNSUPPORTED_DTYPE;
+  if (!c->k || !c->v || !st->q_start || !st->kv_len || !st->pages) return AFF_ERR_INVALID_ARG;
+  if (c->G < 1 || c->page_size < 1 || c->d_head < 1 || c->n_pages < 1 || st->T < 1 || st->B < 1 || st->H < 1 ||
+      st->pages_stride < 1 || st->prefix_len < 0 || (st->prefix_len > 0 && !st->prefix_pages))
+    return AFF_ERR_INVALID_ARG;
+  const int es = c->dtype == AFF_BF16 ? 2 : 4;
+  const int64_t lim = (int64_t)1 << 30;
+  if (st->H % c->G || st->H > 4096 || c->d_head > 256 || c->d_head * es % 16 || c->page_size % 8 ||
+      c->page_size > (1 << 20) || c->n_pages > INT32_MAX || st->T > lim / st->H || st->B > (1 << 20) ||
+      st->prefix_len > lim || st->pages_stride > lim / c->page_size)
+    return AFF_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_stride < 0 || c->group_stride < 0 || c->token_stride < c->d_head) return AFF_ERR_INVALID_ARG;
+  if (c->page_stride * es % 16 || c->group_stride * es % 16 || c->token_stride * es % 16) return AFF_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15u) return AFF_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(st->q_start) | reinterpret_cast<uintptr_t>(st->kv_len) |
+       reinterpret_cast<uintptr_t>(st->pages) | reinterpret_cast<uintptr_t>(st->prefix_pages)) & 3u)
+    return AFF_ERR_ALIGNMENT;
+  StepGeom g{};
+  g.T = (int)st->T;
+  g.B = st->B;
+  g.H = st->H;
+  g.G = c->G;
+  g.R = st->H / c->G;
+  g.d = c->d_head;
+  g.page_size = c->page_size;
+  g.dtype = c->dtype;
+  g.pages_stride = (int)st->pages_stride;
+  g.prefix_len = (int)st->prefix_len;
+  g.n_pages = c->n_pages;
+  g.q_start = st->q_start;
+  g.kv_len = st->kv_len;
+  g.pages = st->pages;
+  g.prefix_pages = st->prefix_pages;
+  g.np = (g.prefix_len + kKeyTile - 1) / kKeyTile;
+  const bool bf = c->dtype == AFF_BF16;
+  g.small = bf ? 128 : 16;
+  g.big = bf ? 256 : 64;
+  const int64_t rows = (int64_t)g.T * g.R;
+  // Jobs of its own for the prefix: worth it while sequences have few rows, so that a
+  // row tile of one sequence would leave most of a tile idle for every key of the prefix.
+  g.separate = g.prefix_len > 0 && g.B > 1 && rows < (int64_t)g.B * g.small;
+  g.prefix_rows = rows <= g.small ? g.small : g.big;
+  g.prefix_tiles = g.separate ? (int)((rows + g.prefix_rows - 1) / g.prefix_rows) : 0;
+  // Most (row tile, group) pairs: each sequence ends in at most one part-filled tile.
+  const int64_t tiles = rows / g.big + g.B + 1;
+  const int64_t jobs = (tiles + g.prefix_tiles) * g.G;
+  const int64_t full = rows / g.big * g.G;
+  g.may_split = g.separate || full < 2 * kPlanSms;
+  const int64_t items = 2 * jobs + kPlanSms * kItemsPerSm + 2 * g.G + 64;
+  int64_t part_rows = 0;
+  if (g.may_split) {
+    // Uncut jobs: with the prefix apart every row has a part from the prefix and one of its own
+    // (a sequence of several row tiles rounds up to whole ones); joined, they write the output.
+    // On top of that, room for cuts.
+    const int64_t multi = std::min<int64_t>(g.B, rows / g.small + 1);
+    part_rows = (int64_t)kPlanSms * 2 * g.big;
+    if (g.separate) part_rows += ((int64_t)g.prefix_tiles * g.prefix_rows + rows + multi * g.big) * g.G;
+  }
+  if (items > INT32_MAX / 64 || part_rows > INT32_MAX / 2) return AFF_ERR_UNSUPPORTED_SHAPE;
+  g.max_items = (int)items;
+  g.max_part_rows = (int)part_rows;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  uint8_t* base = static_cast<uint8_t*>(plan);
+  g.head = reinterpret_cast<PlanHeader*>(base + take(256));
+  g.tok = reinterpret_cast<TokenInfo*>(base + take((size_t)g.T * sizeof(TokenInfo)));
+  g.seq = reinterpret_cast<SeqInfo*>(base + take((size_t)g.B * sizeof(SeqInfo)));
+  g.items = reinterpret_cast<WorkItem*>(base + take((size_t)g.max_items * sizeof(WorkItem)));
+  g.part_lse = reinterpret_cast<float*>(base + take((size_t)part_rows * 4));
+  g.part_out = reinterpret_cast<float*>(base + take((size_t)part_rows * g.d * 4));
+  g.bytes = off;
+  *out = g;
+  return AFF_OK;
+}
+
+}  // namespace aff
+
+using namespace aff;
+
+extern "C" {
+
+aff_status affinity_step_plan_size(const aff_step* step, const aff_kv_cache* cache, size_t* bytes) {
+  if (!bytes) return AFF_ERR_INVALID_ARG;
+  StepGeom g;
+  aff_status st = step_geom(step, cache, nullptr, &g);
+  if (st != AFF_OK) return st;
+  *bytes = g.bytes;
+  return AFF_OK;
+}
+
+aff_status affinity_step_plan(const aff_step* step, const aff_kv_cache* cache, void* plan, size_t plan_bytes,
+                              aff_stream_t stream) {
+  StepGeom g;
+  aff_status st = step_geom(step, cache, plan, &g);
+  if (st != AFF_OK) return st;
+  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AFF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  AFF_CUDA(cudaMemsetAsync(plan, 0, sizeof(PlanHeader), s));
+  AFF_CUDA(launch_pdl(step_plan_kernel, 1 + (g.T + kThreads - 1) / kThreads, kThreads, 0, s, g));
+  return AFF_OK;
+}
+
+}  // extern "C"
