@@ -211,7 +211,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building the Stream object of torch.cuda.current_stream() takes microseconds
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -220,8 +221,8 @@ def _stream(stream) -> Optional[int]:
 def _ws_bytes(workspace, workspace_bytes):
     if workspace_bytes is not None:
         return int(workspace_bytes)
-    if hasattr(workspace, "numel"):
-        return workspace.numel() * workspace.element_size()
+    if hasattr(workspace, "nbytes"):
+        return workspace.nbytes
     raise ValueError("workspace_bytes is required when the workspace is a raw address")
 
 
@@ -425,25 +426,33 @@ def gather_blocks(src, dst, rows: int, n_blocks: int, block_bytes: int, order, w
                                          _stream(stream)), "affinity_gather_blocks")
 
 
+_types = {}     # torch dtype -> aff_dtype, filled at first use (importing this module does not import torch)
+
+
 def _dtype(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return AFF_BF16
-    if t.dtype == torch.float32:
-        return AFF_FP32
-    raise TypeError("tensors must be bfloat16 or float32")
+    code = _types.get(t.dtype)
+    if code is None:
+        import torch
+        _types.update({torch.bfloat16: AFF_BF16, torch.float32: AFF_FP32})
+        if t.dtype not in _types:
+            raise TypeError("tensors must be bfloat16 or float32")
+        code = _types[t.dtype]
+    return code
 
 
 def _row_stride(t, width: int, name: str) -> int:
     """Elements between the rows of a [T, ...] tensor whose rows are dense and `width` elements wide."""
-    inner = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and s != inner:
-            raise ValueError(f"{name}: rows must be dense")
-        inner *= n
-    if inner != width:
-        raise ValueError(f"{name}: rows of {width} elements expected, got {inner}")
-    return t.stride(0) if t.shape[0] > 1 else width
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n == 3:
+        ok = shape[1] * shape[2] == width and (stride[2] == 1 or shape[2] == 1) and \
+            (stride[1] == shape[2] or shape[1] == 1)
+    else:
+        ok = n == 2 and shape[1] == width and (stride[1] == 1 or width == 1)
+    if not ok:
+        raise ValueError(f"{name}: dense rows of {width} elements expected, got shape {tuple(shape)} with strides "
+                         f"{tuple(stride)}")
+    return stride[0] if shape[0] > 1 else width
 
 
 def _same_type(like, **tensors) -> None:
@@ -514,63 +523,71 @@ def rotary(cos, sin, interleaved: bool = False, q_gain=None, k_gain=None, eps: f
         raise ValueError("cos and sin must be dense")
     r = aff_rotary(cos.data_ptr(), sin.data_ptr(), _ptr(q_gain), _ptr(k_gain), cos.shape[0], float(eps),
                    2 * cos.shape[1], int(bool(interleaved)))
-    r.keep = (cos, sin, q_gain, k_gain)
+    r.keep, r.gains = (cos, sin), (q_gain, k_gain)
     return r
 
 
 def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan, stream=None,
               plan_bytes=None) -> None:
     """Enqueue affinity_kv_append: q [T, H, d_head], k and v [T, G, d_head] (rows may be strided), q_out like q."""
-    hd, gd = s.H * c.d_head, c.G * c.d_head
-    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
-        if t.shape[0] != s.T or _dtype(t) != c.dtype:
-            raise ValueError(f"{name} must have {s.T} rows of the cache's type")
-    for name, t in zip(("q_gain", "k_gain"), getattr(r, "keep", (None,) * 4)[2:]):
-        if t is not None and (t.shape != (c.d_head,) or _dtype(t) != c.dtype):
-            raise ValueError(f"{name} must be [d_head] of the cache's type")
-    _check(load().affinity_kv_append(_ptr(q), _row_stride(q, hd, "q"), _ptr(k), _row_stride(k, gd, "k"), _ptr(v),
-                                     _row_stride(v, gd, "v"), ctypes.byref(c), ctypes.byref(s), ctypes.byref(r),
-                                     _ptr(q_out), _row_stride(q_out, hd, "q_out"), _ptr(plan),
-                                     _ws_bytes(plan, plan_bytes), _stream(stream)), "affinity_kv_append")
+    T, d, code = s.T, c.d_head, c.dtype
+    hd, gd = s.H * d, c.G * d
+    if not (q.shape[0] == k.shape[0] == v.shape[0] == q_out.shape[0] == T):
+        raise ValueError(f"q, k, v and q_out must have {T} rows")
+    if not (_dtype(q) == _dtype(k) == _dtype(v) == _dtype(q_out) == code):
+        raise TypeError("q, k, v and q_out must be of the cache's type")
+    for t in r.gains:
+        if t is not None and (t.shape != (d,) or _dtype(t) != code):
+            raise ValueError("q_gain and k_gain must be [d_head] of the cache's type")
+    _check(load().affinity_kv_append(q.data_ptr(), _row_stride(q, hd, "q"), k.data_ptr(), _row_stride(k, gd, "k"),
+                                     v.data_ptr(), _row_stride(v, gd, "v"), c, s, r, q_out.data_ptr(),
+                                     _row_stride(q_out, hd, "q_out"), _ptr(plan), _ws_bytes(plan, plan_bytes),
+                                     _stream(stream)), "affinity_kv_append")
 
 
 def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, plan, stream=None,
                      plan_bytes=None) -> None:
     """Enqueue affinity_prefix_attention: q and out [T, H, d_head], lse fp32 [T, H] or None."""
-    hd = s.H * c.d_head
-    for name, t in (("q", q), ("out", out)):
-        if t.shape[0] != s.T or _dtype(t) != c.dtype:
-            raise ValueError(f"{name} must have {s.T} rows of the cache's type")
+    T, H, code = s.T, s.H, c.dtype
+    hd = H * c.d_head
+    if not (q.shape[0] == out.shape[0] == T):
+        raise ValueError(f"q and out must have {T} rows")
+    if not (_dtype(q) == _dtype(out) == code):
+        raise TypeError("q and out must be of the cache's type")
     if _row_stride(out, hd, "out") != hd:
         raise ValueError("out must be dense")
-    if lse is not None and (_dtype(lse) != AFF_FP32 or not lse.is_contiguous() or lse.numel() != s.T * s.H):
+    if lse is not None and (_dtype(lse) != AFF_FP32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, H]")
-    _check(load().affinity_prefix_attention(_ptr(q), _row_stride(q, hd, "q"), ctypes.byref(c), ctypes.byref(s),
-                                            float(scale), _ptr(out), _ptr(lse), _ptr(plan),
-                                            _ws_bytes(plan, plan_bytes), _stream(stream)),
+    _check(load().affinity_prefix_attention(q.data_ptr(), _row_stride(q, hd, "q"), c, s, scale, out.data_ptr(),
+                                            _ptr(lse), _ptr(plan), _ws_bytes(plan, plan_bytes), _stream(stream)),
            "affinity_prefix_attention")
 
 
 def block_norm(x, f, y, h=None, post_gain=None, pre_gain=None, gate=None, rows_per_gate: int = 1, scale: float = 1.0,
                eps: float = 1e-6, stream=None) -> None:
     """Enqueue affinity_block_norm: x, f, y, h [T, D] (rows may be strided), gains [D], gate [n, D]."""
-    T, D = x.shape
-    _same_type(x, f=f, y=y, h=h, post_gain=post_gain, pre_gain=pre_gain, gate=gate)
-    for name, t in (("f", f), ("y", y), ("h", h)):
-        if t is not None and t.shape != (T, D):
-            raise ValueError(f"{name} must be [{T}, {D}]")
-    for name, t in (("post_gain", post_gain), ("pre_gain", pre_gain)):
-        if t is not None and (t.shape != (D,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be dense [{D}]")
-    if gate is not None and (gate.dim() != 2 or gate.shape[1] != D or gate.shape[0] * rows_per_gate < T):
+    shape, dtype = x.shape, x.dtype
+    T, D = shape
+    if f.shape != shape or y.shape != shape or (h is not None and h.shape != shape):
+        raise ValueError(f"x, f, y and h must all be [{T}, {D}]")
+    if gate is not None and (gate.dim() != 2 or rows_per_gate < 1 or gate.shape[1] != D or
+                             gate.shape[0] * rows_per_gate < T):
         raise ValueError("gate must be [n, D] with n * rows_per_gate >= T")
-
-    def rs(t, name):
-        return 0 if t is None else _row_stride(t, D, name)
-    a = aff_block_norm(_ptr(x), _ptr(f), _ptr(gate), _ptr(post_gain), _ptr(pre_gain), _ptr(y), _ptr(h), T, D,
-                       rs(x, "x"), rs(f, "f"), rs(gate, "gate"), rs(y, "y"), rs(h, "h"), int(rows_per_gate),
-                       float(scale), float(eps), _dtype(x))
-    _check(load().affinity_block_norm(ctypes.byref(a), _stream(stream)), "affinity_block_norm")
+    ptrs = []
+    for t in (x, f, gate, post_gain, pre_gain, y, h):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"all tensors must be {dtype}")
+        ptrs.append(t.data_ptr())
+    for t in (post_gain, pre_gain):
+        if t is not None and (t.shape != (D,) or not t.is_contiguous()):
+            raise ValueError(f"gains must be dense [{D}]")
+    a = aff_block_norm(*ptrs, T, D, _row_stride(x, D, "x"), _row_stride(f, D, "f"),
+                       0 if gate is None else _row_stride(gate, D, "gate"), _row_stride(y, D, "y"),
+                       0 if h is None else _row_stride(h, D, "h"), rows_per_gate, scale, eps, _dtype(x))
+    _check(load().affinity_block_norm(a, _stream(stream)), "affinity_block_norm")
 
 
 def set_timing_events(start_event, stop_event) -> None:

@@ -141,10 +141,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Bounded wait like mbar_wait, for the short waits of this pipeline: the clock is first read after
+// 64 polls (a poll suspends for a while by itself), since reading it takes longer than most waits.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, reinterpret_cast<volatile int*>(&b->abort_flag), status);
+}
 // The whole warp waits; false (in every lane) once the CTA has given up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* status) {
-  const bool ok = mbar_wait(bar, parity, reinterpret_cast<volatile int*>(&b->abort_flag), status);
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, wait_for(bar, parity, b, status));
 }
 
 // Keys that tile `ti` of an item holds (1 .. 128), and the first of them within its segment.
@@ -164,28 +171,74 @@ __device__ __forceinline__ WorkItem load_item(const WorkItem* p) {
   return it;
 }
 
-// The order in which an item's key and value tiles are first used; the producer,
-// the MMA thread and the clearing warp all walk it.  f(is_value, stream, j, fresh,
-// last) returns false to stop: fresh, the tile is not loaded yet; last, nobody
-// uses it afterwards.  Streams that share their tiles (alt == 0) have n0 <= n1.
+// The same in every lane and known to be: what follows from it stays in uniform registers,
+// where the tensor instructions take their descriptors from.
+__device__ __forceinline__ WorkItem uniform_item(const WorkItem* p) {
+  WorkItem it = load_item(p);
+  int* v = reinterpret_cast<int*>(&it);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(WorkItem) / 4); ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+  return it;
+}
+
+// One lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// The order in which an item's key and value tiles are used; the producer, the MMA
+// thread and the clearing warp all walk it: scores of both streams' first tile, then
+// for each round the values of stream 0, its next scores, and the same of stream 1.
+// f(is_value, stream, j, fresh, last) returns false to stop: fresh, the tile is not
+// loaded yet; last, nobody uses it afterwards.  Streams that share their tiles (alt
+// == 0) have n0 <= n1.  One loop around one copy of f: the MMA thread runs through
+// its code once per tile, and more copies would not stay in the instruction cache.
 template <typename F>
 __device__ __forceinline__ bool walk_item(const WorkItem& it, F&& f) {
-  const int n = max(it.n0, it.n1);
-  auto use = [&](bool value, int s, int j) {
-    const int mine = s ? it.n1 : it.n0;
-    if (j >= mine) return true;
+  const int ops = 2 + 4 * max(it.n0, it.n1);
+#pragma unroll 1
+  for (int o = 0; o < ops; ++o) {
+    const int w = (o + 2) & 3, s = o < 2 ? o : w >> 1;      // w: 0 values of 0, 1 scores of 0, 2 and 3 of stream 1
+    const bool value = o >= 2 && !(w & 1);
+    const int j = o < 2 ? 0 : ((o - 2) >> 2) + (w & 1);
+    if (j >= (s ? it.n1 : it.n0)) continue;
     const bool fresh = it.alt || s == 0 || j >= it.n0;
     const bool last = it.alt || s == 1 || j >= it.n1;
-    return f(value, s, j, fresh, last);
-  };
-  if (!use(false, 0, 0) || !use(false, 1, 0)) return false;
-  for (int j = 0; j < n; ++j)
-    for (int s = 0; s < 2; ++s)
-      if (!use(true, s, j) || !use(false, s, j + 1)) return false;
+    if (!f(value, s, j, fresh, last)) return false;
+  }
   return true;
 }
 
 __device__ __forceinline__ int tile_of(const WorkItem& it, int s, int j) { return it.t0 + (it.alt ? 2 * j + s : j); }
+
+// S = Q K^T over NK slices of 16 head elements, and O (+)= P V over NK slices of 16 keys.
+// Straight-line code for the common widths (NK 0: any): one thread issues every product,
+// and a branch for each would take longer than the 64 clocks of a 128 x 128 x 16 product.
+template <int NK>
+__device__ __forceinline__ void issue_scores(int nk, uint32_t dst, uint64_t da, uint64_t db, uint32_t id) {
+  auto one = [&](int k) {
+    const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+    mma_f16_ss(dst, da + o, db + o, id, k > 0);
+  };
+  if constexpr (NK > 0) {
+#pragma unroll
+    for (int k = 0; k < NK; ++k) one(k);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < nk; ++k) one(k);
+  }
+}
+__device__ __forceinline__ void issue_values(int ks, uint32_t dst, uint32_t pa, uint64_t db, uint32_t id, bool acc) {
+  if (ks == kKeyTile / 16) {
+#pragma unroll
+    for (int k = 0; k < kKeyTile / 16; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
+  } else {      // the last tile of a run of keys
+#pragma unroll 1
+    for (int k = 0; k < ks; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
+  }
+}
 
 struct Ring {
   int s = 0;
@@ -198,6 +251,7 @@ struct Ring {
   }
 };
 
+template <int NK>      // 16-element slices of a head: 8 (d_head 128), 6 (96), 4 (64), 0 (any)
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ AttnParams p) {
@@ -301,68 +355,77 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      Ring r;
-      volatile int* ab = &bars->abort_flag;
-      const uint32_t q_addr = smem_u32(q_smem), kv_addr = smem_u32(kv_smem);
-      const uint32_t id_qk = idesc_f16(kRows, kKeyTile, 1);
-      const uint32_t id_pv = idesc_f16(kRows, (uint32_t)p.kd, 1) | (1u << 16);   // V is N-major
-      uint32_t q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {0, 0}, fix_ph = 0;
-      int k_st = 0, v_st = 0;          // stages of the shared key and value tile
-      bool ok = true;
-      for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-        const WorkItem it = load_item(g.items + i);
-        if (!mbar_wait(&bars->q_full, q_ph, ab, status)) { ok = false; break; }
-        q_ph ^= 1u;
-        ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool last) {
-          const int ti = tile_of(it, s, j);
+    // The whole warp walks, one lane issues.
+    Ring r;
+    const uint32_t id_qk = idesc_f16(kRows, kKeyTile, 1);
+    const uint32_t id_pv = idesc_f16(kRows, (uint32_t)p.kd, 1) | (1u << 16);   // V is N-major
+    // descriptors: the high half is the same for every tile, the low half counts 16-byte steps
+    const uint64_t dq0 = smem_desc_k_sw128(smem_u32(q_smem)), dk0 = smem_desc_k_sw128(smem_u32(kv_smem));
+    const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(kv_smem), kHalfBytes);
+    const uint32_t tile_step = tile_bytes >> 4;
+    const int nk = p.kd / 16;
+    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, fix_ph = 0;      // bit s: stream s; fix_ph: bit per stage
+    int k_st = 0, v_st = 0;          // stages of the shared key and value tile
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+      const WorkItem it = uniform_item(g.items + i);
+      if (!warp_wait(&bars->q_full, q_ph, bars, status)) { ok = false; break; }
+      q_ph ^= 1u;
+      ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool last) {
+        int ks = kKeyTile / 16;
+        if (value) {
           int key0;
-          const int keys = tile_keys(it, g.prefix_len, ti, &key0);
-          if (value) {
-            if (!mbar_wait(&bars->p_full[s], p_ph[s], ab, status)) return false;
-            p_ph[s] ^= 1u;
-            if (j == 0) {
-              if (!mbar_wait(&bars->o_empty[s], oe_ph[s] ^ 1u, ab, status)) return false;
-              oe_ph[s] ^= 1u;
-            }
-          }
-          int st;
+          const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
+          ks = (keys + 15) >> 4;
           if (fresh) {
-            st = r.s;
-            if (!mbar_wait(&bars->kv_full[st], r.ph, ab, status)) return false;
-            if (value && (keys & 15)) {       // its last rows are cleared by another warp
-              if (!mbar_wait(&bars->kv_fixed[st], (fix_ph >> st) & 1u, ab, status)) return false;
-              fix_ph ^= 1u << st;
+            v_st = r.s;
+            if (!warp_wait(&bars->kv_full[v_st], r.ph, bars, status)) return false;
+            if (keys & 15) {       // its last rows are cleared by another warp
+              if (!warp_wait(&bars->kv_fixed[v_st], (fix_ph >> v_st) & 1u, bars, status)) return false;
+              fix_ph ^= 1u << v_st;
             }
             r.next(p.stages);
-            (value ? v_st : k_st) = st;
-          } else {
-            st = value ? v_st : k_st;
+          }
+          if (j == 0) {
+            if (!warp_wait(&bars->o_empty[s], ((oe_ph >> s) & 1u) ^ 1u, bars, status)) return false;
+            oe_ph ^= 1u << s;
+          }
+          if (!warp_wait(&bars->p_full[s], (p_ph >> s) & 1u, bars, status)) return false;
+          p_ph ^= 1u << s;
+          tc_fence_after();
+          const uint64_t db = dv0 + v_st * tile_step;
+          const uint32_t dst = tmem + kColO + s * kRows, pa = tmem + s * kKeyTile;
+          const bool end = j + 1 == (s ? it.n1 : it.n0);
+          if (elect_one()) {
+            issue_values(ks, dst, pa, db, id_pv, j > 0);
+            if (last) mma_commit(&bars->kv_empty[v_st]);
+            if (end) mma_commit(&bars->o_full[s]);
+          }
+        } else {
+          if (fresh) {
+            k_st = r.s;
+            if (!warp_wait(&bars->kv_full[k_st], r.ph, bars, status)) return false;
+            r.next(p.stages);
           }
           tc_fence_after();
-          const uint32_t tile = kv_addr + st * tile_bytes;
-          if (!value) {
-            const uint32_t qa = q_addr + (it.alt ? 0 : s) * tile_bytes;
-            for (int k = 0; k < p.kd / 16; ++k) {
-              const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
-              mma_f16_ss(tmem + s * kKeyTile, smem_desc_k_sw128(qa + o), smem_desc_k_sw128(tile + o), id_qk, k > 0);
-            }
+          const uint64_t da = dq0 + (it.alt ? 0 : s) * tile_step, db = dk0 + k_st * tile_step;
+          const uint32_t dst = tmem + s * kKeyTile;
+          // the item's last scores: the query rows may be replaced
+          const bool end = it.n1 >= it.n0 ? s == 1 && j + 1 == it.n1 : s == 0 && j + 1 == it.n0;
+          if (elect_one()) {
+            issue_scores<NK>(nk, dst, da, db, id_qk);
             mma_commit(&bars->s_full[s]);
-            if (last) mma_commit(&bars->kv_empty[st]);
-            // the item's last scores: the query rows may be replaced
-            if (it.n1 >= it.n0 ? s == 1 && j + 1 == it.n1 : s == 0 && j + 1 == it.n0) mma_commit(&bars->q_empty);
-          } else {
-            const int ks = (keys + 15) >> 4;
-            for (int k = 0; k < ks; ++k)
-              mma_f16_ts(tmem + kColO + s * kRows, tmem + s * kKeyTile + k * 8,
-                         smem_desc_mn_sw128(tile + k * 2048, kHalfBytes), id_pv, j > 0 || k > 0);
-            if (last) mma_commit(&bars->kv_empty[st]);
-            if (j + 1 == (s ? it.n1 : it.n0)) mma_commit(&bars->o_full[s]);
+            if (last) mma_commit(&bars->kv_empty[k_st]);
+            if (end) mma_commit(&bars->q_empty);
           }
-          return true;
-        });
-        if (ok && it.n0 == 0 && it.n1 == 0) mma_commit(&bars->q_empty);
-      }
+        }
+        __syncwarp();
+        return true;
+      });
+      if (ok && it.n0 == 0 && it.n1 == 0 && elect_one()) mma_commit(&bars->q_empty);
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&bars->drain);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_test_wait(&bars->drain, 0) && global_timer_ns() - t0 < 2000000000ull) {}
@@ -624,6 +687,23 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   }
 }
 
+
+template <int NK>
+aff_status launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, unsigned grid, int smem,
+                            cudaStream_t s) {
+  // The register split needs the launch to own 168 registers a thread: 2 x 208 + 88 = 3 x 168.
+  static const cudaError_t ready = [] {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK>);
+    if (e == cudaSuccess && fa.numRegs != 168) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attention_kernel<NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    return e;
+  }();
+  AFF_CUDA(ready);
+  AFF_CUDA(launch_pdl(attention_kernel<NK>, grid, kThreads, (size_t)smem, s, mk, mv, p));
+  return AFF_OK;
+}
 
 // ---------------------------------------------------------------- fp32
 constexpr int kF32Threads = 256;
@@ -926,17 +1006,13 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
                              (uint64_t)cache->page_stride * 2};
     if ((st = map_16bit_sw128(&mk, cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
     if ((st = map_16bit_sw128(&mv, cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
-    // The register split needs the launch to own 168 registers a thread: 2 x 208 + 88 = 3 x 168.
-    static const cudaError_t ready = [] {
-      cudaFuncAttributes fa;
-      cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel);
-      if (e == cudaSuccess && fa.numRegs != 168) e = cudaErrorInvalidConfiguration;
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-      return e;
-    }();
-    AFF_CUDA(ready);
-    AFF_CUDA(launch_pdl(attention_kernel, grid, kThreads, (size_t)smem, s, mk, mv, p));
+    switch (p.kd / 16) {
+      case 8: st = launch_attention<8>(mk, mv, p, grid, smem, s); break;
+      case 6: st = launch_attention<6>(mk, mv, p, grid, smem, s); break;
+      case 4: st = launch_attention<4>(mk, mv, p, grid, smem, s); break;
+      default: st = launch_attention<0>(mk, mv, p, grid, smem, s); break;
+    }
+    if (st != AFF_OK) return st;
   }
   if (g.may_split) {
     const unsigned blocks = (unsigned)(((int64_t)g.T * g.H + 7) / 8);
