@@ -11,12 +11,12 @@
 //   A work item (step.cuh) is up to 256 packed rows against a run of 128-key
 //   tiles.  Two streams alternate on the tensor core: while the threads of one
 //   turn its scores S into probabilities P, the products of the other run.
-//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
+//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row; they also copy
+//                      their query rows, the next item's while this one's last tile runs
 //     warp 8           TMA: key and value tiles through the page tables
-//     warp 9           issues the products  S = Q K^T (both from shared memory)
-//                      and O += P V (P from tensor memory)
-//     warps 10, 11     copy the item's query rows; 11 also clears the rows of a
-//                      value tile past its keys, since 0 * NaN would stay
+//     warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from
+//                      shared memory) and O += P V (P from tensor memory)
+//     warp 11          clears the rows of a value tile past its keys: 0 * NaN would stay
 //   Tensor memory: S of both streams (128 columns each, P overlays its first
 //   half), O of both (128 columns each).
 //   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
@@ -47,6 +47,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;                   // rows of a stream
 constexpr int kHalfBytes = kRows * 128;      // a tile's 64-column half: 128 rows of 128 bytes
 constexpr int kMaxStages = 12;
+constexpr int kStageOut = 8 * 32 * 128;      // output staging: 32 rows of 128 bytes for each softmax warp
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kRescale = 8.f;              // log2 growth of the maximum that O is rescaled for
 constexpr uint32_t kTmemCols = 512;
@@ -69,10 +70,9 @@ struct AttnParams {
 };
 
 struct alignas(8) Bars {
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_fixed[kMaxStages];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t merge, drain;
+  uint64_t kv_full[kMaxStages], kv_clear[kMaxStages], kv_empty[kMaxStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t merge, drain[2];
   uint32_t tmem;
   int abort_flag;
 };
@@ -188,28 +188,8 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// The order in which an item's key and value tiles are used; the producer, the MMA
-// thread and the clearing warp all walk it: scores of both streams' first tile, then
-// for each round the values of stream 0, its next scores, and the same of stream 1.
-// f(is_value, stream, j, fresh, last) returns false to stop: fresh, the tile is not
-// loaded yet; last, nobody uses it afterwards.  Streams that share their tiles (alt
-// == 0) have n0 <= n1.  One loop around one copy of f: the MMA thread runs through
-// its code once per tile, and more copies would not stay in the instruction cache.
-template <typename F>
-__device__ __forceinline__ bool walk_item(const WorkItem& it, F&& f) {
-  const int ops = 2 + 4 * max(it.n0, it.n1);
-#pragma unroll 1
-  for (int o = 0; o < ops; ++o) {
-    const int w = (o + 2) & 3, s = o < 2 ? o : w >> 1;      // w: 0 values of 0, 1 scores of 0, 2 and 3 of stream 1
-    const bool value = o >= 2 && !(w & 1);
-    const int j = o < 2 ? 0 : ((o - 2) >> 2) + (w & 1);
-    if (j >= (s ? it.n1 : it.n0)) continue;
-    const bool fresh = it.alt || s == 0 || j >= it.n0;
-    const bool last = it.alt || s == 1 || j >= it.n1;
-    if (!f(value, s, j, fresh, last)) return false;
-  }
-  return true;
-}
+// An item's tiles pass through the ring in order, keys then values of tile t0, t0 + 1, ..
+__device__ __forceinline__ int item_tiles(const WorkItem& it) { return it.alt ? it.n0 + it.n1 : max(it.n0, it.n1); }
 
 __device__ __forceinline__ int tile_of(const WorkItem& it, int s, int j) { return it.t0 + (it.alt ? 2 * j + s : j); }
 
@@ -243,13 +223,50 @@ __device__ __forceinline__ void issue_values(int ks, uint32_t dst, uint32_t pa, 
 struct Ring {
   int s = 0;
   uint32_t ph = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++s == stages) {
-      s = 0;
+  __device__ __forceinline__ void skip(int n, int stages) {      // n <= stages
+    s += n;
+    if (s >= stages) {
+      s -= stages;
       ph ^= 1u;
     }
   }
 };
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// A warp's 32 query rows into their place of a 128-byte swizzled K-major tile (`tile` points at the
+// first); lane i gives the address of row i (null: no such row).  16 (8) neighbouring lanes copy a row
+// of up to 128 (64) elements, so that a request covers whole lines; pieces past d are zero.
+__device__ __forceinline__ void copy_queries(const AttnParams& p, const uint16_t* src, uint8_t* tile) {
+  const int lane = threadIdx.x & 31;
+  const int shift = p.halves == 2 ? 4 : 3, per = 32 >> shift;
+  const int c = lane & ((1 << shift) - 1), sub = lane >> shift;
+  const int bytes = c * 8 < p.g.d ? 16 : 0;
+  const uint32_t dst = smem_u32(tile) + (c >> 3) * kHalfBytes;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 32; r0 += per) {
+    const int r = r0 + sub;
+    const uint16_t* from =
+        reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+    if (from && c * 8 < p.kd)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                   "l"(from + (bytes ? c * 8 : 0)), "r"(bytes)
+                   : "memory");
+  }
+}
+
+// 16 bytes to / from row `row` of a warp's 32 x 128-byte staging block, in place c of 8.
+__device__ __forceinline__ uint32_t stage_at(uint32_t base, int row, int c) { return base + row * 128 + ((c ^ (row & 7)) << 4); }
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
 template <int NK>      // 16-element slices of a head: 8 (d_head 128), 6 (96), 4 (64), 0 (any)
 __global__ void __launch_bounds__(kThreads, 1)
@@ -261,7 +278,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   const int tile_bytes = p.halves * kHalfBytes;
   uint8_t* q_smem = smem;                              // two row tiles
   uint8_t* kv_smem = smem + 2 * tile_bytes;
-  float2* merge_ml = reinterpret_cast<float2*>(kv_smem + p.stages * tile_bytes);   // stream 1's (m, l) of every row
+  uint8_t* out_smem = kv_smem + p.stages * tile_bytes;
+  float2* merge_ml = reinterpret_cast<float2*>(out_smem + kStageOut);   // stream 1's (m, l) of every row
   Bars* bars = reinterpret_cast<Bars*>(merge_ml + kRows);
   uint32_t* status = &g.head->status;
 
@@ -269,19 +287,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 2);      // the products that read it, and the clearing warp
-      mbar_init(&bars->kv_fixed[i], 1);
+      mbar_init(&bars->kv_clear[i], 1);
+      mbar_init(&bars->kv_empty[i], 3);      // both streams' products and the clearing warp
     }
-    mbar_init(&bars->q_full, 2);
-    mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 4);
+      mbar_init(&bars->drain[s], 1);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_empty[s], 4);
     }
     mbar_init(&bars->merge, 4);
-    mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -309,21 +326,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     // ------------------------------------------------------------ key and value tiles
     Ring r;
     bool ok = true;
-    const int nb_all = kKeyTile / p.box;
     int in_flight = 0;
+    // one lane per box: 64 columns of `box` keys
+    const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
       const WorkItem it = load_item(g.items + i);
-      ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool) {
-        if (!fresh) return true;
-        const int ti = tile_of(it, s, j);
+      const int n = item_tiles(it);
+      for (int u = 0; u < n && ok; ++u) {
+        const int ti = it.t0 + u;
         int key0;
         const int keys = tile_keys(it, g.prefix_len, ti, &key0);
         const int32_t* table = ti < it.np ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
         const int boxes = (keys + p.box - 1) / p.box;
-        // one lane per box (a lane and its upper neighbours share one page id)
-        const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
         int page = 0, off = 0;
-        if (bx < boxes && bx < nb_all) {
+        if (bx < boxes) {
           const int key = key0 + bx * p.box;
           const int pi = key / g.page_size;
           off = key - pi * g.page_size;
@@ -333,17 +349,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             page = 0;
           }
         }
-        if (!warp_wait(&bars->kv_empty[r.s], r.ph ^ 1u, bars, status)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.s], (uint32_t)(boxes * p.halves * p.box * 128));
-        __syncwarp();
-        uint8_t* dst = kv_smem + r.s * tile_bytes + hf * kHalfBytes + bx * p.box * 128;
-        if (bx < boxes)
-          tma_load_4d(dst, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64, off, it.group, page);
-        __syncwarp();
-        r.next(p.stages);
-        in_flight = min(in_flight + 1, p.stages);
-        return true;
-      });
+        for (int value = 0; value < 2; ++value) {
+          if (!warp_wait(&bars->kv_empty[r.s], r.ph ^ 1u, bars, status)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.s], (uint32_t)(boxes * p.halves * p.box * 128));
+          __syncwarp();
+          uint8_t* dst = kv_smem + r.s * tile_bytes + hf * kHalfBytes + bx * p.box * 128;
+          if (bx < boxes)
+            tma_load_4d(dst, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64, off, it.group, page);
+          __syncwarp();
+          r.skip(1, p.stages);
+          in_flight = min(in_flight + 1, p.stages);
+        }
+      }
     }
     if (!ok) {      // given up: wait for the copies that were issued before shared memory goes away
       for (int i = 0; i < in_flight; ++i) {
@@ -353,144 +370,122 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         while (!mbar_test_wait(&bars->kv_full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
       }
     }
-  } else if (warp == 9) {
+  } else if (warp < 11) {
     // ------------------------------------------------------------ products
-    // The whole warp walks, one lane issues.
-    Ring r;
+    // The whole warp walks, one lane issues.  The tensor pipe holds about four products, so what
+    // this warp does between two batches has to fit in 250 clocks or hide behind the other stream.
+    const int s = warp - 9;
     const uint32_t id_qk = idesc_f16(kRows, kKeyTile, 1);
     const uint32_t id_pv = idesc_f16(kRows, (uint32_t)p.kd, 1) | (1u << 16);   // V is N-major
     // descriptors: the high half is the same for every tile, the low half counts 16-byte steps
-    const uint64_t dq0 = smem_desc_k_sw128(smem_u32(q_smem)), dk0 = smem_desc_k_sw128(smem_u32(kv_smem));
+    const uint64_t dq = smem_desc_k_sw128(smem_u32(q_smem + s * tile_bytes)), dk0 = smem_desc_k_sw128(smem_u32(kv_smem));
     const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(kv_smem), kHalfBytes);
-    const uint32_t tile_step = tile_bytes >> 4;
+    const uint32_t tile_step = tile_bytes >> 4, tS = tmem + s * kKeyTile, tO = tmem + kColO + s * kRows;
     const int nk = p.kd / 16;
-    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, fix_ph = 0;      // bit s: stream s; fix_ph: bit per stage
-    int k_st = 0, v_st = 0;          // stages of the shared key and value tile
+    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, used = 0, seen = ~0u;
     bool ok = true;
+    // Waits until the clearing warp has passed tile number x of the ring, at r.  That warp goes in
+    // order, so tile x implies those before it; a parity tells two neighbouring rounds apart, so no
+    // wait may be more than one round (`stages` tiles) past the last one: the other stream's tiles
+    // in between are caught up with.
+    auto tile_ready = [&](uint32_t x, const Ring& r) {
+      while (x - seen > (uint32_t)p.stages) {
+        seen += p.stages;
+        if (!warp_wait(&bars->kv_clear[seen % p.stages], (seen / p.stages) & 1u, bars, status)) return false;
+      }
+      seen = x;
+      return warp_wait(&bars->kv_clear[r.s], r.ph, bars, status);
+    };
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
       const WorkItem it = uniform_item(g.items + i);
-      if (!warp_wait(&bars->q_full, q_ph, bars, status)) { ok = false; break; }
+      const int n = s ? it.n1 : it.n0;
+      uint32_t x = used + (it.alt ? 2 * s : 0);      // ring number of the stream's first keys
+      used += 2 * item_tiles(it);
+      if (n == 0) continue;
+      Ring r;
+      r.s = x % p.stages;
+      r.ph = (x / p.stages) & 1u;
+      const int to_next = it.alt ? 3 : 1;            // from a tile's values to the stream's next keys
+      ok = warp_wait(&bars->q_full[s], q_ph, bars, status) && tile_ready(x, r);
+      if (!ok) break;
       q_ph ^= 1u;
-      ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool last) {
-        int ks = kKeyTile / 16;
-        if (value) {
-          int key0;
-          const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
-          ks = (keys + 15) >> 4;
-          if (fresh) {
-            v_st = r.s;
-            if (!warp_wait(&bars->kv_full[v_st], r.ph, bars, status)) return false;
-            if (keys & 15) {       // its last rows are cleared by another warp
-              if (!warp_wait(&bars->kv_fixed[v_st], (fix_ph >> v_st) & 1u, bars, status)) return false;
-              fix_ph ^= 1u << v_st;
-            }
-            r.next(p.stages);
-          }
-          if (j == 0) {
-            if (!warp_wait(&bars->o_empty[s], ((oe_ph >> s) & 1u) ^ 1u, bars, status)) return false;
-            oe_ph ^= 1u << s;
-          }
-          if (!warp_wait(&bars->p_full[s], (p_ph >> s) & 1u, bars, status)) return false;
-          p_ph ^= 1u << s;
-          tc_fence_after();
-          const uint64_t db = dv0 + v_st * tile_step;
-          const uint32_t dst = tmem + kColO + s * kRows, pa = tmem + s * kKeyTile;
-          const bool end = j + 1 == (s ? it.n1 : it.n0);
-          if (elect_one()) {
-            issue_values(ks, dst, pa, db, id_pv, j > 0);
-            if (last) mma_commit(&bars->kv_empty[v_st]);
-            if (end) mma_commit(&bars->o_full[s]);
-          }
-        } else {
-          if (fresh) {
-            k_st = r.s;
-            if (!warp_wait(&bars->kv_full[k_st], r.ph, bars, status)) return false;
-            r.next(p.stages);
-          }
-          tc_fence_after();
-          const uint64_t da = dq0 + (it.alt ? 0 : s) * tile_step, db = dk0 + k_st * tile_step;
-          const uint32_t dst = tmem + s * kKeyTile;
-          // the item's last scores: the query rows may be replaced
-          const bool end = it.n1 >= it.n0 ? s == 1 && j + 1 == it.n1 : s == 0 && j + 1 == it.n0;
-          if (elect_one()) {
-            issue_scores<NK>(nk, dst, da, db, id_qk);
-            mma_commit(&bars->s_full[s]);
-            if (last) mma_commit(&bars->kv_empty[k_st]);
-            if (end) mma_commit(&bars->q_empty);
-          }
+      tc_fence_after();
+      if (elect_one()) {
+        issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
+        mma_commit(&bars->s_full[s]);
+        mma_commit(&bars->kv_empty[r.s]);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        int key0;
+        const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
+        r.skip(1, p.stages);
+        if (!tile_ready(++x, r)) { ok = false; break; }
+        if (j == 0) {
+          if (!warp_wait(&bars->o_empty[s], oe_ph ^ 1u, bars, status)) { ok = false; break; }
+          oe_ph ^= 1u;
+        }
+        if (!warp_wait(&bars->p_full[s], p_ph, bars, status)) { ok = false; break; }
+        p_ph ^= 1u;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_values((keys + 15) >> 4, tO, tS, dv0 + r.s * tile_step, id_pv, j > 0);
+          mma_commit(&bars->kv_empty[r.s]);
+          if (j + 1 == n) mma_commit(&bars->o_full[s]);
         }
         __syncwarp();
-        return true;
-      });
-      if (ok && it.n0 == 0 && it.n1 == 0 && elect_one()) mma_commit(&bars->q_empty);
-      __syncwarp();
+        if (j + 1 == n) break;
+        r.skip(to_next, p.stages);
+        x += to_next;
+        if (!tile_ready(x, r)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
+          mma_commit(&bars->s_full[s]);
+          mma_commit(&bars->kv_empty[r.s]);
+        }
+        __syncwarp();
+      }
     }
     if (elect_one()) {
-      mma_commit(&bars->drain);
+      mma_commit(&bars->drain[s]);
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_test_wait(&bars->drain, 0) && global_timer_ns() - t0 < 2000000000ull) {}
+      while (!mbar_test_wait(&bars->drain[s], 0) && global_timer_ns() - t0 < 2000000000ull) {}
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ query rows; ragged value tiles
+    // ------------------------------------------------------------ ragged value tiles
+    // Every tile is waited for and passed on, so that this warp never trails a barrier by a round;
+    // it also stands in for a stream that does not use a tile.
     Ring r;
-    uint32_t q_ph = 0;
     bool ok = true;
-    const int mine = warp - 10;          // row tile
-    const int chunks = p.kd / 8;         // 16-byte pieces of a row, at most 16
-    const int c = lane & 15, rsub = lane >> 4;
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
       const WorkItem it = load_item(g.items + i);
-      if (!warp_wait(&bars->q_empty, q_ph ^ 1u, bars, status)) break;
-      q_ph ^= 1u;
-      const int rows = min(kRows, it.nrows - mine * kRows);
-      if (max(it.n0, it.n1) > 0) {
-        uint8_t* dst = q_smem + mine * tile_bytes + (c >> 3) * kHalfBytes;
-        const int bytes = c * 8 < g.d ? 16 : 0;
-        int rr = it.row0 + mine * kRows + rsub;
-        int tok = rr / g.R, hh = rr - tok * g.R;
-        for (int row = rsub; row < rows; row += 2) {
-          const uint16_t* src = p.q + (int64_t)tok * p.q_stride + (it.group * g.R + hh) * g.d + (bytes ? c * 8 : 0);
-          if (c < chunks)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             smem_u32(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4))),
-                         "l"(src), "r"(bytes)
-                         : "memory");
-          hh += 2;
-          while (hh >= g.R) {
-            hh -= g.R;
-            ++tok;
-          }
-        }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        fence_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_full);
-      if (mine == 1)
-        ok = walk_item(it, [&](bool value, int s, int j, bool fresh, bool) {
-          if (!fresh) return true;
-          const int st = r.s;
-          const uint32_t ph = r.ph;
-          r.next(p.stages);
-          // every tile is waited for, so that this warp never trails a barrier by a whole round
-          if (!warp_wait(&bars->kv_full[st], ph, bars, status)) return false;
-          int key0;
-          const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
+      const int n = item_tiles(it);
+      for (int u = 0; u < n && ok; ++u) {
+        int key0;
+        const int keys = tile_keys(it, g.prefix_len, it.t0 + u, &key0);
+        const uint32_t arrivals = it.alt || u >= it.n0 ? 2 : 1;
+        for (int value = 0; value < 2; ++value) {
+          if (!warp_wait(&bars->kv_full[r.s], r.ph, bars, status)) { ok = false; break; }
           if (value && (keys & 15)) {
             // rows keys .. the next multiple of 16: whole 128-byte rows, so the swizzle does not matter
             const int rows_clear = 16 - (keys & 15);
-            uint8_t* tile = kv_smem + st * tile_bytes + keys * 128;
+            uint8_t* tile = kv_smem + r.s * tile_bytes + keys * 128;
             for (int q = lane; q < rows_clear * 8; q += 32)
               for (int h = 0; h < p.halves; ++h)
                 *reinterpret_cast<uint4*>(tile + h * kHalfBytes + q * 16) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->kv_fixed[st]);
           }
-          if (lane == 0) mbar_arrive(&bars->kv_empty[st]);
-          return true;
-        });
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->kv_clear[r.s]);
+            mbar_arrive_n(&bars->kv_empty[r.s], arrivals);
+          }
+          r.skip(1, p.stages);
+        }
+      }
     }
   }
   } else {
@@ -501,11 +496,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + s * kKeyTile;
     const uint32_t tO = tmem + lane_base + kColO + s * kRows;
+    uint8_t* q_tile = q_smem + s * tile_bytes;
     uint32_t s_ph = 0, o_ph = 0, m_ph = 0;
     bool ok = true;
+    const uint32_t stage_out = smem_u32(out_smem) + warp * 4096;
+    // this thread's query row in an item, null if there is none (the stream has no tile, or the item no such row)
+    auto query_row = [&](const WorkItem& it) {
+      const int r_item = row + (it.alt ? 0 : s * kRows);
+      if ((s ? it.n1 : it.n0) == 0 || r_item >= it.nrows) return static_cast<const uint16_t*>(nullptr);
+      const int rr = it.row0 + r_item, tok = rr / g.R;
+      return p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+    };
+    if ((int)blockIdx.x < n_items) copy_queries(p, query_row(load_item(g.items + blockIdx.x)), q_tile + (row & ~31) * 128);
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
       const WorkItem it = load_item(g.items + i);
       const int n = s ? it.n1 : it.n0;
+      if (n > 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full[s]);
+      }
+      const bool more = i + (int)gridDim.x < n_items;
+      const uint16_t* next_row = more ? query_row(load_item(g.items + i + gridDim.x)) : nullptr;
+      if (n == 0) copy_queries(p, next_row, q_tile + (row & ~31) * 128);
       const int r_item = row + (it.alt ? 0 : s * kRows);
       const int rr = it.row0 + r_item;
       const bool live = r_item < it.nrows;
@@ -518,6 +532,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       for (int j = 0; j < n; ++j) {
         if (!warp_wait(&bars->s_full[s], s_ph, bars, status)) { ok = false; break; }
         s_ph ^= 1u;
+        // the stream's last scores are there, so its query rows are free for the next item's
+        if (j + 1 == n) copy_queries(p, next_row, q_tile + (row & ~31) * 128);
         if (warp_live) {
           tc_fence_after();
           uint32_t v[128];
@@ -625,41 +641,56 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         tc_fence_after();
         const int h = it.group * g.R + rr - tok * g.R;
         const bool direct = it.part_row < 0;
-        uint16_t* ob = static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d;
-        float* of = g.part_out + (int64_t)(it.part_row + r_item) * g.d;
-        for (int c = 0; c < p.kd; c += 16) {
-          uint32_t o[16], o1[16];
-          float y[16];
-          if (n > 0) {
-            tmem_ld16(tO + c, o);
-            if (merging) tmem_ld16(tO + kRows + c, o1);
-            tmem_ld_wait();
+        // 128 bytes of each row at a time go through shared memory, so that the stores cover whole
+        // lines: 64 bf16 columns of the output, 32 fp32 columns of a partial row.
+        uint8_t* mine = !live ? nullptr
+                        : direct ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d)
+                                 : reinterpret_cast<uint8_t*>(g.part_out + (int64_t)(it.part_row + r_item) * g.d);
+        const int cols = direct ? 64 : 32, row_bytes = g.d * (direct ? 2 : 4);
+#pragma unroll 1
+        for (int c0 = 0; c0 < p.kd; c0 += cols) {
+#pragma unroll 1
+          for (int c = c0; c < min(c0 + cols, p.kd); c += 16) {
+            float y[16];
+            if (n > 0) {
+              uint32_t o[16], o1[16];
+              tmem_ld16(tO + c, o);
+              if (merging) tmem_ld16(tO + kRows + c, o1);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              y[e] = __uint_as_float(o[e]) * f0;
-              if (merging) y[e] += __uint_as_float(o1[e]) * f1;
-              if (l == 0.f) y[e] = 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = 0.f;
-          }
-          if (live) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              if (c + q * 8 >= g.d) break;
-              if (direct) {
-                *reinterpret_cast<uint4*>(ob + c + q * 8) =
-                    make_uint4(bf16x2(y[q * 8], y[q * 8 + 1]), bf16x2(y[q * 8 + 2], y[q * 8 + 3]),
-                               bf16x2(y[q * 8 + 4], y[q * 8 + 5]), bf16x2(y[q * 8 + 6], y[q * 8 + 7]));
-              } else {
-                *reinterpret_cast<float4*>(of + c + q * 8) =
-                    make_float4(y[q * 8], y[q * 8 + 1], y[q * 8 + 2], y[q * 8 + 3]);
-                *reinterpret_cast<float4*>(of + c + q * 8 + 4) =
-                    make_float4(y[q * 8 + 4], y[q * 8 + 5], y[q * 8 + 6], y[q * 8 + 7]);
+              for (int e = 0; e < 16; ++e) {
+                y[e] = __uint_as_float(o[e]) * f0;
+                if (merging) y[e] += __uint_as_float(o1[e]) * f1;
+                if (l == 0.f) y[e] = 0.f;
               }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = 0.f;
+            }
+            if (direct) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                st_shared16(stage_at(stage_out, lane, (c - c0) / 8 + q),
+                            make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                       bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7])));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                st_shared16(stage_at(stage_out, lane, (c - c0) / 4 + q),
+                            make_uint4(__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]),
+                                       __float_as_uint(y[4 * q + 2]), __float_as_uint(y[4 * q + 3])));
             }
           }
+          __syncwarp();
+          const int piece = lane & 7, byte = c0 * (direct ? 2 : 4) + piece * 16;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            uint8_t* dst =
+                reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+            if (dst && byte < row_bytes) *reinterpret_cast<uint4*>(dst + byte) = ld_shared16(stage_at(stage_out, r, piece));
+          }
+          __syncwarp();
         }
         if (live) {
           const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
@@ -996,7 +1027,7 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
     p.box = 128;
     while (g.page_size % p.box) p.box /= 2;       // page_size % 8 == 0: at least 8
     const int tile = p.halves * kHalfBytes;
-    const int fixed = 1024 + 2 * tile + kRows * (int)sizeof(float2) + (int)sizeof(Bars);
+    const int fixed = 1024 + 2 * tile + kStageOut + kRows * (int)sizeof(float2) + (int)sizeof(Bars);
     p.stages = (kSmemMax - fixed) / tile;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const int smem = fixed + p.stages * tile;
