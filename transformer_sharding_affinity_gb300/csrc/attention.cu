@@ -47,6 +47,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;                   // rows of a stream
 constexpr int kHalfBytes = kRows * 128;      // a tile's 64-column half: 128 rows of 128 bytes
 constexpr int kMaxStages = 12;
+constexpr int kSlots = 4;                    // items on their way through the CTA
 constexpr int kStageOut = 8 * 32 * 128;      // output staging: 32 rows of 128 bytes for each softmax warp
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kRescale = 8.f;              // log2 growth of the maximum that O is rescaled for
@@ -69,10 +70,12 @@ struct AttnParams {
   int64_t page_stride, group_stride, token_stride;
 };
 
-struct alignas(8) Bars {
-  uint64_t kv_full[kMaxStages], kv_clear[kMaxStages], kv_empty[kMaxStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t merge, drain[2];
+struct alignas(16) Bars {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t kv_ready[2][kMaxStages];          // by stream: its own tiles, in its own order
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t merge, drain[2], slot_full[kSlots], slot_empty[kSlots];
+  alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
   uint32_t tmem;
   int abort_flag;
 };
@@ -171,14 +174,21 @@ __device__ __forceinline__ WorkItem load_item(const WorkItem* p) {
   return it;
 }
 
-// The same in every lane and known to be: what follows from it stays in uniform registers,
-// where the tensor instructions take their descriptors from.
-__device__ __forceinline__ WorkItem uniform_item(const WorkItem* p) {
-  WorkItem it = load_item(p);
+// The item in slot k.  The same in every lane and known to be: what follows from it stays in
+// uniform registers, where the tensor instructions take their descriptors from.
+__device__ __forceinline__ WorkItem uniform_item(const Bars* bars, int k) {
+  WorkItem it = load_item(&bars->slot[k % kSlots]);
   int* v = reinterpret_cast<int*>(&it);
 #pragma unroll
   for (int i = 0; i < (int)(sizeof(WorkItem) / 4); ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
   return it;
+}
+__device__ __forceinline__ bool slot_wait(Bars* b, int k, uint32_t* status) {
+  return warp_wait(&b->slot_full[k % kSlots], (k / kSlots) & 1, b, status);
+}
+__device__ __forceinline__ void slot_done(Bars* b, int k) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&b->slot_empty[k % kSlots]);
 }
 
 // One lane of the (converged) warp, always the same one.
@@ -210,13 +220,14 @@ __device__ __forceinline__ void issue_scores(int nk, uint32_t dst, uint64_t da, 
     for (int k = 0; k < nk; ++k) one(k);
   }
 }
-__device__ __forceinline__ void issue_values(int ks, uint32_t dst, uint32_t pa, uint64_t db, uint32_t id, bool acc) {
-  if (ks == kKeyTile / 16) {
+// Slices k0 .. k0 + 3 of the keys, those below ks (the last tile of a run of keys has fewer).
+__device__ __forceinline__ void issue_values(int k0, int ks, uint32_t dst, uint32_t pa, uint64_t db, uint32_t id, bool acc) {
+  if (ks >= k0 + 4) {
 #pragma unroll
-    for (int k = 0; k < kKeyTile / 16; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
-  } else {      // the last tile of a run of keys
+    for (int k = 0; k < 4; ++k) mma_f16_ts(dst, pa + (k0 + k) * 8, db + (k0 + k) * 128, id, k > 0 || acc);
+  } else {
 #pragma unroll 1
-    for (int k = 0; k < ks; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
+    for (int k = k0; k < ks; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > k0 || acc);
   }
 }
 
@@ -287,16 +298,22 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_clear[i], 1);
+      mbar_init(&bars->kv_ready[0][i], 1);
+      mbar_init(&bars->kv_ready[1][i], 1);
       mbar_init(&bars->kv_empty[i], 3);      // both streams' products and the clearing warp
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->q_full[s], 4);
       mbar_init(&bars->drain[s], 1);
       mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_half[s], 4);
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_empty[s], 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bars->slot_full[i], 1);
+      mbar_init(&bars->slot_empty[i], 11);   // softmax warps 8, product warps 2, clearing warp 1
     }
     mbar_init(&bars->merge, 4);
     bars->abort_flag = 0;
@@ -321,7 +338,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
   // The softmax threads hold a row of scores each: registers move to them from the other warps.
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 8) {
     // ------------------------------------------------------------ key and value tiles
     Ring r;
@@ -329,8 +346,23 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     int in_flight = 0;
     // one lane per box: 64 columns of `box` keys
     const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+    // Items are claimed one ahead: the first of a CTA is its own number, the others come from a counter,
+    // so that CTAs with cheap items take more of them.
+    auto publish = [&](int k, int item) {
+      if (!warp_wait(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars, status)) return false;
+      int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
+      if (lane < (int)(sizeof(WorkItem) / 4))
+        d[lane] = item < n_items ? reinterpret_cast<const int*>(g.items + item)[lane] : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
+      return true;
+    };
+    int i = blockIdx.x;
+    ok = publish(0, i);
+    for (int k = 0; i < n_items && ok; ++k) {
       const WorkItem it = load_item(g.items + i);
+      int next = 0;
+      if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
       const int n = item_tiles(it);
       for (int u = 0; u < n && ok; ++u) {
         const int ti = it.t0 + u;
@@ -360,7 +392,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           r.skip(1, p.stages);
           in_flight = min(in_flight + 1, p.stages);
         }
+        if (u == 0 && ok) {         // the claim has come back behind the first copies
+          next = __shfl_sync(0xffffffffu, next, 0);
+          ok = publish(k + 1, next);
+        }
       }
+      if (n == 0) {
+        next = __shfl_sync(0xffffffffu, next, 0);
+        ok = publish(k + 1, next);
+      }
+      i = next;
     }
     if (!ok) {      // given up: wait for the copies that were issued before shared memory goes away
       for (int i = 0; i < in_flight; ++i) {
@@ -382,31 +423,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(kv_smem), kHalfBytes);
     const uint32_t tile_step = tile_bytes >> 4, tS = tmem + s * kKeyTile, tO = tmem + kColO + s * kRows;
     const int nk = p.kd / 16;
-    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, used = 0, seen = ~0u;
+    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, used = 0;
     bool ok = true;
-    // Waits until the clearing warp has passed tile number x of the ring, at r.  That warp goes in
-    // order, so tile x implies those before it; a parity tells two neighbouring rounds apart, so no
-    // wait may be more than one round (`stages` tiles) past the last one: the other stream's tiles
-    // in between are caught up with.
-    auto tile_ready = [&](uint32_t x, const Ring& r) {
-      while (x - seen > (uint32_t)p.stages) {
-        seen += p.stages;
-        if (!warp_wait(&bars->kv_clear[seen % p.stages], (seen / p.stages) & 1u, bars, status)) return false;
-      }
-      seen = x;
-      return warp_wait(&bars->kv_clear[r.s], r.ph, bars, status);
+    // The stream's tiles become ready in its own order on barriers of its own, so that it sees every
+    // phase of each: at most `stages` of its tiles are in the ring.
+    Ring turn;
+    auto tile_ready = [&]() {
+      const bool there = warp_wait(&bars->kv_ready[s][turn.s], turn.ph, bars, status);
+      turn.skip(1, p.stages);
+      return there;
     };
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const WorkItem it = uniform_item(g.items + i);
+    for (int k = 0; ok; ++k) {
+      if (!slot_wait(bars, k, status)) break;
+      const WorkItem it = uniform_item(bars, k);
+      slot_done(bars, k);
+      if (it.row0 < 0) break;
       const int n = s ? it.n1 : it.n0;
-      uint32_t x = used + (it.alt ? 2 * s : 0);      // ring number of the stream's first keys
+      const uint32_t x = used + (it.alt ? 2 * s : 0);      // the ring's number of the stream's first keys
       used += 2 * item_tiles(it);
       if (n == 0) continue;
       Ring r;
       r.s = x % p.stages;
       r.ph = (x / p.stages) & 1u;
       const int to_next = it.alt ? 3 : 1;            // from a tile's values to the stream's next keys
-      ok = warp_wait(&bars->q_full[s], q_ph, bars, status) && tile_ready(x, r);
+      ok = warp_wait(&bars->q_full[s], q_ph, bars, status) && tile_ready();
       if (!ok) break;
       q_ph ^= 1u;
       tc_fence_after();
@@ -421,24 +461,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         int key0;
         const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
         r.skip(1, p.stages);
-        if (!tile_ready(++x, r)) { ok = false; break; }
+        if (!tile_ready()) { ok = false; break; }
         if (j == 0) {
           if (!warp_wait(&bars->o_empty[s], oe_ph ^ 1u, bars, status)) { ok = false; break; }
           oe_ph ^= 1u;
         }
+        // the first 64 keys' products go ahead while the other probabilities are still computed
+        const int ks = (keys + 15) >> 4;
+        const uint64_t dv = dv0 + r.s * tile_step;
+        if (!warp_wait(&bars->p_half[s], p_ph, bars, status)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) issue_values(0, ks, tO, tS, dv, id_pv, j > 0);
+        __syncwarp();
         if (!warp_wait(&bars->p_full[s], p_ph, bars, status)) { ok = false; break; }
         p_ph ^= 1u;
         tc_fence_after();
         if (elect_one()) {
-          issue_values((keys + 15) >> 4, tO, tS, dv0 + r.s * tile_step, id_pv, j > 0);
+          issue_values(4, ks, tO, tS, dv, id_pv, true);
           mma_commit(&bars->kv_empty[r.s]);
           if (j + 1 == n) mma_commit(&bars->o_full[s]);
         }
         __syncwarp();
         if (j + 1 == n) break;
         r.skip(to_next, p.stages);
-        x += to_next;
-        if (!tile_ready(x, r)) { ok = false; break; }
+        if (!tile_ready()) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
@@ -456,17 +502,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     __syncwarp();
   } else {
     // ------------------------------------------------------------ ragged value tiles
-    // Every tile is waited for and passed on, so that this warp never trails a barrier by a round;
-    // it also stands in for a stream that does not use a tile.
+    // Every tile is waited for and passed on to the streams that use it, so that nobody trails a
+    // barrier by a round; for a stream that does not use it this warp empties it.
+    Ring turn[2];
     Ring r;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const WorkItem it = load_item(g.items + i);
+    for (int k = 0; ok; ++k) {
+      if (!slot_wait(bars, k, status)) break;
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      slot_done(bars, k);
+      if (it.row0 < 0) break;
       const int n = item_tiles(it);
       for (int u = 0; u < n && ok; ++u) {
         int key0;
         const int keys = tile_keys(it, g.prefix_len, it.t0 + u, &key0);
-        const uint32_t arrivals = it.alt || u >= it.n0 ? 2 : 1;
+        const bool use0 = it.alt ? !(u & 1) : u < it.n0, use1 = it.alt ? u & 1 : u < it.n1;
         for (int value = 0; value < 2; ++value) {
           if (!warp_wait(&bars->kv_full[r.s], r.ph, bars, status)) { ok = false; break; }
           if (value && (keys & 15)) {
@@ -480,9 +530,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bars->kv_clear[r.s]);
-            mbar_arrive_n(&bars->kv_empty[r.s], arrivals);
+            if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
+            if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
+            mbar_arrive_n(&bars->kv_empty[r.s], 3 - (use0 ? 1 : 0) - (use1 ? 1 : 0));
           }
+          if (use0) turn[0].skip(1, p.stages);
+          if (use1) turn[1].skip(1, p.stages);
           r.skip(1, p.stages);
         }
       }
@@ -490,7 +543,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   }
   } else {
     // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int s = warp >> 2;                         // stream
     const int row = threadIdx.x & (kRows - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -507,9 +560,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       const int rr = it.row0 + r_item, tok = rr / g.R;
       return p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
     };
-    if ((int)blockIdx.x < n_items) copy_queries(p, query_row(load_item(g.items + blockIdx.x)), q_tile + (row & ~31) * 128);
-    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-      const WorkItem it = load_item(g.items + i);
+    auto fetch = [&](int k) {          // the stream's query rows of the item in slot k
+      const WorkItem& it = bars->slot[k % kSlots];
+      copy_queries(p, it.row0 < 0 ? nullptr : query_row(it), q_tile + (row & ~31) * 128);
+    };
+    ok = slot_wait(bars, 0, status);
+    if (ok) fetch(0);
+    for (int k = 0; ok; ++k) {
+      const WorkItem& it = bars->slot[k % kSlots];      // held until the item is done
+      if (it.row0 < 0) break;
       const int n = s ? it.n1 : it.n0;
       if (n > 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -517,9 +576,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full[s]);
       }
-      const bool more = i + (int)gridDim.x < n_items;
-      const uint16_t* next_row = more ? query_row(load_item(g.items + i + gridDim.x)) : nullptr;
-      if (n == 0) copy_queries(p, next_row, q_tile + (row & ~31) * 128);
       const int r_item = row + (it.alt ? 0 : s * kRows);
       const int rr = it.row0 + r_item;
       const bool live = r_item < it.nrows;
@@ -533,7 +589,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         if (!warp_wait(&bars->s_full[s], s_ph, bars, status)) { ok = false; break; }
         s_ph ^= 1u;
         // the stream's last scores are there, so its query rows are free for the next item's
-        if (j + 1 == n) copy_queries(p, next_row, q_tile + (row & ~31) * 128);
+        if (j + 1 == n) {
+          if (!slot_wait(bars, k + 1, status)) { ok = false; break; }
+          fetch(k + 1);
+        }
         if (warp_live) {
           tc_fence_after();
           uint32_t v[128];
@@ -585,6 +644,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           uint64_t sum0 = pk(0.f, 0.f), sum1 = sum0;
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
+            if (c == 64) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->p_half[s]);
+            }
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -602,7 +667,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[s]);
+        if (lane == 0) {
+          if (!warp_live) mbar_arrive(&bars->p_half[s]);
+          mbar_arrive(&bars->p_full[s]);
+        }
+      }
+      if (ok && n == 0) {
+        ok = slot_wait(bars, k + 1, status);
+        if (ok) fetch(k + 1);
       }
       if (!ok) break;
       // ---- output.  Streams that share the rows are merged by stream 0's threads.
@@ -618,6 +690,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->merge);
         }
+        slot_done(bars, k);
         continue;
       }
       float f0 = 1.f, f1 = 0.f;
@@ -707,6 +780,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         if (n > 0) mbar_arrive(&bars->o_empty[s]);
         if (merging) mbar_arrive(&bars->o_empty[1]);
       }
+      slot_done(bars, k);
     }
   }
 
@@ -716,13 +790,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
+  if (fits && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(&g.head->done, 1u) == gridDim.x - 1) {
+      g.head->claimed = 0;
+      g.head->done = 0;
+    }
+  }
 }
 
 
 template <int NK>
 aff_status launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
-  // The register split needs the launch to own 168 registers a thread: 2 x 208 + 88 = 3 x 168.
+  // The register split needs the launch to own 168 registers a thread: 2 x 216 + 72 = 3 x 168.
   static const cudaError_t ready = [] {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK>);

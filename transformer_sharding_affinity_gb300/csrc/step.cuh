@@ -61,6 +61,8 @@ struct PlanHeader {      // at the start of the plan buffer; its first word is t
   int32_t prefix_parts;  // separate: parts of each prefix job
   int32_t prefix_per;    // separate: key tiles of each part
   int32_t key[10];       // the geometry it was made for
+  uint32_t claimed;      // items claimed beyond the first of every CTA, and CTAs done, in the call
+  uint32_t done;         // under way; the last CTA sets both back to 0
 };
 
 // Everything the kernels need to know of the step, by value.
