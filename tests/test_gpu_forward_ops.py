@@ -141,7 +141,7 @@ def test_prompts(heads, prefix, page):
     Case(heads, [150, 1, 0, 33, 20], [150, 140, 9, 64, 21], prefix, page, seed=1).check_attention()
 
 
-@pytest.mark.parametrize("page", [8, 40, 64, 128, 136, 256])
+@pytest.mark.parametrize("page", [8, 40, 64, 128, 136, 200, 256])
 @pytest.mark.parametrize("token_major", [False, True])
 def test_page_sizes_and_orders(page, token_major):
     Case((4, 2, 128), [1, 3, 130], [200, 129, 131], 70, page, token_major=token_major, seed=2).check_attention()
@@ -158,6 +158,21 @@ def test_many_sequences_share_a_prefix():
     """More rows than a row tile behind one prefix: row tiles run across sequences."""
     n = 150
     Case((8, 2, 64), [1] * n, [1 + (7 * i) % 40 for i in range(n)], 260, seed=6).check_attention()
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_many_items_of_every_kind(prefix):
+    """Every CTA takes several items in turn: single rows, a few tokens, more than one row tile; short and long keys."""
+    n = 170
+    q = [(1, 1, 20, 1, 9, 150, 1)[i % 7] if i % 31 else 0 for i in range(n)]
+    kv = [max(q[i], 1 + (37 * i) % 400) for i in range(n)]
+    c = Case((4, 4, 64), q, kv, prefix, page=24, seed=30)
+    first = c.check_attention()
+    for _ in range(3):
+        out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+        B.prefix_attention(c.q.cuda(), c.cache, c.step, 0.125, out, lse, c.plan)
+        assert B.device_status(c.plan) == B.AFF_OK
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
 def test_padding_rows_are_zero():

@@ -253,8 +253,8 @@ aff_status make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* d
 }  // namespace
 
 aff_status aff::map_16bit_sw128(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
-                                const uint64_t* strides, uint32_t box1, int box1_dim) {
-  return make_map(m, ptr, rank, dims, strides, box1, box1_dim);
+                                const uint64_t* strides, uint32_t box1, int box1_dim, uint32_t box2, int box2_dim) {
+  return make_map(m, ptr, rank, dims, strides, box1, box1_dim, box2, box2_dim);
 }
 
 namespace {

@@ -19,6 +19,7 @@
 //     warp 11          clears the rows of a value tile past its keys: 0 * NaN would stay
 //   Tensor memory: S of both streams (128 columns each, P overlays its first
 //   half), O of both (128 columns each).
+//   Items of at most 16 rows leave the tensor tiles aside: few_rows.
 //   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
 //   when m has grown by more than 8 (in log2): until then p <= 2^8, far inside
 //   fp32 and bf16.  P is rounded to bf16, the type of V (a product's operands
@@ -46,7 +47,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 128;                   // rows of a stream
 constexpr int kHalfBytes = kRows * 128;      // a tile's 64-column half: 128 rows of 128 bytes
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 6;
 constexpr int kSlots = 4;                    // items on their way through the CTA
 constexpr int kStageOut = 8 * 32 * 128;      // output staging: 32 rows of 128 bytes for each softmax warp
 constexpr int kSmemMax = 227 * 1024;
@@ -64,20 +65,22 @@ struct AttnParams {
   float scale, scale_log2;
   int32_t halves;           // 64-column halves of a head row
   int32_t kd;               // head width rounded up to 16
-  int32_t box;              // keys of a TMA box: gcd(page_size, 128)
+  int32_t box;              // keys of a TMA box: a page, or a tile of a larger page
   int32_t stages;
+  int32_t whole_rows;       // few-rows tiles: a box holds both halves (d_head 128; few_k, few_v)
   const float *kc, *vc;     // the pools, read by the fp32 kernel (the bf16 kernel has tensor maps)
   int64_t page_stride, group_stride, token_stride;
 };
 
 struct alignas(16) Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-  uint64_t kv_ready[2][kMaxStages];          // by stream: its own tiles, in its own order
+  uint64_t kv_ready[3][kMaxStages];          // stream 0, stream 1, few rows: their own tiles, in their own order
   uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t merge, drain[2], slot_full[kSlots], slot_empty[kSlots];
+  uint64_t merge, few, drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
   uint32_t tmem;
   int abort_flag;
+  uint32_t pipe;             // 1 while a warp issues a batch of products
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: the probabilities stay in tensor memory.
@@ -126,6 +129,15 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t g
   return d;
 }
 
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* m, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float v) {
@@ -158,10 +170,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* 
 }
 
 // Keys that tile `ti` of an item holds (1 .. 128), and the first of them within its segment.
-__device__ __forceinline__ int tile_keys(const WorkItem& it, int prefix_len, int ti, int* key0) {
+__device__ __forceinline__ int tile_keys(const WorkItem& it, const StepGeom& g, int ti, int* key0) {
   const bool pre = ti < it.np;
-  *key0 = (pre ? ti : ti - it.np) * kKeyTile;
-  return min(kKeyTile, (pre ? prefix_len : it.own_len) - *key0);
+  return tile_span(g, pre ? g.prefix_len : it.own_len, pre ? ti : ti - it.np, key0);
 }
 
 __device__ __forceinline__ WorkItem load_item(const WorkItem* p) {
@@ -199,7 +210,13 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // An item's tiles pass through the ring in order, keys then values of tile t0, t0 + 1, ..
-__device__ __forceinline__ int item_tiles(const WorkItem& it) { return it.alt ? it.n0 + it.n1 : max(it.n0, it.n1); }
+__device__ __forceinline__ int item_tiles(const WorkItem& it) { return it.alt ? it.n0 + it.n1 : it.n1; }   // n0 <= n1
+
+// Byte of key `key`'s first half in a few-rows tile.
+__device__ __forceinline__ uint32_t few_row(const AttnParams& p, int key) {
+  const int box = key / p.box;
+  return (box * p.halves * p.box + key - box * p.box) * 128;
+}
 
 __device__ __forceinline__ int tile_of(const WorkItem& it, int s, int j) { return it.t0 + (it.alt ? 2 * j + s : j); }
 
@@ -231,6 +248,17 @@ __device__ __forceinline__ void issue_values(int k0, int ks, uint32_t dst, uint3
   }
 }
 
+// One stream's products at a time: interleaved, both streams' scores would be done late and at the same
+// time, and both softmax groups would then wait and work in step.  Called by one lane.
+__device__ __forceinline__ bool lock_pipe(Bars* b) {
+  for (int i = 0; i < (1 << 22); ++i) {
+    if (atomicCAS(&b->pipe, 0u, 1u) == 0u) return true;
+    if ((i & 1023) == 1023 && *reinterpret_cast<volatile int*>(&b->abort_flag)) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ void unlock_pipe(Bars* b) { atomicExch(&b->pipe, 0u); }
+
 struct Ring {
   int s = 0;
   uint32_t ph = 0;
@@ -252,6 +280,7 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 // of up to 128 (64) elements, so that a request covers whole lines; pieces past d are zero.
 __device__ __forceinline__ void copy_queries(const AttnParams& p, const uint16_t* src, uint8_t* tile) {
   const int lane = threadIdx.x & 31;
+  if (!__any_sync(0xffffffffu, src != nullptr)) return;
   const int shift = p.halves == 2 ? 4 : 3, per = 32 >> shift;
   const int c = lane & ((1 << shift) - 1), sub = lane >> shift;
   const int bytes = c * 8 < p.g.d ? 16 : 0;
@@ -279,9 +308,255 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
   return v;
 }
 
-template <int NK>      // 16-element slices of a head: 8 (d_head 128), 6 (96), 4 (64), 0 (any)
+__device__ __forceinline__ void ldmatrix4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements, two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// An item of at most 8 * RN rows, by the eight softmax warps.  It is bound by the keys and values it reads
+// (a tile's 64 KB take an SM 2800 clocks of its share of HBM), and a 128-row tensor tile would pass through
+// scores, probabilities and products one after the other for rows that are mostly not there.  Here warp w
+// takes keys 16 w .. + 15 of every tile with its own running maximum, sum and output on the warp's own
+// products, transposed so that the rows are the short side:  S^T = K Q^T (16 keys x 8 rows) and
+// O^T += V^T P^T (16 columns x 8 rows); nothing is exchanged before the end of the item.  The maximum is
+// taken over a row's lanes only when some score has passed it by more than kRescale (log2).
+// A tile's pages lie one after the other, each as its 64-column halves.
+template <int NK, int RN>
+__device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it, Bars* bars, uint32_t* status,
+                                         uint8_t* kv_smem, uint8_t* out_smem, uint32_t first, Ring& turn,
+                                         uint32_t& few_ph) {
+  constexpr int kSlices = NK > 0 ? NK : kKeyTile / 16;
+  constexpr int kPitch = 132;                    // floats of a staged row: rows start in different banks
+  const StepGeom& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nk = NK > 0 ? NK : p.kd / 16, tile_bytes = p.halves * kHalfBytes;
+  const int nrows = it.nrows, quad = lane >> 2, col2 = (lane & 3) * 2;
+  // B operand of S^T: row quad of each 8, columns col2, + 1 and + 8, + 9 of each slice
+  uint32_t q[RN][kSlices][2];
+#pragma unroll
+  for (int t = 0; t < RN; ++t) {
+    const int r = quad + 8 * t, rr = it.row0 + r, tok = rr / g.R;
+    const uint16_t* src = p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+#pragma unroll
+    for (int k = 0; k < kSlices; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = k * 16 + e * 8 + col2;
+        q[t][k][e] = r < nrows && c < g.d ? __ldg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
+      }
+  }
+  // rows col2 and col2 + 1 of each 8: own keys in view, maximum (that O and l refer to), sum
+  int own_vis[RN][2];
+  float m[RN][2], l[RN][2], o[RN][kSlices][4];
+#pragma unroll
+  for (int t = 0; t < RN; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * t + col2 + e;
+      own_vis[t][e] = r >= nrows ? -1 : it.seq < 0 ? INT32_MAX : (it.row0 + r) / g.R + it.own_off + 1;
+      m[t][e] = -INFINITY;
+      l[t][e] = 0.f;
+#pragma unroll
+      for (int n = 0; n < kSlices; ++n) o[t][n][e] = o[t][n][2 + e] = 0.f;
+    }
+  Ring r;
+  r.s = first % p.stages;
+  // ldmatrix: lane 8 i + j gives row j of matrix i.  A operand of S^T: (keys 0-7, 8-15) x (columns 0-7 | 8-15);
+  // of O^T, transposed: (columns 0-7, 8-15) x (keys 0-7 | 8-15).
+  const int kj = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), kc = lane >> 4;
+  const int vj = warp * 16 + (lane >> 4) * 8 + (lane & 7), vc = (lane >> 3) & 1;
+  const uint32_t half_step = p.box * 128;
+  const uint32_t k_at = smem_u32(kv_smem) + few_row(p, kj), v_at = smem_u32(kv_smem) + few_row(p, vj);
+  bool ok = true;
+#pragma unroll 1
+  for (int u = 0; u < it.n0; ++u) {
+    const int ti = it.t0 + u;
+    int key0;
+    const int keys = tile_keys(it, g, ti, &key0);
+    const bool mine = warp * 16 < keys;
+    float sc[RN][4];
+    if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
+    turn.skip(1, p.stages);
+    if (mine) {
+      uint32_t a[kSlices][4];
+#pragma unroll
+      for (int k = 0; k < kSlices; ++k)
+        if (k < nk)
+          ldmatrix4(k_at + r.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k]);
+      float s2[RN][4];                // two chains of products
+#pragma unroll
+      for (int t = 0; t < RN; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][e] = s2[t][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSlices; ++k)
+          if (k < nk) mma_16x8x16((k & 1) ? s2[t] : sc[t], a[k], q[t][k][0], q[t][k][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][e] += s2[t][e];
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
+    r.skip(1, p.stages);
+    uint32_t pb[RN][2];
+    if (mine) {
+      // sc[t][e]: key quad, row col2 + e; sc[t][2 + e]: key quad + 8
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < RN; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          int vis = ti < it.np ? keys : min(keys, own_vis[t][e] - key0);
+          if (own_vis[t][e] <= 0) vis = 0;
+          if (warp * 16 + quad >= vis) sc[t][e] = -INFINITY;
+          if (warp * 16 + quad + 8 >= vis) sc[t][2 + e] = -INFINITY;
+          grow |= (fmaxf(sc[t][e], sc[t][2 + e]) - m[t][e]) * p.scale_log2 > kRescale;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int t = 0; t < RN; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(sc[t][e], sc[t][2 + e]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float f = mx > m[t][e] ? ex2((m[t][e] - mx) * p.scale_log2) : 1.f;
+            m[t][e] = fmaxf(m[t][e], mx);
+            l[t][e] *= f;
+#pragma unroll
+            for (int n = 0; n < kSlices; ++n) {
+              o[t][n][e] *= f;
+              o[t][n][2 + e] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < RN; ++t) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float neg = m[t][e] == -INFINITY ? 0.f : -m[t][e] * p.scale_log2;
+          x[e] = ex2(fmaf(sc[t][e], p.scale_log2, neg));
+          x[2 + e] = ex2(fmaf(sc[t][2 + e], p.scale_log2, neg));
+          l[t][e] += x[e] + x[2 + e];
+        }
+        pb[t][0] = transpose8(bf16x2(x[0], x[1]));      // keys x rows -> rows x keys, the B operand of O^T
+        pb[t][1] = transpose8(bf16x2(x[2], x[3]));
+      }
+    }
+    if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
+    turn.skip(1, p.stages);
+    if (mine) {
+      uint32_t a[kSlices][4];
+#pragma unroll
+      for (int n = 0; n < kSlices; ++n)
+        if (n < nk)
+          ldmatrix4_t(v_at + r.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n]);
+#pragma unroll
+      for (int t = 0; t < RN; ++t)
+#pragma unroll
+        for (int n = 0; n < kSlices; ++n)
+          if (n < nk) mma_16x8x16(o[t][n], a[n], pb[t][0], pb[t][1]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
+    r.skip(1, p.stages);
+  }
+  auto all_warps = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->few);
+    const bool there = warp_wait(&bars->few, few_ph, bars, status);
+    few_ph ^= 1u;
+    return there;
+  };
+  // ---- the eight warps' parts are added in shared memory, four rows at a time
+  if (!ok || !all_warps()) return false;          // every warp's staging of the item before is done
+  float* part = reinterpret_cast<float*>(out_smem);                       // [warp][4 rows][kPitch]
+  float2* ml = reinterpret_cast<float2*>(out_smem + 24 * 1024);           // [warp][16 rows]
+#pragma unroll
+  for (int t = 0; t < RN; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
+      if (quad == 0) ml[warp * 16 + 8 * t + col2 + e] = make_float2(m[t][e], l[t][e]);
+    }
+#pragma unroll
+  for (int pass = 0; pass < 2 * RN; ++pass) {
+    if (pass * 4 >= nrows) break;
+    if ((col2 >> 2) == (pass & 1)) {
+      float* dst = part + (warp * 4 + (col2 & 3)) * kPitch + quad;
+#pragma unroll
+      for (int n = 0; n < kSlices; ++n) {
+        dst[n * 16] = o[pass >> 1][n][0];
+        dst[n * 16 + kPitch] = o[pass >> 1][n][1];
+        dst[n * 16 + 8] = o[pass >> 1][n][2];
+        dst[n * 16 + 8 + kPitch] = o[pass >> 1][n][3];
+      }
+    }
+    if (!all_warps()) return false;
+    const int rl = threadIdx.x >> 6, r_item = pass * 4 + rl, c = (threadIdx.x & 63) * 2;
+    if (r_item < nrows && c < g.d) {
+      float2 a[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) a[w] = ml[w * 16 + r_item];
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) mm = fmaxf(mm, a[w].x);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(part + (w * 4 + rl) * kPitch + c);
+        if (a[w].y == 0.f) continue;              // nothing seen by this warp
+        const float f = ex2((a[w].x - ref) * p.scale_log2);
+        sum += a[w].y * f;
+        x += v.x * f;
+        y += v.y * f;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int rr = it.row0 + r_item, tok = rr / g.R, h = it.group * g.R + rr - tok * g.R;
+      const float lse = sum == 0.f ? -INFINITY : mm * p.scale + logf(sum);
+      if (it.part_row < 0) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + c) =
+            bf16x2(x * inv, y * inv);
+        if (c == 0 && p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+      } else {
+        *reinterpret_cast<float2*>(g.part_out + (int64_t)(it.part_row + r_item) * g.d + c) = make_float2(x * inv, y * inv);
+        if (c == 0) g.part_lse[it.part_row + r_item] = lse;
+      }
+    }
+    if (!all_warps()) return false;
+  }
+  return true;
+}
+
+// NK: 16-element slices of a head: 8 (d_head 128), 6 (96), 4 (64), 0 (any).  FEW: with the few-rows path;
+// steps of whole prompts do without its registers and code (an 8192-token prompt: 535 -> 500 us).
+template <int NK, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap few_k, const __grid_constant__ CUtensorMap few_v,
                  const __grid_constant__ AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   const StepGeom& g = p.g;
@@ -300,7 +575,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       mbar_init(&bars->kv_full[i], 1);
       mbar_init(&bars->kv_ready[0][i], 1);
       mbar_init(&bars->kv_ready[1][i], 1);
-      mbar_init(&bars->kv_empty[i], 3);      // both streams' products and the clearing warp
+      mbar_init(&bars->kv_ready[2][i], 1);
+      mbar_init(&bars->kv_empty[i], 9);      // few rows: 8 warps and the clearing warp, which stands in for whoever does not use it
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->q_full[s], 4);
@@ -316,7 +592,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       mbar_init(&bars->slot_empty[i], 11);   // softmax warps 8, product warps 2, clearing warp 1
     }
     mbar_init(&bars->merge, 4);
+    mbar_init(&bars->few, 8);
     bars->abort_flag = 0;
+    bars->pipe = 0;
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -367,14 +645,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       for (int u = 0; u < n && ok; ++u) {
         const int ti = it.t0 + u;
         int key0;
-        const int keys = tile_keys(it, g.prefix_len, ti, &key0);
+        const int keys = tile_keys(it, g, ti, &key0);
         const int32_t* table = ti < it.np ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-        const int boxes = (keys + p.box - 1) / p.box;
+        const int boxes = g.tile_pages ? (keys + p.box - 1) / p.box : 1;
         int page = 0, off = 0;
         if (bx < boxes) {
-          const int key = key0 + bx * p.box;
-          const int pi = key / g.page_size;
-          off = key - pi * g.page_size;
+          const int idx = ti < it.np ? ti : ti - it.np;
+          int pi = idx * g.tile_pages + bx;
+          if (!g.tile_pages) {
+            pi = key0 / g.page_size;
+            off = key0 - pi * g.page_size;
+          }
           page = __ldg(table + pi);
           if (page < 0 || page >= g.n_pages) {      // the copy would read zeros: report it
             latch_status(status, kStatusRange);
@@ -385,9 +666,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           if (!warp_wait(&bars->kv_empty[r.s], r.ph ^ 1u, bars, status)) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.s], (uint32_t)(boxes * p.halves * p.box * 128));
           __syncwarp();
-          uint8_t* dst = kv_smem + r.s * tile_bytes + hf * kHalfBytes + bx * p.box * 128;
-          if (bx < boxes)
-            tma_load_4d(dst, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64, off, it.group, page);
+          uint8_t* dst = kv_smem + r.s * tile_bytes;
+          if (bx >= boxes) {
+          } else if (it.alt != 2) {
+            tma_load_4d(dst + hf * kHalfBytes + bx * p.box * 128, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64,
+                        off, it.group, page);
+          } else {
+            dst += (bx * p.halves + hf) * p.box * 128;
+            // both halves of a page in one copy: a copy of 2 KB takes its issue of 65 clocks, not its bytes
+            if (!p.whole_rows)
+              tma_load_4d(dst, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64, off, it.group, page);
+            else if (hf == 0)
+              tma_load_5d(dst, value ? &few_v : &few_k, &bars->kv_full[r.s], 0, off, 0, it.group, page);
+          }
           __syncwarp();
           r.skip(1, p.stages);
           in_flight = min(in_flight + 1, p.stages);
@@ -441,7 +732,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       const int n = s ? it.n1 : it.n0;
       const uint32_t x = used + (it.alt ? 2 * s : 0);      // the ring's number of the stream's first keys
       used += 2 * item_tiles(it);
-      if (n == 0) continue;
+      if (n == 0 || it.alt == 2) continue;
       Ring r;
       r.s = x % p.stages;
       r.ph = (x / p.stages) & 1u;
@@ -459,7 +750,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         int key0;
-        const int keys = tile_keys(it, g.prefix_len, tile_of(it, s, j), &key0);
+        const int keys = tile_keys(it, g, tile_of(it, s, j), &key0);
         r.skip(1, p.stages);
         if (!tile_ready()) { ok = false; break; }
         if (j == 0) {
@@ -476,20 +767,25 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         if (!warp_wait(&bars->p_full[s], p_ph, bars, status)) { ok = false; break; }
         p_ph ^= 1u;
         tc_fence_after();
-        if (elect_one()) {
-          issue_values(4, ks, tO, tS, dv, id_pv, true);
-          mma_commit(&bars->kv_empty[r.s]);
-          if (j + 1 == n) mma_commit(&bars->o_full[s]);
+        const int v_st = r.s;
+        const bool end = j + 1 == n;
+        if (!end) {
+          r.skip(to_next, p.stages);
+          if (!tile_ready()) { ok = false; break; }
+          tc_fence_after();
         }
-        __syncwarp();
-        if (j + 1 == n) break;
-        r.skip(to_next, p.stages);
-        if (!tile_ready()) { ok = false; break; }
-        tc_fence_after();
         if (elect_one()) {
-          issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
-          mma_commit(&bars->s_full[s]);
-          mma_commit(&bars->kv_empty[r.s]);
+          const bool held = lock_pipe(bars);
+          issue_values(4, ks, tO, tS, dv, id_pv, true);
+          mma_commit(&bars->kv_empty[v_st]);
+          if (end) {
+            mma_commit(&bars->o_full[s]);
+          } else {
+            issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
+            mma_commit(&bars->s_full[s]);
+            mma_commit(&bars->kv_empty[r.s]);
+          }
+          if (held) unlock_pipe(bars);
         }
         __syncwarp();
       }
@@ -504,7 +800,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     // ------------------------------------------------------------ ragged value tiles
     // Every tile is waited for and passed on to the streams that use it, so that nobody trails a
     // barrier by a round; for a stream that does not use it this warp empties it.
-    Ring turn[2];
+    Ring turn[3];
     Ring r;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -515,27 +811,33 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       const int n = item_tiles(it);
       for (int u = 0; u < n && ok; ++u) {
         int key0;
-        const int keys = tile_keys(it, g.prefix_len, it.t0 + u, &key0);
-        const bool use0 = it.alt ? !(u & 1) : u < it.n0, use1 = it.alt ? u & 1 : u < it.n1;
+        const int keys = tile_keys(it, g, it.t0 + u, &key0);
+        const bool few = it.alt == 2;
+        const bool use0 = !few && (it.alt ? !(u & 1) : u < it.n0), use1 = !few && (it.alt ? u & 1 : u < it.n1);
         for (int value = 0; value < 2; ++value) {
           if (!warp_wait(&bars->kv_full[r.s], r.ph, bars, status)) { ok = false; break; }
           if (value && (keys & 15)) {
             // rows keys .. the next multiple of 16: whole 128-byte rows, so the swizzle does not matter
             const int rows_clear = 16 - (keys & 15);
-            uint8_t* tile = kv_smem + r.s * tile_bytes + keys * 128;
-            for (int q = lane; q < rows_clear * 8; q += 32)
-              for (int h = 0; h < p.halves; ++h)
-                *reinterpret_cast<uint4*>(tile + h * kHalfBytes + q * 16) = make_uint4(0, 0, 0, 0);
+            uint8_t* tile = kv_smem + r.s * tile_bytes;
+            const uint32_t step = few ? p.box * 128 : kHalfBytes;
+            for (int q = lane; q < rows_clear * 8; q += 32) {
+              const int key = keys + (q >> 3);
+              uint8_t* at = tile + (few ? few_row(p, key) : key * 128) + (q & 7) * 16;
+              for (int h = 0; h < p.halves; ++h) *reinterpret_cast<uint4*>(at + h * step) = make_uint4(0, 0, 0, 0);
+            }
             fence_async_smem();
           }
           __syncwarp();
           if (lane == 0) {
             if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
             if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
-            mbar_arrive_n(&bars->kv_empty[r.s], 3 - (use0 ? 1 : 0) - (use1 ? 1 : 0));
+            if (few) mbar_arrive(&bars->kv_ready[2][turn[2].s]);
+            mbar_arrive_n(&bars->kv_empty[r.s], few ? 1 : 9 - (use0 ? 1 : 0) - (use1 ? 1 : 0));
           }
           if (use0) turn[0].skip(1, p.stages);
           if (use1) turn[1].skip(1, p.stages);
+          if (few) turn[2].skip(1, p.stages);
           r.skip(1, p.stages);
         }
       }
@@ -550,13 +852,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint32_t tS = tmem + lane_base + s * kKeyTile;
     const uint32_t tO = tmem + lane_base + kColO + s * kRows;
     uint8_t* q_tile = q_smem + s * tile_bytes;
-    uint32_t s_ph = 0, o_ph = 0, m_ph = 0;
+    uint32_t s_ph = 0, o_ph = 0, m_ph = 0, used = 0, few_ph = 0;
+    Ring few_turn;
     bool ok = true;
     const uint32_t stage_out = smem_u32(out_smem) + warp * 4096;
     // this thread's query row in an item, null if there is none (the stream has no tile, or the item no such row)
     auto query_row = [&](const WorkItem& it) {
       const int r_item = row + (it.alt ? 0 : s * kRows);
-      if ((s ? it.n1 : it.n0) == 0 || r_item >= it.nrows) return static_cast<const uint16_t*>(nullptr);
+      if ((s ? it.n1 : it.n0) == 0 || it.alt == 2 || r_item >= it.nrows) return static_cast<const uint16_t*>(nullptr);
       const int rr = it.row0 + r_item, tok = rr / g.R;
       return p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
     };
@@ -569,6 +872,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     for (int k = 0; ok; ++k) {
       const WorkItem& it = bars->slot[k % kSlots];      // held until the item is done
       if (it.row0 < 0) break;
+      const uint32_t first_tile = used;
+      used += 2 * item_tiles(it);
+      if constexpr (FEW) {
+        if (it.alt == 2) {
+          ok = it.nrows <= 8 ? few_rows<NK, 1>(p, it, bars, status, kv_smem, out_smem, first_tile, few_turn, few_ph)
+                             : few_rows<NK, 2>(p, it, bars, status, kv_smem, out_smem, first_tile, few_turn, few_ph);
+          ok = ok && slot_wait(bars, k + 1, status);
+          if (ok) fetch(k + 1);
+          slot_done(bars, k);
+          continue;
+        }
+      }
       const int n = s ? it.n1 : it.n0;
       if (n > 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -602,14 +917,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           tmem_ld32(tS + 96, v + 96);
           const int ti = tile_of(it, s, j);
           int key0;
-          const int keys = tile_keys(it, g.prefix_len, ti, &key0);
+          const int keys = tile_keys(it, g, ti, &key0);
           int vis = ti < it.np ? keys : min(keys, own_vis - key0);
           if (blind) vis = 0;
           tmem_ld_wait();
           if (__any_sync(0xffffffffu, vis < kKeyTile)) {
+            const int least = __reduce_min_sync(0xffffffffu, vis);
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= vis) v[c] = 0xff800000u;      // -inf: chosen, not added, so a NaN behind the mask is gone
+            for (int c0 = 0; c0 < 128; c0 += 32)
+              if (least < c0 + 32) {
+#pragma unroll
+                for (int c = c0; c < c0 + 32; ++c)
+                  if (c >= vis) v[c] = 0xff800000u;  // -inf: chosen, not added, so a NaN behind the mask is gone
+              }
           }
           float mx[4];
 #pragma unroll
@@ -801,21 +1121,31 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 }
 
 
-template <int NK>
-aff_status launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, unsigned grid, int smem,
+template <int NK, bool FEW>
+aff_status launch_attention(const CUtensorMap (&m)[4], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
   // The register split needs the launch to own 168 registers a thread: 2 x 216 + 72 = 3 x 168.
   static const cudaError_t ready = [] {
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK, FEW>);
     if (e == cudaSuccess && fa.numRegs != 168) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attention_kernel<NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+      e = cudaFuncSetAttribute(attention_kernel<NK, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     return e;
   }();
   AFF_CUDA(ready);
-  AFF_CUDA(launch_pdl(attention_kernel<NK>, grid, kThreads, (size_t)smem, s, mk, mv, p));
+  AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[1], m[2], m[3], p));
   return AFF_OK;
+}
+template <bool FEW>
+aff_status launch_attention(const CUtensorMap (&m)[4], const AttnParams& p, unsigned grid, int smem,
+                            cudaStream_t s) {
+  switch (p.kd / 16) {
+    case 8: return launch_attention<8, FEW>(m, p, grid, smem, s);
+    case 6: return launch_attention<6, FEW>(m, p, grid, smem, s);
+    case 4: return launch_attention<4, FEW>(m, p, grid, smem, s);
+    default: return launch_attention<0, FEW>(m, p, grid, smem, s);
+  }
 }
 
 // ---------------------------------------------------------------- fp32
@@ -863,7 +1193,7 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
   for (int j = 0; j < 2 * it.n0; ++j) {
     const int ti = it.t0 + (j >> 1);
     int key0;
-    int keys = tile_keys(it, g.prefix_len, ti, &key0);
+    int keys = tile_keys(it, g, ti, &key0);
     key0 += (j & 1) * kF32Keys;
     keys = min(keys - (j & 1) * kF32Keys, kF32Keys);
     if (keys <= 0) continue;
@@ -1106,25 +1436,29 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
   } else {
     p.halves = g.d > 64 ? 2 : 1;
     p.kd = (g.d + 15) / 16 * 16;
-    p.box = 128;
-    while (g.page_size % p.box) p.box /= 2;       // page_size % 8 == 0: at least 8
+    p.box = g.tile_pages ? g.page_size : g.key_tile;
     const int tile = p.halves * kHalfBytes;
     const int fixed = 1024 + 2 * tile + kStageOut + kRows * (int)sizeof(float2) + (int)sizeof(Bars);
     p.stages = (kSmemMax - fixed) / tile;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const int smem = fixed + p.stages * tile;
-    CUtensorMap mk, mv;
+    CUtensorMap m[4];
+    const uint64_t tok = (uint64_t)cache->token_stride * 2, grp = (uint64_t)cache->group_stride * 2,
+                   pag = (uint64_t)cache->page_stride * 2;
     const uint64_t dims[4] = {(uint64_t)g.d, (uint64_t)g.page_size, (uint64_t)g.G, (uint64_t)g.n_pages};
-    const uint64_t str[3] = {(uint64_t)cache->token_stride * 2, (uint64_t)cache->group_stride * 2,
-                             (uint64_t)cache->page_stride * 2};
-    if ((st = map_16bit_sw128(&mk, cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
-    if ((st = map_16bit_sw128(&mv, cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
-    switch (p.kd / 16) {
-      case 8: st = launch_attention<8>(mk, mv, p, grid, smem, s); break;
-      case 6: st = launch_attention<6>(mk, mv, p, grid, smem, s); break;
-      case 4: st = launch_attention<4>(mk, mv, p, grid, smem, s); break;
-      default: st = launch_attention<0>(mk, mv, p, grid, smem, s); break;
+    const uint64_t str[3] = {tok, grp, pag};
+    if ((st = map_16bit_sw128(&m[0], cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
+    if ((st = map_16bit_sw128(&m[1], cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
+    m[2] = m[0];
+    m[3] = m[1];
+    p.whole_rows = g.few && g.d == 128;
+    if (p.whole_rows) {       // the halves as a dimension of their own
+      const uint64_t dims5[5] = {64, (uint64_t)g.page_size, 2, (uint64_t)g.G, (uint64_t)g.n_pages};
+      const uint64_t str5[4] = {tok, 128, grp, pag};
+      if ((st = map_16bit_sw128(&m[2], cache->k, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
+      if ((st = map_16bit_sw128(&m[3], cache->v, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
     }
+    st = g.few ? launch_attention<true>(m, p, grid, smem, s) : launch_attention<false>(m, p, grid, smem, s);
     if (st != AFF_OK) return st;
   }
   if (g.may_split) {

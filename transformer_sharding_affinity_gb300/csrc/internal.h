@@ -18,9 +18,10 @@ aff_status cuda_fail(cudaError_t e, const char* where);
 aff_status check_device(int* sm_count);
 
 // Tensor map of a 16-bit tensor of `rank` dims (dims[0] innermost, contiguous; strides in bytes),
-// 128 B swizzle, box = 64 innermost elements x box1 in dimension box1_dim; out of bounds reads zero.
+// 128 B swizzle, box = 64 innermost elements x box1 in dimension box1_dim (x box2 in box2_dim, if given);
+// out of bounds reads zero.
 aff_status map_16bit_sw128(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
-                           uint32_t box1, int box1_dim);
+                           uint32_t box1, int box1_dim, uint32_t box2 = 1, int box2_dim = -1);
 
 }  // namespace aff
 

@@ -7,8 +7,13 @@
 // head g * R + r of token t, R = H / G.  The heads of a group share its keys and
 // values, so a tile of rows meets each key tile once.
 //
+// Key tiles.  A tile is up to 128 keys of one segment (the prefix, or a sequence's
+// own keys): as many whole pages as fit, or, for pages of more than 128 tokens, an
+// equal cut of a page.  A page's share of a tile is one TMA box then, whatever the
+// page size (a 128-key tile of 24-token pages would take boxes of 8 keys).
+//
 // Jobs and items.  A job is a tile of rows of one group against a run of key
-// tiles (128 keys each).  A sequence's rows are cut into tiles of `big` rows (of
+// tiles.  A sequence's rows are cut into tiles of `big` rows (of
 // `small` rows, one tile, when it has no more than that).  The shared prefix is
 // read in one of two ways, chosen on the host from the shapes alone:
 //   separate   its own jobs, whose row tiles run across sequences, so each key
@@ -28,7 +33,8 @@
 
 namespace aff {
 
-constexpr int kKeyTile = 128;
+constexpr int kKeyTile = 128;            // most keys of a tile
+constexpr int kFewRows = 16;             // most rows of an item that takes the few-rows path
 constexpr int kPlanSms = 152;            // SMs of a GB300: sizes the plan without a device
 constexpr uint32_t kPlanMagic = 0x41465331u;
 
@@ -52,6 +58,7 @@ struct WorkItem {        // 48 bytes
 };
 // alt == 0: stream s holds rows s*128 .. of the item and walks tiles t0 .. t0 + n_s - 1.
 // alt == 1: at most 128 rows; both streams hold them, stream s walks tiles t0 + s, t0 + s + 2, ...
+// alt == 2: at most 16 rows, for which a tile is split over warps by its keys; n0 tiles.
 
 struct PlanHeader {      // at the start of the plan buffer; its first word is the status word
   uint32_t status;
@@ -70,8 +77,12 @@ struct StepGeom {
   int32_t T, B, H, G, R, d;
   int32_t page_size, dtype;
   int32_t pages_stride, prefix_len;
+  int32_t key_tile;      // keys of a tile (see above)
+  int32_t tile_pages;    // whole pages of a tile, 0 if a page has several tiles
+  int32_t page_tiles;    // tiles of a page then, else 0
   int32_t np;            // key tiles of the prefix
   int32_t separate;      // the prefix has jobs of its own
+  int32_t few;           // items of at most kFewRows rows take the few-rows path
   int32_t may_split;     // jobs may be cut (then the join kernel runs)
   int32_t small, big;    // row tiles
   int32_t prefix_rows;   // row tile of the prefix's jobs
@@ -97,6 +108,24 @@ aff_status check_plan(const StepGeom& g, const void* plan, size_t plan_bytes);
 
 #ifdef __CUDACC__
 __host__ __device__ inline int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
+
+// Key tiles of a segment of `len` keys.
+__host__ __device__ __forceinline__ int segment_tiles(const StepGeom& g, int len) {
+  if (g.tile_pages) return (len + g.key_tile - 1) / g.key_tile;
+  const int pages = len / g.page_size;
+  return pages * g.page_tiles + (len - pages * g.page_size + g.key_tile - 1) / g.key_tile;
+}
+
+// First key and number of keys of tile `idx` of a segment of `len` keys.
+__device__ __forceinline__ int tile_span(const StepGeom& g, int len, int idx, int* key0) {
+  if (g.tile_pages) {
+    *key0 = idx * g.key_tile;
+    return min(g.key_tile, len - *key0);
+  }
+  const int page = idx / g.page_tiles, in_page = (idx - page * g.page_tiles) * g.key_tile;
+  *key0 = page * g.page_size + in_page;
+  return min(min(g.key_tile, g.page_size - in_page), len - *key0);
+}
 
 struct SeqShape {        // what a sequence's jobs are cut from
   int32_t q0, q1, kv, rows, tr, nt;
@@ -130,7 +159,7 @@ __device__ __forceinline__ int keys_in_view(const StepGeom& g, const SeqShape& s
 // Key tiles that the first `upto` rows of a sequence meet in its own jobs.
 __device__ __forceinline__ int key_tiles(const StepGeom& g, const SeqShape& s, int upto) {
   const int v = keys_in_view(g, s, upto);
-  return v == 0 ? 0 : (v + kKeyTile - 1) / kKeyTile + (g.separate ? 0 : g.np);
+  return v == 0 ? 0 : segment_tiles(g, v) + (g.separate ? 0 : g.np);
 }
 
 // Parts of a job of `tiles` key tiles, `streams` row tiles at a time, and the key tiles of each.
