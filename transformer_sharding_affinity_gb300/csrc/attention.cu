@@ -67,6 +67,7 @@ struct AttnParams {
   int32_t kd;               // head width rounded up to 16
   int32_t box;              // keys of a TMA box: a page, or a tile of a larger page
   int32_t stages;
+  int32_t q_boxes;          // a row tile of queries is one TMA box per half: R divides 128 (map_q)
   int32_t whole_rows;       // few-rows tiles: a box holds both halves (d_head 128; few_k, few_v)
   const float *kc, *vc;     // the pools, read by the fp32 kernel (the bf16 kernel has tensor maps)
   int64_t page_stride, group_stride, token_stride;
@@ -143,6 +144,11 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 __device__ __forceinline__ float ex2(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -397,22 +403,28 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
     if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
     turn.skip(1, p.stages);
     if (mine) {
-      uint32_t a[kSlices][4];
-#pragma unroll
-      for (int k = 0; k < kSlices; ++k)
-        if (k < nk)
-          ldmatrix4(k_at + r.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k]);
       float s2[RN][4];                // two chains of products
 #pragma unroll
-      for (int t = 0; t < RN; ++t) {
+      for (int t = 0; t < RN; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[t][e] = s2[t][e] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kSlices; ++k)
-          if (k < nk) mma_16x8x16((k & 1) ? s2[t] : sc[t], a[k], q[t][k][0], q[t][k][1]);
+      for (int k0 = 0; k0 < kSlices; k0 += 4) {      // four loads ahead of their products
+        uint32_t a[4][4];
+#pragma unroll
+        for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
+          if (k < nk)
+            ldmatrix4(k_at + r.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k - k0]);
+#pragma unroll
+        for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
+#pragma unroll
+          for (int t = 0; t < RN; ++t)
+            if (k < nk) mma_16x8x16((k & 1) ? s2[t] : sc[t], a[k - k0], q[t][k][0], q[t][k][1]);
+      }
+#pragma unroll
+      for (int t = 0; t < RN; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[t][e] += s2[t][e];
-      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
@@ -467,16 +479,19 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
     if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
     turn.skip(1, p.stages);
     if (mine) {
-      uint32_t a[kSlices][4];
 #pragma unroll
-      for (int n = 0; n < kSlices; ++n)
-        if (n < nk)
-          ldmatrix4_t(v_at + r.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n]);
+      for (int n0 = 0; n0 < kSlices; n0 += 4) {
+        uint32_t a[4][4];
 #pragma unroll
-      for (int t = 0; t < RN; ++t)
+        for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
+          if (n < nk)
+            ldmatrix4_t(v_at + r.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n - n0]);
 #pragma unroll
-        for (int n = 0; n < kSlices; ++n)
-          if (n < nk) mma_16x8x16(o[t][n], a[n], pb[t][0], pb[t][1]);
+        for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
+#pragma unroll
+          for (int t = 0; t < RN; ++t)
+            if (n < nk) mma_16x8x16(o[t][n], a[n - n0], pb[t][0], pb[t][1]);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
@@ -555,7 +570,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
 // steps of whole prompts do without its registers and code (an 8192-token prompt: 535 -> 500 us).
 template <int NK, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap few_k, const __grid_constant__ CUtensorMap few_v,
                  const __grid_constant__ AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -598,6 +613,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
+    if (p.q_boxes) prefetch_tmap(&map_q);
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
@@ -865,7 +881,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     };
     auto fetch = [&](int k) {          // the stream's query rows of the item in slot k
       const WorkItem& it = bars->slot[k % kSlots];
-      copy_queries(p, it.row0 < 0 ? nullptr : query_row(it), q_tile + (row & ~31) * 128);
+      if (it.row0 < 0 || (s ? it.n1 : it.n0) == 0 || it.alt == 2) return;
+      if (!p.q_boxes) {
+        copy_queries(p, query_row(it), q_tile + (row & ~31) * 128);
+      } else if ((warp & 3) == 0 && elect_one()) {
+        const int tok = (it.row0 + (it.alt ? 0 : s * kRows)) / g.R;
+        mbar_arrive_expect_tx(&bars->q_full[s], (uint32_t)tile_bytes);
+        for (int h = 0; h < p.halves; ++h)
+          tma_load_4d(q_tile + h * kHalfBytes, &map_q, &bars->q_full[s], h * 64, 0, it.group, tok);
+      }
     };
     ok = slot_wait(bars, 0, status);
     if (ok) fetch(0);
@@ -886,10 +910,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       }
       const int n = s ? it.n1 : it.n0;
       if (n > 0) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
+        if (!p.q_boxes) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full[s]);
+        if (lane == 0 && !(p.q_boxes && (warp & 3) == 0)) mbar_arrive(&bars->q_full[s]);
       }
       const int r_item = row + (it.alt ? 0 : s * kRows);
       const int rr = it.row0 + r_item;
@@ -901,45 +927,43 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       const bool blind = !live || (it.seq >= 0 && own_vis <= 0);
       float m = -INFINITY, l = 0.f;                  // m: the maximum that O and l refer to
       for (int j = 0; j < n; ++j) {
+        const int ti = tile_of(it, s, j);
+        int key0;
+        const int keys = tile_keys(it, g, ti, &key0);
+        int vis = ti < it.np ? keys : min(keys, own_vis - key0);      // keys in view of this row
+        if (blind) vis = 0;
+        const bool masked = __any_sync(0xffffffffu, vis < kKeyTile);
         if (!warp_wait(&bars->s_full[s], s_ph, bars, status)) { ok = false; break; }
         s_ph ^= 1u;
-        // the stream's last scores are there, so its query rows are free for the next item's
-        if (j + 1 == n) {
-          if (!slot_wait(bars, k + 1, status)) { ok = false; break; }
-          fetch(k + 1);
-        }
         if (warp_live) {
           tc_fence_after();
+          // the second half's scores come in while the first half's maximum is taken
           uint32_t v[128];
           tmem_ld32(tS, v);
           tmem_ld32(tS + 32, v + 32);
+          tmem_ld_wait();
           tmem_ld32(tS + 64, v + 64);
           tmem_ld32(tS + 96, v + 96);
-          const int ti = tile_of(it, s, j);
-          int key0;
-          const int keys = tile_keys(it, g, ti, &key0);
-          int vis = ti < it.np ? keys : min(keys, own_vis - key0);
-          if (blind) vis = 0;
-          tmem_ld_wait();
-          if (__any_sync(0xffffffffu, vis < kKeyTile)) {
-            const int least = __reduce_min_sync(0xffffffffu, vis);
+          const int least = masked ? __reduce_min_sync(0xffffffffu, vis) : kKeyTile;
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 32)
-              if (least < c0 + 32) {
+          for (int half = 0; half < 128; half += 64) {
+            if (half) tmem_ld_wait();
+            if (masked) {
 #pragma unroll
-                for (int c = c0; c < c0 + 32; ++c)
-                  if (c >= vis) v[c] = 0xff800000u;  // -inf: chosen, not added, so a NaN behind the mask is gone
-              }
+              for (int c0 = half; c0 < half + 64; c0 += 32)
+                if (least < c0 + 32) {
+#pragma unroll
+                  for (int c = c0; c < c0 + 32; ++c)
+                    if (c >= vis) v[c] = 0xff800000u;  // -inf: chosen, not added, so a NaN behind the mask is gone
+                }
+            }
+#pragma unroll
+            for (int c = half; c < half + 64; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(v[c + e]), __uint_as_float(v[c + e + 4]));
           }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 4]));
-#pragma unroll
-          for (int c = 8; c < 128; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 4])));
-          const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
           if (j == 0) {
             m = m_new;
           } else {
@@ -991,6 +1015,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
           if (!warp_live) mbar_arrive(&bars->p_half[s]);
           mbar_arrive(&bars->p_full[s]);
         }
+        // the stream's last scores have been read, so its query rows are free for the next item's
+        if (j + 1 == n) {
+          if (!slot_wait(bars, k + 1, status)) { ok = false; break; }
+          fetch(k + 1);
+        }
       }
       if (ok && n == 0) {
         ok = slot_wait(bars, k + 1, status);
@@ -1034,48 +1063,38 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         tc_fence_after();
         const int h = it.group * g.R + rr - tok * g.R;
         const bool direct = it.part_row < 0;
-        // 128 bytes of each row at a time go through shared memory, so that the stores cover whole
-        // lines: 64 bf16 columns of the output, 32 fp32 columns of a partial row.
         uint8_t* mine = !live ? nullptr
                         : direct ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d)
                                  : reinterpret_cast<uint8_t*>(g.part_out + (int64_t)(it.part_row + r_item) * g.d);
-        const int cols = direct ? 64 : 32, row_bytes = g.d * (direct ? 2 : 4);
-#pragma unroll 1
-        for (int c0 = 0; c0 < p.kd; c0 += cols) {
-#pragma unroll 1
-          for (int c = c0; c < min(c0 + cols, p.kd); c += 16) {
-            float y[16];
-            if (n > 0) {
-              uint32_t o[16], o1[16];
-              tmem_ld16(tO + c, o);
-              if (merging) tmem_ld16(tO + kRows + c, o1);
-              tmem_ld_wait();
+        const bool none = l == 0.f;                                // a row without keys is zero
+        // 32 columns of the row, finished
+        auto read32 = [&](int c, float* y) {
+          uint32_t v[32];
+          if (n > 0) tmem_ld32(tO + c, v);
+          tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                y[e] = __uint_as_float(o[e]) * f0;
-                if (merging) y[e] += __uint_as_float(o1[e]) * f1;
-                if (l == 0.f) y[e] = 0.f;
-              }
-            } else {
+          for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : __uint_as_float(v[e]) * f0;
+          if (merging) {
+            tmem_ld32(tO + kRows + c, v);
+            tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = 0.f;
-            }
-            if (direct) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                st_shared16(stage_at(stage_out, lane, (c - c0) / 8 + q),
-                            make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                                       bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7])));
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                st_shared16(stage_at(stage_out, lane, (c - c0) / 4 + q),
-                            make_uint4(__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]),
-                                       __float_as_uint(y[4 * q + 2]), __float_as_uint(y[4 * q + 3])));
-            }
+            for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : y[e] + __uint_as_float(v[e]) * f1;
           }
+        };
+        auto free_o = [&]() {                                      // for the next item's products
+          tc_fence_before();
           __syncwarp();
-          const int piece = lane & 7, byte = c0 * (direct ? 2 : 4) + piece * 16;
+          if (lane == 0) {
+            if (n > 0) mbar_arrive(&bars->o_empty[s]);
+            if (merging) mbar_arrive(&bars->o_empty[1]);
+          }
+        };
+        // 128 bytes of each row at a time go through shared memory, so that the stores cover whole
+        // lines: 64 bf16 columns of the output, 32 fp32 columns of a partial row.
+        const int row_bytes = g.d * (direct ? 2 : 4);
+        auto put = [&](int byte0) {
+          __syncwarp();
+          const int piece = lane & 7, byte = byte0 + piece * 16;
 #pragma unroll
           for (int r0 = 0; r0 < 32; r0 += 4) {
             const int r = r0 + (lane >> 3);
@@ -1084,6 +1103,27 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             if (dst && byte < row_bytes) *reinterpret_cast<uint4*>(dst + byte) = ld_shared16(stage_at(stage_out, r, piece));
           }
           __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < p.kd; c += 32) {
+          float y[32];
+          read32(c, y);
+          if (c + 32 >= p.kd) free_o();
+          if (direct) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              st_shared16(stage_at(stage_out, lane, (c & 32) / 8 + q),
+                          make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                     bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7])));
+            if ((c & 32) || c + 32 >= p.kd) put((c & 64) * 2);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              st_shared16(stage_at(stage_out, lane, q),
+                          make_uint4(__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]), __float_as_uint(y[4 * q + 2]),
+                                     __float_as_uint(y[4 * q + 3])));
+            put(c * 4);
+          }
         }
         if (live) {
           const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
@@ -1093,10 +1133,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             g.part_lse[it.part_row + r_item] = lse;
           }
         }
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) {
+      } else if (lane == 0) {
         if (n > 0) mbar_arrive(&bars->o_empty[s]);
         if (merging) mbar_arrive(&bars->o_empty[1]);
       }
@@ -1122,7 +1159,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
 
 template <int NK, bool FEW>
-aff_status launch_attention(const CUtensorMap (&m)[4], const AttnParams& p, unsigned grid, int smem,
+aff_status launch_attention(const CUtensorMap (&m)[5], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
   // The register split needs the launch to own 168 registers a thread: 2 x 216 + 72 = 3 x 168.
   static const cudaError_t ready = [] {
@@ -1134,11 +1171,11 @@ aff_status launch_attention(const CUtensorMap (&m)[4], const AttnParams& p, unsi
     return e;
   }();
   AFF_CUDA(ready);
-  AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[1], m[2], m[3], p));
+  AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[1], m[2], m[3], m[4], p));
   return AFF_OK;
 }
 template <bool FEW>
-aff_status launch_attention(const CUtensorMap (&m)[4], const AttnParams& p, unsigned grid, int smem,
+aff_status launch_attention(const CUtensorMap (&m)[5], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
   switch (p.kd / 16) {
     case 8: return launch_attention<8, FEW>(m, p, grid, smem, s);
@@ -1442,21 +1479,28 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
     p.stages = (kSmemMax - fixed) / tile;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const int smem = fixed + p.stages * tile;
-    CUtensorMap m[4];
+    CUtensorMap m[5];          // queries, keys, values; keys and values with whole rows
     const uint64_t tok = (uint64_t)cache->token_stride * 2, grp = (uint64_t)cache->group_stride * 2,
                    pag = (uint64_t)cache->page_stride * 2;
     const uint64_t dims[4] = {(uint64_t)g.d, (uint64_t)g.page_size, (uint64_t)g.G, (uint64_t)g.n_pages};
     const uint64_t str[3] = {tok, grp, pag};
-    if ((st = map_16bit_sw128(&m[0], cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
-    if ((st = map_16bit_sw128(&m[1], cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
-    m[2] = m[0];
+    if ((st = map_16bit_sw128(&m[1], cache->k, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
+    if ((st = map_16bit_sw128(&m[2], cache->v, 4, dims, str, (uint32_t)p.box, 1)) != AFF_OK) return st;
     m[3] = m[1];
+    m[4] = m[2];
+    p.q_boxes = kRows % g.R == 0;
+    m[0] = m[1];
+    if (p.q_boxes) {
+      const uint64_t qd[4] = {(uint64_t)g.d, (uint64_t)g.R, (uint64_t)g.G, (uint64_t)g.T};
+      const uint64_t qs[3] = {(uint64_t)g.d * 2, (uint64_t)g.R * g.d * 2, (uint64_t)q_stride * 2};
+      if ((st = map_16bit_sw128(&m[0], q, 4, qd, qs, (uint32_t)g.R, 1, (uint32_t)(kRows / g.R), 3)) != AFF_OK) return st;
+    }
     p.whole_rows = g.few && g.d == 128;
     if (p.whole_rows) {       // the halves as a dimension of their own
       const uint64_t dims5[5] = {64, (uint64_t)g.page_size, 2, (uint64_t)g.G, (uint64_t)g.n_pages};
       const uint64_t str5[4] = {tok, 128, grp, pag};
-      if ((st = map_16bit_sw128(&m[2], cache->k, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
-      if ((st = map_16bit_sw128(&m[3], cache->v, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
+      if ((st = map_16bit_sw128(&m[3], cache->k, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
+      if ((st = map_16bit_sw128(&m[4], cache->v, 5, dims5, str5, (uint32_t)p.box, 1, 2, 2)) != AFF_OK) return st;
     }
     st = g.few ? launch_attention<true>(m, p, grid, smem, s) : launch_attention<false>(m, p, grid, smem, s);
     if (st != AFF_OK) return st;
