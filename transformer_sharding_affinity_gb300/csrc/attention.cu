@@ -11,14 +11,16 @@
 //   A work item (step.cuh) is up to 256 packed rows against a run of 128-key
 //   tiles.  Two streams alternate on the tensor core: while the threads of one
 //   turn its scores S into probabilities P, the products of the other run.
-//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row; they also copy
-//                      their query rows, the next item's while this one's last tile runs
+//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row; they also fetch
+//                      their query rows, the next item's when this one's scores are read
 //     warp 8           TMA: key and value tiles through the page tables
 //     warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from
 //                      shared memory) and O += P V (P from tensor memory)
 //     warp 11          clears the rows of a value tile past its keys: 0 * NaN would stay
-//   Tensor memory: S of both streams (128 columns each, P overlays its first
-//   half), O of both (128 columns each).
+//     warps 12-15      output, while the softmax goes on to the next item
+//   Tensor memory: S of both streams (128 columns each, as two buffers of half a
+//   tile's 64 keys; P overlays the first half of its buffer), O of both (128
+//   columns each).
 //   Items of at most 16 rows leave the tensor tiles aside: few_rows.
 //   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
 //   when m has grown by more than 8 (in log2): until then p <= 2^8, far inside
@@ -44,12 +46,13 @@
 namespace aff {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kRows = 128;                   // rows of a stream
 constexpr int kHalfBytes = kRows * 128;      // a tile's 64-column half: 128 rows of 128 bytes
 constexpr int kMaxStages = 6;
+constexpr int kHalfKeys = kKeyTile / 2;      // scores are computed and turned into probabilities by half tiles
 constexpr int kSlots = 4;                    // items on their way through the CTA
-constexpr int kStageOut = 8 * 32 * 128;      // output staging: 32 rows of 128 bytes for each softmax warp
+constexpr int kStageOut = 4 * 32 * 128;      // output staging: 32 rows of 128 bytes for each output warp
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kRescale = 8.f;              // log2 growth of the maximum that O is rescaled for
 constexpr uint32_t kTmemCols = 512;
@@ -68,20 +71,29 @@ struct AttnParams {
   int32_t box;              // keys of a TMA box: a page, or a tile of a larger page
   int32_t stages;
   int32_t q_boxes;          // a row tile of queries is one TMA box per half: R divides 128 (map_q)
+  int32_t out_boxes;        // a warp's 32 rows of the output are one box per half: R divides 32 (map_out)
   int32_t whole_rows;       // few-rows tiles: a box holds both halves (d_head 128; few_k, few_v)
   const float *kc, *vc;     // the pools, read by the fp32 kernel (the bf16 kernel has tensor maps)
   int64_t page_stride, group_stride, token_stride;
 };
 
+constexpr int kFewPitch = 132;                                   // floats of a staged row: rows start in different banks
+constexpr int kFewBytes = 8 * 2 * kFewPitch * 4 + 8 * kFewRows * 8;     // two rows and all (m, l) of each softmax warp
+
+// Ring stages that fit beside the query tiles and the staging.
+__host__ __device__ constexpr int ring_stages(int halves) {
+  const int n = (kSmemMax - 1024 - kStageOut - 2 * kRows * 8 - kFewBytes - 1024) / (halves * kHalfBytes) - 2;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
 struct alignas(16) Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t kv_ready[3][kMaxStages];          // stream 0, stream 1, few rows: their own tiles, in their own order
-  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t merge, few, drain[2], slot_full[kSlots], slot_empty[kSlots];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
+  uint64_t stat_full[2], stat_empty[2], few, drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
   uint32_t tmem;
   int abort_flag;
-  uint32_t pipe;             // 1 while a warp issues a batch of products
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: the probabilities stay in tensor memory.
@@ -114,6 +126,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor for an MN-major operand tile written by TMA
@@ -139,6 +161,14 @@ __device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2,
+                                             int32_t c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
+               "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(smem_src))
+               : "memory");
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float v) {
@@ -162,17 +192,26 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// Bounded wait like mbar_wait, for the short waits of this pipeline: the clock is first read after
-// 64 polls (a poll suspends for a while by itself), since reading it takes longer than most waits.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* status) {
+__device__ __forceinline__ bool gave_up(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
+
+// The whole warp waits, for 2 s at most; then the CTA gives up: every later wait ends soon, what is computed
+// is thrown away with the status word, and the roles leave at their next item.  Little code, because the
+// roles' code together has to stay in the instruction cache: the clock is read every 256 polls (a poll
+// suspends for a while by itself), and only its low 32 bits.
+__device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, Bars* b) {
+  if (!mbar_try_wait(bar, parity)) {
+    uint32_t t0 = 0;
 #pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, reinterpret_cast<volatile int*>(&b->abort_flag), status);
-}
-// The whole warp waits; false (in every lane) once the CTA has given up.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* status) {
-  return __all_sync(0xffffffffu, wait_for(bar, parity, b, status));
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+      if (n & 255u) continue;
+      uint32_t t;
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+      if (n == 256) t0 = t;
+      if (t - t0 > 2000000000u) b->abort_flag = 1;
+      if (gave_up(b)) break;
+    }
+  }
+  __syncwarp();
 }
 
 // Keys that tile `ti` of an item holds (1 .. 128), and the first of them within its segment.
@@ -200,8 +239,10 @@ __device__ __forceinline__ WorkItem uniform_item(const Bars* bars, int k) {
   for (int i = 0; i < (int)(sizeof(WorkItem) / 4); ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
   return it;
 }
-__device__ __forceinline__ bool slot_wait(Bars* b, int k, uint32_t* status) {
-  return warp_wait(&b->slot_full[k % kSlots], (k / kSlots) & 1, b, status);
+// Waits for slot k; false when there is no item left, or the CTA has given up.
+__device__ __forceinline__ bool slot_wait(Bars* b, int k) {
+  wait_on(&b->slot_full[k % kSlots], (k / kSlots) & 1, b);
+  return __all_sync(0xffffffffu, !gave_up(b) && b->slot[k % kSlots].row0 >= 0);
 }
 __device__ __forceinline__ void slot_done(Bars* b, int k) {
   __syncwarp();
@@ -218,10 +259,24 @@ __device__ __forceinline__ bool elect_one() {
 // An item's tiles pass through the ring in order, keys then values of tile t0, t0 + 1, ..
 __device__ __forceinline__ int item_tiles(const WorkItem& it) { return it.alt ? it.n0 + it.n1 : it.n1; }   // n0 <= n1
 
+// Box of a tile that holds key `key`: its page, or the only one (pages of several tiles).
+__device__ __forceinline__ int box_of(const AttnParams& p, int key) { return p.g.tile_pages ? p.g.by_page(key) : 0; }
+
 // Byte of key `key`'s first half in a few-rows tile.
 __device__ __forceinline__ uint32_t few_row(const AttnParams& p, int key) {
-  const int box = key / p.box;
+  const int box = box_of(p, key);
   return (box * p.halves * p.box + key - box * p.box) * 128;
+}
+
+// Own keys that the last row of stream s sees, and the keys of its tile that it has any use for.
+__device__ __forceinline__ int stream_limit(const WorkItem& it, const StepGeom& g, int s) {
+  const int last = it.row0 + min(it.nrows, it.alt || s ? it.nrows : kRows) - 1;
+  return min(it.own_len, g.by_R(last) + it.own_off + 1);
+}
+__device__ __forceinline__ int stream_keys(const WorkItem& it, const StepGeom& g, int ti, int limit) {
+  const bool pre = ti < it.np;
+  int key0;
+  return tile_span(g, pre ? g.prefix_len : limit, pre ? ti : ti - it.np, &key0);
 }
 
 __device__ __forceinline__ int tile_of(const WorkItem& it, int s, int j) { return it.t0 + (it.alt ? 2 * j + s : j); }
@@ -243,27 +298,16 @@ __device__ __forceinline__ void issue_scores(int nk, uint32_t dst, uint64_t da, 
     for (int k = 0; k < nk; ++k) one(k);
   }
 }
-// Slices k0 .. k0 + 3 of the keys, those below ks (the last tile of a run of keys has fewer).
-__device__ __forceinline__ void issue_values(int k0, int ks, uint32_t dst, uint32_t pa, uint64_t db, uint32_t id, bool acc) {
-  if (ks >= k0 + 4) {
+// The half tile's keys, up to 4 slices of 16 (`ks` counts on into the next half; a run's last half tile has fewer).
+__device__ __forceinline__ void issue_values(int ks, uint32_t dst, uint32_t pa, uint64_t db, uint32_t id, uint32_t acc) {
+  if (ks >= 4) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16_ts(dst, pa + (k0 + k) * 8, db + (k0 + k) * 128, id, k > 0 || acc);
+    for (int k = 0; k < 4; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
   } else {
 #pragma unroll 1
-    for (int k = k0; k < ks; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > k0 || acc);
+    for (int k = 0; k < ks; ++k) mma_f16_ts(dst, pa + k * 8, db + k * 128, id, k > 0 || acc);
   }
 }
-
-// One stream's products at a time: interleaved, both streams' scores would be done late and at the same
-// time, and both softmax groups would then wait and work in step.  Called by one lane.
-__device__ __forceinline__ bool lock_pipe(Bars* b) {
-  for (int i = 0; i < (1 << 22); ++i) {
-    if (atomicCAS(&b->pipe, 0u, 1u) == 0u) return true;
-    if ((i & 1023) == 1023 && *reinterpret_cast<volatile int*>(&b->abort_flag)) return false;
-  }
-  return false;
-}
-__device__ __forceinline__ void unlock_pipe(Bars* b) { atomicExch(&b->pipe, 0u); }
 
 struct Ring {
   int s = 0;
@@ -274,6 +318,11 @@ struct Ring {
       s -= stages;
       ph ^= 1u;
     }
+  }
+  __device__ __forceinline__ void advance(int n, int stages) {   // any n
+    const int rounds = n / stages;
+    ph ^= rounds & 1u;
+    skip(n - rounds * stages, stages);
   }
 };
 
@@ -291,7 +340,7 @@ __device__ __forceinline__ void copy_queries(const AttnParams& p, const uint16_t
   const int c = lane & ((1 << shift) - 1), sub = lane >> shift;
   const int bytes = c * 8 < p.g.d ? 16 : 0;
   const uint32_t dst = smem_u32(tile) + (c >> 3) * kHalfBytes;
-#pragma unroll 4
+#pragma unroll 1
   for (int r0 = 0; r0 < 32; r0 += per) {
     const int r = r0 + sub;
     const uint16_t* from =
@@ -347,11 +396,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // taken over a row's lanes only when some score has passed it by more than kRescale (log2).
 // A tile's pages lie one after the other, each as its 64-column halves.
 template <int NK, int RN>
-__device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it, Bars* bars, uint32_t* status,
-                                         uint8_t* kv_smem, uint8_t* out_smem, uint32_t first, Ring& turn,
+__device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it, Bars* bars, uint32_t* status,
+                                         uint8_t* kv_smem, uint8_t* few_smem, uint32_t first, Ring& turn,
                                          uint32_t& few_ph) {
   constexpr int kSlices = NK > 0 ? NK : kKeyTile / 16;
-  constexpr int kPitch = 132;                    // floats of a staged row: rows start in different banks
   const StepGeom& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nk = NK > 0 ? NK : p.kd / 16, tile_bytes = p.halves * kHalfBytes;
@@ -360,7 +408,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
   uint32_t q[RN][kSlices][2];
 #pragma unroll
   for (int t = 0; t < RN; ++t) {
-    const int r = quad + 8 * t, rr = it.row0 + r, tok = rr / g.R;
+    const int r = quad + 8 * t, rr = it.row0 + r, tok = g.by_R(rr);
     const uint16_t* src = p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
 #pragma unroll
     for (int k = 0; k < kSlices; ++k)
@@ -378,7 +426,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * t + col2 + e;
-      own_vis[t][e] = r >= nrows ? -1 : it.seq < 0 ? INT32_MAX : (it.row0 + r) / g.R + it.own_off + 1;
+      own_vis[t][e] = r >= nrows ? -1 : it.seq < 0 ? INT32_MAX : g.by_R(it.row0 + r) + it.own_off + 1;
       m[t][e] = -INFINITY;
       l[t][e] = 0.f;
 #pragma unroll
@@ -392,7 +440,6 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
   const int vj = warp * 16 + (lane >> 4) * 8 + (lane & 7), vc = (lane >> 3) & 1;
   const uint32_t half_step = p.box * 128;
   const uint32_t k_at = smem_u32(kv_smem) + few_row(p, kj), v_at = smem_u32(kv_smem) + few_row(p, vj);
-  bool ok = true;
 #pragma unroll 1
   for (int u = 0; u < it.n0; ++u) {
     const int ti = it.t0 + u;
@@ -400,7 +447,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
     const int keys = tile_keys(it, g, ti, &key0);
     const bool mine = warp * 16 < keys;
     float sc[RN][4];
-    if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
+    wait_on(&bars->kv_ready[2][turn.s], turn.ph, bars);
     turn.skip(1, p.stages);
     if (mine) {
       float s2[RN][4];                // two chains of products
@@ -476,7 +523,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
         pb[t][1] = transpose8(bf16x2(x[2], x[3]));
       }
     }
-    if (!warp_wait(&bars->kv_ready[2][turn.s], turn.ph, bars, status)) { ok = false; break; }
+    wait_on(&bars->kv_ready[2][turn.s], turn.ph, bars);
     turn.skip(1, p.stages);
     if (mine) {
 #pragma unroll
@@ -500,41 +547,39 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
   auto all_warps = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->few);
-    const bool there = warp_wait(&bars->few, few_ph, bars, status);
+    wait_on(&bars->few, few_ph, bars);
     few_ph ^= 1u;
-    return there;
   };
-  // ---- the eight warps' parts are added in shared memory, four rows at a time
-  if (!ok || !all_warps()) return false;          // every warp's staging of the item before is done
-  float* part = reinterpret_cast<float*>(out_smem);                       // [warp][4 rows][kPitch]
-  float2* ml = reinterpret_cast<float2*>(out_smem + 24 * 1024);           // [warp][16 rows]
+  // ---- the eight warps' parts are added in shared memory, two rows at a time
+  float* part = reinterpret_cast<float*>(few_smem);                       // [warp][2 rows][kFewPitch]
+  float2* ml = reinterpret_cast<float2*>(part + 8 * 2 * kFewPitch);       // [warp][kFewRows]
 #pragma unroll
   for (int t = 0; t < RN; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
-      if (quad == 0) ml[warp * 16 + 8 * t + col2 + e] = make_float2(m[t][e], l[t][e]);
+      if (quad == 0) ml[warp * kFewRows + 8 * t + col2 + e] = make_float2(m[t][e], l[t][e]);
     }
 #pragma unroll
-  for (int pass = 0; pass < 2 * RN; ++pass) {
-    if (pass * 4 >= nrows) break;
-    if ((col2 >> 2) == (pass & 1)) {
-      float* dst = part + (warp * 4 + (col2 & 3)) * kPitch + quad;
+  for (int pass = 0; pass < 4 * RN; ++pass) {
+    if (pass * 2 >= nrows) break;
+    if (col2 >> 1 == (pass & 3)) {
+      float* dst = part + warp * 2 * kFewPitch + quad;
 #pragma unroll
       for (int n = 0; n < kSlices; ++n) {
-        dst[n * 16] = o[pass >> 1][n][0];
-        dst[n * 16 + kPitch] = o[pass >> 1][n][1];
-        dst[n * 16 + 8] = o[pass >> 1][n][2];
-        dst[n * 16 + 8 + kPitch] = o[pass >> 1][n][3];
+        dst[n * 16] = o[pass >> 2][n][0];
+        dst[n * 16 + kFewPitch] = o[pass >> 2][n][1];
+        dst[n * 16 + 8] = o[pass >> 2][n][2];
+        dst[n * 16 + 8 + kFewPitch] = o[pass >> 2][n][3];
       }
     }
-    if (!all_warps()) return false;
-    const int rl = threadIdx.x >> 6, r_item = pass * 4 + rl, c = (threadIdx.x & 63) * 2;
-    if (r_item < nrows && c < g.d) {
+    all_warps();
+    const int rl = threadIdx.x >> 6, r_item = pass * 2 + rl, c = (threadIdx.x & 63) * 2;
+    if (rl < 2 && r_item < nrows && c < g.d) {
       float2 a[8];
 #pragma unroll
-      for (int w = 0; w < 8; ++w) a[w] = ml[w * 16 + r_item];
+      for (int w = 0; w < 8; ++w) a[w] = ml[w * kFewRows + r_item];
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < 8; ++w) mm = fmaxf(mm, a[w].x);
@@ -542,7 +587,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
       float sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(part + (w * 4 + rl) * kPitch + c);
+        const float2 v = *reinterpret_cast<const float2*>(part + (w * 2 + rl) * kFewPitch + c);
         if (a[w].y == 0.f) continue;              // nothing seen by this warp
         const float f = ex2((a[w].x - ref) * p.scale_log2);
         sum += a[w].y * f;
@@ -550,7 +595,7 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
         y += v.y * f;
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int rr = it.row0 + r_item, tok = rr / g.R, h = it.group * g.R + rr - tok * g.R;
+      const int rr = it.row0 + r_item, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
       const float lse = sum == 0.f ? -INFINITY : mm * p.scale + logf(sum);
       if (it.part_row < 0) {
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + c) =
@@ -561,32 +606,36 @@ __device__ __forceinline__ bool few_rows(const AttnParams& p, const WorkItem& it
         if (c == 0) g.part_lse[it.part_row + r_item] = lse;
       }
     }
-    if (!all_warps()) return false;
+    all_warps();          // read: the next rows, or the next item's, may be written
   }
-  return true;
 }
 
 // NK: 16-element slices of a head: 8 (d_head 128), 6 (96), 4 (64), 0 (any).  FEW: with the few-rows path;
 // steps of whole prompts do without its registers and code (an 8192-token prompt: 535 -> 500 us).
 template <int NK, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_out,
+                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap few_k, const __grid_constant__ CUtensorMap few_v,
                  const __grid_constant__ AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
+  // Registers of the softmax threads and of the others: two warpgroups each, 256 in all for two threads.
+  constexpr int kSoftmaxRegs = FEW ? 168 : 144, kOtherRegs = 256 - kSoftmaxRegs;
   const StepGeom& g = p.g;
+  const int stages = NK > 0 ? ring_stages(NK > 4 ? 2 : 1) : p.stages;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tile_bytes = p.halves * kHalfBytes;
   uint8_t* q_smem = smem;                              // two row tiles
   uint8_t* kv_smem = smem + 2 * tile_bytes;
-  uint8_t* out_smem = kv_smem + p.stages * tile_bytes;
-  float2* merge_ml = reinterpret_cast<float2*>(out_smem + kStageOut);   // stream 1's (m, l) of every row
-  Bars* bars = reinterpret_cast<Bars*>(merge_ml + kRows);
+  uint8_t* out_smem = kv_smem + stages * tile_bytes;
+  float2* stats = reinterpret_cast<float2*>(out_smem + kStageOut);      // [stream][row]: (m, l)
+  uint8_t* few_smem = reinterpret_cast<uint8_t*>(stats + 2 * kRows);
+  Bars* bars = reinterpret_cast<Bars*>(few_smem + kFewBytes);
   uint32_t* status = &g.head->status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&bars->kv_full[i], 1);
       mbar_init(&bars->kv_ready[0][i], 1);
       mbar_init(&bars->kv_ready[1][i], 1);
@@ -594,22 +643,24 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       mbar_init(&bars->kv_empty[i], 9);      // few rows: 8 warps and the clearing warp, which stands in for whoever does not use it
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->q_full[s], 4);
+      mbar_init(&bars->q_full[s], p.q_boxes ? 1 : 4);
       mbar_init(&bars->drain[s], 1);
-      mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_half[s], 4);
-      mbar_init(&bars->p_full[s], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[s][b], 1);
+        mbar_init(&bars->p_full[s][b], 4);
+        mbar_init(&bars->pv_done[s][b], 1);
+      }
       mbar_init(&bars->o_full[s], 1);
+      mbar_init(&bars->stat_full[s], 4);
+      mbar_init(&bars->stat_empty[s], 4);
       mbar_init(&bars->o_empty[s], 4);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars->slot_full[i], 1);
-      mbar_init(&bars->slot_empty[i], 11);   // softmax warps 8, product warps 2, clearing warp 1
+      mbar_init(&bars->slot_empty[i], 15);   // softmax warps 8, output warps 4, product warps 2, clearing warp 1
     }
-    mbar_init(&bars->merge, 4);
     mbar_init(&bars->few, 8);
     bars->abort_flag = 0;
-    bars->pipe = 0;
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -631,45 +682,44 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const int n_items = fits ? g.head->n_items : 0;
 
   // The softmax threads hold a row of scores each: registers move to them from the other warps.
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if (warp >= 8 && warp < 12) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ key and value tiles
     Ring r;
-    bool ok = true;
     int in_flight = 0;
     // one lane per box: 64 columns of `box` keys
     const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
     // Items are claimed one ahead: the first of a CTA is its own number, the others come from a counter,
     // so that CTAs with cheap items take more of them.
     auto publish = [&](int k, int item) {
-      if (!warp_wait(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars, status)) return false;
+      wait_on(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars);
       int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
       if (lane < (int)(sizeof(WorkItem) / 4))
         d[lane] = item < n_items ? reinterpret_cast<const int*>(g.items + item)[lane] : -1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
-      return true;
     };
     int i = blockIdx.x;
-    ok = publish(0, i);
-    for (int k = 0; i < n_items && ok; ++k) {
+    publish(0, i);
+    for (int k = 0; i < n_items && !gave_up(bars); ++k) {
       const WorkItem it = load_item(g.items + i);
       int next = 0;
       if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
       const int n = item_tiles(it);
-      for (int u = 0; u < n && ok; ++u) {
+#pragma unroll 1
+      for (int u = 0; u < n && !gave_up(bars); ++u) {
         const int ti = it.t0 + u;
         int key0;
         const int keys = tile_keys(it, g, ti, &key0);
         const int32_t* table = ti < it.np ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-        const int boxes = g.tile_pages ? (keys + p.box - 1) / p.box : 1;
+        const int boxes = g.tile_pages ? g.by_page(keys + p.box - 1) : 1;      // box: a page
         int page = 0, off = 0;
         if (bx < boxes) {
           const int idx = ti < it.np ? ti : ti - it.np;
           int pi = idx * g.tile_pages + bx;
           if (!g.tile_pages) {
-            pi = key0 / g.page_size;
+            pi = g.by_page(key0);
             off = key0 - pi * g.page_size;
           }
           page = __ldg(table + pi);
@@ -678,8 +728,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             page = 0;
           }
         }
+#pragma unroll 1
         for (int value = 0; value < 2; ++value) {
-          if (!warp_wait(&bars->kv_empty[r.s], r.ph ^ 1u, bars, status)) { ok = false; break; }
+          wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
           if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[r.s], (uint32_t)(boxes * p.halves * p.box * 128));
           __syncwarp();
           uint8_t* dst = kv_smem + r.s * tile_bytes;
@@ -696,23 +747,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
               tma_load_5d(dst, value ? &few_v : &few_k, &bars->kv_full[r.s], 0, off, 0, it.group, page);
           }
           __syncwarp();
-          r.skip(1, p.stages);
-          in_flight = min(in_flight + 1, p.stages);
-        }
-        if (u == 0 && ok) {         // the claim has come back behind the first copies
-          next = __shfl_sync(0xffffffffu, next, 0);
-          ok = publish(k + 1, next);
+          r.skip(1, stages);
+          in_flight = min(in_flight + 1, stages);
         }
       }
-      if (n == 0) {
-        next = __shfl_sync(0xffffffffu, next, 0);
-        ok = publish(k + 1, next);
-      }
-      i = next;
+      publish(k + 1, __shfl_sync(0xffffffffu, next, 0));      // the claim has come back behind the copies
+      i = __shfl_sync(0xffffffffu, next, 0);
     }
-    if (!ok) {      // given up: wait for the copies that were issued before shared memory goes away
+    if (gave_up(bars)) {      // wait for the copies that were issued before shared memory goes away
       for (int i = 0; i < in_flight; ++i) {
-        const int st = (r.s + p.stages - 1 - i) % p.stages;
+        const int st = (r.s + stages - 1 - i) % stages;
         const uint32_t ph = st < r.s ? r.ph : r.ph ^ 1u;
         const uint64_t t0 = global_timer_ns();
         while (!mbar_test_wait(&bars->kv_full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
@@ -723,87 +767,104 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // The whole warp walks, one lane issues.  The tensor pipe holds about four products, so what
     // this warp does between two batches has to fit in 250 clocks or hide behind the other stream.
     const int s = warp - 9;
-    const uint32_t id_qk = idesc_f16(kRows, kKeyTile, 1);
+    const uint32_t id_qk = idesc_f16(kRows, kHalfKeys, 1);
     const uint32_t id_pv = idesc_f16(kRows, (uint32_t)p.kd, 1) | (1u << 16);   // V is N-major
     // descriptors: the high half is the same for every tile, the low half counts 16-byte steps
     const uint64_t dq = smem_desc_k_sw128(smem_u32(q_smem + s * tile_bytes)), dk0 = smem_desc_k_sw128(smem_u32(kv_smem));
     const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(kv_smem), kHalfBytes);
     const uint32_t tile_step = tile_bytes >> 4, tS = tmem + s * kKeyTile, tO = tmem + kColO + s * kRows;
     const int nk = p.kd / 16;
-    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0, used = 0;
-    bool ok = true;
-    // The stream's tiles become ready in its own order on barriers of its own, so that it sees every
-    // phase of each: at most `stages` of its tiles are in the ring.
-    Ring turn;
-    auto tile_ready = [&]() {
-      const bool there = warp_wait(&bars->kv_ready[s][turn.s], turn.ph, bars, status);
-      turn.skip(1, p.stages);
-      return there;
-    };
-    for (int k = 0; ok; ++k) {
-      if (!slot_wait(bars, k, status)) break;
-      const WorkItem it = uniform_item(bars, k);
-      slot_done(bars, k);
-      if (it.row0 < 0) break;
-      const int n = s ? it.n1 : it.n0;
-      const uint32_t x = used + (it.alt ? 2 * s : 0);      // the ring's number of the stream's first keys
-      used += 2 * item_tiles(it);
-      if (n == 0 || it.alt == 2) continue;
-      Ring r;
-      r.s = x % p.stages;
-      r.ph = (x / p.stages) & 1u;
-      const int to_next = it.alt ? 3 : 1;            // from a tile's values to the stream's next keys
-      ok = warp_wait(&bars->q_full[s], q_ph, bars, status) && tile_ready();
-      if (!ok) break;
-      q_ph ^= 1u;
-      tc_fence_after();
+    uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;
+    Ring base, turn;      // the item's first ring stage; the stream's next turn
+    // The stream's query rows of an item, once its last scores of the one before are done.
+    auto fetch = [&](int k) {
+      const WorkItem& it = bars->slot[k % kSlots];
+      if (!p.q_boxes || (s ? it.n1 : it.n0) == 0 || it.alt == 2) return;
+      const int tok = g.by_R(it.row0 + (it.alt ? 0 : s * kRows));
       if (elect_one()) {
-        issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
-        mma_commit(&bars->s_full[s]);
-        mma_commit(&bars->kv_empty[r.s]);
+        mbar_arrive_expect_tx(&bars->q_full[s], (uint32_t)tile_bytes);
+        for (int h = 0; h < p.halves; ++h)
+          tma_load_4d(q_smem + s * tile_bytes + h * kHalfBytes, &map_q, &bars->q_full[s], h * 64, 0, it.group, tok);
       }
       __syncwarp();
+    };
+    bool fetched = false;
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      if (!fetched) fetch(k);
+      fetched = false;
+      const WorkItem it = uniform_item(bars, k);
+      slot_done(bars, k);
+      const int n = s ? it.n1 : it.n0, tiles = item_tiles(it);
+      Ring rk = base;                                   // stage of the stream's next keys
+      base.advance(2 * tiles, stages);
+      if (n == 0 || it.alt == 2) continue;
+      if (it.alt && s) rk.skip(2, stages);
+      // The stream's tiles become ready in its own order on barriers of its own, so that it sees every
+      // phase of each.  tk and tv: the turns of its next keys and values.
+      Ring rv = rk, tk = turn, tv = turn;
+      rv.skip(1, stages);
+      tv.skip(1, stages);
+      turn.advance(2 * n, stages);
+      const int stride = it.alt ? 4 : 2;                // ring steps from tile to tile of the stream; stages >= 4
+      const int ti_step = it.alt ? 2 : 1, limit = stream_limit(it, g, s);
+      int ti = tile_of(it, s, 0), keys = stream_keys(it, g, ti, limit);
+      // Scores run a tile ahead of the values' products, in half tiles: while the softmax works on one
+      // half, the half before it is multiplied with its values and the next tile's scores take its buffer.
+      wait_on(&bars->q_full[s], q_ph, bars);
+      q_ph ^= 1u;
+      wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+      tc_fence_after();
+      // Every loop over halves is kept one: unrolled, the products' code alone would be 15 KB.
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        int key0;
-        const int keys = tile_keys(it, g, tile_of(it, s, j), &key0);
-        r.skip(1, p.stages);
-        if (!tile_ready()) { ok = false; break; }
-        if (j == 0) {
-          if (!warp_wait(&bars->o_empty[s], oe_ph ^ 1u, bars, status)) { ok = false; break; }
-          oe_ph ^= 1u;
-        }
-        // the first 64 keys' products go ahead while the other probabilities are still computed
-        const int ks = (keys + 15) >> 4;
-        const uint64_t dv = dv0 + r.s * tile_step;
-        if (!warp_wait(&bars->p_half[s], p_ph, bars, status)) { ok = false; break; }
-        tc_fence_after();
-        if (elect_one()) issue_values(0, ks, tO, tS, dv, id_pv, j > 0);
-        __syncwarp();
-        if (!warp_wait(&bars->p_full[s], p_ph, bars, status)) { ok = false; break; }
-        p_ph ^= 1u;
-        tc_fence_after();
-        const int v_st = r.s;
-        const bool end = j + 1 == n;
-        if (!end) {
-          r.skip(to_next, p.stages);
-          if (!tile_ready()) { ok = false; break; }
-          tc_fence_after();
-        }
+      for (int from = 0; from < kKeyTile; from += kHalfKeys) {
         if (elect_one()) {
-          const bool held = lock_pipe(bars);
-          issue_values(4, ks, tO, tS, dv, id_pv, true);
-          mma_commit(&bars->kv_empty[v_st]);
-          if (end) {
-            mma_commit(&bars->o_full[s]);
-          } else {
-            issue_scores<NK>(nk, tS, dq, dk0 + r.s * tile_step, id_qk);
-            mma_commit(&bars->s_full[s]);
-            mma_commit(&bars->kv_empty[r.s]);
-          }
-          if (held) unlock_pipe(bars);
+          if (keys > from) issue_scores<NK>(nk, tS + from, dq, dk0 + rk.s * tile_step + (from * 128 >> 4), id_qk);
+          mma_commit(&bars->s_full[s][from / kHalfKeys]);
+          if (from) mma_commit(&bars->kv_empty[rk.s]);
         }
         __syncwarp();
+      }
+      wait_on(&bars->o_empty[s], oe_ph ^ 1u, bars);
+      oe_ph ^= 1u;
+#pragma unroll 1
+      for (int left = n; left > 0; --left) {
+        const bool more = left > 1;
+        ti += ti_step;
+        const int next_keys = more ? stream_keys(it, g, ti, limit) : 0;
+        wait_on(&bars->kv_ready[s][tv.s], tv.ph, bars);
+        tv.skip(2, stages);
+        rk.skip(stride, stages);
+        tk.skip(2, stages);
+        if (more) wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+        const uint64_t dv = dv0 + rv.s * tile_step, dk = dk0 + rk.s * tile_step;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int from = h * kHalfKeys;
+          wait_on(&bars->p_full[s][h], p_ph, bars);
+          tc_fence_after();
+          if (elect_one()) {
+            issue_values((keys - from + 15) >> 4, tO, tS + from, dv + (from * 128 >> 4), id_pv, h > 0 || left < n);
+            mma_commit(&bars->pv_done[s][h]);
+            if (h == 1) mma_commit(&bars->kv_empty[rv.s]);
+            if (more) {
+              if (next_keys > from) issue_scores<NK>(nk, tS + from, dq, dk + (from * 128 >> 4), id_qk);
+              mma_commit(&bars->s_full[s][h]);
+              if (h == 1) mma_commit(&bars->kv_empty[rk.s]);
+            } else if (h == 1) {
+              mma_commit(&bars->o_full[s]);
+            }
+          }
+          __syncwarp();
+          // the last scores are done (this wait takes no part in the barrier): the next item's rows may come
+          if (h == 0 && !more) {
+            wait_on(&bars->s_full[s][1], p_ph, bars);
+            if (slot_wait(bars, k + 1)) fetch(k + 1);
+            fetched = true;
+          }
+        }
+        p_ph ^= 1u;
+        rv.skip(stride, stages);
+        keys = next_keys;
       }
     }
     if (elect_one()) {
@@ -818,25 +879,25 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // barrier by a round; for a stream that does not use it this warp empties it.
     Ring turn[3];
     Ring r;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!slot_wait(bars, k, status)) break;
+    for (int k = 0; slot_wait(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       slot_done(bars, k);
-      if (it.row0 < 0) break;
       const int n = item_tiles(it);
-      for (int u = 0; u < n && ok; ++u) {
+#pragma unroll 1
+      for (int u = 0; u < n; ++u) {
         int key0;
         const int keys = tile_keys(it, g, it.t0 + u, &key0);
         const bool few = it.alt == 2;
         const bool use0 = !few && (it.alt ? !(u & 1) : u < it.n0), use1 = !few && (it.alt ? u & 1 : u < it.n1);
+#pragma unroll 1
         for (int value = 0; value < 2; ++value) {
-          if (!warp_wait(&bars->kv_full[r.s], r.ph, bars, status)) { ok = false; break; }
+          wait_on(&bars->kv_full[r.s], r.ph, bars);
           if (value && (keys & 15)) {
             // rows keys .. the next multiple of 16: whole 128-byte rows, so the swizzle does not matter
             const int rows_clear = 16 - (keys & 15);
             uint8_t* tile = kv_smem + r.s * tile_bytes;
             const uint32_t step = few ? p.box * 128 : kHalfBytes;
+#pragma unroll 1
             for (int q = lane; q < rows_clear * 8; q += 32) {
               const int key = keys + (q >> 3);
               uint8_t* at = tile + (few ? few_row(p, key) : key * 128) + (q & 7) * 16;
@@ -851,237 +912,186 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (few) mbar_arrive(&bars->kv_ready[2][turn[2].s]);
             mbar_arrive_n(&bars->kv_empty[r.s], few ? 1 : 9 - (use0 ? 1 : 0) - (use1 ? 1 : 0));
           }
-          if (use0) turn[0].skip(1, p.stages);
-          if (use1) turn[1].skip(1, p.stages);
-          if (few) turn[2].skip(1, p.stages);
-          r.skip(1, p.stages);
+          if (use0) turn[0].skip(1, stages);
+          if (use1) turn[1].skip(1, stages);
+          if (few) turn[2].skip(1, stages);
+          r.skip(1, stages);
         }
       }
     }
   }
-  } else {
-    // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2;                         // stream
     const int row = threadIdx.x & (kRows - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + s * kKeyTile;
     const uint32_t tO = tmem + lane_base + kColO + s * kRows;
-    uint8_t* q_tile = q_smem + s * tile_bytes;
-    uint32_t s_ph = 0, o_ph = 0, m_ph = 0, used = 0, few_ph = 0;
+    uint32_t s_ph = 0, st_ph = 0, used = 0, few_ph = 0;
     Ring few_turn;
-    bool ok = true;
-    const uint32_t stage_out = smem_u32(out_smem) + warp * 4096;
-    // this thread's query row in an item, null if there is none (the stream has no tile, or the item no such row)
-    auto query_row = [&](const WorkItem& it) {
-      const int r_item = row + (it.alt ? 0 : s * kRows);
-      if ((s ? it.n1 : it.n0) == 0 || it.alt == 2 || r_item >= it.nrows) return static_cast<const uint16_t*>(nullptr);
-      const int rr = it.row0 + r_item, tok = rr / g.R;
-      return p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-    };
-    auto fetch = [&](int k) {          // the stream's query rows of the item in slot k
-      const WorkItem& it = bars->slot[k % kSlots];
-      if (it.row0 < 0 || (s ? it.n1 : it.n0) == 0 || it.alt == 2) return;
-      if (!p.q_boxes) {
-        copy_queries(p, query_row(it), q_tile + (row & ~31) * 128);
-      } else if ((warp & 3) == 0 && elect_one()) {
-        const int tok = (it.row0 + (it.alt ? 0 : s * kRows)) / g.R;
-        mbar_arrive_expect_tx(&bars->q_full[s], (uint32_t)tile_bytes);
-        for (int h = 0; h < p.halves; ++h)
-          tma_load_4d(q_tile + h * kHalfBytes, &map_q, &bars->q_full[s], h * 64, 0, it.group, tok);
-      }
-    };
-    ok = slot_wait(bars, 0, status);
-    if (ok) fetch(0);
-    for (int k = 0; ok; ++k) {
-      const WorkItem& it = bars->slot[k % kSlots];      // held until the item is done
-      if (it.row0 < 0) break;
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
       const uint32_t first_tile = used;
       used += 2 * item_tiles(it);
       if constexpr (FEW) {
         if (it.alt == 2) {
-          ok = it.nrows <= 8 ? few_rows<NK, 1>(p, it, bars, status, kv_smem, out_smem, first_tile, few_turn, few_ph)
-                             : few_rows<NK, 2>(p, it, bars, status, kv_smem, out_smem, first_tile, few_turn, few_ph);
-          ok = ok && slot_wait(bars, k + 1, status);
-          if (ok) fetch(k + 1);
+          if (it.nrows <= 8) few_rows<NK, 1>(p, it, bars, status, kv_smem, few_smem, first_tile, few_turn, few_ph);
+          else few_rows<NK, 2>(p, it, bars, status, kv_smem, few_smem, first_tile, few_turn, few_ph);
           slot_done(bars, k);
           continue;
         }
       }
       const int n = s ? it.n1 : it.n0;
-      if (n > 0) {
-        if (!p.q_boxes) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0 && !(p.q_boxes && (warp & 3) == 0)) mbar_arrive(&bars->q_full[s]);
-      }
       const int r_item = row + (it.alt ? 0 : s * kRows);
       const int rr = it.row0 + r_item;
       const bool live = r_item < it.nrows;
       const bool warp_live = (row & ~31) + (it.alt ? 0 : s * kRows) < it.nrows;
-      const int tok = rr / g.R;
+      const int tok = g.by_R(rr);
       // own keys in view of this row; padding rows see nothing at all
       const int own_vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
       const bool blind = !live || (it.seq >= 0 && own_vis <= 0);
+      if (n > 0 && !p.q_boxes) {      // query rows that no box holds (R does not divide 128); the stream's last scores are done
+        copy_queries(p, live ? p.q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d : nullptr,
+                     q_smem + s * tile_bytes + (row & ~31) * 128);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full[s]);
+      }
       float m = -INFINITY, l = 0.f;                  // m: the maximum that O and l refer to
+      const int limit = stream_limit(it, g, s);
       for (int j = 0; j < n; ++j) {
         const int ti = tile_of(it, s, j);
         int key0;
-        const int keys = tile_keys(it, g, ti, &key0);
-        int vis = ti < it.np ? keys : min(keys, own_vis - key0);      // keys in view of this row
-        if (blind) vis = 0;
-        const bool masked = __any_sync(0xffffffffu, vis < kKeyTile);
-        if (!warp_wait(&bars->s_full[s], s_ph, bars, status)) { ok = false; break; }
-        s_ph ^= 1u;
-        if (warp_live) {
-          tc_fence_after();
-          // the second half's scores come in while the first half's maximum is taken
-          uint32_t v[128];
-          tmem_ld32(tS, v);
-          tmem_ld32(tS + 32, v + 32);
-          tmem_ld_wait();
-          tmem_ld32(tS + 64, v + 64);
-          tmem_ld32(tS + 96, v + 96);
-          const int least = masked ? __reduce_min_sync(0xffffffffu, vis) : kKeyTile;
-          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int half = 0; half < 128; half += 64) {
-            if (half) tmem_ld_wait();
+        const int keys = tile_keys(it, g, ti, &key0), used_keys = stream_keys(it, g, ti, limit);
+        int vis_tile = ti < it.np ? keys : min(keys, own_vis - key0);      // keys in view of this row
+        if (blind) vis_tile = 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int vis = vis_tile - h * kHalfKeys;
+          const bool masked = __any_sync(0xffffffffu, vis < kHalfKeys);
+          const uint32_t tB = tS + h * kHalfKeys;
+          wait_on(&bars->s_full[s][h], s_ph, bars);
+          if (warp_live && h * kHalfKeys < used_keys) {
+            tc_fence_after();
+            uint32_t v[kHalfKeys];
+            tmem_ld32(tB, v);
+            tmem_ld32(tB + 32, v + 32);
+            tmem_ld_wait();
             if (masked) {
 #pragma unroll
-              for (int c0 = half; c0 < half + 64; c0 += 32)
-                if (least < c0 + 32) {
-#pragma unroll
-                  for (int c = c0; c < c0 + 32; ++c)
-                    if (c >= vis) v[c] = 0xff800000u;  // -inf: chosen, not added, so a NaN behind the mask is gone
-                }
+              for (int c = 0; c < kHalfKeys; ++c)
+                if (c >= vis) v[c] = 0xff800000u;      // -inf: chosen, not added, so a NaN behind the mask is gone
             }
+            float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = half; c < half + 64; c += 8)
+            for (int c = 0; c < kHalfKeys; c += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(v[c + e]), __uint_as_float(v[c + e + 4]));
-          }
-          const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          if (j == 0) {
-            m = m_new;
-          } else {
-            const bool grow = (m_new - m) * p.scale_log2 > kRescale;
-            if (__any_sync(0xffffffffu, grow)) {
-              // the products of earlier tiles are done: S of this tile was issued after them
-              const float f = grow ? ex2((m - m_new) * p.scale_log2) : 1.f;
-              if (grow) m = m_new;
-              l *= f;
-              for (int c = 0; c < p.kd; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(tO + c, o);
-                tmem_ld_wait();
+            const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            if (j == 0 && h == 0) {
+              m = m_new;
+            } else {
+              const bool grow = (m_new - m) * p.scale_log2 > kRescale;
+              if (__any_sync(0xffffffffu, grow)) {
+                // O is this warp's once the latest product is done (those before it are: these scores were
+                // issued after them)
+                wait_on(&bars->pv_done[s][h ^ 1], h ? s_ph : s_ph ^ 1u, bars);
+                tc_fence_after();
+                const float f = grow ? ex2((m - m_new) * p.scale_log2) : 1.f;
+                if (grow) m = m_new;
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < p.kd; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + c, o);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tO + c, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(tO + c, o);
+                }
               }
             }
-          }
-          const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          const uint64_t sc2 = pk(p.scale_log2, p.scale_log2), ng2 = pk(neg, neg);
-          uint64_t sum0 = pk(0.f, 0.f), sum1 = sum0;
+            const float neg = m == -INFINITY ? 0.f : -m * p.scale_log2;
+            const uint64_t sc2 = pk(p.scale_log2, p.scale_log2), ng2 = pk(neg, neg);
+            uint64_t sum0 = pk(0.f, 0.f), sum1 = sum0;
+            uint32_t w[kHalfKeys / 2];
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            if (c == 64) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars->p_half[s]);
-            }
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = unpk(fma2(pk_u(v[c + 2 * e], v[c + 2 * e + 1]), sc2, ng2));
+            for (int e = 0; e < kHalfKeys / 2; ++e) {
+              const float2 x = unpk(fma2(pk_u(v[2 * e], v[2 * e + 1]), sc2, ng2));
               const float a = ex2(x.x), b = ex2(x.y);
               if (e & 1) sum1 = add2(sum1, pk(a, b));
               else sum0 = add2(sum0, pk(a, b));
               w[e] = bf16x2(a, b);
             }
-            tmem_st16(tS + c / 2, w);
+            tmem_st32(tB, w);
+            const float2 z = unpk(add2(sum0, sum1));
+            l += z.x + z.y;
+            tmem_st_wait();
+            tc_fence_before();
           }
-          const float2 z = unpk(add2(sum0, sum1));
-          l += z.x + z.y;
-          tmem_st_wait();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (!warp_live) mbar_arrive(&bars->p_half[s]);
-          mbar_arrive(&bars->p_full[s]);
-        }
-        // the stream's last scores have been read, so its query rows are free for the next item's
-        if (j + 1 == n) {
-          if (!slot_wait(bars, k + 1, status)) { ok = false; break; }
-          fetch(k + 1);
-        }
-      }
-      if (ok && n == 0) {
-        ok = slot_wait(bars, k + 1, status);
-        if (ok) fetch(k + 1);
-      }
-      if (!ok) break;
-      // ---- output.  Streams that share the rows are merged by stream 0's threads.
-      const bool merging = it.alt && it.n1 > 0;
-      if (n > 0) {
-        if (!warp_wait(&bars->o_full[s], o_ph, bars, status)) { ok = false; break; }
-        o_ph ^= 1u;
-      }
-      if (s == 1 && it.alt) {
-        if (n > 0) {
-          // stream 0 has read the previous item's (m, l): it freed this O, hence these products, afterwards
-          merge_ml[row] = make_float2(m, l);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->merge);
+          if (lane == 0) mbar_arrive(&bars->p_full[s][h]);
         }
-        slot_done(bars, k);
-        continue;
+        s_ph ^= 1u;
       }
-      float f0 = 1.f, f1 = 0.f;
-      if (merging) {
-        // arrives after stream 1's last product, so its O is complete as well
-        if (!warp_wait(&bars->merge, m_ph, bars, status)) { ok = false; break; }
-        m_ph ^= 1u;
-        const float2 o = merge_ml[row];
-        const float mm = fmaxf(m, o.x);
-        if (mm != -INFINITY) {
-          f0 = ex2((m - mm) * p.scale_log2);
-          f1 = ex2((o.x - mm) * p.scale_log2);
-        }
-        l = l * f0 + o.y * f1;
-        m = mm;
+      if (n > 0) {
+        // (m, l) to the output warps, once they have taken the item's before
+        wait_on(&bars->stat_empty[s], st_ph ^ 1u, bars);
+        st_ph ^= 1u;
+        stats[s * kRows + row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->stat_full[s]);
       }
-      if (warp_live) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;      // a row without keys: zero
-        f0 *= inv;
-        f1 *= inv;
-        tc_fence_after();
-        const int h = it.group * g.R + rr - tok * g.R;
-        const bool direct = it.part_row < 0;
-        uint8_t* mine = !live ? nullptr
-                        : direct ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d)
-                                 : reinterpret_cast<uint8_t*>(g.part_out + (int64_t)(it.part_row + r_item) * g.d);
-        const bool none = l == 0.f;                                // a row without keys is zero
-        // 32 columns of the row, finished
-        auto read32 = [&](int c, float* y) {
-          uint32_t v[32];
-          if (n > 0) tmem_ld32(tO + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : __uint_as_float(v[e]) * f0;
-          if (merging) {
-            tmem_ld32(tO + kRows + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : y[e] + __uint_as_float(v[e]) * f1;
-          }
+      slot_done(bars, k);
+    }
+  } else {
+    // ------------------------------------------------------------ output
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int row = threadIdx.x & (kRows - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t stage_out = smem_u32(out_smem) + (warp & 3) * 4096;
+    uint32_t ph = 0;                                 // bit s: stream s
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      slot_done(bars, k);
+      if (it.alt == 2) continue;
+      const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
+#pragma unroll 1
+      for (int s = 0; s < (it.alt ? 1 : 2); ++s) {
+        const int n = s ? it.n1 : it.n0;
+        const uint32_t tO = tmem + lane_base + kColO + s * kRows;
+        const int r_item = row + s * kRows;
+        const int rr = it.row0 + r_item;
+        const bool live = r_item < it.nrows, warp_live = (row & ~31) + s * kRows < it.nrows;
+        const int tok = g.by_R(rr);
+        float m = -INFINITY, l = 0.f, f0 = 1.f, f1 = 0.f;
+        auto take = [&](int x) {                     // stream x's (m, l); its O is complete then
+          wait_on(&bars->stat_full[x], (ph >> x) & 1u, bars);
+          const float2 v = stats[x * kRows + row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->stat_empty[x]);
+          wait_on(&bars->o_full[x], (ph >> x) & 1u, bars);
+          ph ^= 1u << x;
+          return v;
         };
-        auto free_o = [&]() {                                      // for the next item's products
+        if (n > 0) {
+          const float2 v = take(s);
+          m = v.x;
+          l = v.y;
+        }
+        if (merging) {
+          const float2 o = take(1);
+          const float mm = fmaxf(m, o.x);
+          if (mm != -INFINITY) {
+            f0 = ex2((m - mm) * p.scale_log2);
+            f1 = ex2((o.x - mm) * p.scale_log2);
+          }
+          l = l * f0 + o.y * f1;
+          m = mm;
+        }
+        auto free_o = [&]() {                        // for the next item's products
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -1089,56 +1099,92 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (merging) mbar_arrive(&bars->o_empty[1]);
           }
         };
-        // 128 bytes of each row at a time go through shared memory, so that the stores cover whole
-        // lines: 64 bf16 columns of the output, 32 fp32 columns of a partial row.
-        const int row_bytes = g.d * (direct ? 2 : 4);
-        auto put = [&](int byte0) {
-          __syncwarp();
-          const int piece = lane & 7, byte = byte0 + piece * 16;
-#pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + (lane >> 3);
-            uint8_t* dst =
-                reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
-            if (dst && byte < row_bytes) *reinterpret_cast<uint4*>(dst + byte) = ld_shared16(stage_at(stage_out, r, piece));
-          }
-          __syncwarp();
-        };
+        if (!warp_live) {
+          free_o();
+          continue;
+        }
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;      // a row without keys: zero
+        f0 *= inv;
+        f1 *= inv;
+        tc_fence_after();
+        const int h = it.group * g.R + rr - tok * g.R;
+        const bool direct = it.part_row < 0;
+        // 128 bytes of each row at a time go through shared memory: 64 bf16 columns of the output, 32 fp32
+        // columns of a partial row.  A warp whose 32 rows are all there (and whole tokens) writes output
+        // as one bulk copy; otherwise stores of whole lines, with the rows' numbers from their lanes.
+        const bool bulk = direct && p.out_boxes && (row & ~31) + s * kRows + 32 <= it.nrows;
+        const int mine = !live ? -1 : direct ? tok * g.H + h : it.part_row + r_item;
+        const bool none = l == 0.f, some_none = __any_sync(0xffffffffu, none);   // rows without keys are zero
+        const int first_tok = __shfl_sync(0xffffffffu, tok, 0);
 #pragma unroll 1
         for (int c = 0; c < p.kd; c += 32) {
-          float y[32];
-          read32(c, y);
+          uint32_t v[32];
+          if (n > 0) tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+          if (merging) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 16) {
+              uint32_t w[16];
+              tmem_ld16(tO + kRows + c + x, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                v[x + e] = __float_as_uint(__uint_as_float(v[x + e]) + __uint_as_float(w[e]) * f1);
+            }
+          }
+          if (some_none) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = none ? 0u : v[e];
+          }
           if (c + 32 >= p.kd) free_o();
           if (direct) {
+            if (!(c & 32)) {       // the block's copy before has been read
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               st_shared16(stage_at(stage_out, lane, (c & 32) / 8 + q),
-                          make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                                     bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7])));
-            if ((c & 32) || c + 32 >= p.kd) put((c & 64) * 2);
+                          make_uint4(bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
+                                     bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
+                                     bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
+                                     bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]))));
+            if (!(c & 32) && c + 32 < p.kd) continue;
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              st_shared16(stage_at(stage_out, lane, q),
-                          make_uint4(__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]), __float_as_uint(y[4 * q + 2]),
-                                     __float_as_uint(y[4 * q + 3])));
-            put(c * 4);
+              st_shared16(stage_at(stage_out, lane, q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
           }
+          if (bulk) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_4d(out_smem + (warp & 3) * 4096, &map_out, c & 64, 0, it.group, first_tok);
+            __syncwarp();
+            continue;
+          }
+          __syncwarp();
+          uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(g.part_out);
+          const int piece = lane & 7, row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & 64) * 2 : c * 4) + piece * 16;
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            const int which = __shfl_sync(0xffffffffu, mine, r);
+            if (which >= 0 && byte < row_bytes)
+              *reinterpret_cast<uint4*>(to + (int64_t)which * row_bytes + byte) = ld_shared16(stage_at(stage_out, r, piece));
+          }
+          __syncwarp();
         }
         if (live) {
           const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
-          if (direct) {
-            if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
-          } else {
-            g.part_lse[it.part_row + r_item] = lse;
-          }
+          if (!direct) g.part_lse[mine] = lse;
+          else if (p.lse) p.lse[mine] = lse;
         }
-      } else if (lane == 0) {
-        if (n > 0) mbar_arrive(&bars->o_empty[s]);
-        if (merging) mbar_arrive(&bars->o_empty[1]);
       }
-      slot_done(bars, k);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -1147,6 +1193,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
   if (fits && threadIdx.x == 0) {
     __threadfence();
@@ -1159,23 +1206,23 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
 
 template <int NK, bool FEW>
-aff_status launch_attention(const CUtensorMap (&m)[5], const AttnParams& p, unsigned grid, int smem,
+aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
-  // The register split needs the launch to own 168 registers a thread: 2 x 216 + 72 = 3 x 168.
+  // The register split needs the launch to own 128 registers a thread.
   static const cudaError_t ready = [] {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK, FEW>);
-    if (e == cudaSuccess && fa.numRegs != 168) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && fa.numRegs != 128) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(attention_kernel<NK, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     return e;
   }();
   AFF_CUDA(ready);
-  AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[1], m[2], m[3], m[4], p));
+  AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[5], m[1], m[2], m[3], m[4], p));
   return AFF_OK;
 }
 template <bool FEW>
-aff_status launch_attention(const CUtensorMap (&m)[5], const AttnParams& p, unsigned grid, int smem,
+aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
   switch (p.kd / 16) {
     case 8: return launch_attention<8, FEW>(m, p, grid, smem, s);
@@ -1210,7 +1257,7 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
     const int r = i / d4, c = (i - r * d4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < it.nrows) {
-      const int rr = it.row0 + r, tok = rr / g.R;
+      const int rr = it.row0 + r, tok = g.by_R(rr);
       v = *reinterpret_cast<const float4*>(q + (int64_t)tok * p.q_stride + (int64_t)(it.group * g.R + rr - tok * g.R) * d + c);
     }
     *reinterpret_cast<float4*>(qs + r * ld + c) = v;
@@ -1219,7 +1266,7 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
   int own_vis[RT];
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
-    const int r = ty * RT + a, tok = (it.row0 + r) / g.R;
+    const int r = ty * RT + a, tok = g.by_R(it.row0 + r);
     m[a] = -INFINITY;
     l[a] = 0.f;
     own_vis[a] = it.seq < 0 ? 1 : tok + it.own_off + 1;
@@ -1241,7 +1288,7 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
       const int r = i / d4, c = (i - r * d4) * 4;
       float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
       if (r < keys) {
-        const int key = key0 + r, pi = key / g.page_size;
+        const int key = key0 + r, pi = g.by_page(key);
         const int page = __ldg(table + pi);
         if (page >= 0 && page < g.n_pages) {
           const int64_t at = page * p.page_stride + it.group * p.group_stride + (int64_t)(key - pi * g.page_size) * p.token_stride + c;
@@ -1319,7 +1366,7 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
   for (int a = 0; a < RT; ++a) {
     const int r = ty * RT + a;
     if (r >= it.nrows) continue;
-    const int rr = it.row0 + r, tok = rr / g.R, h = it.group * g.R + rr - tok * g.R;
+    const int rr = it.row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
     const bool empty = l[a] == 0.f;
     const float inv = empty ? 0.f : 1.f / l[a];
     float* dst = it.part_row < 0 ? static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * d
@@ -1374,7 +1421,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   const int lane = threadIdx.x & 31;
   if (at >= (int64_t)g.T * g.H || !plan_matches(g) || g.head->n_items < 0) return;
   const int t = (int)(at / g.H), h = (int)(at - (int64_t)t * g.H);
-  const int group = h / g.R, rr = t * g.R + h - group * g.R;
+  const int group = g.by_R(h), rr = t * g.R + h - group * g.R;
   const TokenInfo ti = g.tok[t];
   const PlanHeader& hd = *g.head;
   int n_pre = 0, pre0 = 0, pre_step = 0, n_own = 0, own0 = 0, own_step = 0;
@@ -1475,11 +1522,10 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
     p.kd = (g.d + 15) / 16 * 16;
     p.box = g.tile_pages ? g.page_size : g.key_tile;
     const int tile = p.halves * kHalfBytes;
-    const int fixed = 1024 + 2 * tile + kStageOut + kRows * (int)sizeof(float2) + (int)sizeof(Bars);
-    p.stages = (kSmemMax - fixed) / tile;
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const int smem = fixed + p.stages * tile;
-    CUtensorMap m[5];          // queries, keys, values; keys and values with whole rows
+    static_assert(sizeof(Bars) <= 1024, "ring_stages leaves 1024 bytes for the barriers");
+    p.stages = ring_stages(p.halves);
+    const int smem = 1024 + (2 + p.stages) * tile + kStageOut + 2 * kRows * (int)sizeof(float2) + kFewBytes + (int)sizeof(Bars);
+    CUtensorMap m[6];          // queries, keys, values; keys and values with whole rows; output
     const uint64_t tok = (uint64_t)cache->token_stride * 2, grp = (uint64_t)cache->group_stride * 2,
                    pag = (uint64_t)cache->page_stride * 2;
     const uint64_t dims[4] = {(uint64_t)g.d, (uint64_t)g.page_size, (uint64_t)g.G, (uint64_t)g.n_pages};
@@ -1494,6 +1540,13 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
       const uint64_t qd[4] = {(uint64_t)g.d, (uint64_t)g.R, (uint64_t)g.G, (uint64_t)g.T};
       const uint64_t qs[3] = {(uint64_t)g.d * 2, (uint64_t)g.R * g.d * 2, (uint64_t)q_stride * 2};
       if ((st = map_16bit_sw128(&m[0], q, 4, qd, qs, (uint32_t)g.R, 1, (uint32_t)(kRows / g.R), 3)) != AFF_OK) return st;
+    }
+    m[5] = m[1];
+    p.out_boxes = 32 % g.R == 0;
+    if (p.out_boxes) {
+      const uint64_t od[4] = {(uint64_t)g.d, (uint64_t)g.R, (uint64_t)g.G, (uint64_t)g.T};
+      const uint64_t os[3] = {(uint64_t)g.d * 2, (uint64_t)g.R * g.d * 2, (uint64_t)g.H * g.d * 2};
+      if ((st = map_16bit_sw128(&m[5], out, 4, od, os, (uint32_t)g.R, 1, (uint32_t)(32 / g.R), 3)) != AFF_OK) return st;
     }
     p.whole_rows = g.few && g.d == 128;
     if (p.whole_rows) {       // the halves as a dimension of their own

@@ -38,6 +38,24 @@ constexpr int kFewRows = 16;             // most rows of an item that takes the 
 constexpr int kPlanSms = 152;            // SMs of a GB300: sizes the plan without a device
 constexpr uint32_t kPlanMagic = 0x41465331u;
 
+// Division of 0 <= x < 2^31 by a number known on the host: a multiply, an add and a shift, where the
+// device's own division by a variable is some forty instructions at every place it is used.
+struct FastDiv {
+  uint32_t m = 1, shift = 0, d = 1;
+  void set(uint32_t by) {
+    d = by;
+    shift = 0;
+    while ((1ull << shift) < by) ++shift;
+    m = (uint32_t)(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+  }
+#ifdef __CUDACC__
+  __host__ __device__
+#endif
+  int operator()(int x) const {
+    return (int)(((uint32_t)(((uint64_t)m * (uint32_t)x) >> 32) + (uint32_t)x) >> shift);
+  }
+};
+
 struct TokenInfo {       // one per token of the step; 16 bytes
   int64_t slot;          // page * page_size + offset of its own key, -1: padding
   int32_t own;           // index among its sequence's own tokens, -1: padding
@@ -88,6 +106,7 @@ struct StepGeom {
   int32_t prefix_rows;   // row tile of the prefix's jobs
   int32_t prefix_tiles;  // row tiles of the prefix's jobs
   int32_t max_items, max_part_rows;
+  FastDiv by_R, by_page, by_tile, by_page_tiles;
   int64_t n_pages;
   const int32_t *q_start, *kv_len, *pages, *prefix_pages;
   // plan buffer
@@ -111,9 +130,9 @@ __host__ __device__ inline int ceil_div_i(int a, int b) { return (a + b - 1) / b
 
 // Key tiles of a segment of `len` keys.
 __host__ __device__ __forceinline__ int segment_tiles(const StepGeom& g, int len) {
-  if (g.tile_pages) return (len + g.key_tile - 1) / g.key_tile;
-  const int pages = len / g.page_size;
-  return pages * g.page_tiles + (len - pages * g.page_size + g.key_tile - 1) / g.key_tile;
+  if (g.tile_pages) return g.by_tile(len + g.key_tile - 1);
+  const int pages = g.by_page(len);
+  return pages * g.page_tiles + g.by_tile(len - pages * g.page_size + g.key_tile - 1);
 }
 
 // First key and number of keys of tile `idx` of a segment of `len` keys.
@@ -122,7 +141,7 @@ __device__ __forceinline__ int tile_span(const StepGeom& g, int len, int idx, in
     *key0 = idx * g.key_tile;
     return min(g.key_tile, len - *key0);
   }
-  const int page = idx / g.page_tiles, in_page = (idx - page * g.page_tiles) * g.key_tile;
+  const int page = g.by_page_tiles(idx), in_page = (idx - page * g.page_tiles) * g.key_tile;
   *key0 = page * g.page_size + in_page;
   return min(min(g.key_tile, g.page_size - in_page), len - *key0);
 }
@@ -152,7 +171,7 @@ __device__ __forceinline__ SeqShape seq_shape(const StepGeom& g, int b) {
 
 // Own keys that the last of the first `upto` rows of a sequence sees.
 __device__ __forceinline__ int keys_in_view(const StepGeom& g, const SeqShape& s, int upto) {
-  const int last = (min(upto, s.rows) - 1) / g.R;
+  const int last = s.rows > 0 ? g.by_R(min(upto, s.rows) - 1) : 0;
   return min(max(s.kv - (s.q1 - s.q0) + last + 1, 0), s.kv);
 }
 

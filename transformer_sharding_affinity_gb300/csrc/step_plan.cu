@@ -330,6 +330,10 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     g.key_tile = (g.page_size / g.page_tiles + (g.page_size % g.page_tiles != 0) + 7) / 8 * 8;
     g.page_tiles = (g.page_size + g.key_tile - 1) / g.key_tile;
   }
+  g.by_R.set((uint32_t)g.R);
+  g.by_page.set((uint32_t)g.page_size);
+  g.by_tile.set((uint32_t)g.key_tile);
+  g.by_page_tiles.set((uint32_t)std::max(g.page_tiles, 1));
   g.np = segment_tiles(g, g.prefix_len);
   const bool bf = c->dtype == AFF_BF16;
   g.small = bf ? 128 : 16;
