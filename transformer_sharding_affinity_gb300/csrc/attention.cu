@@ -11,9 +11,8 @@
 //   A work item (step.cuh) is up to 256 packed rows against a run of 128-key
 //   tiles.  Two streams alternate on the tensor core: while the threads of one
 //   turn its scores S into probabilities P, the products of the other run.
-//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row; they also fetch
-//                      their query rows, the next item's when this one's scores are read
-//     warp 8           TMA: key and value tiles through the page tables
+//     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
+//     warp 8           TMA: query rows; key and value tiles through the page tables
 //     warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from
 //                      shared memory) and O += P V (P from tensor memory)
 //     warp 11          clears the rows of a value tile past its keys: 0 * NaN would stay
@@ -89,7 +88,7 @@ __host__ __device__ constexpr int ring_stages(int halves) {
 struct alignas(16) Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t kv_ready[3][kMaxStages];          // stream 0, stream 1, few rows: their own tiles, in their own order
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
   uint64_t stat_full[2], stat_empty[2], few, drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
   uint32_t tmem;
@@ -644,6 +643,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->q_full[s], p.q_boxes ? 1 : 4);
+      mbar_init(&bars->q_empty[s], 1);
       mbar_init(&bars->drain[s], 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars->s_full[s][b], 1);
@@ -688,6 +688,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // ------------------------------------------------------------ key and value tiles
     Ring r;
     int in_flight = 0;
+    uint32_t q_ph = 0;                  // bit x: stream x
     // one lane per box: 64 columns of `box` keys
     const int bx = p.halves == 2 ? lane >> 1 : lane, hf = p.halves == 2 ? lane & 1 : 0;
     // Items are claimed one ahead: the first of a CTA is its own number, the others come from a counter,
@@ -707,6 +708,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       int next = 0;
       if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
       const int n = item_tiles(it);
+      // the streams' query rows, as soon as the item before has no scores left to compute
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (!p.q_boxes || (FEW && it.alt == 2) || (x ? it.n1 : it.n0) == 0) continue;
+        wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+        q_ph ^= 1u << x;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->q_full[x], (uint32_t)tile_bytes);
+        __syncwarp();
+        if (lane < p.halves)
+          tma_load_4d(q_smem + x * tile_bytes + lane * kHalfBytes, &map_q, &bars->q_full[x], lane * 64, 0, it.group,
+                      g.by_R(it.row0 + (it.alt ? 0 : x * kRows)));
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int u = 0; u < n && !gave_up(bars); ++u) {
         const int ti = it.t0 + u;
@@ -735,7 +749,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           __syncwarp();
           uint8_t* dst = kv_smem + r.s * tile_bytes;
           if (bx >= boxes) {
-          } else if (it.alt != 2) {
+          } else if (!(FEW && it.alt == 2)) {
             tma_load_4d(dst + hf * kHalfBytes + bx * p.box * 128, value ? &map_v : &map_k, &bars->kv_full[r.s], hf * 64,
                         off, it.group, page);
           } else {
@@ -761,6 +775,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const uint64_t t0 = global_timer_ns();
         while (!mbar_test_wait(&bars->kv_full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
       }
+      for (int x = 0; x < 2 && p.q_boxes; ++x) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test_wait(&bars->q_full[x], ((q_ph >> x) & 1u) ^ 1u) && global_timer_ns() - t0 < 100000000ull) {}
+      }
     }
   } else if (warp < 11) {
     // ------------------------------------------------------------ products
@@ -776,28 +794,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const int nk = p.kd / 16;
     uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;
     Ring base, turn;      // the item's first ring stage; the stream's next turn
-    // The stream's query rows of an item, once its last scores of the one before are done.
-    auto fetch = [&](int k) {
-      const WorkItem& it = bars->slot[k % kSlots];
-      if (!p.q_boxes || (s ? it.n1 : it.n0) == 0 || it.alt == 2) return;
-      const int tok = g.by_R(it.row0 + (it.alt ? 0 : s * kRows));
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&bars->q_full[s], (uint32_t)tile_bytes);
-        for (int h = 0; h < p.halves; ++h)
-          tma_load_4d(q_smem + s * tile_bytes + h * kHalfBytes, &map_q, &bars->q_full[s], h * 64, 0, it.group, tok);
-      }
-      __syncwarp();
-    };
-    bool fetched = false;
     for (int k = 0; slot_wait(bars, k); ++k) {
-      if (!fetched) fetch(k);
-      fetched = false;
       const WorkItem it = uniform_item(bars, k);
       slot_done(bars, k);
       const int n = s ? it.n1 : it.n0, tiles = item_tiles(it);
       Ring rk = base;                                   // stage of the stream's next keys
       base.advance(2 * tiles, stages);
-      if (n == 0 || it.alt == 2) continue;
+      if (n == 0 || (FEW && it.alt == 2)) continue;
       if (it.alt && s) rk.skip(2, stages);
       // The stream's tiles become ready in its own order on barriers of its own, so that it sees every
       // phase of each.  tk and tv: the turns of its next keys and values.
@@ -821,6 +824,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           if (keys > from) issue_scores<NK>(nk, tS + from, dq, dk0 + rk.s * tile_step + (from * 128 >> 4), id_qk);
           mma_commit(&bars->s_full[s][from / kHalfKeys]);
           if (from) mma_commit(&bars->kv_empty[rk.s]);
+          if (from && n == 1) mma_commit(&bars->q_empty[s]);
         }
         __syncwarp();
       }
@@ -850,17 +854,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
               if (next_keys > from) issue_scores<NK>(nk, tS + from, dq, dk + (from * 128 >> 4), id_qk);
               mma_commit(&bars->s_full[s][h]);
               if (h == 1) mma_commit(&bars->kv_empty[rk.s]);
+              if (h == 1 && left == 2) mma_commit(&bars->q_empty[s]);      // the item's last scores
             } else if (h == 1) {
               mma_commit(&bars->o_full[s]);
             }
           }
           __syncwarp();
-          // the last scores are done (this wait takes no part in the barrier): the next item's rows may come
-          if (h == 0 && !more) {
-            wait_on(&bars->s_full[s][1], p_ph, bars);
-            if (slot_wait(bars, k + 1)) fetch(k + 1);
-            fetched = true;
-          }
         }
         p_ph ^= 1u;
         rv.skip(stride, stages);
@@ -877,31 +876,29 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // ------------------------------------------------------------ ragged value tiles
     // Every tile is waited for and passed on to the streams that use it, so that nobody trails a
     // barrier by a round; for a stream that does not use it this warp empties it.
-    Ring turn[3];
-    Ring r;
+    Ring r, turn[3];
     for (int k = 0; slot_wait(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       slot_done(bars, k);
+      const bool few = FEW && it.alt == 2;
       const int n = item_tiles(it);
 #pragma unroll 1
       for (int u = 0; u < n; ++u) {
         int key0;
-        const int keys = tile_keys(it, g, it.t0 + u, &key0);
-        const bool few = it.alt == 2;
+        const int keys = tile_keys(it, g, it.t0 + u, &key0), to = (keys + 15) & ~15;
         const bool use0 = !few && (it.alt ? !(u & 1) : u < it.n0), use1 = !few && (it.alt ? u & 1 : u < it.n1);
 #pragma unroll 1
         for (int value = 0; value < 2; ++value) {
           wait_on(&bars->kv_full[r.s], r.ph, bars);
-          if (value && (keys & 15)) {
-            // rows keys .. the next multiple of 16: whole 128-byte rows, so the swizzle does not matter
-            const int rows_clear = 16 - (keys & 15);
-            uint8_t* tile = kv_smem + r.s * tile_bytes;
-            const uint32_t step = few ? p.box * 128 : kHalfBytes;
+          if (value && keys < to) {
+            // rows keys .. the next multiple of 16, one half of one row for each lane: whole 128-byte rows,
+            // so the swizzle does not matter
+            const int key = keys + (lane >> 1), h = lane & 1;
+            if (key < to && h < p.halves) {
+              uint4* at = reinterpret_cast<uint4*>(kv_smem + r.s * tile_bytes + (few ? few_row(p, key) : key * 128) +
+                                                   h * (few ? p.box * 128 : kHalfBytes));
 #pragma unroll 1
-            for (int q = lane; q < rows_clear * 8; q += 32) {
-              const int key = keys + (q >> 3);
-              uint8_t* at = tile + (few ? few_row(p, key) : key * 128) + (q & 7) * 16;
-              for (int h = 0; h < p.halves; ++h) *reinterpret_cast<uint4*>(at + h * step) = make_uint4(0, 0, 0, 0);
+              for (int q = 0; q < 8; ++q) at[q] = make_uint4(0, 0, 0, 0);
             }
             fence_async_smem();
           }
@@ -1056,7 +1053,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     for (int k = 0; slot_wait(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       slot_done(bars, k);
-      if (it.alt == 2) continue;
+      if (FEW && it.alt == 2) continue;
       const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
 #pragma unroll 1
       for (int s = 0; s < (it.alt ? 1 : 2); ++s) {
