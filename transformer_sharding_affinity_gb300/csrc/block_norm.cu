@@ -142,12 +142,30 @@ aff_status go(const NormParams& p, cudaStream_t s) {
   return AFF_OK;
 }
 
-// Threads per row: one run of VW elements each up to 1024 threads, then more runs.
+// Few rows: a thread has one run of VW elements, for latency.  Many rows (more than kManyRows, enough to
+// give every SM several): up to four runs each, so that a row takes one or a few warps and more of its
+// bytes are in flight per thread.  One row to a block: 65536 rows of 1024 bf16 take 88 us with a warp to a
+// row and a block, 101 with four rows to a block, 108 with 128 threads to a row.
+constexpr int64_t kManyRows = 152 * 8;
+
 template <typename E, int VW>
 aff_status pick(const NormParams& p, cudaStream_t s) {
   const int runs = (p.D + VW - 1) / VW;
+  if constexpr (VW > 1) {
+    if (p.T > kManyRows && runs > 32) {
+      if (runs <= 64) return go<E, VW, 2, 32, 32>(p, s);
+      if (runs <= 96) return go<E, VW, 3, 32, 32>(p, s);
+      if (runs <= 128) return go<E, VW, 4, 32, 32>(p, s);
+      if (runs <= 192) return go<E, VW, 3, 64, 64>(p, s);
+      if (runs <= 256) return go<E, VW, 4, 64, 64>(p, s);
+      if (runs <= 384) return go<E, VW, 3, 128, 128>(p, s);
+      if (runs <= 512) return go<E, VW, 4, 128, 128>(p, s);
+      if (runs <= 768) return go<E, VW, 3, 256, 256>(p, s);
+      if (runs <= 1024) return go<E, VW, 4, 256, 256>(p, s);
+    }
+  }
   if (runs <= 32) return go<E, VW, 1, 32, 128>(p, s);
-  if (runs <= 64) return go<E, VW, 1, 64, 128>(p, s);
+  if (runs <= 64) return go<E, VW, 1, 64, 64>(p, s);
   if (runs <= 128) return go<E, VW, 1, 128, 128>(p, s);
   if (runs <= 256) return go<E, VW, 1, 256, 256>(p, s);
   if (runs <= 512) return go<E, VW, 1, 512, 512>(p, s);

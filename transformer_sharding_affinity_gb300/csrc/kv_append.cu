@@ -36,148 +36,218 @@ struct AppendParams {
   const float *cos, *sin;
   const void *q_gain, *k_gain;
   int64_t n_pos;
-  float eps;
-  int32_t rot, interleaved, lanes;
+  float eps, inv_d;
+  int32_t rot, interleaved, lanes, lane_bits;
 };
 
+// VW neighbouring elements as they lie in memory.  bf16 pairs stay whole 32-bit words: taken apart by a shift
+// and a mask, put together by one conversion.
 template <typename E, int VW>
 struct alignas(sizeof(E) * VW) Vec {
   E e[VW];
+  __device__ __forceinline__ void get(float (&f)[VW]) const {
+#pragma unroll
+    for (int i = 0; i < VW; ++i) f[i] = (float)e[i];
+  }
+  __device__ __forceinline__ void put(const float (&f)[VW]) {
+#pragma unroll
+    for (int i = 0; i < VW; ++i) e[i] = (E)f[i];
+  }
 };
+template <int VW>
+struct alignas(2 * VW) PairVec {
+  uint32_t w[VW / 2];
+  __device__ __forceinline__ void get(float (&f)[VW]) const {
+#pragma unroll
+    for (int i = 0; i < VW / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[VW]) {
+#pragma unroll
+    for (int i = 0; i < VW / 2; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+  }
+};
+template <>
+struct alignas(4) Vec<__nv_bfloat16, 2> : PairVec<2> {};
+template <>
+struct alignas(8) Vec<__nv_bfloat16, 4> : PairVec<4> {};
+template <>
+struct alignas(16) Vec<__nv_bfloat16, 8> : PairVec<8> {};
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
-__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+// Units a lane can hold (d <= 256 in 32 lanes of 2 VW elements) and rows of a thread.
+__host__ __device__ constexpr int units_of(int vw) { return vw >= 4 ? 1 : 4 / vw; }
+// (65536 tokens of 32 bf16 rows: 248 us with one row a thread, 196 with two, 226 with four; 22681 x 28 fp32
+// rows: 35.6, 34.2, 32.3.)
+__host__ __device__ constexpr int rows_of(int vw) { return vw == 8 ? 2 : vw == 4 ? 4 : 1; }
 
-// One row.  Unit u of the row is two runs of VW elements: below rot / 2 units'
-// worth they are the two halves of VW pairs (or, interleaved, two neighbouring
-// runs whose pairs lie side by side); past rot they are plain neighbours.
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float z = x * c - y * s;
+  y = x * s + y * c;
+  x = z;
+}
+
+// A run of a row that nothing else reads.
+template <typename E, int VW>
+__device__ __forceinline__ Vec<E, VW> load_once(const Vec<E, VW>* at) {
+  if constexpr (sizeof(Vec<E, VW>) == 16) {
+    union {
+      uint4 w;
+      Vec<E, VW> v;
+    } x;
+    x.w = __ldcs(reinterpret_cast<const uint4*>(at));
+    return x.v;
+  } else {
+    return *at;
+  }
+}
+
+// VW neighbouring floats, aligned to VW (up to 4).
+template <int VW>
+__device__ __forceinline__ void load_row(const float* at, float (&v)[VW]) {
+  if constexpr (VW >= 4) {
+#pragma unroll
+    for (int e = 0; e < VW; e += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(at + e));
+      v[e] = w.x; v[e + 1] = w.y; v[e + 2] = w.z; v[e + 3] = w.w;
+    }
+  } else if constexpr (VW == 2) {
+    const float2 w = __ldg(reinterpret_cast<const float2*>(at));
+    v[0] = w.x; v[1] = w.y;
+  } else {
+    v[0] = __ldg(at);
+  }
+}
+
+// A block is (a part of) one token.  A row is dealt to `lanes` threads, a thread has kPer rows, `slots`
+// apart: their loads are all in flight at once, and the token's cosines and sines are read once for them.
+// Unit u of a row is two runs of VW elements: of the rotated part the two halves of VW pairs (or,
+// interleaved, two neighbouring runs whose pairs lie side by side), past it and in value rows neighbours.
 template <typename E, int VW>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kUnits = VW >= 4 ? 1 : 4 / VW;   // units a lane can hold: d <= 256 in 32 lanes of 2 VW elements
+  constexpr int kUnits = units_of(VW), kPer = rows_of(VW);
   pdl_enter();
   const StepGeom& g = p.g;
-  const int rows = g.H + 2 * g.G;
-  const int64_t at = (int64_t)blockIdx.x * (kThreads / p.lanes) + threadIdx.x / p.lanes;
-  const int lane = threadIdx.x & (p.lanes - 1);
-  const bool live = at < (int64_t)g.T * rows && plan_matches(g);
-  if (at < (int64_t)g.T * rows && !live && threadIdx.x == 0) latch_status(&g.head->status, 1);
-  const int t = live ? (int)(at / rows) : 0;
-  const int r = live ? (int)(at - (int64_t)t * rows) : 0;
-  TokenInfo ti{-1, -1, -1};
-  if (live) ti = g.tok[t];
-  const bool is_q = r < g.H, is_k = !is_q && r < g.H + g.G;
-  const int64_t pos = (int64_t)g.prefix_len + ti.own;
-  bool stand = live && ti.own >= 0;              // the token is no padding
-  if (stand && (is_q || is_k) && pos >= p.n_pos) {
-    stand = false;
-    if (lane == 0) latch_status(&g.head->status, kStatusRange);
-  }
-  const E* src;
-  E* dst = nullptr;
-  if (is_q) {
-    src = static_cast<const E*>(p.q) + (int64_t)t * p.q_stride + (int64_t)r * g.d;
-    dst = static_cast<E*>(p.q_out) + (int64_t)t * p.q_out_stride + (int64_t)r * g.d;
-  } else {
-    const int grp = is_k ? r - g.H : r - g.H - g.G;
-    src = is_k ? static_cast<const E*>(p.k) + (int64_t)t * p.k_stride + (int64_t)grp * g.d
-               : static_cast<const E*>(p.v) + (int64_t)t * p.v_stride + (int64_t)grp * g.d;
-    if (stand) {
-      const int64_t page = ti.slot / g.page_size, off = ti.slot - page * g.page_size;
-      dst = static_cast<E*>(is_k ? p.kc : p.vc) + page * p.page_stride + grp * p.group_stride + off * p.token_stride;
-    }
-  }
-  const int half = p.rot / 2;
-  const int rot_units = (is_q || is_k) ? half / VW : 0;   // VW divides rot / 2 and d - rot (host)
-  const int rot_end = (is_q || is_k) ? p.rot : 0;
+  const int t = blockIdx.x, lane = threadIdx.x & (p.lanes - 1);
+  const int slots = blockDim.x >> p.lane_bits;
+  const int r0 = blockIdx.y * slots * kPer + (threadIdx.x >> p.lane_bits);
+  const int half = p.rot / 2, rot_units = half / VW, n_rot = g.H + g.G, rows = n_rot + g.G;
   using V = Vec<E, VW>;
-  float a[kUnits][VW], b[kUnits][VW];
-  int ja[kUnits], jb[kUnits];
-  float ss = 0.f;
+  // the rows first: they do not depend on where their token stands
+  V va[kPer][kUnits], vb[kPer][kUnits];
+  auto first_run = [&](int u, bool turned) {
+    if (!turned) return 2 * u * VW;
+    return u >= rot_units ? p.rot + 2 * (u - rot_units) * VW : p.interleaved ? 2 * u * VW : u * VW;
+  };
+  auto second_run = [&](int u, int j, bool turned) {
+    return turned && u < rot_units && !p.interleaved ? j + half : j + VW;      // VW divides rot / 2 and d - rot (host)
+  };
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int u = lane + i * p.lanes;
-    if (u < rot_units) {
-      ja[i] = p.interleaved ? 2 * u * VW : u * VW;
-      jb[i] = p.interleaved ? ja[i] + VW : ja[i] + half;
-    } else {
-      ja[i] = rot_end + 2 * (u - rot_units) * VW;
-      jb[i] = ja[i] + VW;
-    }
-    const bool ha = stand && ja[i] < g.d, hb = stand && jb[i] < g.d;
-    V va{}, vb{};
-    if (ha) va = *reinterpret_cast<const V*>(src + ja[i]);
-    if (hb) vb = *reinterpret_cast<const V*>(src + jb[i]);
+  for (int k = 0; k < kPer; ++k) {
+    const int r = r0 + k * slots;
+    const E* src = r < g.H   ? static_cast<const E*>(p.q) + (int64_t)t * p.q_stride + r * g.d
+                   : r < n_rot ? static_cast<const E*>(p.k) + (int64_t)t * p.k_stride + (r - g.H) * g.d
+                               : static_cast<const E*>(p.v) + (int64_t)t * p.v_stride + (r - n_rot) * g.d;
 #pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      a[i][e] = ha ? to_f(va.e[e]) : 0.f;
-      b[i][e] = hb ? to_f(vb.e[e]) : 0.f;
-      ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = lane + i * p.lanes, ja = first_run(u, r < n_rot), jb = second_run(u, ja, r < n_rot);
+      va[k][i] = V{};
+      vb[k][i] = V{};
+      if (r < rows && ja < g.d) va[k][i] = load_once(reinterpret_cast<const V*>(src + ja));
+      if (r < rows && jb < g.d) vb[k][i] = load_once(reinterpret_cast<const V*>(src + jb));
     }
   }
-  const E* gain = static_cast<const E*>(is_q ? p.q_gain : is_k ? p.k_gain : nullptr);
-  // every lane of the warp takes part in the sum
-  for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float inv = gain ? rsqrtf(ss / (float)g.d + p.eps) : 1.f;
-  if (!live) return;
-  if (!stand && !is_q) return;                   // padding is not stored; its query row is zero
+  const TokenInfo ti = g.tok[t];
+  const bool fits = plan_matches(g);
+  if (!fits) {
+    if (threadIdx.x == 0) latch_status(&g.head->status, 1);
+    return;
+  }
+  const int64_t pos = (int64_t)g.prefix_len + ti.own;
+  bool stand = ti.own >= 0;                      // the token is no padding
+  if (stand && pos >= p.n_pos) {
+    stand = false;
+    if (threadIdx.x == 0) latch_status(&g.head->status, kStatusRange);
+  }
+  float c[kUnits][VW], s[kUnits][VW];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = lane + i * p.lanes;
-    if (ja[i] >= g.d) continue;
-    const bool hb = jb[i] < g.d;
-    if (gain && stand) {
-      const V ga = *reinterpret_cast<const V*>(gain + ja[i]);
-      V gb{};
-      if (hb) gb = *reinterpret_cast<const V*>(gain + jb[i]);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        a[i][e] *= inv * to_f(ga.e[e]);
-        if (hb) b[i][e] *= inv * to_f(gb.e[e]);
-      }
+    if (stand && u < rot_units) {
+      load_row<VW>(p.cos + pos * half + u * VW, c[i]);
+      load_row<VW>(p.sin + pos * half + u * VW, s[i]);
     }
-    if (u < rot_units && stand) {
-      const float* cs = p.cos + pos * half + (p.interleaved ? u * VW : ja[i]);
-      const float* sn = p.sin + pos * half + (p.interleaved ? u * VW : ja[i]);
-      float c[VW], s[VW];
+  }
+  const int64_t at = (ti.slot >> 32) * p.page_stride + (ti.slot & 0xffffffff) * p.token_stride;
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        c[e] = cs[e];
-        s[e] = sn[e];
-      }
-      if (!p.interleaved) {
+  for (int k = 0; k < kPer; ++k) {
+    const int r = r0 + k * slots;
+    const bool is_q = r < g.H, turned = r < n_rot;
+    float a[kUnits][VW], b[kUnits][VW], inv = 1.f;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const float x = a[i][e], y = b[i][e];
-          a[i][e] = x * c[e] - y * s[e];
-          b[i][e] = x * s[e] + y * c[e];
+    for (int i = 0; i < kUnits; ++i) {
+      va[k][i].get(a[i]);
+      vb[k][i].get(b[i]);
+    }
+    const E* gain = static_cast<const E*>(is_q ? p.q_gain : p.k_gain);
+    if (p.q_gain || p.k_gain) {
+      // every lane of the warp takes part in the sum
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+      for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      inv = rsqrtf(ss * p.inv_d + p.eps);
+    }
+    if (r >= rows || (!stand && !is_q)) continue;      // padding is not stored; its query row is zero
+    E* dst = is_q ? static_cast<E*>(p.q_out) + (int64_t)t * p.q_out_stride + r * g.d
+                  : static_cast<E*>(turned ? p.kc : p.vc) + at + (turned ? r - g.H : r - n_rot) * p.group_stride;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = lane + i * p.lanes, ja = first_run(u, turned), jb = second_run(u, ja, turned);
+      if (ja >= g.d) continue;
+      const bool hb = jb < g.d;
+      V wa = va[k][i], wb = vb[k][i];
+      if (!stand) {
+        wa = wb = V{};
+      } else if (turned) {
+        if (gain) {
+          const V ga = *reinterpret_cast<const V*>(gain + ja);
+          V gb{};
+          if (hb) gb = *reinterpret_cast<const V*>(gain + jb);
+          float fa[VW], fb[VW];
+          ga.get(fa);
+          gb.get(fb);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            a[i][e] *= inv * fa[e];
+            b[i][e] *= inv * fb[e];
+          }
         }
-      } else if constexpr (VW > 1) {
-        // pairs (2e, 2e + 1) of the 2 VW neighbours: the first VW / 2 in a, the others in b
+        if (u < rot_units) {
+          if (!p.interleaved) {
 #pragma unroll
-        for (int e = 0; e < VW / 2; ++e) {
-          float x = a[i][2 * e], y = a[i][2 * e + 1];
-          a[i][2 * e] = x * c[e] - y * s[e];
-          a[i][2 * e + 1] = x * s[e] + y * c[e];
-          x = b[i][2 * e], y = b[i][2 * e + 1];
-          b[i][2 * e] = x * c[e + VW / 2] - y * s[e + VW / 2];
-          b[i][2 * e + 1] = x * s[e + VW / 2] + y * c[e + VW / 2];
+            for (int e = 0; e < VW; ++e) turn(a[i][e], b[i][e], c[i][e], s[i][e]);
+          } else if constexpr (VW > 1) {
+            // pairs (2e, 2e + 1) of the 2 VW neighbours: the first VW / 2 in a, the others in b
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) {
+              turn(a[i][2 * e], a[i][2 * e + 1], c[i][e], s[i][e]);
+              turn(b[i][2 * e], b[i][2 * e + 1], c[i][e + VW / 2], s[i][e + VW / 2]);
+            }
+          } else {
+            turn(a[i][0], b[i][0], c[i][0], s[i][0]);
+          }
         }
-      } else {
-        const float x = a[i][0], y = b[i][0];
-        a[i][0] = x * c[0] - y * s[0];
-        b[i][0] = x * s[0] + y * c[0];
+        wa.put(a[i]);
+        wb.put(b[i]);
       }
+      *reinterpret_cast<V*>(dst + ja) = wa;
+      if (hb) *reinterpret_cast<V*>(dst + jb) = wb;
     }
-    V va, vb;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      from_f(a[i][e], va.e[e]);
-      from_f(b[i][e], vb.e[e]);
-    }
-    *reinterpret_cast<V*>(dst + ja[i]) = va;
-    if (hb) *reinterpret_cast<V*>(dst + jb[i]) = vb;
   }
 }
 
@@ -185,10 +255,16 @@ template <typename E, int VW>
 aff_status launch(AppendParams& p, cudaStream_t s) {
   const int units = (p.g.d + 2 * VW - 1) / (2 * VW);   // the rotated part is whole units, the plain part may end in half a one
   p.lanes = 1;
-  while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
-  const int64_t rows = (int64_t)p.g.T * (p.g.H + 2 * p.g.G);
-  const int64_t per = kThreads / p.lanes;
-  AFF_CUDA(launch_pdl(kv_append_kernel<E, VW>, (unsigned)((rows + per - 1) / per), kThreads, 0, s, p));
+  p.lane_bits = 0;
+  while (p.lanes < units && p.lanes < 32) {
+    p.lanes *= 2;
+    ++p.lane_bits;
+  }
+  p.inv_d = 1.f / (float)p.g.d;
+  const int need = (p.g.H + 2 * p.g.G + rows_of(VW) - 1) / rows_of(VW) * p.lanes;
+  const int threads = need < kThreads ? (need + 31) / 32 * 32 : kThreads;
+  AFF_CUDA(launch_pdl(kv_append_kernel<E, VW>, dim3((unsigned)p.g.T, (unsigned)((need + threads - 1) / threads)), threads, 0,
+                      s, p));
   return AFF_OK;
 }
 

@@ -36,7 +36,6 @@ namespace aff {
 constexpr int kKeyTile = 128;            // most keys of a tile
 constexpr int kFewRows = 16;             // most rows of an item that takes the few-rows path
 constexpr int kPlanSms = 152;            // SMs of a GB300: sizes the plan without a device
-constexpr uint32_t kPlanMagic = 0x41465331u;
 
 // Division of 0 <= x < 2^31 by a number known on the host: a multiply, an add and a shift, where the
 // device's own division by a variable is some forty instructions at every place it is used.
@@ -57,7 +56,7 @@ struct FastDiv {
 };
 
 struct TokenInfo {       // one per token of the step; 16 bytes
-  int64_t slot;          // page * page_size + offset of its own key, -1: padding
+  int64_t slot;          // page << 32 | offset in it, of its own key; -1: padding
   int32_t own;           // index among its sequence's own tokens, -1: padding
   int32_t seq;           // its sequence, -1: none
 };
@@ -80,12 +79,12 @@ struct WorkItem {        // 48 bytes
 
 struct PlanHeader {      // at the start of the plan buffer; its first word is the status word
   uint32_t status;
-  uint32_t magic;
   int32_t n_items;       // -1: the step was malformed
   int32_t unit;          // most cost (key tiles x streams) of an item; 0: jobs are not cut
   int32_t prefix_parts;  // separate: parts of each prefix job
   int32_t prefix_per;    // separate: key tiles of each part
-  int32_t key[10];       // the geometry it was made for
+  int32_t pad[3];
+  uint32_t key[4];       // a hash of the geometry it was made for
   uint32_t claimed;      // items claimed beyond the first of every CTA, and CTAs done, in the call
   uint32_t done;         // under way; the last CTA sets both back to 0
 };
@@ -106,6 +105,7 @@ struct StepGeom {
   int32_t prefix_rows;   // row tile of the prefix's jobs
   int32_t prefix_tiles;  // row tiles of the prefix's jobs
   int32_t max_items, max_part_rows;
+  uint32_t key[4];       // of everything the plan depends on but the arrays' contents
   FastDiv by_R, by_page, by_tile, by_page_tiles;
   int64_t n_pages;
   const int32_t *q_start, *kv_len, *pages, *prefix_pages;
@@ -191,9 +191,7 @@ __device__ __forceinline__ int job_parts(int tiles, int streams, int unit, int* 
 
 __device__ __forceinline__ bool plan_matches(const StepGeom& g) {
   const PlanHeader& h = *g.head;
-  return h.magic == kPlanMagic && h.key[0] == g.T && h.key[1] == g.B && h.key[2] == g.H && h.key[3] == g.G &&
-         h.key[4] == g.d && h.key[5] == g.page_size && h.key[6] == g.pages_stride && h.key[7] == g.prefix_len &&
-         h.key[8] == g.dtype && h.key[9] == (int)min(g.n_pages, (int64_t)INT32_MAX);
+  return h.key[0] == g.key[0] && h.key[1] == g.key[1] && h.key[2] == g.key[2] && h.key[3] == g.key[3];
 }
 #endif
 

@@ -245,11 +245,7 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const __grid_consta
   pdl_enter();
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) {
-      PlanHeader& h = *g.head;
-      const int key[10] = {g.T, g.B, g.H, g.G, g.d, g.page_size, g.pages_stride, g.prefix_len, g.dtype,
-                           (int)min(g.n_pages, (int64_t)INT32_MAX)};
-      for (int i = 0; i < 10; ++i) h.key[i] = key[i];
-      h.magic = kPlanMagic;
+      for (int i = 0; i < 4; ++i) g.head->key[i] = g.key[i];
     }
     plan_items(g);
     return;
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const __grid_consta
       const int page = g.pages[(int64_t)lo * g.pages_stride + own / g.page_size];
       if (page >= 0 && page < g.n_pages) {
         ti.own = (int)own;
-        ti.slot = (int64_t)page * g.page_size + own % g.page_size;
+        ti.slot = (int64_t)page << 32 | own % g.page_size;
       } else {
         latch_status(&g.head->status, kStatusRange);
       }
@@ -335,6 +331,15 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   g.by_tile.set((uint32_t)g.key_tile);
   g.by_page_tiles.set((uint32_t)std::max(g.page_tiles, 1));
   g.np = segment_tiles(g, g.prefix_len);
+  const int64_t all[10] = {g.T, g.B, g.H, g.G, g.d, g.page_size, g.pages_stride, g.prefix_len, g.dtype, g.n_pages};
+  for (int i = 0; i < 4; ++i) {
+    uint64_t h = 0x9e3779b97f4a7c15ull * (i + 1);
+    for (int64_t v : all) {
+      h = (h ^ (uint64_t)v) * 0xbf58476d1ce4e5b9ull;
+      h ^= h >> 29;
+    }
+    g.key[i] = (uint32_t)(h >> 16);
+  }
   const bool bf = c->dtype == AFF_BF16;
   g.small = bf ? 128 : 16;
   g.big = bf ? 256 : 64;
