@@ -431,99 +431,106 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
 #pragma unroll
       for (int n = 0; n < kSlices; ++n) o[t][n][e] = o[t][n][2 + e] = 0.f;
     }
-  Ring r;
-  r.s = first % p.stages;
+  const int stages = NK > 0 ? ring_stages(NK > 4 ? 2 : 1) : p.stages;
+  Ring rk, tk = turn;
+  rk.s = first % stages;
+  Ring rv = rk, tv = turn;
+  rv.skip(1, stages);
+  tv.skip(1, stages);
+  turn.advance(2 * it.n0, stages);
   // ldmatrix: lane 8 i + j gives row j of matrix i.  A operand of S^T: (keys 0-7, 8-15) x (columns 0-7 | 8-15);
   // of O^T, transposed: (columns 0-7, 8-15) x (keys 0-7 | 8-15).
   const int kj = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), kc = lane >> 4;
   const int vj = warp * 16 + (lane >> 4) * 8 + (lane & 7), vc = (lane >> 3) & 1;
   const uint32_t half_step = p.box * 128;
   const uint32_t k_at = smem_u32(kv_smem) + few_row(p, kj), v_at = smem_u32(kv_smem) + few_row(p, vj);
+  // S^T of the stream's next tile (garbage past the tile's keys: masked afterwards)
+  float sc[RN][4];
+  auto scores = [&]() {
+    wait_on(&bars->kv_ready[2][tk.s], tk.ph, bars);
+    tk.skip(2, stages);
+    float s2[RN][4];                // two chains of products
+#pragma unroll
+    for (int t = 0; t < RN; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[t][e] = s2[t][e] = 0.f;
+#pragma unroll
+    for (int k0 = 0; k0 < kSlices; k0 += 4) {      // four loads ahead of their products
+      uint32_t a[4][4];
+#pragma unroll
+      for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
+        if (k < nk)
+          ldmatrix4(k_at + rk.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k - k0]);
+#pragma unroll
+      for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
+#pragma unroll
+        for (int t = 0; t < RN; ++t)
+          if (k < nk) mma_16x8x16((k & 1) ? s2[t] : sc[t], a[k - k0], q[t][k][0], q[t][k][1]);
+    }
+#pragma unroll
+    for (int t = 0; t < RN; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[t][e] += s2[t][e];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->kv_empty[rk.s]);
+    rk.skip(2, stages);
+  };
+  if (it.n0 > 0) scores();
 #pragma unroll 1
   for (int u = 0; u < it.n0; ++u) {
     const int ti = it.t0 + u;
     int key0;
     const int keys = tile_keys(it, g, ti, &key0);
     const bool mine = warp * 16 < keys;
-    float sc[RN][4];
-    wait_on(&bars->kv_ready[2][turn.s], turn.ph, bars);
-    turn.skip(1, p.stages);
-    if (mine) {
-      float s2[RN][4];                // two chains of products
-#pragma unroll
-      for (int t = 0; t < RN; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[t][e] = s2[t][e] = 0.f;
-#pragma unroll
-      for (int k0 = 0; k0 < kSlices; k0 += 4) {      // four loads ahead of their products
-        uint32_t a[4][4];
-#pragma unroll
-        for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
-          if (k < nk)
-            ldmatrix4(k_at + r.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k - k0]);
-#pragma unroll
-        for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
-#pragma unroll
-          for (int t = 0; t < RN; ++t)
-            if (k < nk) mma_16x8x16((k & 1) ? s2[t] : sc[t], a[k - k0], q[t][k][0], q[t][k][1]);
-      }
-#pragma unroll
-      for (int t = 0; t < RN; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[t][e] += s2[t][e];
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
-    r.skip(1, p.stages);
     uint32_t pb[RN][2];
-    if (mine) {
-      // sc[t][e]: key quad, row col2 + e; sc[t][2 + e]: key quad + 8
-      bool grow = false;
+    // sc[t][e]: key quad, row col2 + e; sc[t][2 + e]: key quad + 8
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < RN; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int vis = ti < it.np ? keys : min(keys, own_vis[t][e] - key0);
+        if (own_vis[t][e] <= 0) vis = 0;
+        if (warp * 16 + quad >= vis) sc[t][e] = -INFINITY;
+        if (warp * 16 + quad + 8 >= vis) sc[t][2 + e] = -INFINITY;
+        grow |= (fmaxf(sc[t][e], sc[t][2 + e]) - m[t][e]) * p.scale_log2 > kRescale;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int t = 0; t < RN; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          int vis = ti < it.np ? keys : min(keys, own_vis[t][e] - key0);
-          if (own_vis[t][e] <= 0) vis = 0;
-          if (warp * 16 + quad >= vis) sc[t][e] = -INFINITY;
-          if (warp * 16 + quad + 8 >= vis) sc[t][2 + e] = -INFINITY;
-          grow |= (fmaxf(sc[t][e], sc[t][2 + e]) - m[t][e]) * p.scale_log2 > kRescale;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
+          float mx = fmaxf(sc[t][e], sc[t][2 + e]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float f = mx > m[t][e] ? ex2((m[t][e] - mx) * p.scale_log2) : 1.f;
+          m[t][e] = fmaxf(m[t][e], mx);
+          l[t][e] *= f;
 #pragma unroll
-        for (int t = 0; t < RN; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[t][e], sc[t][2 + e]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float f = mx > m[t][e] ? ex2((m[t][e] - mx) * p.scale_log2) : 1.f;
-            m[t][e] = fmaxf(m[t][e], mx);
-            l[t][e] *= f;
-#pragma unroll
-            for (int n = 0; n < kSlices; ++n) {
-              o[t][n][e] *= f;
-              o[t][n][2 + e] *= f;
-            }
+          for (int n = 0; n < kSlices; ++n) {
+            o[t][n][e] *= f;
+            o[t][n][2 + e] *= f;
           }
-      }
-#pragma unroll
-      for (int t = 0; t < RN; ++t) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float neg = m[t][e] == -INFINITY ? 0.f : -m[t][e] * p.scale_log2;
-          x[e] = ex2(fmaf(sc[t][e], p.scale_log2, neg));
-          x[2 + e] = ex2(fmaf(sc[t][2 + e], p.scale_log2, neg));
-          l[t][e] += x[e] + x[2 + e];
         }
-        pb[t][0] = transpose8(bf16x2(x[0], x[1]));      // keys x rows -> rows x keys, the B operand of O^T
-        pb[t][1] = transpose8(bf16x2(x[2], x[3]));
-      }
     }
-    wait_on(&bars->kv_ready[2][turn.s], turn.ph, bars);
-    turn.skip(1, p.stages);
+#pragma unroll
+    for (int t = 0; t < RN; ++t) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float neg = m[t][e] == -INFINITY ? 0.f : -m[t][e] * p.scale_log2;
+        x[e] = ex2(fmaf(sc[t][e], p.scale_log2, neg));
+        x[2 + e] = ex2(fmaf(sc[t][2 + e], p.scale_log2, neg));
+        l[t][e] += x[e] + x[2 + e];
+      }
+      pb[t][0] = transpose8(bf16x2(x[0], x[1]));      // keys x rows -> rows x keys, the B operand of O^T
+      pb[t][1] = transpose8(bf16x2(x[2], x[3]));
+    }
+    // the next tile's scores beside this one's values: two independent chains of loads and products
+    if (u + 1 < it.n0) scores();
+    wait_on(&bars->kv_ready[2][tv.s], tv.ph, bars);
+    tv.skip(2, stages);
     if (mine) {
 #pragma unroll
       for (int n0 = 0; n0 < kSlices; n0 += 4) {
@@ -531,7 +538,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
 #pragma unroll
         for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
           if (n < nk)
-            ldmatrix4_t(v_at + r.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n - n0]);
+            ldmatrix4_t(v_at + rv.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n - n0]);
 #pragma unroll
         for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
 #pragma unroll
@@ -540,8 +547,8 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->kv_empty[r.s]);
-    r.skip(1, p.stages);
+    if (lane == 0) mbar_arrive(&bars->kv_empty[rv.s]);
+    rv.skip(2, stages);
   }
   auto all_warps = [&]() {
     __syncwarp();
@@ -1443,12 +1450,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   const int n = n_pre + n_own;
   auto row_of = [&](int i) { return i < n_pre ? pre0 + i * pre_step : own0 + (i - n_pre) * own_step; };
   float mx = -INFINITY;
-  bool nan = false;
-  for (int i = lane; i < n; i += 32) {
-    const float x = g.part_lse[row_of(i)];
-    nan |= x != x;
-    mx = fmaxf(mx, x);
-  }
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, g.part_lse[row_of(i)]);
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
@@ -1456,16 +1458,24 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   for (int i0 = 0; i0 < n; i0 += 32) {
     const float w_mine = i0 + lane < n ? expf(g.part_lse[row_of(i0 + lane)] - ref) : 0.f;
     const int upto = min(32, n - i0);
-    for (int i = 0; i < upto; ++i) {
-      const float w = __shfl_sync(0xffffffffu, w_mine, i);
-      if (w == 0.f) continue;                  // an empty part's row
-      sum += w;
-      if (4 * lane < g.d) {
-        const float4 v = *reinterpret_cast<const float4*>(g.part_out + (int64_t)row_of(i0 + i) * g.d + 4 * lane);
-        acc.x += w * v.x;
-        acc.y += w * v.y;
-        acc.z += w * v.z;
-        acc.w += w * v.w;
+    for (int i = 0; i < upto; i += 4) {          // four parts' loads in flight; an empty part's row is not used
+      float w[4];
+      float4 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        w[x] = i + x < upto ? __shfl_sync(0xffffffffu, w_mine, (i + x) & 31) : 0.f;
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[x] != 0.f && 4 * lane < g.d)
+          v[x] = *reinterpret_cast<const float4*>(g.part_out + (int64_t)row_of(i0 + i + x) * g.d + 4 * lane);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (w[x] == 0.f) continue;
+        sum += w[x];
+        acc.x += w[x] * v[x].x;
+        acc.y += w[x] * v[x].y;
+        acc.z += w[x] * v[x].z;
+        acc.w += w[x] * v[x].w;
       }
     }
   }
