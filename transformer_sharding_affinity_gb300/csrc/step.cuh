@@ -106,7 +106,7 @@ struct StepGeom {
   int32_t prefix_tiles;  // row tiles of the prefix's jobs
   int32_t max_items, max_part_rows;
   uint32_t key[4];       // of everything the plan depends on but the arrays' contents
-  FastDiv by_R, by_page, by_tile, by_page_tiles;
+  FastDiv by_R, by_G, by_page, by_tile, by_page_tiles;
   int64_t n_pages;
   const int32_t *q_start, *kv_len, *pages, *prefix_pages;
   // plan buffer
@@ -159,14 +159,6 @@ __device__ __forceinline__ SeqShape seq_shape(const StepGeom& g, int q0, int q1,
   s.tr = s.rows <= g.small ? g.small : g.big;
   s.nt = (s.rows + s.tr - 1) / s.tr;
   return s;
-}
-
-// As the step's arrays give it (planning only: later kernels go by the plan).
-__device__ __forceinline__ SeqShape seq_shape(const StepGeom& g, int b) {
-  const int q0 = min(max(g.q_start[b], 0), g.T);
-  const int q1 = min(max(g.q_start[b + 1], q0), g.T);
-  const int64_t room = (int64_t)g.pages_stride * g.page_size;
-  return seq_shape(g, q0, q1, (int)min((int64_t)max(g.kv_len[b], 0), room));
 }
 
 // Own keys that the last of the first `upto` rows of a sequence sees.

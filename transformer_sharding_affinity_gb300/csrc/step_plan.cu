@@ -15,8 +15,9 @@ namespace aff {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kItemsPerSm = 4;    // items that a cut aims at for each SM
-constexpr int kMinUnit = 4;       // least cost of an item when jobs are cut
+constexpr int kItemsPerSm = 4;    // items that a cut of unequal jobs aims at for each SM
+constexpr int kMinUnit = 4;       // least cost of an item then
+constexpr int kMaxParts = 64;     // most parts that equal jobs are cut into
 
 __device__ int64_t warp_sum(int64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -41,6 +42,31 @@ __device__ int warp_inclusive(int v) {
   return v;
 }
 
+// Sum over the threads before this one; *total over the block.
+__device__ int block_exclusive(int v, int* total, int* sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int incl = warp_inclusive(v);
+  __syncthreads();
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  const int warps = warp_inclusive(sh[lane]);
+  *total = __shfl_sync(0xffffffffu, warps, 31);
+  return __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, sh[lane], warp) + incl - v;
+}
+
+// Parts (1 .. most) of each of `jobs` equal jobs of `cost`: the least of the time of the fullest SM, where an
+// item takes its cost and `start` for its beginning and end, and of a part's trip through memory.  Warp-wide.
+__device__ int best_parts(int64_t jobs, int64_t cost, int most, int start) {
+  int64_t best = INT64_MAX;
+  for (int parts = 1 + (threadIdx.x & 31); parts <= kMaxParts; parts += 32) {
+    if (parts > most || parts > cost) continue;
+    const int64_t rounds = (jobs * parts + kPlanSms - 1) / kPlanSms;
+    best = min(best, (rounds * ((cost + parts - 1) / parts + start) + parts) << 8 | parts);
+  }
+  for (int o = 16; o > 0; o >>= 1) best = min(best, (int64_t)__shfl_xor_sync(0xffffffffu, best, o));
+  return best == INT64_MAX ? 1 : (int)(best & 255);
+}
+
 // A sequence's (row tile, group) pairs, late row tiles first: they have the most keys.
 struct Job {
   int k, group, tiles, parts, per, streams;
@@ -48,8 +74,9 @@ struct Job {
 
 __device__ __forceinline__ Job job_of(const StepGeom& g, const SeqShape& s, int i, int unit) {
   Job j;
-  j.k = s.nt - 1 - i / g.G;
-  j.group = i % g.G;
+  const int q = g.by_G(i);
+  j.k = s.nt - 1 - q;
+  j.group = i - q * g.G;
   j.streams = s.tr > 128 ? 2 : 1;
   j.tiles = key_tiles(g, s, (j.k + 1) * s.tr);
   j.parts = job_parts(j.tiles, j.streams, unit, &j.per);
@@ -57,48 +84,98 @@ __device__ __forceinline__ Job job_of(const StepGeom& g, const SeqShape& s, int 
   return j;
 }
 
+// One block.  Sequences are taken kThreads at a time, one to a thread, their numbers kept in shared memory
+// (reloaded only when there are more of them); their jobs are then cut by a warp each.
 __device__ void plan_items(const StepGeom& g) {
   __shared__ int64_t wide_sh[32];
   __shared__ int sh[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- the batch as given: starts in order, from 0, within the step
-  int bad = 0;
-  for (int b = threadIdx.x; b < g.B; b += kThreads) {
+  __shared__ int s_q0[kThreads], s_q1[kThreads], s_kv[kThreads], s_item[kThreads], s_row[kThreads], s_most[kThreads];
+  __shared__ int s_min, s_max, s_parts[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x;
+  if (me == 0) {
+    s_min = INT32_MAX;
+    s_max = 0;
+  }
+  auto load = [&](int b) {       // sequence b as given; false if it is malformed
+    s_q0[me] = s_q1[me] = s_kv[me] = 0;
+    if (b >= g.B) return true;
     const int q0 = g.q_start[b], q1 = g.q_start[b + 1], kv = g.kv_len[b];
-    if ((b == 0 && q0 != 0) || q1 < q0 || q1 > g.T || kv < 0 || kv > (int64_t)g.pages_stride * g.page_size) bad = 1;
+    const bool good = !(b == 0 && q0 != 0) && q1 >= q0 && q0 >= 0 && q1 <= g.T && kv >= 0 &&
+                      kv <= (int64_t)g.pages_stride * g.page_size;
+    if (good) {
+      s_q0[me] = q0;
+      s_q1[me] = q1;
+      s_kv[me] = kv;
+    }
+    return good;
+  };
+  auto shape = [&](int i) { return seq_shape(g, s_q0[i], s_q1[i], s_kv[i]); };
+  const bool one_load = g.B <= kThreads;
+
+  // ---- check the batch; the cost of all own jobs of one group, in key tiles x streams, and their extremes
+  int64_t cost = 0, jobs = 0, bad = 0;
+  int least = INT32_MAX, most_cost = 0;
+  for (int b0 = 0; b0 < g.B; b0 += kThreads) {
+    if (!load(b0 + me)) bad = 1;
+    if (!g.may_split) continue;
+    const SeqShape s = shape(me);
+    for (int k = 0; k < s.nt; ++k) {
+      const int c = key_tiles(g, s, (k + 1) * s.tr) * (s.tr > 128 ? 2 : 1);
+      if (c == 0) continue;
+      cost += c;
+      ++jobs;
+      least = min(least, c);
+      most_cost = max(most_cost, c);
+    }
   }
   if (block_sum(bad, wide_sh)) {
-    if (threadIdx.x == 0) {
+    if (me == 0) {
       g.head->n_items = -1;
       latch_status(&g.head->status, kStatusRange);
     }
     return;
   }
 
-  // ---- the cost of all jobs, in key tiles x streams, and from it the most cost of an item
+  // ---- how jobs are cut
   const int prefix_streams = g.prefix_rows > 128 ? 2 : 1;
-  int unit = 0;
+  int unit = 0, prefix_parts = 0, prefix_per = 0;
   if (g.may_split) {
-    int64_t cost = 0;      // of one group; warp w takes sequences w, w + 32, ...
-    for (int b = warp; b < g.B; b += kThreads / 32) {
-      const SeqShape s = seq_shape(g, b);
-      for (int k = lane; k < s.nt; k += 32)
-        cost += (int64_t)key_tiles(g, s, (k + 1) * s.tr) * (s.tr > 128 ? 2 : 1);
+    cost = block_sum(cost, wide_sh);
+    jobs = block_sum(jobs, wide_sh);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most_cost = __reduce_max_sync(0xffffffffu, most_cost);
+    if (lane == 0) {
+      atomicMin(&s_min, least);
+      atomicMax(&s_max, most_cost);
     }
-    cost = block_sum(cost, wide_sh) + (int64_t)g.prefix_tiles * g.np * prefix_streams;
+    __syncthreads();
+    const int start = g.few ? 2 : 5;               // an item's beginning and end, in the cost of a tile
+    if (warp < 2) {                                // warp 0: own jobs, warp 1: the prefix's
+      // half of the room for cuts (a row tile for every SM and stream) each
+      const int64_t row_jobs = warp ? (int64_t)g.prefix_tiles * g.prefix_rows * g.G : jobs * g.G * g.big;
+      const int64_t most = 1 + (int64_t)kPlanSms * g.big / max(row_jobs, (int64_t)1);
+      const int parts = warp ? best_parts((int64_t)g.prefix_tiles * g.G, (int64_t)g.np * prefix_streams,
+                                          (int)min(most, (int64_t)kMaxParts), start)
+                             : best_parts(jobs * g.G, s_max, (int)min(most, (int64_t)kMaxParts), start);
+      if (lane == 0) s_parts[warp] = parts;
+    }
+    __syncthreads();
+    if (g.separate) {
+      prefix_per = (g.np + s_parts[1] - 1) / s_parts[1];
+      prefix_parts = (g.np + prefix_per - 1) / prefix_per;
+    }
+    // equal jobs: the best number of parts; unequal ones: a few items for every SM to even out with
     const int64_t aim = kPlanSms * kItemsPerSm;
-    unit = (int)min(max((int64_t)kMinUnit, (cost * g.G + aim - 1) / aim), (int64_t)INT32_MAX / 4);
+    if (s_max > 0 && s_min >= s_max - s_max / 8) unit = (s_max + s_parts[0] - 1) / s_parts[0];
+    else unit = (int)min(max((int64_t)kMinUnit, (cost * g.G + aim - 1) / aim), (int64_t)INT32_MAX / 4);
   }
 
   // ---- the smallest unit (by doubling) whose partial rows and items fit; uncut jobs always do
-  int prefix_parts = 0, prefix_per = 0;
-  for (;;) {
-    if (g.separate) prefix_parts = job_parts(g.np, prefix_streams, unit, &prefix_per);
-    if (unit == 0) break;
+  while (unit > 0) {
     int64_t rows = 0, items = 0;
-    for (int b = threadIdx.x; b < g.B; b += kThreads) {
-      const SeqShape s = seq_shape(g, b);
+    for (int b0 = 0; b0 < g.B; b0 += kThreads) {
+      if (!one_load) load(b0 + me);
+      const SeqShape s = shape(me);
       if (s.rows == 0) continue;
       int per;
       const int most = job_parts(key_tiles(g, s, s.rows), s.tr > 128 ? 2 : 1, unit, &per);
@@ -110,83 +187,82 @@ __device__ void plan_items(const StepGeom& g) {
     items = block_sum(items, wide_sh) + prefix_jobs;
     if (rows <= g.max_part_rows && items <= g.max_items) break;
     unit = unit > (1 << 28) ? 0 : unit * 2;
+    if (unit == 0 && g.separate) {               // nothing is cut
+      prefix_per = g.np;
+      prefix_parts = 1;
+    }
   }
 
-  // ---- first item and first partial row of every sequence
+  // ---- first item and first partial row of every sequence, then its items
   const int prefix_items = prefix_parts * g.prefix_tiles * g.G;
   int item_base = prefix_items;
   int row_base = prefix_parts * g.prefix_tiles * g.prefix_rows * g.G;
-  for (int b0 = 0; b0 < g.B; b0 += 32) {         // 32 sequences at a time, one per warp
-    const int b = b0 + warp;
-    int n_items = 0, n_rows = 0, most = 0;
-    if (b < g.B) {
-      const SeqShape s = seq_shape(g, b);
-      const int n_jobs = s.nt * g.G;
-      for (int i = lane; i < n_jobs; i += 32) n_items += job_of(g, s, i, unit).parts;
-      n_items = __reduce_add_sync(0xffffffffu, n_items);
-      if (s.rows > 0) {
-        int per;
-        most = job_parts(key_tiles(g, s, s.rows), s.tr > 128 ? 2 : 1, unit, &per);
-        if (g.separate || most > 1) n_rows = most * g.G * (s.nt == 1 ? s.rows : s.nt * s.tr);
-      }
+  for (int b0 = 0; b0 < g.B; b0 += kThreads) {
+    if (!one_load) {
+      __syncthreads();
+      load(b0 + me);
     }
+    const SeqShape s = shape(me);
+    int n_items = 0, n_rows = 0, most = 0, total;
+    if (s.rows > 0) {
+      int per;
+      most = job_parts(key_tiles(g, s, s.rows), s.tr > 128 ? 2 : 1, unit, &per);
+      if (g.separate || most > 1) n_rows = most * g.G * (s.nt == 1 ? s.rows : s.nt * s.tr);
+      if (most == 1 && !g.separate) n_items = s.nt * g.G;      // every job, whether it has keys or not
+      else
+        for (int k = 0; k < s.nt; ++k) n_items += job_of(g, s, k * g.G, unit).parts * g.G;
+    }
+    s_item[me] = item_base + block_exclusive(n_items, &total, sh);
+    item_base += total;
+    s_row[me] = row_base + block_exclusive(n_rows, &total, sh);
+    row_base += total;
+    s_most[me] = most;
+    if (b0 + me < g.B) g.seq[b0 + me] = SeqInfo{s.q0, s.q1, s.kv, s_row[me], most, {0, 0, 0}};
     __syncthreads();
-    if (lane == 0) sh[warp] = n_items;
-    __syncthreads();
-    const int it_incl = warp_inclusive(sh[lane]);
-    __syncthreads();
-    if (lane == 0) sh[warp] = n_rows;
-    __syncthreads();
-    const int ro_incl = warp_inclusive(sh[lane]);
-    const int it0 = item_base + __shfl_sync(0xffffffffu, it_incl, warp) - n_items;
-    const int ro0 = row_base + __shfl_sync(0xffffffffu, ro_incl, warp) - n_rows;
-    item_base += __shfl_sync(0xffffffffu, it_incl, 31);
-    row_base += __shfl_sync(0xffffffffu, ro_incl, 31);
-    if (b >= g.B) continue;                       // whole warps only
-    const SeqShape s = seq_shape(g, b);
-    if (lane == 0) g.seq[b] = SeqInfo{s.q0, s.q1, s.kv, ro0, most, {0, 0, 0}};
-    // ---- its items
-    const int n_jobs = s.nt * g.G;
-    int at = it0;
-    for (int i0 = 0; i0 < n_jobs; i0 += 32) {
-      const int i = i0 + lane;
-      Job j{};
-      if (i < n_jobs) j = job_of(g, s, i, unit);
-      const int incl = warp_inclusive(j.parts);
-      int w = at + incl - j.parts;
-      at += __shfl_sync(0xffffffffu, incl, 31);
-      if (i >= n_jobs) continue;
-      const int r0 = j.k * s.tr;
-      const int nrows = min(s.tr, s.rows - r0);
-      const int slot_rows = s.nt == 1 ? s.rows : s.tr;
-      const bool direct = j.parts == 1 && !g.separate;
-      const int alt = g.dtype != AFF_BF16 ? 0 : g.few && nrows <= kFewRows ? 2 : nrows <= 128;
-      const int first = key_tiles(g, s, r0 + 128);    // key tiles that stream 0's rows meet
-      for (int p = 0; p < j.parts; ++p, ++w) {
-        if (w >= g.max_items) break;
+    for (int x = warp; x < min(kThreads, g.B - b0); x += kThreads / 32) {
+      const SeqShape s = shape(x);
+      const int n_jobs = s.nt * g.G;
+      int at = s_item[x];
+      for (int i0 = 0; i0 < n_jobs; i0 += 32) {
+        const int i = i0 + lane;
+        Job j{};
+        if (i < n_jobs) j = job_of(g, s, i, unit);
+        const int incl = warp_inclusive(j.parts);
+        int w = at + incl - j.parts;
+        at += __shfl_sync(0xffffffffu, incl, 31);
+        if (i >= n_jobs) continue;
+        const int r0 = j.k * s.tr;
+        const int nrows = min(s.tr, s.rows - r0);
+        const int slot_rows = s.nt == 1 ? s.rows : s.tr;
+        const bool direct = j.parts == 1 && !g.separate;
+        const int alt = g.dtype != AFF_BF16 ? 0 : g.few && nrows <= kFewRows ? 2 : nrows <= 128;
+        const int first = key_tiles(g, s, r0 + 128);    // key tiles that stream 0's rows meet
         WorkItem it;
         it.row0 = s.q0 * g.R + r0;
         it.nrows = nrows;
         it.group = j.group;
-        it.seq = b;
-        it.t0 = p * j.per;
-        const int n = min(j.per, j.tiles - it.t0);
-        if (g.dtype != AFF_BF16 || alt == 2) {
-          it.n0 = n;
-          it.n1 = 0;
-        } else if (alt) {
-          it.n0 = (n + 1) / 2;
-          it.n1 = n / 2;
-        } else {
-          it.n0 = min(max(first - it.t0, 0), n);
-          it.n1 = n;
-        }
-        it.part_row = direct ? -1 : ro0 + ((j.group * s.nt + j.k) * most + p) * slot_rows;
+        it.seq = b0 + x;
         it.own_off = s.kv - s.q1;                  // token t has own index kv - (q1 - q0) + t - q0
         it.own_len = keys_in_view(g, s, r0 + nrows);
         it.alt = alt;
         it.np = g.separate ? 0 : g.np;
-        g.items[w] = it;
+        for (int p = 0; p < j.parts; ++p, ++w) {
+          if (w >= g.max_items) break;
+          it.t0 = p * j.per;
+          const int n = min(j.per, j.tiles - it.t0);
+          if (g.dtype != AFF_BF16 || alt == 2) {
+            it.n0 = n;
+            it.n1 = 0;
+          } else if (alt) {
+            it.n0 = (n + 1) / 2;
+            it.n1 = n / 2;
+          } else {
+            it.n0 = min(max(first - it.t0, 0), n);
+            it.n1 = n;
+          }
+          it.part_row = direct ? -1 : s_row[x] + ((j.group * s.nt + j.k) * s_most[x] + p) * slot_rows;
+          g.items[w] = it;
+        }
       }
     }
   }
@@ -327,6 +403,7 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     g.page_tiles = (g.page_size + g.key_tile - 1) / g.key_tile;
   }
   g.by_R.set((uint32_t)g.R);
+  g.by_G.set((uint32_t)g.G);
   g.by_page.set((uint32_t)g.page_size);
   g.by_tile.set((uint32_t)g.key_tile);
   g.by_page_tiles.set((uint32_t)std::max(g.page_tiles, 1));
@@ -356,7 +433,7 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   const int64_t jobs = (tiles + g.prefix_tiles) * g.G;
   const int64_t full = rows / g.big * g.G;
   g.may_split = g.separate || full < 2 * kPlanSms;
-  const int64_t items = 2 * jobs + kPlanSms * kItemsPerSm + 2 * g.G + 64;
+  const int64_t items = 2 * jobs + (int64_t)kPlanSms * 2 * kItemsPerSm + 2 * g.G + 64;
   int64_t part_rows = 0;
   if (g.may_split) {
     // Uncut jobs: with the prefix apart every row has a part from the prefix and one of its own
