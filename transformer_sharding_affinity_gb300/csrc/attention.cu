@@ -89,7 +89,7 @@ struct alignas(16) Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t kv_ready[3][kMaxStages];          // stream 0, stream 1, few rows: their own tiles, in their own order
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
-  uint64_t stat_full[2], stat_empty[2], few, drain[2], slot_full[kSlots], slot_empty[kSlots];
+  uint64_t stat_full[2], stat_empty[2], few, few_read, drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
   uint32_t tmem;
   int abort_flag;
@@ -550,26 +550,26 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
     if (lane == 0) mbar_arrive(&bars->kv_empty[rv.s]);
     rv.skip(2, stages);
   }
-  auto all_warps = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->few);
-    wait_on(&bars->few, few_ph, bars);
-    few_ph ^= 1u;
-  };
-  // ---- the eight warps' parts are added in shared memory, two rows at a time
+  // ---- the eight warps' parts are added in shared memory, two rows at a time, by the first four warps;
+  // the others go on to the next item at once and wait only where they would write over what is not read
   float* part = reinterpret_cast<float*>(few_smem);                       // [warp][2 rows][kFewPitch]
   float2* ml = reinterpret_cast<float2*>(part + 8 * 2 * kFewPitch);       // [warp][kFewRows]
 #pragma unroll
   for (int t = 0; t < RN; ++t)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
-      if (quad == 0) ml[warp * kFewRows + 8 * t + col2 + e] = make_float2(m[t][e], l[t][e]);
-    }
 #pragma unroll
   for (int pass = 0; pass < 4 * RN; ++pass) {
     if (pass * 2 >= nrows) break;
+    wait_on(&bars->few_read, few_ph ^ 1u, bars);
+    if (pass == 0 && quad == 0) {
+#pragma unroll
+      for (int t = 0; t < RN; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ml[warp * kFewRows + 8 * t + col2 + e] = make_float2(m[t][e], l[t][e]);
+    }
     if (col2 >> 1 == (pass & 3)) {
       float* dst = part + warp * 2 * kFewPitch + quad;
 #pragma unroll
@@ -580,9 +580,13 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
         dst[n * 16 + 8 + kFewPitch] = o[pass >> 2][n][3];
       }
     }
-    all_warps();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->few);
+    few_ph ^= 1u;
+    if (warp >= 4) continue;
+    wait_on(&bars->few, few_ph ^ 1u, bars);
     const int rl = threadIdx.x >> 6, r_item = pass * 2 + rl, c = (threadIdx.x & 63) * 2;
-    if (rl < 2 && r_item < nrows && c < g.d) {
+    if (r_item < nrows && c < g.d) {
       float2 a[8];
 #pragma unroll
       for (int w = 0; w < 8; ++w) a[w] = ml[w * kFewRows + r_item];
@@ -612,7 +616,8 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
         if (c == 0) g.part_lse[it.part_row + r_item] = lse;
       }
     }
-    all_warps();          // read: the next rows, or the next item's, may be written
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->few_read);
   }
 }
 
@@ -667,6 +672,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       mbar_init(&bars->slot_empty[i], 15);   // softmax warps 8, output warps 4, product warps 2, clearing warp 1
     }
     mbar_init(&bars->few, 8);
+    mbar_init(&bars->few_read, 4);
     bars->abort_flag = 0;
     fence_mbar_init();
   }

@@ -113,12 +113,13 @@ __device__ void plan_items(const StepGeom& g) {
   const bool one_load = g.B <= kThreads;
 
   // ---- check the batch; the cost of all own jobs of one group, in key tiles x streams, and their extremes
-  int64_t cost = 0, jobs = 0, bad = 0;
+  int64_t cost = 0, jobs = 0, rows_all = 0, bad = 0;
   int least = INT32_MAX, most_cost = 0;
   for (int b0 = 0; b0 < g.B; b0 += kThreads) {
     if (!load(b0 + me)) bad = 1;
     if (!g.may_split) continue;
     const SeqShape s = shape(me);
+    rows_all += s.nt <= 1 ? s.rows : s.nt * s.tr;
     for (int k = 0; k < s.nt; ++k) {
       const int c = key_tiles(g, s, (k + 1) * s.tr) * (s.tr > 128 ? 2 : 1);
       if (c == 0) continue;
@@ -142,6 +143,7 @@ __device__ void plan_items(const StepGeom& g) {
   if (g.may_split) {
     cost = block_sum(cost, wide_sh);
     jobs = block_sum(jobs, wide_sh);
+    rows_all = block_sum(rows_all, wide_sh);
     least = __reduce_min_sync(0xffffffffu, least);
     most_cost = __reduce_max_sync(0xffffffffu, most_cost);
     if (lane == 0) {
@@ -152,7 +154,7 @@ __device__ void plan_items(const StepGeom& g) {
     const int start = g.few ? 2 : 5;               // an item's beginning and end, in the cost of a tile
     if (warp < 2) {                                // warp 0: own jobs, warp 1: the prefix's
       // half of the room for cuts (a row tile for every SM and stream) each
-      const int64_t row_jobs = warp ? (int64_t)g.prefix_tiles * g.prefix_rows * g.G : jobs * g.G * g.big;
+      const int64_t row_jobs = (warp ? (int64_t)g.prefix_tiles * g.prefix_rows : rows_all) * g.G;     // rows of a part
       const int64_t most = 1 + (int64_t)kPlanSms * g.big / max(row_jobs, (int64_t)1);
       const int parts = warp ? best_parts((int64_t)g.prefix_tiles * g.G, (int64_t)g.np * prefix_streams,
                                           (int)min(most, (int64_t)kMaxParts), start)
