@@ -41,6 +41,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 namespace aff {
 namespace {
@@ -1243,101 +1244,183 @@ aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsi
 }
 
 // ---------------------------------------------------------------- fp32
+// On the CUDA cores: a product of two fp32 numbers keeps all its bits there.  Two CTAs per SM; items are
+// claimed from the plan's counter.
 constexpr int kF32Threads = 256;
-constexpr int kF32Keys = 64;
+constexpr int kF32Keys = 64;                 // keys of a step of the tiled path
+constexpr int kF32Rows = 64;                 // its rows
+constexpr int kF32Few = 32;                  // most rows of the streaming path
 
-// One item of up to 16 * RT rows: thread (ty, tx) holds rows ty * RT .. + RT - 1,
-// scores of keys tx, tx + 16, .. and output columns 4 tx .. + 3 of each 64.  Scores go
-// through shared memory between the two products.  Bound by the fp32 FMA rate and
-// by shared-memory loads; meant for small shapes, like every fp32 path here.
-template <int RT>
-__device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(void* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// Where key `key` of the prefix or of an item's sequence lies in the pools; -1 if its page is out of range.
+__device__ __forceinline__ int64_t key_at(const AttnParams& p, const WorkItem& it, bool pre, int key) {
   const StepGeom& g = p.g;
-  const int d = g.d, ld = d + 4;
-  constexpr int kR = 16 * RT;
-  float* qs = smem;                       // [kR][ld]
-  float* ks = qs + 64 * ld;               // [64][ld]
-  float* vs = ks + kF32Keys * ld;         // [64][ld]
-  float* ps = vs + kF32Keys * ld;         // [kR][68]
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const float* q = reinterpret_cast<const float*>(p.q);
-  const int d4 = d / 4;
-  __syncthreads();
-  for (int i = threadIdx.x; i < kR * d4; i += kF32Threads) {
-    const int r = i / d4, c = (i - r * d4) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < it.nrows) {
-      const int rr = it.row0 + r, tok = g.by_R(rr);
-      v = *reinterpret_cast<const float4*>(q + (int64_t)tok * p.q_stride + (int64_t)(it.group * g.R + rr - tok * g.R) * d + c);
-    }
-    *reinterpret_cast<float4*>(qs + r * ld + c) = v;
+  const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+  const int pi = g.by_page(key);
+  const int page = __ldg(table + pi);
+  if (page < 0 || page >= g.n_pages) {
+    latch_status(&g.head->status, kStatusRange);
+    return -1;
   }
-  float m[RT], l[RT], o[RT][8];
-  int own_vis[RT];
+  return page * p.page_stride + it.group * p.group_stride + (int64_t)(key - pi * g.page_size) * p.token_stride;
+}
+
+__device__ __forceinline__ void f32_write(const AttnParams& p, const WorkItem& it, int r, int c, float4 v) {
+  const StepGeom& g = p.g;
+  const int rr = it.row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+  float* dst = it.part_row < 0 ? static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d
+                               : g.part_out + (int64_t)(it.part_row + r) * g.d;
+  *reinterpret_cast<float4*>(dst + c) = v;
+}
+__device__ __forceinline__ void f32_write_lse(const AttnParams& p, const WorkItem& it, int r, float m, float l) {
+  const StepGeom& g = p.g;
+  const int rr = it.row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+  const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+  if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
+  else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+}
+
+// Up to 64 rows against 64 keys a step.  Thread (ty, tx) holds rows 4 ty .. + 3: the scores of keys tx + 16 b and
+// output columns 4 tx .. + 3 of each 64.  Both products take two fp32 lanes an instruction, which leaves issue
+// slots for the shared-memory loads.  Probabilities pass through shared memory by key, so that a thread's four
+// rows are one load.  Rows of q and k are swizzled by 16-byte chunks: no load has a bank conflict.  The next keys
+// are copied in behind this step's softmax and second product, the next values behind the first product; the
+// other CTA of the SM fills what remains.
+__device__ void f32_tile(const AttnParams& p, const WorkItem& it, float* smem) {
+  const StepGeom& g = p.g;
+  constexpr int ld = 128;
+  const int d = g.d;
+  float* qs = smem;                       // [row][chunk ^ row % 8]
+  float* ks = qs + kF32Rows * ld;         // [key][chunk ^ key % 8]
+  float* vs = ks + kF32Keys * ld;         // [key]
+  float* ps = vs + kF32Keys * ld;         // [key][chunk ^ key % 8] of 64 rows
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, sw = tx & 7;
+  const int cr = threadIdx.x >> 3, cc = (threadIdx.x & 7) * 4;          // copies: rows cr, cr + 32; 16 bytes of each 128
+  const float* q = reinterpret_cast<const float*>(p.q);
+  for (int r = cr; r < kF32Rows; r += 32) {
+    const int rr = it.row0 + min(r, it.nrows - 1), tok = g.by_R(rr);
+    const float* src = q + (int64_t)tok * p.q_stride + (int64_t)(it.group * g.R + rr - tok * g.R) * d;
+    for (int c = cc; c < d; c += 32) copy16(qs + r * ld + (c ^ ((r & 7) * 4)), src + c, r < it.nrows);
+  }
+  float m[4], l[4];
+  uint64_t o[4][4];
+  int own_vis[4];
 #pragma unroll
-  for (int a = 0; a < RT; ++a) {
-    const int r = ty * RT + a, tok = g.by_R(it.row0 + r);
+  for (int a = 0; a < 4; ++a) {
+    const int r = ty * 4 + a;
     m[a] = -INFINITY;
     l[a] = 0.f;
-    own_vis[a] = it.seq < 0 ? 1 : tok + it.own_off + 1;
-    if (r >= it.nrows) own_vis[a] = 0;
+    own_vis[a] = r >= it.nrows ? 0 : it.seq < 0 ? 1 : g.by_R(it.row0 + r) + it.own_off + 1;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[a][e] = 0.f;
+    for (int e = 0; e < 4; ++e) o[a][e] = 0;
   }
-  for (int j = 0; j < 2 * it.n0; ++j) {
-    const int ti = it.t0 + (j >> 1);
-    int key0;
-    int keys = tile_keys(it, g, ti, &key0);
-    key0 += (j & 1) * kF32Keys;
-    keys = min(keys - (j & 1) * kF32Keys, kF32Keys);
-    if (keys <= 0) continue;
-    const bool pre = ti < it.np;
-    const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kF32Keys * d4; i += kF32Threads) {
-      const int r = i / d4, c = (i - r * d4) * 4;
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (r < keys) {
-        const int key = key0 + r, pi = g.by_page(key);
-        const int page = __ldg(table + pi);
-        if (page >= 0 && page < g.n_pages) {
-          const int64_t at = page * p.page_stride + it.group * p.group_stride + (int64_t)(key - pi * g.page_size) * p.token_stride + c;
-          kv = *reinterpret_cast<const float4*>(p.kc + at);
-          vv = *reinterpret_cast<const float4*>(p.vc + at);
-        } else {
-          latch_status(&g.head->status, kStatusRange);
+  // the walk: half tiles of 64 keys; `keys` 0 at its end
+  struct Half {
+    int tile, half, key0, keys;
+    bool pre;
+  };
+  auto span = [&](Half& s) {
+    s.keys = 0;
+    while (s.tile < it.t0 + it.n0) {
+      s.pre = s.tile < it.np;
+      const int n = tile_keys(it, g, s.tile, &s.key0);
+      if (s.half * kF32Keys < n) {
+        s.key0 += s.half * kF32Keys;
+        s.keys = min(n - s.half * kF32Keys, kF32Keys);
+        return;
+      }
+      s.half = 0;
+      ++s.tile;
+    }
+  };
+  int64_t at[2];                          // of the rows this thread copies
+  auto locate = [&](const Half& s) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) at[x] = cr + 32 * x < s.keys ? key_at(p, it, s.pre, s.key0 + cr + 32 * x) : -1;
+  };
+  auto copy = [&](const Half& s, float* dst, const float* pool, int swizzle) {
+#pragma unroll
+    for (int x = 0; x < 2 && s.keys > 0; ++x) {
+      const int r = cr + 32 * x;
+      for (int c = cc; c < d; c += 32) copy16(dst + r * ld + (c ^ swizzle), at[x] < 0 ? pool : pool + at[x] + c, at[x] >= 0);
+    }
+    copy_commit();
+  };
+  Half cur{it.t0, 0, 0, 0, false};
+  span(cur);
+  locate(cur);
+  copy(cur, ks, p.kc, (cr & 7) * 4);
+  copy(cur, vs, p.vc, 0);
+  while (cur.keys > 0) {
+    Half next = cur;
+    ++next.half;
+    span(next);
+    copy_wait_but_one();
+    __syncthreads();                      // the keys are here
+    float s[4][4];
+    {
+      uint64_t acc[4][4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[a][b] = 0;
+#pragma unroll 4
+      for (int c = 0; c < d; c += 4) {
+        ulonglong2 kf[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) kf[b] = *reinterpret_cast<const ulonglong2*>(ks + (tx + 16 * b) * ld + (c ^ (sw * 4)));
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int r = ty * 4 + a;
+          const ulonglong2 qf = *reinterpret_cast<const ulonglong2*>(qs + r * ld + (c ^ ((r & 7) * 4)));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[a][b] = fma2(qf.y, kf[b].y, fma2(qf.x, kf[b].x, acc[a][b]));
         }
       }
-      *reinterpret_cast<float4*>(ks + r * ld + c) = kv;
-      *reinterpret_cast<float4*>(vs + r * ld + c) = vv;
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float2 v = halves2(acc[a][b]);
+          s[a][b] = v.x + v.y;
+        }
     }
-    __syncthreads();
-    float sc[RT][4];
+    __syncthreads();                      // the keys are read
+    locate(next);
+    copy(next, ks, p.kc, (cr & 7) * 4);
+    int last = 0, first = kF32Keys;       // keys of this step that any, and that all of the thread's rows see
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) sc[a][b] = 0.f;
-    for (int c = 0; c < d; c += 4) {
-      float4 kf[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) kf[b] = *reinterpret_cast<const float4*>(ks + (tx + 16 * b) * ld + c);
-#pragma unroll
-      for (int a = 0; a < RT; ++a) {
-        const float4 qf = *reinterpret_cast<const float4*>(qs + (ty * RT + a) * ld + c);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          sc[a][b] += qf.x * kf[b].x + qf.y * kf[b].y + qf.z * kf[b].z + qf.w * kf[b].w;
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      int vis = pre ? keys : min(keys, own_vis[a] - key0);
-      if (own_vis[a] <= 0) vis = 0;
+    for (int a = 0; a < 4; ++a) {
+      const int vis = own_vis[a] <= 0 ? 0 : cur.pre ? cur.keys : min(cur.keys, own_vis[a] - cur.key0);
+      last = max(last, vis);
+      first = min(first, vis);
       float mx = -INFINITY;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (tx + 16 * b >= vis) sc[a][b] = -INFINITY;
-        mx = fmaxf(mx, sc[a][b]);
+        if (tx + 16 * b >= vis) s[a][b] = -INFINITY;
+        mx = fmaxf(mx, s[a][b]);
       }
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -1347,71 +1430,245 @@ __device__ void f32_item(const AttnParams& p, const WorkItem& it, float* smem) {
       float sum = 0.f;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const float e = expf((sc[a][b] - ref) * p.scale);
-        sum += e;
-        ps[(ty * RT + a) * 68 + tx + 16 * b] = e;
+        s[a][b] = expf((s[a][b] - ref) * p.scale);
+        sum += s[a][b];
       }
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       l[a] = l[a] * f + sum;
       m[a] = m_new;
+      const uint64_t ff = pair2(f, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[a][e] *= f;
+      for (int e = 0; e < 4; ++e) o[a][e] = fma2(o[a][e], ff, 0);
     }
-    __syncwarp();      // a row's scores are written and read by the same half warp
-    for (int k = 0; k < keys; ++k) {
-      float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-      if (4 * tx < d) v0 = *reinterpret_cast<const float4*>(vs + k * ld + 4 * tx);
-      if (64 + 4 * tx < d) v1 = *reinterpret_cast<const float4*>(vs + k * ld + 64 + 4 * tx);
 #pragma unroll
-      for (int a = 0; a < RT; ++a) {
-        const float w = ps[(ty * RT + a) * 68 + k];
-        if (w == 0.f) continue;                 // masked: whatever lies there
-        o[a][0] += w * v0.x; o[a][1] += w * v0.y; o[a][2] += w * v0.z; o[a][3] += w * v0.w;
-        o[a][4] += w * v1.x; o[a][5] += w * v1.y; o[a][6] += w * v1.z; o[a][7] += w * v1.w;
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<float4*>(ps + (tx + 16 * b) * kF32Rows + ((ty ^ sw) * 4)) = make_float4(s[0][b], s[1][b], s[2][b], s[3][b]);
+    copy_wait_but_one();
+    __syncthreads();                      // the values are here
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    auto add = [&](int k, auto masked) {
+      const float4 w = *reinterpret_cast<const float4*>(ps + k * kF32Rows + ((ty ^ (k & 7)) * 4));
+      const float wa[4] = {w.x, w.y, w.z, w.w};
+      ulonglong2 v0 = make_ulonglong2(0, 0), v1 = v0;
+      if (4 * tx < d) v0 = *reinterpret_cast<const ulonglong2*>(vs + k * ld + 4 * tx);
+      if (64 + 4 * tx < d) v1 = *reinterpret_cast<const ulonglong2*>(vs + k * ld + 64 + 4 * tx);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        if (decltype(masked)::value && wa[a] == 0.f) continue;                // whatever lies there stays out
+        const uint64_t ww = pair2(wa[a], wa[a]);
+        o[a][0] = fma2(ww, v0.x, o[a][0]);
+        o[a][1] = fma2(ww, v0.y, o[a][1]);
+        o[a][2] = fma2(ww, v1.x, o[a][2]);
+        o[a][3] = fma2(ww, v1.y, o[a][3]);
       }
-    }
+    };
+    int k = 0;
+#pragma unroll 2
+    for (; k < first; ++k) add(k, std::false_type());
+#pragma unroll 1
+    for (; k < last; ++k) add(k, std::true_type());
+    __syncthreads();                      // the values and the probabilities are read
+    copy(next, vs, p.vc, 0);
+    cur = next;
   }
+  copy_wait_all();                        // an item without keys leaves its queries under way
 #pragma unroll
-  for (int a = 0; a < RT; ++a) {
-    const int r = ty * RT + a;
+  for (int a = 0; a < 4; ++a) {
+    const int r = ty * 4 + a;
     if (r >= it.nrows) continue;
-    const int rr = it.row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
-    const bool empty = l[a] == 0.f;
-    const float inv = empty ? 0.f : 1.f / l[a];
-    float* dst = it.part_row < 0 ? static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * d
-                                 : g.part_out + (int64_t)(it.part_row + r) * d;
+    const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = 64 * x + 4 * tx;
       if (c >= d) continue;
-      *reinterpret_cast<float4*>(dst + c) =
-          empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                : make_float4(o[a][4 * x] * inv, o[a][4 * x + 1] * inv, o[a][4 * x + 2] * inv, o[a][4 * x + 3] * inv);
+      const float2 v0 = halves2(o[a][2 * x]), v1 = halves2(o[a][2 * x + 1]);
+      f32_write(p, it, r, c, l[a] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                         : make_float4(v0.x * inv, v0.y * inv, v1.x * inv, v1.y * inv));
     }
-    if (tx == 0) {
-      const float lse = empty ? -INFINITY : m[a] * p.scale + logf(l[a]);
-      if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
-      else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
-    }
+    if (tx == 0) f32_write_lse(p, it, r, m[a], l[a]);
   }
 }
 
-size_t f32_smem_bytes(int d) { return (size_t)(64 * (d + 4) * 3 + 64 * 68) * 4; }
+// Up to 32 rows: bound by the cache's bytes.  A warp takes NR rows (1, 2, 4) and every n-th run of eight keys, straight
+// from global memory to registers (a key's row is one load of the warp, 4 columns to a lane); warps with other
+// rows of the same keys find them in the first cache.  The 8 NR dot products of a run are summed over the lanes
+// by halving: 31 shuffles for four rows leave lane 8 r + k with the score of row r and key k (4 / NR lanes each).  A warp's running maximum and
+// sum are its own; the warps' parts are joined at the end of the item.
+template <int NR>
+__device__ void f32_few(const AttnParams& p, const WorkItem& it, float* smem) {
+  const StepGeom& g = p.g;
+  const int d = g.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int S = NR == 1 ? 2 : NR == 2 ? 1 : 0;                      // a score lies in 2^S neighbouring lanes
+  const int blocks = it.nrows <= NR ? 1 : it.nrows <= 8 ? 2 : it.nrows <= 16 ? 4 : 8;       // of NR rows; warp % blocks takes one
+  const int r0 = (warp % blocks) * NR, stride = 8 / blocks;
+  const int kk = (lane >> S) & 7;
+  const int c = 4 * lane;
+  const bool has = c < d;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 q[NR], o[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    q[r] = o[r] = zero;
+    if (has && r0 + r < it.nrows) {
+      const int rr = it.row0 + r0 + r, tok = g.by_R(rr);
+      q[r] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + (int64_t)tok * p.q_stride +
+                                              (int64_t)(it.group * g.R + rr - tok * g.R) * d + c);
+    }
+  }
+  const int row = r0 + (lane >> (3 + S));                                   // the row whose scores this lane ends up with
+  const int own_vis = row >= it.nrows ? 0 : it.seq < 0 ? 1 : g.by_R(it.row0 + row) + it.own_off + 1;
+  float m = -INFINITY, l = 0.f;
+  const int runs = (g.key_tile + 7) / 8, end = it.t0 + it.n0;
+  struct Run {
+    int tile, sub, key, keys;             // key: this lane's (kk of the run), keys: of the run
+    bool pre;
+  };
+  auto step_to = [&](Run& s) {            // the next run that holds a key; keys 0 at the end
+    s.keys = 0;
+    while (s.tile < end) {
+      s.pre = s.tile < it.np;
+      int key0;
+      const int n = tile_keys(it, g, s.tile, &key0) - 8 * s.sub;
+      if (n > 0) {
+        s.keys = min(n, 8);
+        s.key = key0 + 8 * s.sub + kk;
+      }
+      s.sub += stride;
+      while (s.sub >= runs) {
+        s.sub -= runs;
+        ++s.tile;
+      }
+      if (n > 0) return;
+    }
+  };
+  auto locate = [&](const Run& s) { return kk < s.keys ? key_at(p, it, s.pre, s.key) : (int64_t)-1; };
+  auto load = [&](float4 (&x)[8], const float* pool, int64_t at) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t a = __shfl_sync(0xffffffffu, at, k << S);
+      x[k] = has && a >= 0 ? __ldg(reinterpret_cast<const float4*>(pool + a + c)) : zero;
+    }
+  };
+  Run cur{it.t0 + (warp / blocks) / runs, (warp / blocks) % runs, 0, 0, false}, next;
+  step_to(cur);
+  next = cur;
+  step_to(next);
+  int64_t at = locate(cur);
+  float4 kf[8], vf[8];
+  load(kf, p.kc, at);
+  while (cur.keys > 0) {
+    load(vf, p.vc, at);
+    float s[8 * NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[r * 8 + k] = q[r].x * kf[k].x + q[r].y * kf[k].y + q[r].z * kf[k].z + q[r].w * kf[k].w;
+#pragma unroll
+    for (int n = 4 * NR, w = 16; w > 0; n >>= 1, w >>= 1) {
+      const bool up = lane & w;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float send = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+      }
+      if (n == 0) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
+    }
+    at = locate(next);
+    load(kf, p.kc, at);
+    const bool seen = own_vis > 0 && kk < cur.keys && (cur.pre || cur.key < own_vis);
+    const float sc = seen ? s[0] : -INFINITY;
+    float mx = sc;
+#pragma unroll
+    for (int x = 4; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x << S));
+    const float m_new = fmaxf(m, mx), ref = m_new == -INFINITY ? 0.f : m_new;
+    const float f = m == -INFINITY ? 0.f : expf((m - ref) * p.scale);
+    const float e = expf((sc - ref) * p.scale);
+    l = l * f + e;                        // this lane's keys alone
+    m = m_new;
+    const bool all = __all_sync(0xffffffffu, seen);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float fr = __shfl_sync(0xffffffffu, f, 8 * r << S);
+      o[r].x *= fr;
+      o[r].y *= fr;
+      o[r].z *= fr;
+      o[r].w *= fr;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __shfl_sync(0xffffffffu, e, (8 * r + k) << S);
+        if (!all && w == 0.f) continue;   // masked: whatever lies there
+        o[r].x += w * vf[k].x;
+        o[r].y += w * vf[k].y;
+        o[r].z += w * vf[k].z;
+        o[r].w += w * vf[k].w;
+      }
+    }
+    cur = next;
+    step_to(next);
+  }
+#pragma unroll
+  for (int x = 4; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x << S);
+  // ---- join the warps' parts
+  float* po = smem;                                                     // [warp][4][128]
+  float2* ml = reinterpret_cast<float2*>(smem + 8 * 4 * 128);           // [warp][4]
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+    if (has) *reinterpret_cast<float4*>(po + (warp * 4 + r) * 128 + c) = o[r];
+  if ((lane & ((8 << S) - 1)) == 0) ml[warp * 4 + (lane >> (3 + S))] = make_float2(m, l);
+  __syncthreads();
+  for (int r = warp; r < it.nrows; r += 8) {
+    const int b = r / NR;
+    float top = -INFINITY, sum = 0.f;
+    for (int w = b; w < 8; w += blocks) top = fmaxf(top, ml[w * 4 + r % NR].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 acc = zero;
+    for (int w = b; w < 8; w += blocks) {
+      const float2 s = ml[w * 4 + r % NR];
+      const float f = s.x == -INFINITY ? 0.f : expf((s.x - ref) * p.scale);
+      sum += f * s.y;
+      const float4 v = has ? *reinterpret_cast<const float4*>(po + (w * 4 + r % NR) * 128 + c) : zero;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (has) f32_write(p, it, r, c, sum == 0.f ? zero : make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (lane == 0) f32_write_lse(p, it, r, top, sum);
+  }
+}
 
-__global__ void __launch_bounds__(kF32Threads) attention_f32_kernel(const __grid_constant__ AttnParams p) {
-  extern __shared__ uint8_t smem_raw[];
+constexpr int kF32Smem = ((kF32Rows + 2 * kF32Keys) * 128 + kF32Keys * kF32Rows) * 4;       // twice on an SM
+static_assert((8 * 4 * 128 + 8 * 4 * 2) * 4 <= kF32Smem, "f32_few's joining fits");
+
+__global__ void __launch_bounds__(kF32Threads, 2) attention_f32_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ int claim;
   pdl_enter();
   const StepGeom& g = p.g;
-  if (!plan_matches(g)) {
-    if (threadIdx.x == 0) latch_status(&g.head->status, kStatusInvalid);
-    return;
-  }
-  const int n = g.head->n_items;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+  const bool fits = plan_matches(g);
+  if (!fits && threadIdx.x == 0) latch_status(&g.head->status, kStatusInvalid);
+  const int n = fits ? g.head->n_items : 0;
+  // as in the bf16 kernel: the first item by number, the others from the counter
+  for (int i = blockIdx.x; i < n; i = claim) {
     const WorkItem it = load_item(g.items + i);
-    if (it.nrows <= 16) f32_item<1>(p, it, reinterpret_cast<float*>(smem_raw));
-    else f32_item<4>(p, it, reinterpret_cast<float*>(smem_raw));
+    __syncthreads();                      // claim and shared memory are free again
+    if (threadIdx.x == 0) claim = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
+    float* smem = reinterpret_cast<float*>(smem_raw);
+    if (it.nrows > kF32Few) f32_tile(p, it, smem);
+    else if (it.nrows > 2) f32_few<4>(p, it, smem);
+    else if (it.nrows == 2) f32_few<2>(p, it, smem);
+    else f32_few<1>(p, it, smem);
+    __syncthreads();
+  }
+  if (fits && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(&g.head->done, 1u) == gridDim.x - 1) {
+      g.head->claimed = 0;
+      g.head->done = 0;
+    }
   }
 }
 
@@ -1527,9 +1784,8 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
   p.token_stride = cache->token_stride;
   const unsigned grid = (unsigned)(g.max_items < sms ? g.max_items : sms);
   if (g.dtype == AFF_FP32) {
-    const size_t smem = f32_smem_bytes(g.d);
-    AFF_CUDA(cudaFuncSetAttribute(attention_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    AFF_CUDA(launch_pdl(attention_f32_kernel, grid * 2, kF32Threads, smem, s, p));
+    AFF_CUDA(cudaFuncSetAttribute(attention_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem));
+    AFF_CUDA(launch_pdl(attention_f32_kernel, grid * 2, kF32Threads, kF32Smem, s, p));
   } else {
     p.halves = g.d > 64 ? 2 : 1;
     p.kd = (g.d + 15) / 16 * 16;

@@ -54,14 +54,15 @@ __device__ int block_exclusive(int v, int* total, int* sh) {
   return __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, sh[lane], warp) + incl - v;
 }
 
-// Parts (1 .. most) of each of `jobs` equal jobs of `cost`: the least of the time of the fullest SM, where an
-// item takes its cost and `start` for its beginning and end, and of a part's trip through memory.  Warp-wide.
-__device__ int best_parts(int64_t jobs, int64_t cost, int most, int start) {
+// Parts (1 .. most) of each of `jobs` equal jobs of `cost`: the least of the time of the fullest slot, where an
+// item takes its cost and `start` for its beginning and end, and of a part's trip through memory.  A unit of cost
+// is `tile` times as long as such a trip.  Warp-wide.
+__device__ int best_parts(int64_t jobs, int64_t cost, int most, int slots, int tile, int start) {
   int64_t best = INT64_MAX;
   for (int parts = 1 + (threadIdx.x & 31); parts <= kMaxParts; parts += 32) {
     if (parts > most || parts > cost) continue;
-    const int64_t rounds = (jobs * parts + kPlanSms - 1) / kPlanSms;
-    best = min(best, (rounds * ((cost + parts - 1) / parts + start) + parts) << 8 | parts);
+    const int64_t rounds = (jobs * parts + slots - 1) / slots;
+    best = min(best, (rounds * ((cost + parts - 1) / parts * tile + start) + parts) << 8 | parts);
   }
   for (int o = 16; o > 0; o >>= 1) best = min(best, (int64_t)__shfl_xor_sync(0xffffffffu, best, o));
   return best == INT64_MAX ? 1 : (int)(best & 255);
@@ -151,14 +152,17 @@ __device__ void plan_items(const StepGeom& g) {
       atomicMax(&s_max, most_cost);
     }
     __syncthreads();
-    const int start = g.few ? 2 : 5;               // an item's beginning and end, in the cost of a tile
+    // fp32: two CTAs per SM, tiles that take some four times as long
+    const bool f32 = g.dtype != AFF_BF16;
+    const int slots = f32 ? 2 * kPlanSms : kPlanSms, tile = f32 ? 4 : 1;
+    const int start = g.few ? 2 : 5;               // an item's beginning and end, in the cost of a bf16 tile
     if (warp < 2) {                                // warp 0: own jobs, warp 1: the prefix's
       // half of the room for cuts (a row tile for every SM and stream) each
       const int64_t row_jobs = (warp ? (int64_t)g.prefix_tiles * g.prefix_rows : rows_all) * g.G;     // rows of a part
       const int64_t most = 1 + (int64_t)kPlanSms * g.big / max(row_jobs, (int64_t)1);
       const int parts = warp ? best_parts((int64_t)g.prefix_tiles * g.G, (int64_t)g.np * prefix_streams,
-                                          (int)min(most, (int64_t)kMaxParts), start)
-                             : best_parts(jobs * g.G, s_max, (int)min(most, (int64_t)kMaxParts), start);
+                                          (int)min(most, (int64_t)kMaxParts), slots, tile, start)
+                             : best_parts(jobs * g.G, s_max, (int)min(most, (int64_t)kMaxParts), slots, tile, start);
       if (lane == 0) s_parts[warp] = parts;
     }
     __syncthreads();
@@ -167,9 +171,9 @@ __device__ void plan_items(const StepGeom& g) {
       prefix_parts = (g.np + prefix_per - 1) / prefix_per;
     }
     // equal jobs: the best number of parts; unequal ones: a few items for every SM to even out with
-    const int64_t aim = kPlanSms * kItemsPerSm;
+    const int64_t aim = slots * kItemsPerSm;
     if (s_max > 0 && s_min >= s_max - s_max / 8) unit = (s_max + s_parts[0] - 1) / s_parts[0];
-    else unit = (int)min(max((int64_t)kMinUnit, (cost * g.G + aim - 1) / aim), (int64_t)INT32_MAX / 4);
+    else unit = (int)min(max((int64_t)kMinUnit / tile, (cost * g.G + aim - 1) / aim), (int64_t)INT32_MAX / 4);
   }
 
   // ---- the smallest unit (by doubling) whose partial rows and items fit; uncut jobs always do
@@ -420,12 +424,12 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     g.key[i] = (uint32_t)(h >> 16);
   }
   const bool bf = c->dtype == AFF_BF16;
-  g.small = bf ? 128 : 16;
+  g.small = bf ? 128 : 32;
   g.big = bf ? 256 : 64;
   const int64_t rows = (int64_t)g.T * g.R;
   // Jobs of its own for the prefix: worth it while sequences have few rows, so that a
   // row tile of one sequence would leave most of a tile idle for every key of the prefix.
-  g.separate = g.prefix_len > 0 && g.B > 1 && rows < (int64_t)g.B * g.small;
+  g.separate = g.prefix_len > 0 && g.B > 1 && rows < (int64_t)g.B * (bf ? g.small : g.big);
   // The few-rows path where sequences have few rows on average: the kernel without it is faster.
   g.few = bf && rows <= (int64_t)g.B * 64;
   g.prefix_rows = rows <= g.small ? g.small : g.big;
@@ -434,7 +438,7 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   const int64_t tiles = rows / g.big + g.B + 1;
   const int64_t jobs = (tiles + g.prefix_tiles) * g.G;
   const int64_t full = rows / g.big * g.G;
-  g.may_split = g.separate || full < 2 * kPlanSms;
+  g.may_split = g.separate || full < (bf ? 2 : 8) * kPlanSms;
   const int64_t items = 2 * jobs + (int64_t)kPlanSms * 2 * kItemsPerSm + 2 * g.G + 64;
   int64_t part_rows = 0;
   if (g.may_split) {
