@@ -151,7 +151,7 @@ constexpr int64_t kManyRows = 152 * 8;
 template <typename E, int VW>
 aff_status pick(const NormParams& p, cudaStream_t s) {
   const int runs = (p.D + VW - 1) / VW;
-  if constexpr (VW > 1) {
+  if constexpr (VW > 2) {
     if (p.T > kManyRows && runs > 32) {
       if (runs <= 64) return go<E, VW, 2, 32, 32>(p, s);
       if (runs <= 96) return go<E, VW, 3, 32, 32>(p, s);
@@ -164,6 +164,15 @@ aff_status pick(const NormParams& p, cudaStream_t s) {
       if (runs <= 1024) return go<E, VW, 4, 256, 256>(p, s);
     }
   }
+  if constexpr (VW <= 2) {
+    if (p.T > kManyRows && runs > 64) {
+      if (runs <= 128) return go<E, VW, 4, 32, 32>(p, s);
+      if (runs <= 256) return go<E, VW, 8, 32, 32>(p, s);
+      if (runs <= 512) return go<E, VW, 8, 64, 64>(p, s);
+      if (runs <= 1024) return go<E, VW, 8, 128, 128>(p, s);
+      if (runs <= 2048) return go<E, VW, 8, 256, 256>(p, s);
+    }
+  }
   if (runs <= 32) return go<E, VW, 1, 32, 128>(p, s);
   if (runs <= 64) return go<E, VW, 1, 64, 64>(p, s);
   if (runs <= 128) return go<E, VW, 1, 128, 128>(p, s);
@@ -172,8 +181,10 @@ aff_status pick(const NormParams& p, cudaStream_t s) {
   if (runs <= 1024) return go<E, VW, 1, 1024, 1024>(p, s);
   if (runs <= 2048) return go<E, VW, 2, 1024, 1024>(p, s);
   if (runs <= 4096) return go<E, VW, 4, 1024, 1024>(p, s);
-  if constexpr (VW == 1) {
+  if constexpr (VW <= 2) {
     if (runs <= 8192) return go<E, VW, 8, 1024, 1024>(p, s);
+  }
+  if constexpr (VW == 1) {
     if (runs <= 16384) return go<E, VW, 16, 1024, 1024>(p, s);
   }
   return AFF_ERR_UNSUPPORTED_SHAPE;
@@ -213,8 +224,10 @@ extern "C" aff_status affinity_block_norm(const aff_block_norm* a, aff_stream_t 
   p.scale = a->scale;
   p.eps = a->eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // 16-byte runs where every row starts on one; single elements otherwise (odd widths or strides)
-  const bool wide = (a->D * es) % 16 == 0 && (strides * es) % 16 == 0;
-  if (a->dtype == AFF_BF16) return wide ? pick<__nv_bfloat16, 8>(p, s) : pick<__nv_bfloat16, 1>(p, s);
-  return wide ? pick<float, 4>(p, s) : pick<float, 1>(p, s);
+  // 16-byte runs where every row starts on one, else pairs, else single elements
+  const int64_t together = a->D | strides;
+  const bool wide = together * es % 16 == 0, pairs = together % 2 == 0;
+  if (a->dtype == AFF_BF16)
+    return wide ? pick<__nv_bfloat16, 8>(p, s) : pairs ? pick<__nv_bfloat16, 2>(p, s) : pick<__nv_bfloat16, 1>(p, s);
+  return wide ? pick<float, 4>(p, s) : pairs ? pick<float, 2>(p, s) : pick<float, 1>(p, s);
 }
