@@ -73,7 +73,7 @@ struct AttnParams {
   int32_t q_boxes;          // a row tile of queries is one TMA box per half: R divides 128 (map_q)
   int32_t out_boxes;        // a warp's 32 rows of the output are one box per half: R divides 32 (map_out)
   int32_t whole_rows;       // few-rows tiles: a box holds both halves (d_head 128; few_k, few_v)
-  const float *kc, *vc;     // the pools, read by the fp32 kernel (the bf16 kernel has tensor maps)
+  const float *kc, *vc;     // the pools as the fp32 kernel reads them (the bf16 kernel has tensor maps)
   int64_t page_stride, group_stride, token_stride;
 };
 
@@ -92,8 +92,10 @@ struct alignas(16) Bars {
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
   uint64_t stat_full[2], stat_empty[2], few, few_read, drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];           // row0 < 0: no more
+  int slot_item[kSlots];                       // their numbers
   uint32_t tmem;
   int abort_flag;
+  int put_back;                                // at the end: this CTA is the last and items are marked
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: the probabilities stay in tensor memory.
@@ -247,6 +249,87 @@ __device__ __forceinline__ bool slot_wait(Bars* b, int k) {
 __device__ __forceinline__ void slot_done(Bars* b, int k) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&b->slot_empty[k % kSlots]);
+}
+
+// Infinite and NaN values of keys that only some rows of an item see.  A product over the tile would carry
+// 0 * inf = NaN to the rows that do not see them, so they are taken out of the tile (bf16 pairs whose exponent is
+// all ones become 0) and the item is marked; add_specials puts them back for the rows that do.
+constexpr int kItemSpecials = 4;                // in WorkItem::alt, in the plan
+
+__device__ __forceinline__ void without_specials(uint4& w) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = ((x[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    x[i] &= ~((top >> 15) * 0xffffu);
+  }
+}
+// sum + 0 x, both halves
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(sum));
+  return d;
+}
+
+// Own keys below this are seen by every row of the item (its first row sees the fewest).
+__device__ __forceinline__ int all_see(const WorkItem& it, const StepGeom& g) {
+  return it.seq < 0 ? INT32_MAX : g.by_R(it.row0) + it.own_off + 1;
+}
+
+// For the marked items, with every output written: adds the values that are not finite to the rows that see
+// their keys.  A probability is never 0, so such a value makes the sum inf or NaN whatever else is in it.
+// One CTA, its first eight warps: a rare case, and bounded by the items' masked keys.
+__device__ __noinline__ void add_specials(const AttnParams& p, const uint16_t* v_pool, int n_items) {
+  const StepGeom& g = p.g;
+  const int warp = threadIdx.x >> 5, c = (threadIdx.x & 31) * 4;
+#pragma unroll 1
+  for (int i = 0; i < n_items; ++i) {
+    const WorkItem it = load_item(g.items + i);
+    if (!(it.alt & kItemSpecials)) continue;
+    const int from = all_see(it, g), alt = it.alt & ~kItemSpecials;
+    const int n = alt ? it.n0 + it.n1 : it.n1 > it.n0 ? it.n1 : it.n0;
+#pragma unroll 1
+    for (int r = warp; r < it.nrows; r += 8) {
+      const int rr = it.row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+      float add[4] = {0.f, 0.f, 0.f, 0.f};
+      bool any = false;
+#pragma unroll 1
+      for (int u = max(it.np - it.t0, 0); u < n; ++u) {
+        int key0;
+        const int keys = tile_keys(it, g, it.t0 + u, &key0);
+        const int end = min(key0 + keys, tok + it.own_off + 1);
+#pragma unroll 1
+        for (int key = max(key0, from); key < end; ++key) {
+          const int pi = g.by_page(key), page = g.pages[(int64_t)it.seq * g.pages_stride + pi];
+          if (page < 0 || page >= g.n_pages || c >= g.d) continue;
+          const uint2 w = *reinterpret_cast<const uint2*>(v_pool + page * p.page_stride + it.group * p.group_stride +
+                                                          (int64_t)(key - pi * g.page_size) * p.token_stride + c);
+          const uint32_t x[4] = {w.x << 16, w.x & 0xffff0000u, w.y << 16, w.y & 0xffff0000u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((x[e] & 0x7f800000u) == 0x7f800000u) {
+              add[e] += __uint_as_float(x[e]);
+              any = true;
+            }
+        }
+      }
+      if (!any) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (add[e] == 0.f) continue;               // not NaN, not inf
+        if (it.part_row >= 0) {
+          g.part_out[(int64_t)(it.part_row + r) * g.d + c + e] += add[e];
+        } else {
+          __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)tok * g.H + h) * g.d + c + e;
+          *at = __float2bfloat16_rn(__bfloat162float(*at) + add[e]);
+        }
+      }
+    }
+  }
+  // taken back for the next call
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+  for (int i = threadIdx.x; i < n_items; i += 256) g.items[i].alt &= ~kItemSpecials;
+  if (threadIdx.x == 0) g.head->specials = 0;
 }
 
 // One lane of the (converged) warp, always the same one.
@@ -712,6 +795,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
       if (lane < (int)(sizeof(WorkItem) / 4))
         d[lane] = item < n_items ? reinterpret_cast<const int*>(g.items + item)[lane] : -1;
+      if (lane == 0) bars->slot_item[k % kSlots] = item;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
     };
@@ -893,9 +977,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     Ring r, turn[3];
     for (int k = 0; slot_wait(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      const int number = bars->slot_item[k % kSlots];
       slot_done(bars, k);
       const bool few = FEW && it.alt == 2;
-      const int n = item_tiles(it);
+      const int n = item_tiles(it), seen_by_all = all_see(it, g);
 #pragma unroll 1
       for (int u = 0; u < n; ++u) {
         int key0;
@@ -904,6 +989,50 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll 1
         for (int value = 0; value < 2; ++value) {
           wait_on(&bars->kv_full[r.s], r.ph, bars);
+          if (value && it.t0 + u >= it.np && key0 + keys > seen_by_all) {
+            // rows that some query row does not see: 16 rows of 128 bytes at a time, each lane's eight pieces in
+            // an order of its own so that no two lanes meet in a bank.  0 * x summed over everything is NaN if
+            // anything is not finite (a fused multiply-add per pair); only then are they looked for.
+            const int h = lane & 1, from = max(seen_by_all - key0, 0) + (lane >> 1);
+            auto row_at = [&](int key) {
+              return smem_u32(kv_smem) + r.s * tile_bytes + (few ? few_row(p, key) : key * 128) +
+                     h * (few ? p.box * 128 : kHalfBytes);
+            };
+            uint32_t sum[4] = {0u, 0u, 0u, 0u};
+            if (h < p.halves) {
+#pragma unroll 1
+              for (int key = from; key < keys; key += 16) {
+                const uint32_t at = row_at(key);
+                uint4 w[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) w[q] = ld_shared16(at + ((q ^ (lane & 7)) << 4));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  sum[0] = add_zero_times(w[q].x, sum[0]);
+                  sum[1] = add_zero_times(w[q].y, sum[1]);
+                  sum[2] = add_zero_times(w[q].z, sum[2]);
+                  sum[3] = add_zero_times(w[q].w, sum[3]);
+                }
+              }
+            }
+            bool found = ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0;
+            if (__any_sync(0xffffffffu, found)) {
+#pragma unroll 1
+              for (int key = from; key < keys && h < p.halves; key += 16)
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                  const uint32_t piece = row_at(key) + q * 16;
+                  uint4 w = ld_shared16(piece);
+                  without_specials(w);
+                  st_shared16(piece, w);
+                }
+              fence_async_smem();
+              if (lane == 0) {
+                atomicOr(&g.items[number].alt, kItemSpecials);
+                atomicExch(&g.head->specials, 1);
+              }
+            }
+          }
           if (value && keys < to) {
             // rows keys .. the next multiple of 16, one half of one row for each lane: whole 128-byte rows,
             // so the swizzle does not matter
@@ -1206,15 +1335,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   }
   if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
+  if (threadIdx.x == 0) bars->put_back = 0;
   if (fits && threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(&g.head->done, 1u) == gridDim.x - 1) {
+      __threadfence();
+      bars->put_back = *reinterpret_cast<volatile int32_t*>(&g.head->specials);
       g.head->claimed = 0;
       g.head->done = 0;
     }
   }
+  __syncthreads();
+  if (bars->put_back && warp < 8) add_specials(p, reinterpret_cast<const uint16_t*>(p.vc), n_items);
 }
-
 
 template <int NK, bool FEW>
 aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsigned grid, int smem,

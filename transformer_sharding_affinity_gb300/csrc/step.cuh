@@ -83,7 +83,8 @@ struct PlanHeader {      // at the start of the plan buffer; its first word is t
   int32_t unit;          // most cost (key tiles x streams) of an item; 0: jobs are not cut
   int32_t prefix_parts;  // separate: parts of each prefix job
   int32_t prefix_per;    // separate: key tiles of each part
-  int32_t pad[3];
+  int32_t specials;      // a call under way has marked items (attention.cu); 0 between calls
+  int32_t pad[2];
   uint32_t key[4];       // a hash of the geometry it was made for
   uint32_t claimed;      // items claimed beyond the first of every CTA, and CTAs done, in the call
   uint32_t done;         // under way; the last CTA sets both back to 0
