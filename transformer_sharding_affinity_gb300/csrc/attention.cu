@@ -251,6 +251,15 @@ __device__ __forceinline__ void slot_done(Bars* b, int k) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(&b->slot_empty[k % kSlots]);
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 // Infinite and NaN values of keys that only some rows of an item see.  A product over the tile would carry
 // 0 * inf = NaN to the rows that do not see them, so they are taken out of the tile (bf16 pairs whose exponent is
 // all ones become 0) and the item is marked; add_specials puts them back for the rows that do.
@@ -262,6 +271,15 @@ __device__ __forceinline__ void without_specials(uint4& w) {
   for (int i = 0; i < 4; ++i) {
     const uint32_t top = ((x[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
     x[i] &= ~((top >> 15) * 0xffffu);
+  }
+}
+// 128 bytes of shared memory; out of line, so that the code of the roles stays together
+__device__ __noinline__ void clean_row(uint32_t at) {
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint4 w = ld_shared16(at + q * 16);
+    without_specials(w);
+    st_shared16(at + q * 16, w);
   }
 }
 // sum + 0 x, both halves
@@ -437,15 +455,6 @@ __device__ __forceinline__ void copy_queries(const AttnParams& p, const uint16_t
 
 // 16 bytes to / from row `row` of a warp's 32 x 128-byte staging block, in place c of 8.
 __device__ __forceinline__ uint32_t stage_at(uint32_t base, int row, int c) { return base + row * 128 + ((c ^ (row & 7)) << 4); }
-__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t at, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -1000,7 +1009,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             };
             uint32_t sum[4] = {0u, 0u, 0u, 0u};
             if (h < p.halves) {
-#pragma unroll 1
+#pragma unroll 2
               for (int key = from; key < keys; key += 16) {
                 const uint32_t at = row_at(key);
                 uint4 w[8];
@@ -1018,14 +1027,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             bool found = ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0;
             if (__any_sync(0xffffffffu, found)) {
 #pragma unroll 1
-              for (int key = from; key < keys && h < p.halves; key += 16)
-#pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                  const uint32_t piece = row_at(key) + q * 16;
-                  uint4 w = ld_shared16(piece);
-                  without_specials(w);
-                  st_shared16(piece, w);
-                }
+              for (int key = from; key < keys && h < p.halves; key += 16) clean_row(row_at(key));
               fence_async_smem();
               if (lane == 0) {
                 atomicOr(&g.items[number].alt, kItemSpecials);
