@@ -553,8 +553,9 @@ AFF_API aff_status affinity_kv_append(const void* q, int64_t q_stride, const voi
  * h / (H/G).  lse[t, h] (fp32, may be NULL) is the log of the softmax's
  * denominator, sum_j exp(scale q.k_j).  A row without keys (padding) is 0, its
  * lse -inf.  q [T, H*d_head] with rows q_stride apart, out [T, H*d_head] dense.
- * Keys past a sequence's own are not read into any sum, whatever the pool holds
- * there.  scale must be positive.  AFF_BF16: fp32 scores, sums and softmax,
+ * What a row does not see (keys past a sequence's own, later tokens of its
+ * sequence) does not reach it, infinite or NaN as it may be; an infinite or NaN
+ * value of a key that it sees does.  scale must be positive.  AFF_BF16: fp32 scores, sums and softmax,
  * probabilities rounded to bf16 for the second product.  AFF_FP32: fp32
  * throughout on the CUDA cores (meant for small shapes).
  */
