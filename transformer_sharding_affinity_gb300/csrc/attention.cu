@@ -1384,7 +1384,9 @@ aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsi
 constexpr int kF32Threads = 256;
 constexpr int kF32Keys = 64;                 // keys of a step of the tiled path
 constexpr int kF32Rows = 64;                 // its rows
-constexpr int kF32Few = 32;                  // most rows of the streaming path
+// Most rows of the streaming path.  Up to 32: 5 x 256 tokens of 16-wide heads 39 us instead of 25, 4 x 6 tokens
+// behind 3889 keys 163 instead of 119; 47 x 10 tokens x 307 keys 175 instead of 192.
+constexpr int kF32Few = 16;
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
@@ -1626,7 +1628,7 @@ __device__ void f32_tile(const AttnParams& p, const WorkItem& it, float* smem) {
   }
 }
 
-// Up to 32 rows: bound by the cache's bytes.  A warp takes NR rows (1, 2, 4) and every n-th run of eight keys, straight
+// Up to 16 rows: bound by the cache's bytes.  A warp takes NR rows (1, 2, 4) and every n-th run of eight keys, straight
 // from global memory to registers (a key's row is one load of the warp, 4 columns to a lane); warps with other
 // rows of the same keys find them in the first cache.  The 8 NR dot products of a run are summed over the lanes
 // by halving: 31 shuffles for four rows leave lane 8 r + k with the score of row r and key k (4 / NR lanes each).  A warp's running maximum and
@@ -1636,7 +1638,7 @@ __device__ void f32_few(const AttnParams& p, const WorkItem& it, float* smem) {
   const StepGeom& g = p.g;
   const int d = g.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int S = NR == 1 ? 2 : NR == 2 ? 1 : 0;                      // a score lies in 2^S neighbouring lanes
-  const int blocks = it.nrows <= NR ? 1 : it.nrows <= 8 ? 2 : it.nrows <= 16 ? 4 : 8;       // of NR rows; warp % blocks takes one
+  const int blocks = it.nrows <= NR ? 1 : it.nrows <= 8 ? 2 : 4;       // of NR rows; warp % blocks takes one
   const int r0 = (warp % blocks) * NR, stride = 8 / blocks;
   const int kk = (lane >> S) & 7;
   const int c = 4 * lane;

@@ -424,7 +424,7 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     g.key[i] = (uint32_t)(h >> 16);
   }
   const bool bf = c->dtype == AFF_BF16;
-  g.small = bf ? 128 : 32;
+  g.small = bf ? 128 : 16;
   g.big = bf ? 256 : 64;
   const int64_t rows = (int64_t)g.T * g.R;
   // Jobs of its own for the prefix: worth it while sequences have few rows, so that a
