@@ -87,6 +87,17 @@ def test_keys_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, q_len
     _check(case)
 
 
+@pytest.mark.parametrize("heads", [(8, 4, 128), (4, 2, 96), (5, 5, 72), (4, 2, 64)])
+@pytest.mark.parametrize("page", [8, 24, 40, 64, 104, 128, 136, 200, 256])
+def test_single_tokens_over_pages_that_do_not_fill_a_tile(heads, page):
+    """Several tiles to an item, so that tiles lie next to each other while they are worked on; one to eight tokens."""
+    case = ops.Case(heads, [1, 1, 4, 1, 8, 0, 1], [900, 411, 640, 128, 1300, 50, 24 * 5], 130, page=page, seed=page)
+    first = case.check_attention()
+    for _ in range(4):
+        again = case.check_attention()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64), (8, 1, 80), (5, 5, 72), (4, 4, 16)])
 @pytest.mark.parametrize("q,kv,B_,prefix", [(1, 300, 3, 0), (2, 131, 2, 0), (3, 70, 5, 260), (7, 9, 2, 1), (17, 400, 2, 0),
                                             (40, 41, 3, 130), (70, 70, 1, 0), (131, 200, 2, 64), (9, 9, 9, 500)])

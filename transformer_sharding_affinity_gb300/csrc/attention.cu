@@ -363,10 +363,15 @@ __device__ __forceinline__ int item_tiles(const WorkItem& it) { return it.alt ? 
 // Box of a tile that holds key `key`: its page, or the only one (pages of several tiles).
 __device__ __forceinline__ int box_of(const AttnParams& p, int key) { return p.g.tile_pages ? p.g.by_page(key) : 0; }
 
-// Byte of key `key`'s first half in a few-rows tile.
+// Byte of key `key`'s first half in a few-rows tile, and from there to its second half.  Rows past the boxes' keys
+// (a tile of whole pages may hold fewer than 128) are a box of their own at the tile's end.
 __device__ __forceinline__ uint32_t few_row(const AttnParams& p, int key) {
+  if (key >= p.g.key_tile) return (p.g.key_tile * (p.halves - 1) + key) * 128;
   const int box = box_of(p, key);
   return (box * p.halves * p.box + key - box * p.box) * 128;
+}
+__device__ __forceinline__ uint32_t few_half(const AttnParams& p, int key) {
+  return (key >= p.g.key_tile ? kKeyTile - p.g.key_tile : p.box) * 128;
 }
 
 // Own keys that the last row of stream s sees, and the keys of its tile that it has any use for.
@@ -535,7 +540,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
   // of O^T, transposed: (columns 0-7, 8-15) x (keys 0-7 | 8-15).
   const int kj = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), kc = lane >> 4;
   const int vj = warp * 16 + (lane >> 4) * 8 + (lane & 7), vc = (lane >> 3) & 1;
-  const uint32_t half_step = p.box * 128;
+  const uint32_t k_half = few_half(p, kj), v_half = few_half(p, vj);
   const uint32_t k_at = smem_u32(kv_smem) + few_row(p, kj), v_at = smem_u32(kv_smem) + few_row(p, vj);
   // S^T of the stream's next tile (garbage past the tile's keys: masked afterwards)
   float sc[RN][4];
@@ -553,7 +558,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
 #pragma unroll
       for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
         if (k < nk)
-          ldmatrix4(k_at + rk.s * tile_bytes + (k >> 2) * half_step + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k - k0]);
+          ldmatrix4(k_at + rk.s * tile_bytes + (k >> 2) * k_half + ((((k & 3) * 2 + kc) ^ (kj & 7)) << 4), a[k - k0]);
 #pragma unroll
       for (int k = k0; k < k0 + 4 && k < kSlices; ++k)
 #pragma unroll
@@ -631,7 +636,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, const WorkItem& it
 #pragma unroll
         for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
           if (n < nk)
-            ldmatrix4_t(v_at + rv.s * tile_bytes + (n >> 2) * half_step + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n - n0]);
+            ldmatrix4_t(v_at + rv.s * tile_bytes + (n >> 2) * v_half + ((((n & 3) * 2 + vc) ^ (vj & 7)) << 4), a[n - n0]);
 #pragma unroll
         for (int n = n0; n < n0 + 4 && n < kSlices; ++n)
 #pragma unroll
@@ -1005,7 +1010,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int h = lane & 1, from = max(seen_by_all - key0, 0) + (lane >> 1);
             auto row_at = [&](int key) {
               return smem_u32(kv_smem) + r.s * tile_bytes + (few ? few_row(p, key) : key * 128) +
-                     h * (few ? p.box * 128 : kHalfBytes);
+                     h * (few ? few_half(p, key) : kHalfBytes);
             };
             uint32_t sum[4] = {0u, 0u, 0u, 0u};
             if (h < p.halves) {
@@ -1041,7 +1046,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int key = keys + (lane >> 1), h = lane & 1;
             if (key < to && h < p.halves) {
               uint4* at = reinterpret_cast<uint4*>(kv_smem + r.s * tile_bytes + (few ? few_row(p, key) : key * 128) +
-                                                   h * (few ? p.box * 128 : kHalfBytes));
+                                                   h * (few ? few_half(p, key) : kHalfBytes));
 #pragma unroll 1
               for (int q = 0; q < 8; ++q) at[q] = make_uint4(0, 0, 0, 0);
             }
