@@ -9,24 +9,44 @@
 //
 // bf16: attention_kernel, persistent, one CTA per SM, on the tensor cores.
 //   A work item (step.cuh) is up to 256 packed rows against a run of 128-key
-//   tiles.  Two streams alternate on the tensor core: while the threads of one
-//   turn its scores S into probabilities P, the products of the other run.
+//   tiles; CTAs claim them from a counter.  Two streams of 128 rows alternate on
+//   the tensor core, each with two score buffers of half a tile: while the threads
+//   of one half turn its scores S into probabilities P, other products run.
 //     warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
-//     warp 8           TMA: query rows; key and value tiles through the page tables
+//     warp 8           claims items; TMA: query rows, key and value tiles through
+//                      the page tables
 //     warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from
 //                      shared memory) and O += P V (P from tensor memory)
-//     warp 11          clears the rows of a value tile past its keys: 0 * NaN would stay
+//     warp 11          passes tiles on; clears the rows of a value tile past its keys
+//                      and takes out infinite and NaN values of keys that some row
+//                      does not see: 0 * NaN would stay
 //     warps 12-15      output, while the softmax goes on to the next item
 //   Tensor memory: S of both streams (128 columns each, as two buffers of half a
 //   tile's 64 keys; P overlays the first half of its buffer), O of both (128
 //   columns each).
 //   Items of at most 16 rows leave the tensor tiles aside: few_rows.
+//   All roles' code together has to stay in the instruction cache (128 KB): at
+//   126-234 KB it was what bounded the kernel (64 x 1024 tokens of 16 / 8 heads of
+//   128: 453 us; 296 at 65 KB).  Hence the unrolling that is not done.
+//   What bounds it now, on sizes of 128-wide heads:
+//     one prompt of 8192 tokens, 32 heads: 350 us, 1.57 PFLOP/s, 84 % of the measured
+//       rate: the tensor core, with the softmax's exponentials close behind;
+//     64 prompts of 1024, 16 heads: 280 us, 0.98 PFLOP/s: items of 1 to 8 tiles, of
+//       which one is half past the diagonal, and their beginnings and ends;
+//     64 tokens against 8192 keys each: 336 us, 6.4 TB/s, 94 % of the measured copy;
+//     256 tokens behind a prefix of 32768 with 1024 own keys: 291 us, 4.1 TB/s and
+//       0.47 PFLOP/s: the prefix's items bound by the tensor core, the others by bytes;
+//     64 tokens behind 8192 with 750 own keys: 69 us, 3.3 TB/s: the items' latencies
+//       and the join (8 us).
 //   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
 //   when m has grown by more than 8 (in log2): until then p <= 2^8, far inside
 //   fp32 and bf16.  P is rounded to bf16, the type of V (a product's operands
 //   share it): one more rounding of at most 2^-8 per probability, unbiased and averaged
 //   over the keys; l sums the unrounded p.
-// fp32: attention_f32_kernel, CUDA cores, for small shapes.
+// fp32: attention_f32_kernel, CUDA cores, for small shapes: 26 prompts of 294 tokens
+// behind 158, 700 us, 27 TFLOP/s of the cores' 74: shared-memory loads (2.8 cycles of
+// the pipe for each) and four barriers a step, beside the products.  64 tokens x 1000
+// keys of 8 heads, 156 us, 3.4 TB/s: a warp's loads wait for its page look-up.
 // Rows in several parts are merged by join_kernel from fp32 partial rows.
 #include "affinity.h"
 #include "internal.h"

@@ -7,7 +7,10 @@
 //   pair (a, b) of z -> (a cos - b sin, a sin + b cos)  at position prefix + own index
 //
 // Memory bound: T (H + 2G) d elements in and out, nothing reused but the cosine
-// and sine row of a token, which its H + G rows share through L1.  A row is held
+// and sine row of a token, which its H + G rows share through L1.  65536 tokens of
+// 16 + 2 x 8 heads of 128 in bf16 with norms: 188 us, 5.7 TB/s, 84 % of the measured
+// copy; 22681 ragged tokens of 96-wide fp32 heads: 32 us, 5.4 TB/s; a step of eight
+// tokens: 8 us, the launch.  A row is held
 // by `lanes` neighbouring lanes (a power of two), each with both halves of its
 // pairs, so that the rotation needs no exchange and the norm only a shuffle sum.
 #include "affinity.h"

@@ -1,5 +1,8 @@
 // step_plan.cu -- affinity_step_plan: one launch that writes a step's plan
 // (step.cuh).  Block 0 cuts the jobs; the other blocks fill the token table.
+// Once a step, not once a layer, and bound by latency: block 0's passes over the
+// sequences (kept in shared memory) and the items' stores.  1 sequence 13 us, 64
+// sequences 18 us, 256 sequences 27 us.
 #include "affinity.h"
 #include "internal.h"
 #include "launch.cuh"
@@ -15,7 +18,9 @@ namespace aff {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kItemsPerSm = 4;    // items that a cut of unequal jobs aims at for each SM
+// Items that a cut of unequal jobs aims at for each SM (64 single tokens of ragged sequences behind 8192 keys:
+// 74 us with 2, 70 with 4 and 8).
+constexpr int kItemsPerSm = 4;
 constexpr int kMinUnit = 4;       // least cost of an item then
 constexpr int kMaxParts = 64;     // most parts that equal jobs are cut into
 
@@ -155,7 +160,7 @@ __device__ void plan_items(const StepGeom& g) {
     // fp32: two CTAs per SM, tiles that take some four times as long
     const bool f32 = g.dtype != AFF_BF16;
     const int slots = f32 ? 2 * kPlanSms : kPlanSms, tile = f32 ? 4 : 1;
-    const int start = g.few ? 2 : 5;               // an item's beginning and end, in the cost of a bf16 tile
+    const int start = g.few ? 2 : 5;      // an item's beginning and end, in the cost of a bf16 tile
     if (warp < 2) {                                // warp 0: own jobs, warp 1: the prefix's
       // half of the room for cuts (a row tile for every SM and stream) each
       const int64_t row_jobs = (warp ? (int64_t)g.prefix_tiles * g.prefix_rows : rows_all) * g.G;     // rows of a part
@@ -427,18 +432,21 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   g.small = bf ? 128 : 16;
   g.big = bf ? 256 : 64;
   const int64_t rows = (int64_t)g.T * g.R;
-  // Jobs of its own for the prefix: worth it while sequences have few rows, so that a
-  // row tile of one sequence would leave most of a tile idle for every key of the prefix.
+  // Jobs of its own for the prefix: worth it while sequences have less than a row tile on average, which
+  // would then be mostly idle for every key of the prefix (64 single tokens behind 8192 keys: 69 us, 359
+  // without; 16 x 50 tokens, 100 rows each, behind 4000: 67 and 100; 64 x 33 behind 2000: 95 and 223; fp32,
+  // 17 x 30 tokens behind 2145: 328 and 369).
   g.separate = g.prefix_len > 0 && g.B > 1 && rows < (int64_t)g.B * (bf ? g.small : g.big);
-  // The few-rows path where sequences have few rows on average: the kernel without it is faster.
-  g.few = bf && rows <= (int64_t)g.B * 64;
+  // The few-rows path where sequences have few rows on average (64 single tokens: 69 us, 98 without); the kernel
+  // without it is faster (64 x 1024 tokens: 280 us, 338 with it; 8 x 17 tokens, 34 rows each: 51 and 53).
+  g.few = bf && rows <= (int64_t)g.B * 32;
   g.prefix_rows = rows <= g.small ? g.small : g.big;
   g.prefix_tiles = g.separate ? (int)((rows + g.prefix_rows - 1) / g.prefix_rows) : 0;
   // Most (row tile, group) pairs: each sequence ends in at most one part-filled tile.
   const int64_t tiles = rows / g.big + g.B + 1;
   const int64_t jobs = (tiles + g.prefix_tiles) * g.G;
   const int64_t full = rows / g.big * g.G;
-  g.may_split = g.separate || full < (bf ? 2 : 8) * kPlanSms;
+  g.may_split = g.separate || full < 2 * kPlanSms;
   const int64_t items = 2 * jobs + (int64_t)kPlanSms * 2 * kItemsPerSm + 2 * g.G + 64;
   int64_t part_rows = 0;
   if (g.may_split) {
