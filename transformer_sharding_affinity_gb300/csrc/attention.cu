@@ -1874,34 +1874,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   }
   const int n = n_pre + n_own;
   auto row_of = [&](int i) { return i < n_pre ? pre0 + i * pre_step : own0 + (i - n_pre) * own_step; };
+  // eight parts' rows in flight, the first of them beside their log-sum-exps; an empty part's row is not used
+  float4 v[8];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      v[x] = i0 + x < n && 4 * lane < g.d ? *reinterpret_cast<const float4*>(g.part_out + (int64_t)row_of(i0 + x) * g.d + 4 * lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(0);
   float mx = -INFINITY;
   for (int i = lane; i < n; i += 32) mx = fmaxf(mx, g.part_lse[row_of(i)]);
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const float w_mine = i0 + lane < n ? expf(g.part_lse[row_of(i0 + lane)] - ref) : 0.f;
-    const int upto = min(32, n - i0);
-    for (int i = 0; i < upto; i += 4) {          // four parts' loads in flight; an empty part's row is not used
-      float w[4];
-      float4 v[4];
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    if (i0 > 0) fetch(i0);
+    const float w_mine = lane < 8 && i0 + lane < n ? expf(g.part_lse[row_of(i0 + lane)] - ref) : 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        w[x] = i + x < upto ? __shfl_sync(0xffffffffu, w_mine, (i + x) & 31) : 0.f;
-        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w[x] != 0.f && 4 * lane < g.d)
-          v[x] = *reinterpret_cast<const float4*>(g.part_out + (int64_t)row_of(i0 + i + x) * g.d + 4 * lane);
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (w[x] == 0.f) continue;
-        sum += w[x];
-        acc.x += w[x] * v[x].x;
-        acc.y += w[x] * v[x].y;
-        acc.z += w[x] * v[x].z;
-        acc.w += w[x] * v[x].w;
-      }
+    for (int x = 0; x < 8; ++x) {
+      const float w = __shfl_sync(0xffffffffu, w_mine, x);
+      if (w == 0.f) continue;
+      sum += w;
+      acc.x += w * v[x].x;
+      acc.y += w * v[x].y;
+      acc.z += w * v[x].z;
+      acc.w += w * v[x].w;
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
