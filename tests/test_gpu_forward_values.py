@@ -76,6 +76,22 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, hea
     assert torch.equal(first.isnan(), again.isnan()) and torch.equal(first.nan_to_num(), again.nan_to_num())
 
 
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_many_items_with_values_that_are_not_finite(prefix):
+    """Every CTA has several items to put back; a call over finite values on the same plan afterwards."""
+    n = 90
+    lens = [(64, 5, 130, 20)[i % 4] for i in range(n)]
+    case = ops.Case((4, 4, 64), lens, [k + 9 * (i % 3) for i, k in enumerate(lens)], prefix, seed=43)
+    clean = (case.v.clone(), case.vd.clone())
+    for b in range(n):
+        _put(case, case.v, case.vd, b, case.kv_lens[b] - 2, math.inf, col=b % 64)
+        _put(case, case.v, case.vd, b, case.kv_lens[b] - 1, math.nan, col=(b + 7) % 64)
+    _check(case)
+    case.v.copy_(clean[0])
+    case.vd.copy_(clean[1])
+    case.check_attention()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("q_lens,kv_lens,prefix", STEPS)
 def test_keys_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, q_lens, kv_lens, prefix):

@@ -115,7 +115,7 @@ struct alignas(16) Bars {
   int slot_item[kSlots];                       // their numbers
   uint32_t tmem;
   int abort_flag;
-  int put_back;                                // at the end: this CTA is the last and items are marked
+  int marked;                                  // items of this CTA are marked (add_specials)
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: the probabilities stay in tensor memory.
@@ -283,7 +283,9 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
 // Infinite and NaN values of keys that only some rows of an item see.  A product over the tile would carry
 // 0 * inf = NaN to the rows that do not see them, so they are taken out of the tile (bf16 pairs whose exponent is
 // all ones become 0) and the item is marked; add_specials puts them back for the rows that do.
-constexpr int kItemSpecials = 4;                // in WorkItem::alt, in the plan
+// The mark, in the plan's copy of WorkItem::alt, is the CTA that has the item.
+constexpr int kMarkShift = 8;
+__device__ __forceinline__ int item_mark() { return (int)(blockIdx.x + 1) << kMarkShift; }
 
 __device__ __forceinline__ void without_specials(uint4& w) {
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
@@ -314,17 +316,18 @@ __device__ __forceinline__ int all_see(const WorkItem& it, const StepGeom& g) {
   return it.seq < 0 ? INT32_MAX : g.by_R(it.row0) + it.own_off + 1;
 }
 
-// For the marked items, with every output written: adds the values that are not finite to the rows that see
-// their keys.  A probability is never 0, so such a value makes the sum inf or NaN whatever else is in it.
-// One CTA, its first eight warps: a rare case, and bounded by the items' masked keys.
+// For the items that this CTA has marked, with all its outputs written: adds the values that are not finite to
+// the rows that see their keys.  A probability is never 0, so such a value makes the sum inf or NaN whatever else
+// is in it.  The first eight warps; a rare case, and bounded by the items' masked keys.
 __device__ __noinline__ void add_specials(const AttnParams& p, const uint16_t* v_pool, int n_items) {
   const StepGeom& g = p.g;
   const int warp = threadIdx.x >> 5, c = (threadIdx.x & 31) * 4;
 #pragma unroll 1
   for (int i = 0; i < n_items; ++i) {
+    const int marked = *reinterpret_cast<const volatile int32_t*>(&g.items[i].alt);
+    if (marked >> kMarkShift != (int)blockIdx.x + 1) continue;
     const WorkItem it = load_item(g.items + i);
-    if (!(it.alt & kItemSpecials)) continue;
-    const int from = all_see(it, g), alt = it.alt & ~kItemSpecials;
+    const int from = all_see(it, g), alt = marked & ((1 << kMarkShift) - 1);
     const int n = alt ? it.n0 + it.n1 : it.n1 > it.n0 ? it.n1 : it.n0;
 #pragma unroll 1
     for (int r = warp; r < it.nrows; r += 8) {
@@ -366,8 +369,10 @@ __device__ __noinline__ void add_specials(const AttnParams& p, const uint16_t* v
   }
   // taken back for the next call
   asm volatile("bar.sync 1, 256;" ::: "memory");
-  for (int i = threadIdx.x; i < n_items; i += 256) g.items[i].alt &= ~kItemSpecials;
-  if (threadIdx.x == 0) g.head->specials = 0;
+  for (int i = threadIdx.x; i < n_items; i += 256) {
+    volatile int32_t* alt = &g.items[i].alt;     // not from the first cache: warp 11 has changed it since
+    if (*alt >> kMarkShift == (int)blockIdx.x + 1) *alt = *alt & ((1 << kMarkShift) - 1);
+  }
 }
 
 // One lane of the (converged) warp, always the same one.
@@ -792,6 +797,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     mbar_init(&bars->few, 8);
     mbar_init(&bars->few_read, 4);
     bars->abort_flag = 0;
+    bars->marked = 0;
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -1055,8 +1061,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
               for (int key = from; key < keys && h < p.halves; key += 16) clean_row(row_at(key));
               fence_async_smem();
               if (lane == 0) {
-                atomicOr(&g.items[number].alt, kItemSpecials);
-                atomicExch(&g.head->specials, 1);
+                atomicOr(&g.items[number].alt, item_mark());
+                bars->marked = 1;
               }
             }
           }
@@ -1362,18 +1368,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   }
   if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
-  if (threadIdx.x == 0) bars->put_back = 0;
   if (fits && threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(&g.head->done, 1u) == gridDim.x - 1) {
-      __threadfence();
-      bars->put_back = *reinterpret_cast<volatile int32_t*>(&g.head->specials);
       g.head->claimed = 0;
       g.head->done = 0;
     }
   }
-  __syncthreads();
-  if (bars->put_back && warp < 8) add_specials(p, reinterpret_cast<const uint16_t*>(p.vc), n_items);
+  if (bars->marked && warp < 8) add_specials(p, reinterpret_cast<const uint16_t*>(p.vc), n_items);
 }
 
 template <int NK, bool FEW>

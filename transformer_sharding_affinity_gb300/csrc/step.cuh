@@ -76,6 +76,7 @@ struct WorkItem {        // 48 bytes
 // alt == 0: stream s holds rows s*128 .. of the item and walks tiles t0 .. t0 + n_s - 1.
 // alt == 1: at most 128 rows; both streams hold them, stream s walks tiles t0 + s, t0 + s + 2, ...
 // alt == 2: at most 16 rows, for which a tile is split over warps by its keys; n0 tiles.
+// Its higher bits are 0 but for a call under way (attention.cu).
 
 struct PlanHeader {      // at the start of the plan buffer; its first word is the status word
   uint32_t status;
@@ -83,8 +84,7 @@ struct PlanHeader {      // at the start of the plan buffer; its first word is t
   int32_t unit;          // most cost (key tiles x streams) of an item; 0: jobs are not cut
   int32_t prefix_parts;  // separate: parts of each prefix job
   int32_t prefix_per;    // separate: key tiles of each part
-  int32_t specials;      // a call under way has marked items (attention.cu); 0 between calls
-  int32_t pad[2];
+  int32_t pad[3];
   uint32_t key[4];       // a hash of the geometry it was made for
   uint32_t claimed;      // items claimed beyond the first of every CTA, and CTAs done, in the call
   uint32_t done;         // under way; the last CTA sets both back to 0
