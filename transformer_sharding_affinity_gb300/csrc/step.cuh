@@ -64,7 +64,7 @@ struct TokenInfo {       // one per token of the step; 16 bytes
 struct SeqInfo {         // one per sequence, for the join: what the plan was made from; 32 bytes
   int32_t q0, q1, kv;    // its tokens of the step, its own keys
   int32_t part_row;      // first partial row
-  int32_t parts;         // partial rows' stride in parts: the most parts a tile of its rows has
+  int32_t parts;         // partial rows' stride in parts: those of its last row tile, which has the most keys
   int32_t reserved[3];
 };
 
@@ -174,12 +174,16 @@ __device__ __forceinline__ int key_tiles(const StepGeom& g, const SeqShape& s, i
   return v == 0 ? 0 : segment_tiles(g, v) + (g.separate ? 0 : g.np);
 }
 
-// Parts of a job of `tiles` key tiles, `streams` row tiles at a time, and the key tiles of each.
+// Parts of a job of `tiles` key tiles, `streams` row tiles at a time, and the key tiles of each.  `unit` counts in
+// whole tiles, rounded up: the parts then never grow fewer as a job grows, which SeqInfo::parts rests on (a bound of
+// unit / streams tiles that is no whole number gives 4 parts of 8 tiles and 3 of 9).
 __device__ __forceinline__ int job_parts(int tiles, int streams, int unit, int* per) {
-  int parts = unit > 0 && tiles > 0 ? (tiles * streams + unit - 1) / unit : 1;
-  if (parts > tiles) parts = tiles > 0 ? tiles : 1;
-  *per = tiles > 0 ? (tiles + parts - 1) / parts : 0;
-  return *per > 0 ? (tiles + *per - 1) / *per : 1;
+  *per = tiles;
+  if (unit <= 0 || tiles <= 0) return 1;
+  const int most = (unit + streams - 1) / streams;
+  const int parts = (tiles + most - 1) / most;
+  *per = (tiles + parts - 1) / parts;            // at most `most`, so these parts are needed: no fewer cover the tiles
+  return parts;
 }
 
 __device__ __forceinline__ bool plan_matches(const StepGeom& g) {
