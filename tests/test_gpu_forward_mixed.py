@@ -156,3 +156,21 @@ def test_more_sequences_than_the_planner_holds_at_a_time(n, prefix):
     c = Mixed((4, 2, 64), q, kv, prefix, 16, seed=53)
     c.check_items()
     c.check_attention()
+
+
+@pytest.mark.parametrize("heads", [(4, 4, 128), (8, 4, 64), (4, 2, 96)])
+def test_items_of_output_rows_before_items_of_partial_rows(heads):
+    """Every CTA goes from items that write whole output rows, by bulk copies, to items that write partial rows from
+    the same staging buffer, and back; short items, so that the one follows close behind the other."""
+    R = heads[0] // heads[1]
+    q = [128 // R if i % 3 else 20 for i in range(180)]
+    kv = [n if i % 3 else 9000 - 17 * i for i, n in enumerate(q)]
+    c = Mixed(heads, q, kv, 0, 64, seed=54)
+    c.check_items()
+    kinds = [i[7] >= 0 for i in c.items().tolist()]
+    assert 100 < sum(kinds) < len(kinds) - 100
+    first = c.check_attention()
+    for _ in range(20):
+        out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+        B.prefix_attention(c.q, c.cache, c.step, heads[2] ** -0.5, out, lse, c.plan)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])

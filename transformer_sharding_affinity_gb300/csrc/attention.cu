@@ -1312,11 +1312,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             for (int e = 0; e < 32; ++e) v[e] = none ? 0u : v[e];
           }
           if (c + 32 >= p.kd) free_o();
+          // the block's bulk copy before has been read: of this item, or of one before it whose rows were output
+          if (!(c & 32)) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+          }
           if (direct) {
-            if (!(c & 32)) {       // the block's copy before has been read
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-              __syncwarp();
-            }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               st_shared16(stage_at(stage_out, lane, (c & 32) / 8 + q),
