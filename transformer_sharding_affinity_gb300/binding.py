@@ -521,6 +521,9 @@ def rotary(cos, sin, interleaved: bool = False, q_gain=None, k_gain=None, eps: f
         raise ValueError("cos and sin must be fp32 [n_pos, rot / 2]")
     if not (cos.is_contiguous() and sin.is_contiguous()):
         raise ValueError("cos and sin must be dense")
+    for t in (q_gain, k_gain):
+        if t is not None and (t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError("q_gain and k_gain must be dense [d_head]")
     r = aff_rotary(cos.data_ptr(), sin.data_ptr(), _ptr(q_gain), _ptr(k_gain), cos.shape[0], float(eps),
                    2 * cos.shape[1], int(bool(interleaved)))
     r.keep, r.gains = (cos, sin), (q_gain, k_gain)
