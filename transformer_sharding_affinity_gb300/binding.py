@@ -56,6 +56,7 @@ class aff_layout_opts(ctypes.Structure):
 
 
 class aff_kv_cache(ctypes.Structure):
+    device = None   # of the tensors it was made from; not known of raw addresses
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("group_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("G", ctypes.c_int32), ("page_size", ctypes.c_int32), ("d_head", ctypes.c_int32),
@@ -63,12 +64,14 @@ class aff_kv_cache(ctypes.Structure):
 
 
 class aff_step(ctypes.Structure):
+    device = None   # of the tensors it was made from; not known of raw addresses
     _fields_ = [("T", ctypes.c_int64), ("prefix_len", ctypes.c_int64), ("pages_stride", ctypes.c_int64),
                 ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
                 ("prefix_pages", ctypes.c_void_p), ("B", ctypes.c_int32), ("H", ctypes.c_int32)]
 
 
 class aff_rotary(ctypes.Structure):
+    device = None   # of the tensors it was made from; not known of raw addresses
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("q_gain", ctypes.c_void_p),
                 ("k_gain", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("eps", ctypes.c_float),
                 ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
@@ -461,6 +464,34 @@ def _same_type(like, **tensors) -> None:
             raise TypeError(f"{name} must be {like.dtype} on {like.device}")
 
 
+def _one_gpu(structs, *tensors) -> None:
+    """All of a call's tensors on one GPU: the kernels would follow a host address too.  Raw addresses are not looked
+    at.  `structs` carry the device index of the tensors that they were made from, -1 for the host."""
+    dev = None
+    for s in structs:
+        if dev is None:
+            dev = s.device
+        elif s.device is not None and s.device != dev:
+            raise TypeError("all tensors of a call must be on one GPU")
+    for t in tensors:
+        if t is None or t.__class__ is int:
+            continue
+        at = t.get_device()
+        if at != dev:
+            if dev is not None:
+                raise TypeError("all tensors of a call must be on one GPU")
+            dev = at
+    if dev is not None and dev < 0:
+        raise TypeError("tensors must be on a GPU")
+
+
+def _device_of(*tensors) -> int:
+    where = {t.get_device() for t in tensors if t is not None}
+    if len(where) != 1:
+        raise TypeError("all tensors must be on one device")
+    return where.pop()
+
+
 def kv_cache(k, v) -> aff_kv_cache:
     """A layer's paged cache from its pools, [n_pages, G, page_size, d_head] in any order of the first three."""
     if k.shape != v.shape or k.dim() != 4:
@@ -470,7 +501,7 @@ def kv_cache(k, v) -> aff_kv_cache:
     _same_type(k, v=v)
     c = aff_kv_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2), k.shape[1],
                      k.shape[2], k.shape[3], _dtype(k))
-    c.keep = (k, v)
+    c.keep, c.device = (k, v), k.get_device()
     return c
 
 
@@ -491,6 +522,7 @@ def step(T: int, H: int, q_start, kv_len, pages, prefix_pages=None, prefix_len: 
                  _ptr(prefix_pages), B, int(H))
     s.keep = (q_start, kv_len, pages, prefix_pages)
     s.n_prefix_pages = 0 if prefix_pages is None else prefix_pages.shape[0]
+    s.device = _device_of(q_start, kv_len, pages, prefix_pages)
     return s
 
 
@@ -510,6 +542,7 @@ def step_plan_size(s: aff_step, c: aff_kv_cache) -> int:
 def step_plan(s: aff_step, c: aff_kv_cache, plan, stream=None, plan_bytes=None) -> None:
     """Enqueue the plan of a step (affinity_step_plan) into `plan`, a CUDA uint8 tensor of step_plan_size bytes."""
     _prefix_covered(s, c)
+    _one_gpu((s, c), plan)
     _check(load().affinity_step_plan(ctypes.byref(s), ctypes.byref(c), _ptr(plan), _ws_bytes(plan, plan_bytes),
                                      _stream(stream)), "affinity_step_plan")
 
@@ -526,7 +559,7 @@ def rotary(cos, sin, interleaved: bool = False, q_gain=None, k_gain=None, eps: f
             raise ValueError("q_gain and k_gain must be dense [d_head]")
     r = aff_rotary(cos.data_ptr(), sin.data_ptr(), _ptr(q_gain), _ptr(k_gain), cos.shape[0], float(eps),
                    2 * cos.shape[1], int(bool(interleaved)))
-    r.keep, r.gains = (cos, sin), (q_gain, k_gain)
+    r.keep, r.gains, r.device = (cos, sin), (q_gain, k_gain), _device_of(cos, sin, q_gain, k_gain)
     return r
 
 
@@ -542,9 +575,10 @@ def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan,
     for t in r.gains:
         if t is not None and (t.shape != (d,) or _dtype(t) != code):
             raise ValueError("q_gain and k_gain must be [d_head] of the cache's type")
-    _check(load().affinity_kv_append(q.data_ptr(), _row_stride(q, hd, "q"), k.data_ptr(), _row_stride(k, gd, "k"),
-                                     v.data_ptr(), _row_stride(v, gd, "v"), c, s, r, q_out.data_ptr(),
-                                     _row_stride(q_out, hd, "q_out"), _ptr(plan), _ws_bytes(plan, plan_bytes),
+    strides = _row_stride(q, hd, "q"), _row_stride(k, gd, "k"), _row_stride(v, gd, "v"), _row_stride(q_out, hd, "q_out")
+    _one_gpu((c, s, r), q, k, v, q_out, plan)
+    _check(load().affinity_kv_append(q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], c, s, r,
+                                     q_out.data_ptr(), strides[3], _ptr(plan), _ws_bytes(plan, plan_bytes),
                                      _stream(stream)), "affinity_kv_append")
 
 
@@ -561,7 +595,9 @@ def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, pl
         raise ValueError("out must be dense")
     if lse is not None and (_dtype(lse) != AFF_FP32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, H]")
-    _check(load().affinity_prefix_attention(q.data_ptr(), _row_stride(q, hd, "q"), c, s, scale, out.data_ptr(),
+    q_stride = _row_stride(q, hd, "q")
+    _one_gpu((c, s), q, out, lse, plan)
+    _check(load().affinity_prefix_attention(q.data_ptr(), q_stride, c, s, scale, out.data_ptr(),
                                             _ptr(lse), _ptr(plan), _ws_bytes(plan, plan_bytes), _stream(stream)),
            "affinity_prefix_attention")
 
@@ -590,6 +626,7 @@ def block_norm(x, f, y, h=None, post_gain=None, pre_gain=None, gate=None, rows_p
     a = aff_block_norm(*ptrs, T, D, _row_stride(x, D, "x"), _row_stride(f, D, "f"),
                        0 if gate is None else _row_stride(gate, D, "gate"), _row_stride(y, D, "y"),
                        0 if h is None else _row_stride(h, D, "h"), rows_per_gate, scale, eps, _dtype(x))
+    _one_gpu((), x, f, gate, post_gain, pre_gain, y, h)
     _check(load().affinity_block_norm(a, _stream(stream)), "affinity_block_norm")
 
 
