@@ -28,6 +28,99 @@ class CachedSequence:
     """A sequence in the cache: its pages and the tokens they hold."""
     pages: List[int] = dataclasses.field(default_factory=list)
     length: int = 0
+    step: Optional["_Step"] = dataclasses.field(default=None, repr=False, compare=False)   # until every layer's cache has it
+
+
+class _Step:
+    """A step that has begun: its sequences have grown, but not every layer's cache holds the new tokens yet."""
+
+    def __init__(self, seqs: Sequence[CachedSequence], lengths: Sequence[int], prefix: Optional[CachedSequence]):
+        self.seqs, self.lengths, self.prefix = list(seqs), list(lengths), prefix
+        self.prefix_len = prefix.length if prefix is not None else 0
+        self.prefix_pages = list(prefix.pages) if self.prefix_len else None
+        self.rest = None           # the layers still to run, where the step may be ended without its caller
+        self.closed = False        # a sequence of it was released
+
+    def check(self) -> None:
+        changed = self.prefix_len and (self.prefix.length < self.prefix_len or
+                                       self.prefix.pages[:len(self.prefix_pages)] != self.prefix_pages)
+        if self.closed or changed:
+            raise ValueError("a sequence of this step was released")
+
+
+def _begin(fwd: "Forward", x, seqs: Sequence[CachedSequence], lengths: Optional[Sequence[int]],
+           prefix: Optional[CachedSequence]) -> _Step:
+    """Checks a step, ends the steps that its sequences still stand in, and grows the sequences."""
+    T, n = x.shape[0], len(seqs)
+    if lengths is None:
+        if T % n:
+            raise ValueError("lengths are needed where tokens do not divide among the sequences")
+        lengths = [T // n] * n
+    if len(lengths) != n or sum(lengths) != T or min(lengths) < 0:
+        raise ValueError(f"lengths must be {n} counts that add up to {T}")
+    if len(set(map(id, seqs))) != n or any(s is prefix for s in seqs):
+        raise ValueError("a sequence can stand in a step only once")
+    used = list(seqs) + ([prefix] if prefix is not None else [])
+    for s in used:
+        if s.step is not None and s.step.rest is not None:
+            for _ in s.step.rest:
+                pass
+    if any(s.step is not None for s in used):
+        raise ValueError("a step of a sequence was left before its last layer: release the sequence")
+    step = _Step(seqs, lengths, prefix)
+    fwd._grow(seqs, lengths, step.prefix_len)
+    for s in seqs:
+        s.step = step
+    return step
+
+
+def _layers(fwd: "Forward", x, step: _Step, check: bool) -> Iterator[tuple]:
+    """A step that has begun, a layer at a time (see Forward.blocks)."""
+    import torch
+    T, n = x.shape[0], len(step.seqs)
+    step.check()
+
+    def ints(v):
+        return torch.tensor(v, dtype=torch.int32).to(x.device)
+
+    starts = [0]
+    for k in step.lengths:
+        starts.append(starts[-1] + k)
+    width = max([len(s.pages) for s in step.seqs] + [1])
+    table = [s.pages + [0] * (width - len(s.pages)) for s in step.seqs]
+    at = B.step(T, fwd.H, ints(starts), ints([s.length for s in step.seqs]), ints(table).reshape(n, width),
+                ints(step.prefix_pages) if step.prefix_len else None, step.prefix_len)
+    plan = torch.empty(B.step_plan_size(at, fwd.caches[0]), dtype=torch.uint8, device=x.device)
+    B.step_plan(at, fwd.caches[0], plan)
+    h, a = torch.empty_like(x), torch.empty(T, fwd.H * fwd.d, dtype=x.dtype, device=x.device)
+    # the first block's input norm: nothing is added yet
+    B.block_norm(x, x, x, h, pre_gain=fwd.layers[0]["g_attn"], scale=0.0, eps=fwd.eps)
+    for i, w in enumerate(fwd.layers):
+        last = i + 1 == len(fwd.layers)
+        q, k, v = h @ w["Wq"].T, h @ w["Wk"].T, h @ w["Wv"].T
+        B.kv_append(q, k, v, fwd.caches[i], at, fwd.rotaries[i], q, plan)
+        B.prefix_attention(q, fwd.caches[i], at, fwd.d ** -0.5, a, None, plan)
+        B.block_norm(x, a @ w["Wo"].T, x, h, pre_gain=w["gamma"], eps=fwd.eps)
+        if check:
+            _status(plan)
+        if last:
+            for s in step.seqs:
+                s.step = None
+        yield i, a, x
+        if not last:
+            step.check()
+        f = (torch.nn.functional.silu(h @ w["Wg"].T) * (h @ w["Wu"].T)) @ w["Wd"].T
+        if last:
+            B.block_norm(x, f, x, eps=fwd.eps)
+        else:
+            B.block_norm(x, f, x, h, pre_gain=fwd.layers[i + 1]["g_attn"], eps=fwd.eps)
+    _status(plan)
+
+
+def _status(plan) -> None:
+    st = B.device_status(plan)
+    if st != B.AFF_OK:
+        raise B.AffinityError(st, "forward step", B.strerror(st))
 
 
 def rotary_tables(n_pos: int, rot: int, base: float = 10000.0, device="cuda"):
@@ -57,7 +150,10 @@ class Forward:
         return CachedSequence()
 
     def release(self, seq: CachedSequence) -> None:
-        """Gives a sequence's pages back."""
+        """Gives a sequence's pages back.  A step that it still stands in ends there, for the others too."""
+        if seq.step is not None:
+            seq.step.closed, seq.step.rest = True, None
+            seq.step = None
         self.free.extend(reversed(seq.pages))
         seq.pages, seq.length = [], 0
 
@@ -78,56 +174,9 @@ class Forward:
         sequence b (equal ones if not given); all sequences stand behind `prefix`.  Yields (i, a, x) of every layer:
         the attention output [T, H d_head] and the residual entering the FFN's pre-norm [T, D], which are
         overwritten when the iteration goes on; x holds the stack's output [T, D] when it ends.  The step's status is
-        read at the end, with `check` (which waits for the stream) before every yield too."""
-        import torch
-        T, D = x.shape
-        B_ = len(seqs)
-        if lengths is None:
-            if T % B_:
-                raise ValueError("lengths are needed where tokens do not divide among the sequences")
-            lengths = [T // B_] * B_
-        if len(lengths) != B_ or sum(lengths) != T or min(lengths) < 0:
-            raise ValueError(f"lengths must be {B_} counts that add up to {T}")
-        if len(set(map(id, seqs))) != B_ or any(s is prefix for s in seqs):
-            raise ValueError("a sequence can stand in a step only once")
-        prefix_len = prefix.length if prefix is not None else 0
-        self._grow(seqs, lengths, prefix_len)
-
-        def ints(v):
-            return torch.tensor(v, dtype=torch.int32).to(x.device)
-
-        starts = [0]
-        for n in lengths:
-            starts.append(starts[-1] + n)
-        width = max([len(s.pages) for s in seqs] + [1])
-        table = [s.pages + [0] * (width - len(s.pages)) for s in seqs]
-        step = B.step(T, self.H, ints(starts), ints([s.length for s in seqs]), ints(table).reshape(B_, width),
-                      ints(prefix.pages) if prefix_len else None, prefix_len)
-        plan = torch.empty(B.step_plan_size(step, self.caches[0]), dtype=torch.uint8, device=x.device)
-        B.step_plan(step, self.caches[0], plan)
-        h, a = torch.empty_like(x), torch.empty(T, self.H * self.d, dtype=x.dtype, device=x.device)
-        # the first block's input norm: nothing is added yet
-        B.block_norm(x, x, x, h, pre_gain=self.layers[0]["g_attn"], scale=0.0, eps=self.eps)
-        for i, w in enumerate(self.layers):
-            q, k, v = h @ w["Wq"].T, h @ w["Wk"].T, h @ w["Wv"].T
-            B.kv_append(q, k, v, self.caches[i], step, self.rotaries[i], q, plan)
-            B.prefix_attention(q, self.caches[i], step, self.d ** -0.5, a, None, plan)
-            B.block_norm(x, a @ w["Wo"].T, x, h, pre_gain=w["gamma"], eps=self.eps)
-            if check:
-                self._status(plan)
-            yield i, a, x
-            f = (torch.nn.functional.silu(h @ w["Wg"].T) * (h @ w["Wu"].T)) @ w["Wd"].T
-            if i + 1 < len(self.layers):
-                B.block_norm(x, f, x, h, pre_gain=self.layers[i + 1]["g_attn"], eps=self.eps)
-            else:
-                B.block_norm(x, f, x, eps=self.eps)
-        self._status(plan)
-
-    @staticmethod
-    def _status(plan) -> None:
-        st = B.device_status(plan)
-        if st != B.AFF_OK:
-            raise B.AffinityError(st, "forward step", B.strerror(st))
+        read at the end, with `check` (which waits for the stream) before every yield too.  Left before its last
+        layer, a step leaves caches without its tokens: its sequences are refused until they are released."""
+        yield from _layers(self, x, _begin(self, x, seqs, lengths, prefix), check)
 
     def run(self, x, seqs: Sequence[CachedSequence], lengths: Optional[Sequence[int]] = None,
             prefix: Optional[CachedSequence] = None):
@@ -140,8 +189,10 @@ class Forward:
     def layer_inputs(self, x, seqs: Sequence[CachedSequence], lengths: Optional[Sequence[int]] = None,
                      prefix: Optional[CachedSequence] = None) -> Callable[[int], Dict[str, object]]:
         """The `layer_inputs` of ``stack.calibrate_stack`` for one step: called with rising layer numbers (some may
-        be left out, as a resumed run does), each time the stack goes on to that layer."""
-        run = self.blocks(x.clone(), seqs, lengths, prefix, check=True)
+        be left out, as a resumed run does), each time the stack goes on to that layer.  The sequences have grown at once;
+        the next step that uses one of them first runs the layers that were not asked for."""
+        step = _begin(self, x, seqs, lengths, prefix)
+        run = step.rest = _layers(self, x.clone(), step, check=True)
 
         def inputs(i: int) -> Dict[str, object]:
             for j, a, residual in run:
