@@ -554,10 +554,11 @@ AFF_API aff_status affinity_kv_append(const void* q, int64_t q_stride, const voi
  * denominator, sum_j exp(scale q.k_j).  A row without keys (padding) is 0, its
  * lse -inf.  q [T, H*d_head] with rows q_stride apart, out [T, H*d_head] dense.
  * What a row does not see (keys past a sequence's own, later tokens of its
- * sequence) does not reach it, infinite or NaN as it may be; an infinite or NaN
- * value of a key that it sees does.  scale must be positive.  AFF_BF16: fp32 scores, sums and softmax,
- * probabilities rounded to bf16 for the second product.  AFF_FP32: fp32
- * throughout on the CUDA cores (meant for small shapes).
+ * sequence) does not reach it, infinite or NaN as it may be.  An infinite or
+ * NaN value of a key that it sees makes that column of the row infinite or NaN,
+ * however small the key's probability.  scale must be positive.  AFF_BF16: fp32
+ * scores, sums and softmax, probabilities rounded to bf16 for the second
+ * product.  AFF_FP32: fp32 throughout on the CUDA cores (meant for small shapes).
  */
 AFF_API aff_status affinity_prefix_attention(const void* q, int64_t q_stride, const aff_kv_cache* cache,
                                              const aff_step* step, float scale, void* out, float* lse, void* plan,

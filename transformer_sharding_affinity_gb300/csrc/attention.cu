@@ -317,8 +317,9 @@ __device__ __forceinline__ int all_see(const WorkItem& it, const StepGeom& g) {
 }
 
 // For the items that this CTA has marked, with all its outputs written: adds the values that are not finite to
-// the rows that see their keys.  A probability is never 0, so such a value makes the sum inf or NaN whatever else
-// is in it.  The first eight warps; a rare case, and bounded by the items' masked keys.
+// the rows that see their keys.  Such a value makes the sum inf or NaN whatever else is in it, and however small its
+// probability: where that has underflowed to 0, the product over a whole tile gives 0 * inf = NaN.  The first eight
+// warps; a rare case, and bounded by the items' masked keys.
 __device__ __noinline__ void add_specials(const AttnParams& p, const uint16_t* v_pool, int n_items) {
   const StepGeom& g = p.g;
   const int warp = threadIdx.x >> 5, c = (threadIdx.x & 31) * 4;
@@ -1576,9 +1577,11 @@ __device__ void f32_tile(const AttnParams& p, const WorkItem& it, float* smem) {
     locate(next);
     copy(next, ks, p.kc, (cr & 7) * 4);
     int last = 0, first = kF32Keys;       // keys of this step that any, and that all of the thread's rows see
+    int seen[4];                          // by each of them
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int vis = own_vis[a] <= 0 ? 0 : cur.pre ? cur.keys : min(cur.keys, own_vis[a] - cur.key0);
+      seen[a] = vis;
       last = max(last, vis);
       first = min(first, vis);
       float mx = -INFINITY;
@@ -1621,7 +1624,7 @@ __device__ void f32_tile(const AttnParams& p, const WorkItem& it, float* smem) {
       if (64 + 4 * tx < d) v1 = *reinterpret_cast<const ulonglong2*>(vs + k * ld + 64 + 4 * tx);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        if (decltype(masked)::value && wa[a] == 0.f) continue;                // whatever lies there stays out
+        if (decltype(masked)::value && k >= seen[a]) continue;                // whatever lies there stays out
         const uint64_t ww = pair2(wa[a], wa[a]);
         o[a][0] = fma2(ww, v0.x, o[a][0]);
         o[a][1] = fma2(ww, v0.y, o[a][1]);
@@ -1752,7 +1755,7 @@ __device__ void f32_few(const AttnParams& p, const WorkItem& it, float* smem) {
     const float e = expf((sc - ref) * p.scale);
     l = l * f + e;                        // this lane's keys alone
     m = m_new;
-    const bool all = __all_sync(0xffffffffu, seen);
+    const unsigned see = __ballot_sync(0xffffffffu, seen);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float fr = __shfl_sync(0xffffffffu, f, 8 * r << S);
@@ -1763,7 +1766,7 @@ __device__ void f32_few(const AttnParams& p, const WorkItem& it, float* smem) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float w = __shfl_sync(0xffffffffu, e, (8 * r + k) << S);
-        if (!all && w == 0.f) continue;   // masked: whatever lies there
+        if (see != ~0u && !(see >> ((8 * r + k) << S) & 1u)) continue;   // masked: whatever lies there
         o[r].x += w * vf[k].x;
         o[r].y += w * vf[k].y;
         o[r].z += w * vf[k].z;
@@ -1877,7 +1880,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   }
   const int n = n_pre + n_own;
   auto row_of = [&](int i) { return i < n_pre ? pre0 + i * pre_step : own0 + (i - n_pre) * own_step; };
-  // eight parts' rows in flight, the first of them beside their log-sum-exps; an empty part's row is not used
+  // eight parts' rows in flight, the first of them beside their log-sum-exps; an empty part's row is zero
   float4 v[8];
   auto fetch = [&](int i0) {
 #pragma unroll
@@ -1897,8 +1900,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
     const float w_mine = lane < 8 && i0 + lane < n ? expf(g.part_lse[row_of(i0 + lane)] - ref) : 0.f;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const float w = __shfl_sync(0xffffffffu, w_mine, x);
-      if (w == 0.f) continue;
+      const float w = __shfl_sync(0xffffffffu, w_mine, x);      // 0 beside the others' or of no part: 0 * NaN stays NaN
       sum += w;
       acc.x += w * v[x].x;
       acc.y += w * v[x].y;
