@@ -58,6 +58,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1383,16 +1384,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 template <int NK, bool FEW>
 aff_status launch_attention(const CUtensorMap (&m)[6], const AttnParams& p, unsigned grid, int smem,
                             cudaStream_t s) {
-  // The register split needs the launch to own 128 registers a thread.
-  static const cudaError_t ready = [] {
+  // The register split needs the launch to own 128 registers a thread: a matter of the compiled kernel, asked once.
+  // The shared-memory limit belongs to the current device, so it is set for every call, as elsewhere.
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, attention_kernel<NK, FEW>);
-    if (e == cudaSuccess && fa.numRegs != 128) e = cudaErrorInvalidConfiguration;
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attention_kernel<NK, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-    return e;
-  }();
-  AFF_CUDA(ready);
+    AFF_CUDA(cudaFuncGetAttributes(&fa, attention_kernel<NK, FEW>));
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != 128) AFF_CUDA(cudaErrorInvalidConfiguration);
+  AFF_CUDA(cudaFuncSetAttribute(attention_kernel<NK, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax));
   AFF_CUDA(launch_pdl(attention_kernel<NK, FEW>, grid, kThreads, (size_t)smem, s, m[0], m[5], m[1], m[2], m[3], m[4], p));
   return AFF_OK;
 }
