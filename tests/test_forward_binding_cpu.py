@@ -100,3 +100,19 @@ def test_raw_addresses_are_taken_as_they_are(no_launch):
     c, s = B.aff_kv_cache(1 << 20, 1 << 20), B.aff_step(3, 0, 1)
     with pytest.raises(_Reached, match="step_plan"):
         B.step_plan(s, c, 1 << 20, stream=0, plan_bytes=4096)
+
+
+def test_a_part_of_a_wider_page_table_is_read_when_the_step_is_planned(no_launch):
+    """The table is changed in place between steps, as a server's is: every plan takes it as it is then."""
+    wide = _elsewhere(torch.arange(12, dtype=torch.int32).reshape(3, 4), 0)
+    at = lambda t: _elsewhere(t, 0)
+    s = B.step(3, 4, at(_ints(0, 1, 2, 3)), at(_ints(1, 2, 2)), wide[:, :2])
+    c = B.kv_cache(at(_pool(40, 2, 16, 64)), at(_pool(40, 2, 16, 64)))
+    read = s.keep[2]
+    assert s.pages == read.data_ptr() and read.is_contiguous() and s.pages_stride == 2
+    wide[1, 1] = 33
+    with pytest.raises(_Reached):
+        B.step_plan(s, c, at(torch.zeros(4096, dtype=torch.uint8)))
+    assert read.tolist() == [[0, 1], [4, 33], [8, 9]]
+    dense = at(torch.zeros(3, 2, dtype=torch.int32))
+    assert B.step(3, 4, at(_ints(0, 1, 2, 3)), at(_ints(1, 2, 2)), dense).pages == dense.data_ptr()

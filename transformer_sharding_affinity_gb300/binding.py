@@ -65,6 +65,7 @@ class aff_kv_cache(ctypes.Structure):
 
 class aff_step(ctypes.Structure):
     device = None   # of the tensors it was made from; not known of raw addresses
+    copied = None   # (a part of a wider page table, its dense copy)
     _fields_ = [("T", ctypes.c_int64), ("prefix_len", ctypes.c_int64), ("pages_stride", ctypes.c_int64),
                 ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
                 ("prefix_pages", ctypes.c_void_p), ("B", ctypes.c_int32), ("H", ctypes.c_int32)]
@@ -506,7 +507,9 @@ def kv_cache(k, v) -> aff_kv_cache:
 
 
 def step(T: int, H: int, q_start, kv_len, pages, prefix_pages=None, prefix_len: int = 0) -> aff_step:
-    """A step of T query tokens with H heads: q_start [B+1], kv_len [B], pages [B, n], prefix_pages (CUDA int32)."""
+    """A step of T query tokens with H heads: q_start [B+1], kv_len [B], pages [B, n], prefix_pages (CUDA int32).
+    Their contents are taken by step_plan: changed in place, they count from the next step_plan on.  The rows of pages
+    may be a part of a wider table's."""
     import torch
     for name, t in (("q_start", q_start), ("kv_len", kv_len), ("pages", pages), ("prefix_pages", prefix_pages)):
         if t is not None and (t.dtype != torch.int32 or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1)):
@@ -516,11 +519,13 @@ def step(T: int, H: int, q_start, kv_len, pages, prefix_pages=None, prefix_len: 
         raise ValueError("q_start must be [B+1], kv_len [B] and pages [B, n]")
     if B > 1 and pages.stride(0) < pages.shape[1]:
         raise ValueError("the rows of pages must not overlap")
+    table = pages
     if B > 1 and pages.stride(0) != pages.shape[1]:
         pages = pages.contiguous()
     s = aff_step(int(T), int(prefix_len), pages.shape[1], q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(),
                  _ptr(prefix_pages), B, int(H))
     s.keep = (q_start, kv_len, pages, prefix_pages)
+    s.copied = None if pages is table else (table, pages)
     s.n_prefix_pages = 0 if prefix_pages is None else prefix_pages.shape[0]
     s.device = _device_of(q_start, kv_len, pages, prefix_pages)
     return s
@@ -539,10 +544,22 @@ def step_plan_size(s: aff_step, c: aff_kv_cache) -> int:
     return n.value
 
 
+def _copy_pages(table, pages, stream) -> None:
+    """A step's dense copy of a part of a wider page table, as that is now."""
+    if stream is None:
+        pages.copy_(table)
+        return
+    import torch
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        pages.copy_(table)
+
+
 def step_plan(s: aff_step, c: aff_kv_cache, plan, stream=None, plan_bytes=None) -> None:
     """Enqueue the plan of a step (affinity_step_plan) into `plan`, a CUDA uint8 tensor of step_plan_size bytes."""
     _prefix_covered(s, c)
     _one_gpu((s, c), plan)
+    if s.copied is not None:
+        _copy_pages(*s.copied, stream)
     _check(load().affinity_step_plan(ctypes.byref(s), ctypes.byref(c), _ptr(plan), _ws_bytes(plan, plan_bytes),
                                      _stream(stream)), "affinity_step_plan")
 
