@@ -116,3 +116,12 @@ def test_a_part_of_a_wider_page_table_is_read_when_the_step_is_planned(no_launch
     assert read.tolist() == [[0, 1], [4, 33], [8, 9]]
     dense = at(torch.zeros(3, 2, dtype=torch.int32))
     assert B.step(3, 4, at(_ints(0, 1, 2, 3)), at(_ints(1, 2, 2)), dense).pages == dense.data_ptr()
+
+
+def test_lengths_and_prefix_pages_are_vectors():
+    """A matrix of lengths would be read as its first elements, a row of prefix pages as one page."""
+    starts, pages = _ints(0, 1, 2), torch.zeros(2, 1, dtype=torch.int32)
+    for kv_len, prefix in ((_ints(1, 2, 3, 4).reshape(2, 2), None), (torch.tensor(1, dtype=torch.int32), None),
+                           (_ints(1, 2), _ints(0, 1).reshape(1, 2)), (_ints(1, 2), torch.tensor(0, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="vectors"):
+            B.step(2, 4, starts, kv_len, pages, prefix, 3 if prefix is not None else 0)

@@ -514,6 +514,8 @@ def step(T: int, H: int, q_start, kv_len, pages, prefix_pages=None, prefix_len: 
     for name, t in (("q_start", q_start), ("kv_len", kv_len), ("pages", pages), ("prefix_pages", prefix_pages)):
         if t is not None and (t.dtype != torch.int32 or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1)):
             raise ValueError(f"{name} must be dense int32")
+    if kv_len.dim() != 1 or (prefix_pages is not None and prefix_pages.dim() != 1):
+        raise ValueError("kv_len and prefix_pages must be vectors")
     B = kv_len.shape[0]
     if q_start.shape != (B + 1,) or pages.dim() != 2 or pages.shape[0] != B:
         raise ValueError("q_start must be [B+1], kv_len [B] and pages [B, n]")
