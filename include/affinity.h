@@ -512,6 +512,7 @@ AFF_API aff_status affinity_step_plan_size(const aff_step* step, const aff_kv_ca
  * word that affinity_device_status(plan) reads: AFF_ERR_RANGE for starts out of
  * order, a kv_len past its pages, a page id outside the pool or a position
  * outside the rotary table; AFF_ERR_INVALID_ARG for a plan made for other shapes.
+ * Reading clears it; every further call on such a plan sets it again.
  */
 AFF_API aff_status affinity_step_plan(const aff_step* step, const aff_kv_cache* cache, void* plan, size_t plan_bytes,
                                       aff_stream_t stream);

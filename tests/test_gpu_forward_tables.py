@@ -52,3 +52,28 @@ def test_a_table_changed_in_place_counts_from_the_next_plan(how, wider):
             go(caches[i], outs[i])
         torch.cuda.synchronize()
         assert torch.equal(outs[i], want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fault", ["starts", "length", "page"])
+def test_every_call_on_a_malformed_step_says_so(dtype, fault):
+    """The status word is cleared when it is read; the step is no better for it."""
+    c = Mixed((4, 2, 64), [1, 3, 2], [40, 90, 33], 0, 16, dtype=dtype, seed=72)
+    bad = {"starts": dict(q_start=torch.tensor([0, 4, 1, 6], dtype=torch.int32, device="cuda")),
+           "length": dict(kv_len=torch.tensor([40, 9000, 33], dtype=torch.int32, device="cuda")),
+           "page": dict(pages=torch.full_like(c.dev["pages"], 999))}[fault]
+    step = B.step(c.T, 4, **dict(c.dev, **bad))
+    B.step_plan(step, c.cache, c.plan)
+    assert B.device_status(c.plan) == B.AFF_ERR_RANGE
+    cos = torch.ones(200, 32, device="cuda")
+    kv = torch.randn(c.T, 2, 64, device="cuda").to(dtype)
+    pools = c.kd.clone(), c.vd.clone()
+    out = torch.empty_like(c.q)
+    for _ in range(2):
+        B.kv_append(c.q, kv, kv, c.cache, step, B.rotary(cos, cos), out, c.plan)
+        assert B.device_status(c.plan) == B.AFF_ERR_RANGE
+        B.prefix_attention(c.q, c.cache, step, 0.125, out, None, c.plan)
+        assert B.device_status(c.plan) == B.AFF_ERR_RANGE
+    assert torch.equal(c.kd.nan_to_num(), pools[0].nan_to_num()) and torch.equal(c.vd.nan_to_num(), pools[1].nan_to_num())
+    B.step_plan(c.step, c.cache, c.plan)
+    c.check_attention()

@@ -817,8 +817,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   const bool fits = plan_matches(g);
-  if (!fits && threadIdx.x == 0) latch_status(status, kStatusInvalid);
   const int n_items = fits ? g.head->n_items : 0;
+  // a plan of other shapes, or of a malformed step: said by every call, as the status is cleared when it is read
+  if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
 
   // The softmax threads hold a row of scores each: registers move to them from the other warps.
   if (warp >= 8 && warp < 12) {
@@ -1818,8 +1819,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attention_f32_kernel(const __g
   pdl_enter();
   const StepGeom& g = p.g;
   const bool fits = plan_matches(g);
-  if (!fits && threadIdx.x == 0) latch_status(&g.head->status, kStatusInvalid);
   const int n = fits ? g.head->n_items : 0;
+  if ((!fits || n < 0) && threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : kStatusInvalid);
   // as in the bf16 kernel: the first item by number, the others from the counter
   for (int i = blockIdx.x; i < n; i = claim) {
     const WorkItem it = load_item(g.items + i);

@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   }
   const TokenInfo ti = g.tok[t];
   const bool fits = plan_matches(g);
-  if (!fits) {
-    if (threadIdx.x == 0) latch_status(&g.head->status, 1);
+  if (!fits || g.head->n_items < 0) {            // a plan of other shapes, or of a malformed step
+    if (threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : 1);
     return;
   }
+  if (ti.own == -2 && threadIdx.x == 0) latch_status(&g.head->status, kStatusRange);
   const int64_t pos = (int64_t)g.prefix_len + ti.own;
   bool stand = ti.own >= 0;                      // the token is no padding
   if (stand && pos >= p.n_pos) {

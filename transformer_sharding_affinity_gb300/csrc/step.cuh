@@ -57,7 +57,7 @@ struct FastDiv {
 
 struct TokenInfo {       // one per token of the step; 16 bytes
   int64_t slot;          // page << 32 | offset in it, of its own key; -1: padding
-  int32_t own;           // index among its sequence's own tokens, -1: padding
+  int32_t own;           // index among its sequence's own tokens, -1: padding, -2: its page is no page of the pool
   int32_t seq;           // its sequence, -1: none
 };
 

@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const __grid_consta
         ti.own = (int)own;
         ti.slot = (int64_t)page << 32 | own % g.page_size;
       } else {
+        ti.own = -2;
         latch_status(&g.head->status, kStatusRange);
       }
     }
