@@ -511,7 +511,9 @@ AFF_API aff_status affinity_step_plan_size(const aff_step* step, const aff_kv_ca
  * partial rows, so calls that share a plan must not overlap, and the status
  * word that affinity_device_status(plan) reads: AFF_ERR_RANGE for starts out of
  * order, a kv_len past its pages, a page id outside the pool or a position
- * outside the rotary table; AFF_ERR_INVALID_ARG for a plan made for other shapes.
+ * outside the rotary table; AFF_ERR_INVALID_ARG for a plan made for other
+ * shapes; AFF_ERR_TIMEOUT if a wait inside the attention took 2 s, as a work item
+ * of several hundred million keys would.
  * Reading clears it; every further call on such a plan sets it again.
  */
 AFF_API aff_status affinity_step_plan(const aff_step* step, const aff_kv_cache* cache, void* plan, size_t plan_bytes,
@@ -547,8 +549,10 @@ AFF_API aff_status affinity_kv_append(const void* q, int64_t q_stride, const voi
                                       size_t plan_bytes, aff_stream_t stream);
 
 /*
- * Causal attention of a step over the cache, the shared prefix read once for
- * the whole batch:
+ * Causal attention of a step over the cache.  The shared prefix is read once
+ * for each 256 query rows (fp32: 64) of the whole batch where sequences have
+ * fewer rows than a row tile on average, T * H / G < 128 B (fp32: 64 B);
+ * otherwise every sequence's row tiles read it with their own keys:
  *   out[t, h] = sum_j softmax_j(scale q[t, h].k_j) v_j,
  * j over the prefix's keys and the own keys with index <= t's, k and v of group
  * h / (H/G).  lse[t, h] (fp32, may be NULL) is the log of the softmax's

@@ -1,6 +1,7 @@
 // attention.cu -- affinity_prefix_attention: causal softmax attention over a
-// paged cache for a batch whose sequences share a prefix, the prefix's keys and
-// values read once for the whole batch.
+// paged cache for a batch whose sequences share a prefix.  Where sequences have
+// few tokens the prefix's keys and values are read once for a row tile of the
+// whole batch (step.cuh, `separate`).
 //
 //   out[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - m)
 //   lse[t, h] = m + log sum_j p_j
@@ -38,6 +39,7 @@
 //       0.47 PFLOP/s: the prefix's items bound by the tensor core, the others by bytes;
 //     64 tokens behind 8192 with 750 own keys: 69 us, 3.3 TB/s: the items' latencies
 //       and the join (8 us).
+//   None of these times holds the step's plan (step_plan.cu), made once for all layers.
 //   Running maximum m and sum l are fp32 and thread-local.  O is rescaled only
 //   when m has grown by more than 8 (in log2): until then p <= 2^8, far inside
 //   fp32 and bf16.  P is rounded to bf16, the type of V (a product's operands

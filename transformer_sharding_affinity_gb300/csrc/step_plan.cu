@@ -436,10 +436,12 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   // Jobs of its own for the prefix: worth it while sequences have less than a row tile on average, which
   // would then be mostly idle for every key of the prefix (64 single tokens behind 8192 keys: 69 us, 359
   // without; 16 x 50 tokens, 100 rows each, behind 4000: 67 and 100; 64 x 33 behind 2000: 95 and 223; fp32,
-  // 17 x 30 tokens behind 2145: 328 and 369).
+  // 17 x 30 tokens behind 2145: 328 and 369).  It goes by the whole step, whatever the prefix's length: single tokens
+  // beside a long prompt each read the prefix with their own keys.
   g.separate = g.prefix_len > 0 && g.B > 1 && rows < (int64_t)g.B * (bf ? g.small : g.big);
   // The few-rows path where sequences have few rows on average (64 single tokens: 69 us, 98 without); the kernel
-  // without it is faster (64 x 1024 tokens: 280 us, 338 with it; 8 x 17 tokens, 34 rows each: 51 and 53).
+  // without it is faster (64 x 1024 tokens: 280 us, 338 with it; 8 x 17 tokens, 34 rows each, over 3000 keys: 48 and
+  // 50).  It goes by the whole step: single tokens beside prompts take the tensor tiles.
   g.few = bf && rows <= (int64_t)g.B * 32;
   g.prefix_rows = rows <= g.small ? g.small : g.big;
   g.prefix_tiles = g.separate ? (int)((rows + g.prefix_rows - 1) / g.prefix_rows) : 0;
