@@ -569,6 +569,84 @@ AFF_API aff_status affinity_prefix_attention(const void* q, int64_t q_stride, co
                                              const aff_step* step, float scale, void* out, float* lse, void* plan,
                                              size_t plan_bytes, aff_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The same cache in 4 bits: 0.28 of the bytes of bf16, held and read.  Steps,
+ * plans, rows and padding are those above.
+ *
+ * 16 neighbouring elements of a head row are a block.  Element x of a block is
+ * held as code * scale * g:
+ *   g      k_scale or v_scale of the cache, a power of two
+ *   scale  8 bits (sign-free e4m3: 0, 2^-9 .. 448): max |x| / (6 g), rounded
+ *   code   4 bits (sign, e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6): x / (scale g), rounded
+ * Both roundings are to nearest, ties to even, and saturate.  A scale of 0 makes
+ * its block 0.  A block that holds an infinity or a NaN gets the scale 0x7F and
+ * reads back as NaN.  code * scale has at most six significant bits: what the
+ * cache holds is exact in fp16, bf16 and fp32 (as long as g keeps it in range).
+ *
+ * Page p of group j is `page_bytes` = 18 * page_size * n bytes at p * page_stride
+ * + j * group_stride, n = ceil(d_head / 32): first the codes, 16 n bytes a token
+ * (element i in nibble i, the low one of a byte first), then the scales, by four
+ * tokens: [page_size / 4][2 n][4] bytes.  The second half of a token's last 16
+ * bytes and their scale are unused where d_head is not a multiple of 32: written
+ * as zeros, not read.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * A layer's paged cache in 4 bits.  Strides in BYTES, multiples of 16, the same
+ * for both pools; dtype is that of the queries, keys and values (AFF_BF16 or
+ * AFF_FP32).  d_head <= 256 (affinity_kv4_attention: <= 128), a multiple of 16;
+ * page_size a multiple of 8; k_scale, v_scale powers of two, 2^-30 .. 2^30.
+ */
+typedef struct {
+  void *k, *v;
+  int64_t n_pages, page_stride, group_stride;
+  int32_t G, page_size, d_head, dtype;
+  float k_scale, v_scale;
+} aff_kv4_cache;
+
+/* Host-only: bytes of a page of one group. */
+AFF_API aff_status affinity_kv4_page_bytes(int32_t page_size, int32_t d_head, size_t* bytes);
+
+/* affinity_step_plan_size and affinity_step_plan for a cache in 4 bits.  A plan serves the calls over one of the kinds. */
+AFF_API aff_status affinity_kv4_plan_size(const aff_step* step, const aff_kv4_cache* cache, size_t* bytes);
+AFF_API aff_status affinity_kv4_plan(const aff_step* step, const aff_kv4_cache* cache, void* plan, size_t plan_bytes,
+                                     aff_stream_t stream);
+
+/*
+ * affinity_kv_append over a cache in 4 bits: the same norms and rotation, queries
+ * to q_out, keys and values quantised to their slots.  The codes are those of
+ * the exact z: fp32 decides where it can, and a row with an element or a block's
+ * maximum next to a border of the rounding is computed again in 64 bits.
+ * rotary->rot is a multiple of 16.
+ */
+AFF_API aff_status affinity_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, const aff_kv4_cache* cache, const aff_step* step,
+                                       const aff_rotary* rotary, void* q_out, int64_t q_out_stride, void* plan,
+                                       size_t plan_bytes, aff_stream_t stream);
+
+/*
+ * Reads a step's tokens back: row t of k_out and v_out [T, G*d_head] (dense, of
+ * the cache's dtype, 16-byte aligned) is what the cache holds for token t, zeros
+ * for padding.  A step whose tokens are a whole sequence (q_start = {0, n}, kv_len
+ * = {n}) reads that sequence.
+ */
+AFF_API aff_status affinity_kv4_read(const aff_kv4_cache* cache, const aff_step* step, void* k_out, void* v_out, void* plan,
+                                     size_t plan_bytes, aff_stream_t stream);
+
+/*
+ * affinity_prefix_attention over a cache in 4 bits.  The cache's values enter the
+ * products as they are, in fp16; queries are scaled by a power of two for each
+ * row and head, into fp16's range.  AFF_BF16: fp32 scores, sums and softmax,
+ * probabilities rounded to 11 bits for the second product.  AFF_FP32: queries
+ * and probabilities as the sum of two fp16 numbers, 22 bits; for small shapes, as
+ * the prefix is read by every 8 query rows.  What a row does not see does not
+ * reach it; a key or value that reads back as NaN makes the rows NaN that see
+ * it (a value: their 16 columns), however small its probability.
+ */
+AFF_API aff_status affinity_kv4_attention(const void* q, int64_t q_stride, const aff_kv4_cache* cache, const aff_step* step,
+                                          float scale, void* out, float* lse, void* plan, size_t plan_bytes,
+                                          aff_stream_t stream);
+
 /*
  * The norms around a block with its gate and residual scale:
  *   u = f / rms(f) * post_gain   (u = f if post_gain is NULL)

@@ -63,6 +63,14 @@ class aff_kv_cache(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class aff_kv4_cache(ctypes.Structure):
+    device = None   # of the tensors it was made from; not known of raw addresses
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("group_stride", ctypes.c_int64), ("G", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("d_head", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 class aff_step(ctypes.Structure):
     device = None   # of the tensors it was made from; not known of raw addresses
     copied = None   # (a part of a wider page table, its dense copy)
@@ -166,6 +174,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                               ctypes.POINTER(aff_step), ctypes.c_float, _P, _P, _P, ctypes.c_size_t,
                                               _P]
     lib.affinity_prefix_attention.restype = st
+    lib.affinity_kv4_page_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.affinity_kv4_page_bytes.restype = st
+    lib.affinity_kv4_plan_size.argtypes = [ctypes.POINTER(aff_step), ctypes.POINTER(aff_kv4_cache),
+                                           ctypes.POINTER(ctypes.c_size_t)]
+    lib.affinity_kv4_plan_size.restype = st
+    lib.affinity_kv4_plan.argtypes = [ctypes.POINTER(aff_step), ctypes.POINTER(aff_kv4_cache), _P, ctypes.c_size_t, _P]
+    lib.affinity_kv4_plan.restype = st
+    lib.affinity_kv4_append.argtypes = [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64,
+                                        ctypes.POINTER(aff_kv4_cache), ctypes.POINTER(aff_step),
+                                        ctypes.POINTER(aff_rotary), _P, ctypes.c_int64, _P, ctypes.c_size_t, _P]
+    lib.affinity_kv4_append.restype = st
+    lib.affinity_kv4_read.argtypes = [ctypes.POINTER(aff_kv4_cache), ctypes.POINTER(aff_step), _P, _P, _P,
+                                      ctypes.c_size_t, _P]
+    lib.affinity_kv4_read.restype = st
+    lib.affinity_kv4_attention.argtypes = [_P, ctypes.c_int64, ctypes.POINTER(aff_kv4_cache), ctypes.POINTER(aff_step),
+                                           ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
+    lib.affinity_kv4_attention.restype = st
     lib.affinity_block_norm.argtypes = [ctypes.POINTER(aff_block_norm), _P]
     lib.affinity_block_norm.restype = st
     lib.affinity_strerror.argtypes = [ctypes.c_int32]
@@ -539,8 +564,13 @@ def _prefix_covered(s: aff_step, c: aff_kv_cache) -> None:
         raise ValueError("prefix_pages does not cover prefix_len")
 
 
-def step_plan_size(s: aff_step, c: aff_kv_cache) -> int:
+def step_plan_size(s: aff_step, c) -> int:
+    """Bytes of a step's plan; c: a kv_cache or a kv4_cache."""
     n = ctypes.c_size_t(0)
+    if isinstance(c, aff_kv4_cache):
+        _check(load().affinity_kv4_plan_size(ctypes.byref(s), ctypes.byref(c), ctypes.byref(n)),
+               "affinity_kv4_plan_size")
+        return n.value
     _check(load().affinity_step_plan_size(ctypes.byref(s), ctypes.byref(c), ctypes.byref(n)),
            "affinity_step_plan_size")
     return n.value
@@ -556,12 +586,17 @@ def _copy_pages(table, pages, stream) -> None:
         pages.copy_(table)
 
 
-def step_plan(s: aff_step, c: aff_kv_cache, plan, stream=None, plan_bytes=None) -> None:
-    """Enqueue the plan of a step (affinity_step_plan) into `plan`, a CUDA uint8 tensor of step_plan_size bytes."""
+def step_plan(s: aff_step, c, plan, stream=None, plan_bytes=None) -> None:
+    """Enqueue the plan of a step (affinity_step_plan, affinity_kv4_plan) into `plan`, a CUDA uint8 tensor of
+    step_plan_size bytes."""
     _prefix_covered(s, c)
     _one_gpu((s, c), plan)
     if s.copied is not None:
         _copy_pages(*s.copied, stream)
+    if isinstance(c, aff_kv4_cache):
+        _check(load().affinity_kv4_plan(ctypes.byref(s), ctypes.byref(c), _ptr(plan), _ws_bytes(plan, plan_bytes),
+                                        _stream(stream)), "affinity_kv4_plan")
+        return
     _check(load().affinity_step_plan(ctypes.byref(s), ctypes.byref(c), _ptr(plan), _ws_bytes(plan, plan_bytes),
                                      _stream(stream)), "affinity_step_plan")
 
@@ -582,9 +617,8 @@ def rotary(cos, sin, interleaved: bool = False, q_gain=None, k_gain=None, eps: f
     return r
 
 
-def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan, stream=None,
-              plan_bytes=None) -> None:
-    """Enqueue affinity_kv_append: q [T, H, d_head], k and v [T, G, d_head] (rows may be strided), q_out like q."""
+def _append_strides(q, k, v, c, s: aff_step, r: aff_rotary, q_out):
+    """Row strides of an append's tensors, after the checks of their shapes and types."""
     T, d, code = s.T, c.d_head, c.dtype
     hd, gd = s.H * d, c.G * d
     if not (q.shape[0] == k.shape[0] == v.shape[0] == q_out.shape[0] == T):
@@ -594,16 +628,21 @@ def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan,
     for t in r.gains:
         if t is not None and (t.shape != (d,) or _dtype(t) != code):
             raise ValueError("q_gain and k_gain must be [d_head] of the cache's type")
-    strides = _row_stride(q, hd, "q"), _row_stride(k, gd, "k"), _row_stride(v, gd, "v"), _row_stride(q_out, hd, "q_out")
+    return _row_stride(q, hd, "q"), _row_stride(k, gd, "k"), _row_stride(v, gd, "v"), _row_stride(q_out, hd, "q_out")
+
+
+def kv_append(q, k, v, c: aff_kv_cache, s: aff_step, r: aff_rotary, q_out, plan, stream=None,
+              plan_bytes=None) -> None:
+    """Enqueue affinity_kv_append: q [T, H, d_head], k and v [T, G, d_head] (rows may be strided), q_out like q."""
+    strides = _append_strides(q, k, v, c, s, r, q_out)
     _one_gpu((c, s, r), q, k, v, q_out, plan)
     _check(load().affinity_kv_append(q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], c, s, r,
                                      q_out.data_ptr(), strides[3], _ptr(plan), _ws_bytes(plan, plan_bytes),
                                      _stream(stream)), "affinity_kv_append")
 
 
-def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, plan, stream=None,
-                     plan_bytes=None) -> None:
-    """Enqueue affinity_prefix_attention: q and out [T, H, d_head], lse fp32 [T, H] or None."""
+def _attention_stride(q, c, s: aff_step, out, lse) -> int:
+    """Row stride of an attention's queries, after the checks of its tensors' shapes and types."""
     T, H, code = s.T, s.H, c.dtype
     hd = H * c.d_head
     if not (q.shape[0] == out.shape[0] == T):
@@ -614,11 +653,75 @@ def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, pl
         raise ValueError("out must be dense")
     if lse is not None and (_dtype(lse) != AFF_FP32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, H]")
-    q_stride = _row_stride(q, hd, "q")
+    return _row_stride(q, hd, "q")
+
+
+def prefix_attention(q, c: aff_kv_cache, s: aff_step, scale: float, out, lse, plan, stream=None,
+                     plan_bytes=None) -> None:
+    """Enqueue affinity_prefix_attention: q and out [T, H, d_head], lse fp32 [T, H] or None."""
+    q_stride = _attention_stride(q, c, s, out, lse)
     _one_gpu((c, s), q, out, lse, plan)
     _check(load().affinity_prefix_attention(q.data_ptr(), q_stride, c, s, scale, out.data_ptr(),
                                             _ptr(lse), _ptr(plan), _ws_bytes(plan, plan_bytes), _stream(stream)),
            "affinity_prefix_attention")
+
+
+def kv4_page_bytes(page_size: int, d_head: int) -> int:
+    """Bytes of a page of one group of a cache in 4 bits."""
+    n = ctypes.c_size_t(0)
+    _check(load().affinity_kv4_page_bytes(int(page_size), int(d_head), ctypes.byref(n)), "affinity_kv4_page_bytes")
+    return n.value
+
+
+def kv4_cache(k, v, page_size: int, d_head: int, dtype, k_scale: float = 1.0, v_scale: float = 1.0) -> aff_kv4_cache:
+    """A layer's paged cache in 4 bits from its pools, uint8 [n_pages, G, kv4_page_bytes(page_size, d_head)] with dense
+    pages, for queries, keys and values of `dtype`.  k_scale and v_scale are powers of two: blocks of 16 elements
+    with a maximum between 0.1 and 2688 times them keep the scale's full precision."""
+    import torch
+    if k.shape != v.shape or k.dim() != 3 or k.dtype != torch.uint8 or v.dtype != torch.uint8:
+        raise ValueError("k and v must be uint8 [n_pages, G, page bytes]")
+    if k.shape[2] != kv4_page_bytes(page_size, d_head):
+        raise ValueError(f"a page of {page_size} tokens of {d_head} elements has {kv4_page_bytes(page_size, d_head)} bytes")
+    if k.stride() != v.stride() or k.stride(2) != 1:
+        raise ValueError("k and v must have the same strides and dense pages")
+    codes = {torch.bfloat16: AFF_BF16, torch.float32: AFF_FP32}
+    if dtype not in codes:
+        raise TypeError("dtype must be bfloat16 or float32")
+    c = aff_kv4_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.shape[1], int(page_size),
+                      int(d_head), codes[dtype], float(k_scale), float(v_scale))
+    c.keep, c.device = (k, v), _device_of(k, v)
+    return c
+
+
+def kv4_append(q, k, v, c: aff_kv4_cache, s: aff_step, r: aff_rotary, q_out, plan, stream=None,
+               plan_bytes=None) -> None:
+    """Enqueue affinity_kv4_append: kv_append's tensors, keys and values quantised into the cache."""
+    strides = _append_strides(q, k, v, c, s, r, q_out)
+    _one_gpu((c, s, r), q, k, v, q_out, plan)
+    _check(load().affinity_kv4_append(q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], c, s, r,
+                                      q_out.data_ptr(), strides[3], _ptr(plan), _ws_bytes(plan, plan_bytes),
+                                      _stream(stream)), "affinity_kv4_append")
+
+
+def kv4_read(c: aff_kv4_cache, s: aff_step, k_out, v_out, plan, stream=None, plan_bytes=None) -> None:
+    """Enqueue affinity_kv4_read: the step's tokens as the cache holds them, k_out and v_out [T, G, d_head]."""
+    gd = c.G * c.d_head
+    for t in (k_out, v_out):
+        if t.shape[0] != s.T or _dtype(t) != c.dtype:
+            raise ValueError(f"k_out and v_out must have {s.T} rows of the cache's type")
+        if _row_stride(t, gd, "k_out and v_out") != gd:
+            raise ValueError("k_out and v_out must be dense")
+    _one_gpu((c, s), k_out, v_out, plan)
+    _check(load().affinity_kv4_read(c, s, k_out.data_ptr(), v_out.data_ptr(), _ptr(plan), _ws_bytes(plan, plan_bytes),
+                                    _stream(stream)), "affinity_kv4_read")
+
+
+def kv4_attention(q, c: aff_kv4_cache, s: aff_step, scale: float, out, lse, plan, stream=None, plan_bytes=None) -> None:
+    """Enqueue affinity_kv4_attention: q and out [T, H, d_head], lse fp32 [T, H] or None."""
+    q_stride = _attention_stride(q, c, s, out, lse)
+    _one_gpu((c, s), q, out, lse, plan)
+    _check(load().affinity_kv4_attention(q.data_ptr(), q_stride, c, s, scale, out.data_ptr(), _ptr(lse), _ptr(plan),
+                                         _ws_bytes(plan, plan_bytes), _stream(stream)), "affinity_kv4_attention")
 
 
 def block_norm(x, f, y, h=None, post_gain=None, pre_gain=None, gate=None, rows_per_gate: int = 1, scale: float = 1.0,

@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libaffinity.so")
 SOURCES = ["tile_kernel.cu", "moment_kernel.cu", "aux_kernels.cu", "api.cu", "layout.cu", "assign.cu", "realise.cu", "noalloc.cu",
-           "step_plan.cu", "kv_append.cu", "attention.cu", "block_norm.cu"]
+           "step_plan.cu", "kv_append.cu", "attention.cu", "block_norm.cu", "kv4_append.cu", "kv4_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

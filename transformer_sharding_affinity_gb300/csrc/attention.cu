@@ -1919,6 +1919,18 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 }
 
 }  // namespace
+
+aff_status launch_join(const StepGeom& g, void* out, float* lse, cudaStream_t s) {
+  AttnParams p{};
+  p.g = g;
+  p.out = out;
+  p.lse = lse;
+  const unsigned blocks = (unsigned)(((int64_t)g.T * g.H + 7) / 8);
+  if (g.dtype == AFF_BF16) AFF_CUDA(launch_pdl(join_kernel<__nv_bfloat16>, blocks, 256, 0, s, p));
+  else AFF_CUDA(launch_pdl(join_kernel<float>, blocks, 256, 0, s, p));
+  return AFF_OK;
+}
+
 }  // namespace aff
 
 using namespace aff;
@@ -1997,10 +2009,5 @@ extern "C" aff_status affinity_prefix_attention(const void* q, int64_t q_stride,
     st = g.few ? launch_attention<true>(m, p, grid, smem, s) : launch_attention<false>(m, p, grid, smem, s);
     if (st != AFF_OK) return st;
   }
-  if (g.may_split) {
-    const unsigned blocks = (unsigned)(((int64_t)g.T * g.H + 7) / 8);
-    if (g.dtype == AFF_BF16) AFF_CUDA(launch_pdl(join_kernel<__nv_bfloat16>, blocks, 256, 0, s, p));
-    else AFF_CUDA(launch_pdl(join_kernel<float>, blocks, 256, 0, s, p));
-  }
-  return AFF_OK;
+  return g.may_split ? launch_join(g, out, lse, s) : AFF_OK;
 }

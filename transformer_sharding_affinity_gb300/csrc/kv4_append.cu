@@ -1,0 +1,614 @@
+// kv4_append.cu -- affinity_kv4_append: a step's queries, keys and values, once over, into a cache in 4 bits; and
+// affinity_kv4_read, a step's tokens back.  Norms and rotation as in kv_append.cu; then, for keys and values,
+//
+//   scale = e4m3(max_block |x| / (6 g)),   code = e2m1(x / (scale g))       (kv4.cuh, include/affinity.h)
+//
+// Memory bound: T (H + 2G) d elements in, T H d elements and 9/16 byte for each of 2 T G d out.
+//
+// Borders.  A code changes where x / (scale g) passes one of seven values, a scale where the maximum does, so a last
+// bit of fp32 may move an element by a third of its size.  Values and plain keys are exact in the activations'
+// type, and their quotients are too wherever they lie on a border (q + (x - q s) / s is the rounded quotient, which
+// reaches a border only from it): fp32 decides.  A rotated or normalised key is off by at most 2^-19 of the
+// products it is the sum of (19 roundings of the norm's sum halved by the root, the root's own 2^-22, four products).
+// Where that crosses a border, in one of 25000 elements, the row is computed again in 64 bits, rounded to odd before
+// each of the two conversions, so that the double rounding does not show.
+#include "affinity.h"
+#include "internal.h"
+#include "kv4.cuh"
+#include "launch.cuh"
+#include "sm103_primitives.cuh"
+#include "step.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+namespace aff {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kMargin = 1.f / (1 << 19);     // of fp32 keys, relative to the products they are the sum of
+
+struct AppendParams {
+  StepGeom g;
+  Kv4Pool pool;
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float *cos, *sin;
+  const void *q_gain, *k_gain;
+  int64_t n_pos;
+  float eps, inv_d;
+  float k_inv, v_inv;          // 1 / k_scale, 1 / v_scale
+  int32_t rot, interleaved, lanes, lane_bits;
+};
+
+// Eight neighbouring elements.
+template <typename E>
+struct Run;
+template <>
+struct Run<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* at) { w = __ldcs(reinterpret_cast<const uint4*>(at)); }
+  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(x[i] << 16);
+      f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* at, const float (&f)[8]) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    *reinterpret_cast<uint4*>(at) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+};
+template <>
+struct Run<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* at) {
+    a = __ldcs(reinterpret_cast<const float4*>(at));
+    b = __ldcs(reinterpret_cast<const float4*>(at) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  static __device__ __forceinline__ void put(float* at, const float (&f)[8]) {
+    reinterpret_cast<float4*>(at)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(at)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// Eight numbers to eight codes.
+__device__ __forceinline__ uint32_t to_codes(const float (&f)[8]) {
+  uint32_t w;
+  asm("{.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};}"
+      : "=r"(w)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return w;
+}
+// Two scales, the first in the low byte.
+__device__ __forceinline__ uint32_t to_scales(float a, float b) {
+  uint32_t r;
+  asm("{.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, 0};}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The value of a scale byte that is no NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  float r;
+  asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;}" : "=f"(r) : "r"(kv4_scale_pair(byte)));
+  return r;
+}
+// x / 6 rounded to nearest (x >= 0, finite or not).
+__device__ __forceinline__ float sixth(float x) { return __fdiv_rn(x, 6.f); }
+
+__device__ __forceinline__ uint32_t largest(const float (&f)[8]) {      // of the magnitudes' bits: a NaN is above infinity
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+  return m;
+}
+
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float z = x * c - y * s;
+  y = x * s + y * c;
+  x = z;
+}
+
+// The codes of eight elements whose block has the maximum `top` (bits), with its scale.  `error`: what the elements
+// may be off by; *near_border is set where that could matter.
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t top, float inv_g, float error, bool inexact,
+                                             uint32_t* scale, bool* near_border) {
+  if (top >= 0x7f800000u) {
+    *scale = 0x7f;
+    return 0;
+  }
+  const float t = __uint_as_float(top);
+  *scale = to_scales(sixth(t * inv_g), 0.f) & 0xff;
+  const float s = scale_value(*scale), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = x[e] * inv_g, q0 = y * inv;
+    q[e] = fabsf(q0) < 16.f ? fmaf(fmaf(-q0, s, y), inv, q0) : q0;      // far out it saturates, and y - q0 s may be no number
+  }
+  const uint32_t w = to_codes(q);
+  if (inexact) {
+    const uint32_t both = to_scales(sixth((t + error) * inv_g), sixth(fmaxf(t - error, 0.f) * inv_g));
+    float lo[8], hi[8];
+    const float d = error * inv_g * inv;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      hi[e] = fabsf(q[e]) + d;
+      lo[e] = fmaxf(fabsf(q[e]) - d, 0.f);
+    }
+    if (to_codes(lo) != to_codes(hi) || (both & 0xff) != both >> 8) *near_border = true;
+  }
+  return w;
+}
+
+// x to fp32, towards zero, its last bit set where something was cut off: a rounding of the result to fewer bits is
+// that of x.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = __double2float_rz(x);
+  return (double)f == x || isnan(x) ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Where the other run of a block is: runs of eight are numbered along the head, 2 i and 2 i + 1 are a block.
+struct Partner {
+  int lane_a, lane_b;          // of the warp
+  bool b_of_a, b_of_b;         // whether it is that lane's second run
+};
+
+struct ExactRow {
+  const void *src, *gain;      // of the row
+  const float *cos, *sin;      // of its position and this lane's pairs; null: not rotated
+  int ja, jb, lanes, d;
+  bool interleaved;
+  float eps, inv_g;
+};
+struct Codes {
+  uint32_t a, b, scale_a, scale_b;
+};
+
+// A key row in 64 bits, by the row's lanes.  Loops stay loops: a rare path, and small.
+template <typename E>
+__device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, bool split) {
+  const E* src = static_cast<const E*>(r.src);
+  const E* gain = static_cast<const E*>(r.gain);
+  const bool has = r.ja < r.d;
+  double inv = 1.0;
+  if (gain) {
+    double ss = 0.0;
+#pragma unroll 1
+    for (int e = 0; has && e < 16; ++e) {
+      const double x = (double)(float)src[e < 8 ? r.ja + e : r.jb + e - 8];
+      ss += x * x;
+    }
+    for (int o = r.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    inv = 1.0 / sqrt(ss / r.d + (double)r.eps);
+  }
+  // pair e: elements (ja + e, jb + e), or two neighbours
+  auto pair = [&](int e, double* x, double* y) {
+    const int i = r.interleaved ? r.ja + 2 * e : r.ja + e, j = r.interleaved ? i + 1 : r.jb + e;
+    *x = (double)(float)src[i] * inv;
+    *y = (double)(float)src[j] * inv;
+    if (gain) {
+      *x *= (double)(float)gain[i];
+      *y *= (double)(float)gain[j];
+    }
+    if (r.cos) {
+      const double c = r.cos[e], s = r.sin[e], z = *x * c - *y * s;
+      *y = *x * s + *y * c;
+      *x = z;
+    }
+  };
+  double top_a = 0.0, top_b = 0.0;
+#pragma unroll 1
+  for (int e = 0; has && e < 8; ++e) {
+    double x, y;
+    pair(e, &x, &y);
+    if (r.interleaved) {
+      x = fmax(fabs(x), fabs(y));
+      if (e < 4) top_a = fmax(top_a, x);
+      else top_b = fmax(top_b, x);
+    } else {
+      top_a = fmax(top_a, fabs(x));
+      top_b = fmax(top_b, fabs(y));
+    }
+  }
+  const double aa = __shfl_sync(0xffffffffu, top_a, p.lane_a), ab = __shfl_sync(0xffffffffu, top_b, p.lane_a);
+  const double ba = __shfl_sync(0xffffffffu, top_a, p.lane_b), bb = __shfl_sync(0xffffffffu, top_b, p.lane_b);
+  const double other_a = split ? (p.b_of_a ? ab : aa) : top_b, other_b = split ? (p.b_of_b ? bb : ba) : top_a;
+  top_a = fmax(top_a, other_a);
+  top_b = fmax(top_b, other_b);
+  Codes c{0, 0, to_scales(to_odd(top_a * r.inv_g / 6.0), 0.f) & 0xff, to_scales(to_odd(top_b * r.inv_g / 6.0), 0.f) & 0xff};
+  const double sa = scale_value(c.scale_a), sb = scale_value(c.scale_b);
+  auto code = [&](double x, double s) {
+    float f[8] = {s > 0.0 ? to_odd(x * r.inv_g / s) : 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    return to_codes(f) & 15u;
+  };
+#pragma unroll 1
+  for (int e = 0; has && e < 8; ++e) {
+    double x, y;
+    pair(e, &x, &y);
+    if (r.interleaved) {
+      const double s = e < 4 ? sa : sb;
+      const uint32_t two = (code(x, s) | code(y, s) << 4) << (8 * (e & 3));
+      if (e < 4) c.a |= two;
+      else c.b |= two;
+    } else {
+      c.a |= code(x, sa) << (4 * e);
+      c.b |= code(y, sb) << (4 * e);
+    }
+  }
+  return c;
+}
+
+// A block is (a part of) one token; a row is dealt to `lanes` neighbouring threads, each with two runs of eight
+// elements: of the rotated part the two halves of eight pairs (or, interleaved, two neighbouring runs whose pairs
+// lie side by side), past it and in value rows neighbours.  A thread has kPer rows, `slots` apart.
+template <typename E>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kPer = 2;
+  pdl_enter();
+  const StepGeom& g = p.g;
+  const int t = blockIdx.x, lane = threadIdx.x & (p.lanes - 1);
+  const int slots = blockDim.x >> p.lane_bits;
+  const int r0 = blockIdx.y * slots * kPer + (threadIdx.x >> p.lane_bits);
+  const int half = p.rot / 2, units = half / 8, n_rot = g.H + g.G, rows = n_rot + g.G;
+  // this lane's runs in a row that is turned and in one that is not
+  const bool rotates = lane < units, split = rotates && !p.interleaved;
+  const int ja = rotates ? (p.interleaved ? 16 : 8) * lane : p.rot + 16 * (lane - units);
+  const int jb = split ? ja + half : ja + 8;
+  // the rows first: they do not depend on where their token stands
+  Run<E> va[kPer], vb[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = r0 + k * slots;
+    const E* src = r < g.H   ? static_cast<const E*>(p.q) + (int64_t)t * p.q_stride + r * g.d
+                   : r < n_rot ? static_cast<const E*>(p.k) + (int64_t)t * p.k_stride + (r - g.H) * g.d
+                               : static_cast<const E*>(p.v) + (int64_t)t * p.v_stride + (r - n_rot) * g.d;
+    const int a = r < n_rot ? ja : 16 * lane, b = r < n_rot ? jb : 16 * lane + 8;
+    va[k].clear();
+    vb[k].clear();
+    if (r < rows && a < g.d) {          // d is whole units of 16: both runs are there, or none
+      va[k].load(src + a);
+      vb[k].load(src + b);
+    }
+  }
+  const TokenInfo ti = g.tok[t];
+  const bool fits = plan_matches(g);
+  if (!fits || g.head->n_items < 0) {            // a plan of other shapes, or of a malformed step
+    if (threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : 1);
+    return;
+  }
+  if (ti.own == -2 && threadIdx.x == 0) latch_status(&g.head->status, kStatusRange);
+  const int64_t pos = (int64_t)g.prefix_len + ti.own;
+  bool stand = ti.own >= 0;                      // the token is no padding
+  if (stand && pos >= p.n_pos) {
+    stand = false;
+    if (threadIdx.x == 0) latch_status(&g.head->status, kStatusRange);
+  }
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = s[e] = 0.f;
+  const float *cos = p.cos + pos * half + 8 * lane, *sin = p.sin + pos * half + 8 * lane;
+  if (stand && rotates) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(cos + e)), y = __ldg(reinterpret_cast<const float4*>(sin + e));
+      c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
+      s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
+    }
+  }
+  Partner with{0, 0, false, false};
+  {
+    const int base = (threadIdx.x & 31) & ~(p.lanes - 1), ra = lane ^ 1, rb = (units + lane) ^ 1;
+    with.b_of_a = ra >= units;
+    with.lane_a = base + (with.b_of_a ? ra - units : ra);
+    with.b_of_b = rb >= units;
+    with.lane_b = base + (with.b_of_b ? rb - units : rb);
+    if (!split) with.lane_a = with.lane_b = base + lane;
+  }
+  const int64_t page = (ti.slot >> 32) * p.pool.page_stride;
+  const int token = (int)(ti.slot & 0xffffffff);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = r0 + k * slots;
+    const bool is_q = r < g.H, turned = r < n_rot, live = r < rows && stand;
+    float a[8], b[8], inv = 1.f;
+    va[k].get(a);
+    vb[k].get(b);
+    const E* gain = static_cast<const E*>(is_q ? p.q_gain : turned ? p.k_gain : nullptr);
+    if (p.q_gain || p.k_gain) {
+      // every lane of the warp takes part in the sum
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+      for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      inv = rsqrtf(ss * p.inv_d + p.eps);
+    }
+    const int at_a = turned ? ja : 16 * lane, at_b = turned ? jb : 16 * lane + 8;
+    const bool has = at_a < g.d;
+    float ma = 0.f, mb = 0.f;                      // the largest sums of products' magnitudes, of each run
+    if (turned && live && has) {
+      if (gain) {
+        Run<E> ga, gb;
+        ga.load(gain + at_a);
+        gb.load(gain + at_b);
+        float fa[8], fb[8];
+        ga.get(fa);
+        gb.get(fb);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] *= inv * fa[e];
+          b[e] *= inv * fb[e];
+        }
+        if (!is_q && !rotates) {
+          ma = __uint_as_float(largest(a));
+          mb = __uint_as_float(largest(b));
+        }
+      }
+      if (rotates && !p.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!is_q) {
+            ma = fmaxf(ma, fabsf(a[e] * c[e]) + fabsf(b[e] * s[e]));
+            mb = fmaxf(mb, fabsf(a[e] * s[e]) + fabsf(b[e] * c[e]));
+          }
+          turn(a[e], b[e], c[e], s[e]);
+        }
+      } else if (rotates) {
+        // pairs (2e, 2e + 1) of 16 neighbours: the first four in a, the others in b
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!is_q) {
+            ma = fmaxf(ma, fmaxf(fabsf(a[2 * e] * c[e]) + fabsf(a[2 * e + 1] * s[e]),
+                                 fabsf(a[2 * e] * s[e]) + fabsf(a[2 * e + 1] * c[e])));
+            mb = fmaxf(mb, fmaxf(fabsf(b[2 * e] * c[e + 4]) + fabsf(b[2 * e + 1] * s[e + 4]),
+                                 fabsf(b[2 * e] * s[e + 4]) + fabsf(b[2 * e + 1] * c[e + 4])));
+          }
+          turn(a[2 * e], a[2 * e + 1], c[e], s[e]);
+          turn(b[2 * e], b[2 * e + 1], c[e + 4], s[e + 4]);
+        }
+      }
+    }
+    if (is_q) {
+      if (r < rows && has) {
+        if (!stand) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;       // padding
+        }
+        E* dst = static_cast<E*>(p.q_out) + (int64_t)t * p.q_out_stride + r * g.d;
+        Run<E>::put(dst + at_a, a);
+        Run<E>::put(dst + at_b, b);
+      }
+    }
+    if (__all_sync(0xffffffffu, is_q || r >= rows)) continue;
+    // the blocks' maxima and errors: of this lane's runs, and of the runs beside them
+    uint32_t top_a = largest(a), top_b = largest(b);
+    const bool across = split && turned;
+    {
+      const uint32_t aa = __shfl_sync(0xffffffffu, top_a, with.lane_a), ab = __shfl_sync(0xffffffffu, top_b, with.lane_a);
+      const uint32_t ba = __shfl_sync(0xffffffffu, top_a, with.lane_b), bb = __shfl_sync(0xffffffffu, top_b, with.lane_b);
+      const uint32_t oa = across ? (with.b_of_a ? ab : aa) : top_b, ob = across ? (with.b_of_b ? bb : ba) : top_a;
+      top_a = max(top_a, oa);
+      top_b = max(top_b, ob);
+      const float eaa = __shfl_sync(0xffffffffu, ma, with.lane_a), eab = __shfl_sync(0xffffffffu, mb, with.lane_a);
+      const float eba = __shfl_sync(0xffffffffu, ma, with.lane_b), ebb = __shfl_sync(0xffffffffu, mb, with.lane_b);
+      const float ea = across ? (with.b_of_a ? eab : eaa) : mb, eb = across ? (with.b_of_b ? ebb : eba) : ma;
+      ma = fmaxf(ma, ea);
+      mb = fmaxf(mb, eb);
+    }
+    const float inv_g = turned ? p.k_inv : p.v_inv;
+    const bool inexact = turned && (gain || rotates);
+    bool near_border = false;
+    Codes w;
+    w.a = quantise(a, top_a, inv_g, ma * kMargin, inexact, &w.scale_a, &near_border);
+    w.b = quantise(b, top_b, inv_g, mb * kMargin, inexact, &w.scale_b, &near_border);
+    const bool keep = live && !is_q;
+    if (__any_sync(0xffffffffu, near_border && keep && has)) {
+      // every key row of the warp that is no plain copy; rows that are not stored stand in with the first of the keys
+      const bool again = keep && turned;
+      ExactRow x;
+      x.src = static_cast<const E*>(p.k) + (int64_t)t * p.k_stride + (again ? r - g.H : 0) * g.d;
+      x.gain = p.k_gain;
+      x.cos = rotates && stand ? cos : nullptr;
+      x.sin = sin;
+      x.ja = ja;
+      x.jb = jb;
+      x.lanes = p.lanes;
+      x.d = g.d;
+      x.interleaved = rotates && p.interleaved;
+      x.eps = p.eps;
+      x.inv_g = p.k_inv;
+      const Codes exact = exact_codes<E>(x, with, split);
+      if (again && inexact) {
+        if (w.scale_a != 0x7f) {
+          w.a = exact.a;
+          w.scale_a = exact.scale_a;
+        }
+        if (w.scale_b != 0x7f) {
+          w.b = exact.b;
+          w.scale_b = exact.scale_b;
+        }
+      }
+    }
+    if (!keep || !has) continue;
+    uint8_t* base = const_cast<uint8_t*>(turned ? p.pool.k : p.pool.v) + page + (turned ? r - g.H : r - n_rot) * p.pool.group_stride;
+    uint8_t* codes = base + token * 16 * p.pool.n;
+    if (at_b == at_a + 8) {
+      *reinterpret_cast<uint2*>(codes + at_a / 2) = make_uint2(w.a, w.b);
+      base[kv4_scale_at(p.pool, token, at_a / 16)] = (uint8_t)w.scale_a;
+    } else {
+      *reinterpret_cast<uint32_t*>(codes + at_a / 2) = w.a;
+      *reinterpret_cast<uint32_t*>(codes + at_b / 2) = w.b;
+      if (!(at_a & 8)) base[kv4_scale_at(p.pool, token, at_a / 16)] = (uint8_t)w.scale_a;
+      if (!(at_b & 8)) base[kv4_scale_at(p.pool, token, at_b / 16)] = (uint8_t)w.scale_b;
+    }
+    if ((g.d & 16) && lane == 0) {                 // the last chunk's other half
+      *reinterpret_cast<uint2*>(codes + g.d / 2) = make_uint2(0, 0);
+      base[kv4_scale_at(p.pool, token, g.d / 16)] = 0;
+    }
+  }
+}
+
+template <typename E>
+aff_status launch(AppendParams& p, cudaStream_t s) {
+  const int units = p.g.d / 16;
+  p.lanes = 1;
+  p.lane_bits = 0;
+  while (p.lanes < units) {
+    p.lanes *= 2;
+    ++p.lane_bits;
+  }
+  p.inv_d = 1.f / (float)p.g.d;
+  const int need = (p.g.H + 2 * p.g.G + 1) / 2 * p.lanes;
+  const int threads = need < kThreads ? (need + 31) / 32 * 32 : kThreads;
+  AFF_CUDA(launch_pdl(kv4_append_kernel<E>, dim3((unsigned)p.g.T, (unsigned)((need + threads - 1) / threads)), threads, 0,
+                      s, p));
+  return AFF_OK;
+}
+
+// ---------------------------------------------------------------- reading back
+struct ReadParams {
+  StepGeom g;
+  Kv4Pool pool;
+  void *k_out, *v_out;
+  float k_scale, v_scale;
+};
+
+// Eight elements to a thread, kTokens tokens of a block one after the other: 4 bytes of codes and a scale in, 16 or 32
+// bytes out, neighbours beside each other on both sides.  Bound by the bytes written.
+constexpr int kTokens = 4;
+template <typename E>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ ReadParams p) {
+  pdl_enter();
+  const StepGeom& g = p.g;
+  const bool fits = plan_matches(g);
+  if (!fits || g.head->n_items < 0) {
+    if (threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : 1);
+    return;
+  }
+  const int per = g.d / 8, pieces = 2 * g.G * per;
+  const int i = blockIdx.y * kThreads + threadIdx.x;
+  if (i >= pieces) return;
+  const int value = i >= pieces / 2, rest = i - value * (pieces / 2), group = rest / per, piece = rest - group * per;
+  const uint8_t* pool = (value ? p.pool.v : p.pool.k) + group * p.pool.group_stride;
+  E* out = static_cast<E*>(value ? p.v_out : p.k_out) + group * g.d + piece * 8;
+  const float scale = value ? p.v_scale : p.k_scale;
+  const int t0 = blockIdx.x * kTokens;
+  uint32_t w[kTokens], sc[kTokens];
+#pragma unroll
+  for (int x = 0; x < kTokens; ++x) {
+    w[x] = sc[x] = 0;
+    if (t0 + x >= g.T) continue;
+    const TokenInfo ti = g.tok[t0 + x];
+    if (ti.own < 0) {
+      if (ti.own == -2 && i == 0) latch_status(&g.head->status, kStatusRange);
+      continue;
+    }
+    const int token = (int)(ti.slot & 0xffffffff);
+    const uint8_t* at = pool + (ti.slot >> 32) * p.pool.page_stride;
+    w[x] = __ldg(reinterpret_cast<const uint32_t*>(at + token * 16 * p.pool.n + piece * 4));
+    sc[x] = __ldg(at + kv4_scale_at(p.pool, token, piece >> 1));
+  }
+#pragma unroll
+  for (int x = 0; x < kTokens; ++x) {
+    if (t0 + x >= g.T) break;
+    uint32_t h[4];
+    kv4_decode(w[x], h);
+    const uint32_t s2 = kv4_scale_pair(sc[x] | sc[x] << 8);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = mul_f16x2(h[e], s2);        // exact
+      asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+          : "=f"(f[2 * e]), "=f"(f[2 * e + 1])
+          : "r"(v));
+      f[2 * e] *= scale;
+      f[2 * e + 1] *= scale;
+    }
+    Run<E>::put(out + (int64_t)(t0 + x) * g.G * g.d, f);
+  }
+}
+
+}  // namespace
+}  // namespace aff
+
+using namespace aff;
+
+extern "C" aff_status affinity_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                          const void* v, int64_t v_stride, const aff_kv4_cache* cache,
+                                          const aff_step* step, const aff_rotary* rotary, void* q_out,
+                                          int64_t q_out_stride, void* plan, size_t plan_bytes, aff_stream_t stream) {
+  AppendParams p{};
+  aff_status st = kv4_geom(step, cache, plan, &p.g);
+  if (st != AFF_OK) return st;
+  if (!q || !k || !v || !q_out || !rotary) return AFF_ERR_INVALID_ARG;
+  const StepGeom& g = p.g;
+  const int64_t hd = (int64_t)g.H * g.d, gd = (int64_t)g.G * g.d;
+  if (q_stride < hd || k_stride < gd || v_stride < gd || q_out_stride < hd) return AFF_ERR_INVALID_ARG;
+  if (rotary->rot < 0 || rotary->rot % 2 || rotary->n_pos < 0 || (rotary->rot > 0 && (!rotary->cos || !rotary->sin)) ||
+      !(std::isfinite(rotary->eps) && rotary->eps >= 0.f))
+    return AFF_ERR_INVALID_ARG;
+  if (rotary->rot > g.d || rotary->rot % 16) return AFF_ERR_UNSUPPORTED_SHAPE;
+  const int es = g.dtype == AFF_BF16 ? 2 : 4;
+  const void* ptrs[] = {q, k, v, q_out, rotary->cos, rotary->sin, rotary->q_gain, rotary->k_gain};
+  for (const void* x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return AFF_ERR_ALIGNMENT;
+  if (q_stride * es % 16 || k_stride * es % 16 || v_stride * es % 16 || q_out_stride * es % 16)
+    return AFF_ERR_ALIGNMENT;
+  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AFF_OK) return st;
+  p.pool = kv4_pool(cache);
+  p.q = q; p.k = k; p.v = v; p.q_out = q_out;
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.q_out_stride = q_out_stride;
+  p.cos = rotary->cos; p.sin = rotary->sin;
+  p.q_gain = rotary->q_gain; p.k_gain = rotary->k_gain;
+  p.n_pos = rotary->rot ? rotary->n_pos : INT64_MAX;
+  p.eps = rotary->eps;
+  p.k_inv = 1.f / cache->k_scale;
+  p.v_inv = 1.f / cache->v_scale;
+  p.rot = rotary->rot;
+  p.interleaved = rotary->interleaved != 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return g.dtype == AFF_BF16 ? launch<__nv_bfloat16>(p, s) : launch<float>(p, s);
+}
+
+extern "C" aff_status affinity_kv4_read(const aff_kv4_cache* cache, const aff_step* step, void* k_out, void* v_out,
+                                        void* plan, size_t plan_bytes, aff_stream_t stream) {
+  ReadParams p{};
+  aff_status st = kv4_geom(step, cache, plan, &p.g);
+  if (st != AFF_OK) return st;
+  if (!k_out || !v_out) return AFF_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15u) return AFF_ERR_ALIGNMENT;
+  const StepGeom& g = p.g;
+  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AFF_OK) return st;
+  p.pool = kv4_pool(cache);
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  const unsigned pieces = 2u * g.G * (g.d / 8);
+  const dim3 grid((unsigned)((g.T + kTokens - 1) / kTokens), (pieces + kThreads - 1) / kThreads);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (g.dtype == AFF_BF16) AFF_CUDA(launch_pdl(kv4_read_kernel<__nv_bfloat16>, grid, kThreads, 0, s, p));
+  else AFF_CUDA(launch_pdl(kv4_read_kernel<float>, grid, kThreads, 0, s, p));
+  return AFF_OK;
+}

@@ -35,6 +35,7 @@ namespace aff {
 
 constexpr int kKeyTile = 128;            // most keys of a tile
 constexpr int kFewRows = 16;             // most rows of an item that takes the few-rows path
+constexpr int kKv4FewRows = 8;           // the same over a cache in 4 bits (kv4_attention.cu)
 constexpr int kPlanSms = 152;            // SMs of a GB300: sizes the plan without a device
 
 // Division of 0 <= x < 2^31 by a number known on the host: a multiply, an add and a shift, where the
@@ -75,7 +76,7 @@ struct WorkItem {        // 48 bytes
 };
 // alt == 0: stream s holds rows s*128 .. of the item and walks tiles t0 .. t0 + n_s - 1.
 // alt == 1: at most 128 rows; both streams hold them, stream s walks tiles t0 + s, t0 + s + 2, ...
-// alt == 2: at most 16 rows, for which a tile is split over warps by its keys; n0 tiles.
+// alt == 2: few rows (StepGeom::few_rows), for which a tile is split over warps by its keys; n0 tiles.
 // Its higher bits are 0 but for a call under way (attention.cu).
 
 struct PlanHeader {      // at the start of the plan buffer; its first word is the status word
@@ -88,6 +89,10 @@ struct PlanHeader {      // at the start of the plan buffer; its first word is t
   uint32_t key[4];       // a hash of the geometry it was made for
   uint32_t claimed;      // items claimed beyond the first of every CTA, and CTAs done, in the call
   uint32_t done;         // under way; the last CTA sets both back to 0
+  uint32_t few_claimed;  // the same of the kernel that takes the few-rows items of a cache in 4 bits
+  uint32_t few_done;
+  int32_t tile_end;      // over a cache in 4 bits: the items before it hold all that are not few-rows items,
+  int32_t few_begin;     // and those from here on all that are
 };
 
 // Everything the kernels need to know of the step, by value.
@@ -100,9 +105,11 @@ struct StepGeom {
   int32_t page_tiles;    // tiles of a page then, else 0
   int32_t np;            // key tiles of the prefix
   int32_t separate;      // the prefix has jobs of its own
-  int32_t few;           // items of at most kFewRows rows take the few-rows path
+  int32_t kv4;           // the cache is in 4 bits (kv4.cuh)
+  int32_t few, few_rows; // items of at most few_rows rows take the few-rows path
   int32_t may_split;     // jobs may be cut (then the join kernel runs)
   int32_t small, big;    // row tiles
+  int32_t cut_rows;      // partial rows for cuts: so many for every SM, twice
   int32_t prefix_rows;   // row tile of the prefix's jobs
   int32_t prefix_tiles;  // row tiles of the prefix's jobs
   int32_t max_items, max_part_rows;
@@ -120,11 +127,17 @@ struct StepGeom {
   size_t bytes;
 };
 
-// Validates (step, cache) and lays the plan out over `plan` (may be null).
-aff_status step_geom(const aff_step* step, const aff_kv_cache* cache, void* plan, StepGeom* g);
+// Validates (step, cache) and lays the plan out over `plan` (may be null).  kv4: `cache` stands for one in 4 bits.
+aff_status step_geom(const aff_step* step, const aff_kv_cache* cache, void* plan, StepGeom* g, bool kv4 = false);
+
+// The same for a cache in 4 bits.
+aff_status kv4_geom(const aff_step* step, const aff_kv4_cache* cache, void* plan, StepGeom* g);
 
 // The plan buffer of a call: present, aligned, large enough.
 aff_status check_plan(const StepGeom& g, const void* plan, size_t plan_bytes);
+
+// Merges the partial rows of an attention call into its output (attention.cu).
+aff_status launch_join(const StepGeom& g, void* out, float* lse, cudaStream_t stream);
 
 #ifdef __CUDACC__
 __host__ __device__ inline int ceil_div_i(int a, int b) { return (a + b - 1) / b; }

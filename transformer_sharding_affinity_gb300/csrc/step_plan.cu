@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 namespace aff {
@@ -96,11 +97,13 @@ __device__ void plan_items(const StepGeom& g) {
   __shared__ int64_t wide_sh[32];
   __shared__ int sh[32];
   __shared__ int s_q0[kThreads], s_q1[kThreads], s_kv[kThreads], s_item[kThreads], s_row[kThreads], s_most[kThreads];
-  __shared__ int s_min, s_max, s_parts[2];
+  __shared__ int s_min, s_max, s_parts[2], s_tile_end, s_few_begin;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x;
   if (me == 0) {
     s_min = INT32_MAX;
     s_max = 0;
+    s_tile_end = 0;
+    s_few_begin = INT32_MAX;
   }
   auto load = [&](int b) {       // sequence b as given; false if it is malformed
     s_q0[me] = s_q1[me] = s_kv[me] = 0;
@@ -158,13 +161,13 @@ __device__ void plan_items(const StepGeom& g) {
     }
     __syncthreads();
     // fp32: two CTAs per SM, tiles that take some four times as long
-    const bool f32 = g.dtype != AFF_BF16;
+    const bool f32 = g.dtype != AFF_BF16 && !g.kv4;
     const int slots = f32 ? 2 * kPlanSms : kPlanSms, tile = f32 ? 4 : 1;
     const int start = g.few ? 2 : 5;      // an item's beginning and end, in the cost of a bf16 tile
     if (warp < 2) {                                // warp 0: own jobs, warp 1: the prefix's
       // half of the room for cuts (a row tile for every SM and stream) each
       const int64_t row_jobs = (warp ? (int64_t)g.prefix_tiles * g.prefix_rows : rows_all) * g.G;     // rows of a part
-      const int64_t most = 1 + (int64_t)kPlanSms * g.big / max(row_jobs, (int64_t)1);
+      const int64_t most = 1 + (int64_t)kPlanSms * g.cut_rows / max(row_jobs, (int64_t)1);
       const int parts = warp ? best_parts((int64_t)g.prefix_tiles * g.G, (int64_t)g.np * prefix_streams,
                                           (int)min(most, (int64_t)kMaxParts), slots, tile, start)
                              : best_parts(jobs * g.G, s_max, (int)min(most, (int64_t)kMaxParts), slots, tile, start);
@@ -246,7 +249,7 @@ __device__ void plan_items(const StepGeom& g) {
         const int nrows = min(s.tr, s.rows - r0);
         const int slot_rows = s.nt == 1 ? s.rows : s.tr;
         const bool direct = j.parts == 1 && !g.separate;
-        const int alt = g.dtype != AFF_BF16 ? 0 : g.few && nrows <= kFewRows ? 2 : nrows <= 128;
+        const int alt = g.few && nrows <= g.few_rows ? 2 : g.dtype != AFF_BF16 ? 0 : nrows <= 128;
         const int first = key_tiles(g, s, r0 + 128);    // key tiles that stream 0's rows meet
         WorkItem it;
         it.row0 = s.q0 * g.R + r0;
@@ -274,6 +277,10 @@ __device__ void plan_items(const StepGeom& g) {
           it.part_row = direct ? -1 : s_row[x] + ((j.group * s.nt + j.k) * s_most[x] + p) * slot_rows;
           g.items[w] = it;
         }
+        if (g.kv4 && j.parts > 0) {
+          if (alt == 2) atomicMin(&s_few_begin, w - j.parts);
+          else atomicMax(&s_tile_end, w);
+        }
       }
     }
   }
@@ -292,7 +299,11 @@ __device__ void plan_items(const StepGeom& g) {
     it.seq = -1;
     it.t0 = p * prefix_per;
     const int n = min(prefix_per, g.np - it.t0);
-    it.alt = g.dtype != AFF_BF16 ? 0 : g.few && it.nrows <= kFewRows ? 2 : it.nrows <= 128;
+    it.alt = g.few && it.nrows <= g.few_rows ? 2 : g.dtype != AFF_BF16 ? 0 : it.nrows <= 128;
+    if (g.kv4) {
+      if (it.alt == 2) atomicMin(&s_few_begin, i);
+      else atomicMax(&s_tile_end, i + 1);
+    }
     it.n0 = it.alt == 1 ? (n + 1) / 2 : n;
     it.n1 = it.alt == 1 ? n / 2 : it.alt == 2 || g.dtype != AFF_BF16 ? 0 : n;
     it.part_row = ((group * g.prefix_tiles + k) * prefix_parts + p) * g.prefix_rows;
@@ -315,16 +326,24 @@ __device__ void plan_items(const StepGeom& g) {
       it.group = i % g.G;
       it.seq = -1;
       it.part_row = -1;
+      if (g.kv4 && g.dtype != AFF_BF16) it.alt = 2;
+      if (g.kv4) {
+        if (it.alt == 2) atomicMin(&s_few_begin, item_base + i);
+        else atomicMax(&s_tile_end, item_base + i + 1);
+      }
       g.items[item_base + i] = it;
     }
     item_base += n * g.G;
   }
+  if (g.kv4) __syncthreads();
   if (threadIdx.x == 0) {
     PlanHeader& h = *g.head;
     h.n_items = min(item_base, g.max_items);
     h.unit = unit;
     h.prefix_parts = prefix_parts;
     h.prefix_per = prefix_per;
+    h.tile_end = min(s_tile_end, h.n_items);
+    h.few_begin = min(s_few_begin, h.n_items);
   }
 }
 
@@ -371,7 +390,7 @@ aff_status check_plan(const StepGeom& g, const void* plan, size_t plan_bytes) {
   return AFF_OK;
 }
 
-aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, StepGeom* out) {
+aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, StepGeom* out, bool kv4) {
   if (!st || !c) return AFF_ERR_INVALID_ARG;
   if (c->dtype != AFF_BF16 && c->dtype != AFF_FP32) return AFF_ERR_UNSUPPORTED_DTYPE;
   if (!c->k || !c->v || !st->q_start || !st->kv_len || !st->pages) return AFF_ERR_INVALID_ARG;
@@ -420,7 +439,9 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   g.by_tile.set((uint32_t)g.key_tile);
   g.by_page_tiles.set((uint32_t)std::max(g.page_tiles, 1));
   g.np = segment_tiles(g, g.prefix_len);
-  const int64_t all[10] = {g.T, g.B, g.H, g.G, g.d, g.page_size, g.pages_stride, g.prefix_len, g.dtype, g.n_pages};
+  g.kv4 = kv4;
+  const int64_t all[10] = {g.T, g.B, g.H, g.G, g.d, g.page_size, g.pages_stride, g.prefix_len, g.dtype + (kv4 ? 256 : 0),
+                           g.n_pages};
   for (int i = 0; i < 4; ++i) {
     uint64_t h = 0x9e3779b97f4a7c15ull * (i + 1);
     for (int64_t v : all) {
@@ -430,8 +451,10 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     g.key[i] = (uint32_t)(h >> 16);
   }
   const bool bf = c->dtype == AFF_BF16;
-  g.small = bf ? 128 : 16;
-  g.big = bf ? 256 : 64;
+  // (over a cache in 4 bits: 8 rows at a time in fp32, where every row tile takes the few-rows path)
+  g.small = kv4 && !bf ? kKv4FewRows : bf ? 128 : 16;
+  g.big = kv4 && !bf ? kKv4FewRows : bf ? 256 : 64;
+  g.cut_rows = bf ? 256 : 64;
   const int64_t rows = (int64_t)g.T * g.R;
   // Jobs of its own for the prefix: worth it while sequences have less than a row tile on average, which
   // would then be mostly idle for every key of the prefix (64 single tokens behind 8192 keys: 69 us, 359
@@ -442,7 +465,8 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   // The few-rows path where sequences have few rows on average (64 single tokens: 69 us, 98 without); the kernel
   // without it is faster (64 x 1024 tokens: 280 us, 338 with it; 8 x 17 tokens, 34 rows each, over 3000 keys: 48 and
   // 50).  It goes by the whole step: single tokens beside prompts take the tensor tiles.
-  g.few = bf && rows <= (int64_t)g.B * 32;
+  g.few = (bf && rows <= (int64_t)g.B * 32) || (kv4 && !bf);
+  g.few_rows = kv4 ? kKv4FewRows : kFewRows;
   g.prefix_rows = rows <= g.small ? g.small : g.big;
   g.prefix_tiles = g.separate ? (int)((rows + g.prefix_rows - 1) / g.prefix_rows) : 0;
   // Most (row tile, group) pairs: each sequence ends in at most one part-filled tile.
@@ -457,7 +481,7 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
     // (a sequence of several row tiles rounds up to whole ones); joined, they write the output.
     // On top of that, room for cuts.
     const int64_t multi = std::min<int64_t>(g.B, rows / g.small + 1);
-    part_rows = (int64_t)kPlanSms * 2 * g.big;
+    part_rows = (int64_t)kPlanSms * 2 * g.cut_rows;
     if (g.separate) part_rows += ((int64_t)g.prefix_tiles * g.prefix_rows + rows + multi * g.big) * g.G;
   }
   if (items > INT32_MAX / 64 || part_rows > INT32_MAX / 2) return AFF_ERR_UNSUPPORTED_SHAPE;
@@ -481,6 +505,36 @@ aff_status step_geom(const aff_step* st, const aff_kv_cache* c, void* plan, Step
   return AFF_OK;
 }
 
+aff_status kv4_geom(const aff_step* st, const aff_kv4_cache* c, void* plan, StepGeom* out) {
+  if (!c) return AFF_ERR_INVALID_ARG;
+  if (c->dtype != AFF_BF16 && c->dtype != AFF_FP32) return AFF_ERR_UNSUPPORTED_DTYPE;
+  const float scales[2] = {c->k_scale, c->v_scale};
+  for (float s : scales) {
+    int e = 0;
+    if (!(s > 0.f) || !std::isfinite(s) || std::frexp(s, &e) != 0.5f || e < -29 || e > 31) return AFF_ERR_INVALID_ARG;
+  }
+  if (c->page_stride < 0 || c->group_stride < 0) return AFF_ERR_INVALID_ARG;
+  if (c->d_head % 16) return AFF_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_stride % 16 || c->group_stride % 16) return AFF_ERR_ALIGNMENT;
+  const aff_kv_cache like{c->k, c->v, c->n_pages, c->page_stride, c->group_stride, c->d_head, c->G, c->page_size,
+                          c->d_head, c->dtype};
+  return step_geom(st, &like, plan, out, true);
+}
+
+namespace {
+
+aff_status launch_plan(const StepGeom& g, void* plan, size_t plan_bytes, aff_stream_t stream) {
+  aff_status st;
+  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AFF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  AFF_CUDA(cudaMemsetAsync(plan, 0, sizeof(PlanHeader), s));
+  AFF_CUDA(launch_pdl(step_plan_kernel, 1 + (g.T + kThreads - 1) / kThreads, kThreads, 0, s, g));
+  return AFF_OK;
+}
+
+}  // namespace
 }  // namespace aff
 
 using namespace aff;
@@ -501,13 +555,31 @@ aff_status affinity_step_plan(const aff_step* step, const aff_kv_cache* cache, v
   StepGeom g;
   aff_status st = step_geom(step, cache, plan, &g);
   if (st != AFF_OK) return st;
-  if ((st = check_plan(g, plan, plan_bytes)) != AFF_OK) return st;
-  int sms = 0;
-  if ((st = check_device(&sms)) != AFF_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  AFF_CUDA(cudaMemsetAsync(plan, 0, sizeof(PlanHeader), s));
-  AFF_CUDA(launch_pdl(step_plan_kernel, 1 + (g.T + kThreads - 1) / kThreads, kThreads, 0, s, g));
+  return launch_plan(g, plan, plan_bytes, stream);
+}
+
+aff_status affinity_kv4_page_bytes(int32_t page_size, int32_t d_head, size_t* bytes) {
+  if (!bytes || page_size < 1 || d_head < 1) return AFF_ERR_INVALID_ARG;
+  if (page_size % 8 || page_size > (1 << 20) || d_head % 16 || d_head > 256) return AFF_ERR_UNSUPPORTED_SHAPE;
+  *bytes = (size_t)page_size * ((d_head + 31) / 32) * 18;
   return AFF_OK;
+}
+
+aff_status affinity_kv4_plan_size(const aff_step* step, const aff_kv4_cache* cache, size_t* bytes) {
+  if (!bytes) return AFF_ERR_INVALID_ARG;
+  StepGeom g;
+  aff_status st = kv4_geom(step, cache, nullptr, &g);
+  if (st != AFF_OK) return st;
+  *bytes = g.bytes;
+  return AFF_OK;
+}
+
+aff_status affinity_kv4_plan(const aff_step* step, const aff_kv4_cache* cache, void* plan, size_t plan_bytes,
+                             aff_stream_t stream) {
+  StepGeom g;
+  aff_status st = kv4_geom(step, cache, plan, &g);
+  if (st != AFF_OK) return st;
+  return launch_plan(g, plan, plan_bytes, stream);
 }
 
 }  // extern "C"
