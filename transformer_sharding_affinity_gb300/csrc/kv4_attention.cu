@@ -9,26 +9,27 @@
 //                 nothing above 2^-31 is lost.
 // fp32 queries and probabilities are the sum of two fp16 numbers each, 22 bits, and two products.
 #include "affinity.h"
+#include "attention_parts.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "launch.cuh"
 #include "sm103_primitives.cuh"
 #include "step.cuh"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 namespace aff {
 namespace {
 
-constexpr float kRescale = 8.f;              // log2 growth of the maximum that O is rescaled for
 constexpr float kShift = 7.f;                // log2 of the probabilities' factor: they stay below 2^15
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr uint32_t kStatusInvalid = 1;
 
 struct Kv4AttnParams {
   StepGeom g;
@@ -41,19 +42,9 @@ struct Kv4AttnParams {
   float v_scale;
 };
 
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ float2 halves(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
@@ -63,21 +54,6 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Transpose of an 8 x 8 matrix of 16-bit elements, two to a lane.
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ WorkItem load_item(const WorkItem* p) {
-  WorkItem it;
-  const int4* s = reinterpret_cast<const int4*>(p);
-  int4* d = reinterpret_cast<int4*>(&it);
-  d[0] = s[0];
-  d[1] = s[1];
-  d[2] = s[2];
-  return it;
 }
 // The factor of a row of queries (its largest magnitude, as bits) and the inverse, both powers of two.
 __device__ __forceinline__ float query_factor(uint32_t top, float* inverse) {
@@ -129,7 +105,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
   pdl_enter();
   const StepGeom& g = p.g;
   const bool fits = plan_matches(g);
-  const int n_items = fits ? g.head->n_items : 0;
+  const int n_items = fits ? g.head->n_items : 0, first_item = fits ? g.head->few_begin : 0;
   if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : kStatusInvalid);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, c = lane & 3;
   const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of a unit: k_off, k_off + 2
@@ -140,364 +116,365 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
   if (threadIdx.x < 8) nan_key[0][threadIdx.x] = INT32_MAX;
   int turn = 0;
 
-  for (int i = blockIdx.x; i < n_items; i = claim) {
+  // the first item by number, the others from the counter
+  for (int i = first_item + blockIdx.x; i < n_items; i = claim, turn ^= 1) {
     const WorkItem it = load_item(g.items + i);
-    const int n = it.alt == 1 ? it.n0 + it.n1 : it.alt == 2 ? it.n0 : it.n1;
-    for (int r0 = 0; r0 < it.nrows; r0 += 8, turn ^= 1) {
-      const int nrows = min(it.nrows - r0, 8), row0 = it.row0 + r0;
-      __syncthreads();                       // what lies in shared memory has been read
-      if (threadIdx.x == 0 && r0 == 0) claim = gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
-      if (threadIdx.x < 8) nan_key[turn ^ 1][threadIdx.x] = INT32_MAX;
-
-      // ---- queries: B operand of S^T, row quad
-      uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
-      float inverse;
-      {
-        const int rr = row0 + quad, tok = g.by_R(rr);
-        const int64_t at = (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-        float x[8 * W];
-        uint32_t top = 0;
+    const int n = it.n0, nrows = it.nrows, row0 = it.row0;
+    __syncthreads();                         // what lies in shared memory has been read
+    if (threadIdx.x == 0) claim = first_item + gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
+    if (threadIdx.x < 8) nan_key[turn ^ 1][threadIdx.x] = INT32_MAX;
+    if (it.alt != 2) {                       // the other kernel's
+      __syncthreads();
+      continue;
+    }
+    // ---- queries: B operand of S^T, row quad
+    uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
+    float inverse;
+    {
+      const int rr = row0 + quad, tok = g.by_R(rr);
+      const int64_t at = (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+      float x[8 * W];
+      uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int e0 = 8 * W * c + 8 * j;
-          const bool has = quad < nrows && e0 < g.d;
-          if constexpr (F32) {
-            const float* src = static_cast<const float*>(p.q) + at + e0;
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 a = has ? __ldg(reinterpret_cast<const float4*>(src)) : z;
-            const float4 b = has ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
-            x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
-            x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
-          } else {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (has) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e0));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
-              x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float f = query_factor(top, &inverse);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
-            qh[s][h] = f16x2(a, b);
-            if constexpr (F32) {
-              const float2 r = halves(qh[s][h]);
-              ql[s][h] = f16x2(a - r.x, b - r.y);
-            }
-          }
-      }
-      // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
-      float sc[2], m[2], l[2], o[MT][4];
-      int own_vis[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 2 * c + e;
-        sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
-        own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
-        m[e] = -INFINITY;
-        l[e] = 0.f;
-      }
-      const int all_see = it.seq < 0 ? INT32_MAX : g.by_R(row0) + it.own_off + 1;    // own keys that every row sees
-#pragma unroll
-      for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-
-      // ---- the walk over this warp's units
-      const uint8_t* const kg = p.pool.k + it.group * p.pool.group_stride;
-      const uint8_t* const vg = p.pool.v + it.group * p.pool.group_stride;
-      const int end = it.t0 + n;
-      auto locate = [&](FewUnit& u) {        // the unit at (tile, sub) or the next one that holds a key; asks for its page
-        u.keys = 0;
-        u.page = -1;
-        while (u.tile < end) {
-          u.pre = u.tile < it.np;
-          int first;
-          const int keys = tile_span(g, u.pre ? g.prefix_len : it.own_len, u.pre ? u.tile : u.tile - it.np, &first) - 16 * u.sub;
-          u.key0 = first + 16 * u.sub;
-          u.sub += 8;
-          while (u.sub >= subs) {
-            u.sub -= subs;
-            ++u.tile;
-          }
-          if (keys > 0) {
-            u.keys = min(keys, 16);
-            break;
-          }
-        }
-        if (4 * c < u.keys) {
-          const int32_t* table = u.pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-          const int pi = g.by_page(u.key0 + 4 * c);
-          u.page = __ldg(table + pi);
-          u.in_page = u.key0 + 4 * c - pi * g.page_size;
-        }
-      };
-      auto load = [&](FewRaw<NC>& r, FewUnit& u) {
-        if (4 * c < u.keys && (u.page < 0 || u.page >= g.n_pages)) {      // read as zeros: report it
-          latch_status(&g.head->status, kStatusRange);
-          u.page = -1;
-        }
-        const int kp = __shfl_sync(0xffffffffu, u.page, quad >> 1), ki = __shfl_sync(0xffffffffu, u.in_page, quad >> 1);
-#pragma unroll
-        for (int x = 0; x < W; ++x) r.k[0][x] = r.k[1][x] = 0;
-#pragma unroll
-        for (int x = 0; x < (W == 4 ? 2 : 1); ++x) r.ks[x] = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int y = 0; y < VW; ++y) r.v[x][y] = 0;
-        r.vs = 0;
-        if (kp >= 0 && k0_has) {
-          const uint8_t* page = kg + kp * p.pool.page_stride;
-          const uint8_t* at = page + (ki + (quad & 1)) * 16 * p.pool.n + c * 4 * W;
-          const uint8_t* s = page + p.pool.scales + ((ki >> 2) * 2 * p.pool.n + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
-#pragma unroll
-          for (int x = 0; x < 2; ++x, at += 32 * p.pool.n) {
-            if constexpr (W == 4) {
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
-              r.k[x][0] = w.x; r.k[x][1] = w.y; r.k[x][2] = w.z; r.k[x][3] = w.w;
-            } else if constexpr (W == 2) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
-              r.k[x][0] = w.x; r.k[x][1] = w.y;
-            } else {
-              r.k[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-            }
-          }
-          if constexpr (W == 4) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(s));
-            r.ks[0] = w.x;
-            r.ks[1] = k1_has ? w.y : 0;
-          } else {
-            r.ks[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-          }
-        }
-        if (u.page >= 0 && v_has) {
-          const uint8_t* page = vg + u.page * p.pool.page_stride;
-          const uint8_t* at = page + u.in_page * 16 * p.pool.n + quad * 2 * W;
-#pragma unroll
-          for (int x = 0; x < 4; ++x, at += 16 * p.pool.n) {
-            if constexpr (W == 4) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
-              r.v[x][0] = w.x; r.v[x][1] = w.y;
-            } else if constexpr (W == 2) {
-              r.v[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-            } else {
-              r.v[x][0] = __ldg(reinterpret_cast<const uint16_t*>(at));
-            }
-          }
-          r.vs = __ldg(reinterpret_cast<const uint32_t*>(page + p.pool.scales + ((u.in_page >> 2) * 2 * p.pool.n + v_block) * 4));
-          const int left = u.keys - 4 * c;
-          if (left < 4) r.vs &= (1u << 8 * left) - 1;       // keys past the end: zero
-        }
-      };
-      auto work = [&](const FewRaw<NC>& r, const FewUnit& u) {
-        // ---- scores
-        uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
-        if constexpr (W == 4) {
-          const uint32_t b = quad & 1;
-          const uint32_t a2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], b | (4 + b) << 4));
-          const uint32_t b2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], (b + 2) | (b + 6) << 4));
-          ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
-          kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
+      for (int j = 0; j < W; ++j) {
+        const int e0 = 8 * W * c + 8 * j;
+        const bool has = quad < nrows && e0 < g.d;
+        if constexpr (F32) {
+          const float* src = static_cast<const float*>(p.q) + at + e0;
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 a = has ? __ldg(reinterpret_cast<const float4*>(src)) : z;
+          const float4 b = has ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
+          x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
+          x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
         } else {
-          const uint32_t b = quad & 1;
-          const uint32_t two = kv4_scale_pair(prmt(r.ks[0], 0, b | (b + 2) << 4));
-          ka[0] = ka[1] = prmt(two, two, 0x1010);
-          kb[0] = kb[1] = prmt(two, two, 0x3232);
-        }
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (has) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e0));
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          uint32_t a[4], b[4];
-          kv4_decode(r.k[0][w], a);
-          kv4_decode(r.k[1][w], b);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = mul_f16x2(a[e], ka[w >> 1]);
-            b[e] = mul_f16x2(b[e], kb[w >> 1]);
+          for (int y = 0; y < 4; ++y) {
+            x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
+            x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
           }
-          mma_16x8x16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
-          mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float f = query_factor(top, &inverse);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
+          qh[s][h] = f16x2(a, b);
           if constexpr (F32) {
-            mma_16x8x16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
-            mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
+            const float2 r = halves(qh[s][h]);
+            ql[s][h] = f16x2(a - r.x, b - r.y);
           }
         }
+    }
+    // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
+    float sc[2], m[2], l[2], o[MT][4];
+    int own_vis[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += s2[e];
-        // ---- s[e]: key k_off, row 2 c + e; s[2 + e]: key k_off + 2
-        if (!(u.keys == 16 && all_see > 0 && (u.pre || u.key0 + 16 <= all_see))) {
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * c + e;
+      sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
+      own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+    }
+    const int all_see = it.seq < 0 ? INT32_MAX : g.by_R(row0) + it.own_off + 1;    // own keys that every row sees
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int vis = own_vis[e] <= 0 ? 0 : u.pre ? u.keys : min(u.keys, own_vis[e] - u.key0);
-            if (k_off >= vis) s[e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
-            if (k_off + 2 >= vis) s[2 + e] = -INFINITY;
+    for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+    // ---- the walk over this warp's units
+    const uint8_t* const kg = p.pool.k + it.group * p.pool.group_stride;
+    const uint8_t* const vg = p.pool.v + it.group * p.pool.group_stride;
+    const int end = it.t0 + n;
+    auto locate = [&](FewUnit& u) {        // the unit at (tile, sub) or the next one that holds a key; asks for its page
+      u.keys = 0;
+      u.page = -1;
+      while (u.tile < end) {
+        u.pre = u.tile < it.np;
+        int first;
+        const int keys = tile_span(g, u.pre ? g.prefix_len : it.own_len, u.pre ? u.tile : u.tile - it.np, &first) - 16 * u.sub;
+        u.key0 = first + 16 * u.sub;
+        u.sub += 8;
+        while (u.sub >= subs) {
+          u.sub -= subs;
+          ++u.tile;
+        }
+        if (keys > 0) {
+          u.keys = min(keys, 16);
+          break;
+        }
+      }
+      if (4 * c < u.keys) {
+        const int32_t* table = u.pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+        const int pi = g.by_page(u.key0 + 4 * c);
+        u.page = __ldg(table + pi);
+        u.in_page = u.key0 + 4 * c - pi * g.page_size;
+      }
+    };
+    auto load = [&](FewRaw<NC>& r, FewUnit& u) {
+      if (4 * c < u.keys && (u.page < 0 || u.page >= g.n_pages)) {      // read as zeros: report it
+        latch_status(&g.head->status, kStatusRange);
+        u.page = -1;
+      }
+      const int kp = __shfl_sync(0xffffffffu, u.page, quad >> 1), ki = __shfl_sync(0xffffffffu, u.in_page, quad >> 1);
+#pragma unroll
+      for (int x = 0; x < W; ++x) r.k[0][x] = r.k[1][x] = 0;
+#pragma unroll
+      for (int x = 0; x < (W == 4 ? 2 : 1); ++x) r.ks[x] = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < VW; ++y) r.v[x][y] = 0;
+      r.vs = 0;
+      if (kp >= 0 && k0_has) {
+        const uint8_t* page = kg + kp * p.pool.page_stride;
+        const uint8_t* at = page + (ki + (quad & 1)) * 16 * p.pool.n + c * 4 * W;
+        const uint8_t* s = page + p.pool.scales + ((ki >> 2) * 2 * p.pool.n + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
+#pragma unroll
+        for (int x = 0; x < 2; ++x, at += 32 * p.pool.n) {
+          if constexpr (W == 4) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
+            r.k[x][0] = w.x; r.k[x][1] = w.y; r.k[x][2] = w.z; r.k[x][3] = w.w;
+          } else if constexpr (W == 2) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+            r.k[x][0] = w.x; r.k[x][1] = w.y;
+          } else {
+            r.k[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
           }
         }
-        bool grow = false;
+        if constexpr (W == 4) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(s));
+          r.ks[0] = w.x;
+          r.ks[1] = k1_has ? w.y : 0;
+        } else {
+          r.ks[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+        }
+      }
+      if (u.page >= 0 && v_has) {
+        const uint8_t* page = vg + u.page * p.pool.page_stride;
+        const uint8_t* at = page + u.in_page * 16 * p.pool.n + quad * 2 * W;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grow |= fmaxf(s[e], s[2 + e]) * sc[e] - m[e] > kRescale;
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[e], s[2 + e]) * sc[e];
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float f = mx > m[e] ? ex2(m[e] - mx) : 1.f;
-            m[e] = fmaxf(m[e], mx);
-            l[e] *= f;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              o[t][e] *= f;
-              o[t][2 + e] *= f;
-            }
+        for (int x = 0; x < 4; ++x, at += 16 * p.pool.n) {
+          if constexpr (W == 4) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+            r.v[x][0] = w.x; r.v[x][1] = w.y;
+          } else if constexpr (W == 2) {
+            r.v[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+          } else {
+            r.v[x][0] = __ldg(reinterpret_cast<const uint16_t*>(at));
           }
         }
-        float x[4];
+        r.vs = __ldg(reinterpret_cast<const uint32_t*>(page + p.pool.scales + ((u.in_page >> 2) * 2 * p.pool.n + v_block) * 4));
+        const int left = u.keys - 4 * c;
+        if (left < 4) r.vs &= (1u << 8 * left) - 1;       // keys past the end: zero
+      }
+    };
+    auto work = [&](const FewRaw<NC>& r, const FewUnit& u) {
+      // ---- scores
+      uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
+      if constexpr (W == 4) {
+        const uint32_t b = quad & 1;
+        const uint32_t a2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], b | (4 + b) << 4));
+        const uint32_t b2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], (b + 2) | (b + 6) << 4));
+        ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
+        kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
+      } else {
+        const uint32_t b = quad & 1;
+        const uint32_t two = kv4_scale_pair(prmt(r.ks[0], 0, b | (b + 2) << 4));
+        ka[0] = ka[1] = prmt(two, two, 0x1010);
+        kb[0] = kb[1] = prmt(two, two, 0x3232);
+      }
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t a[4], b[4];
+        kv4_decode(r.k[0][w], a);
+        kv4_decode(r.k[1][w], b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[e] = mul_f16x2(a[e], ka[w >> 1]);
+          b[e] = mul_f16x2(b[e], kb[w >> 1]);
+        }
+        mma_16x8x16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
+        mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
+        if constexpr (F32) {
+          mma_16x8x16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
+          mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += s2[e];
+      // ---- s[e]: key k_off, row 2 c + e; s[2 + e]: key k_off + 2
+      if (!(u.keys == 16 && all_see > 0 && (u.pre || u.key0 + 16 <= all_see))) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float neg = m[e] == -INFINITY ? kShift : kShift - m[e];
-          x[e] = ex2(fmaf(s[e], sc[e], neg));
-          x[2 + e] = ex2(fmaf(s[2 + e], sc[e], neg));
-          l[e] += x[e] + x[2 + e];
-        }
-        // keys x rows -> rows x keys, the B operand of O^T
-        const uint32_t p0 = f16x2(x[0], x[1]), p1 = f16x2(x[2], x[3]);
-        const uint32_t ph0 = transpose8(p0), ph1 = transpose8(p1);
-        uint32_t pl0 = 0, pl1 = 0;
-        if constexpr (F32) {
-          const float2 r0 = halves(p0), r1 = halves(p1);
-          pl0 = transpose8(f16x2(x[0] - r0.x, x[1] - r0.y));
-          pl1 = transpose8(f16x2(x[2] - r1.x, x[3] - r1.y));
-        }
-        // ---- values
-        uint32_t vs = r.vs;
-        const uint32_t odd = kv4_nan_scales(vs);
-        if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
-#pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const int key = u.key0 + 4 * c + x;
-            if (!u.pre && (odd >> (8 * x + 7) & 1u) && key >= all_see) {
-              vs &= ~(0xffu << 8 * x);
-              atomicMin(&nan_key[turn][v_block], key);
-            }
-          }
-        }
-        const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
-          constexpr uint32_t lo = 0x0f0f0f0fu;
-          kv4_decode((r.v[0][j] & lo) | ((r.v[1][j] << 4) & ~lo), a0);
-          kv4_decode(((r.v[0][j] >> 4) & lo) | (r.v[1][j] & ~lo), a1);
-          kv4_decode((r.v[2][j] & lo) | ((r.v[3][j] << 4) & ~lo), a2);
-          kv4_decode(((r.v[2][j] >> 4) & lo) | (r.v[3][j] & ~lo), a3);
-#pragma unroll
-          for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
-            const int t = 4 * j + b;
-            const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
-                           w3 = mul_f16x2(a3[b], v23);
-            if constexpr (F32) {
-              // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
-              float z[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16x8x16(z, w0, w1, w2, w3, pl0, pl1);
-              mma_16x8x16(z, w0, w1, w2, w3, ph0, ph1);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][e] += z[e];
-            } else {
-              mma_16x8x16(o[t], w0, w1, w2, w3, ph0, ph1);
-            }
-          }
-        }
-      };
-      FewUnit ua{it.t0, warp, 0, 0, false, -1, 0}, ub;
-      while (ua.sub >= subs) {
-        ua.sub -= subs;
-        ++ua.tile;
-      }
-      FewRaw<NC> ra, rb;
-      locate(ua);
-      load(ra, ua);
-      ub = ua;
-      locate(ub);
-      while (ua.keys > 0) {
-        load(rb, ub);
-        FewUnit next = ub;
-        locate(next);
-        work(ra, ua);
-        ua = next;
-        load(ra, ua);
-        if (ub.keys > 0) {
-          next = ua;
-          locate(next);
-          work(rb, ub);
-          ub = next;
+          const int vis = own_vis[e] <= 0 ? 0 : u.pre ? u.keys : min(u.keys, own_vis[e] - u.key0);
+          if (k_off >= vis) s[e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
+          if (k_off + 2 >= vis) s[2 + e] = -INFINITY;
         }
       }
-
-      // ---- the warps' parts
+      bool grow = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) grow |= fmaxf(s[e], s[2 + e]) * sc[e] - m[e] > kRescale;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[e], s[2 + e]) * sc[e];
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float f = mx > m[e] ? ex2(m[e] - mx) : 1.f;
+          m[e] = fmaxf(m[e], mx);
+          l[e] *= f;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            o[t][e] *= f;
+            o[t][2 + e] *= f;
+          }
+        }
+      }
+      float x[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
-        const int r = 2 * c + e;
-        if (r >= nrows) continue;
-        if (quad == 0) ml[warp][r] = make_float2(m[e], l[e]);
-        float* dst = &po[warp][r][4 * W * quad];
-#pragma unroll
-        for (int t = 0; t < MT; t += 2)
-          *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
+        const float neg = m[e] == -INFINITY ? kShift : kShift - m[e];
+        x[e] = ex2(fmaf(s[e], sc[e], neg));
+        x[2 + e] = ex2(fmaf(s[2 + e], sc[e], neg));
+        l[e] += x[e] + x[2 + e];
       }
-      __syncthreads();
-      const int r = warp, e0 = 4 * lane;
-      if (r < nrows) {
-        const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][r].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float2 s = ml[w][r];
-          if (s.y == 0.f) continue;                      // nothing seen by this warp
-          const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
-          sum += f * s.y;
-          const float4 v = *reinterpret_cast<const float4*>(&po[w][r][min(e0, 4 * W * 8 - 4)]);
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
-        }
-        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
-        if (e0 < g.d) {
-          if (nan_key[turn][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
-          if (it.part_row >= 0) {
-            *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r0 + r) * g.d + e0) = acc;
-          } else if constexpr (F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
-          } else {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
-                make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+      // keys x rows -> rows x keys, the B operand of O^T
+      const uint32_t p0 = f16x2(x[0], x[1]), p1 = f16x2(x[2], x[3]);
+      const uint32_t ph0 = transpose8(p0), ph1 = transpose8(p1);
+      uint32_t pl0 = 0, pl1 = 0;
+      if constexpr (F32) {
+        const float2 r0 = halves(p0), r1 = halves(p1);
+        pl0 = transpose8(f16x2(x[0] - r0.x, x[1] - r0.y));
+        pl1 = transpose8(f16x2(x[2] - r1.x, x[3] - r1.y));
+      }
+      // ---- values
+      uint32_t vs = r.vs;
+      const uint32_t odd = kv4_nan_scales(vs);
+      if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const int key = u.key0 + 4 * c + x;
+          if (!u.pre && (odd >> (8 * x + 7) & 1u) && key >= all_see) {
+            vs &= ~(0xffu << 8 * x);
+            atomicMin(&nan_key[turn][v_block], key);
           }
         }
-        if (lane == 0) {
-          const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
-          if (it.part_row >= 0) g.part_lse[it.part_row + r0 + r] = lse;
-          else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+      }
+      const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
+        constexpr uint32_t lo = 0x0f0f0f0fu;
+        kv4_decode((r.v[0][j] & lo) | ((r.v[1][j] << 4) & ~lo), a0);
+        kv4_decode(((r.v[0][j] >> 4) & lo) | (r.v[1][j] & ~lo), a1);
+        kv4_decode((r.v[2][j] & lo) | ((r.v[3][j] << 4) & ~lo), a2);
+        kv4_decode(((r.v[2][j] >> 4) & lo) | (r.v[3][j] & ~lo), a3);
+#pragma unroll
+        for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
+          const int t = 4 * j + b;
+          const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
+                         w3 = mul_f16x2(a3[b], v23);
+          if constexpr (F32) {
+            // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_16x8x16(z, w0, w1, w2, w3, pl0, pl1);
+            mma_16x8x16(z, w0, w1, w2, w3, ph0, ph1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][e] += z[e];
+          } else {
+            mma_16x8x16(o[t], w0, w1, w2, w3, ph0, ph1);
+          }
         }
+      }
+    };
+    FewUnit ua{it.t0, warp, 0, 0, false, -1, 0}, ub;
+    while (ua.sub >= subs) {
+      ua.sub -= subs;
+      ++ua.tile;
+    }
+    FewRaw<NC> ra, rb;
+    locate(ua);
+    load(ra, ua);
+    ub = ua;
+    locate(ub);
+    while (ua.keys > 0) {
+      load(rb, ub);
+      FewUnit next = ub;
+      locate(next);
+      work(ra, ua);
+      ua = next;
+      load(ra, ua);
+      if (ub.keys > 0) {
+        next = ua;
+        locate(next);
+        work(rb, ub);
+        ub = next;
+      }
+    }
+
+    // ---- the warps' parts
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+      const int r = 2 * c + e;
+      if (r >= nrows) continue;
+      if (quad == 0) ml[warp][r] = make_float2(m[e], l[e]);
+      float* dst = &po[warp][r][4 * W * quad];
+#pragma unroll
+      for (int t = 0; t < MT; t += 2)
+        *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
+    }
+    __syncthreads();
+    const int r = warp, e0 = 4 * lane;
+    if (r < nrows) {
+      const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][r].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 s = ml[w][r];
+        if (s.y == 0.f) continue;                      // nothing seen by this warp
+        const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
+        sum += f * s.y;
+        const float4 v = *reinterpret_cast<const float4*>(&po[w][r][min(e0, 4 * W * 8 - 4)]);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+      if (e0 < g.d) {
+        if (nan_key[turn][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
+        if (it.part_row >= 0) {
+          *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r) * g.d + e0) = acc;
+        } else if constexpr (F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
+        } else {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
+              make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+        }
+      }
+      if (lane == 0) {
+        const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
+        if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
+        else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
       }
     }
   }
@@ -509,6 +486,766 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
       g.head->few_done = 0;
     }
   }
+}
+
+// ---------------------------------------------------------------- row tiles
+// Items of more rows, bf16: persistent, one CTA per SM, on the tensor cores.  A work item is up to 256 packed rows
+// against a run of 128-key tiles; CTAs claim them from a counter.  Two streams of 128 rows alternate on the tensor
+// core, each with two score buffers of half a tile.
+//   warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
+//   warp 8           claims items
+//   warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from shared memory) and O += P V (P from
+//                    tensor memory)
+//   warps 12-15      output, while the softmax goes on to the next item
+//   warps 16-19      query rows, keys and values: from global memory through registers to fp16 tiles in shared memory
+//                    in the 128-byte swizzle that the products read
+// Tensor memory is laid out as in attention.cu.
+//
+// A thread of warps 16-19 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
+// for each of the two blocks.  The next tile's keys are asked for when this tile's have been converted, its page a tile
+// earlier, so memory has the time of a tile (1.3 us) to answer; a conversion and a product make two elements, some 400
+// instructions a tile and thread.
+constexpr int kTileThreads = 640;
+// Registers of the warpgroups: 96 for each of 640 threads at the launch.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kIssueRegs = 40, kOutRegs = 72, kConvertRegs = 80;
+static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + kConvertRegs <= 5 * kLaunchRegs, "what the launch owns");
+
+// Ring stages that fit beside the query tiles and the staging.
+__host__ __device__ constexpr int kv4_stages(int halves) { return halves == 2 ? 4 : 6; }
+
+struct alignas(16) TileBars {
+  uint64_t kv_ready[2][6], kv_empty[6];      // kv_ready: each stream's own tiles, in its own order
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
+  uint64_t stat_full[2], stat_empty[2], drain[2], slot_full[kSlots], slot_empty[kSlots];
+  alignas(16) WorkItem slot[kSlots];         // row0 < 0: no more
+  int nan_key[kSlots][8];                    // the first key, not seen by every row, whose values of a block are NaN
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + kStageOut + 2 * kRows * 8 + kSlots * 2 * kRows * 4 + (int)sizeof(TileBars);
+static_assert(kTileSmem <= kSmemMax, "fits an SM");
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+struct TilePos {
+  int k, u, n;                               // item, tile of it, its tiles
+};
+
+template <int NC>
+__global__ void __launch_bounds__(kTileThreads, 1)
+kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Kv4AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr int kHalves = NC > 2 ? 2 : 1, kD = 32 * NC, kSlices = 2 * NC, kStages = kv4_stages(kHalves);
+  constexpr int kTileBytes = kHalves * kHalfBytes;
+  const StepGeom& g = p.g;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_smem = smem;                              // two row tiles
+  uint8_t* kv_smem = smem + 2 * kTileBytes;
+  uint8_t* out_smem = kv_smem + kStages * kTileBytes;
+  float2* stats = reinterpret_cast<float2*>(out_smem + kStageOut);      // [stream][row]: (m, l)
+  float* q_factor = reinterpret_cast<float*>(stats + 2 * kRows);        // [slot][stream][row]: of the scores
+  TileBars* bars = reinterpret_cast<TileBars*>(q_factor + kSlots * 2 * kRows);
+  uint32_t* status = &g.head->status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->kv_ready[0][i], 4);
+      mbar_init(&bars->kv_ready[1][i], 4);
+      mbar_init(&bars->kv_empty[i], 2);      // the streams; the converting warps stand in for one that does not use it
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 4);
+      mbar_init(&bars->q_empty[s], 1);
+      mbar_init(&bars->drain[s], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[s][b], 1);
+        mbar_init(&bars->p_full[s][b], 4);
+        mbar_init(&bars->pv_done[s][b], 1);
+      }
+      mbar_init(&bars->o_full[s], 1);
+      mbar_init(&bars->stat_full[s], 4);
+      mbar_init(&bars->stat_empty[s], 4);
+      mbar_init(&bars->o_empty[s], 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bars->slot_full[i], 1);
+      mbar_init(&bars->slot_empty[i], 18);   // softmax warps 8, output 4, product 2, converting 4
+    }
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_enter();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const bool fits = plan_matches(g);
+  const bool good = fits && g.head->n_items >= 0;
+  // a plan of other shapes, or of a malformed step: said by every call, as the status is cleared when it is read
+  if (!good && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
+
+  if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 8) {
+      // ---------------------------------------------------------- items
+      // Claimed one ahead: the first of a CTA is its own number, the others come from a counter.
+      const int end = good ? g.head->tile_end : 0;
+      auto publish = [&](int k, int item) {
+        wait_on(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars);
+        int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
+        if (lane < (int)(sizeof(WorkItem) / 4))
+          d[lane] = item < end ? reinterpret_cast<const int*>(g.items + item)[lane] : -1;
+        if (lane < 8) bars->nan_key[k % kSlots][lane] = INT32_MAX;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
+      };
+      auto pass_few = [&](int i) {           // past the other kernel's items
+        while (i < end && g.items[i].alt == 2) {
+          int next = 0;
+          if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
+          i = __shfl_sync(0xffffffffu, next, 0);
+        }
+        return i;
+      };
+      int i = pass_few(blockIdx.x), k = 0;
+      publish(0, i);
+      while (i < end && !gave_up(bars)) {
+        int next = 0;
+        if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
+        i = pass_few(__shfl_sync(0xffffffffu, next, 0));
+        publish(++k, i);
+      }
+    } else if (warp < 11) {
+      // ---------------------------------------------------------- products
+      // The whole warp walks, one lane issues; see attention.cu.
+      const int s = warp - 9;
+      const uint32_t id_qk = idesc_f16(kRows, kHalfKeys, 0);
+      const uint32_t id_pv = idesc_f16(kRows, (uint32_t)kD, 0) | (1u << 16);   // V is N-major
+      const uint64_t dq = smem_desc_k_sw128(smem_u32(q_smem + s * kTileBytes)), dk0 = smem_desc_k_sw128(smem_u32(kv_smem));
+      const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(kv_smem), kHalfBytes);
+      constexpr uint32_t tile_step = kTileBytes >> 4;
+      const uint32_t tS = tmem + s * kKeyTile, tO = tmem + kColO + s * kRows;
+      uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;
+      Ring base, turn;      // the item's first ring stage; the stream's next turn
+      for (int k = 0; slot_wait(bars, k); ++k) {
+        const WorkItem it = uniform_item(bars, k);
+        slot_done(bars, k);
+        const int n = s ? it.n1 : it.n0, tiles = item_tiles(it);
+        Ring rk = base;                                   // stage of the stream's next keys
+        base.advance(2 * tiles, kStages);
+        if (n == 0) continue;
+        if (it.alt && s) rk.skip(2, kStages);
+        Ring rv = rk, tk = turn, tv = turn;
+        rv.skip(1, kStages);
+        tv.skip(1, kStages);
+        turn.advance(2 * n, kStages);
+        const int stride = it.alt ? 4 : 2;                // ring steps from tile to tile of the stream
+        const int ti_step = it.alt ? 2 : 1, limit = stream_limit(it, g, s);
+        int ti = tile_of(it, s, 0), keys = stream_keys(it, g, ti, limit);
+        wait_on(&bars->q_full[s], q_ph, bars);
+        q_ph ^= 1u;
+        wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+        tc_fence_after();
+#pragma unroll 1
+        for (int from = 0; from < kKeyTile; from += kHalfKeys) {
+          if (elect_one()) {
+            if (keys > from) issue_scores<kSlices>(0, tS + from, dq, dk0 + rk.s * tile_step + (from * 128 >> 4), id_qk);
+            mma_commit(&bars->s_full[s][from / kHalfKeys]);
+            if (from) mma_commit(&bars->kv_empty[rk.s]);
+            if (from && n == 1) mma_commit(&bars->q_empty[s]);
+          }
+          __syncwarp();
+        }
+        wait_on(&bars->o_empty[s], oe_ph ^ 1u, bars);
+        oe_ph ^= 1u;
+#pragma unroll 1
+        for (int left = n; left > 0; --left) {
+          const bool more = left > 1;
+          ti += ti_step;
+          const int next_keys = more ? stream_keys(it, g, ti, limit) : 0;
+          wait_on(&bars->kv_ready[s][tv.s], tv.ph, bars);
+          tv.skip(2, kStages);
+          rk.skip(stride, kStages);
+          tk.skip(2, kStages);
+          if (more) wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+          const uint64_t dv = dv0 + rv.s * tile_step, dk = dk0 + rk.s * tile_step;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int from = h * kHalfKeys;
+            wait_on(&bars->p_full[s][h], p_ph, bars);
+            tc_fence_after();
+            if (elect_one()) {
+              issue_values((keys - from + 15) >> 4, tO, tS + from, dv + (from * 128 >> 4), id_pv, h > 0 || left < n);
+              mma_commit(&bars->pv_done[s][h]);
+              if (h == 1) mma_commit(&bars->kv_empty[rv.s]);
+              if (more) {
+                if (next_keys > from) issue_scores<kSlices>(0, tS + from, dq, dk + (from * 128 >> 4), id_qk);
+                mma_commit(&bars->s_full[s][h]);
+                if (h == 1) mma_commit(&bars->kv_empty[rk.s]);
+                if (h == 1 && left == 2) mma_commit(&bars->q_empty[s]);      // the item's last scores
+              } else if (h == 1) {
+                mma_commit(&bars->o_full[s]);
+              }
+            }
+            __syncwarp();
+          }
+          p_ph ^= 1u;
+          rv.skip(stride, kStages);
+          keys = next_keys;
+        }
+      }
+      if (elect_one()) {
+        mma_commit(&bars->drain[s]);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test_wait(&bars->drain[s], 0) && global_timer_ns() - t0 < 2000000000ull) {}
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int s = warp >> 2;                         // stream
+    const int row = threadIdx.x & (kRows - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + s * kKeyTile;
+    const uint32_t tO = tmem + lane_base + kColO + s * kRows;
+    uint32_t s_ph = 0, st_ph = 0;
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      const int n = s ? it.n1 : it.n0;
+      const int r_item = row + (it.alt ? 0 : s * kRows);
+      const bool live = r_item < it.nrows;
+      const bool warp_live = (row & ~31) + (it.alt ? 0 : s * kRows) < it.nrows;
+      const int tok = g.by_R(it.row0 + r_item);
+      // own keys in view of this row; padding rows see nothing at all
+      const int own_vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+      const bool blind = !live || (it.seq >= 0 && own_vis <= 0);
+      float m = -INFINITY, l = 0.f, sc = 0.f;        // m: the maximum (log2) that O and l refer to
+      const int limit = stream_limit(it, g, s);
+      for (int j = 0; j < n; ++j) {
+        const int ti = tile_of(it, s, j);
+        int key0;
+        const int keys = tile_keys(it, g, ti, &key0), used_keys = stream_keys(it, g, ti, limit);
+        int vis_tile = ti < it.np ? keys : min(keys, own_vis - key0);      // keys in view of this row
+        if (blind) vis_tile = 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int vis = vis_tile - h * kHalfKeys;
+          const bool masked = __any_sync(0xffffffffu, vis < kHalfKeys);
+          const uint32_t tB = tS + h * kHalfKeys;
+          wait_on(&bars->s_full[s][h], s_ph, bars);
+          if (j == 0 && h == 0) sc = q_factor[((k % kSlots) * 2 + s) * kRows + row];      // there before the queries were
+          if (warp_live && h * kHalfKeys < used_keys) {
+            tc_fence_after();
+            uint32_t v[kHalfKeys];
+            tmem_ld32(tB, v);
+            tmem_ld32(tB + 32, v + 32);
+            tmem_ld_wait();
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < kHalfKeys; ++c)
+                if (c >= vis) v[c] = 0xff800000u;      // -inf: chosen, not added, so a NaN behind the mask is gone
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kHalfKeys; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(v[c + e]), __uint_as_float(v[c + e + 4]));
+            const float m_new = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc);
+            if (j == 0 && h == 0) {
+              m = m_new;
+            } else {
+              const bool grow = m_new - m > kRescale;
+              if (__any_sync(0xffffffffu, grow)) {
+                // O is this warp's once the latest product is done (those before it are: these scores were
+                // issued after them)
+                wait_on(&bars->pv_done[s][h ^ 1], h ? s_ph : s_ph ^ 1u, bars);
+                tc_fence_after();
+                const float f = grow ? ex2(m - m_new) : 1.f;
+                if (grow) m = m_new;
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + c, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(tO + c, o);
+                }
+              }
+            }
+            const float neg = m == -INFINITY ? kShift : kShift - m;
+            const uint64_t sc2 = pk(sc, sc), ng2 = pk(neg, neg);
+            uint64_t sum0 = pk(0.f, 0.f), sum1 = sum0;
+            uint32_t w[kHalfKeys / 2];
+#pragma unroll
+            for (int e = 0; e < kHalfKeys / 2; ++e) {
+              const float2 x = unpk(fma2(pk_u(v[2 * e], v[2 * e + 1]), sc2, ng2));
+              const float a = ex2(x.x), b = ex2(x.y);
+              if (e & 1) sum1 = add2(sum1, pk(a, b));
+              else sum0 = add2(sum0, pk(a, b));
+              w[e] = f16x2(a, b);
+            }
+            tmem_st32(tB, w);
+            const float2 z = unpk(add2(sum0, sum1));
+            l += z.x + z.y;
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[s][h]);
+        }
+        s_ph ^= 1u;
+      }
+      if (n > 0) {
+        // (m, l) to the output warps, once they have taken the item's before
+        wait_on(&bars->stat_empty[s], st_ph ^ 1u, bars);
+        st_ph ^= 1u;
+        stats[s * kRows + row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->stat_full[s]);
+      }
+      slot_done(bars, k);
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------ output
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    const int row = threadIdx.x & (kRows - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t stage_out = smem_u32(out_smem) + (warp & 3) * 4096;
+    uint32_t ph = 0;                                 // bit s: stream s
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
+#pragma unroll 1
+      for (int s = 0; s < (it.alt ? 1 : 2); ++s) {
+        const int n = s ? it.n1 : it.n0;
+        const uint32_t tO = tmem + lane_base + kColO + s * kRows;
+        const int r_item = row + s * kRows;
+        const int rr = it.row0 + r_item;
+        const bool live = r_item < it.nrows, warp_live = (row & ~31) + s * kRows < it.nrows;
+        const int tok = g.by_R(rr);
+        float m = -INFINITY, l = 0.f, f0 = 1.f, f1 = 0.f;
+        auto take = [&](int x) {                     // stream x's (m, l); its O is complete then
+          wait_on(&bars->stat_full[x], (ph >> x) & 1u, bars);
+          const float2 v = stats[x * kRows + row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->stat_empty[x]);
+          wait_on(&bars->o_full[x], (ph >> x) & 1u, bars);
+          ph ^= 1u << x;
+          return v;
+        };
+        if (n > 0) {
+          const float2 v = take(s);
+          m = v.x;
+          l = v.y;
+        }
+        if (merging) {
+          const float2 o = take(1);
+          const float mm = fmaxf(m, o.x);
+          if (mm != -INFINITY) {
+            f0 = ex2(m - mm);
+            f1 = ex2(o.x - mm);
+          }
+          l = l * f0 + o.y * f1;
+          m = mm;
+        }
+        auto free_o = [&]() {                        // for the next item's products
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (n > 0) mbar_arrive(&bars->o_empty[s]);
+            if (merging) mbar_arrive(&bars->o_empty[1]);
+          }
+        };
+        if (!warp_live) {
+          free_o();
+          continue;
+        }
+        const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;      // a row without keys: zero
+        f0 *= inv;
+        f1 *= inv;
+        tc_fence_after();
+        const int h = it.group * g.R + rr - tok * g.R;
+        const bool direct = it.part_row < 0;
+        // 128 bytes of each row at a time go through shared memory: 64 bf16 columns of the output, 32 fp32
+        // columns of a partial row.  A warp whose 32 rows are all there (and whole tokens) writes output
+        // as one bulk copy; otherwise stores of whole lines, with the rows' numbers from their lanes.
+        const bool bulk = direct && 32 % g.R == 0 && (row & ~31) + s * kRows + 32 <= it.nrows;
+        const int mine = !live ? -1 : direct ? tok * g.H + h : it.part_row + r_item;
+        const bool none = l == 0.f, some_none = __any_sync(0xffffffffu, none);   // rows without keys are zero
+        const int first_tok = __shfl_sync(0xffffffffu, tok, 0);
+        // values that are NaN and were taken out of the tiles: of the rows that see their keys
+        const int* nan_key = bars->nan_key[k % kSlots];
+        const bool some_nan = __any_sync(0xffffffffu, nan_key[lane & 7] != INT32_MAX);
+        const int own_vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t v[32];
+          if (n > 0) tmem_ld32(tO + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+          if (merging) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              uint32_t w[8];
+              tmem_ld8(tO + kRows + c + x, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[x + e] = __float_as_uint(__uint_as_float(v[x + e]) + __uint_as_float(w[e]) * f1);
+            }
+          }
+          if (some_none) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = none ? 0u : v[e];
+          }
+          if (some_nan) {
+            const bool a = nan_key[c / 16] < own_vis, b = nan_key[c / 16 + 1] < own_vis;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e < 16 ? a : b) v[e] = 0x7fc00000u;
+          }
+          if (c + 32 >= kD) free_o();
+          // the block's bulk copy before has been read: of this item, or of one before it whose rows were output
+          if (!(c & 32)) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+          }
+          if (direct) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              st_shared16(stage_at(stage_out, lane, (c & 32) / 8 + q),
+                          make_uint4(bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
+                                     bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
+                                     bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
+                                     bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]))));
+            if (!(c & 32) && c + 32 < kD) continue;
+          } else {
+            // a partial row's 32 columns have the block to themselves: the warp has read the ones before
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              st_shared16(stage_at(stage_out, lane, q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+          }
+          if (bulk) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_4d(out_smem + (warp & 3) * 4096, &map_out, c & 64, 0, it.group, first_tok);
+            __syncwarp();
+            continue;
+          }
+          __syncwarp();
+          uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(g.part_out);
+          const int piece = lane & 7, row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & 64) * 2 : c * 4) + piece * 16;
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            const int which = __shfl_sync(0xffffffffu, mine, r);
+            if (which >= 0 && byte < row_bytes)
+              *reinterpret_cast<uint4*>(to + (int64_t)which * row_bytes + byte) = ld_shared16(stage_at(stage_out, r, piece));
+          }
+          __syncwarp();
+        }
+        if (live) {
+          const float lse = l == 0.f ? -INFINITY : (m - kShift) * kLn2 + logf(l);
+          if (!direct) g.part_lse[mine] = lse;
+          else if (p.lse) p.lse[mine] = lse;
+        }
+      }
+      slot_done(bars, k);
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ queries, keys and values
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    const int ct = threadIdx.x - 512, cw = warp - 16;
+    const bool busy = ct < 32 * NC;                  // a chunk c of keys 4 j .. 4 j + 3
+    const int j = ct / NC, c = ct - j * NC;
+    const bool second = 32 * c + 16 < g.d;           // the chunk's other block holds elements
+    // Words go out in an order of the lane's own, x ^ f for x = 0 .. 3, so that a quarter warp's 16-byte stores meet in
+    // no bank: rows that are alike modulo 8 lie four threads of keys apart.
+    const int f = NC > 2 ? (c >> 1) | (j & 1) << 1 : (j >> 1 & 1) | (j & 1) << 1;
+    const uint32_t place = ((((c & 1) << 2) | f) ^ ((j & 1) << 2)) << 4;
+    const uint32_t to0 = smem_u32(kv_smem) + (c >> 1) * kHalfBytes + 4 * j * 128;
+    const int64_t row_bytes = 16 * NC;
+    struct Raw {
+      uint4 k[4];
+      uint2 s;
+    };
+    Ring r, turn[2];
+    uint32_t q_ph = 0;                               // bit x: stream x
+
+    // the next tile of the item or, if it has one, the first of the item after it
+    auto look_ahead = [&](TilePos& t) {
+      if (t.u + 1 < t.n) {
+        ++t.u;
+        return true;
+      }
+      t.u = 0;
+      ++t.k;
+      t.n = slot_wait(bars, t.k) ? item_tiles(bars->slot[t.k % kSlots]) : 0;
+      return t.n > 0;
+    };
+    // past items without tiles; no slot may be held meanwhile, the items might not fit the others
+    auto advance = [&](TilePos& t) {
+      t.u = 0;
+      for (; slot_wait(bars, t.k); ++t.k) {
+        t.n = item_tiles(bars->slot[t.k % kSlots]);
+        if (t.n > 0) return true;
+        slot_done(bars, t.k);
+      }
+      return false;
+    };
+    struct Where {
+      int page, in_page, left;                       // of this thread's keys; keys from the first of them on
+      int own_key;                                   // the first of them among the sequence's own; -1: the prefix's
+      int group;
+    };
+    auto locate = [&](const TilePos& t) {            // asks for the page
+      const WorkItem& it = bars->slot[t.k % kSlots];
+      const int ti = it.t0 + t.u;
+      const bool pre = ti < it.np;
+      int key0;
+      const int keys = tile_span(g, pre ? g.prefix_len : it.own_len, pre ? ti : ti - it.np, &key0);
+      Where w;
+      w.left = keys - 4 * j;
+      w.own_key = pre ? -1 : key0 + 4 * j;
+      w.group = it.group;
+      w.page = -1;
+      w.in_page = 0;
+      if (busy && w.left > 0) {
+        const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+        const int pi = g.by_page(key0 + 4 * j);
+        w.page = __ldg(table + pi);
+        w.in_page = key0 + 4 * j - pi * g.page_size;
+      }
+      return w;
+    };
+    auto check = [&](Where& w) {
+      if (busy && w.left > 0 && (w.page < 0 || w.page >= g.n_pages)) {      // read as zeros: report it
+        latch_status(status, kStatusRange);
+        w.page = -1;
+      }
+    };
+    auto load = [&](Raw& x, const Where& w, const uint8_t* pool) {
+      x.s = make_uint2(0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.k[i] = make_uint4(0, 0, 0, 0);
+      if (w.page >= 0) {
+        const uint8_t* page = pool + w.page * p.pool.page_stride + w.group * p.pool.group_stride;
+        const uint8_t* at = page + w.in_page * row_bytes + c * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.k[i] = __ldg(reinterpret_cast<const uint4*>(at + i * row_bytes));
+        x.s = __ldg(reinterpret_cast<const uint2*>(page + p.pool.scales + ((w.in_page >> 2) * 2 * NC + 2 * c) * 4));
+        if (w.left < 4) {                            // keys past the end: zero
+          const uint32_t keep = (1u << 8 * w.left) - 1;
+          x.s.x &= keep;
+          x.s.y &= keep;
+        }
+        if (!second) x.s.y = 0;
+      }
+    };
+    auto convert = [&](const Raw& x, uint32_t to) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t both = kv4_scale_pair(prmt(x.s.x, x.s.y, i | (4 + i) << 4));
+        uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
+        uint4 w = x.k[i];
+        if (f & 1) w = make_uint4(w.y, w.x, w.w, w.z);
+        if (f & 2) {
+          w = make_uint4(w.z, w.w, w.x, w.y);
+          const uint32_t t = s0;
+          s0 = s1;
+          s1 = t;
+        }
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t h[4];
+          kv4_decode(words[y], h);
+          const uint32_t s = y < 2 ? s0 : s1;
+          st_shared16(to + i * 128 + (place ^ (uint32_t)((y ^ i) << 4)),
+                      make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s)));
+        }
+      }
+    };
+    // 128 rows of stream x's queries, 16 lanes (8, 4) to a row
+    auto queries = [&](const WorkItem& it, int slot, int x, bool twice) {
+      constexpr int kLanes = NC > 2 ? 16 : 4 * NC, kPer = 32 / kLanes, kAhead = 4;
+      const int lc = lane % kLanes, sub = lane / kLanes;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q);
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += kPer * kAhead) {
+        uint4 w[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const int r_item = (it.alt ? 0 : x * kRows) + cw * 32 + r0 + y * kPer + sub;
+          w[y] = make_uint4(0, 0, 0, 0);
+          if (r_item < it.nrows && lc * 8 < g.d) {
+            const int rr = it.row0 + r_item, tok = g.by_R(rr);
+            w[y] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride +
+                                                        (it.group * g.R + rr - tok * g.R) * g.d + lc * 8));
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const int row = cw * 32 + r0 + y * kPer + sub;
+          uint32_t top = max_u16x2(max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
+                                   max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          float inverse;
+          const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
+          auto half = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
+          const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
+          const uint32_t at = (lc >> 3) * kHalfBytes + row * 128 + (((lc & 7) ^ (row & 7)) << 4);
+          if (lc * 8 < kD) {
+            st_shared16(smem_u32(q_smem) + x * kTileBytes + at, h);
+            if (twice) st_shared16(smem_u32(q_smem) + kTileBytes + at, h);
+          }
+          if (lc == 0) {
+            q_factor[(slot * 2 + x) * kRows + row] = inverse * p.score_log2;
+            if (twice) q_factor[(slot * 2 + 1) * kRows + row] = inverse * p.score_log2;
+          }
+        }
+      }
+    };
+
+    TilePos cur{0, 0, 0};
+    Raw kr, vr;
+    Where w{}, next_w{};
+    bool any = advance(cur), fetched = false;
+#pragma unroll 1
+    while (any && !gave_up(bars)) {
+      if (!fetched) {
+        w = locate(cur);
+        check(w);
+        load(kr, w, p.pool.k);
+        load(vr, w, p.pool.v);
+      }
+      TilePos next = cur;
+      const bool more = look_ahead(next);
+      if (more) next_w = locate(next);
+      const int slot = cur.k % kSlots;
+      const WorkItem& it = bars->slot[slot];
+      const int alt = it.alt, n0 = it.n0, n1 = it.n1;
+      const bool use0 = alt ? !(cur.u & 1) : cur.u < n0, use1 = alt ? cur.u & 1 : cur.u < n1;
+      auto pass_on = [&]() {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
+          if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
+          if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
+        }
+        if (use0) turn[0].skip(1, kStages);
+        if (use1) turn[1].skip(1, kStages);
+        r.skip(1, kStages);
+      };
+      // ---- keys
+      wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
+      if (busy) convert(kr, to0 + r.s * kTileBytes);
+      pass_on();
+      // ---- the item's queries, when the one before has no scores left to compute
+      if (cur.u == 0) {
+        const WorkItem item = load_item(&it);
+#pragma unroll 1
+        for (int x = 0; x < (alt ? 1 : 2); ++x) {
+          const bool twice = alt && n1 > 0;
+          if ((x ? n1 : n0) == 0) continue;
+          wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+          q_ph ^= 1u << x;
+          if (twice) {
+            wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
+            q_ph ^= 2u;
+          }
+          queries(item, slot, x, twice);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->q_full[x]);
+            if (twice) mbar_arrive(&bars->q_full[1]);
+          }
+        }
+      }
+      if (more) {
+        check(next_w);
+        load(kr, next_w, p.pool.k);
+      }
+      // ---- values; those that are NaN and that some row does not see are taken out: 0 * NaN would stay
+      if (__any_sync(0xffffffffu, w.own_key >= 0 && (kv4_nan_scales(vr.s.x) | kv4_nan_scales(vr.s.y)) != 0)) {
+        const int seen_by_all = all_see(load_item(&it), g);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          if (w.own_key < 0 || w.own_key + i < seen_by_all) continue;
+          const uint32_t byte = 0xffu << 8 * i, top = 0x80u << 8 * i;
+          if (kv4_nan_scales(vr.s.x) & top) {
+            vr.s.x &= ~byte;
+            atomicMin(&bars->nan_key[slot][2 * c], w.own_key + i);
+          }
+          if (kv4_nan_scales(vr.s.y) & top) {
+            vr.s.y &= ~byte;
+            atomicMin(&bars->nan_key[slot][2 * c + 1], w.own_key + i);
+          }
+        }
+      }
+      wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
+      if (busy) convert(vr, to0 + r.s * kTileBytes);
+      pass_on();
+      if (next.k != cur.k) slot_done(bars, cur.k);
+      if (more) {
+        load(vr, next_w, p.pool.v);
+        w = next_w;
+      }
+      cur = next;
+      fetched = more;
+      any = more || advance(cur);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
+  // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
+  if (fits && threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(&g.head->done, 1u) == gridDim.x - 1) {
+      g.head->claimed = 0;
+      g.head->done = 0;
+    }
+  }
+}
+
+template <int NC>
+aff_status launch_tile(const CUtensorMap& map_out, const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
+  // The register split needs the launch to own that many: a matter of the compiled kernel, asked once.  The
+  // shared-memory limit belongs to the current device, so it is set for every call.
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    AFF_CUDA(cudaFuncGetAttributes(&fa, kv4_tile_kernel<NC>));
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) AFF_CUDA(cudaErrorInvalidConfiguration);
+  AFF_CUDA(cudaFuncSetAttribute(kv4_tile_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
+  AFF_CUDA(launch_pdl(kv4_tile_kernel<NC>, grid, kTileThreads, (size_t)kTileSmem, s, map_out, p));
+  return AFF_OK;
 }
 
 template <int NC>
@@ -548,13 +1285,33 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
   p.lse = lse;
   p.score_log2 = scale * 1.4426950408889634f * cache->k_scale;
   p.v_scale = cache->v_scale;
-  const unsigned few_grid = (unsigned)(g.max_items < 2 * sms ? g.max_items : 2 * sms);
-  switch (p.pool.n) {
-    case 1: st = launch_few<1>(p, few_grid, s); break;
-    case 2: st = launch_few<2>(p, few_grid, s); break;
-    case 3: st = launch_few<3>(p, few_grid, s); break;
-    default: st = launch_few<4>(p, few_grid, s); break;
+  // all rows of a step of at most 8 are one sequence's few-rows items; otherwise only the device knows (step.cuh)
+  const bool tiles = g.dtype == AFF_BF16 && !(g.few && (int64_t)g.T * g.R <= g.few_rows);
+  if (tiles) {
+    CUtensorMap out_map{};
+    if (32 % g.R == 0) {
+      const uint64_t od[4] = {(uint64_t)g.d, (uint64_t)g.R, (uint64_t)g.G, (uint64_t)g.T};
+      const uint64_t os[3] = {(uint64_t)g.d * 2, (uint64_t)g.R * g.d * 2, (uint64_t)g.H * g.d * 2};
+      if ((st = map_16bit_sw128(&out_map, out, 4, od, os, (uint32_t)g.R, 1, (uint32_t)(32 / g.R), 3)) != AFF_OK) return st;
+    }
+    const unsigned grid = (unsigned)(g.max_items < sms ? g.max_items : sms);
+    switch (p.pool.n) {
+      case 1: st = launch_tile<1>(out_map, p, grid, s); break;
+      case 2: st = launch_tile<2>(out_map, p, grid, s); break;
+      case 3: st = launch_tile<3>(out_map, p, grid, s); break;
+      default: st = launch_tile<4>(out_map, p, grid, s); break;
+    }
+    if (st != AFF_OK) return st;
   }
-  if (st != AFF_OK) return st;
+  if (g.few) {
+    const unsigned grid = (unsigned)(g.max_items < 2 * sms ? g.max_items : 2 * sms);
+    switch (p.pool.n) {
+      case 1: st = launch_few<1>(p, grid, s); break;
+      case 2: st = launch_few<2>(p, grid, s); break;
+      case 3: st = launch_few<3>(p, grid, s); break;
+      default: st = launch_few<4>(p, grid, s); break;
+    }
+    if (st != AFF_OK) return st;
+  }
   return g.may_split ? launch_join(g, out, lse, s) : AFF_OK;
 }
