@@ -493,22 +493,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 // against a run of 128-key tiles; CTAs claim them from a counter.  Two streams of 128 rows alternate on the tensor
 // core, each with two score buffers of half a tile.
 //   warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
-//   warp 8           claims items
+//   warp 8           claims items, and asks for an item's queries an item ahead (into L2)
 //   warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from shared memory) and O += P V (P from
 //                    tensor memory)
-//   warps 12-15      output, while the softmax goes on to the next item
-//   warps 16-19      query rows, keys and values: from global memory through registers to fp16 tiles in shared memory
-//                    in the 128-byte swizzle that the products read
+//   warps 12-15      the next item's queries, as fp16 tiles; output, while the softmax goes on to the next item
+//   warps 16-19      keys, and warps 20-23 values: from global memory through registers to fp16 tiles in shared
+//                    memory, in the 128-byte swizzle that the products read
 // Tensor memory is laid out as in attention.cu.
 //
-// A thread of warps 16-19 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
-// for each of the two blocks.  The next tile's keys are asked for when this tile's have been converted, its page a tile
-// earlier, so memory has the time of a tile (1.3 us) to answer; a conversion and a product make two elements, some 400
-// instructions a tile and thread.
-constexpr int kTileThreads = 640;
-// Registers of the warpgroups: 96 for each of 640 threads at the launch.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kIssueRegs = 40, kOutRegs = 72, kConvertRegs = 80;
-static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + kConvertRegs <= 5 * kLaunchRegs, "what the launch owns");
+// A thread of warps 16-23 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
+// for each of the two blocks.  The next tile's are asked for when this tile's have been converted, its page a tile
+// earlier, so memory has most of a tile's time (1.3 us) to answer.
+constexpr int kTileThreads = 768;
+// Registers of the warpgroups: 80 for each of 768 threads at the launch.
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 120, kIssueRegs = 56, kOutRegs = 72, kConvertRegs = 56;
+static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + 2 * kConvertRegs <= 6 * kLaunchRegs, "what the launch owns");
 
 // Ring stages that fit beside the query tiles and the staging.
 __host__ __device__ constexpr int kv4_stages(int halves) { return halves == 2 ? 4 : 6; }
@@ -574,7 +573,7 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars->slot_full[i], 1);
-      mbar_init(&bars->slot_empty[i], 18);   // softmax warps 8, output 4, product 2, converting 4
+      mbar_init(&bars->slot_empty[i], 22);   // softmax warps 8, output 4, product 2, converting 8
     }
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -619,6 +618,18 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       int i = pass_few(blockIdx.x), k = 0;
       publish(0, i);
       while (i < end && !gave_up(bars)) {
+        {
+          const WorkItem it = load_item(g.items + i);
+          const uint16_t* q = static_cast<const uint16_t*>(p.q);
+#pragma unroll 1
+          for (int r = lane; r < (it.n0 + it.n1 > 0 ? it.nrows : 0); r += 32) {
+            const int rr = it.row0 + r, tok = g.by_R(rr);
+            const uint16_t* at = q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+            if (kHalves == 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
+          }
+          __syncwarp();
+        }
         int next = 0;
         if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
         i = pass_few(__shfl_sync(0xffffffffu, next, 0));
@@ -823,8 +834,73 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     const int row = threadIdx.x & (kRows - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t stage_out = smem_u32(out_smem) + (warp & 3) * 4096;
-    uint32_t ph = 0;                                 // bit s: stream s
+    uint32_t ph = 0, q_ph = 0;                       // bit s: stream s
+    // An item's queries, a row tile a stream (the same one, where both hold the same rows): 32 rows to a warp, 16 lanes
+    // (8, 4) to a row.  The first are on their way before the item before has no scores left to compute.
+    auto queries = [&](int k) {
+      constexpr int kLanes = NC > 2 ? 16 : 4 * NC, kPer = 32 / kLanes, kAhead = 4;
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      const int lc = lane % kLanes, sub = lane / kLanes, cw = warp & 3;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q);
+      const bool twice = it.alt && it.n1 > 0;
+#pragma unroll 1
+      for (int x = 0; x < (it.alt ? 1 : 2); ++x) {
+        if ((x ? it.n1 : it.n0) == 0) continue;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += kPer * kAhead) {
+          uint4 w[kAhead];
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            const int r_item = x * kRows + cw * 32 + r0 + y * kPer + sub;
+            w[y] = make_uint4(0, 0, 0, 0);
+            if (r_item < it.nrows && lc * 8 < g.d) {
+              const int rr = it.row0 + r_item, tok = g.by_R(rr);
+              w[y] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride +
+                                                          (it.group * g.R + rr - tok * g.R) * g.d + lc * 8));
+            }
+          }
+          if (r0 == 0) {
+            wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+            q_ph ^= 1u << x;
+            if (twice) {
+              wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
+              q_ph ^= 2u;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            const int r = cw * 32 + r0 + y * kPer + sub;
+            uint32_t top = max_u16x2(max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
+                                     max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float inverse;
+            const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
+            auto half = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
+            const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
+            const uint32_t at = smem_u32(q_smem) + (lc >> 3) * kHalfBytes + r * 128 + (((lc & 7) ^ (r & 7)) << 4);
+            if (lc * 8 < kD) {
+              st_shared16(at + x * kTileBytes, h);
+              if (twice) st_shared16(at + kTileBytes, h);
+            }
+            if (lc == 0) {
+              float* to = q_factor + (k % kSlots) * 2 * kRows + r;
+              to[x * kRows] = inverse * p.score_log2;
+              if (twice) to[kRows] = inverse * p.score_log2;
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->q_full[x]);
+          if (twice) mbar_arrive(&bars->q_full[1]);
+        }
+      }
+    };
+    if (slot_wait(bars, 0)) queries(0);
     for (int k = 0; slot_wait(bars, k); ++k) {
+      if (slot_wait(bars, k + 1)) queries(k + 1);
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
 #pragma unroll 1
@@ -968,24 +1044,28 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ queries, keys and values
+    // ------------------------------------------------------------ keys and values
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
-    const int ct = threadIdx.x - 512, cw = warp - 16;
+    const bool value = warp >= 20;
+    const int ct = threadIdx.x & 127, cw = warp & 3;
     const bool busy = ct < 32 * NC;                  // a chunk c of keys 4 j .. 4 j + 3
     const int j = ct / NC, c = ct - j * NC;
     const bool second = 32 * c + 16 < g.d;           // the chunk's other block holds elements
     // Words go out in an order of the lane's own, x ^ f for x = 0 .. 3, so that a quarter warp's 16-byte stores meet in
-    // no bank: rows that are alike modulo 8 lie four threads of keys apart.
+    // no bank: rows that are alike modulo 8 lie four threads of keys apart.  The words' halves are loaded in that order.
     const int f = NC > 2 ? (c >> 1) | (j & 1) << 1 : (j >> 1 & 1) | (j & 1) << 1;
     const uint32_t place = ((((c & 1) << 2) | f) ^ ((j & 1) << 2)) << 4;
     const uint32_t to0 = smem_u32(kv_smem) + (c >> 1) * kHalfBytes + 4 * j * 128;
-    const int64_t row_bytes = 16 * NC;
+    constexpr int kRowBytes = 16 * NC;
     struct Raw {
-      uint4 k[4];
-      uint2 s;
-    };
-    Ring r, turn[2];
-    uint32_t q_ph = 0;                               // bit x: stream x
+      uint2 lo[4], hi[4], s;
+    } raw;
+    Ring r, turn[2];                                 // keys and values take the ring's stages in turns
+    if (value) {
+      r.skip(1, kStages);
+      turn[0].skip(1, kStages);
+      turn[1].skip(1, kStages);
+    }
 
     // the next tile of the item or, if it has one, the first of the item after it
     auto look_ahead = [&](TilePos& t) {
@@ -1011,7 +1091,6 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     struct Where {
       int page, in_page, left;                       // of this thread's keys; keys from the first of them on
       int own_key;                                   // the first of them among the sequence's own; -1: the prefix's
-      int group;
     };
     auto locate = [&](const TilePos& t) {            // asks for the page
       const WorkItem& it = bars->slot[t.k % kSlots];
@@ -1022,7 +1101,6 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       Where w;
       w.left = keys - 4 * j;
       w.own_key = pre ? -1 : key0 + 4 * j;
-      w.group = it.group;
       w.page = -1;
       w.in_page = 0;
       if (busy && w.left > 0) {
@@ -1033,44 +1111,40 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       }
       return w;
     };
-    auto check = [&](Where& w) {
+    // Nothing here looks at what is loaded: that would be waiting for it.
+    auto load = [&](const TilePos& t, Where& w) {
       if (busy && w.left > 0 && (w.page < 0 || w.page >= g.n_pages)) {      // read as zeros: report it
         latch_status(status, kStatusRange);
         w.page = -1;
       }
-    };
-    auto load = [&](Raw& x, const Where& w, const uint8_t* pool) {
-      x.s = make_uint2(0, 0);
+      raw.s = make_uint2(0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.k[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) raw.lo[i] = raw.hi[i] = make_uint2(0, 0);
       if (w.page >= 0) {
-        const uint8_t* page = pool + w.page * p.pool.page_stride + w.group * p.pool.group_stride;
-        const uint8_t* at = page + w.in_page * row_bytes + c * 16;
+        const uint8_t* page = (value ? p.pool.v : p.pool.k) + w.page * p.pool.page_stride +
+                              bars->slot[t.k % kSlots].group * p.pool.group_stride;
+        const uint8_t* at = page + w.in_page * kRowBytes + c * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x.k[i] = __ldg(reinterpret_cast<const uint4*>(at + i * row_bytes));
-        x.s = __ldg(reinterpret_cast<const uint2*>(page + p.pool.scales + ((w.in_page >> 2) * 2 * NC + 2 * c) * 4));
-        if (w.left < 4) {                            // keys past the end: zero
-          const uint32_t keep = (1u << 8 * w.left) - 1;
-          x.s.x &= keep;
-          x.s.y &= keep;
+        for (int i = 0; i < 4; ++i) {
+          raw.lo[i] = __ldg(reinterpret_cast<const uint2*>(at + i * kRowBytes + (f & 2) * 4));
+          raw.hi[i] = __ldg(reinterpret_cast<const uint2*>(at + i * kRowBytes + 8 - (f & 2) * 4));
         }
-        if (!second) x.s.y = 0;
+        raw.s = __ldg(reinterpret_cast<const uint2*>(page + p.pool.scales + ((w.in_page >> 2) * 2 * NC + 2 * c) * 4));
       }
     };
-    auto convert = [&](const Raw& x, uint32_t to) {
+    auto convert = [&](uint32_t sx, uint32_t sy, uint32_t to) {
+      if (f & 2) {
+        const uint32_t t = sx;
+        sx = sy;
+        sy = t;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t both = kv4_scale_pair(prmt(x.s.x, x.s.y, i | (4 + i) << 4));
-        uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
-        uint4 w = x.k[i];
-        if (f & 1) w = make_uint4(w.y, w.x, w.w, w.z);
-        if (f & 2) {
-          w = make_uint4(w.z, w.w, w.x, w.y);
-          const uint32_t t = s0;
-          s0 = s1;
-          s1 = t;
-        }
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t both = kv4_scale_pair(prmt(sx, sy, i | (4 + i) << 4));
+        const uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
+        const uint2 lo = f & 1 ? make_uint2(raw.lo[i].y, raw.lo[i].x) : raw.lo[i];
+        const uint2 hi = f & 1 ? make_uint2(raw.hi[i].y, raw.hi[i].x) : raw.hi[i];
+        const uint32_t words[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           uint32_t h[4];
@@ -1081,134 +1155,61 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
         }
       }
     };
-    // 128 rows of stream x's queries, 16 lanes (8, 4) to a row
-    auto queries = [&](const WorkItem& it, int slot, int x, bool twice) {
-      constexpr int kLanes = NC > 2 ? 16 : 4 * NC, kPer = 32 / kLanes, kAhead = 4;
-      const int lc = lane % kLanes, sub = lane / kLanes;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q);
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += kPer * kAhead) {
-        uint4 w[kAhead];
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-          const int r_item = (it.alt ? 0 : x * kRows) + cw * 32 + r0 + y * kPer + sub;
-          w[y] = make_uint4(0, 0, 0, 0);
-          if (r_item < it.nrows && lc * 8 < g.d) {
-            const int rr = it.row0 + r_item, tok = g.by_R(rr);
-            w[y] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride +
-                                                        (it.group * g.R + rr - tok * g.R) * g.d + lc * 8));
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-          const int row = cw * 32 + r0 + y * kPer + sub;
-          uint32_t top = max_u16x2(max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
-                                   max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
-          float inverse;
-          const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
-          auto half = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-          const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
-          const uint32_t at = (lc >> 3) * kHalfBytes + row * 128 + (((lc & 7) ^ (row & 7)) << 4);
-          if (lc * 8 < kD) {
-            st_shared16(smem_u32(q_smem) + x * kTileBytes + at, h);
-            if (twice) st_shared16(smem_u32(q_smem) + kTileBytes + at, h);
-          }
-          if (lc == 0) {
-            q_factor[(slot * 2 + x) * kRows + row] = inverse * p.score_log2;
-            if (twice) q_factor[(slot * 2 + 1) * kRows + row] = inverse * p.score_log2;
-          }
-        }
-      }
-    };
 
     TilePos cur{0, 0, 0};
-    Raw kr, vr;
     Where w{}, next_w{};
     bool any = advance(cur), fetched = false;
 #pragma unroll 1
     while (any && !gave_up(bars)) {
       if (!fetched) {
         w = locate(cur);
-        check(w);
-        load(kr, w, p.pool.k);
-        load(vr, w, p.pool.v);
+        load(cur, w);
       }
       TilePos next = cur;
       const bool more = look_ahead(next);
       if (more) next_w = locate(next);
       const int slot = cur.k % kSlots;
       const WorkItem& it = bars->slot[slot];
-      const int alt = it.alt, n0 = it.n0, n1 = it.n1;
-      const bool use0 = alt ? !(cur.u & 1) : cur.u < n0, use1 = alt ? cur.u & 1 : cur.u < n1;
-      auto pass_on = [&]() {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
-          if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
-          if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
-        }
-        if (use0) turn[0].skip(1, kStages);
-        if (use1) turn[1].skip(1, kStages);
-        r.skip(1, kStages);
-      };
-      // ---- keys
+      const int alt = it.alt;
+      const bool use0 = alt ? !(cur.u & 1) : cur.u < it.n0, use1 = alt ? cur.u & 1 : cur.u < it.n1;
       wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
-      if (busy) convert(kr, to0 + r.s * kTileBytes);
-      pass_on();
-      // ---- the item's queries, when the one before has no scores left to compute
-      if (cur.u == 0) {
-        const WorkItem item = load_item(&it);
-#pragma unroll 1
-        for (int x = 0; x < (alt ? 1 : 2); ++x) {
-          const bool twice = alt && n1 > 0;
-          if ((x ? n1 : n0) == 0) continue;
-          wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
-          q_ph ^= 1u << x;
-          if (twice) {
-            wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
-            q_ph ^= 2u;
-          }
-          queries(item, slot, x, twice);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars->q_full[x]);
-            if (twice) mbar_arrive(&bars->q_full[1]);
-          }
-        }
+      uint32_t sx = raw.s.x, sy = second ? raw.s.y : 0;
+      if (w.left < 4) {                              // keys past the end: zero
+        const uint32_t keep = (1u << 8 * max(w.left, 0)) - 1;
+        sx &= keep;
+        sy &= keep;
       }
-      if (more) {
-        check(next_w);
-        load(kr, next_w, p.pool.k);
-      }
-      // ---- values; those that are NaN and that some row does not see are taken out: 0 * NaN would stay
-      if (__any_sync(0xffffffffu, w.own_key >= 0 && (kv4_nan_scales(vr.s.x) | kv4_nan_scales(vr.s.y)) != 0)) {
+      // values that are NaN and that some row does not see are taken out: 0 * NaN would stay
+      if (value && __any_sync(0xffffffffu, w.own_key >= 0 && (kv4_nan_scales(sx) | kv4_nan_scales(sy)) != 0)) {
         const int seen_by_all = all_see(load_item(&it), g);
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           if (w.own_key < 0 || w.own_key + i < seen_by_all) continue;
           const uint32_t byte = 0xffu << 8 * i, top = 0x80u << 8 * i;
-          if (kv4_nan_scales(vr.s.x) & top) {
-            vr.s.x &= ~byte;
+          if (kv4_nan_scales(sx) & top) {
+            sx &= ~byte;
             atomicMin(&bars->nan_key[slot][2 * c], w.own_key + i);
           }
-          if (kv4_nan_scales(vr.s.y) & top) {
-            vr.s.y &= ~byte;
+          if (kv4_nan_scales(sy) & top) {
+            sy &= ~byte;
             atomicMin(&bars->nan_key[slot][2 * c + 1], w.own_key + i);
           }
         }
       }
-      wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
-      if (busy) convert(vr, to0 + r.s * kTileBytes);
-      pass_on();
-      if (next.k != cur.k) slot_done(bars, cur.k);
-      if (more) {
-        load(vr, next_w, p.pool.v);
-        w = next_w;
+      if (busy) convert(sx, sy, to0 + r.s * kTileBytes);
+      if (more) load(next, next_w);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
+        if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
+        if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
       }
+      if (use0) turn[0].skip(2, kStages);
+      if (use1) turn[1].skip(2, kStages);
+      r.skip(2, kStages);
+      if (next.k != cur.k) slot_done(bars, cur.k);
+      w = next_w;
       cur = next;
       fetched = more;
       any = more || advance(cur);
