@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 // earlier, so memory has most of a tile's time (1.3 us) to answer.
 constexpr int kTileThreads = 768;
 // Registers of the warpgroups: 80 for each of 768 threads at the launch.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 120, kIssueRegs = 56, kOutRegs = 72, kConvertRegs = 56;
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 64, kConvertRegs = 64;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + 2 * kConvertRegs <= 6 * kLaunchRegs, "what the launch owns");
 
 // Ring stages that fit beside the query tiles and the staging.
@@ -966,15 +966,15 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
         const bool some_nan = __any_sync(0xffffffffu, nan_key[lane & 7] != INT32_MAX);
         const int own_vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t v[32];
-          if (n > 0) tmem_ld32(tO + c, v);
+        for (int c = 0; c < kD; c += 16) {
+          uint32_t v[16];
+          if (n > 0) tmem_ld16(tO + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
           if (merging) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
+            for (int x = 0; x < 16; x += 8) {
               uint32_t w[8];
               tmem_ld8(tO + kRows + c + x, w);
               tmem_ld_wait();
@@ -985,34 +985,33 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
           }
           if (some_none) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = none ? 0u : v[e];
+            for (int e = 0; e < 16; ++e) v[e] = none ? 0u : v[e];
           }
-          if (some_nan) {
-            const bool a = nan_key[c / 16] < own_vis, b = nan_key[c / 16 + 1] < own_vis;
+          if (some_nan && nan_key[c / 16] < own_vis) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e < 16 ? a : b) v[e] = 0x7fc00000u;
+            for (int e = 0; e < 16; ++e) v[e] = 0x7fc00000u;
           }
-          if (c + 32 >= kD) free_o();
+          if (c + 16 >= kD) free_o();
           // the block's bulk copy before has been read: of this item, or of one before it whose rows were output
-          if (!(c & 32)) {
+          if (!(c & 48)) {
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
           }
           if (direct) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              st_shared16(stage_at(stage_out, lane, (c & 32) / 8 + q),
+            for (int q = 0; q < 2; ++q)
+              st_shared16(stage_at(stage_out, lane, (c & 48) / 8 + q),
                           make_uint4(bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
                                      bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
                                      bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
                                      bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]))));
-            if (!(c & 32) && c + 32 < kD) continue;
+            if ((c & 48) != 48 && c + 16 < kD) continue;
           } else {
-            // a partial row's 32 columns have the block to themselves: the warp has read the ones before
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              st_shared16(stage_at(stage_out, lane, q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+            for (int q = 0; q < 4; ++q)
+              st_shared16(stage_at(stage_out, lane, (c & 16) / 4 + q),
+                          make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+            if (!(c & 16)) continue;
           }
           if (bulk) {
             fence_async_smem();
@@ -1023,7 +1022,7 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
           }
           __syncwarp();
           uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(g.part_out);
-          const int piece = lane & 7, row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & 64) * 2 : c * 4) + piece * 16;
+          const int piece = lane & 7, row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & 64) * 2 : (c & ~31) * 4) + piece * 16;
 #pragma unroll 4
           for (int r0 = 0; r0 < 32; r0 += 4) {
             const int r = r0 + (lane >> 3);
