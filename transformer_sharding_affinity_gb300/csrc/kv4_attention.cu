@@ -16,7 +16,6 @@
 #include "sm103_primitives.cuh"
 #include "step.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -496,24 +495,29 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 //   warp 8           claims items, and asks for an item's queries an item ahead (into L2)
 //   warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from shared memory) and O += P V (P from
 //                    tensor memory)
-//   warps 12-15      the next item's queries, as fp16 tiles; output, while the softmax goes on to the next item
-//   warps 16-19      keys, and warps 20-23 values: from global memory through registers to fp16 tiles in shared
-//                    memory, in the 128-byte swizzle that the products read
+//   warp 11          copies tiles as they lie in the cache, keys and values into a buffer each, through the page tables
+//   warps 12-15      output, while the softmax goes on to the next item
+//   warps 16-19      keys, and warps 20-23 values: from that buffer to fp16 tiles in the 128-byte swizzle that the
+//                    products read
+//   warps 12-23      the next item's queries, as fp16 tiles
 // Tensor memory is laid out as in attention.cu.
 //
 // A thread of warps 16-23 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
-// for each of the two blocks.  The next tile's are asked for when this tile's have been converted, its page a tile
-// earlier, so memory has most of a tile's time (1.3 us) to answer.
+// for each of the two blocks.  The buffer is free again, and the next tile on its way, as soon as that is in registers.
+// (Without the buffer, loaded from global memory a tile ahead, the same took 1.4 times as long: with 220 KB of shared
+// memory there is hardly any first cache left for the loads to pass through.  Spilled registers cost as much: the split of
+// registers is the one whose tile walks spill nothing.)
 constexpr int kTileThreads = 768;
 // Registers of the warpgroups: 80 for each of 768 threads at the launch.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 64, kConvertRegs = 64;
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 72, kConvertRegs = 56;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + 2 * kConvertRegs <= 6 * kLaunchRegs, "what the launch owns");
 
-// Ring stages that fit beside the query tiles and the staging.
+// Ring stages that fit beside the query tiles, the copies and the staging.
 __host__ __device__ constexpr int kv4_stages(int halves) { return halves == 2 ? 4 : 6; }
 
 struct alignas(16) TileBars {
   uint64_t kv_ready[2][6], kv_empty[6];      // kv_ready: each stream's own tiles, in its own order
+  uint64_t raw_full[2], raw_empty[2];        // keys, values
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2];   // [stream][score buffer]
   uint64_t stat_full[2], stat_empty[2], drain[2], slot_full[kSlots], slot_empty[kSlots];
   alignas(16) WorkItem slot[kSlots];         // row0 < 0: no more
@@ -521,22 +525,26 @@ struct alignas(16) TileBars {
   uint32_t tmem;
   int abort_flag;
 };
-constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + kStageOut + 2 * kRows * 8 + kSlots * 2 * kRows * 4 + (int)sizeof(TileBars);
+constexpr int kRawBytes = kKeyTile * 4 * 18;           // a tile's keys or values as they lie in the cache
+constexpr int kTileStage = 4 * 32 * 64;                // output staging: 32 rows of 64 bytes for each output warp
+constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + 2 * kRawBytes + kTileStage + 2 * kRows * 8 + kSlots * 2 * kRows * 4 +
+                          (int)sizeof(TileBars);
 static_assert(kTileSmem <= kSmemMax, "fits an SM");
 
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-struct TilePos {
-  int k, u, n;                               // item, tile of it, its tiles
-};
-
 template <int NC>
 __global__ void __launch_bounds__(kTileThreads, 1)
-kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Kv4AttnParams p) {
+kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr int kHalves = NC > 2 ? 2 : 1, kD = 32 * NC, kSlices = 2 * NC, kStages = kv4_stages(kHalves);
   constexpr int kTileBytes = kHalves * kHalfBytes;
@@ -544,8 +552,9 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = smem;                              // two row tiles
   uint8_t* kv_smem = smem + 2 * kTileBytes;
-  uint8_t* out_smem = kv_smem + kStages * kTileBytes;
-  float2* stats = reinterpret_cast<float2*>(out_smem + kStageOut);      // [stream][row]: (m, l)
+  uint8_t* raw_smem = kv_smem + kStages * kTileBytes;                  // keys, values: codes, then scales
+  uint8_t* out_smem = raw_smem + 2 * kRawBytes;
+  float2* stats = reinterpret_cast<float2*>(out_smem + kTileStage);     // [stream][row]: (m, l)
   float* q_factor = reinterpret_cast<float*>(stats + 2 * kRows);        // [slot][stream][row]: of the scores
   TileBars* bars = reinterpret_cast<TileBars*>(q_factor + kSlots * 2 * kRows);
   uint32_t* status = &g.head->status;
@@ -558,7 +567,7 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       mbar_init(&bars->kv_empty[i], 2);      // the streams; the converting warps stand in for one that does not use it
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->q_full[s], 4);
+      mbar_init(&bars->q_full[s], 12);
       mbar_init(&bars->q_empty[s], 1);
       mbar_init(&bars->drain[s], 1);
       for (int b = 0; b < 2; ++b) {
@@ -570,10 +579,12 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       mbar_init(&bars->stat_full[s], 4);
       mbar_init(&bars->stat_empty[s], 4);
       mbar_init(&bars->o_empty[s], 4);
+      mbar_init(&bars->raw_full[s], 1);
+      mbar_init(&bars->raw_empty[s], 4);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars->slot_full[i], 1);
-      mbar_init(&bars->slot_empty[i], 22);   // softmax warps 8, output 4, product 2, converting 8
+      mbar_init(&bars->slot_empty[i], 23);   // softmax warps 8, output 4, product 2, converting 8, copying 1
     }
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -591,6 +602,88 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
   const bool good = fits && g.head->n_items >= 0;
   // a plan of other shapes, or of a malformed step: said by every call, as the status is cleared when it is read
   if (!good && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
+
+  // An item's queries, a row tile a stream (the same one, where both hold the same rows), by twelve warps: eight rows at
+  // a time, four lanes to a row.  A lane's chunks of 16 bytes lie 64 bytes apart, in another order in odd rows: a
+  // quarter warp's stores meet in no bank then.
+  auto queries = [&](int k, int w12, uint32_t& q_ph) {
+    const WorkItem it = load_item(&bars->slot[k % kSlots]);
+    const int l4 = lane & 3, sub = lane >> 2;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q);
+    const bool twice = it.alt && it.n1 > 0;
+    const int flip = NC % 2 == 0 ? sub & 1 : 0;
+    int x = -1;                                      // the stream whose queries are under way
+    auto next_stream = [&]() {                       // hands over stream x, waits for the next one's tile to be free
+      if (x >= 0) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if ((x ? it.n1 : it.n0) > 0) mbar_arrive(&bars->q_full[x]);
+          if (twice) mbar_arrive(&bars->q_full[1]);
+        }
+      }
+      ++x;
+      if (x < (it.alt ? 1 : 2)) {
+        if ((x ? it.n1 : it.n0) > 0) {
+          wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+          q_ph ^= 1u << x;
+        }
+        if (twice) {
+          wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
+          q_ph ^= 2u;
+        }
+      }
+    };
+    if (it.n0 + it.n1 == 0) return;
+    const int tasks = it.alt ? 16 : 32;
+#pragma unroll 1
+    for (int t = w12; t < tasks; t += 12) {
+      const int row = (t & 15) * 8 + sub, r_item = t * 8 + sub;
+      uint4 w[NC];
+#pragma unroll
+      for (int y = 0; y < NC; ++y) w[y] = make_uint4(0, 0, 0, 0);
+      if (r_item < it.nrows) {
+        const int rr = it.row0 + r_item, tok = g.by_R(rr);
+        const uint16_t* from = q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+#pragma unroll
+        for (int y = 0; y < NC; ++y) {
+          const int e = (l4 + 4 * (y ^ flip)) * 8;
+          if (e < g.d) w[y] = __ldg(reinterpret_cast<const uint4*>(from + e));
+        }
+      }
+      while (x < t >> 4) next_stream();
+      if ((x ? it.n1 : it.n0) == 0) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int y = 0; y < NC; ++y) {
+        top = max_u16x2(top, max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu));
+        top = max_u16x2(top, max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
+      }
+      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float inverse;
+      const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
+      const uint64_t up2 = pk(up, up);
+      auto half = [&](uint32_t v) {
+        const float2 f = unpk(mul2(pk_u(v << 16, v & 0xffff0000u), up2));
+        return f16x2(f.x, f.y);
+      };
+#pragma unroll
+      for (int y = 0; y < NC; ++y) {
+        const int chunk = l4 + 4 * (y ^ flip);
+        const uint32_t at = smem_u32(q_smem) + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
+        st_shared16(at + x * kTileBytes, h);
+        if (twice) st_shared16(at + kTileBytes, h);
+      }
+      if (l4 == 0) {
+        float* to = q_factor + (k % kSlots) * 2 * kRows + row;
+        to[x * kRows] = inverse * p.score_log2;
+        if (twice) to[kRows] = inverse * p.score_log2;
+      }
+    }
+    while (x < (it.alt ? 1 : 2)) next_stream();
+  };
 
   if (warp >= 8 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -720,6 +813,66 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
         while (!mbar_test_wait(&bars->drain[s], 0) && global_timer_ns() - t0 < 2000000000ull) {}
       }
       __syncwarp();
+    } else {
+      // ---------------------------------------------------------- copies
+      // A page's codes are a lane's copy, its scales another's; a page has whole groups of 8 tokens.
+      const bool scales = lane >= 16;
+      const int box = lane & 15;
+      const int per_page = g.tile_pages ? g.page_size : g.key_tile;
+      uint32_t ph = 0, copied = 0;
+      for (int k = 0; slot_wait(bars, k); ++k) {
+        const WorkItem it = load_item(&bars->slot[k % kSlots]);
+        const int n = item_tiles(it);
+        const int64_t group = it.group * p.pool.group_stride;
+        int page = 0, token = 0, keys = 0, mine = 0;
+        auto locate = [&](int u) {           // asks for the page of this lane's share of a tile
+          const bool pre = it.t0 + u < it.np;
+          int key0;
+          keys = tile_keys(it, g, it.t0 + u, &key0);
+          const int key = key0 + box * per_page;
+          mine = min(per_page, keys - box * per_page);
+          page = token = 0;
+          if (mine > 0) {
+            const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+            const int pi = g.by_page(key);
+            page = __ldg(table + pi);
+            token = key - pi * g.page_size;
+          }
+        };
+        if (n > 0) locate(0);
+#pragma unroll 1
+        for (int u = 0; u < n && !gave_up(bars); ++u) {
+          const uint32_t total = ((keys + 7) & ~7) * 18 * NC;
+          const uint32_t count = mine > 0 ? ((mine + 7) & ~7) : 0;
+          if (count && (page < 0 || page >= g.n_pages)) {      // reported; what is copied instead does not matter
+            latch_status(status, kStatusRange);
+            page = 0;
+          }
+          const int64_t from = page * p.pool.page_stride + group + (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
+          const uint32_t to = smem_u32(raw_smem) + (scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC
+                                                           : box * per_page * 16 * NC);
+          const uint32_t bytes = count * (scales ? 2 * NC : 16 * NC);
+          if (u + 1 < n) locate(u + 1);
+#pragma unroll 1
+          for (int value = 0; value < 2; ++value) {
+            wait_on(&bars->raw_empty[value], ph ^ 1u, bars);
+            if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[value], total);
+            __syncwarp();
+            if (bytes) copy_bulk(to + value * kRawBytes, (value ? p.pool.v : p.pool.k) + from, bytes, &bars->raw_full[value]);
+            __syncwarp();
+          }
+          ph ^= 1u;
+          copied = 1;
+        }
+        slot_done(bars, k);
+      }
+      if (copied) {                          // shared memory goes away: the last copies have to be there
+        for (int value = 0; value < 2; ++value) {
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_test_wait(&bars->raw_full[value], ph ^ 1u) && global_timer_ns() - t0 < 2000000000ull) {}
+        }
+      }
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -833,74 +986,12 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     const int row = threadIdx.x & (kRows - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t stage_out = smem_u32(out_smem) + (warp & 3) * 4096;
+    // 16 bytes of row `row` of a warp's 32 rows of 64 bytes, in place c of 4: eight rows' stores meet in no bank
+    auto staged = [&](int row, int c) { return smem_u32(out_smem) + (warp & 3) * 2048 + row * 64 + ((c ^ (row >> 1 & 3)) << 4); };
     uint32_t ph = 0, q_ph = 0;                       // bit s: stream s
-    // An item's queries, a row tile a stream (the same one, where both hold the same rows): 32 rows to a warp, 16 lanes
-    // (8, 4) to a row.  The first are on their way before the item before has no scores left to compute.
-    auto queries = [&](int k) {
-      constexpr int kLanes = NC > 2 ? 16 : 4 * NC, kPer = 32 / kLanes, kAhead = 4;
-      const WorkItem it = load_item(&bars->slot[k % kSlots]);
-      const int lc = lane % kLanes, sub = lane / kLanes, cw = warp & 3;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q);
-      const bool twice = it.alt && it.n1 > 0;
-#pragma unroll 1
-      for (int x = 0; x < (it.alt ? 1 : 2); ++x) {
-        if ((x ? it.n1 : it.n0) == 0) continue;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += kPer * kAhead) {
-          uint4 w[kAhead];
-#pragma unroll
-          for (int y = 0; y < kAhead; ++y) {
-            const int r_item = x * kRows + cw * 32 + r0 + y * kPer + sub;
-            w[y] = make_uint4(0, 0, 0, 0);
-            if (r_item < it.nrows && lc * 8 < g.d) {
-              const int rr = it.row0 + r_item, tok = g.by_R(rr);
-              w[y] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)tok * p.q_stride +
-                                                          (it.group * g.R + rr - tok * g.R) * g.d + lc * 8));
-            }
-          }
-          if (r0 == 0) {
-            wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
-            q_ph ^= 1u << x;
-            if (twice) {
-              wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
-              q_ph ^= 2u;
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < kAhead; ++y) {
-            const int r = cw * 32 + r0 + y * kPer + sub;
-            uint32_t top = max_u16x2(max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
-                                     max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float inverse;
-            const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
-            auto half = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-            const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
-            const uint32_t at = smem_u32(q_smem) + (lc >> 3) * kHalfBytes + r * 128 + (((lc & 7) ^ (r & 7)) << 4);
-            if (lc * 8 < kD) {
-              st_shared16(at + x * kTileBytes, h);
-              if (twice) st_shared16(at + kTileBytes, h);
-            }
-            if (lc == 0) {
-              float* to = q_factor + (k % kSlots) * 2 * kRows + r;
-              to[x * kRows] = inverse * p.score_log2;
-              if (twice) to[kRows] = inverse * p.score_log2;
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->q_full[x]);
-          if (twice) mbar_arrive(&bars->q_full[1]);
-        }
-      }
-    };
-    if (slot_wait(bars, 0)) queries(0);
+    if (slot_wait(bars, 0)) queries(0, warp - 12, q_ph);
     for (int k = 0; slot_wait(bars, k); ++k) {
-      if (slot_wait(bars, k + 1)) queries(k + 1);
+      if (slot_wait(bars, k + 1)) queries(k + 1, warp - 12, q_ph);
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
 #pragma unroll 1
@@ -954,13 +1045,10 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
         tc_fence_after();
         const int h = it.group * g.R + rr - tok * g.R;
         const bool direct = it.part_row < 0;
-        // 128 bytes of each row at a time go through shared memory: 64 bf16 columns of the output, 32 fp32
-        // columns of a partial row.  A warp whose 32 rows are all there (and whole tokens) writes output
-        // as one bulk copy; otherwise stores of whole lines, with the rows' numbers from their lanes.
-        const bool bulk = direct && 32 % g.R == 0 && (row & ~31) + s * kRows + 32 <= it.nrows;
+        // 64 bytes of each row at a time go through shared memory, 32 bf16 columns of the output or 16 fp32 columns of a
+        // partial row, so that four lanes store two whole sectors of a row; the rows' numbers come from their lanes.
         const int mine = !live ? -1 : direct ? tok * g.H + h : it.part_row + r_item;
         const bool none = l == 0.f, some_none = __any_sync(0xffffffffu, none);   // rows without keys are zero
-        const int first_tok = __shfl_sync(0xffffffffu, tok, 0);
         // values that are NaN and were taken out of the tiles: of the rows that see their keys
         const int* nan_key = bars->nan_key[k % kSlots];
         const bool some_nan = __any_sync(0xffffffffu, nan_key[lane & 7] != INT32_MAX);
@@ -992,43 +1080,29 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
             for (int e = 0; e < 16; ++e) v[e] = 0x7fc00000u;
           }
           if (c + 16 >= kD) free_o();
-          // the block's bulk copy before has been read: of this item, or of one before it whose rows were output
-          if (!(c & 48)) {
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-          }
           if (direct) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              st_shared16(stage_at(stage_out, lane, (c & 48) / 8 + q),
+              st_shared16(staged(lane, (c & 16) / 8 + q),
                           make_uint4(bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
                                      bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
                                      bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
                                      bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]))));
-            if ((c & 48) != 48 && c + 16 < kD) continue;
+            if (!(c & 16)) continue;
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              st_shared16(stage_at(stage_out, lane, (c & 16) / 4 + q),
-                          make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-            if (!(c & 16)) continue;
-          }
-          if (bulk) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tma_store_4d(out_smem + (warp & 3) * 4096, &map_out, c & 64, 0, it.group, first_tok);
-            __syncwarp();
-            continue;
+              st_shared16(staged(lane, q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
           }
           __syncwarp();
           uint8_t* const to = direct ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(g.part_out);
-          const int piece = lane & 7, row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & 64) * 2 : (c & ~31) * 4) + piece * 16;
-#pragma unroll 4
-          for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + (lane >> 3);
+          const int row_bytes = g.d * (direct ? 2 : 4), byte = (direct ? (c & ~31) * 2 : c * 4) + (lane & 3) * 16;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            const int r = r0 + (lane >> 2);
             const int which = __shfl_sync(0xffffffffu, mine, r);
             if (which >= 0 && byte < row_bytes)
-              *reinterpret_cast<uint4*>(to + (int64_t)which * row_bytes + byte) = ld_shared16(stage_at(stage_out, r, piece));
+              *reinterpret_cast<uint4*>(to + (int64_t)which * row_bytes + byte) = ld_shared16(staged(r, lane & 3));
           }
           __syncwarp();
         }
@@ -1040,8 +1114,6 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
       }
       slot_done(bars, k);
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ keys and values
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
@@ -1050,168 +1122,107 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
     const bool busy = ct < 32 * NC;                  // a chunk c of keys 4 j .. 4 j + 3
     const int j = ct / NC, c = ct - j * NC;
     const bool second = 32 * c + 16 < g.d;           // the chunk's other block holds elements
-    // Words go out in an order of the lane's own, x ^ f for x = 0 .. 3, so that a quarter warp's 16-byte stores meet in
-    // no bank: rows that are alike modulo 8 lie four threads of keys apart.  The words' halves are loaded in that order.
-    const int f = NC > 2 ? (c >> 1) | (j & 1) << 1 : (j >> 1 & 1) | (j & 1) << 1;
-    const uint32_t place = ((((c & 1) << 2) | f) ^ ((j & 1) << 2)) << 4;
+    // Words go out in an order of the lane's own, x ^ f for x = 0 .. 3, and odd threads of keys take their keys in the order
+    // 1 0 3 2, so that a quarter warp's 16-byte loads and stores meet in no bank.
+    const int f = NC > 2 ? (c >> 1) | (j & 1) << 1 : (j >> 1 & 1) | (j & 1) << 1, odd = j & 1;
+    const uint32_t place = ((((c & 1) << 2) | f) ^ (odd << 2 | odd)) << 4;
     const uint32_t to0 = smem_u32(kv_smem) + (c >> 1) * kHalfBytes + 4 * j * 128;
-    constexpr int kRowBytes = 16 * NC;
-    struct Raw {
-      uint2 lo[4], hi[4], s;
-    } raw;
+    const uint32_t raw = smem_u32(raw_smem) + value * kRawBytes;
     Ring r, turn[2];                                 // keys and values take the ring's stages in turns
     if (value) {
       r.skip(1, kStages);
       turn[0].skip(1, kStages);
       turn[1].skip(1, kStages);
     }
-
-    // the next tile of the item or, if it has one, the first of the item after it
-    auto look_ahead = [&](TilePos& t) {
-      if (t.u + 1 < t.n) {
-        ++t.u;
-        return true;
-      }
-      t.u = 0;
-      ++t.k;
-      t.n = slot_wait(bars, t.k) ? item_tiles(bars->slot[t.k % kSlots]) : 0;
-      return t.n > 0;
-    };
-    // past items without tiles; no slot may be held meanwhile, the items might not fit the others
-    auto advance = [&](TilePos& t) {
-      t.u = 0;
-      for (; slot_wait(bars, t.k); ++t.k) {
-        t.n = item_tiles(bars->slot[t.k % kSlots]);
-        if (t.n > 0) return true;
-        slot_done(bars, t.k);
-      }
-      return false;
-    };
-    struct Where {
-      int page, in_page, left;                       // of this thread's keys; keys from the first of them on
-      int own_key;                                   // the first of them among the sequence's own; -1: the prefix's
-    };
-    auto locate = [&](const TilePos& t) {            // asks for the page
-      const WorkItem& it = bars->slot[t.k % kSlots];
-      const int ti = it.t0 + t.u;
-      const bool pre = ti < it.np;
-      int key0;
-      const int keys = tile_span(g, pre ? g.prefix_len : it.own_len, pre ? ti : ti - it.np, &key0);
-      Where w;
-      w.left = keys - 4 * j;
-      w.own_key = pre ? -1 : key0 + 4 * j;
-      w.page = -1;
-      w.in_page = 0;
-      if (busy && w.left > 0) {
-        const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-        const int pi = g.by_page(key0 + 4 * j);
-        w.page = __ldg(table + pi);
-        w.in_page = key0 + 4 * j - pi * g.page_size;
-      }
-      return w;
-    };
-    // Nothing here looks at what is loaded: that would be waiting for it.
-    auto load = [&](const TilePos& t, Where& w) {
-      if (busy && w.left > 0 && (w.page < 0 || w.page >= g.n_pages)) {      // read as zeros: report it
-        latch_status(status, kStatusRange);
-        w.page = -1;
-      }
-      raw.s = make_uint2(0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) raw.lo[i] = raw.hi[i] = make_uint2(0, 0);
-      if (w.page >= 0) {
-        const uint8_t* page = (value ? p.pool.v : p.pool.k) + w.page * p.pool.page_stride +
-                              bars->slot[t.k % kSlots].group * p.pool.group_stride;
-        const uint8_t* at = page + w.in_page * kRowBytes + c * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          raw.lo[i] = __ldg(reinterpret_cast<const uint2*>(at + i * kRowBytes + (f & 2) * 4));
-          raw.hi[i] = __ldg(reinterpret_cast<const uint2*>(at + i * kRowBytes + 8 - (f & 2) * 4));
-        }
-        raw.s = __ldg(reinterpret_cast<const uint2*>(page + p.pool.scales + ((w.in_page >> 2) * 2 * NC + 2 * c) * 4));
-      }
-    };
-    auto convert = [&](uint32_t sx, uint32_t sy, uint32_t to) {
-      if (f & 2) {
-        const uint32_t t = sx;
-        sx = sy;
-        sy = t;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t both = kv4_scale_pair(prmt(sx, sy, i | (4 + i) << 4));
-        const uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
-        const uint2 lo = f & 1 ? make_uint2(raw.lo[i].y, raw.lo[i].x) : raw.lo[i];
-        const uint2 hi = f & 1 ? make_uint2(raw.hi[i].y, raw.hi[i].x) : raw.hi[i];
-        const uint32_t words[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t h[4];
-          kv4_decode(words[y], h);
-          const uint32_t s = y < 2 ? s0 : s1;
-          st_shared16(to + i * 128 + (place ^ (uint32_t)((y ^ i) << 4)),
-                      make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s)));
-        }
-      }
-    };
-
-    TilePos cur{0, 0, 0};
-    Where w{}, next_w{};
-    bool any = advance(cur), fetched = false;
+    uint32_t ph = 0, q_ph = 0;
+    for (int k = 0; slot_wait(bars, k); ++k) {
+      const WorkItem& it = bars->slot[k % kSlots];
+      const int n = item_tiles(it), alt = it.alt;
 #pragma unroll 1
-    while (any && !gave_up(bars)) {
-      if (!fetched) {
-        w = locate(cur);
-        load(cur, w);
-      }
-      TilePos next = cur;
-      const bool more = look_ahead(next);
-      if (more) next_w = locate(next);
-      const int slot = cur.k % kSlots;
-      const WorkItem& it = bars->slot[slot];
-      const int alt = it.alt;
-      const bool use0 = alt ? !(cur.u & 1) : cur.u < it.n0, use1 = alt ? cur.u & 1 : cur.u < it.n1;
-      wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
-      uint32_t sx = raw.s.x, sy = second ? raw.s.y : 0;
-      if (w.left < 4) {                              // keys past the end: zero
-        const uint32_t keep = (1u << 8 * max(w.left, 0)) - 1;
-        sx &= keep;
-        sy &= keep;
-      }
-      // values that are NaN and that some row does not see are taken out: 0 * NaN would stay
-      if (value && __any_sync(0xffffffffu, w.own_key >= 0 && (kv4_nan_scales(sx) | kv4_nan_scales(sy)) != 0)) {
-        const int seen_by_all = all_see(load_item(&it), g);
+      for (int u = 0; u < n && !gave_up(bars); ++u) {
+        if (value && u == 0) queries(k, 8 + cw, q_ph);
+        // ---- this thread's share of the tile, to registers
+        wait_on(&bars->raw_full[value], ph, bars);
+        ph ^= 1u;
+        uint4 w[4];
+        uint2 s = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (busy) {
+          const uint32_t at = raw + (4 * j * NC + c) * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = ld_shared16(at + (i ^ odd) * 16 * NC);
+          const uint32_t sat = raw + kKeyTile * 16 * NC + (2 * j * NC + 2 * c) * 4;
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "r"(sat) : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->raw_empty[value]);
+        // ---- scales: none of what is past d or the last key
+        const bool pre = it.t0 + u < it.np;
+        int key0;
+        const int left = tile_keys(it, g, it.t0 + u, &key0) - 4 * j;
+        if (!second) s.y = 0;
+        if (left < 4) {
+          const uint32_t keep = (1u << 8 * max(left, 0)) - 1;
+          s.x &= keep;
+          s.y &= keep;
+        }
+        // values that are NaN and that some row does not see are taken out: 0 * NaN would stay
+        if (value && __any_sync(0xffffffffu, !pre && (kv4_nan_scales(s.x) | kv4_nan_scales(s.y)) != 0)) {
+          const int seen_by_all = all_see(load_item(&it), g);
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          if (w.own_key < 0 || w.own_key + i < seen_by_all) continue;
-          const uint32_t byte = 0xffu << 8 * i, top = 0x80u << 8 * i;
-          if (kv4_nan_scales(sx) & top) {
-            sx &= ~byte;
-            atomicMin(&bars->nan_key[slot][2 * c], w.own_key + i);
-          }
-          if (kv4_nan_scales(sy) & top) {
-            sy &= ~byte;
-            atomicMin(&bars->nan_key[slot][2 * c + 1], w.own_key + i);
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 4 * j + i;
+            if (key < seen_by_all) continue;
+            const uint32_t byte = 0xffu << 8 * i, top = 0x80u << 8 * i;
+            if (kv4_nan_scales(s.x) & top) {
+              s.x &= ~byte;
+              atomicMin(&bars->nan_key[k % kSlots][2 * c], key);
+            }
+            if (kv4_nan_scales(s.y) & top) {
+              s.y &= ~byte;
+              atomicMin(&bars->nan_key[k % kSlots][2 * c + 1], key);
+            }
           }
         }
+        if (f & 2) s = make_uint2(s.y, s.x);
+        // ---- to fp16
+        wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
+        if (busy) {
+          const uint32_t to = to0 + r.s * kTileBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t both = kv4_scale_pair(prmt(s.x, s.y, (i ^ odd) | (4 + (i ^ odd)) << 4));
+            const uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
+            uint4 x = w[i];
+            if (f & 1) x = make_uint4(x.y, x.x, x.w, x.z);
+            if (f & 2) x = make_uint4(x.z, x.w, x.x, x.y);
+            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t h[4];
+              kv4_decode(words[y], h);
+              const uint32_t sc = y < 2 ? s0 : s1;
+              st_shared16(to + (i ^ odd) * 128 + (place ^ (uint32_t)((y ^ i) << 4)),
+                          make_uint4(mul_f16x2(h[0], sc), mul_f16x2(h[1], sc), mul_f16x2(h[2], sc), mul_f16x2(h[3], sc)));
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        const bool use0 = alt ? !(u & 1) : u < it.n0, use1 = alt ? u & 1 : u < it.n1;
+        if (lane == 0) {
+          if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
+          if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
+          if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
+        }
+        if (use0) turn[0].skip(2, kStages);
+        if (use1) turn[1].skip(2, kStages);
+        r.skip(2, kStages);
+        // the next item's queries come behind its first keys and before its first values
+        if (!value && u == 0) queries(k, 4 + cw, q_ph);
       }
-      if (busy) convert(sx, sy, to0 + r.s * kTileBytes);
-      if (more) load(next, next_w);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
-        if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
-        if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
-      }
-      if (use0) turn[0].skip(2, kStages);
-      if (use1) turn[1].skip(2, kStages);
-      r.skip(2, kStages);
-      if (next.k != cur.k) slot_done(bars, cur.k);
-      w = next_w;
-      cur = next;
-      fetched = more;
-      any = more || advance(cur);
+      slot_done(bars, k);
     }
   }
 
@@ -1233,7 +1244,7 @@ kv4_tile_kernel(const __grid_constant__ CUtensorMap map_out, const __grid_consta
 }
 
 template <int NC>
-aff_status launch_tile(const CUtensorMap& map_out, const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
+aff_status launch_tile(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
   // The register split needs the launch to own that many: a matter of the compiled kernel, asked once.  The
   // shared-memory limit belongs to the current device, so it is set for every call.
   static std::atomic<int> regs{0};
@@ -1244,7 +1255,7 @@ aff_status launch_tile(const CUtensorMap& map_out, const Kv4AttnParams& p, unsig
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) AFF_CUDA(cudaErrorInvalidConfiguration);
   AFF_CUDA(cudaFuncSetAttribute(kv4_tile_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
-  AFF_CUDA(launch_pdl(kv4_tile_kernel<NC>, grid, kTileThreads, (size_t)kTileSmem, s, map_out, p));
+  AFF_CUDA(launch_pdl(kv4_tile_kernel<NC>, grid, kTileThreads, (size_t)kTileSmem, s, p));
   return AFF_OK;
 }
 
@@ -1288,18 +1299,12 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
   // all rows of a step of at most 8 are one sequence's few-rows items; otherwise only the device knows (step.cuh)
   const bool tiles = g.dtype == AFF_BF16 && !(g.few && (int64_t)g.T * g.R <= g.few_rows);
   if (tiles) {
-    CUtensorMap out_map{};
-    if (32 % g.R == 0) {
-      const uint64_t od[4] = {(uint64_t)g.d, (uint64_t)g.R, (uint64_t)g.G, (uint64_t)g.T};
-      const uint64_t os[3] = {(uint64_t)g.d * 2, (uint64_t)g.R * g.d * 2, (uint64_t)g.H * g.d * 2};
-      if ((st = map_16bit_sw128(&out_map, out, 4, od, os, (uint32_t)g.R, 1, (uint32_t)(32 / g.R), 3)) != AFF_OK) return st;
-    }
     const unsigned grid = (unsigned)(g.max_items < sms ? g.max_items : sms);
     switch (p.pool.n) {
-      case 1: st = launch_tile<1>(out_map, p, grid, s); break;
-      case 2: st = launch_tile<2>(out_map, p, grid, s); break;
-      case 3: st = launch_tile<3>(out_map, p, grid, s); break;
-      default: st = launch_tile<4>(out_map, p, grid, s); break;
+      case 1: st = launch_tile<1>(p, grid, s); break;
+      case 2: st = launch_tile<2>(p, grid, s); break;
+      case 3: st = launch_tile<3>(p, grid, s); break;
+      default: st = launch_tile<4>(p, grid, s); break;
     }
     if (st != AFF_OK) return st;
   }
