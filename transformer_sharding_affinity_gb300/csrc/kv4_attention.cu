@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 // registers is the one whose tile walks spill nothing.)
 constexpr int kTileThreads = 768;
 // Registers of the warpgroups: 80 for each of 768 threads at the launch.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 72, kConvertRegs = 56;
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 72, kOutRegs = 72, kConvertRegs = 56;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + 2 * kConvertRegs <= 6 * kLaunchRegs, "what the launch owns");
 
 // Ring stages that fit beside the query tiles, the copies and the staging.
@@ -820,38 +820,35 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       const int box = lane & 15;
       const int per_page = g.tile_pages ? g.page_size : g.key_tile;
       uint32_t ph = 0, copied = 0;
+      const uint32_t to = smem_u32(raw_smem) + (scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC : box * per_page * 16 * NC);
       for (int k = 0; slot_wait(bars, k); ++k) {
-        const WorkItem it = load_item(&bars->slot[k % kSlots]);
+        const WorkItem& it = bars->slot[k % kSlots];
         const int n = item_tiles(it);
-        const int64_t group = it.group * p.pool.group_stride;
-        int page = 0, token = 0, keys = 0, mine = 0;
+        int page = 0, token = 0, keys = 0;
         auto locate = [&](int u) {           // asks for the page of this lane's share of a tile
           const bool pre = it.t0 + u < it.np;
           int key0;
           keys = tile_keys(it, g, it.t0 + u, &key0);
-          const int key = key0 + box * per_page;
-          mine = min(per_page, keys - box * per_page);
-          page = token = 0;
-          if (mine > 0) {
+          key0 += box * per_page;
+          if (box * per_page < keys) {
             const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-            const int pi = g.by_page(key);
+            const int pi = g.by_page(key0);
             page = __ldg(table + pi);
-            token = key - pi * g.page_size;
+            token = key0 - pi * g.page_size;
           }
         };
         if (n > 0) locate(0);
 #pragma unroll 1
         for (int u = 0; u < n && !gave_up(bars); ++u) {
           const uint32_t total = ((keys + 7) & ~7) * 18 * NC;
-          const uint32_t count = mine > 0 ? ((mine + 7) & ~7) : 0;
-          if (count && (page < 0 || page >= g.n_pages)) {      // reported; what is copied instead does not matter
+          const int mine = min(per_page, keys - box * per_page);
+          const uint32_t bytes = mine > 0 ? ((mine + 7) & ~7) * (scales ? 2 * NC : 16 * NC) : 0;
+          if (bytes && (page < 0 || page >= g.n_pages)) {      // reported; what is copied instead does not matter
             latch_status(status, kStatusRange);
             page = 0;
           }
-          const int64_t from = page * p.pool.page_stride + group + (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
-          const uint32_t to = smem_u32(raw_smem) + (scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC
-                                                           : box * per_page * 16 * NC);
-          const uint32_t bytes = count * (scales ? 2 * NC : 16 * NC);
+          const int64_t from = page * p.pool.page_stride + it.group * p.pool.group_stride +
+                               (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
           if (u + 1 < n) locate(u + 1);
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
@@ -1122,18 +1119,17 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     const bool busy = ct < 32 * NC;                  // a chunk c of keys 4 j .. 4 j + 3
     const int j = ct / NC, c = ct - j * NC;
     const bool second = 32 * c + 16 < g.d;           // the chunk's other block holds elements
-    // Words go out in an order of the lane's own, x ^ f for x = 0 .. 3, and odd threads of keys take their keys in the order
-    // 1 0 3 2, so that a quarter warp's 16-byte loads and stores meet in no bank.
-    const int f = NC > 2 ? (c >> 1) | (j & 1) << 1 : (j >> 1 & 1) | (j & 1) << 1, odd = j & 1;
-    const uint32_t place = ((((c & 1) << 2) | f) ^ (odd << 2 | odd)) << 4;
+    // A thread takes its keys in an order of its own, i ^ o for i = 0 .. 3, so that a quarter warp's 16-byte loads (two keys
+    // beside each other, four chunks) and stores (a swizzled row's pieces) meet in no bank.
+    const int o = NC > 2 ? (c >> 1) << 1 | (j & 1) : NC == 2 ? j & 3 : j >> 1 & 3;
+    const uint32_t place = ((((c & 1) ^ (j & 1)) << 2) ^ o) << 4;
+    const uint32_t pick = o | (4 + o) << 4;          // of a key's two scales
     const uint32_t to0 = smem_u32(kv_smem) + (c >> 1) * kHalfBytes + 4 * j * 128;
     const uint32_t raw = smem_u32(raw_smem) + value * kRawBytes;
-    Ring r, turn[2];                                 // keys and values take the ring's stages in turns
-    if (value) {
-      r.skip(1, kStages);
-      turn[0].skip(1, kStages);
-      turn[1].skip(1, kStages);
-    }
+    Ring r;                                          // keys and values take the ring's stages in turns
+    r.s = value;
+    int turn0 = value, turn1 = value;                // of the streams' own tiles
+    const uint32_t at = raw + (4 * j * NC + c) * 16, sat = raw + kKeyTile * 16 * NC + (2 * j * NC + 2 * c) * 4;
     uint32_t ph = 0, q_ph = 0;
     for (int k = 0; slot_wait(bars, k); ++k) {
       const WorkItem& it = bars->slot[k % kSlots];
@@ -1141,22 +1137,10 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
 #pragma unroll 1
       for (int u = 0; u < n && !gave_up(bars); ++u) {
         if (value && u == 0) queries(k, 8 + cw, q_ph);
-        // ---- this thread's share of the tile, to registers
         wait_on(&bars->raw_full[value], ph, bars);
         ph ^= 1u;
-        uint4 w[4];
         uint2 s = make_uint2(0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (busy) {
-          const uint32_t at = raw + (4 * j * NC + c) * 16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ld_shared16(at + (i ^ odd) * 16 * NC);
-          const uint32_t sat = raw + kKeyTile * 16 * NC + (2 * j * NC + 2 * c) * 4;
-          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "r"(sat) : "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->raw_empty[value]);
+        if (busy) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "r"(sat) : "memory");
         // ---- scales: none of what is past d or the last key
         const bool pre = it.t0 + u < it.np;
         int key0;
@@ -1185,25 +1169,22 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
             }
           }
         }
-        if (f & 2) s = make_uint2(s.y, s.x);
         // ---- to fp16
         wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
         if (busy) {
           const uint32_t to = to0 + r.s * kTileBytes;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t both = kv4_scale_pair(prmt(s.x, s.y, (i ^ odd) | (4 + (i ^ odd)) << 4));
+            const uint32_t both = kv4_scale_pair(prmt(s.x, s.y, pick ^ (uint32_t)(i | i << 4)));
             const uint32_t s0 = prmt(both, both, 0x1010), s1 = prmt(both, both, 0x3232);
-            uint4 x = w[i];
-            if (f & 1) x = make_uint4(x.y, x.x, x.w, x.z);
-            if (f & 2) x = make_uint4(x.z, x.w, x.x, x.y);
-            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+            const uint4 w = ld_shared16(at + (i ^ o) * 16 * NC);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint32_t h[4];
               kv4_decode(words[y], h);
               const uint32_t sc = y < 2 ? s0 : s1;
-              st_shared16(to + (i ^ odd) * 128 + (place ^ (uint32_t)((y ^ i) << 4)),
+              st_shared16(to + (i ^ o) * 128 + (place ^ (uint32_t)((y ^ i) << 4)),
                           make_uint4(mul_f16x2(h[0], sc), mul_f16x2(h[1], sc), mul_f16x2(h[2], sc), mul_f16x2(h[3], sc)));
             }
           }
@@ -1212,12 +1193,13 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         __syncwarp();
         const bool use0 = alt ? !(u & 1) : u < it.n0, use1 = alt ? u & 1 : u < it.n1;
         if (lane == 0) {
-          if (use0) mbar_arrive(&bars->kv_ready[0][turn[0].s]);
-          if (use1) mbar_arrive(&bars->kv_ready[1][turn[1].s]);
+          mbar_arrive(&bars->raw_empty[value]);
+          if (use0) mbar_arrive(&bars->kv_ready[0][turn0]);
+          if (use1) mbar_arrive(&bars->kv_ready[1][turn1]);
           if (cw == 0 && !(use0 && use1)) mbar_arrive(&bars->kv_empty[r.s]);
         }
-        if (use0) turn[0].skip(2, kStages);
-        if (use1) turn[1].skip(2, kStages);
+        if (use0) turn0 = turn0 + 2 >= kStages ? value : turn0 + 2;
+        if (use1) turn1 = turn1 + 2 >= kStages ? value : turn1 + 2;
         r.skip(2, kStages);
         // the next item's queries come behind its first keys and before its first values
         if (!value && u == 0) queries(k, 4 + cw, q_ph);
