@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 //   warps 12-15      output, while the softmax goes on to the next item
 //   warps 16-19      keys, and warps 20-23 values: from that buffer to fp16 tiles in the 128-byte swizzle that the
 //                    products read
-//   warps 12-23      the next item's queries, as fp16 tiles
+//                    and the next item's queries
 // Tensor memory is laid out as in attention.cu.
 //
 // A thread of warps 16-23 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
@@ -536,10 +536,28 @@ __device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_
                "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+// 16 bytes that are read once: they take no room in what there is of a first cache.
+__device__ __forceinline__ uint4 load_once(const void* at) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+  return v;
+}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+// A wait that ends with the CTA's giving up: warp 8 alone looks at the clock.  Every role's progress frees slots, which
+// that warp waits for (2 s at most) to its end; so the waits in the other roles stay a few instructions each.
+__device__ __forceinline__ void await(uint64_t* bar, uint32_t parity, TileBars* b) {
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity) && !gave_up(b)) {}
+  __syncwarp();
+}
+__device__ __forceinline__ bool slot_ready(TileBars* b, int k) {
+  await(&b->slot_full[k % kSlots], (k / kSlots) & 1, b);
+  return __all_sync(0xffffffffu, !gave_up(b) && b->slot[k % kSlots].row0 >= 0);
 }
 
 template <int NC>
@@ -567,7 +585,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       mbar_init(&bars->kv_empty[i], 2);      // the streams; the converting warps stand in for one that does not use it
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->q_full[s], 12);
+      mbar_init(&bars->q_full[s], 8);
       mbar_init(&bars->q_empty[s], 1);
       mbar_init(&bars->drain[s], 1);
       for (int b = 0; b < 2; ++b) {
@@ -602,88 +620,6 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
   const bool good = fits && g.head->n_items >= 0;
   // a plan of other shapes, or of a malformed step: said by every call, as the status is cleared when it is read
   if (!good && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
-
-  // An item's queries, a row tile a stream (the same one, where both hold the same rows), by twelve warps: eight rows at
-  // a time, four lanes to a row.  A lane's chunks of 16 bytes lie 64 bytes apart, in another order in odd rows: a
-  // quarter warp's stores meet in no bank then.
-  auto queries = [&](int k, int w12, uint32_t& q_ph) {
-    const WorkItem it = load_item(&bars->slot[k % kSlots]);
-    const int l4 = lane & 3, sub = lane >> 2;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q);
-    const bool twice = it.alt && it.n1 > 0;
-    const int flip = NC % 2 == 0 ? sub & 1 : 0;
-    int x = -1;                                      // the stream whose queries are under way
-    auto next_stream = [&]() {                       // hands over stream x, waits for the next one's tile to be free
-      if (x >= 0) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if ((x ? it.n1 : it.n0) > 0) mbar_arrive(&bars->q_full[x]);
-          if (twice) mbar_arrive(&bars->q_full[1]);
-        }
-      }
-      ++x;
-      if (x < (it.alt ? 1 : 2)) {
-        if ((x ? it.n1 : it.n0) > 0) {
-          wait_on(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
-          q_ph ^= 1u << x;
-        }
-        if (twice) {
-          wait_on(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
-          q_ph ^= 2u;
-        }
-      }
-    };
-    if (it.n0 + it.n1 == 0) return;
-    const int tasks = it.alt ? 16 : 32;
-#pragma unroll 1
-    for (int t = w12; t < tasks; t += 12) {
-      const int row = (t & 15) * 8 + sub, r_item = t * 8 + sub;
-      uint4 w[NC];
-#pragma unroll
-      for (int y = 0; y < NC; ++y) w[y] = make_uint4(0, 0, 0, 0);
-      if (r_item < it.nrows) {
-        const int rr = it.row0 + r_item, tok = g.by_R(rr);
-        const uint16_t* from = q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-#pragma unroll
-        for (int y = 0; y < NC; ++y) {
-          const int e = (l4 + 4 * (y ^ flip)) * 8;
-          if (e < g.d) w[y] = __ldg(reinterpret_cast<const uint4*>(from + e));
-        }
-      }
-      while (x < t >> 4) next_stream();
-      if ((x ? it.n1 : it.n0) == 0) continue;
-      uint32_t top = 0;
-#pragma unroll
-      for (int y = 0; y < NC; ++y) {
-        top = max_u16x2(top, max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu));
-        top = max_u16x2(top, max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
-      }
-      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      float inverse;
-      const float up = query_factor(max(top & 0xffffu, top >> 16) << 16, &inverse);
-      const uint64_t up2 = pk(up, up);
-      auto half = [&](uint32_t v) {
-        const float2 f = unpk(mul2(pk_u(v << 16, v & 0xffff0000u), up2));
-        return f16x2(f.x, f.y);
-      };
-#pragma unroll
-      for (int y = 0; y < NC; ++y) {
-        const int chunk = l4 + 4 * (y ^ flip);
-        const uint32_t at = smem_u32(q_smem) + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-        const uint4 h = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
-        st_shared16(at + x * kTileBytes, h);
-        if (twice) st_shared16(at + kTileBytes, h);
-      }
-      if (l4 == 0) {
-        float* to = q_factor + (k % kSlots) * 2 * kRows + row;
-        to[x * kRows] = inverse * p.score_log2;
-        if (twice) to[kRows] = inverse * p.score_log2;
-      }
-    }
-    while (x < (it.alt ? 1 : 2)) next_stream();
-  };
 
   if (warp >= 8 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -728,6 +664,8 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         i = pass_few(__shfl_sync(0xffffffffu, next, 0));
         publish(++k, i);
       }
+      // to the end of the last item (the others' slots were empty when theirs were filled again)
+      for (int x = max(k - kSlots + 1, 0); x < k; ++x) wait_on(&bars->slot_empty[x % kSlots], (x / kSlots) & 1, bars);
     } else if (warp < 11) {
       // ---------------------------------------------------------- products
       // The whole warp walks, one lane issues; see attention.cu.
@@ -740,7 +678,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       const uint32_t tS = tmem + s * kKeyTile, tO = tmem + kColO + s * kRows;
       uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;
       Ring base, turn;      // the item's first ring stage; the stream's next turn
-      for (int k = 0; slot_wait(bars, k); ++k) {
+      for (int k = 0; slot_ready(bars, k); ++k) {
         const WorkItem it = uniform_item(bars, k);
         slot_done(bars, k);
         const int n = s ? it.n1 : it.n0, tiles = item_tiles(it);
@@ -755,9 +693,9 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         const int stride = it.alt ? 4 : 2;                // ring steps from tile to tile of the stream
         const int ti_step = it.alt ? 2 : 1, limit = stream_limit(it, g, s);
         int ti = tile_of(it, s, 0), keys = stream_keys(it, g, ti, limit);
-        wait_on(&bars->q_full[s], q_ph, bars);
+        await(&bars->q_full[s], q_ph, bars);
         q_ph ^= 1u;
-        wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+        await(&bars->kv_ready[s][tk.s], tk.ph, bars);
         tc_fence_after();
 #pragma unroll 1
         for (int from = 0; from < kKeyTile; from += kHalfKeys) {
@@ -769,23 +707,23 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           }
           __syncwarp();
         }
-        wait_on(&bars->o_empty[s], oe_ph ^ 1u, bars);
+        await(&bars->o_empty[s], oe_ph ^ 1u, bars);
         oe_ph ^= 1u;
 #pragma unroll 1
         for (int left = n; left > 0; --left) {
           const bool more = left > 1;
           ti += ti_step;
           const int next_keys = more ? stream_keys(it, g, ti, limit) : 0;
-          wait_on(&bars->kv_ready[s][tv.s], tv.ph, bars);
+          await(&bars->kv_ready[s][tv.s], tv.ph, bars);
           tv.skip(2, kStages);
           rk.skip(stride, kStages);
           tk.skip(2, kStages);
-          if (more) wait_on(&bars->kv_ready[s][tk.s], tk.ph, bars);
+          if (more) await(&bars->kv_ready[s][tk.s], tk.ph, bars);
           const uint64_t dv = dv0 + rv.s * tile_step, dk = dk0 + rk.s * tile_step;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int from = h * kHalfKeys;
-            wait_on(&bars->p_full[s][h], p_ph, bars);
+            await(&bars->p_full[s][h], p_ph, bars);
             tc_fence_after();
             if (elect_one()) {
               issue_values((keys - from + 15) >> 4, tO, tS + from, dv + (from * 128 >> 4), id_pv, h > 0 || left < n);
@@ -821,7 +759,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       const int per_page = g.tile_pages ? g.page_size : g.key_tile;
       uint32_t ph = 0, copied = 0;
       const uint32_t to = smem_u32(raw_smem) + (scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC : box * per_page * 16 * NC);
-      for (int k = 0; slot_wait(bars, k); ++k) {
+      for (int k = 0; slot_ready(bars, k); ++k) {
         const WorkItem& it = bars->slot[k % kSlots];
         const int n = item_tiles(it);
         int page = 0, token = 0, keys = 0;
@@ -852,7 +790,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           if (u + 1 < n) locate(u + 1);
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
-            wait_on(&bars->raw_empty[value], ph ^ 1u, bars);
+            await(&bars->raw_empty[value], ph ^ 1u, bars);
             if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[value], total);
             __syncwarp();
             if (bytes) copy_bulk(to + value * kRawBytes, (value ? p.pool.v : p.pool.k) + from, bytes, &bars->raw_full[value]);
@@ -880,7 +818,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     const uint32_t tS = tmem + lane_base + s * kKeyTile;
     const uint32_t tO = tmem + lane_base + kColO + s * kRows;
     uint32_t s_ph = 0, st_ph = 0;
-    for (int k = 0; slot_wait(bars, k); ++k) {
+    for (int k = 0; slot_ready(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       const int n = s ? it.n1 : it.n0;
       const int r_item = row + (it.alt ? 0 : s * kRows);
@@ -903,7 +841,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           const int vis = vis_tile - h * kHalfKeys;
           const bool masked = __any_sync(0xffffffffu, vis < kHalfKeys);
           const uint32_t tB = tS + h * kHalfKeys;
-          wait_on(&bars->s_full[s][h], s_ph, bars);
+          await(&bars->s_full[s][h], s_ph, bars);
           if (j == 0 && h == 0) sc = q_factor[((k % kSlots) * 2 + s) * kRows + row];      // there before the queries were
           if (warp_live && h * kHalfKeys < used_keys) {
             tc_fence_after();
@@ -929,7 +867,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
               if (__any_sync(0xffffffffu, grow)) {
                 // O is this warp's once the latest product is done (those before it are: these scores were
                 // issued after them)
-                wait_on(&bars->pv_done[s][h ^ 1], h ? s_ph : s_ph ^ 1u, bars);
+                await(&bars->pv_done[s][h ^ 1], h ? s_ph : s_ph ^ 1u, bars);
                 tc_fence_after();
                 const float f = grow ? ex2(m - m_new) : 1.f;
                 if (grow) m = m_new;
@@ -970,7 +908,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       }
       if (n > 0) {
         // (m, l) to the output warps, once they have taken the item's before
-        wait_on(&bars->stat_empty[s], st_ph ^ 1u, bars);
+        await(&bars->stat_empty[s], st_ph ^ 1u, bars);
         st_ph ^= 1u;
         stats[s * kRows + row] = make_float2(m, l);
         __syncwarp();
@@ -985,10 +923,8 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // 16 bytes of row `row` of a warp's 32 rows of 64 bytes, in place c of 4: eight rows' stores meet in no bank
     auto staged = [&](int row, int c) { return smem_u32(out_smem) + (warp & 3) * 2048 + row * 64 + ((c ^ (row >> 1 & 3)) << 4); };
-    uint32_t ph = 0, q_ph = 0;                       // bit s: stream s
-    if (slot_wait(bars, 0)) queries(0, warp - 12, q_ph);
-    for (int k = 0; slot_wait(bars, k); ++k) {
-      if (slot_wait(bars, k + 1)) queries(k + 1, warp - 12, q_ph);
+    uint32_t ph = 0;                                 // bit s: stream s
+    for (int k = 0; slot_ready(bars, k); ++k) {
       const WorkItem it = load_item(&bars->slot[k % kSlots]);
       const bool merging = it.alt && it.n1 > 0;      // both streams hold parts of the same rows
 #pragma unroll 1
@@ -1001,11 +937,11 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         const int tok = g.by_R(rr);
         float m = -INFINITY, l = 0.f, f0 = 1.f, f1 = 0.f;
         auto take = [&](int x) {                     // stream x's (m, l); its O is complete then
-          wait_on(&bars->stat_full[x], (ph >> x) & 1u, bars);
+          await(&bars->stat_full[x], (ph >> x) & 1u, bars);
           const float2 v = stats[x * kRows + row];
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->stat_empty[x]);
-          wait_on(&bars->o_full[x], (ph >> x) & 1u, bars);
+          await(&bars->o_full[x], (ph >> x) & 1u, bars);
           ph ^= 1u << x;
           return v;
         };
@@ -1130,14 +1066,115 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     r.s = value;
     int turn0 = value, turn1 = value;                // of the streams' own tiles
     const uint32_t at = raw + (4 * j * NC + c) * 16, sat = raw + kKeyTile * 16 * NC + (2 * j * NC + 2 * c) * 4;
+    // An item's queries, a row tile a stream (the same one, where both hold the same rows), by these eight warps: 4 rows (8) at a
+    // time, 8 lanes (4) to a row, the next rows on their way meanwhile.
+    auto queries = [&](int k, int w8, uint32_t& q_ph) {
+      constexpr int kLanes = NC > 2 ? 8 : 4, kPer = 32 / kLanes, kChunks = (4 * NC + kLanes - 1) / kLanes, kTasks = kRows / kPer;
+      const WorkItem& it = bars->slot[k % kSlots];
+      const int alt = it.alt, n0 = it.n0, n1 = it.n1;
+      if (n0 + n1 == 0) return;
+      const int lc = lane % kLanes, sub = lane / kLanes, streams = alt ? 1 : 2;
+      const bool twice = alt && n1 > 0;
+      auto fetch = [&](int t, uint4 (&w)[kChunks]) {
+        const int r_item = t * kPer + sub;
+  #pragma unroll
+        for (int y = 0; y < kChunks; ++y) w[y] = make_uint4(0, 0, 0, 0);
+        if (r_item < it.nrows) {
+          const int rr = it.row0 + r_item, tok = g.by_R(rr);
+          const uint16_t* from = static_cast<const uint16_t*>(p.q) + (int64_t)tok * p.q_stride +
+                                 (it.group * g.R + rr - tok * g.R) * g.d;
+  #pragma unroll
+          for (int y = 0; y < kChunks; ++y)
+            if ((lc + y * kLanes) * 8 < g.d) w[y] = load_once(from + (lc + y * kLanes) * 8);
+        }
+      };
+      int x = -1;                                      // the stream whose queries are under way
+      auto next_stream = [&]() {                       // hands over stream x, waits for the next one's tile to be free
+        if (x >= 0) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if ((x ? n1 : n0) > 0) mbar_arrive(&bars->q_full[x]);
+            if (twice) mbar_arrive(&bars->q_full[1]);
+          }
+        }
+        ++x;
+        if (x < streams) {
+          if ((x ? n1 : n0) > 0) {
+            await(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+            q_ph ^= 1u << x;
+          }
+          if (twice) {
+            await(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
+            q_ph ^= 2u;
+          }
+        }
+      };
+      uint4 w[kChunks];
+      fetch(w8, w);
+  #pragma unroll 1
+      for (int t = w8; t < kTasks * streams; t += 8) {
+        uint4 ahead[kChunks];
+        fetch(t + 8 < kTasks * streams ? t + 8 : 2 * kTasks, ahead);      // (past the last: nothing)
+        while (x < t / kTasks) next_stream();
+        if ((x ? n1 : n0) > 0) {
+          uint32_t top2 = 0;
+  #pragma unroll
+          for (int y = 0; y < kChunks; ++y) {
+            top2 = max_u16x2(top2, max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu));
+            top2 = max_u16x2(top2, max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
+          }
+  #pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top2 = max_u16x2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
+          const uint32_t top = max(top2 & 0xffffu, top2 >> 16), e = top >> 7;
+          float inverse;
+          const float up = query_factor(top << 16, &inverse);
+          const int row = (t % kTasks) * kPer + sub;
+          uint8_t* const to = q_smem + x * kTileBytes + row * 128;
+          // bf16 to fp16 by its bits, the largest element's exponent e becoming 28; out of fp16's normal range below (2^27
+          // under the largest): 0 or some subnormal number
+          const bool plain = top == 0 || (e > 28 && e < 255);
+          const uint32_t less = top == 0 ? 0 : (e - 28) << 7, less2 = less | less << 16;
+          auto bits = [&](uint32_t v) {
+            return (max_u16x2(v & 0x7fff7fffu, less2) - less2) << 3 | (v & 0x80008000u);
+          };
+          auto scaled = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
+          const bool all_plain = __all_sync(0xffffffffu, plain);
+  #pragma unroll
+          for (int y = 0; y < kChunks; ++y) {
+            const int chunk = lc + y * kLanes;
+            if (chunk >= 4 * NC) continue;
+            const uint4 h = all_plain ? make_uint4(bits(w[y].x), bits(w[y].y), bits(w[y].z), bits(w[y].w))
+                                      : make_uint4(scaled(w[y].x), scaled(w[y].y), scaled(w[y].z), scaled(w[y].w));
+            uint8_t* const at = to + (chunk >> 3) * kHalfBytes + (((chunk & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = h;
+            if (twice) *reinterpret_cast<uint4*>(at + kTileBytes) = h;
+          }
+          if (lc == 0) {
+            float* const f = q_factor + (k % kSlots) * 2 * kRows + row;
+            f[x * kRows] = inverse * p.score_log2;
+            if (twice) f[kRows] = inverse * p.score_log2;
+          }
+        }
+  #pragma unroll
+        for (int y = 0; y < kChunks; ++y) w[y] = ahead[y];
+      }
+      while (x < streams) next_stream();
+    };
+    // The next item's queries come behind its first keys and before its first values.
     uint32_t ph = 0, q_ph = 0;
-    for (int k = 0; slot_wait(bars, k); ++k) {
+    for (int k = 0; slot_ready(bars, k); ++k) {
       const WorkItem& it = bars->slot[k % kSlots];
       const int n = item_tiles(it), alt = it.alt;
 #pragma unroll 1
-      for (int u = 0; u < n && !gave_up(bars); ++u) {
-        if (value && u == 0) queries(k, 8 + cw, q_ph);
-        wait_on(&bars->raw_full[value], ph, bars);
+      for (int step = 0; step < (n ? n + 1 : 0) && !gave_up(bars); ++step) {
+        const int before = value ? 0 : 1;
+        if (step == before) {
+          queries(k, warp - 16, q_ph);
+          continue;
+        }
+        const int u = step - (step > before);
+        await(&bars->raw_full[value], ph, bars);
         ph ^= 1u;
         uint2 s = make_uint2(0, 0);
         if (busy) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "r"(sat) : "memory");
@@ -1170,7 +1207,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           }
         }
         // ---- to fp16
-        wait_on(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
+        await(&bars->kv_empty[r.s], r.ph ^ 1u, bars);
         if (busy) {
           const uint32_t to = to0 + r.s * kTileBytes;
 #pragma unroll
@@ -1201,8 +1238,6 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         if (use0) turn0 = turn0 + 2 >= kStages ? value : turn0 + 2;
         if (use1) turn1 = turn1 + 2 >= kStages ? value : turn1 + 2;
         r.skip(2, kStages);
-        // the next item's queries come behind its first keys and before its first values
-        if (!value && u == 0) queries(k, 4 + cw, q_ph);
       }
       slot_done(bars, k);
     }
