@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 // against a run of 128-key tiles; CTAs claim them from a counter.  Two streams of 128 rows alternate on the tensor
 // core, each with two score buffers of half a tile.
 //   warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row
-//   warp 8           claims items, and asks for an item's queries an item ahead (into L2)
+//   warp 8           claims items, and looks at the clock
 //   warps 9, 10      issue the products of stream 0 / 1:  S = Q K^T (both from shared memory) and O += P V (P from
 //                    tensor memory)
 //   warp 11          copies tiles as they lie in the cache, keys and values into a buffer each, through the page tables
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_co
 // registers is the one whose tile walks spill nothing.)
 constexpr int kTileThreads = 768;
 // Registers of the warpgroups: 80 for each of 768 threads at the launch.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 72, kOutRegs = 72, kConvertRegs = 56;
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 64, kConvertRegs = 64;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kOutRegs + 2 * kConvertRegs <= 6 * kLaunchRegs, "what the launch owns");
 
 // Ring stages that fit beside the query tiles, the copies and the staging.
@@ -647,18 +647,6 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       int i = pass_few(blockIdx.x), k = 0;
       publish(0, i);
       while (i < end && !gave_up(bars)) {
-        {
-          const WorkItem it = load_item(g.items + i);
-          const uint16_t* q = static_cast<const uint16_t*>(p.q);
-#pragma unroll 1
-          for (int r = lane; r < (it.n0 + it.n1 > 0 ? it.nrows : 0); r += 32) {
-            const int rr = it.row0 + r, tok = g.by_R(rr);
-            const uint16_t* at = q + (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-            if (kHalves == 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
-          }
-          __syncwarp();
-        }
         int next = 0;
         if (lane == 0) next = gridDim.x + (int)atomicAdd(&g.head->claimed, 1u);
         i = pass_few(__shfl_sync(0xffffffffu, next, 0));
@@ -692,57 +680,56 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         turn.advance(2 * n, kStages);
         const int stride = it.alt ? 4 : 2;                // ring steps from tile to tile of the stream
         const int ti_step = it.alt ? 2 : 1, limit = stream_limit(it, g, s);
-        int ti = tile_of(it, s, 0), keys = stream_keys(it, g, ti, limit);
+        int ti = tile_of(it, s, 0), keys = 0, next_keys = stream_keys(it, g, ti, limit);
         await(&bars->q_full[s], q_ph, bars);
         q_ph ^= 1u;
-        await(&bars->kv_ready[s][tk.s], tk.ph, bars);
-        tc_fence_after();
+        // Scores run a tile ahead of the values' products, in half tiles (step 0: scores alone); one copy of the loop's
+        // body, and no unrolling, for the instruction cache's sake.
 #pragma unroll 1
-        for (int from = 0; from < kKeyTile; from += kHalfKeys) {
-          if (elect_one()) {
-            if (keys > from) issue_scores<kSlices>(0, tS + from, dq, dk0 + rk.s * tile_step + (from * 128 >> 4), id_qk);
-            mma_commit(&bars->s_full[s][from / kHalfKeys]);
-            if (from) mma_commit(&bars->kv_empty[rk.s]);
-            if (from && n == 1) mma_commit(&bars->q_empty[s]);
-          }
-          __syncwarp();
-        }
-        await(&bars->o_empty[s], oe_ph ^ 1u, bars);
-        oe_ph ^= 1u;
-#pragma unroll 1
-        for (int left = n; left > 0; --left) {
-          const bool more = left > 1;
-          ti += ti_step;
-          const int next_keys = more ? stream_keys(it, g, ti, limit) : 0;
-          await(&bars->kv_ready[s][tv.s], tv.ph, bars);
-          tv.skip(2, kStages);
-          rk.skip(stride, kStages);
-          tk.skip(2, kStages);
+        for (int step = 0; step <= n; ++step) {
+          const bool more = step < n;
+          if (step) await(&bars->kv_ready[s][tv.s], tv.ph, bars);
           if (more) await(&bars->kv_ready[s][tk.s], tk.ph, bars);
+          if (step == 1) {
+            await(&bars->o_empty[s], oe_ph ^ 1u, bars);
+            oe_ph ^= 1u;
+          }
+          tc_fence_after();
           const uint64_t dv = dv0 + rv.s * tile_step, dk = dk0 + rk.s * tile_step;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int from = h * kHalfKeys;
-            await(&bars->p_full[s][h], p_ph, bars);
-            tc_fence_after();
+            if (step) {
+              await(&bars->p_full[s][h], p_ph, bars);
+              tc_fence_after();
+            }
             if (elect_one()) {
-              issue_values((keys - from + 15) >> 4, tO, tS + from, dv + (from * 128 >> 4), id_pv, h > 0 || left < n);
-              mma_commit(&bars->pv_done[s][h]);
-              if (h == 1) mma_commit(&bars->kv_empty[rv.s]);
+              if (step) {
+                issue_values((keys - from + 15) >> 4, tO, tS + from, dv + (from * 128 >> 4), id_pv, h > 0 || step > 1);
+                mma_commit(&bars->pv_done[s][h]);
+                if (h == 1) mma_commit(&bars->kv_empty[rv.s]);
+              }
               if (more) {
                 if (next_keys > from) issue_scores<kSlices>(0, tS + from, dq, dk + (from * 128 >> 4), id_qk);
                 mma_commit(&bars->s_full[s][h]);
                 if (h == 1) mma_commit(&bars->kv_empty[rk.s]);
-                if (h == 1 && left == 2) mma_commit(&bars->q_empty[s]);      // the item's last scores
+                if (h == 1 && step == n - 1) mma_commit(&bars->q_empty[s]);      // the item's last scores
               } else if (h == 1) {
                 mma_commit(&bars->o_full[s]);
               }
             }
             __syncwarp();
           }
-          p_ph ^= 1u;
-          rv.skip(stride, kStages);
+          if (step) {
+            p_ph ^= 1u;
+            rv.skip(stride, kStages);
+            tv.skip(2, kStages);
+          }
+          rk.skip(stride, kStages);
+          tk.skip(2, kStages);
           keys = next_keys;
+          ti += ti_step;
+          next_keys = step + 1 < n ? stream_keys(it, g, ti, limit) : 0;
         }
       }
       if (elect_one()) {
@@ -762,32 +749,26 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       for (int k = 0; slot_ready(bars, k); ++k) {
         const WorkItem& it = bars->slot[k % kSlots];
         const int n = item_tiles(it);
-        int page = 0, token = 0, keys = 0;
-        auto locate = [&](int u) {           // asks for the page of this lane's share of a tile
-          const bool pre = it.t0 + u < it.np;
-          int key0;
-          keys = tile_keys(it, g, it.t0 + u, &key0);
-          key0 += box * per_page;
-          if (box * per_page < keys) {
-            const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-            const int pi = g.by_page(key0);
-            page = __ldg(table + pi);
-            token = key0 - pi * g.page_size;
-          }
-        };
-        if (n > 0) locate(0);
 #pragma unroll 1
         for (int u = 0; u < n && !gave_up(bars); ++u) {
-          const uint32_t total = ((keys + 7) & ~7) * 18 * NC;
-          const int mine = min(per_page, keys - box * per_page);
-          const uint32_t bytes = mine > 0 ? ((mine + 7) & ~7) * (scales ? 2 * NC : 16 * NC) : 0;
-          if (bytes && (page < 0 || page >= g.n_pages)) {      // reported; what is copied instead does not matter
-            latch_status(status, kStatusRange);
-            page = 0;
+          const bool pre = it.t0 + u < it.np;
+          int key0;
+          const int keys = tile_keys(it, g, it.t0 + u, &key0), mine = min(per_page, keys - box * per_page);
+          uint32_t bytes = 0;
+          int64_t from = 0;
+          if (mine > 0) {
+            const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+            const int key = key0 + box * per_page, pi = g.by_page(key), token = key - pi * g.page_size;
+            int page = __ldg(table + pi);
+            if (page < 0 || page >= g.n_pages) {               // reported; what is copied instead does not matter
+              latch_status(status, kStatusRange);
+              page = 0;
+            }
+            bytes = ((mine + 7) & ~7) * (scales ? 2 * NC : 16 * NC);
+            from = page * p.pool.page_stride + it.group * p.pool.group_stride +
+                   (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
           }
-          const int64_t from = page * p.pool.page_stride + it.group * p.pool.group_stride +
-                               (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
-          if (u + 1 < n) locate(u + 1);
+          const uint32_t total = ((keys + 7) & ~7) * 18 * NC;
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
             await(&bars->raw_empty[value], ph ^ 1u, bars);
@@ -842,7 +823,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           const bool masked = __any_sync(0xffffffffu, vis < kHalfKeys);
           const uint32_t tB = tS + h * kHalfKeys;
           await(&bars->s_full[s][h], s_ph, bars);
-          if (j == 0 && h == 0) sc = q_factor[((k % kSlots) * 2 + s) * kRows + row];      // there before the queries were
+          if (j == 0 && h == 0) sc = blind ? 1.f : q_factor[((k % kSlots) * 2 + s) * kRows + row];    // there before the queries
           if (warp_live && h * kHalfKeys < used_keys) {
             tc_fence_after();
             uint32_t v[kHalfKeys];
@@ -1126,26 +1107,19 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           }
   #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top2 = max_u16x2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
-          const uint32_t top = max(top2 & 0xffffu, top2 >> 16), e = top >> 7;
-          float inverse;
-          const float up = query_factor(top << 16, &inverse);
+          // bf16 to fp16 by its bits: `less` from the exponent, so that the largest element's is 28 at most; what falls out
+          // of fp16's range below (2^27 under the largest) becomes 0 or some subnormal number.  A row with an infinity or
+          // a NaN has no scores.
+          const uint32_t e = max(max(top2 & 0xffffu, top2 >> 16) >> 7, 28u), less2 = (e - 28) * 0x00800080u;
+          const float inverse = e == 255 ? __int_as_float(0x7fc00000) : __uint_as_float((e - 13) << 23);
+          auto bits = [&](uint32_t v) { return (max_u16x2(v & 0x7fff7fffu, less2) - less2) << 3 | (v & 0x80008000u); };
           const int row = (t % kTasks) * kPer + sub;
           uint8_t* const to = q_smem + x * kTileBytes + row * 128;
-          // bf16 to fp16 by its bits, the largest element's exponent e becoming 28; out of fp16's normal range below (2^27
-          // under the largest): 0 or some subnormal number
-          const bool plain = top == 0 || (e > 28 && e < 255);
-          const uint32_t less = top == 0 ? 0 : (e - 28) << 7, less2 = less | less << 16;
-          auto bits = [&](uint32_t v) {
-            return (max_u16x2(v & 0x7fff7fffu, less2) - less2) << 3 | (v & 0x80008000u);
-          };
-          auto scaled = [&](uint32_t v) { return f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-          const bool all_plain = __all_sync(0xffffffffu, plain);
-  #pragma unroll
+#pragma unroll
           for (int y = 0; y < kChunks; ++y) {
             const int chunk = lc + y * kLanes;
             if (chunk >= 4 * NC) continue;
-            const uint4 h = all_plain ? make_uint4(bits(w[y].x), bits(w[y].y), bits(w[y].z), bits(w[y].w))
-                                      : make_uint4(scaled(w[y].x), scaled(w[y].y), scaled(w[y].z), scaled(w[y].w));
+            const uint4 h = make_uint4(bits(w[y].x), bits(w[y].y), bits(w[y].z), bits(w[y].w));
             uint8_t* const at = to + (chunk >> 3) * kHalfBytes + (((chunk & 7) ^ (row & 7)) << 4);
             *reinterpret_cast<uint4*>(at) = h;
             if (twice) *reinterpret_cast<uint4*>(at + kTileBytes) = h;
@@ -1156,12 +1130,12 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
             if (twice) f[kRows] = inverse * p.score_log2;
           }
         }
-  #pragma unroll
+#pragma unroll
         for (int y = 0; y < kChunks; ++y) w[y] = ahead[y];
       }
       while (x < streams) next_stream();
     };
-    // The next item's queries come behind its first keys and before its first values.
+    // An item's queries come behind its first keys and before its first values.
     uint32_t ph = 0, q_ph = 0;
     for (int k = 0; slot_ready(bars, k); ++k) {
       const WorkItem& it = bars->slot[k % kSlots];
