@@ -47,6 +47,21 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float2 halves(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+__device__ __forceinline__ uint2 ld_shared8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared2(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
@@ -63,420 +78,490 @@ __device__ __forceinline__ float query_factor(uint32_t top, float* inverse) {
   return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
+// ---------------------------------------------------------------- shared by both kernels
+// A tile's keys or values as they lie in the cache: codes of up to 128 keys, then their scales.
+__host__ __device__ constexpr int raw_bytes(int chunks) { return kKeyTile * 18 * chunks; }
+
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A wait that ends with the CTA's giving up: one warp alone looks at the clock.  Every role's progress frees slots, which
+// that warp waits for (2 s at most) to its end; so the waits in the other roles stay a few instructions each.
+template <class Bars>
+__device__ __forceinline__ void await(uint64_t* bar, uint32_t parity, Bars* b) {
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity) && !gave_up(b)) {}
+  __syncwarp();
+}
+template <class Bars>
+__device__ __forceinline__ bool slot_ready(Bars* b, int k) {
+  await(&b->slot_full[k % kSlots], (k / kSlots) & 1, b);
+  return __all_sync(0xffffffffu, !gave_up(b) && b->slot[k % kSlots].row0 >= 0);
+}
+
+// A copying warp's share of a tile: a page's codes are a lane's copy, its scales another's; a page has whole groups of
+// 8 tokens.
+struct TileShare {
+  int64_t from;             // in either pool
+  uint32_t to, bytes;       // in a buffer of raw_bytes; 0 bytes: none
+  uint32_t total;           // of the tile's keys, or values
+};
+template <int NC>
+__device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const WorkItem& it, int tile, uint32_t* status) {
+  const StepGeom& g = p.g;
+  const int lane = threadIdx.x & 31, box = lane & 15;
+  const bool scales = lane >= 16, pre = tile < it.np;
+  const int per_page = g.tile_pages ? g.page_size : g.key_tile;
+  int key0;
+  const int keys = tile_keys(it, g, tile, &key0), mine = min(per_page, keys - box * per_page);
+  TileShare x{0, 0, 0, (uint32_t)((keys + 7) & ~7) * 18 * NC};
+  if (mine > 0) {
+    const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+    const int key = key0 + box * per_page, pi = g.by_page(key), token = key - pi * g.page_size;
+    int page = __ldg(table + pi);
+    if (page < 0 || page >= g.n_pages) {               // reported; what is copied instead does not matter
+      latch_status(status, kStatusRange);
+      page = 0;
+    }
+    x.bytes = ((mine + 7) & ~7) * (scales ? 2 * NC : 16 * NC);
+    x.from = page * p.pool.page_stride + it.group * p.pool.group_stride +
+             (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
+    x.to = scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC : box * per_page * 16 * NC;
+  }
+  return x;
+}
+
 // ---------------------------------------------------------------- few rows
-// Items of at most 8 rows, bound by the bytes of the cache.  Eight warps share an item: 16 keys at a time are a warp's
-// unit, straight from global memory to the registers of the products that read them, and nothing is exchanged before
-// the item's end.  Products are transposed, keys as the long side:  S^T = K Q^T and O^T += V^T P^T.
+// Items of at most 8 rows, bound by the bytes of the cache.  Warp 8 claims items and copies their tiles as they lie into
+// a ring, running ahead over the items' ends; two CTAs of an SM have 147 KB on their way.  Eight warps share a tile by
+// its keys, 16 each, and nothing is exchanged before the item's end.  Products are transposed, keys as the long side:
+// S^T = K Q^T and O^T += V^T P^T, their operands made in registers from the copies.
 //   K  lane (key quad, c) holds its key's elements 8 W c .. + 8 W - 1 as they lie in memory (W words of codes); the
 //      contraction does not care which elements are a slice's, so the queries are dealt the same way.
 //   V  lane (quad, c) holds elements 4 W quad .. of keys 4 c .. 4 c + 3; a byte of two keys' codes for the same
 //      element makes the pair that V^T wants, two shifts and two selections for 16 elements.
 // Rows of S^T are dealt to keys so that a lane's four probabilities' keys are those it holds the values of.
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 288;
 constexpr int kFewPitch = 132;               // floats of a staged row
+constexpr int kFewStages = 4;
 
-template <int NC>
-struct FewShape {
-  static constexpr int W = NC >= 3 ? 4 : NC;           // words of codes a lane holds of a key
-  static constexpr int VW = W == 4 ? 2 : 1;            // of a value (W == 1: half a word)
+struct alignas(16) FewBars {
+  uint64_t full[kFewStages], empty[kFewStages], slot_full[kSlots], slot_empty[kSlots];
+  alignas(16) WorkItem slot[kSlots];         // row0 < 0: no more
+  int nan_key[kSlots][8];                    // the first key, not seen by every row, whose values of a block are NaN
+  float2 ml[8 * 8];                          // [warp][row]: (m, l)
+  int abort_flag;
 };
-
-template <int NC>
-struct FewRaw {                              // a unit as it lies in memory
-  static constexpr int W = FewShape<NC>::W, VW = FewShape<NC>::VW;
-  uint32_t k[2][W], ks[W == 4 ? 2 : 1], v[4][VW], vs;
-};
-
-struct FewUnit {
-  int tile, sub;                             // of the walk
-  int key0, keys;                            // first key within the segment, keys (at most 16); 0: past the end
-  bool pre;
-  int page, in_page;                         // of the four keys that this lane holds the values of; page -1: none
-};
+constexpr int few_smem(int chunks) { return kFewStages * 2 * raw_bytes(chunks) + 8 * 8 * kFewPitch * 4 + (int)sizeof(FewBars); }
+static_assert(2 * (few_smem(4) + 1024) <= 228 * 1024, "two CTAs of an SM");
 
 template <int NC, bool F32>
-__global__ void __launch_bounds__(kFewThreads, 2) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
-  constexpr int W = FewShape<NC>::W, VW = FewShape<NC>::VW, KS = 2 * W, MT = 2 * W;
-  __shared__ __align__(16) float po[8][8][kFewPitch];
-  __shared__ float2 ml[8][8];
-  __shared__ int nan_key[2][8];              // the first key, not seen by every row, whose values of a block are NaN
-  __shared__ int claim;
-  pdl_enter();
+__global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
+  // W: words of codes that a lane holds of a key (of a value: half as many)
+  constexpr int W = NC >= 3 ? 4 : NC, VW = W == 4 ? 2 : 1, KS = 2 * W, MT = 2 * W;
+  constexpr int kRaw = raw_bytes(NC);
+  extern __shared__ __align__(16) uint8_t few_raw[];       // ring: keys and values of a tile
+  float* const po = reinterpret_cast<float*>(few_raw + kFewStages * 2 * kRaw);      // [warp][row][kFewPitch]
+  FewBars* const bars = reinterpret_cast<FewBars*>(po + 8 * 8 * kFewPitch);
+  float2* const ml = bars->ml;
   const StepGeom& g = p.g;
+  uint32_t* status = &g.head->status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 8);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bars->slot_full[i], 1);
+      mbar_init(&bars->slot_empty[i], 8);
+    }
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_enter();
+  __syncthreads();
   const bool fits = plan_matches(g);
-  const int n_items = fits ? g.head->n_items : 0, first_item = fits ? g.head->few_begin : 0;
-  if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(&g.head->status, fits ? kStatusRange : kStatusInvalid);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, c = lane & 3;
-  const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of a unit: k_off, k_off + 2
-  const bool k0_has = 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of this lane's key elements
-  const bool v_has = 4 * W * quad < g.d;
-  const int v_block = 4 * W * quad / 16;
-  const int subs = (g.key_tile + 15) / 16;
-  if (threadIdx.x < 8) nan_key[0][threadIdx.x] = INT32_MAX;
-  int turn = 0;
+  const int n_items = fits ? g.head->n_items : 0, first = fits ? g.head->few_begin : 0;
+  if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
 
-  // the first item by number, the others from the counter
-  for (int i = first_item + blockIdx.x; i < n_items; i = claim, turn ^= 1) {
-    const WorkItem it = load_item(g.items + i);
-    const int n = it.n0, nrows = it.nrows, row0 = it.row0;
-    __syncthreads();                         // what lies in shared memory has been read
-    if (threadIdx.x == 0) claim = first_item + gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
-    if (threadIdx.x < 8) nan_key[turn ^ 1][threadIdx.x] = INT32_MAX;
-    if (it.alt != 2) {                       // the other kernel's
-      __syncthreads();
-      continue;
-    }
-    // ---- queries: B operand of S^T, row quad
-    uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
-    float inverse;
-    {
-      const int rr = row0 + quad, tok = g.by_R(rr);
-      const int64_t at = (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-      float x[8 * W];
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const int e0 = 8 * W * c + 8 * j;
-        const bool has = quad < nrows && e0 < g.d;
-        if constexpr (F32) {
-          const float* src = static_cast<const float*>(p.q) + at + e0;
-          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 a = has ? __ldg(reinterpret_cast<const float4*>(src)) : z;
-          const float4 b = has ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
-          x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
-          x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
-        } else {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (has) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e0));
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
-            x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-          }
+  if (warp == 8) {
+    // ------------------------------------------------------------ items and copies
+    Ring r;
+    int copied = 0;
+    auto claim = [&]() {
+      int next = 0;
+      if (lane == 0) next = first + gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
+      return next;                           // of lane 0
+    };
+    auto pass_tiles = [&](int i) {           // past the other kernel's items
+      while (i < n_items && g.items[i].alt != 2) i = __shfl_sync(0xffffffffu, claim(), 0);
+      return i;
+    };
+    int i = pass_tiles(first + blockIdx.x), k = 0;
+    for (;; ++k) {
+      wait_on(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars);
+      int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
+      if (lane < (int)(sizeof(WorkItem) / 4)) d[lane] = i < n_items ? reinterpret_cast<const int*>(g.items + i)[lane] : -1;
+      if (lane < 8) bars->nan_key[k % kSlots][lane] = INT32_MAX;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
+      if (i >= n_items || gave_up(bars)) break;
+      const int next = claim();              // comes back behind the copies
+      const WorkItem it = load_item(g.items + i);
+      TileShare x{};
+      if (it.n0 > 0) x = tile_share<NC>(p, it, it.t0, status);
+#pragma unroll 1
+      for (int u = 0; u < it.n0 && !gave_up(bars); ++u) {
+        TileShare ahead{};                   // the next tile's page is asked for meanwhile
+        if (u + 1 < it.n0) ahead = tile_share<NC>(p, it, it.t0 + u + 1, status);
+        wait_on(&bars->empty[r.s], r.ph ^ 1u, bars);
+        if (lane == 0) mbar_arrive_expect_tx(&bars->full[r.s], 2 * x.total);
+        __syncwarp();
+        if (x.bytes) {
+          const uint32_t to = smem_u32(few_raw) + r.s * 2 * kRaw + x.to;
+          copy_bulk(to, p.pool.k + x.from, x.bytes, &bars->full[r.s]);
+          copy_bulk(to + kRaw, p.pool.v + x.from, x.bytes, &bars->full[r.s]);
         }
+        __syncwarp();
+        r.skip(1, kFewStages);
+        copied = min(copied + 1, kFewStages);
+        x = ahead;
       }
+      i = pass_tiles(__shfl_sync(0xffffffffu, next, 0));
+    }
+    // to the end of the last items, and of the copies, where the CTA has given up
+    for (int x = max(k - kSlots + 1, 0); x < k; ++x) wait_on(&bars->slot_empty[x % kSlots], (x / kSlots) & 1, bars);
+    for (int x = 0; x < copied; ++x) {
+      const int st = (r.s + kFewStages - 1 - x) % kFewStages;
+      const uint32_t ph = st < r.s ? r.ph : r.ph ^ 1u;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_test_wait(&bars->full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ products
+    const int quad = lane >> 2, c = lane & 3;
+    const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of the warp's 16: k_off, k_off + 2
+    const bool k0_has = 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of its key elements
+    const bool v_has = 4 * W * quad < g.d;
+    const int v_block = 4 * W * quad / 16;
+    // from a tile's start: this lane's share of its keys, their scales, of its values, theirs
+    const uint32_t ring = smem_u32(few_raw);
+    const uint32_t k_at = (16 * warp + k_off) * 16 * NC + c * 4 * W;
+    const uint32_t ks_at = kKeyTile * 16 * NC + ((4 * warp + (quad >> 1)) * 2 * NC + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
+    const uint32_t v_at = kRaw + (16 * warp + 4 * c) * 16 * NC + quad * 2 * W;
+    const uint32_t vs_at = kRaw + kKeyTile * 16 * NC + ((4 * warp + c) * 2 * NC + v_block) * 4;
+    Ring ring_at;
+    for (int k = 0; slot_ready(bars, k); ++k) {
+      const WorkItem it = load_item(&bars->slot[k % kSlots]);
+      const int n = it.n0, nrows = it.nrows, row0 = it.row0;
+      // ---- queries: B operand of S^T, row quad
+      uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
+      float inverse;
+      {
+        const int rr = row0 + quad, tok = g.by_R(rr);
+        const int64_t at = (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+        float x[8 * W];
+        uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float f = query_factor(top, &inverse);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
-          qh[s][h] = f16x2(a, b);
+        for (int j = 0; j < W; ++j) {
+          const int e0 = 8 * W * c + 8 * j;
+          const bool has = quad < nrows && e0 < g.d;
           if constexpr (F32) {
-            const float2 r = halves(qh[s][h]);
-            ql[s][h] = f16x2(a - r.x, b - r.y);
-          }
-        }
-    }
-    // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
-    float sc[2], m[2], l[2], o[MT][4];
-    int own_vis[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 2 * c + e;
-      sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
-      own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
-      m[e] = -INFINITY;
-      l[e] = 0.f;
-    }
-    const int all_see = it.seq < 0 ? INT32_MAX : g.by_R(row0) + it.own_off + 1;    // own keys that every row sees
-#pragma unroll
-    for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-
-    // ---- the walk over this warp's units
-    const uint8_t* const kg = p.pool.k + it.group * p.pool.group_stride;
-    const uint8_t* const vg = p.pool.v + it.group * p.pool.group_stride;
-    const int end = it.t0 + n;
-    auto locate = [&](FewUnit& u) {        // the unit at (tile, sub) or the next one that holds a key; asks for its page
-      u.keys = 0;
-      u.page = -1;
-      while (u.tile < end) {
-        u.pre = u.tile < it.np;
-        int first;
-        const int keys = tile_span(g, u.pre ? g.prefix_len : it.own_len, u.pre ? u.tile : u.tile - it.np, &first) - 16 * u.sub;
-        u.key0 = first + 16 * u.sub;
-        u.sub += 8;
-        while (u.sub >= subs) {
-          u.sub -= subs;
-          ++u.tile;
-        }
-        if (keys > 0) {
-          u.keys = min(keys, 16);
-          break;
-        }
-      }
-      if (4 * c < u.keys) {
-        const int32_t* table = u.pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-        const int pi = g.by_page(u.key0 + 4 * c);
-        u.page = __ldg(table + pi);
-        u.in_page = u.key0 + 4 * c - pi * g.page_size;
-      }
-    };
-    auto load = [&](FewRaw<NC>& r, FewUnit& u) {
-      if (4 * c < u.keys && (u.page < 0 || u.page >= g.n_pages)) {      // read as zeros: report it
-        latch_status(&g.head->status, kStatusRange);
-        u.page = -1;
-      }
-      const int kp = __shfl_sync(0xffffffffu, u.page, quad >> 1), ki = __shfl_sync(0xffffffffu, u.in_page, quad >> 1);
-#pragma unroll
-      for (int x = 0; x < W; ++x) r.k[0][x] = r.k[1][x] = 0;
-#pragma unroll
-      for (int x = 0; x < (W == 4 ? 2 : 1); ++x) r.ks[x] = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < VW; ++y) r.v[x][y] = 0;
-      r.vs = 0;
-      if (kp >= 0 && k0_has) {
-        const uint8_t* page = kg + kp * p.pool.page_stride;
-        const uint8_t* at = page + (ki + (quad & 1)) * 16 * p.pool.n + c * 4 * W;
-        const uint8_t* s = page + p.pool.scales + ((ki >> 2) * 2 * p.pool.n + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
-#pragma unroll
-        for (int x = 0; x < 2; ++x, at += 32 * p.pool.n) {
-          if constexpr (W == 4) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
-            r.k[x][0] = w.x; r.k[x][1] = w.y; r.k[x][2] = w.z; r.k[x][3] = w.w;
-          } else if constexpr (W == 2) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
-            r.k[x][0] = w.x; r.k[x][1] = w.y;
+            const float* src = static_cast<const float*>(p.q) + at + e0;
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 a = has ? __ldg(reinterpret_cast<const float4*>(src)) : z;
+            const float4 b = has ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
+            x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
+            x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
           } else {
-            r.k[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (has) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e0));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
+              x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
+            }
           }
         }
-        if constexpr (W == 4) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(s));
-          r.ks[0] = w.x;
-          r.ks[1] = k1_has ? w.y : 0;
-        } else {
-          r.ks[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-        }
-      }
-      if (u.page >= 0 && v_has) {
-        const uint8_t* page = vg + u.page * p.pool.page_stride;
-        const uint8_t* at = page + u.in_page * 16 * p.pool.n + quad * 2 * W;
 #pragma unroll
-        for (int x = 0; x < 4; ++x, at += 16 * p.pool.n) {
-          if constexpr (W == 4) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
-            r.v[x][0] = w.x; r.v[x][1] = w.y;
-          } else if constexpr (W == 2) {
-            r.v[x][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-          } else {
-            r.v[x][0] = __ldg(reinterpret_cast<const uint16_t*>(at));
+        for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float f = query_factor(top, &inverse);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
+            qh[s][h] = f16x2(a, b);
+            if constexpr (F32) {
+              const float2 r = halves(qh[s][h]);
+              ql[s][h] = f16x2(a - r.x, b - r.y);
+            }
           }
-        }
-        r.vs = __ldg(reinterpret_cast<const uint32_t*>(page + p.pool.scales + ((u.in_page >> 2) * 2 * p.pool.n + v_block) * 4));
-        const int left = u.keys - 4 * c;
-        if (left < 4) r.vs &= (1u << 8 * left) - 1;       // keys past the end: zero
       }
-    };
-    auto work = [&](const FewRaw<NC>& r, const FewUnit& u) {
-      // ---- scores
-      uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
-      if constexpr (W == 4) {
-        const uint32_t b = quad & 1;
-        const uint32_t a2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], b | (4 + b) << 4));
-        const uint32_t b2 = kv4_scale_pair(prmt(r.ks[0], r.ks[1], (b + 2) | (b + 6) << 4));
-        ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
-        kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
-      } else {
-        const uint32_t b = quad & 1;
-        const uint32_t two = kv4_scale_pair(prmt(r.ks[0], 0, b | (b + 2) << 4));
-        ka[0] = ka[1] = prmt(two, two, 0x1010);
-        kb[0] = kb[1] = prmt(two, two, 0x3232);
-      }
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t a[4], b[4];
-        kv4_decode(r.k[0][w], a);
-        kv4_decode(r.k[1][w], b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = mul_f16x2(a[e], ka[w >> 1]);
-          b[e] = mul_f16x2(b[e], kb[w >> 1]);
-        }
-        mma_16x8x16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
-        mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
-        if constexpr (F32) {
-          mma_16x8x16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
-          mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += s2[e];
-      // ---- s[e]: key k_off, row 2 c + e; s[2 + e]: key k_off + 2
-      if (!(u.keys == 16 && all_see > 0 && (u.pre || u.key0 + 16 <= all_see))) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int vis = own_vis[e] <= 0 ? 0 : u.pre ? u.keys : min(u.keys, own_vis[e] - u.key0);
-          if (k_off >= vis) s[e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
-          if (k_off + 2 >= vis) s[2 + e] = -INFINITY;
-        }
-      }
-      bool grow = false;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) grow |= fmaxf(s[e], s[2 + e]) * sc[e] - m[e] > kRescale;
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(s[e], s[2 + e]) * sc[e];
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float f = mx > m[e] ? ex2(m[e] - mx) : 1.f;
-          m[e] = fmaxf(m[e], mx);
-          l[e] *= f;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            o[t][e] *= f;
-            o[t][2 + e] *= f;
-          }
-        }
-      }
-      float x[4];
+      // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
+      float sc[2], m[2], l[2], o[MT][4];
+      int own_vis[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float neg = m[e] == -INFINITY ? kShift : kShift - m[e];
-        x[e] = ex2(fmaf(s[e], sc[e], neg));
-        x[2 + e] = ex2(fmaf(s[2 + e], sc[e], neg));
-        l[e] += x[e] + x[2 + e];
+        const int r = 2 * c + e;
+        sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
+        own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
+        m[e] = -INFINITY;
+        l[e] = 0.f;
       }
-      // keys x rows -> rows x keys, the B operand of O^T
-      const uint32_t p0 = f16x2(x[0], x[1]), p1 = f16x2(x[2], x[3]);
-      const uint32_t ph0 = transpose8(p0), ph1 = transpose8(p1);
-      uint32_t pl0 = 0, pl1 = 0;
-      if constexpr (F32) {
-        const float2 r0 = halves(p0), r1 = halves(p1);
-        pl0 = transpose8(f16x2(x[0] - r0.x, x[1] - r0.y));
-        pl1 = transpose8(f16x2(x[2] - r1.x, x[3] - r1.y));
-      }
-      // ---- values
-      uint32_t vs = r.vs;
-      const uint32_t odd = kv4_nan_scales(vs);
-      if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          const int key = u.key0 + 4 * c + x;
-          if (!u.pre && (odd >> (8 * x + 7) & 1u) && key >= all_see) {
-            vs &= ~(0xffu << 8 * x);
-            atomicMin(&nan_key[turn][v_block], key);
-          }
-        }
-      }
-      const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
+      const int seen_by_all = all_see(it, g);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
-        constexpr uint32_t lo = 0x0f0f0f0fu;
-        kv4_decode((r.v[0][j] & lo) | ((r.v[1][j] << 4) & ~lo), a0);
-        kv4_decode(((r.v[0][j] >> 4) & lo) | (r.v[1][j] & ~lo), a1);
-        kv4_decode((r.v[2][j] & lo) | ((r.v[3][j] << 4) & ~lo), a2);
-        kv4_decode(((r.v[2][j] >> 4) & lo) | (r.v[3][j] & ~lo), a3);
-#pragma unroll
-        for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
-          const int t = 4 * j + b;
-          const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
-                         w3 = mul_f16x2(a3[b], v23);
-          if constexpr (F32) {
-            // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
-            float z[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_16x8x16(z, w0, w1, w2, w3, pl0, pl1);
-            mma_16x8x16(z, w0, w1, w2, w3, ph0, ph1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] += z[e];
-          } else {
-            mma_16x8x16(o[t], w0, w1, w2, w3, ph0, ph1);
-          }
-        }
-      }
-    };
-    FewUnit ua{it.t0, warp, 0, 0, false, -1, 0}, ub;
-    while (ua.sub >= subs) {
-      ua.sub -= subs;
-      ++ua.tile;
-    }
-    FewRaw<NC> ra, rb;
-    locate(ua);
-    load(ra, ua);
-    ub = ua;
-    locate(ub);
-    while (ua.keys > 0) {
-      load(rb, ub);
-      FewUnit next = ub;
-      locate(next);
-      work(ra, ua);
-      ua = next;
-      load(ra, ua);
-      if (ub.keys > 0) {
-        next = ua;
-        locate(next);
-        work(rb, ub);
-        ub = next;
-      }
-    }
+      for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
-    // ---- the warps' parts
+#pragma unroll 1
+      for (int tile = 0; tile < n && !gave_up(bars); ++tile) {
+        const bool pre = it.t0 + tile < it.np;
+        int key0;
+        const int left = tile_keys(it, g, it.t0 + tile, &key0) - 16 * warp, unit0 = key0 + 16 * warp;    // from this warp's on
+        await(&bars->full[ring_at.s], ring_at.ph, bars);
+        if (left > 0) {
+          // ---- this lane's share
+          const uint32_t base = ring + ring_at.s * 2 * kRaw;
+          uint32_t kr[2][W], ks[2] = {0, 0}, vr[4][VW], vs = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
-      const int r = 2 * c + e;
-      if (r >= nrows) continue;
-      if (quad == 0) ml[warp][r] = make_float2(m[e], l[e]);
-      float* dst = &po[warp][r][4 * W * quad];
+            for (int y = 0; y < W; ++y) kr[x][y] = 0;
 #pragma unroll
-      for (int t = 0; t < MT; t += 2)
-        *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
-    }
-    __syncthreads();
-    const int r = warp, e0 = 4 * lane;
-    if (r < nrows) {
-      const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
-      float top = -INFINITY, sum = 0.f;
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][r].x);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < VW; ++y) vr[x][y] = 0;
+          if (k0_has) {
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float2 s = ml[w][r];
-        if (s.y == 0.f) continue;                      // nothing seen by this warp
-        const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
-        sum += f * s.y;
-        const float4 v = *reinterpret_cast<const float4*>(&po[w][r][min(e0, 4 * W * 8 - 4)]);
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t at = base + k_at + x * 32 * NC;
+              if constexpr (W == 4) {
+                const uint4 w = ld_shared16(at);
+                kr[x][0] = w.x; kr[x][1] = w.y; kr[x][2] = w.z; kr[x][3] = w.w;
+              } else if constexpr (W == 2) {
+                const uint2 w = ld_shared8(at);
+                kr[x][0] = w.x; kr[x][1] = w.y;
+              } else {
+                kr[x][0] = ld_shared4(at);
+              }
+            }
+            if constexpr (W == 4) {
+              const uint2 w = ld_shared8(base + ks_at);
+              ks[0] = w.x;
+              ks[1] = k1_has ? w.y : 0;
+            } else {
+              ks[0] = ld_shared4(base + ks_at);
+            }
+          }
+          if (v_has) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t at = base + v_at + x * 16 * NC;
+              if constexpr (W == 4) {
+                const uint2 w = ld_shared8(at);
+                vr[x][0] = w.x; vr[x][1] = w.y;
+              } else if constexpr (W == 2) {
+                vr[x][0] = ld_shared4(at);
+              } else {
+                vr[x][0] = ld_shared2(at);
+              }
+            }
+            vs = ld_shared4(base + vs_at);
+            const int mine = left - 4 * c;               // keys past the end: zero
+            if (mine < 4) vs &= (1u << 8 * max(mine, 0)) - 1;
+          }
+          // ---- scores
+          uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
+          if constexpr (W == 4) {
+            const uint32_t b = quad & 1;
+            const uint32_t a2 = kv4_scale_pair(prmt(ks[0], ks[1], b | (4 + b) << 4));
+            const uint32_t b2 = kv4_scale_pair(prmt(ks[0], ks[1], (b + 2) | (b + 6) << 4));
+            ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
+            kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
+          } else {
+            const uint32_t b = quad & 1;
+            const uint32_t two = kv4_scale_pair(prmt(ks[0], 0, b | (b + 2) << 4));
+            ka[0] = ka[1] = prmt(two, two, 0x1010);
+            kb[0] = kb[1] = prmt(two, two, 0x3232);
+          }
+          float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            uint32_t a[4], b[4];
+            kv4_decode(kr[0][w], a);
+            kv4_decode(kr[1][w], b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = mul_f16x2(a[e], ka[w >> 1]);
+              b[e] = mul_f16x2(b[e], kb[w >> 1]);
+            }
+            mma_16x8x16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
+            mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
+            if constexpr (F32) {
+              mma_16x8x16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
+              mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] += s2[e];
+          // ---- s[e]: key k_off, row 2 c + e; s[2 + e]: key k_off + 2
+          if (!(left >= 16 && seen_by_all > 0 && (pre || unit0 + 16 <= seen_by_all))) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int vis = own_vis[e] <= 0 ? 0 : pre ? left : min(left, own_vis[e] - unit0);
+              if (k_off >= vis) s[e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
+              if (k_off + 2 >= vis) s[2 + e] = -INFINITY;
+            }
+          }
+          bool grow = false;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) grow |= fmaxf(s[e], s[2 + e]) * sc[e] - m[e] > kRescale;
+          if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(s[e], s[2 + e]) * sc[e];
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float f = mx > m[e] ? ex2(m[e] - mx) : 1.f;
+              m[e] = fmaxf(m[e], mx);
+              l[e] *= f;
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                o[t][e] *= f;
+                o[t][2 + e] *= f;
+              }
+            }
+          }
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float neg = m[e] == -INFINITY ? kShift : kShift - m[e];
+            x[e] = ex2(fmaf(s[e], sc[e], neg));
+            x[2 + e] = ex2(fmaf(s[2 + e], sc[e], neg));
+            l[e] += x[e] + x[2 + e];
+          }
+          // keys x rows -> rows x keys, the B operand of O^T
+          const uint32_t p0 = f16x2(x[0], x[1]), p1 = f16x2(x[2], x[3]);
+          const uint32_t ph0 = transpose8(p0), ph1 = transpose8(p1);
+          uint32_t pl0 = 0, pl1 = 0;
+          if constexpr (F32) {
+            const float2 r0 = halves(p0), r1 = halves(p1);
+            pl0 = transpose8(f16x2(x[0] - r0.x, x[1] - r0.y));
+            pl1 = transpose8(f16x2(x[2] - r1.x, x[3] - r1.y));
+          }
+          // ---- values
+                const uint32_t odd = kv4_nan_scales(vs);
+          if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              const int key = unit0 + 4 * c + x;
+              if (!pre && (odd >> (8 * x + 7) & 1u) && key >= seen_by_all) {
+                vs &= ~(0xffu << 8 * x);
+                atomicMin(&bars->nan_key[k % kSlots][v_block], key);
+              }
+            }
+          }
+          const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
+            constexpr uint32_t lo = 0x0f0f0f0fu;
+            kv4_decode((vr[0][j] & lo) | ((vr[1][j] << 4) & ~lo), a0);
+            kv4_decode(((vr[0][j] >> 4) & lo) | (vr[1][j] & ~lo), a1);
+            kv4_decode((vr[2][j] & lo) | ((vr[3][j] << 4) & ~lo), a2);
+            kv4_decode(((vr[2][j] >> 4) & lo) | (vr[3][j] & ~lo), a3);
+#pragma unroll
+            for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
+              const int t = 4 * j + b;
+              const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
+                             w3 = mul_f16x2(a3[b], v23);
+              if constexpr (F32) {
+                // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16x8x16(z, w0, w1, w2, w3, pl0, pl1);
+                mma_16x8x16(z, w0, w1, w2, w3, ph0, ph1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][e] += z[e];
+              } else {
+                mma_16x8x16(o[t], w0, w1, w2, w3, ph0, ph1);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->empty[ring_at.s]);
+        ring_at.skip(1, kFewStages);
       }
-      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
-      if (e0 < g.d) {
-        if (nan_key[turn][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
-        if (it.part_row >= 0) {
-          *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r) * g.d + e0) = acc;
-        } else if constexpr (F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
-              make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+      asm volatile("bar.sync 1, 256;" ::: "memory");       // the item before's parts have been read
+      // ---- the warps' parts
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+        const int r = 2 * c + e;
+        if (r >= nrows) continue;
+        if (quad == 0) ml[warp * 8 + r] = make_float2(m[e], l[e]);
+        float* dst = po + (warp * 8 + r) * kFewPitch + 4 * W * quad;
+#pragma unroll
+        for (int t = 0; t < MT; t += 2)
+          *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int r = warp, e0 = 4 * lane;
+      if (r < nrows) {
+        const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w * 8 + r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float2 s = ml[w * 8 + r];
+          if (s.y == 0.f) continue;                      // nothing seen by this warp
+          const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
+          sum += f * s.y;
+          const float4 v = *reinterpret_cast<const float4*>(po + (w * 8 + r) * kFewPitch + min(e0, 32 * W - 4));
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+        if (e0 < g.d) {
+          if (bars->nan_key[k % kSlots][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
+          if (it.part_row >= 0) {
+            *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r) * g.d + e0) = acc;
+          } else if constexpr (F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
+          } else {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
+                make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+          }
+        }
+        if (lane == 0) {
+          const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
+          if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
+          else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
         }
       }
-      if (lane == 0) {
-        const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
-        if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
-        else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
-      }
+      slot_done(bars, k);
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
   if (fits && threadIdx.x == 0) {
     __threadfence();
@@ -525,17 +610,11 @@ struct alignas(16) TileBars {
   uint32_t tmem;
   int abort_flag;
 };
-constexpr int kRawBytes = kKeyTile * 4 * 18;           // a tile's keys or values as they lie in the cache
 constexpr int kTileStage = 4 * 32 * 64;                // output staging: 32 rows of 64 bytes for each output warp
-constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + 2 * kRawBytes + kTileStage + 2 * kRows * 8 + kSlots * 2 * kRows * 4 +
+constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + 2 * raw_bytes(4) + kTileStage + 2 * kRows * 8 + kSlots * 2 * kRows * 4 +
                           (int)sizeof(TileBars);
 static_assert(kTileSmem <= kSmemMax, "fits an SM");
 
-__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-               "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 // 16 bytes that are read once: they take no room in what there is of a first cache.
 __device__ __forceinline__ uint4 load_once(const void* at) {
   uint4 v;
@@ -548,30 +627,18 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// A wait that ends with the CTA's giving up: warp 8 alone looks at the clock.  Every role's progress frees slots, which
-// that warp waits for (2 s at most) to its end; so the waits in the other roles stay a few instructions each.
-__device__ __forceinline__ void await(uint64_t* bar, uint32_t parity, TileBars* b) {
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity) && !gave_up(b)) {}
-  __syncwarp();
-}
-__device__ __forceinline__ bool slot_ready(TileBars* b, int k) {
-  await(&b->slot_full[k % kSlots], (k / kSlots) & 1, b);
-  return __all_sync(0xffffffffu, !gave_up(b) && b->slot[k % kSlots].row0 >= 0);
-}
-
 template <int NC>
 __global__ void __launch_bounds__(kTileThreads, 1)
 kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr int kHalves = NC > 2 ? 2 : 1, kD = 32 * NC, kSlices = 2 * NC, kStages = kv4_stages(kHalves);
-  constexpr int kTileBytes = kHalves * kHalfBytes;
+  constexpr int kTileBytes = kHalves * kHalfBytes, kRaw = raw_bytes(NC);
   const StepGeom& g = p.g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = smem;                              // two row tiles
   uint8_t* kv_smem = smem + 2 * kTileBytes;
   uint8_t* raw_smem = kv_smem + kStages * kTileBytes;                  // keys, values: codes, then scales
-  uint8_t* out_smem = raw_smem + 2 * kRawBytes;
+  uint8_t* out_smem = raw_smem + 2 * kRaw;
   float2* stats = reinterpret_cast<float2*>(out_smem + kTileStage);     // [stream][row]: (m, l)
   float* q_factor = reinterpret_cast<float*>(stats + 2 * kRows);        // [slot][stream][row]: of the scores
   TileBars* bars = reinterpret_cast<TileBars*>(q_factor + kSlots * 2 * kRows);
@@ -740,41 +807,21 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
       __syncwarp();
     } else {
       // ---------------------------------------------------------- copies
-      // A page's codes are a lane's copy, its scales another's; a page has whole groups of 8 tokens.
-      const bool scales = lane >= 16;
-      const int box = lane & 15;
-      const int per_page = g.tile_pages ? g.page_size : g.key_tile;
       uint32_t ph = 0, copied = 0;
-      const uint32_t to = smem_u32(raw_smem) + (scales ? kKeyTile * 16 * NC + box * per_page * 2 * NC : box * per_page * 16 * NC);
       for (int k = 0; slot_ready(bars, k); ++k) {
         const WorkItem& it = bars->slot[k % kSlots];
         const int n = item_tiles(it);
 #pragma unroll 1
         for (int u = 0; u < n && !gave_up(bars); ++u) {
-          const bool pre = it.t0 + u < it.np;
-          int key0;
-          const int keys = tile_keys(it, g, it.t0 + u, &key0), mine = min(per_page, keys - box * per_page);
-          uint32_t bytes = 0;
-          int64_t from = 0;
-          if (mine > 0) {
-            const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-            const int key = key0 + box * per_page, pi = g.by_page(key), token = key - pi * g.page_size;
-            int page = __ldg(table + pi);
-            if (page < 0 || page >= g.n_pages) {               // reported; what is copied instead does not matter
-              latch_status(status, kStatusRange);
-              page = 0;
-            }
-            bytes = ((mine + 7) & ~7) * (scales ? 2 * NC : 16 * NC);
-            from = page * p.pool.page_stride + it.group * p.pool.group_stride +
-                   (scales ? p.pool.scales + token * 2 * NC : token * 16 * NC);
-          }
-          const uint32_t total = ((keys + 7) & ~7) * 18 * NC;
+          const TileShare x = tile_share<NC>(p, it, it.t0 + u, status);
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
             await(&bars->raw_empty[value], ph ^ 1u, bars);
-            if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[value], total);
+            if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[value], x.total);
             __syncwarp();
-            if (bytes) copy_bulk(to + value * kRawBytes, (value ? p.pool.v : p.pool.k) + from, bytes, &bars->raw_full[value]);
+            if (x.bytes)
+              copy_bulk(smem_u32(raw_smem) + value * kRaw + x.to, (value ? p.pool.v : p.pool.k) + x.from, x.bytes,
+                        &bars->raw_full[value]);
             __syncwarp();
           }
           ph ^= 1u;
@@ -1042,7 +1089,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     const uint32_t place = ((((c & 1) ^ (j & 1)) << 2) ^ o) << 4;
     const uint32_t pick = o | (4 + o) << 4;          // of a key's two scales
     const uint32_t to0 = smem_u32(kv_smem) + (c >> 1) * kHalfBytes + 4 * j * 128;
-    const uint32_t raw = smem_u32(raw_smem) + value * kRawBytes;
+    const uint32_t raw = smem_u32(raw_smem) + value * kRaw;
     Ring r;                                          // keys and values take the ring's stages in turns
     r.s = value;
     int turn0 = value, turn1 = value;                // of the streams' own tiles
@@ -1151,7 +1198,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
         await(&bars->raw_full[value], ph, bars);
         ph ^= 1u;
         uint2 s = make_uint2(0, 0);
-        if (busy) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "r"(sat) : "memory");
+        if (busy) s = ld_shared8(sat);
         // ---- scales: none of what is past d or the last key
         const bool pre = it.t0 + u < it.np;
         int key0;
@@ -1250,11 +1297,15 @@ aff_status launch_tile(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
   return AFF_OK;
 }
 
+template <int NC, bool F32>
+aff_status launch_few(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
+  AFF_CUDA(cudaFuncSetAttribute(kv4_few_kernel<NC, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(NC)));
+  AFF_CUDA(launch_pdl(kv4_few_kernel<NC, F32>, grid, kFewThreads, (size_t)few_smem(NC), s, p));
+  return AFF_OK;
+}
 template <int NC>
 aff_status launch_few(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
-  if (p.g.dtype == AFF_BF16) AFF_CUDA(launch_pdl(kv4_few_kernel<NC, false>, grid, kFewThreads, 0, s, p));
-  else AFF_CUDA(launch_pdl(kv4_few_kernel<NC, true>, grid, kFewThreads, 0, s, p));
-  return AFF_OK;
+  return p.g.dtype == AFF_BF16 ? launch_few<NC, false>(p, grid, s) : launch_few<NC, true>(p, grid, s);
 }
 
 }  // namespace
