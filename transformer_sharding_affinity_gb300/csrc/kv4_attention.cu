@@ -135,433 +135,507 @@ __device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const Wo
 }
 
 // ---------------------------------------------------------------- few rows
-// Items of at most 8 rows, bound by the bytes of the cache.  Warp 8 claims items and copies their tiles as they lie into
-// a ring, running ahead over the items' ends; two CTAs of an SM have 147 KB on their way.  Eight warps share a tile by
-// its keys, 16 each, and nothing is exchanged before the item's end.  Products are transposed, keys as the long side:
-// S^T = K Q^T and O^T += V^T P^T, their operands made in registers from the copies.
+// Items of at most 8 rows, bound by the bytes of the cache.  Eight warps share an item: 32 keys at a time are a warp's
+// unit, which it copies for itself, a unit ahead (also over an item's end), into a buffer of its own; nothing is
+// exchanged before the item's end.  Two CTAs of an SM have 74 to 147 KB on their way.  Products are transposed, keys as
+// the long side:  S^T = K Q^T and O^T += V^T P^T, for 16 keys at a time, their operands made in registers from the copies.
 //   K  lane (key quad, c) holds its key's elements 8 W c .. + 8 W - 1 as they lie in memory (W words of codes); the
 //      contraction does not care which elements are a slice's, so the queries are dealt the same way.
 //   V  lane (quad, c) holds elements 4 W quad .. of keys 4 c .. 4 c + 3; a byte of two keys' codes for the same
 //      element makes the pair that V^T wants, two shifts and two selections for 16 elements.
 // Rows of S^T are dealt to keys so that a lane's four probabilities' keys are those it holds the values of.
-constexpr int kFewThreads = 288;
+constexpr int kFewThreads = 256;
 constexpr int kFewPitch = 132;               // floats of a staged row
-constexpr int kFewStages = 4;
+constexpr int kUnit = 32;                    // keys
 
-struct alignas(16) FewBars {
-  uint64_t full[kFewStages], empty[kFewStages], slot_full[kSlots], slot_empty[kSlots];
-  alignas(16) WorkItem slot[kSlots];         // row0 < 0: no more
-  int nan_key[kSlots][8];                    // the first key, not seen by every row, whose values of a block are NaN
-  float2 ml[8 * 8];                          // [warp][row]: (m, l)
-  int abort_flag;
+struct alignas(16) FewShared {
+  alignas(16) WorkItem slot[4];              // items k, k + 1, k + 2 in slot k % 4 ..; row0 < 0: no more
+  int nan_key[4][8];                         // the first key, not seen by every row, whose values of a block are NaN
+  float2 ml[8][8];                           // [warp][row]: (m, l)
 };
-constexpr int few_smem(int chunks) { return kFewStages * 2 * raw_bytes(chunks) + 8 * 8 * kFewPitch * 4 + (int)sizeof(FewBars); }
-static_assert(2 * (few_smem(4) + 1024) <= 228 * 1024, "two CTAs of an SM");
+__host__ __device__ constexpr int few_smem(int chunks, bool f32) {
+  return 8 * 2 * 2 * kUnit * 18 * chunks + 8 * 8 * kFewPitch * 4 + 2 * 8 * 32 * chunks * (f32 ? 4 : 2) + (int)sizeof(FewShared);
+}
+static_assert(2 * (few_smem(4, false) + 1024) <= 228 * 1024, "two CTAs of an SM");
+
+// 16 bytes from global to shared memory, past the first cache, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <int NC, bool F32>
 __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
   // W: words of codes that a lane holds of a key (of a value: half as many)
   constexpr int W = NC >= 3 ? 4 : NC, VW = W == 4 ? 2 : 1, KS = 2 * W, MT = 2 * W;
-  constexpr int kRaw = raw_bytes(NC);
-  extern __shared__ __align__(16) uint8_t few_raw[];       // ring: keys and values of a tile
-  float* const po = reinterpret_cast<float*>(few_raw + kFewStages * 2 * kRaw);      // [warp][row][kFewPitch]
-  FewBars* const bars = reinterpret_cast<FewBars*>(po + 8 * 8 * kFewPitch);
-  float2* const ml = bars->ml;
+  constexpr int kRaw = kUnit * 18 * NC, kE = F32 ? 4 : 2, kQRow = 32 * NC * kE;
+  extern __shared__ __align__(16) uint8_t few_raw[];       // two units of each warp: keys, values
+  float* const po = reinterpret_cast<float*>(few_raw + 8 * 4 * kRaw);               // [warp][row][kFewPitch]
+  uint8_t* const q_rows = reinterpret_cast<uint8_t*>(po + 8 * 8 * kFewPitch);       // two items' queries
+  FewShared& sh = *reinterpret_cast<FewShared*>(q_rows + 2 * 8 * kQRow);
   const StepGeom& g = p.g;
   uint32_t* status = &g.head->status;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kFewStages; ++i) {
-      mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 8);
-    }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bars->slot_full[i], 1);
-      mbar_init(&bars->slot_empty[i], 8);
-    }
-    bars->abort_flag = 0;
-    fence_mbar_init();
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, c = lane & 3;
   pdl_enter();
-  __syncthreads();
   const bool fits = plan_matches(g);
   const int n_items = fits ? g.head->n_items : 0, first = fits ? g.head->few_begin : 0;
   if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ items and copies
-    Ring r;
-    int copied = 0;
-    auto claim = [&]() {
-      int next = 0;
-      if (lane == 0) next = first + gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
-      return next;                           // of lane 0
-    };
-    auto pass_tiles = [&](int i) {           // past the other kernel's items
-      while (i < n_items && g.items[i].alt != 2) i = __shfl_sync(0xffffffffu, claim(), 0);
-      return i;
-    };
-    int i = pass_tiles(first + blockIdx.x), k = 0;
-    for (;; ++k) {
-      wait_on(&bars->slot_empty[k % kSlots], ((k / kSlots) & 1) ^ 1, bars);
-      int* d = reinterpret_cast<int*>(&bars->slot[k % kSlots]);
-      if (lane < (int)(sizeof(WorkItem) / 4)) d[lane] = i < n_items ? reinterpret_cast<const int*>(g.items + i)[lane] : -1;
-      if (lane < 8) bars->nan_key[k % kSlots][lane] = INT32_MAX;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->slot_full[k % kSlots]);
-      if (i >= n_items || gave_up(bars)) break;
-      const int next = claim();              // comes back behind the copies
-      const WorkItem it = load_item(g.items + i);
-      TileShare x{};
-      if (it.n0 > 0) x = tile_share<NC>(p, it, it.t0, status);
-#pragma unroll 1
-      for (int u = 0; u < it.n0 && !gave_up(bars); ++u) {
-        TileShare ahead{};                   // the next tile's page is asked for meanwhile
-        if (u + 1 < it.n0) ahead = tile_share<NC>(p, it, it.t0 + u + 1, status);
-        wait_on(&bars->empty[r.s], r.ph ^ 1u, bars);
-        if (lane == 0) mbar_arrive_expect_tx(&bars->full[r.s], 2 * x.total);
-        __syncwarp();
-        if (x.bytes) {
-          const uint32_t to = smem_u32(few_raw) + r.s * 2 * kRaw + x.to;
-          copy_bulk(to, p.pool.k + x.from, x.bytes, &bars->full[r.s]);
-          copy_bulk(to + kRaw, p.pool.v + x.from, x.bytes, &bars->full[r.s]);
-        }
-        __syncwarp();
-        r.skip(1, kFewStages);
-        copied = min(copied + 1, kFewStages);
-        x = ahead;
-      }
-      i = pass_tiles(__shfl_sync(0xffffffffu, next, 0));
+  // Items come by number for the first two rounds and then from a counter, two ahead; warp 0 looks after them.
+  auto claim = [&]() {
+    int next = 0;
+    if (lane == 0) next = first + 2 * gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
+    return next;                             // of lane 0
+  };
+  auto own_item = [&](int i) {               // past the other kernel's items
+    while (i < n_items && g.items[i].alt != 2) i = __shfl_sync(0xffffffffu, claim(), 0);
+    return i;
+  };
+  auto word_of = [&](int i) {                // this lane's word of the item
+    return lane < (int)(sizeof(WorkItem) / 4) && i < n_items ? reinterpret_cast<const int*>(g.items + i)[lane] : -1;
+  };
+  auto publish = [&](int k, int word) {
+    if (lane < (int)(sizeof(WorkItem) / 4)) reinterpret_cast<int*>(&sh.slot[k & 3])[lane] = word;
+    if (lane < 8) sh.nan_key[k & 3][lane] = INT32_MAX;
+  };
+  if (warp == 0) {
+    int i0 = own_item(first + blockIdx.x), i1 = own_item(first + gridDim.x + blockIdx.x);
+    if (i0 >= n_items) {                     // the other kernel's, and none left for it: the second is the first
+      i0 = i1;
+      i1 = n_items;
     }
-    // to the end of the last items, and of the copies, where the CTA has given up
-    for (int x = max(k - kSlots + 1, 0); x < k; ++x) wait_on(&bars->slot_empty[x % kSlots], (x / kSlots) & 1, bars);
-    for (int x = 0; x < copied; ++x) {
-      const int st = (r.s + kFewStages - 1 - x) % kFewStages;
-      const uint32_t ph = st < r.s ? r.ph : r.ph ^ 1u;
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_test_wait(&bars->full[st], ph) && global_timer_ns() - t0 < 100000000ull) {}
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ products
-    const int quad = lane >> 2, c = lane & 3;
-    const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of the warp's 16: k_off, k_off + 2
-    const bool k0_has = 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of its key elements
-    const bool v_has = 4 * W * quad < g.d;
-    const int v_block = 4 * W * quad / 16;
-    // from a tile's start: this lane's share of its keys, their scales, of its values, theirs
-    const uint32_t ring = smem_u32(few_raw);
-    const uint32_t k_at = (16 * warp + k_off) * 16 * NC + c * 4 * W;
-    const uint32_t ks_at = kKeyTile * 16 * NC + ((4 * warp + (quad >> 1)) * 2 * NC + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
-    const uint32_t v_at = kRaw + (16 * warp + 4 * c) * 16 * NC + quad * 2 * W;
-    const uint32_t vs_at = kRaw + kKeyTile * 16 * NC + ((4 * warp + c) * 2 * NC + v_block) * 4;
-    Ring ring_at;
-    for (int k = 0; slot_ready(bars, k); ++k) {
-      const WorkItem it = load_item(&bars->slot[k % kSlots]);
-      const int n = it.n0, nrows = it.nrows, row0 = it.row0;
-      // ---- queries: B operand of S^T, row quad
-      uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
-      float inverse;
-      {
-        const int rr = row0 + quad, tok = g.by_R(rr);
-        const int64_t at = (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
-        float x[8 * W];
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int e0 = 8 * W * c + 8 * j;
-          const bool has = quad < nrows && e0 < g.d;
-          if constexpr (F32) {
-            const float* src = static_cast<const float*>(p.q) + at + e0;
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 a = has ? __ldg(reinterpret_cast<const float4*>(src)) : z;
-            const float4 b = has ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
-            x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
-            x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
-          } else {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (has) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e0));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
-              x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float f = query_factor(top, &inverse);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
-            qh[s][h] = f16x2(a, b);
-            if constexpr (F32) {
-              const float2 r = halves(qh[s][h]);
-              ql[s][h] = f16x2(a - r.x, b - r.y);
-            }
-          }
-      }
-      // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
-      float sc[2], m[2], l[2], o[MT][4];
-      int own_vis[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 2 * c + e;
-        sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
-        own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
-        m[e] = -INFINITY;
-        l[e] = 0.f;
-      }
-      const int seen_by_all = all_see(it, g);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-
-#pragma unroll 1
-      for (int tile = 0; tile < n && !gave_up(bars); ++tile) {
-        const bool pre = it.t0 + tile < it.np;
-        int key0;
-        const int left = tile_keys(it, g, it.t0 + tile, &key0) - 16 * warp, unit0 = key0 + 16 * warp;    // from this warp's on
-        await(&bars->full[ring_at.s], ring_at.ph, bars);
-        if (left > 0) {
-          // ---- this lane's share
-          const uint32_t base = ring + ring_at.s * 2 * kRaw;
-          uint32_t kr[2][W], ks[2] = {0, 0}, vr[4][VW], vs = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < W; ++y) kr[x][y] = 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < VW; ++y) vr[x][y] = 0;
-          if (k0_has) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t at = base + k_at + x * 32 * NC;
-              if constexpr (W == 4) {
-                const uint4 w = ld_shared16(at);
-                kr[x][0] = w.x; kr[x][1] = w.y; kr[x][2] = w.z; kr[x][3] = w.w;
-              } else if constexpr (W == 2) {
-                const uint2 w = ld_shared8(at);
-                kr[x][0] = w.x; kr[x][1] = w.y;
-              } else {
-                kr[x][0] = ld_shared4(at);
-              }
-            }
-            if constexpr (W == 4) {
-              const uint2 w = ld_shared8(base + ks_at);
-              ks[0] = w.x;
-              ks[1] = k1_has ? w.y : 0;
-            } else {
-              ks[0] = ld_shared4(base + ks_at);
-            }
-          }
-          if (v_has) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t at = base + v_at + x * 16 * NC;
-              if constexpr (W == 4) {
-                const uint2 w = ld_shared8(at);
-                vr[x][0] = w.x; vr[x][1] = w.y;
-              } else if constexpr (W == 2) {
-                vr[x][0] = ld_shared4(at);
-              } else {
-                vr[x][0] = ld_shared2(at);
-              }
-            }
-            vs = ld_shared4(base + vs_at);
-            const int mine = left - 4 * c;               // keys past the end: zero
-            if (mine < 4) vs &= (1u << 8 * max(mine, 0)) - 1;
-          }
-          // ---- scores
-          uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
-          if constexpr (W == 4) {
-            const uint32_t b = quad & 1;
-            const uint32_t a2 = kv4_scale_pair(prmt(ks[0], ks[1], b | (4 + b) << 4));
-            const uint32_t b2 = kv4_scale_pair(prmt(ks[0], ks[1], (b + 2) | (b + 6) << 4));
-            ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
-            kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
-          } else {
-            const uint32_t b = quad & 1;
-            const uint32_t two = kv4_scale_pair(prmt(ks[0], 0, b | (b + 2) << 4));
-            ka[0] = ka[1] = prmt(two, two, 0x1010);
-            kb[0] = kb[1] = prmt(two, two, 0x3232);
-          }
-          float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            uint32_t a[4], b[4];
-            kv4_decode(kr[0][w], a);
-            kv4_decode(kr[1][w], b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[e] = mul_f16x2(a[e], ka[w >> 1]);
-              b[e] = mul_f16x2(b[e], kb[w >> 1]);
-            }
-            mma_16x8x16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
-            mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
-            if constexpr (F32) {
-              mma_16x8x16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
-              mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] += s2[e];
-          // ---- s[e]: key k_off, row 2 c + e; s[2 + e]: key k_off + 2
-          if (!(left >= 16 && seen_by_all > 0 && (pre || unit0 + 16 <= seen_by_all))) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int vis = own_vis[e] <= 0 ? 0 : pre ? left : min(left, own_vis[e] - unit0);
-              if (k_off >= vis) s[e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
-              if (k_off + 2 >= vis) s[2 + e] = -INFINITY;
-            }
-          }
-          bool grow = false;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) grow |= fmaxf(s[e], s[2 + e]) * sc[e] - m[e] > kRescale;
-          if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(s[e], s[2 + e]) * sc[e];
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float f = mx > m[e] ? ex2(m[e] - mx) : 1.f;
-              m[e] = fmaxf(m[e], mx);
-              l[e] *= f;
-#pragma unroll
-              for (int t = 0; t < MT; ++t) {
-                o[t][e] *= f;
-                o[t][2 + e] *= f;
-              }
-            }
-          }
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float neg = m[e] == -INFINITY ? kShift : kShift - m[e];
-            x[e] = ex2(fmaf(s[e], sc[e], neg));
-            x[2 + e] = ex2(fmaf(s[2 + e], sc[e], neg));
-            l[e] += x[e] + x[2 + e];
-          }
-          // keys x rows -> rows x keys, the B operand of O^T
-          const uint32_t p0 = f16x2(x[0], x[1]), p1 = f16x2(x[2], x[3]);
-          const uint32_t ph0 = transpose8(p0), ph1 = transpose8(p1);
-          uint32_t pl0 = 0, pl1 = 0;
-          if constexpr (F32) {
-            const float2 r0 = halves(p0), r1 = halves(p1);
-            pl0 = transpose8(f16x2(x[0] - r0.x, x[1] - r0.y));
-            pl1 = transpose8(f16x2(x[2] - r1.x, x[3] - r1.y));
-          }
-          // ---- values
-                const uint32_t odd = kv4_nan_scales(vs);
-          if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
-#pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              const int key = unit0 + 4 * c + x;
-              if (!pre && (odd >> (8 * x + 7) & 1u) && key >= seen_by_all) {
-                vs &= ~(0xffu << 8 * x);
-                atomicMin(&bars->nan_key[k % kSlots][v_block], key);
-              }
-            }
-          }
-          const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
-            constexpr uint32_t lo = 0x0f0f0f0fu;
-            kv4_decode((vr[0][j] & lo) | ((vr[1][j] << 4) & ~lo), a0);
-            kv4_decode(((vr[0][j] >> 4) & lo) | (vr[1][j] & ~lo), a1);
-            kv4_decode((vr[2][j] & lo) | ((vr[3][j] << 4) & ~lo), a2);
-            kv4_decode(((vr[2][j] >> 4) & lo) | (vr[3][j] & ~lo), a3);
-#pragma unroll
-            for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
-              const int t = 4 * j + b;
-              const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
-                             w3 = mul_f16x2(a3[b], v23);
-              if constexpr (F32) {
-                // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16x8x16(z, w0, w1, w2, w3, pl0, pl1);
-                mma_16x8x16(z, w0, w1, w2, w3, ph0, ph1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][e] += z[e];
-              } else {
-                mma_16x8x16(o[t], w0, w1, w2, w3, ph0, ph1);
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->empty[ring_at.s]);
-        ring_at.skip(1, kFewStages);
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");       // the item before's parts have been read
-      // ---- the warps' parts
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
-        const int r = 2 * c + e;
-        if (r >= nrows) continue;
-        if (quad == 0) ml[warp * 8 + r] = make_float2(m[e], l[e]);
-        float* dst = po + (warp * 8 + r) * kFewPitch + 4 * W * quad;
-#pragma unroll
-        for (int t = 0; t < MT; t += 2)
-          *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const int r = warp, e0 = 4 * lane;
-      if (r < nrows) {
-        const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w * 8 + r].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float2 s = ml[w * 8 + r];
-          if (s.y == 0.f) continue;                      // nothing seen by this warp
-          const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
-          sum += f * s.y;
-          const float4 v = *reinterpret_cast<const float4*>(po + (w * 8 + r) * kFewPitch + min(e0, 32 * W - 4));
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
-        }
-        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
-        if (e0 < g.d) {
-          if (bars->nan_key[k % kSlots][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
-          if (it.part_row >= 0) {
-            *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r) * g.d + e0) = acc;
-          } else if constexpr (F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
-          } else {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
-                make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
-          }
-        }
-        if (lane == 0) {
-          const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
-          if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
-          else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
-        }
-      }
-      slot_done(bars, k);
-    }
+    const int w0 = word_of(i0), w1 = word_of(i1);
+    publish(0, w0);
+    publish(1, w1);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && gave_up(bars)) latch_status(status, kStatusTimeout);
+
+  const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of 16: k_off, k_off + 2
+  const bool k0_has = 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of its key elements
+  const bool v_has = 4 * W * quad < g.d;
+  const int v_block = 4 * W * quad / 16;
+  const int subs = (g.key_tile + kUnit - 1) / kUnit;
+  const uint32_t mine_at = smem_u32(few_raw) + warp * 4 * kRaw;       // this warp's two units
+  // from a unit's start: this lane's share of its first 16 keys, their scales, of their values, theirs
+  const uint32_t k_at = k_off * 16 * NC + c * 4 * W;
+  const uint32_t ks_at = kUnit * 16 * NC + ((quad >> 1) * 2 * NC + (W == 4 ? 2 * c : W == 2 ? c : c >> 1)) * 4;
+  const uint32_t v_at = kRaw + 4 * c * 16 * NC + quad * 2 * W;
+  const uint32_t vs_at = kRaw + kUnit * 16 * NC + (c * 2 * NC + v_block) * 4;
+
+  // A place in this warp's walk over an item's units, 8 apart; `tile` counts from the item's first.
+  struct Walk {
+    int tile, sub;
+  };
+  auto begin = [&]() {
+    Walk w{0, warp};
+    while (w.sub >= subs) {
+      w.sub -= subs;
+      ++w.tile;
+    }
+    return w;
+  };
+  auto step = [&](Walk& w) {
+    w.sub += 8;
+    while (w.sub >= subs) {
+      w.sub -= subs;
+      ++w.tile;
+    }
+  };
+  // Keys from the unit at w on (none: 0 or less), the first of them in its segment; w moves over units without any.
+  auto find = [&](const WorkItem& it, Walk& w, int* unit0) {
+    for (; w.tile < it.n0; step(w)) {
+      int key0;
+      const int left = tile_keys(it, g, it.t0 + w.tile, &key0) - kUnit * w.sub;
+      *unit0 = key0 + kUnit * w.sub;
+      if (left > 0) return left;
+    }
+    return 0;
+  };
+  // Copies the unit at w, if there is one: 8 tokens at a time lie beside each other in a page, their codes and their
+  // scales.  Lanes 0 .. 3 look the pages up.
+  auto copy_unit = [&](const WorkItem& it, Walk& w, int buffer) {
+    int unit0;
+    const int left = find(it, w, &unit0);
+    if (left <= 0) return false;
+    const bool pre = it.t0 + w.tile < it.np;
+    int page = -1, token = 0;
+    if (lane < 4 && 8 * lane < left) {
+      const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+      const int pi = g.by_page(unit0 + 8 * lane);
+      page = __ldg(table + pi);
+      token = unit0 + 8 * lane - pi * g.page_size;
+      if (page < 0 || page >= g.n_pages) {               // read as zeros: report it
+        latch_status(status, kStatusRange);
+        page = -1;
+      }
+    }
+    const int64_t head = it.group * p.pool.group_stride;
+    const uint32_t to = mine_at + buffer * 2 * kRaw;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int q = i * 32 + lane, group = NC == 4 ? i : q / (8 * NC), rest = NC == 4 ? lane : q - group * 8 * NC;
+      const int pg = __shfl_sync(0xffffffffu, page, group), tk = __shfl_sync(0xffffffffu, token, group);
+      const int64_t from = max(pg, 0) * p.pool.page_stride + head + (tk * NC + rest) * 16;
+      copy16(to + q * 16, p.pool.k + from, pg >= 0);
+      copy16(to + kRaw + q * 16, p.pool.v + from, pg >= 0);
+    }
+    {
+      const int q = lane % (4 * NC), value = lane / (4 * NC), group = q / NC, rest = q - group * NC;
+      const int pg = __shfl_sync(0xffffffffu, page, group), tk = __shfl_sync(0xffffffffu, token, group);
+      const int64_t from = max(pg, 0) * p.pool.page_stride + head + p.pool.scales + tk * 2 * NC + rest * 16;
+      if (value < 2) copy16(to + value * kRaw + kUnit * 16 * NC + q * 16, (value ? p.pool.v : p.pool.k) + from, pg >= 0);
+    }
+    return true;
+  };
+  // Row `warp` of an item's queries.
+  auto copy_query = [&](int k) {
+    const WorkItem& it = sh.slot[k & 3];
+    if (it.row0 < 0) return;
+    const int rr = it.row0 + warp, tok = g.by_R(rr);
+    const bool live = warp < it.nrows && lane * 16 < g.d * kE;
+    const int64_t at = live ? ((int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d) * kE + lane * 16 : 0;
+    if (lane * 16 < kQRow)
+      copy16(smem_u32(q_rows) + ((k & 1) * 8 + warp) * kQRow + lane * 16, static_cast<const uint8_t*>(p.q) + at, live);
+  };
+  copy_query(0);
+
+  bool under_way = false;                    // this warp's next unit is
+  int buffer = 0;
+#pragma unroll 1
+  for (int k = 0;; ++k) {
+    asm volatile("cp.async.wait_all;" ::: "memory");       // this warp's row of queries is here
+    __syncthreads();                         // everybody's, and the item before's parts have been read
+    const WorkItem& it = sh.slot[k & 3];
+    const int nrows = it.nrows, row0 = it.row0;
+    if (row0 < 0) break;
+    copy_query(k + 1);
+    int claimed = 0, word = 0;
+    bool asked = false;
+    if (warp == 0) claimed = claim();
+    // ---- queries: B operand of S^T, row quad
+    uint32_t qh[KS][2], ql[F32 ? KS : 1][2];
+    float inverse;
+    {
+      const uint8_t* src = q_rows + ((k & 1) * 8 + quad) * kQRow + 8 * W * c * kE;
+      const bool has = 8 * W * c < 32 * NC;
+      float x[8 * W];
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if constexpr (F32) {
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 a = has ? reinterpret_cast<const float4*>(src)[2 * j] : z;
+          const float4 b = has ? reinterpret_cast<const float4*>(src)[2 * j + 1] : z;
+          x[8 * j] = a.x; x[8 * j + 1] = a.y; x[8 * j + 2] = a.z; x[8 * j + 3] = a.w;
+          x[8 * j + 4] = b.x; x[8 * j + 5] = b.y; x[8 * j + 6] = b.z; x[8 * j + 7] = b.w;
+        } else {
+          const uint4 w = has ? reinterpret_cast<const uint4*>(src)[j] : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            x[8 * j + 2 * y] = __uint_as_float(u[y] << 16);
+            x[8 * j + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8 * W; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float f = query_factor(top, &inverse);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = x[4 * s + 2 * h] * f, b = x[4 * s + 2 * h + 1] * f;
+          qh[s][h] = f16x2(a, b);
+          if constexpr (F32) {
+            const float2 r = halves(qh[s][h]);
+            ql[s][h] = f16x2(a - r.x, b - r.y);
+          }
+        }
+    }
+    // rows 2 c and 2 c + 1: the scores' factor, own keys in view, maximum (log2) that O and l refer to, sum
+    float sc[2], m[2], l[2], o[MT][4];
+    int own_vis[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * c + e;
+      sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
+      own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+    }
+    const int seen_by_all = all_see(it, g);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+
+    Walk at = begin(), ahead;
+    int unit0, left = find(it, at, &unit0);
+    ahead = at;
+#pragma unroll 1
+    while (left > 0) {
+      if (!under_way) {
+        copy_unit(it, ahead, buffer);
+        copy_commit();
+      }
+      // the next unit, of this item or else of the next
+      step(ahead);
+      under_way = copy_unit(it, ahead, buffer ^ 1);
+      if (!under_way && sh.slot[(k + 1) & 3].row0 >= 0) {
+        ahead = begin();
+        under_way = copy_unit(sh.slot[(k + 1) & 3], ahead, buffer ^ 1);
+      }
+      copy_commit();
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const uint32_t base = mine_at + buffer * 2 * kRaw;
+      const bool pre = it.t0 + at.tile < it.np;
+      float s[2][4];                         // s[h][e]: key 16 h + k_off, row 2 c + e; s[h][2 + e]: key 16 h + k_off + 2
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t kr[2][W], ks[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int y = 0; y < W; ++y) kr[x][y] = 0;
+        if (k0_has) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t from = base + k_at + (16 * h + 2 * x) * 16 * NC;
+            if constexpr (W == 4) {
+              const uint4 w = ld_shared16(from);
+              kr[x][0] = w.x; kr[x][1] = w.y; kr[x][2] = w.z; kr[x][3] = w.w;
+            } else if constexpr (W == 2) {
+              const uint2 w = ld_shared8(from);
+              kr[x][0] = w.x; kr[x][1] = w.y;
+            } else {
+              kr[x][0] = ld_shared4(from);
+            }
+          }
+          if constexpr (W == 4) {
+            const uint2 w = ld_shared8(base + ks_at + h * 32 * NC);
+            ks[0] = w.x;
+            ks[1] = k1_has ? w.y : 0;
+          } else {
+            ks[0] = ld_shared4(base + ks_at + h * 32 * NC);
+          }
+        }
+        uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
+        if constexpr (W == 4) {
+          const uint32_t b = quad & 1;
+          const uint32_t a2 = kv4_scale_pair(prmt(ks[0], ks[1], b | (4 + b) << 4));
+          const uint32_t b2 = kv4_scale_pair(prmt(ks[0], ks[1], (b + 2) | (b + 6) << 4));
+          ka[0] = prmt(a2, a2, 0x1010); ka[1] = prmt(a2, a2, 0x3232);
+          kb[0] = prmt(b2, b2, 0x1010); kb[1] = prmt(b2, b2, 0x3232);
+        } else {
+          const uint32_t b = quad & 1;
+          const uint32_t two = kv4_scale_pair(prmt(ks[0], 0, b | (b + 2) << 4));
+          ka[0] = ka[1] = prmt(two, two, 0x1010);
+          kb[0] = kb[1] = prmt(two, two, 0x3232);
+        }
+        float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint32_t a[4], b[4];
+          kv4_decode(kr[0][w], a);
+          kv4_decode(kr[1][w], b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = mul_f16x2(a[e], ka[w >> 1]);
+            b[e] = mul_f16x2(b[e], kb[w >> 1]);
+          }
+          mma_16x8x16(s1, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
+          mma_16x8x16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
+          if constexpr (F32) {
+            mma_16x8x16(s1, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
+            mma_16x8x16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][e] = s1[e] + s2[e];
+      }
+      if (!(left >= kUnit && seen_by_all > 0 && (pre || unit0 + kUnit <= seen_by_all))) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int vis = own_vis[e] <= 0 ? 0 : pre ? left : min(left, own_vis[e] - unit0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (16 * h + k_off >= vis) s[h][e] = -INFINITY;          // chosen, not added: a NaN behind the mask is gone
+            if (16 * h + k_off + 2 >= vis) s[h][2 + e] = -INFINITY;
+          }
+        }
+      }
+      float mx[2];
+      bool grow = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e])) * sc[e];
+        grow |= mx[e] - m[e] > kRescale;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+          const float f = mx[e] > m[e] ? ex2(m[e] - mx[e]) : 1.f;
+          m[e] = fmaxf(m[e], mx[e]);
+          l[e] *= f;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            o[t][e] *= f;
+            o[t][2 + e] *= f;
+          }
+        }
+      }
+      uint32_t ph[2][2], pl[2][2];           // keys x rows -> rows x keys, the B operand of O^T
+      const float neg[2] = {m[0] == -INFINITY ? kShift : kShift - m[0], m[1] == -INFINITY ? kShift : kShift - m[1]};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float a = ex2(fmaf(s[h][2 * y], sc[0], neg[0])), b = ex2(fmaf(s[h][2 * y + 1], sc[1], neg[1]));
+          l[0] += a;
+          l[1] += b;
+          const uint32_t both = f16x2(a, b);
+          ph[h][y] = transpose8(both);
+          if constexpr (F32) {
+            const float2 r = halves(both);
+            pl[h][y] = transpose8(f16x2(a - r.x, b - r.y));
+          }
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t vr[4][VW];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t from = base + v_at + (16 * h + x) * 16 * NC;
+#pragma unroll
+          for (int y = 0; y < VW; ++y) vr[x][y] = 0;
+          if (v_has) {
+            if constexpr (W == 4) {
+              const uint2 w = ld_shared8(from);
+              vr[x][0] = w.x; vr[x][1] = w.y;
+            } else if constexpr (W == 2) {
+              vr[x][0] = ld_shared4(from);
+            } else {
+              vr[x][0] = ld_shared2(from);
+            }
+          }
+        }
+        uint32_t vs = v_has ? ld_shared4(base + vs_at + h * 32 * NC) : 0;
+            const int mine = left - 16 * h - 4 * c;          // keys past the end: zero
+            if (mine < 4) vs &= (1u << 8 * max(mine, 0)) - 1;
+        const uint32_t odd = kv4_nan_scales(vs);
+        if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            const int key = unit0 + 16 * h + 4 * c + x;
+            if (!pre && (odd >> (8 * x + 7) & 1u) && key >= seen_by_all) {
+              vs &= ~(0xffu << 8 * x);
+              atomicMin(&sh.nan_key[k & 3][v_block], key);
+            }
+          }
+        }
+        const uint32_t v01 = kv4_scale_pair(vs), v23 = kv4_scale_pair(vs >> 16);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          uint32_t a0[4], a1[4], a2[4], a3[4];           // elements 2 b, 2 b + 1 of keys 0, 1; of keys 2, 3
+          constexpr uint32_t lo = 0x0f0f0f0fu;
+          kv4_decode((vr[0][j] & lo) | ((vr[1][j] << 4) & ~lo), a0);
+          kv4_decode(((vr[0][j] >> 4) & lo) | (vr[1][j] & ~lo), a1);
+          kv4_decode((vr[2][j] & lo) | ((vr[3][j] << 4) & ~lo), a2);
+          kv4_decode(((vr[2][j] >> 4) & lo) | (vr[3][j] & ~lo), a3);
+#pragma unroll
+          for (int b = 0; b < (W == 1 ? 2 : 4); ++b) {
+            const int t = 4 * j + b;
+            const uint32_t w0 = mul_f16x2(a0[b], v01), w1 = mul_f16x2(a1[b], v01), w2 = mul_f16x2(a2[b], v23),
+                           w3 = mul_f16x2(a3[b], v23);
+            if constexpr (F32) {
+              // summed apart: the products' own accumulation cuts bits off, which would add up over long keys
+              float z[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16x8x16(z, w0, w1, w2, w3, pl[h][0], pl[h][1]);
+              mma_16x8x16(z, w0, w1, w2, w3, ph[h][0], ph[h][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][e] += z[e];
+            } else {
+              mma_16x8x16(o[t], w0, w1, w2, w3, ph[h][0], ph[h][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();                          // the buffer may be filled again
+      buffer ^= 1;
+      if (warp == 0 && !asked) {             // once an item: the claim has come back
+        word = word_of(own_item(__shfl_sync(0xffffffffu, claimed, 0)));
+        asked = true;
+      }
+      step(at);
+      left = find(it, at, &unit0);
+    }
+    if (warp == 0) {
+      if (!asked) word = word_of(own_item(__shfl_sync(0xffffffffu, claimed, 0)));
+      publish(k + 2, word);
+    }
+
+    // ---- the warps' parts
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+      const int r = 2 * c + e;
+      if (r >= nrows) continue;
+      if (quad == 0) sh.ml[warp][r] = make_float2(m[e], l[e]);
+      float* dst = po + (warp * 8 + r) * kFewPitch + 4 * W * quad;
+#pragma unroll
+      for (int t = 0; t < MT; t += 2)
+        *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
+    }
+    __syncthreads();
+    const int r = warp, e0 = 4 * lane;
+    if (r < nrows) {
+      const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, sh.ml[w][r].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 s = sh.ml[w][r];
+        if (s.y == 0.f) continue;                      // nothing seen by this warp
+        const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
+        sum += f * s.y;
+        const float4 v = *reinterpret_cast<const float4*>(po + (w * 8 + r) * kFewPitch + min(e0, 32 * W - 4));
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int vis = it.seq < 0 ? 0 : tok + it.own_off + 1;
+      if (e0 < g.d) {
+        if (sh.nan_key[k & 3][e0 / 16] < vis) acc.x = acc.y = acc.z = acc.w = __int_as_float(0x7fc00000);
+        if (it.part_row >= 0) {
+          *reinterpret_cast<float4*>(g.part_out + (int64_t)(it.part_row + r) * g.d + e0) = acc;
+        } else if constexpr (F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) = acc;
+        } else {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tok * g.H + h) * g.d + e0) =
+              make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+        }
+      }
+      if (lane == 0) {
+        const float lse = sum == 0.f ? -INFINITY : (ref - kShift) * kLn2 + logf(sum);
+        if (it.part_row >= 0) g.part_lse[it.part_row + r] = lse;
+        else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
+      }
+    }
+  }
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
   if (fits && threadIdx.x == 0) {
     __threadfence();
@@ -1299,8 +1373,8 @@ aff_status launch_tile(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
 
 template <int NC, bool F32>
 aff_status launch_few(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
-  AFF_CUDA(cudaFuncSetAttribute(kv4_few_kernel<NC, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(NC)));
-  AFF_CUDA(launch_pdl(kv4_few_kernel<NC, F32>, grid, kFewThreads, (size_t)few_smem(NC), s, p));
+  AFF_CUDA(cudaFuncSetAttribute(kv4_few_kernel<NC, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(NC, F32)));
+  AFF_CUDA(launch_pdl(kv4_few_kernel<NC, F32>, grid, kFewThreads, (size_t)few_smem(NC, F32), s, p));
   return AFF_OK;
 }
 template <int NC>
