@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
   __syncthreads();
 
   const int k_off = (quad >> 1) * 4 + (quad & 1);          // this lane's keys of 16: k_off, k_off + 2
-  const bool k0_has = 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of its key elements
+  const bool k0_has = NC == 4 || 8 * W * c < g.d, k1_has = W == 4 && 8 * W * c + 16 < g.d;      // blocks of its key elements
   const bool v_has = 4 * W * quad < g.d;
   const int v_block = 4 * W * quad / 16;
   const int subs = (g.key_tile + kUnit - 1) / kUnit;
@@ -258,32 +258,32 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
     const int left = find(it, w, &unit0);
     if (left <= 0) return false;
     const bool pre = it.t0 + w.tile < it.np;
-    int page = -1, token = 0;
+    int64_t codes = -1;                      // lane x < 4: where its tokens' codes begin; their scales lie `scales` further
+    int scales = 0;
     if (lane < 4 && 8 * lane < left) {
       const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-      const int pi = g.by_page(unit0 + 8 * lane);
-      page = __ldg(table + pi);
-      token = unit0 + 8 * lane - pi * g.page_size;
+      const int pi = g.by_page(unit0 + 8 * lane), page = __ldg(table + pi), token = unit0 + 8 * lane - pi * g.page_size;
       if (page < 0 || page >= g.n_pages) {               // read as zeros: report it
         latch_status(status, kStatusRange);
-        page = -1;
+      } else {
+        codes = page * p.pool.page_stride + it.group * p.pool.group_stride + token * 16 * NC;
+        scales = p.pool.scales - token * 14 * NC;
       }
     }
-    const int64_t head = it.group * p.pool.group_stride;
     const uint32_t to = mine_at + buffer * 2 * kRaw;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int q = i * 32 + lane, group = NC == 4 ? i : q / (8 * NC), rest = NC == 4 ? lane : q - group * 8 * NC;
-      const int pg = __shfl_sync(0xffffffffu, page, group), tk = __shfl_sync(0xffffffffu, token, group);
-      const int64_t from = max(pg, 0) * p.pool.page_stride + head + (tk * NC + rest) * 16;
-      copy16(to + q * 16, p.pool.k + from, pg >= 0);
-      copy16(to + kRaw + q * 16, p.pool.v + from, pg >= 0);
+      const int64_t at = __shfl_sync(0xffffffffu, codes, group), from = max(at, (int64_t)0) + rest * 16;
+      copy16(to + q * 16, p.pool.k + from, at >= 0);
+      copy16(to + kRaw + q * 16, p.pool.v + from, at >= 0);
     }
     {
       const int q = lane % (4 * NC), value = lane / (4 * NC), group = q / NC, rest = q - group * NC;
-      const int pg = __shfl_sync(0xffffffffu, page, group), tk = __shfl_sync(0xffffffffu, token, group);
-      const int64_t from = max(pg, 0) * p.pool.page_stride + head + p.pool.scales + tk * 2 * NC + rest * 16;
-      if (value < 2) copy16(to + value * kRaw + kUnit * 16 * NC + q * 16, (value ? p.pool.v : p.pool.k) + from, pg >= 0);
+      const int64_t at = __shfl_sync(0xffffffffu, codes, group), from = max(at, (int64_t)0) + rest * 16;
+      const int more = __shfl_sync(0xffffffffu, scales, group);
+      if (value < 2)
+        copy16(to + value * kRaw + kUnit * 16 * NC + q * 16, (value ? p.pool.v : p.pool.k) + from + more, at >= 0);
     }
     return true;
   };
@@ -395,32 +395,28 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
       float s[2][4];                         // s[h][e]: key 16 h + k_off, row 2 c + e; s[h][2 + e]: key 16 h + k_off + 2
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        // (a lane without elements reads what lies beside: its scales are 0)
         uint32_t kr[2][W], ks[2] = {0, 0};
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < W; ++y) kr[x][y] = 0;
-        if (k0_has) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t from = base + k_at + (16 * h + 2 * x) * 16 * NC;
-            if constexpr (W == 4) {
-              const uint4 w = ld_shared16(from);
-              kr[x][0] = w.x; kr[x][1] = w.y; kr[x][2] = w.z; kr[x][3] = w.w;
-            } else if constexpr (W == 2) {
-              const uint2 w = ld_shared8(from);
-              kr[x][0] = w.x; kr[x][1] = w.y;
-            } else {
-              kr[x][0] = ld_shared4(from);
-            }
-          }
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t from = base + k_at + (16 * h + 2 * x) * 16 * NC;
           if constexpr (W == 4) {
-            const uint2 w = ld_shared8(base + ks_at + h * 32 * NC);
-            ks[0] = w.x;
-            ks[1] = k1_has ? w.y : 0;
+            const uint4 w = ld_shared16(from);
+            kr[x][0] = w.x; kr[x][1] = w.y; kr[x][2] = w.z; kr[x][3] = w.w;
+          } else if constexpr (W == 2) {
+            const uint2 w = ld_shared8(from);
+            kr[x][0] = w.x; kr[x][1] = w.y;
           } else {
-            ks[0] = ld_shared4(base + ks_at + h * 32 * NC);
+            kr[x][0] = ld_shared4(from);
           }
+        }
+        if constexpr (W == 4) {
+          const uint2 w = ld_shared8(base + ks_at + h * 32 * NC);
+          ks[0] = k0_has ? w.x : 0;
+          ks[1] = k1_has ? w.y : 0;
+        } else {
+          const uint32_t w = ld_shared4(base + ks_at + h * 32 * NC);
+          ks[0] = k0_has ? w : 0;
         }
         uint32_t ka[2], kb[2];               // scales of this lane's blocks, twice, of either key
         if constexpr (W == 4) {
@@ -456,7 +452,8 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[h][e] = s1[e] + s2[e];
       }
-      if (!(left >= kUnit && seen_by_all > 0 && (pre || unit0 + kUnit <= seen_by_all))) {
+      const bool all = left >= kUnit && seen_by_all > 0 && (pre || unit0 + kUnit <= seen_by_all);    // rows see all keys
+      if (!all) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int vis = own_vis[e] <= 0 ? 0 : pre ? left : min(left, own_vis[e] - unit0);
@@ -512,30 +509,29 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint32_t from = base + v_at + (16 * h + x) * 16 * NC;
-#pragma unroll
-          for (int y = 0; y < VW; ++y) vr[x][y] = 0;
-          if (v_has) {
-            if constexpr (W == 4) {
-              const uint2 w = ld_shared8(from);
-              vr[x][0] = w.x; vr[x][1] = w.y;
-            } else if constexpr (W == 2) {
-              vr[x][0] = ld_shared4(from);
-            } else {
-              vr[x][0] = ld_shared2(from);
-            }
+          if constexpr (W == 4) {
+            const uint2 w = ld_shared8(from);
+            vr[x][0] = w.x; vr[x][1] = w.y;
+          } else if constexpr (W == 2) {
+            vr[x][0] = ld_shared4(from);
+          } else {
+            vr[x][0] = ld_shared2(from);
           }
         }
-        uint32_t vs = v_has ? ld_shared4(base + vs_at + h * 32 * NC) : 0;
-            const int mine = left - 16 * h - 4 * c;          // keys past the end: zero
-            if (mine < 4) vs &= (1u << 8 * max(mine, 0)) - 1;
-        const uint32_t odd = kv4_nan_scales(vs);
-        if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
+        uint32_t vs = ld_shared4(base + vs_at + h * 32 * NC);
+        if (!v_has) vs = 0;
+        if (!all) {
+          const int mine = left - 16 * h - 4 * c;          // keys past the end: zero
+          if (mine < 4) vs &= (1u << 8 * max(mine, 0)) - 1;
+          const uint32_t odd = kv4_nan_scales(vs);
+          if (__any_sync(0xffffffffu, odd)) {              // rare: NaN values that some row does not see are taken out
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const int key = unit0 + 16 * h + 4 * c + x;
-            if (!pre && (odd >> (8 * x + 7) & 1u) && key >= seen_by_all) {
-              vs &= ~(0xffu << 8 * x);
-              atomicMin(&sh.nan_key[k & 3][v_block], key);
+            for (int x = 0; x < 4; ++x) {
+              const int key = unit0 + 16 * h + 4 * c + x;
+              if (!pre && (odd >> (8 * x + 7) & 1u) && key >= seen_by_all) {
+                vs &= ~(0xffu << 8 * x);
+                atomicMin(&sh.nan_key[k & 3][v_block], key);
+              }
             }
           }
         }
