@@ -7,11 +7,12 @@
 //
 // Borders.  A code changes where x / (scale g) passes one of seven values, a scale where the maximum does, so a last
 // bit of fp32 may move an element by a third of its size.  Values and plain keys are exact in the activations'
-// type, and their quotients are too wherever they lie on a border (q + (x - q s) / s is the rounded quotient, which
-// reaches a border only from it): fp32 decides.  A rotated or normalised key is off by at most 2^-19 of the
-// products it is the sum of (19 roundings of the norm's sum halved by the root, the root's own 2^-22, four products).
-// Where that crosses a border, in one of 25000 elements, the row is computed again in 64 bits, rounded to odd before
-// each of the two conversions, so that the double rounding does not show.
+// type, and their quotients are too wherever they lie on a border: q + (x - q s) / s, with q off by an ulp or two, is the
+// rounded quotient (the remainder is exact, as s has four bits), and that reaches a border only from it: fp32 decides.
+// Rotated and normalised keys are off by at most kMarginNorm or kMarginTurn of the products they are the sum of.
+// Where that crosses a border, the row is computed again in 64 bits, rounded to odd before each of the two
+// conversions, so that the double rounding does not show.  It happens to 1 in 60000 normalised elements; the 64-bit
+// units have a sixty-fourth of the others' rate, so a narrow margin is worth its arithmetic.
 #include "affinity.h"
 #include "internal.h"
 #include "kv4.cuh"
@@ -29,7 +30,11 @@ namespace aff {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kMargin = 1.f / (1 << 19);     // of fp32 keys, relative to the products they are the sum of
+// What fp32 keys may be off by, in units of 2^-24 of the products they are the sum of.  Turned: a product and a fused
+// product and sum, 2; with a norm before it: the sum of squares (a lane's chain of four, two sums, four levels of
+// shuffles) 10, the mean and eps 3, together halved by the root; the root after a step of Newton's 1.5; the gain's two
+// products 2.  Rounded up to 4 and 14.
+constexpr float kMarginTurn = 4.f / (1 << 24), kMarginNorm = 14.f / (1 << 24);
 
 struct AppendParams {
   StepGeom g;
@@ -41,10 +46,14 @@ struct AppendParams {
   const void *q_gain, *k_gain;
   int64_t n_pos;
   float eps, inv_d;
-  float k_inv, v_inv;          // 1 / k_scale, 1 / v_scale
+  float k_scale, v_scale, k_inv, v_inv;      // and their reciprocals
   int32_t rot, interleaved, lanes, lane_bits;
 };
 
+// Eight numbers, as four pairs for the packed instructions.
+struct Eight {
+  uint64_t p[4];
+};
 // Eight neighbouring elements.
 template <typename E>
 struct Run;
@@ -52,19 +61,22 @@ template <>
 struct Run<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* at) { w = __ldcs(reinterpret_cast<const uint4*>(at)); }
+  __device__ __forceinline__ void load_shared(const __nv_bfloat16* at) { w = __ldg(reinterpret_cast<const uint4*>(at)); }
   __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ Eight get() const {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    Eight f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(x[i] << 16);
-      f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f.p[i] = pk_u(x[i] << 16, x[i] & 0xffff0000u);
+    return f;
   }
-  static __device__ __forceinline__ void put(__nv_bfloat16* at, const float (&f)[8]) {
+  static __device__ __forceinline__ void put(__nv_bfloat16* at, const Eight& f) {
     uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpk(f.p[i]);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(v.y), "f"(v.x));
+    }
     *reinterpret_cast<uint4*>(at) = make_uint4(x[0], x[1], x[2], x[3]);
   }
 };
@@ -75,13 +87,16 @@ struct Run<float> {
     a = __ldcs(reinterpret_cast<const float4*>(at));
     b = __ldcs(reinterpret_cast<const float4*>(at) + 1);
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ void load_shared(const float* at) {
+    a = __ldg(reinterpret_cast<const float4*>(at));
+    b = __ldg(reinterpret_cast<const float4*>(at) + 1);
   }
-  static __device__ __forceinline__ void put(float* at, const float (&f)[8]) {
-    reinterpret_cast<float4*>(at)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(at)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ Eight get() const { return {{pk(a.x, a.y), pk(a.z, a.w), pk(b.x, b.y), pk(b.z, b.w)}}; }
+  static __device__ __forceinline__ void put(float* at, const Eight& f) {
+    const float2 x = unpk(f.p[0]), y = unpk(f.p[1]), z = unpk(f.p[2]), w = unpk(f.p[3]);
+    reinterpret_cast<float4*>(at)[0] = make_float4(x.x, x.y, y.x, y.y);
+    reinterpret_cast<float4*>(at)[1] = make_float4(z.x, z.y, w.x, w.y);
   }
 };
 
@@ -110,50 +125,71 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;}" : "=f"(r) : "r"(kv4_scale_pair(byte)));
   return r;
 }
-// x / 6 rounded to nearest (x >= 0, finite or not).
-__device__ __forceinline__ float sixth(float x) { return __fdiv_rn(x, 6.f); }
-
-__device__ __forceinline__ uint32_t largest(const float (&f)[8]) {      // of the magnitudes' bits: a NaN is above infinity
-  uint32_t m = 0;
+// x / 6 rounded to nearest (x >= 0), for x past 4096 what saturates as x / 6 does.
+__device__ __forceinline__ float sixth(float x) {
+  x = fminf(x, 4096.f);
+  const float q = x * (1.f / 6.f);
+  return fmaf(fmaf(-q, 6.f, x), 1.f / 6.f, q);
+}
+__device__ __forceinline__ float reciprocal(float x) {      // within an ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The larger of m and two magnitudes; NaN if one is.
+__device__ __forceinline__ float largest(float m, uint64_t pair) {
+  const float2 v = unpk(pair);
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float largest(const Eight& f) {
+  float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+  for (int i = 0; i < 4; ++i) m = largest(m, f.p[i]);
   return m;
 }
 
-__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
-  const float z = x * c - y * s;
-  y = x * s + y * c;
-  x = z;
-}
-
-// The codes of eight elements whose block has the maximum `top` (bits), with its scale.  `error`: what the elements
-// may be off by; *near_border is set where that could matter.
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t top, float inv_g, float error, bool inexact,
+// The codes of eight elements whose block has the maximum `top`, with its scale.  `error`: what the elements may be off
+// by, where that is looked at; *near_border is set where it could matter.
+__device__ __forceinline__ uint32_t quantise(Eight x, float top, float g, float inv_g, float error, bool inexact,
                                              uint32_t* scale, bool* near_border) {
-  if (top >= 0x7f800000u) {
-    *scale = 0x7f;
-    return 0;
+  const bool finite = top < INFINITY;
+  const float t = top * inv_g;
+  *scale = finite ? to_scales(sixth(t), 0.f) & 0xff : 0x7f;
+  const float s = scale_value(finite ? *scale : 0), inv = s > 0.f ? reciprocal(s) * inv_g : 0.f;
+  if (!(t < 4096.f)) {                           // far past what saturates: the quotients might overflow
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpk(x.p[i]);
+      x.p[i] = pk(fminf(fmaxf(v.x, -4096.f * g), 4096.f * g), fminf(fmaxf(v.y, -4096.f * g), 4096.f * g));
+    }
   }
-  const float t = __uint_as_float(top);
-  *scale = to_scales(sixth(t * inv_g), 0.f) & 0xff;
-  const float s = scale_value(*scale), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  const uint64_t inv2 = pk(inv, inv), less2 = pk(-s * g, -s * g);
   float q[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float y = x[e] * inv_g, q0 = y * inv;
-    q[e] = fabsf(q0) < 16.f ? fmaf(fmaf(-q0, s, y), inv, q0) : q0;      // far out it saturates, and y - q0 s may be no number
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t q0 = mul2(x.p[i], inv2);
+    const float2 v = unpk(fma2(fma2(q0, less2, x.p[i]), inv2, q0));
+    q[2 * i] = v.x;
+    q[2 * i + 1] = v.y;
   }
-  const uint32_t w = to_codes(q);
+  const uint32_t w = finite ? to_codes(q) : 0;
   if (inexact) {
-    const uint32_t both = to_scales(sixth((t + error) * inv_g), sixth(fmaxf(t - error, 0.f) * inv_g));
+    const uint32_t both = to_scales(sixth((top + error) * inv_g), sixth(fmaxf(top - error, 0.f) * inv_g));
     float lo[8], hi[8];
-    const float d = error * inv_g * inv;
+    const float d = error * inv;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       hi[e] = fabsf(q[e]) + d;
-      lo[e] = fmaxf(fabsf(q[e]) - d, 0.f);
+      lo[e] = fabsf(q[e]) - d;
     }
-    if (to_codes(lo) != to_codes(hi) || (both & 0xff) != both >> 8) *near_border = true;
+    if (((to_codes(lo) ^ to_codes(hi)) & 0x77777777u) || (both & 0xff) != both >> 8) *near_border = finite;
   }
   return w;
 }
@@ -256,11 +292,25 @@ __device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, boo
   return c;
 }
 
+// (x, y) turned, both of each pair of pairs.
+__device__ __forceinline__ void turn2(uint64_t& x, uint64_t& y, uint64_t c, uint64_t s) {
+  const float2 t = unpk(s);
+  const uint64_t minus = pk(-t.x, -t.y);
+  const uint64_t z = fma2(y, minus, mul2(x, c));
+  y = fma2(x, s, mul2(y, c));
+  x = z;
+}
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float z = x * c - y * s;
+  y = x * s + y * c;
+  x = z;
+}
+
 // A block is (a part of) one token; a row is dealt to `lanes` neighbouring threads, each with two runs of eight
 // elements: of the rotated part the two halves of eight pairs (or, interleaved, two neighbouring runs whose pairs
 // lie side by side), past it and in value rows neighbours.  A thread has kPer rows, `slots` apart.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kPer = 2;
   pdl_enter();
   const StepGeom& g = p.g;
@@ -301,87 +351,87 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
     stand = false;
     if (threadIdx.x == 0) latch_status(&g.head->status, kStatusRange);
   }
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = s[e] = 0.f;
   const float *cos = p.cos + pos * half + 8 * lane, *sin = p.sin + pos * half + 8 * lane;
-  if (stand && rotates) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(cos + e)), y = __ldg(reinterpret_cast<const float4*>(sin + e));
-      c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
-      s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
-    }
-  }
-  Partner with{0, 0, false, false};
-  {
-    const int base = (threadIdx.x & 31) & ~(p.lanes - 1), ra = lane ^ 1, rb = (units + lane) ^ 1;
-    with.b_of_a = ra >= units;
-    with.lane_a = base + (with.b_of_a ? ra - units : ra);
-    with.b_of_b = rb >= units;
-    with.lane_b = base + (with.b_of_b ? rb - units : rb);
-    if (!split) with.lane_a = with.lane_b = base + lane;
-  }
   const int64_t page = (ti.slot >> 32) * p.pool.page_stride;
   const int token = (int)(ti.slot & 0xffffffff);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = r0 + k * slots;
     const bool is_q = r < g.H, turned = r < n_rot, live = r < rows && stand;
-    float a[8], b[8], inv = 1.f;
-    va[k].get(a);
-    vb[k].get(b);
+    Eight a = va[k].get(), b = vb[k].get();
     const E* gain = static_cast<const E*>(is_q ? p.q_gain : turned ? p.k_gain : nullptr);
-    if (p.q_gain || p.k_gain) {
+    float inv = 1.f;
+    if ((p.q_gain || p.k_gain) && !__all_sync(0xffffffffu, !turned)) {
       // every lane of the warp takes part in the sum
-      float ss = 0.f;
+      uint64_t s2 = mul2(a.p[0], a.p[0]), s3 = mul2(b.p[0], b.p[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+      for (int i = 1; i < 4; ++i) {
+        s2 = fma2(a.p[i], a.p[i], s2);
+        s3 = fma2(b.p[i], b.p[i], s3);
+      }
+      const float2 x = unpk(s2), y = unpk(s3);
+      float ss = (x.x + x.y) + (y.x + y.y);
       for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      inv = rsqrtf(ss * p.inv_d + p.eps);
+      const float m = ss * p.inv_d + p.eps;
+      inv = rsqrtf(m);
+      const float more = fmaf(0.5f * inv, fmaf(-m * inv, inv, 1.f), inv);      // a step of Newton's
+      if (m > 1e-30f && m < 1e30f) inv = more;
     }
     const int at_a = turned ? ja : 16 * lane, at_b = turned ? jb : 16 * lane + 8;
     const bool has = at_a < g.d;
-    float ma = 0.f, mb = 0.f;                      // the largest sums of products' magnitudes, of each run
+    float error_a = 0.f, error_b = 0.f;            // bounds of the products' magnitudes, of each run
     if (turned && live && has) {
       if (gain) {
         Run<E> ga, gb;
-        ga.load(gain + at_a);
-        gb.load(gain + at_b);
-        float fa[8], fb[8];
-        ga.get(fa);
-        gb.get(fb);
+        ga.load_shared(gain + at_a);
+        gb.load_shared(gain + at_b);
+        const Eight fa = ga.get(), fb = gb.get();
+        const uint64_t inv2 = pk(inv, inv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] *= inv * fa[e];
-          b[e] *= inv * fb[e];
-        }
-        if (!is_q && !rotates) {
-          ma = __uint_as_float(largest(a));
-          mb = __uint_as_float(largest(b));
+        for (int i = 0; i < 4; ++i) {
+          a.p[i] = mul2(a.p[i], mul2(inv2, fa.p[i]));
+          b.p[i] = mul2(b.p[i], mul2(inv2, fb.p[i]));
         }
       }
-      if (rotates && !p.interleaved) {
+      if (!is_q) {
+        error_a = largest(a);
+        error_b = largest(b);
+      }
+      if (rotates) {
+        Eight c, s;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!is_q) {
-            ma = fmaxf(ma, fabsf(a[e] * c[e]) + fabsf(b[e] * s[e]));
-            mb = fmaxf(mb, fabsf(a[e] * s[e]) + fabsf(b[e] * c[e]));
-          }
-          turn(a[e], b[e], c[e], s[e]);
+        for (int i = 0; i < 4; i += 2) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(cos + 2 * i)), y = __ldg(reinterpret_cast<const float4*>(sin + 2 * i));
+          c.p[i] = pk(x.x, x.y);
+          c.p[i + 1] = pk(x.z, x.w);
+          s.p[i] = pk(y.x, y.y);
+          s.p[i + 1] = pk(y.z, y.w);
         }
-      } else if (rotates) {
-        // pairs (2e, 2e + 1) of 16 neighbours: the first four in a, the others in b
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!is_q) {
-            ma = fmaxf(ma, fmaxf(fabsf(a[2 * e] * c[e]) + fabsf(a[2 * e + 1] * s[e]),
-                                 fabsf(a[2 * e] * s[e]) + fabsf(a[2 * e + 1] * c[e])));
-            mb = fmaxf(mb, fmaxf(fabsf(b[2 * e] * c[e + 4]) + fabsf(b[2 * e + 1] * s[e + 4]),
-                                 fabsf(b[2 * e] * s[e + 4]) + fabsf(b[2 * e + 1] * c[e + 4])));
+        if (!is_q) {
+          const float mc = largest(c), ms = largest(s);
+          if (p.interleaved) {
+            error_a *= mc + ms;
+            error_b *= mc + ms;
+          } else {
+            const float x = error_a * mc + error_b * ms;
+            error_b = error_a * ms + error_b * mc;
+            error_a = x;
           }
-          turn(a[2 * e], a[2 * e + 1], c[e], s[e]);
-          turn(b[2 * e], b[2 * e + 1], c[e + 4], s[e + 4]);
+        }
+        if (!p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) turn2(a.p[i], b.p[i], c.p[i], s.p[i]);
+        } else {
+          // pairs (2e, 2e + 1) of 16 neighbours: the first four in a, the others in b
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 x = unpk(a.p[i]), y = unpk(b.p[i]);
+            const float2 ca = unpk(c.p[i >> 1]), sa = unpk(s.p[i >> 1]), cb = unpk(c.p[2 + (i >> 1)]), sb = unpk(s.p[2 + (i >> 1)]);
+            turn(x.x, x.y, i & 1 ? ca.y : ca.x, i & 1 ? sa.y : sa.x);
+            turn(y.x, y.y, i & 1 ? cb.y : cb.x, i & 1 ? sb.y : sb.x);
+            a.p[i] = pk(x.x, x.y);
+            b.p[i] = pk(y.x, y.y);
+          }
         }
       }
     }
@@ -389,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
       if (r < rows && has) {
         if (!stand) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;       // padding
+          for (int i = 0; i < 4; ++i) a.p[i] = b.p[i] = 0;       // padding
         }
         E* dst = static_cast<E*>(p.q_out) + (int64_t)t * p.q_out_stride + r * g.d;
         Run<E>::put(dst + at_a, a);
@@ -398,26 +448,35 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
     }
     if (__all_sync(0xffffffffu, is_q || r >= rows)) continue;
     // the blocks' maxima and errors: of this lane's runs, and of the runs beside them
-    uint32_t top_a = largest(a), top_b = largest(b);
-    const bool across = split && turned;
-    {
-      const uint32_t aa = __shfl_sync(0xffffffffu, top_a, with.lane_a), ab = __shfl_sync(0xffffffffu, top_b, with.lane_a);
-      const uint32_t ba = __shfl_sync(0xffffffffu, top_a, with.lane_b), bb = __shfl_sync(0xffffffffu, top_b, with.lane_b);
-      const uint32_t oa = across ? (with.b_of_a ? ab : aa) : top_b, ob = across ? (with.b_of_b ? bb : ba) : top_a;
-      top_a = max(top_a, oa);
-      top_b = max(top_b, ob);
-      const float eaa = __shfl_sync(0xffffffffu, ma, with.lane_a), eab = __shfl_sync(0xffffffffu, mb, with.lane_a);
-      const float eba = __shfl_sync(0xffffffffu, ma, with.lane_b), ebb = __shfl_sync(0xffffffffu, mb, with.lane_b);
-      const float ea = across ? (with.b_of_a ? eab : eaa) : mb, eb = across ? (with.b_of_b ? ebb : eba) : ma;
-      ma = fmaxf(ma, ea);
-      mb = fmaxf(mb, eb);
-    }
-    const float inv_g = turned ? p.k_inv : p.v_inv;
+    float top_a = largest(a), top_b = largest(b);
     const bool inexact = turned && (gain || rotates);
+    Partner with{0, 0, false, false};
+    if (__any_sync(0xffffffffu, split && turned)) {
+      const int base = (threadIdx.x & 31) & ~(p.lanes - 1), ra = lane ^ 1, rb = (units + lane) ^ 1;
+      with.b_of_a = ra >= units;
+      with.lane_a = split ? base + (with.b_of_a ? ra - units : ra) : base + lane;
+      with.b_of_b = rb >= units;
+      with.lane_b = split ? base + (with.b_of_b ? rb - units : rb) : base + lane;
+      const bool across = split && turned;
+      auto beside = [&](float& x, float& y) {
+        const float aa = __shfl_sync(0xffffffffu, x, with.lane_a), ab = __shfl_sync(0xffffffffu, y, with.lane_a);
+        const float ba = __shfl_sync(0xffffffffu, x, with.lane_b), bb = __shfl_sync(0xffffffffu, y, with.lane_b);
+        const float oa = across ? (with.b_of_a ? ab : aa) : y, ob = across ? (with.b_of_b ? bb : ba) : x;
+        x = larger(x, oa);
+        y = larger(y, ob);
+      };
+      beside(top_a, top_b);
+      beside(error_a, error_b);
+    } else {
+      top_a = top_b = larger(top_a, top_b);
+      error_a = error_b = larger(error_a, error_b);
+    }
+    const float scale = turned ? p.k_scale : p.v_scale, inv_g = turned ? p.k_inv : p.v_inv;
+    const float margin = gain ? kMarginNorm : kMarginTurn;
     bool near_border = false;
     Codes w;
-    w.a = quantise(a, top_a, inv_g, ma * kMargin, inexact, &w.scale_a, &near_border);
-    w.b = quantise(b, top_b, inv_g, mb * kMargin, inexact, &w.scale_b, &near_border);
+    w.a = quantise(a, top_a, scale, inv_g, error_a * margin, inexact, &w.scale_a, &near_border);
+    w.b = quantise(b, top_b, scale, inv_g, error_b * margin, inexact, &w.scale_b, &near_border);
     const bool keep = live && !is_q;
     if (__any_sync(0xffffffffu, near_border && keep && has)) {
       // every key row of the warp that is no plain copy; rows that are not stored stand in with the first of the keys
@@ -531,15 +590,13 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
     uint32_t h[4];
     kv4_decode(w[x], h);
     const uint32_t s2 = kv4_scale_pair(sc[x] | sc[x] << 8);
-    float f[8];
+    Eight f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t v = mul_f16x2(h[e], s2);        // exact
-      asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
-          : "=f"(f[2 * e]), "=f"(f[2 * e + 1])
-          : "r"(v));
-      f[2 * e] *= scale;
-      f[2 * e + 1] *= scale;
+      float x, y;
+      asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(x), "=f"(y) : "r"(v));
+      f.p[e] = mul2(pk(x, y), pk(scale, scale));
     }
     Run<E>::put(out + (int64_t)(t0 + x) * g.G * g.d, f);
   }
@@ -581,6 +638,8 @@ extern "C" aff_status affinity_kv4_append(const void* q, int64_t q_stride, const
   p.q_gain = rotary->q_gain; p.k_gain = rotary->k_gain;
   p.n_pos = rotary->rot ? rotary->n_pos : INT64_MAX;
   p.eps = rotary->eps;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
   p.k_inv = 1.f / cache->k_scale;
   p.v_inv = 1.f / cache->v_scale;
   p.rot = rotary->rot;
