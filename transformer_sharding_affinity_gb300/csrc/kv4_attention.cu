@@ -158,7 +158,11 @@ __host__ __device__ constexpr int few_smem(int chunks, bool f32) {
 }
 static_assert(2 * (few_smem(4, false) + 1024) <= 228 * 1024, "two CTAs of an SM");
 
-// 16 bytes from global to shared memory, past the first cache, or 16 zero bytes.
+// 16 bytes from global to shared memory, past the first cache.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// The same, or 16 zero bytes.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
@@ -241,51 +245,58 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
       ++w.tile;
     }
   };
-  // Keys from the unit at w on (none: 0 or less), the first of them in its segment; w moves over units without any.
-  auto find = [&](const WorkItem& it, Walk& w, int* unit0) {
-    for (; w.tile < it.n0; step(w)) {
-      int key0;
-      const int left = tile_keys(it, g, it.t0 + w.tile, &key0) - kUnit * w.sub;
-      *unit0 = key0 + kUnit * w.sub;
-      if (left > 0) return left;
-    }
-    return 0;
+  struct Unit {
+    int key0, left;                          // its first key within its segment, keys from it on; left 0: none
+    bool pre;
   };
-  // Copies the unit at w, if there is one: 8 tokens at a time lie beside each other in a page, their codes and their
-  // scales.  Lanes 0 .. 3 look the pages up.
+  const uint8_t* const k_pool = p.pool.k + lane * 16;
+  const uint8_t* const v_pool = p.pool.v + lane * 16;
+  // Copies the unit at w or the next one that holds a key (w moves there): 8 tokens at a time lie beside each other in a
+  // page, their codes and their scales.  Lanes 0 .. 3 look the pages up.  What lies behind the last key stays as it was.
   auto copy_unit = [&](const WorkItem& it, Walk& w, int buffer) {
-    int unit0;
-    const int left = find(it, w, &unit0);
-    if (left <= 0) return false;
-    const bool pre = it.t0 + w.tile < it.np;
-    int64_t codes = -1;                      // lane x < 4: where its tokens' codes begin; their scales lie `scales` further
-    int scales = 0;
-    if (lane < 4 && 8 * lane < left) {
-      const int32_t* table = pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
-      const int pi = g.by_page(unit0 + 8 * lane), page = __ldg(table + pi), token = unit0 + 8 * lane - pi * g.page_size;
-      if (page < 0 || page >= g.n_pages) {               // read as zeros: report it
-        latch_status(status, kStatusRange);
-      } else {
-        codes = page * p.pool.page_stride + it.group * p.pool.group_stride + token * 16 * NC;
-        scales = p.pool.scales - token * 14 * NC;
-      }
+    Unit u{0, 0, false};
+    for (; w.tile < it.n0; step(w)) {
+      const int keys = tile_keys(it, g, it.t0 + w.tile, &u.key0);
+      u.key0 += kUnit * w.sub;
+      u.left = keys - kUnit * w.sub;
+      if (u.left > 0) break;
     }
-    const uint32_t to = mine_at + buffer * 2 * kRaw;
+    if (w.tile >= it.n0) {
+      u.left = 0;
+      return u;
+    }
+    u.pre = it.t0 + w.tile < it.np;
+    int64_t codes = 0;                       // lane x < 4: where its tokens' codes begin; their scales lie `scales` further
+    int scales = 0;
+    if (lane < 4 && 8 * lane < u.left) {
+      const int32_t* table = u.pre ? g.prefix_pages : g.pages + (int64_t)it.seq * g.pages_stride;
+      const int key = u.key0 + 8 * lane, pi = g.by_page(key), token = key - pi * g.page_size;
+      int page = __ldg(table + pi);
+      if (page < 0 || page >= g.n_pages) {               // reported; what is copied instead does not matter
+        latch_status(status, kStatusRange);
+        page = 0;
+      }
+      codes = page * p.pool.page_stride + it.group * p.pool.group_stride + token * 16 * NC;
+      scales = p.pool.scales - token * 14 * NC;
+    }
+    const uint32_t to = mine_at + buffer * 2 * kRaw + lane * 16;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int q = i * 32 + lane, group = NC == 4 ? i : q / (8 * NC), rest = NC == 4 ? lane : q - group * 8 * NC;
-      const int64_t at = __shfl_sync(0xffffffffu, codes, group), from = max(at, (int64_t)0) + rest * 16;
-      copy16(to + q * 16, p.pool.k + from, at >= 0);
-      copy16(to + kRaw + q * 16, p.pool.v + from, at >= 0);
+      const int q = i * 32 + lane, group = NC == 4 ? i : q / (8 * NC);
+      const int64_t from = __shfl_sync(0xffffffffu, codes, group) + (NC == 4 ? 0 : (i * 32 - group * 8 * NC) * 16);
+      if (8 * group < u.left) {
+        copy16(to + i * 512, k_pool + from);
+        copy16(to + kRaw + i * 512, v_pool + from);
+      }
     }
     {
-      const int q = lane % (4 * NC), value = lane / (4 * NC), group = q / NC, rest = q - group * NC;
-      const int64_t at = __shfl_sync(0xffffffffu, codes, group), from = max(at, (int64_t)0) + rest * 16;
-      const int more = __shfl_sync(0xffffffffu, scales, group);
-      if (value < 2)
-        copy16(to + value * kRaw + kUnit * 16 * NC + q * 16, (value ? p.pool.v : p.pool.k) + from + more, at >= 0);
+      const int q = lane % (4 * NC), value = lane / (4 * NC), group = q / NC;
+      const int64_t from = __shfl_sync(0xffffffffu, codes, group);
+      const int more = __shfl_sync(0xffffffffu, scales, group) + (q - group * NC - lane) * 16;
+      if (value < 2 && 8 * group < u.left)
+        copy16(to + value * kRaw + kUnit * 16 * NC + (q - lane) * 16, (value ? v_pool : k_pool) + from + more);
     }
-    return true;
+    return u;
   };
   // Row `warp` of an item's queries.
   auto copy_query = [&](int k) {
@@ -299,7 +310,8 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
   };
   copy_query(0);
 
-  bool under_way = false;                    // this warp's next unit is
+  Walk w = begin();
+  Unit carried{0, 0, false};                 // the item's first unit, where it was copied before the last one's end
   int buffer = 0;
 #pragma unroll 1
   for (int k = 0;; ++k) {
@@ -371,27 +383,28 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
     for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
 
-    Walk at = begin(), ahead;
-    int unit0, left = find(it, at, &unit0);
-    ahead = at;
+    Unit u = carried;
+    if (u.left <= 0) {
+      w = begin();
+      u = copy_unit(it, w, buffer);
+      copy_commit();
+    }
+    carried.left = 0;
 #pragma unroll 1
-    while (left > 0) {
-      if (!under_way) {
-        copy_unit(it, ahead, buffer);
-        copy_commit();
-      }
+    while (u.left > 0) {
       // the next unit, of this item or else of the next
-      step(ahead);
-      under_way = copy_unit(it, ahead, buffer ^ 1);
-      if (!under_way && sh.slot[(k + 1) & 3].row0 >= 0) {
-        ahead = begin();
-        under_way = copy_unit(sh.slot[(k + 1) & 3], ahead, buffer ^ 1);
+      step(w);
+      const Unit next = copy_unit(it, w, buffer ^ 1);
+      if (next.left <= 0 && sh.slot[(k + 1) & 3].row0 >= 0) {
+        w = begin();
+        carried = copy_unit(sh.slot[(k + 1) & 3], w, buffer ^ 1);
       }
+      const int left = u.left, unit0 = u.key0;
+      const bool pre = u.pre;
       copy_commit();
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       const uint32_t base = mine_at + buffer * 2 * kRaw;
-      const bool pre = it.t0 + at.tile < it.np;
       float s[2][4];                         // s[h][e]: key 16 h + k_off, row 2 c + e; s[h][2 + e]: key 16 h + k_off + 2
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -568,8 +581,7 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
         word = word_of(own_item(__shfl_sync(0xffffffffu, claimed, 0)));
         asked = true;
       }
-      step(at);
-      left = find(it, at, &unit0);
+      u = next;
     }
     if (warp == 0) {
       if (!asked) word = word_of(own_item(__shfl_sync(0xffffffffu, claimed, 0)));
