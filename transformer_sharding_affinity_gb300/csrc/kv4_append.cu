@@ -101,7 +101,8 @@ struct Run<float> {
 };
 
 // Eight numbers to eight codes.
-__device__ __forceinline__ uint32_t to_codes(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t to_codes(const Eight& x) {
+  const float2 a = unpk(x.p[0]), b = unpk(x.p[1]), c = unpk(x.p[2]), d = unpk(x.p[3]);
   uint32_t w;
   asm("{.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -110,7 +111,7 @@ __device__ __forceinline__ uint32_t to_codes(const float (&f)[8]) {
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};}"
       : "=r"(w)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return w;
 }
 // Two scales, the first in the low byte.
@@ -155,43 +156,57 @@ __device__ __forceinline__ float largest(const Eight& f) {
   return m;
 }
 
-// The codes of eight elements whose block has the maximum `top`, with its scale.  `error`: what the elements may be off
-// by, where that is looked at; *near_border is set where it could matter.
-__device__ __forceinline__ uint32_t quantise(Eight x, float top, float g, float inv_g, float error, bool inexact,
-                                             uint32_t* scale, bool* near_border) {
+// The scale of a block whose maximum is `top`, which may be off by `error`; *near_border is set where that could matter.
+struct Scale {
+  uint32_t byte;
+  float step, inv;                               // scale g and its reciprocal, 0 where that is 0 or the block not finite
+};
+__device__ __forceinline__ Scale make_scale(float top, float g, float inv_g, float error, bool inexact, bool* near_border) {
   const bool finite = top < INFINITY;
-  const float t = top * inv_g;
-  *scale = finite ? to_scales(sixth(t), 0.f) & 0xff : 0x7f;
-  const float s = scale_value(finite ? *scale : 0), inv = s > 0.f ? reciprocal(s) * inv_g : 0.f;
-  if (!(t < 4096.f)) {                           // far past what saturates: the quotients might overflow
+  const uint32_t two = to_scales(sixth(top * inv_g), 0.f) & 0xff;
+  const float s = finite ? scale_value(two) : 0.f;
+  if (inexact) {
+    const uint32_t both = to_scales(sixth((top + error) * inv_g), sixth(fmaxf(top - error, 0.f) * inv_g));
+    if (finite && (both & 0xff) != both >> 8) *near_border = true;
+  }
+  return {finite ? two : 0x7f, s * g, s > 0.f ? reciprocal(s) * inv_g : 0.f};
+}
+
+// The codes of eight elements of a block, which may be off by e_i margin where `inexact`: lo and hi differ in the elements
+// for which that could matter.
+struct Quantised {
+  uint32_t codes, lo, hi;
+};
+__device__ __forceinline__ Quantised quantise(Eight x, float top, float g, const Scale& s, const Eight& e, float margin,
+                                              bool inexact) {
+  if (top >= 4096.f * g) {                       // far past what saturates: the quotients might overflow
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = unpk(x.p[i]);
       x.p[i] = pk(fminf(fmaxf(v.x, -4096.f * g), 4096.f * g), fminf(fmaxf(v.y, -4096.f * g), 4096.f * g));
     }
   }
-  const uint64_t inv2 = pk(inv, inv), less2 = pk(-s * g, -s * g);
-  float q[8];
+  const uint64_t inv2 = pk(s.inv, s.inv), less2 = pk(-s.step, -s.step);
+  Eight q;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t q0 = mul2(x.p[i], inv2);
-    const float2 v = unpk(fma2(fma2(q0, less2, x.p[i]), inv2, q0));
-    q[2 * i] = v.x;
-    q[2 * i + 1] = v.y;
+    q.p[i] = fma2(fma2(q0, less2, x.p[i]), inv2, q0);
   }
-  const uint32_t w = finite ? to_codes(q) : 0;
-  if (inexact) {
-    const uint32_t both = to_scales(sixth((top + error) * inv_g), sixth(fmaxf(top - error, 0.f) * inv_g));
-    float lo[8], hi[8];
-    const float d = error * inv;
+  Quantised r{to_codes(q), 0, 0};
+  if (s.byte == 0x7f) r.codes = 0;
+  if (inexact && s.byte != 0x7f) {
+    const float d = margin * s.inv;
+    Eight lo, hi;                                // away from zero and towards it, or the other way round
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      hi[e] = fabsf(q[e]) + d;
-      lo[e] = fabsf(q[e]) - d;
+    for (int i = 0; i < 4; ++i) {
+      hi.p[i] = fma2(e.p[i], pk(d, d), q.p[i]);
+      lo.p[i] = fma2(e.p[i], pk(-d, -d), q.p[i]);
     }
-    if (((to_codes(lo) ^ to_codes(hi)) & 0x77777777u) || (both & 0xff) != both >> 8) *near_border = finite;
+    r.lo = to_codes(lo) & 0x77777777u;
+    r.hi = to_codes(hi) & 0x77777777u;
   }
-  return w;
+  return r;
 }
 
 // x to fp32, towards zero, its last bit set where something was cut off: a rounding of the result to fewer bits is
@@ -218,9 +233,12 @@ struct Codes {
   uint32_t a, b, scale_a, scale_b;
 };
 
-// A key row in 64 bits, by the row's lanes.  Loops stay loops: a rare path, and small.
+// A key row in 64 bits, by the row's lanes.  Loops stay loops: a rare path, and small.  `a`, `b`: the lane's runs as fp32
+// has them.  Where no scale is in doubt (`whole` false), the elements that are, alone: each is on one side or the other
+// of the border between its two codes, which is exact.
 template <typename E>
-__device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, bool split) {
+__device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, bool split, Codes c, const Quantised a,
+                                          const Quantised b, bool whole) {
   const E* src = static_cast<const E*>(r.src);
   const E* gain = static_cast<const E*>(r.gain);
   const bool has = r.ja < r.d;
@@ -250,6 +268,26 @@ __device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, boo
       *x = z;
     }
   };
+  if (!whole) {
+    const float step_a = scale_value(c.scale_a), step_b = scale_value(c.scale_b);
+    uint32_t in_a = a.lo ^ a.hi, in_b = b.lo ^ b.hi;
+#pragma unroll 1
+    while (has && (in_a | in_b)) {
+      const bool second = in_a == 0;
+      const int i = (__ffs(second ? in_b : in_a) - 1) >> 2, at = (second ? 8 : 0) + i;
+      double x, y;
+      pair(r.interleaved ? at >> 1 : i, &x, &y);
+      const double v = fabs((r.interleaved ? at & 1 : second) ? y : x) * r.inv_g;
+      const uint32_t u = (second ? b.lo : a.lo) >> (4 * i) & 7, w = (second ? b.hi : a.hi) >> (4 * i) & 7, low = min(u, w);
+      const float mid = low < 4 ? 0.25f + 0.5f * low : low == 4 ? 2.5f : low == 5 ? 3.5f : 5.f;
+      const double border = (double)(mid * (second ? step_b : step_a));
+      const uint32_t code = v > border || (v == border && (low & 1)) ? low + 1 : low;
+      uint32_t& word = second ? c.b : c.a;
+      word = (word & ~(7u << 4 * i)) | code << 4 * i;
+      (second ? in_b : in_a) &= ~(15u << 4 * i);
+    }
+    return c;
+  }
   double top_a = 0.0, top_b = 0.0;
 #pragma unroll 1
   for (int e = 0; has && e < 8; ++e) {
@@ -269,11 +307,10 @@ __device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, boo
   const double other_a = split ? (p.b_of_a ? ab : aa) : top_b, other_b = split ? (p.b_of_b ? bb : ba) : top_a;
   top_a = fmax(top_a, other_a);
   top_b = fmax(top_b, other_b);
-  Codes c{0, 0, to_scales(to_odd(top_a * r.inv_g / 6.0), 0.f) & 0xff, to_scales(to_odd(top_b * r.inv_g / 6.0), 0.f) & 0xff};
+  c = Codes{0, 0, to_scales(to_odd(top_a * r.inv_g / 6.0), 0.f) & 0xff, to_scales(to_odd(top_b * r.inv_g / 6.0), 0.f) & 0xff};
   const double sa = scale_value(c.scale_a), sb = scale_value(c.scale_b);
   auto code = [&](double x, double s) {
-    float f[8] = {s > 0.0 ? to_odd(x * r.inv_g / s) : 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    return to_codes(f) & 15u;
+    return to_codes(Eight{{pk(s > 0.0 ? to_odd(x * r.inv_g / s) : 0.f, 0.f), 0, 0, 0}}) & 15u;
   };
 #pragma unroll 1
   for (int e = 0; has && e < 8; ++e) {
@@ -310,7 +347,7 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
 // elements: of the rotated part the two halves of eight pairs (or, interleaved, two neighbouring runs whose pairs
 // lie side by side), past it and in value rows neighbours.  A thread has kPer rows, `slots` apart.
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kPer = 2;
   pdl_enter();
   const StepGeom& g = p.g;
@@ -379,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_co
     }
     const int at_a = turned ? ja : 16 * lane, at_b = turned ? jb : 16 * lane + 8;
     const bool has = at_a < g.d;
-    float error_a = 0.f, error_b = 0.f;            // bounds of the products' magnitudes, of each run
+    Eight ea{{0, 0, 0, 0}}, eb = ea;               // what the products are at most, by magnitude, but for cos and sin
+    const bool inexact = turned && !is_q && (gain || rotates);
+    float margin = gain ? kMarginNorm : kMarginTurn;
     if (turned && live && has) {
       if (gain) {
         Run<E> ga, gb;
@@ -393,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_co
           b.p[i] = mul2(b.p[i], mul2(inv2, fb.p[i]));
         }
       }
-      if (!is_q) {
-        error_a = largest(a);
-        error_b = largest(b);
+      if (inexact) {
+        ea = a;
+        eb = b;
       }
       if (rotates) {
         Eight c, s;
@@ -407,15 +446,18 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_co
           s.p[i] = pk(y.x, y.y);
           s.p[i + 1] = pk(y.z, y.w);
         }
-        if (!is_q) {
-          const float mc = largest(c), ms = largest(s);
-          if (p.interleaved) {
-            error_a *= mc + ms;
-            error_b *= mc + ms;
-          } else {
-            const float x = error_a * mc + error_b * ms;
-            error_b = error_a * ms + error_b * mc;
-            error_a = x;
+        if (inexact) {
+          margin *= larger(largest(c), largest(s));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = unpk(a.p[i]), y = unpk(b.p[i]);
+            if (p.interleaved) {
+              const float ex = fabsf(x.x) + fabsf(x.y), ey = fabsf(y.x) + fabsf(y.y);
+              ea.p[i] = pk(ex, ex);
+              eb.p[i] = pk(ey, ey);
+            } else {
+              ea.p[i] = eb.p[i] = pk(fabsf(x.x) + fabsf(y.x), fabsf(x.y) + fabsf(y.y));
+            }
           }
         }
         if (!p.interleaved) {
@@ -447,39 +489,46 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_co
       }
     }
     if (__all_sync(0xffffffffu, is_q || r >= rows)) continue;
-    // the blocks' maxima and errors: of this lane's runs, and of the runs beside them
+    // the blocks' maxima: of this lane's runs and of the runs beside them
     float top_a = largest(a), top_b = largest(b);
-    const bool inexact = turned && (gain || rotates);
     Partner with{0, 0, false, false};
-    if (__any_sync(0xffffffffu, split && turned)) {
+    const bool across = split && turned;
+    if (__any_sync(0xffffffffu, across)) {
       const int base = (threadIdx.x & 31) & ~(p.lanes - 1), ra = lane ^ 1, rb = (units + lane) ^ 1;
       with.b_of_a = ra >= units;
       with.lane_a = split ? base + (with.b_of_a ? ra - units : ra) : base + lane;
       with.b_of_b = rb >= units;
       with.lane_b = split ? base + (with.b_of_b ? rb - units : rb) : base + lane;
-      const bool across = split && turned;
-      auto beside = [&](float& x, float& y) {
-        const float aa = __shfl_sync(0xffffffffu, x, with.lane_a), ab = __shfl_sync(0xffffffffu, y, with.lane_a);
-        const float ba = __shfl_sync(0xffffffffu, x, with.lane_b), bb = __shfl_sync(0xffffffffu, y, with.lane_b);
-        const float oa = across ? (with.b_of_a ? ab : aa) : y, ob = across ? (with.b_of_b ? bb : ba) : x;
-        x = larger(x, oa);
-        y = larger(y, ob);
-      };
-      beside(top_a, top_b);
-      beside(error_a, error_b);
+      float oa, ob;
+      if (units & 1) {
+        const float aa = __shfl_sync(0xffffffffu, top_a, with.lane_a), ab = __shfl_sync(0xffffffffu, top_b, with.lane_a);
+        const float ba = __shfl_sync(0xffffffffu, top_a, with.lane_b), bb = __shfl_sync(0xffffffffu, top_b, with.lane_b);
+        oa = with.b_of_a ? ab : aa;
+        ob = with.b_of_b ? bb : ba;
+      } else {                                     // a run's neighbour is the same run of the next lane
+        oa = __shfl_xor_sync(0xffffffffu, top_a, 1);
+        ob = __shfl_xor_sync(0xffffffffu, top_b, 1);
+      }
+      const float ta = larger(top_a, across ? oa : top_b), tb = larger(top_b, across ? ob : top_a);
+      top_a = ta;
+      top_b = tb;
     } else {
       top_a = top_b = larger(top_a, top_b);
-      error_a = error_b = larger(error_a, error_b);
     }
-    const float scale = turned ? p.k_scale : p.v_scale, inv_g = turned ? p.k_inv : p.v_inv;
-    const float margin = gain ? kMarginNorm : kMarginTurn;
-    bool near_border = false;
-    Codes w;
-    w.a = quantise(a, top_a, scale, inv_g, error_a * margin, inexact, &w.scale_a, &near_border);
-    w.b = quantise(b, top_b, scale, inv_g, error_b * margin, inexact, &w.scale_b, &near_border);
-    const bool keep = live && !is_q;
-    if (__any_sync(0xffffffffu, near_border && keep && has)) {
-      // every key row of the warp that is no plain copy; rows that are not stored stand in with the first of the keys
+    // Every lane looks with its own errors at whether a maximum is near a border: the one that has it is among them.
+    const float g_scale = turned ? p.k_scale : p.v_scale, inv_g = turned ? p.k_inv : p.v_inv;
+    const float error = inexact ? larger(largest(ea), largest(eb)) * margin : 0.f;
+    bool scale_in_doubt = false;
+    const Scale scale_a = make_scale(top_a, g_scale, inv_g, error, inexact, &scale_in_doubt);
+    Scale scale_b = scale_a;
+    if (__any_sync(0xffffffffu, across)) scale_b = make_scale(top_b, g_scale, inv_g, error, inexact, &scale_in_doubt);
+    const Quantised qa = quantise(a, top_a, g_scale, scale_a, ea, margin, inexact);
+    const Quantised qb = quantise(b, top_b, g_scale, scale_b, eb, margin, inexact);
+    Codes w{qa.codes, qb.codes, scale_a.byte, scale_b.byte};
+    const bool keep = live && !is_q, watch = keep && has && inexact;
+    const bool whole = __any_sync(0xffffffffu, scale_in_doubt && watch);
+    if (whole || __any_sync(0xffffffffu, watch && (qa.lo != qa.hi || qb.lo != qb.hi))) {
+      // the key rows of the warp that are no plain copies; rows that are not stored stand in with the first of the keys
       const bool again = keep && turned;
       ExactRow x;
       x.src = static_cast<const E*>(p.k) + (int64_t)t * p.k_stride + (again ? r - g.H : 0) * g.d;
@@ -493,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_append_kernel(const __grid_co
       x.interleaved = rotates && p.interleaved;
       x.eps = p.eps;
       x.inv_g = p.k_inv;
-      const Codes exact = exact_codes<E>(x, with, split);
+      const Codes exact = exact_codes<E>(x, with, split, w, qa, qb, whole);
       if (again && inexact) {
         if (w.scale_a != 0x7f) {
           w.a = exact.a;
