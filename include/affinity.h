@@ -615,9 +615,11 @@ AFF_API aff_status affinity_kv4_plan(const aff_step* step, const aff_kv4_cache* 
 /*
  * affinity_kv_append over a cache in 4 bits: the same norms and rotation, queries
  * to q_out, keys and values quantised to their slots.  The codes are those of
- * the exact z: fp32 decides where it can, and a row with an element or a block's
- * maximum next to a border of the rounding is computed again in 64 bits.
- * rotary->rot is a multiple of 16.
+ * the exact z: fp32 decides where it can, and an element or a block's maximum
+ * next to a border of the rounding is computed again in 64 bits.  That holds for
+ * keys whose mean square (with a norm) and whose elements, turned, are within
+ * fp32's normal range; an element past it counts as an infinity.  rotary->rot is
+ * a multiple of 16.
  */
 AFF_API aff_status affinity_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                        int64_t v_stride, const aff_kv4_cache* cache, const aff_step* step,
@@ -641,7 +643,9 @@ AFF_API aff_status affinity_kv4_read(const aff_kv4_cache* cache, const aff_step*
  * and probabilities as the sum of two fp16 numbers, 22 bits; for small shapes, as
  * the prefix is read by every 8 query rows.  What a row does not see does not
  * reach it; a key or value that reads back as NaN makes the rows NaN that see
- * it (a value: their 16 columns), however small its probability.
+ * it (a value: their 16 columns), however small its probability.  A row of
+ * queries that holds an infinity or a NaN is NaN (0 if it sees nothing).  scale,
+ * and scale * k_scale * log2(e), must be positive and finite in fp32.
  */
 AFF_API aff_status affinity_kv4_attention(const void* q, int64_t q_stride, const aff_kv4_cache* cache, const aff_step* step,
                                           float scale, void* out, float* lse, void* plan, size_t plan_bytes,

@@ -316,6 +316,29 @@ def test_infinite_and_nan_queries_stay_in_their_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("q_lens,kv_lens,prefix", [([4], [300], 0), ([3, 1], [1, 40], 0), ([150], [200], 0), ([140], [100], 30),
+                                                   ([1] * 9, [70] * 9, 200)])
+def test_rows_with_an_infinity_are_nan(q_lens, kv_lens, prefix, dtype):
+    """Whatever the signs of the keys' elements: no row is taken for one that sees nothing.  Rows that see nothing stay so."""
+    c = Case((4, 2, 64), q_lens, kv_lens, prefix, seed=18, dtype=dtype)
+    clean, lse = c.check()
+    for value in (math.inf, -math.inf):
+        q = c.q.cuda().clone()
+        rows = [(0, 1), (c.T - 1, 0), (c.T - 1, 3)]
+        for t, h in rows:
+            q[t, h, 5] = value
+            q[t, h, 6] = 1e30
+        out, got = c.run(q=q)
+        for t, h in rows:
+            if math.isinf(lse[t, h]):
+                assert not out[t, h].any() and math.isinf(got[t, h])
+            else:
+                assert torch.isnan(out[t, h]).all() and math.isnan(got[t, h])
+            out[t, h], got[t, h] = clean[t, h], lse[t, h]
+        assert torch.equal(out, clean) and torch.equal(got, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_results_repeat_bit_for_bit(dtype):
     c = Case((4, 2, 128), [1, 40, 1], [900, 200, 3], 1500, seed=17, dtype=dtype)
     first = c.run()

@@ -126,6 +126,11 @@ def test_attention_arguments(lib, kw, code):
     assert _attend(lib, **kw) == code
 
 
+def test_the_factor_of_the_scores_is_a_number(lib):
+    for scale, k_scale in [(1e38, 2.0 ** 30), (1e-38, 2.0 ** -30)]:
+        assert _attend(lib, c=_cache(k_scale=k_scale), scale=scale) == BAD
+
+
 def test_attention_takes_heads_of_128_at_most(lib):
     assert _attend(lib, c=_cache(d_head=144), q_stride=4 * 144) == SHAPE
 

@@ -69,12 +69,12 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The factor of a row of queries (its largest magnitude, as bits) and the inverse, both powers of two.
+// The factor of a row of queries (its largest magnitude, as bits) and the inverse, both powers of two.  A row with an
+// infinity or a NaN has no scores.
 __device__ __forceinline__ float query_factor(uint32_t top, float* inverse) {
-  int e = (int)(top >> 23);
-  if (e == 255) e = 127 + 13;                 // infinite or NaN: as it is
+  const int e = (int)(top >> 23);
   const int up = min(127 + 13 - e, 126);      // a row of zeros or subnormals: 2^126
-  *inverse = __uint_as_float((uint32_t)(127 - up) << 23);
+  *inverse = e == 255 ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 - up) << 23);
   return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * c + e;
-      sc[e] = __shfl_sync(0xffffffffu, inverse, r * 4) * p.score_log2;
+      const float back = __shfl_sync(0xffffffffu, inverse, r * 4);
       own_vis[e] = r >= nrows ? 0 : it.seq < 0 ? INT32_MAX : g.by_R(row0 + r) + it.own_off + 1;
+      sc[e] = own_vis[e] <= 0 ? 1.f : back * p.score_log2;
       m[e] = -INFINITY;
       l[e] = 0.f;
     }
@@ -1419,7 +1420,8 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
   if (st != AFF_OK) return st;
   const StepGeom& g = p.g;
   if (!q || !out || q_stride < (int64_t)g.H * g.d) return AFF_ERR_INVALID_ARG;
-  if (!(std::isfinite(scale) && scale > 0.f)) return AFF_ERR_INVALID_ARG;
+  p.score_log2 = scale * 1.4426950408889634f * cache->k_scale;
+  if (!(scale > 0.f && std::isfinite(p.score_log2) && p.score_log2 > 0.f)) return AFF_ERR_INVALID_ARG;
   if (g.d > 128) return AFF_ERR_UNSUPPORTED_SHAPE;
   const int es = g.dtype == AFF_BF16 ? 2 : 4;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u || q_stride * es % 16 ||
@@ -1434,7 +1436,6 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
   p.q_stride = q_stride;
   p.out = out;
   p.lse = lse;
-  p.score_log2 = scale * 1.4426950408889634f * cache->k_scale;
   p.v_scale = cache->v_scale;
   // all rows of a step of at most 8 are one sequence's few-rows items; otherwise only the device knows (step.cuh)
   const bool tiles = g.dtype == AFF_BF16 && !(g.few && (int64_t)g.T * g.R <= g.few_rows);
