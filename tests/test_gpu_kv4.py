@@ -436,6 +436,34 @@ def test_no_key_falls_on_the_wrong_side_of_a_border(dtype, interleaved):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k_scale", [2.0 ** -30, 2.0 ** -28, 2.0 ** -26, 2.0 ** 30])
+def test_keys_far_from_the_caches_scale(dtype, k_scale):
+    """fp32's errors are whole codes where every block saturates, and nothing where every block is zero."""
+    for norm, interleaved in [(True, False), (False, False), (True, True)]:
+        c = Case((2, 2, 64), [64], [64], 0, page=64, dtype=dtype, seed=28, k_scale=k_scale)
+        _append(c, 64, interleaved, norm)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_blocks_whose_rotation_cancels(interleaved):
+    """The block is 2^-24 to 2^-8 of the products that it is the difference of: fp32 is sure of nothing, of some codes, of most."""
+    c = Case((2, 2, 64), [340], [340], 0, page=40, dtype=F32, seed=29, k_scale=2.0 ** -12)
+    rng = np.random.default_rng(30)
+    ang = np.arange(340)[:, None] * 100.0 ** (-np.arange(32) / 32)
+    co, si = (f(ang)[:, None] for f in (np.cos, np.sin))
+    size = rng.standard_normal((340, 6, 32)) * 2.0 ** -rng.uniform(8, 24, (340, 6, 1))
+    far = 1 + rng.random((340, 6, 32))
+    if interleaved:                                # (whole blocks of neighbours: both of a pair)
+        size[..., 1::2] = size[..., ::2]
+    # z = (size, far) where it is turned back: x = z turned by the opposite angle
+    a, b = (slice(0, None, 2), slice(1, None, 2)) if interleaved else (slice(0, 32), slice(32, 64))
+    x = np.zeros((340, 6, 64))
+    z = (size, size * 0.7) if interleaved else (size, far)
+    x[..., a], x[..., b] = z[0] * co + z[1] * si, z[1] * co - z[0] * si
+    _append(c, 64, interleaved, norm=False, x=torch.tensor(x.reshape(340, 384)).to(F32), n_pos=340)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_ties_are_those_of_the_exact_values(dtype):
     """Elements and maxima on the borders, at position 0 (not turned at all), past the rotated part and in values."""
     for norm, rot in [(False, 64), (False, 16), (False, 0)]:

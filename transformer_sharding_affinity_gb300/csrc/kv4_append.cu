@@ -156,7 +156,8 @@ __device__ __forceinline__ float largest(const Eight& f) {
   return m;
 }
 
-// The scale of a block whose maximum is `top`, which may be off by `error`; *near_border is set where that could matter.
+// The scale of a block whose maximum is `top`, which may be off by `error`; *near_border is set where that could matter, or
+// where an element that is off by as much could be one of three codes (their borders are half a step apart or more).
 struct Scale {
   uint32_t byte;
   float step, inv;                               // scale g and its reciprocal, 0 where that is 0 or the block not finite
@@ -164,12 +165,12 @@ struct Scale {
 __device__ __forceinline__ Scale make_scale(float top, float g, float inv_g, float error, bool inexact, bool* near_border) {
   const bool finite = top < INFINITY;
   const uint32_t two = to_scales(sixth(top * inv_g), 0.f) & 0xff;
-  const float s = finite ? scale_value(two) : 0.f;
+  const float s = finite ? scale_value(two) : 0.f, inv = s > 0.f ? reciprocal(s) * inv_g : 0.f;
   if (inexact) {
     const uint32_t both = to_scales(sixth((top + error) * inv_g), sixth(fmaxf(top - error, 0.f) * inv_g));
-    if (finite && (both & 0xff) != both >> 8) *near_border = true;
+    if (finite && ((both & 0xff) != both >> 8 || error * inv > 0.2f)) *near_border = true;
   }
-  return {finite ? two : 0x7f, s * g, s > 0.f ? reciprocal(s) * inv_g : 0.f};
+  return {finite ? two : 0x7f, s * g, inv};
 }
 
 // The codes of eight elements of a block, which may be off by e_i margin where `inexact`: lo and hi differ in the elements
@@ -235,7 +236,7 @@ struct Codes {
 
 // A key row in 64 bits, by the row's lanes.  Loops stay loops: a rare path, and small.  `a`, `b`: the lane's runs as fp32
 // has them.  Where no scale is in doubt (`whole` false), the elements that are, alone: each is on one side or the other
-// of the border between its two codes, which is exact.
+// of the border between its two codes, which is exact (make_scale sees to it that there are no more than two).
 template <typename E>
 __device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, bool split, Codes c, const Quantised a,
                                           const Quantised b, bool whole) {
