@@ -39,6 +39,7 @@ struct Kv4AttnParams {
   float* lse;               // [T][H] or null
   float score_log2;         // scale k_scale log2(e)
   float v_scale;
+  int32_t overlap;          // the few-rows kernel follows the row tiles' and starts beside it
 };
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -182,7 +183,9 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
   const StepGeom& g = p.g;
   uint32_t* status = &g.head->status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, c = lane & 3;
-  pdl_enter();
+  // Beside the row tiles' kernel: that one has waited for what came before the call, and lets this one start after that; its
+  // own results are waited for at the end, for the sake of what follows.  (Blocks start where that kernel's have ended.)
+  if (!p.overlap) pdl_enter();
   const bool fits = plan_matches(g);
   const int n_items = fits ? g.head->n_items : 0, first = fits ? g.head->few_begin : 0;
   if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
@@ -655,6 +658,7 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
       g.head->few_done = 0;
     }
   }
+  if (p.overlap) pdl_wait();
 }
 
 // ---------------------------------------------------------------- row tiles
@@ -764,6 +768,7 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     tmem_relinquish();
   }
   pdl_enter();
+  if (p.overlap) pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1439,6 +1444,7 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
   p.v_scale = cache->v_scale;
   // all rows of a step of at most 8 are one sequence's few-rows items; otherwise only the device knows (step.cuh)
   const bool tiles = g.dtype == AFF_BF16 && !(g.few && (int64_t)g.T * g.R <= g.few_rows);
+  p.overlap = tiles && g.few;
   if (tiles) {
     const unsigned grid = (unsigned)(g.max_items < sms ? g.max_items : sms);
     switch (p.pool.n) {
