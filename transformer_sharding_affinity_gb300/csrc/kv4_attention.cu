@@ -190,10 +190,12 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
   const int n_items = fits ? g.head->n_items : 0, first = fits ? g.head->few_begin : 0;
   if ((!fits || n_items < 0) && threadIdx.x == 0) latch_status(status, fits ? kStatusRange : kStatusInvalid);
 
-  // Items come by number for the first two rounds and then from a counter, two ahead; warp 0 looks after them.
-  auto claim = [&]() {
+  // Items come by number for the first two rounds (beside another kernel, where blocks start one after the other: from the
+  // counter) and then from a counter, two ahead; warp 0 looks after them.
+  const int counted = first + (p.overlap ? 0 : 2 * gridDim.x);
+  auto claim = [&](unsigned n = 1u) {
     int next = 0;
-    if (lane == 0) next = first + 2 * gridDim.x + (int)atomicAdd(&g.head->few_claimed, 1u);
+    if (lane == 0) next = counted + (int)atomicAdd(&g.head->few_claimed, n);
     return next;                             // of lane 0
   };
   auto own_item = [&](int i) {               // past the other kernel's items
@@ -208,7 +210,13 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
     if (lane < 8) sh.nan_key[k & 3][lane] = INT32_MAX;
   };
   if (warp == 0) {
-    int i0 = own_item(first + blockIdx.x), i1 = own_item(first + gridDim.x + blockIdx.x);
+    int i0 = first + blockIdx.x, i1 = i0 + gridDim.x;
+    if (p.overlap) {
+      i0 = __shfl_sync(0xffffffffu, claim(2), 0);
+      i1 = i0 + 1;
+    }
+    i0 = own_item(i0);
+    i1 = own_item(i1);
     if (i0 >= n_items) {                     // the other kernel's, and none left for it: the second is the first
       i0 = i1;
       i1 = n_items;
