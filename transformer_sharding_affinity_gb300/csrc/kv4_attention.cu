@@ -712,12 +712,6 @@ constexpr int kTileSmem = 1024 + 6 * 2 * kHalfBytes + 2 * raw_bytes(4) + kTileSt
                           (int)sizeof(TileBars);
 static_assert(kTileSmem <= kSmemMax, "fits an SM");
 
-// 16 bytes that are read once: they take no room in what there is of a first cache.
-__device__ __forceinline__ uint4 load_once(const void* at) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
-  return v;
-}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -1206,65 +1200,54 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
     r.s = value;
     int turn0 = value, turn1 = value;                // of the streams' own tiles
     const uint32_t at = raw + (4 * j * NC + c) * 16, sat = raw + kKeyTile * 16 * NC + (2 * j * NC + 2 * c) * 4;
-    // An item's queries, a row tile a stream (the same one, where both hold the same rows), by these eight warps: 4 rows (8) at a
-    // time, 8 lanes (4) to a row, the next rows on their way meanwhile.
+    // An item's queries, a row tile a stream (the same one, where both hold the same rows), by these eight warps, 8 lanes (4)
+    // to a row: copied as they are to where they will be, all on their way at once, and made fp16 there.
     auto queries = [&](int k, int w8, uint32_t& q_ph) {
-      constexpr int kLanes = NC > 2 ? 8 : 4, kPer = 32 / kLanes, kChunks = (4 * NC + kLanes - 1) / kLanes, kTasks = kRows / kPer;
+      constexpr int kLanes = NC > 2 ? 8 : 4, kPer = 32 / kLanes, kChunks = (4 * NC + kLanes - 1) / kLanes, kTasks = kRows / kPer / 8;
       const WorkItem& it = bars->slot[k % kSlots];
       const int alt = it.alt, n0 = it.n0, n1 = it.n1;
-      if (n0 + n1 == 0) return;
-      const int lc = lane % kLanes, sub = lane / kLanes, streams = alt ? 1 : 2;
+      const int lc = lane % kLanes, first_row = w8 * kTasks * kPer + lane / kLanes;
       const bool twice = alt && n1 > 0;
-      auto fetch = [&](int t, uint4 (&w)[kChunks]) {
-        const int r_item = t * kPer + sub;
-  #pragma unroll
-        for (int y = 0; y < kChunks; ++y) w[y] = make_uint4(0, 0, 0, 0);
-        if (r_item < it.nrows) {
-          const int rr = it.row0 + r_item, tok = g.by_R(rr);
-          const uint16_t* from = static_cast<const uint16_t*>(p.q) + (int64_t)tok * p.q_stride +
-                                 (it.group * g.R + rr - tok * g.R) * g.d;
-  #pragma unroll
-          for (int y = 0; y < kChunks; ++y)
-            if ((lc + y * kLanes) * 8 < g.d) w[y] = load_once(from + (lc + y * kLanes) * 8);
-        }
+      // chunk lc + y kLanes of row `row` of tile x
+      auto place = [&](int row, int x, int y) {
+        const uint32_t at = smem_u32(q_smem) + x * kTileBytes + row * 128 + ((lc ^ (row & 7)) << 4);
+        return NC > 2 ? at + y * kHalfBytes : at ^ (uint32_t)(y << 6);
       };
-      int x = -1;                                      // the stream whose queries are under way
-      auto next_stream = [&]() {                       // hands over stream x, waits for the next one's tile to be free
-        if (x >= 0) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if ((x ? n1 : n0) > 0) mbar_arrive(&bars->q_full[x]);
-            if (twice) mbar_arrive(&bars->q_full[1]);
-          }
+#pragma unroll 1
+      for (int x = 0; x < (alt ? 1 : 2); ++x) {
+        if ((x ? n1 : n0) == 0) continue;
+        await(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
+        q_ph ^= 1u << x;
+        if (twice) {
+          await(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
+          q_ph ^= 2u;
         }
-        ++x;
-        if (x < streams) {
-          if ((x ? n1 : n0) > 0) {
-            await(&bars->q_empty[x], ((q_ph >> x) & 1u) ^ 1u, bars);
-            q_ph ^= 1u << x;
-          }
-          if (twice) {
-            await(&bars->q_empty[1], ((q_ph >> 1) & 1u) ^ 1u, bars);
-            q_ph ^= 2u;
-          }
-        }
-      };
-      uint4 w[kChunks];
-      fetch(w8, w);
-  #pragma unroll 1
-      for (int t = w8; t < kTasks * streams; t += 8) {
-        uint4 ahead[kChunks];
-        fetch(t + 8 < kTasks * streams ? t + 8 : 2 * kTasks, ahead);      // (past the last: nothing)
-        while (x < t / kTasks) next_stream();
-        if ((x ? n1 : n0) > 0) {
-          uint32_t top2 = 0;
-  #pragma unroll
+#pragma unroll 1
+        for (int i = 0; i < kTasks; ++i) {
+          const int row = first_row + i * kPer, rr = it.row0 + x * kRows + row, tok = g.by_R(rr);
+          const bool live = x * kRows + row < it.nrows;
+          const uint16_t* from = static_cast<const uint16_t*>(p.q);
+          if (live) from += (int64_t)tok * p.q_stride + (it.group * g.R + rr - tok * g.R) * g.d;
+#pragma unroll
           for (int y = 0; y < kChunks; ++y) {
+            const int e = (lc + y * kLanes) * 8;
+            if (e < kD) copy16(place(row, x, y), e < g.d ? from + e : from, live && e < g.d);
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int i = 0; i < kTasks; ++i) {
+          const int row = first_row + i * kPer;
+          uint4 w[kChunks];
+          uint32_t top2 = 0;
+#pragma unroll
+          for (int y = 0; y < kChunks; ++y) {
+            w[y] = make_uint4(0, 0, 0, 0);
+            if ((lc + y * kLanes) * 8 < kD) w[y] = ld_shared16(place(row, x, y));
             top2 = max_u16x2(top2, max_u16x2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu));
             top2 = max_u16x2(top2, max_u16x2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
           }
-  #pragma unroll
+#pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top2 = max_u16x2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
           // bf16 to fp16 by its bits: `less` from the exponent, so that the largest element's is 28 at most; what falls out
           // of fp16's range below (2^27 under the largest) becomes 0 or some subnormal number.  A row with an infinity or
@@ -1272,16 +1255,12 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
           const uint32_t e = max(max(top2 & 0xffffu, top2 >> 16) >> 7, 28u), less2 = (e - 28) * 0x00800080u;
           const float inverse = e == 255 ? __int_as_float(0x7fc00000) : __uint_as_float((e - 13) << 23);
           auto bits = [&](uint32_t v) { return (max_u16x2(v & 0x7fff7fffu, less2) - less2) << 3 | (v & 0x80008000u); };
-          const int row = (t % kTasks) * kPer + sub;
-          uint8_t* const to = q_smem + x * kTileBytes + row * 128;
 #pragma unroll
           for (int y = 0; y < kChunks; ++y) {
-            const int chunk = lc + y * kLanes;
-            if (chunk >= 4 * NC) continue;
+            if ((lc + y * kLanes) * 8 >= kD) continue;
             const uint4 h = make_uint4(bits(w[y].x), bits(w[y].y), bits(w[y].z), bits(w[y].w));
-            uint8_t* const at = to + (chunk >> 3) * kHalfBytes + (((chunk & 7) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = h;
-            if (twice) *reinterpret_cast<uint4*>(at + kTileBytes) = h;
+            st_shared16(place(row, x, y), h);
+            if (twice) st_shared16(place(row, x, y) + kTileBytes, h);
           }
           if (lc == 0) {
             float* const f = q_factor + (k % kSlots) * 2 * kRows + row;
@@ -1289,10 +1268,13 @@ kv4_tile_kernel(const __grid_constant__ Kv4AttnParams p) {
             if (twice) f[kRows] = inverse * p.score_log2;
           }
         }
-#pragma unroll
-        for (int y = 0; y < kChunks; ++y) w[y] = ahead[y];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->q_full[x]);
+          if (twice) mbar_arrive(&bars->q_full[1]);
+        }
       }
-      while (x < streams) next_stream();
     };
     // An item's queries come behind its first keys and before its first values.
     uint32_t ph = 0, q_ph = 0;
