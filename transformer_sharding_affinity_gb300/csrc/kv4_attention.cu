@@ -138,7 +138,7 @@ __device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const Wo
 }
 
 // ---------------------------------------------------------------- few rows
-// Items of at most 8 rows, bound by the bytes of the cache.  Eight warps share an item: 32 keys at a time are a warp's
+// Items of at most 8 rows.  Eight warps share an item: 32 keys at a time are a warp's
 // unit, which it copies for itself, a unit ahead (also over an item's end), into a buffer of its own; nothing is
 // exchanged before the item's end.  Two CTAs of an SM have 74 to 147 KB on their way.  Products are transposed, keys as
 // the long side:  S^T = K Q^T and O^T += V^T P^T, for 16 keys at a time, their operands made in registers from the copies.
@@ -147,6 +147,10 @@ __device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const Wo
 //   V  lane (quad, c) holds elements 4 W quad .. of keys 4 c .. 4 c + 3; a byte of two keys' codes for the same
 //      element makes the pair that V^T wants, two shifts and two selections for 16 elements.
 // Rows of S^T are dealt to keys so that a lane's four probabilities' keys are those it holds the values of.
+// 64 tokens over 8192 keys each of 8 heads of 128: 144 us, 4.2 TB/s (a cache in bf16: 336 us).  Bound by issue, 377
+// instructions of a warp for 16 keys at two thirds of the rate; steps that counted: every warp its own copies (244 -> 155 us,
+// a warp that copies for all had them wait for one another), fewer instructions for copies and masks (-> 146).
+// fp32: one CTA of an SM, every row tile of the prefix too; 9 x 5 tokens over 1900 + 100 keys of 4 heads of 64: 11 us.
 constexpr int kFewThreads = 256;
 constexpr int kFewPitch = 132;               // floats of a staged row
 constexpr int kUnit = 32;                    // keys
@@ -171,8 +175,11 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live)
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// CTAs of an SM: in fp32, wider heads take more registers than two leave.
+__host__ __device__ constexpr int few_ctas(int chunks, bool f32) { return f32 && chunks > 2 ? 1 : 2; }
+
 template <int NC, bool F32>
-__global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
+__global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
   // W: words of codes that a lane holds of a key (of a value: half as many)
   constexpr int W = NC >= 3 ? 4 : NC, VW = W == 4 ? 2 : 1, KS = 2 * W, MT = 2 * W;
   constexpr int kRaw = kUnit * 18 * NC, kE = F32 ? 4 : 2, kQRow = 32 * NC * kE;
@@ -685,10 +692,17 @@ __global__ void __launch_bounds__(kFewThreads, F32 ? 1 : 2) kv4_few_kernel(const
 // Tensor memory is laid out as in attention.cu.
 //
 // A thread of warps 16-23 has a chunk (32 elements) of four neighbouring keys: 16 bytes of each and one word of scales
-// for each of the two blocks.  The buffer is free again, and the next tile on its way, as soon as that is in registers.
-// (Without the buffer, loaded from global memory a tile ahead, the same took 1.4 times as long: with 220 KB of shared
-// memory there is hardly any first cache left for the loads to pass through.  Spilled registers cost as much: the split of
-// registers is the one whose tile walks spill nothing.)
+// for each of the two blocks.  The buffer is free again, and the next tile on its way, as soon as that is converted.
+//
+// A prompt of 8192 tokens, 32 / 8 heads of 128: 440 us, 1.25 PFLOP/s; 64 of 1024 tokens, 16 / 8 heads: 372 us (a cache in
+// bf16: 350 and 277 us).  The conversion is what that costs more: it writes a tile that TMA would have written, through two
+// warpgroups, whose loads and stores share an SM's issue slots and shared memory with the softmax.  No unit is full (4096
+// tokens: tensor pipe 43 % of the cycles, issue slots 50 %); what is left is the tiles' chain of waits.  What counted (8192
+// tokens): a warpgroup each for keys and values (967 -> 559 us); registers dealt so that tile walks spill nothing, as next
+// to 220 KB of shared memory there is hardly any first cache (-> 498); tiles copied as they lie instead of loaded into
+// registers a tile ahead (-> 470); shared-memory accesses that meet in no bank (-> 459); 76 KB of code instead of 113, for
+// the instruction cache (-> 439; 64 x 1024 tokens 568 -> 438).  Measured slower: whole tiles of scores for half tiles
+// (458 -> 515), values before queries, page look-ups a tile ahead.
 constexpr int kTileThreads = 768;
 // Registers of the warpgroups: 80 for each of 768 threads at the launch.
 constexpr int kLaunchRegs = 80, kSoftmaxRegs = 112, kIssueRegs = 64, kOutRegs = 64, kConvertRegs = 64;
@@ -1392,14 +1406,16 @@ aff_status launch_tile(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
 }
 
 template <int NC, bool F32>
-aff_status launch_few(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
+aff_status launch_few(const Kv4AttnParams& p, int sms, cudaStream_t s) {
+  const int ctas = few_ctas(NC, F32) * sms;
+  const unsigned grid = (unsigned)(p.g.max_items < ctas ? p.g.max_items : ctas);
   AFF_CUDA(cudaFuncSetAttribute(kv4_few_kernel<NC, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(NC, F32)));
   AFF_CUDA(launch_pdl(kv4_few_kernel<NC, F32>, grid, kFewThreads, (size_t)few_smem(NC, F32), s, p));
   return AFF_OK;
 }
 template <int NC>
-aff_status launch_few(const Kv4AttnParams& p, unsigned grid, cudaStream_t s) {
-  return p.g.dtype == AFF_BF16 ? launch_few<NC, false>(p, grid, s) : launch_few<NC, true>(p, grid, s);
+aff_status launch_few(const Kv4AttnParams& p, int sms, cudaStream_t s) {
+  return p.g.dtype == AFF_BF16 ? launch_few<NC, false>(p, sms, s) : launch_few<NC, true>(p, sms, s);
 }
 
 }  // namespace
@@ -1446,12 +1462,11 @@ extern "C" aff_status affinity_kv4_attention(const void* q, int64_t q_stride, co
     if (st != AFF_OK) return st;
   }
   if (g.few) {
-    const unsigned grid = (unsigned)(g.max_items < 2 * sms ? g.max_items : 2 * sms);
     switch (p.pool.n) {
-      case 1: st = launch_few<1>(p, grid, s); break;
-      case 2: st = launch_few<2>(p, grid, s); break;
-      case 3: st = launch_few<3>(p, grid, s); break;
-      default: st = launch_few<4>(p, grid, s); break;
+      case 1: st = launch_few<1>(p, sms, s); break;
+      case 2: st = launch_few<2>(p, sms, s); break;
+      case 3: st = launch_few<3>(p, sms, s); break;
+      default: st = launch_few<4>(p, sms, s); break;
     }
     if (st != AFF_OK) return st;
   }

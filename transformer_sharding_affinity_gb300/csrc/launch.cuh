@@ -9,6 +9,9 @@
 // started), and its first statement, pdl_wait(), blocks until the previous
 // kernel has completed and its writes are visible.  Nothing is read or written
 // before that wait, so the results are those of plain stream order.
+// One kernel starts beside the one before it, which has waited for what came
+// before both: the few-rows kernel over a cache in 4 bits (kv4_attention.cu).
+// It takes nothing from that one, and waits for it at its own end.
 // AFFINITY_PDL=0 launches them plainly.
 //
 // Measured on the Qwen3-shaped layer (steps, ms, against plain launches): ADD
