@@ -175,8 +175,9 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live)
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// CTAs of an SM: in fp32, wider heads take more registers than two leave.
-__host__ __device__ constexpr int few_ctas(int chunks, bool f32) { return f32 && chunks > 2 ? 1 : 2; }
+// CTAs of an SM: in fp32, the widest heads take more shared memory and registers than two leave.  (Heads of 65 to 96: 30 x 32
+// tokens 62 -> 47 us with two, although some registers are spilled then; one token over 3000 keys 14.4 -> 16.1.)
+__host__ __device__ constexpr int few_ctas(int chunks, bool f32) { return f32 && chunks > 3 ? 1 : 2; }
 
 template <int NC, bool F32>
 __global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel(const __grid_constant__ Kv4AttnParams p) {
