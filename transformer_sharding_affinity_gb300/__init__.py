@@ -8,8 +8,8 @@ The computation lives in libaffinity.so (C ABI, include/affinity.h).  Modules:
   scores     one-call s_up / s_down helpers for PyTorch tensors
   stack      a layer stack: calibration with resume, head placement, the
              alternating layout search, realisation of a layer's layout
-  forward    a stack's forward pass over a paged cache: the attention outputs
-             and residuals that calibration reads
+  forward    a stack's forward pass over a paged cache, in the weights' type or
+             in 4 bits: the attention outputs and residuals that calibration reads
   shards     merging S computed on disjoint token shards across processes
   workloads  seeded synthetic inputs (no method arithmetic)
   device     host -> device plumbing for those inputs

@@ -150,7 +150,8 @@ __device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const Wo
 // 64 tokens over 8192 keys each of 8 heads of 128: 144 us, 4.2 TB/s (a cache in bf16: 336 us).  Bound by issue, 377
 // instructions of a warp for 16 keys at two thirds of the rate; steps that counted: every warp its own copies (244 -> 155 us,
 // a warp that copies for all had them wait for one another), fewer instructions for copies and masks (-> 146).
-// fp32: one CTA of an SM, every row tile of the prefix too; 9 x 5 tokens over 1900 + 100 keys of 4 heads of 64: 11 us.
+// fp32 takes this path for rows of any number: 9 x 5 tokens over 1900 + 100 keys of 4 heads of 64: 11.5 us; 5 x 219 tokens,
+// 16 / 8 heads of 128: 72 us.
 constexpr int kFewThreads = 256;
 constexpr int kFewPitch = 132;               // floats of a staged row
 constexpr int kUnit = 32;                    // keys

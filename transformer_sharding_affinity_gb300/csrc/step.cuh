@@ -1,7 +1,8 @@
 // step.cuh -- the plan of one forward step: where each of its tokens stands,
 // and the attention's work items.  Written by affinity_step_plan (step_plan.cu),
 // read by affinity_kv_append (kv_append.cu) and affinity_prefix_attention
-// (attention.cu) of every layer of the step.
+// (attention.cu) of every layer of the step, or by the same over a cache in
+// 4 bits (kv4_append.cu, kv4_attention.cu).
 //
 // Rows.  Attention works on packed rows: row t * R + r of KV group g is query
 // head g * R + r of token t, R = H / G.  The heads of a group share its keys and
