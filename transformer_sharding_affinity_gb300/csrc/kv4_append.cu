@@ -5,7 +5,7 @@
 //
 // T (H + 2G) d elements in, T H d elements and 9/16 byte for each of 2 T G d out.  64 x 1024 tokens of 16 + 2 x 8 heads of
 // 128, bf16, normalised and turned: 285 us, 3.1 TB/s.  Bound by issue (918 instructions of a warp for 8 rows of 128, 73 %
-// of the slots): a key element costs some forty, two thirds of them for its codes and for whether fp32 is sure of them.
+// of the slots): an element's bounds are quantised beside it.
 // What counted: packed arithmetic and quotients by reciprocal and remainder instead of division (500 -> 356 us, with
 // 64 x 1024 tokens read back), bounds for each element and only those in doubt in 64 bits (-> 345).  Two tokens to a
 // thread instead of two rows of one: 428.
@@ -15,9 +15,10 @@
 // type, and their quotients are too wherever they lie on a border: q + (x - q s) / s, with q off by an ulp or two, is the
 // rounded quotient (the remainder is exact, as s has four bits), and that reaches a border only from it: fp32 decides.
 // Rotated and normalised keys are off by at most kMarginNorm or kMarginTurn of the products they are the sum of.
-// Where that crosses a border, the row is computed again in 64 bits, rounded to odd before each of the two
-// conversions, so that the double rounding does not show.  It happens to 1 in 60000 normalised elements; the 64-bit
-// units have a sixty-fourth of the others' rate, so a narrow margin is worth its arithmetic.
+// Where that crosses a border of codes, the element is compared with it in 64 bits; where it crosses one of scales, or more
+// than one of codes, the row is computed again in 64 bits, rounded to odd before each of the two conversions, so that the
+// double rounding does not show.  1 in 60000 normalised elements is in doubt; the 64-bit units have a sixty-fourth of
+// the others' rate, so a narrow margin is worth its arithmetic.
 #include "affinity.h"
 #include "internal.h"
 #include "kv4.cuh"
