@@ -339,6 +339,16 @@ def test_rows_with_an_infinity_are_nan(q_lens, kv_lens, prefix, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_items_of_few_and_of_more_rows_one_after_the_other(dtype, prefix):
+    """2, 4, 6 and 8 rows, several items to every CTA, from one key to some hundred."""
+    rng = np.random.default_rng(19)
+    q_lens = rng.choice([0, 1, 2, 3, 4], 500).tolist()
+    kv_lens = [n + int(rng.integers(0, 5) if i % 3 else rng.integers(0, 200)) for i, n in enumerate(q_lens)]
+    Case((8, 4, 32), q_lens, kv_lens, prefix, page=16, seed=31, dtype=dtype).check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_results_repeat_bit_for_bit(dtype):
     c = Case((4, 2, 128), [1, 40, 1], [900, 200, 3], 1500, seed=17, dtype=dtype)
     first = c.run()

@@ -335,10 +335,11 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel
   Walk w = begin();
   Unit carried{0, 0, false};                 // the item's first unit, where it was copied before the last one's end
   int buffer = 0;
+  bool few_before = false;                   // the item before has parts in one half of their room
+  asm volatile("cp.async.wait_all;" ::: "memory");         // this warp's row of queries is here
+  __syncthreads();                           // everybody's
 #pragma unroll 1
   for (int k = 0;; ++k) {
-    asm volatile("cp.async.wait_all;" ::: "memory");       // this warp's row of queries is here
-    __syncthreads();                         // everybody's, and the item before's parts have been read
     const WorkItem& it = sh.slot[k & 3];
     const int nrows = it.nrows, row0 = it.row0;
     if (row0 < 0) break;
@@ -413,8 +414,9 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel
       copy_commit();
     }
     carried.left = 0;
+    int units = 0;
 #pragma unroll 1
-    while (u.left > 0) {
+    for (; u.left > 0; ++units) {
       // the next unit, of this item or else of the next
       step(w);
       const Unit next = copy_unit(it, w, buffer ^ 1);
@@ -611,35 +613,40 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel
       publish(k + 2, word);
     }
 
-    // ---- the warps' parts
+    // ---- the warps' parts.  One barrier an item: the parts of at most 4 rows take turns in the two halves of their room, and
+    // while the last warps join them, the others go on.
+    if (units < 2) asm volatile("cp.async.wait_all;" ::: "memory");        // the next item's queries (the waits above: one unit late)
+    if (nrows > 4 && few_before) __syncthreads();          // the item before's parts have been read
+    few_before = nrows <= 4;
+    const int half = nrows > 4 ? 0 : (k & 1) * 4;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
       const int r = 2 * c + e;
       if (r >= nrows) continue;
-      if (quad == 0) sh.ml[warp][r] = make_float2(m[e], l[e]);
-      float* dst = po + (warp * 8 + r) * kFewPitch + 4 * W * quad;
+      if (quad == 0) sh.ml[warp][half + r] = make_float2(m[e], l[e]);
+      float* dst = po + (warp * 8 + half + r) * kFewPitch + 4 * W * quad;
 #pragma unroll
       for (int t = 0; t < MT; t += 2)
         *reinterpret_cast<float4*>(dst + 2 * t) = make_float4(o[t][e], o[t][2 + e], o[t + 1][e], o[t + 1][2 + e]);
     }
     __syncthreads();
-    const int r = warp, e0 = 4 * lane;
+    const int r = 7 - warp, e0 = 4 * lane;
     if (r < nrows) {
       const int rr = row0 + r, tok = g.by_R(rr), h = it.group * g.R + rr - tok * g.R;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, sh.ml[w][r].x);
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, sh.ml[w][half + r].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const float2 s = sh.ml[w][r];
+        const float2 s = sh.ml[w][half + r];
         if (s.y == 0.f) continue;                      // nothing seen by this warp
         const float f = s.x == -INFINITY ? 1.f : ex2(s.x - ref);
         sum += f * s.y;
-        const float4 v = *reinterpret_cast<const float4*>(po + (w * 8 + r) * kFewPitch + min(e0, 32 * W - 4));
+        const float4 v = *reinterpret_cast<const float4*>(po + (w * 8 + half + r) * kFewPitch + min(e0, 32 * W - 4));
         acc.x += f * v.x;
         acc.y += f * v.y;
         acc.z += f * v.z;
@@ -666,6 +673,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(NC, F32)) kv4_few_kernel
         else if (p.lse) p.lse[(int64_t)tok * g.H + h] = lse;
       }
     }
+    if (nrows > 4) __syncthreads();
   }
   // every claim of this CTA has been made: the last one leaves the counters as the next call needs them
   if (fits && threadIdx.x == 0) {
