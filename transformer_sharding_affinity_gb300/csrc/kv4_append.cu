@@ -200,9 +200,11 @@ __device__ __forceinline__ Quantised quantise(Eight x, float top, float g, const
     const uint64_t q0 = mul2(x.p[i], inv2);
     q.p[i] = fma2(fma2(q0, less2, x.p[i]), inv2, q0);
   }
-  Quantised r{to_codes(q), 0, 0};
-  if (s.byte == 0x7f) r.codes = 0;
-  if (inexact && s.byte != 0x7f) {
+  Quantised r{0, 0, 0};
+  if (s.byte == 0x7f) return r;
+  if (!inexact) {
+    r.codes = to_codes(q);
+  } else {
     const float d = margin * s.inv;
     Eight lo, hi;                                // away from zero and towards it, or the other way round
 #pragma unroll
@@ -210,8 +212,9 @@ __device__ __forceinline__ Quantised quantise(Eight x, float top, float g, const
       hi.p[i] = fma2(e.p[i], pk(d, d), q.p[i]);
       lo.p[i] = fma2(e.p[i], pk(-d, -d), q.p[i]);
     }
+    r.codes = to_codes(hi);                        // (of an element in doubt neither is taken)
     r.lo = to_codes(lo) & 0x77777777u;
-    r.hi = to_codes(hi) & 0x77777777u;
+    r.hi = r.codes & 0x77777777u;
   }
   return r;
 }
@@ -284,13 +287,13 @@ __device__ __noinline__ Codes exact_codes(const ExactRow r, const Partner p, boo
       const int i = (__ffs(second ? in_b : in_a) - 1) >> 2, at = (second ? 8 : 0) + i;
       double x, y;
       pair(r.interleaved ? at >> 1 : i, &x, &y);
-      const double v = fabs((r.interleaved ? at & 1 : second) ? y : x) * r.inv_g;
+      const double z = (r.interleaved ? at & 1 : second) ? y : x, v = fabs(z) * r.inv_g;
       const uint32_t u = (second ? b.lo : a.lo) >> (4 * i) & 7, w = (second ? b.hi : a.hi) >> (4 * i) & 7, low = min(u, w);
       const float mid = low < 4 ? 0.25f + 0.5f * low : low == 4 ? 2.5f : low == 5 ? 3.5f : 5.f;
       const double border = (double)(mid * (second ? step_b : step_a));
       const uint32_t code = v > border || (v == border && (low & 1)) ? low + 1 : low;
       uint32_t& word = second ? c.b : c.a;
-      word = (word & ~(7u << 4 * i)) | code << 4 * i;
+      word = (word & ~(15u << 4 * i)) | (code | (z < 0.0 ? 8u : 0u)) << 4 * i;
       (second ? in_b : in_a) &= ~(15u << 4 * i);
     }
     return c;
