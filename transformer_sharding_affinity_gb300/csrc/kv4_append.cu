@@ -7,8 +7,9 @@
 // 128, bf16, normalised and turned: 285 us, 3.1 TB/s.  Bound by issue (918 instructions of a warp for 8 rows of 128, 73 %
 // of the slots): an element's bounds are quantised beside it.
 // What counted: packed arithmetic and quotients by reciprocal and remainder instead of division (500 -> 356 us, with
-// 64 x 1024 tokens read back), bounds for each element and only those in doubt in 64 bits (-> 345).  Two tokens to a
-// thread instead of two rows of one: 428.
+// 64 x 1024 tokens read back), bounds for each element and only those in doubt in 64 bits (-> 347).  Two tokens to a
+// thread instead of two rows of one: 428; one row to a thread 411; 80 registers instead of 64: 358, 48: 425.  Of the 347,
+// 47 go to the bounds and 47 to the path in 64 bits, most of that for the last ones' latency at the kernel's end.
 //
 // Borders.  A code changes where x / (scale g) passes one of seven values, a scale where the maximum does, so a last
 // bit of fp32 may move an element by a third of its size.  Values and plain keys are exact in the activations'

@@ -147,9 +147,10 @@ __device__ __forceinline__ TileShare tile_share(const Kv4AttnParams& p, const Wo
 //   V  lane (quad, c) holds elements 4 W quad .. of keys 4 c .. 4 c + 3; a byte of two keys' codes for the same
 //      element makes the pair that V^T wants, two shifts and two selections for 16 elements.
 // Rows of S^T are dealt to keys so that a lane's four probabilities' keys are those it holds the values of.
-// 64 tokens over 8192 keys each of 8 heads of 128: 144 us, 4.2 TB/s (a cache in bf16: 336 us).  Bound by issue, 377
+// 64 tokens over 8192 keys each of 8 heads of 128: 141 us, 4.3 TB/s (a cache in bf16: 336 us).  Bound by issue, 377
 // instructions of a warp for 16 keys at two thirds of the rate; steps that counted: every warp its own copies (244 -> 155 us,
-// a warp that copies for all had them wait for one another), fewer instructions for copies and masks (-> 146).
+// a warp that copies for all had them wait for one another), fewer instructions for copies and masks (-> 146), one barrier
+// an item (-> 141; 256 tokens over up to 100 keys 37 -> 33).
 // fp32 takes this path for rows of any number: 9 x 5 tokens over 1900 + 100 keys of 4 heads of 64: 11.5 us; 5 x 219 tokens,
 // 16 / 8 heads of 128: 72 us.
 constexpr int kFewThreads = 256;
