@@ -578,6 +578,51 @@ def test_another_stream_and_a_graph():
         assert torch.equal(out, want)
 
 
+def test_calls_in_a_row_take_and_leave_what_stands_between_them():
+    """Single tokens behind a prefix: both of the attention's kernels, side by side at the first one's end.  Queries are written
+    just before each call, outputs and partial rows just after; each result is that of the call by itself."""
+    rng = np.random.default_rng(34)
+    own = rng.integers(1, 400, 200).tolist()
+    c = Case((8, 2, 128), [1] * 200, own, 5000, page=64, seed=35)
+    base = c.q.cuda()
+    factors = [1.0, -0.5, 2.0, 0.25, -1.5, 0.75]
+    want = []
+    for f in factors:
+        q = base * f
+        torch.cuda.synchronize()
+        out, lse = c.run(q=q)
+        torch.cuda.synchronize()
+        want.append((out.clone(), lse.clone()))
+    q = torch.empty_like(base)
+    out, lse = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    got = [(torch.empty_like(out), torch.empty_like(lse)) for _ in factors]
+
+    def chain():
+        for f, (o, l) in zip(factors, got):
+            torch.mul(base, f, out=q)
+            B.kv4_attention(q, c.cache, c.step, 128 ** -0.5, out, lse, c.plan)
+            o.copy_(out)
+            l.copy_(lse)
+
+    def same():
+        torch.cuda.synchronize()
+        assert B.device_status(c.plan) == B.AFF_OK
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            a[0].zero_()
+            a[1].zero_()
+
+    for _ in range(5):
+        chain()
+        same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(5):
+        graph.replay()
+        same()
+
+
 def test_a_plan_of_the_other_kind_or_of_a_malformed_step_is_reported():
     c = Case((4, 2, 64), [2, 1], [20, 9], 0, seed=32)
     k = torch.zeros(c.kd.shape[0], 2, 16, 64, dtype=BF, device="cuda")
